@@ -16,7 +16,7 @@ import threading
 
 __all__ = [
     "GemmError", "lib", "library_path", "gemm_f16", "gemm_f16_f32out", "f32_to_f16",
-    "sgemm_f32", "gemm_f16_host",
+    "sgemm_f32", "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe", "gemm_f16_host",
     "sgemm_f32_host", "gemm_f16_splitk_noalloc", "l2_flush", "force_path", "force_splits", "stage_kblocks",
     "set_wait_limit_ns",
     "debug_status", "last_path", "launch_count", "plan_stream_k", "release", "EXPORTS",
@@ -34,6 +34,7 @@ EXPORTS = (
     "gemm_debug_status", "gemm_last_path", "gemm_strerror", "gemm_release",
     "gemm_f16_splitk_noalloc", "gemm_launch_count", "gemm_plan_stream_k", "gemm_f16_f32out",
     "gemm_f32_to_f16", "gemm_debug_wait_probe", "gemm_plan_tf32_slices", "gemm_stage_kblocks",
+    "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe",
 )
 
 PATH_AUTO, PATH_TMA, PATH_MANUAL, PATH_SPLITK, PATH_F32_SCALAR = 0, 1, 2, 3, 4
@@ -76,6 +77,12 @@ def lib():
             L.gemm_f16_f32out.argtypes = [vp, vp, vp, i, i, i, i, i, i, f, f, vp]
             L.gemm_f32_to_f16.restype = i
             L.gemm_f32_to_f16.argtypes = [vp, vp, ctypes.c_longlong, vp]
+            L.gemm_f16_lora.restype = i
+            L.gemm_f16_lora.argtypes = [vp] * 7 + [i] * 10 + [f, f, vp]
+            L.gemm_f16_lora_grad.restype = i
+            L.gemm_f16_lora_grad.argtypes = [vp] * 10 + [i] * 11 + [f, f, vp]
+            L.gemm_f16_moe.restype = i
+            L.gemm_f16_moe.argtypes = [vp] * 7 + [i] * 8 + [f, vp]
             L.gemm_f16_splitk_noalloc.restype = i
             L.gemm_f16_splitk_noalloc.argtypes = [vp, vp, vp, i, i, i, i, i, i, f, f, i, vp]
             L.gemm_l2_flush.restype = i
@@ -213,6 +220,78 @@ def sgemm_f32(A, B, C, alpha=1.0, beta=0.0, M=None, N=None, K=None, lda=None, ld
                             int(K if lda is None else lda), int(N if ldb is None else ldb),
                             int(N if ldc is None else ldc), float(alpha), float(beta), s)
     _check(rc, "sgemm_f32")
+
+
+def _adapter_dims(A, R, adapters):
+    if adapters is None:
+        adapters = A.shape[0]
+    if R is None:
+        R = A.shape[2]
+    return int(R), int(adapters)
+
+
+def gemm_f16_lora(X, W, C, A, B, ids, scales=None, alpha=1.0, beta=0.0, M=None, N=None, K=None,
+                  R=None, adapters=None, ldx=None, ldw=None, ldc=None, lda=None, ldb=None,
+                  stream=None):
+    """C_i := alpha*(X_i*W + s[a]*(X_i*A[a])*B[a]) + beta*C_i with a = ids[i]
+    (int32; outside [0, adapters): no adapter) on device fp16 operands; A is
+    (adapters, K, R), B (adapters, R, N), scales fp32 or None for ones."""
+    M, N, K = _dims(X, W, M, N, K)
+    R, adapters = _adapter_dims(A, R, adapters)
+    rc = lib().gemm_f16_lora(_addr(X), _addr(W), _addr(C), _addr(A), _addr(B), _addr(ids),
+                             _addr(scales), M, N, K, R, adapters, int(K if ldx is None else ldx),
+                             int(N if ldw is None else ldw), int(N if ldc is None else ldc),
+                             int(R if lda is None else lda), int(N if ldb is None else ldb),
+                             float(alpha), float(beta), _stream(stream))
+    _check(rc, "gemm_f16_lora")
+
+
+def gemm_f16_lora_grad(dC, X, W, A, B, ids, scales=None, dX=None, dA=None, dB=None, alpha=1.0,
+                       beta=0.0, M=None, N=None, K=None, R=None, adapters=None, lddc=None,
+                       ldx=None, ldw=None, lda=None, ldb=None, lddx=None, stream=None):
+    """Gradients of gemm_f16_lora, W frozen: dX (M, K) fp16, and dA
+    (adapters, K, R), dB (adapters, R, N) fp32, which are accumulated onto
+    beta times their old values.  Any of the three may be None."""
+    if N is None:
+        N = dC.shape[1]
+    if M is None:
+        M = dC.shape[0]
+    if K is None:
+        K = W.shape[0] if W is not None else X.shape[1]
+    if R is None:
+        R = A.shape[2] if A is not None else B.shape[1]
+    if adapters is None:
+        adapters = A.shape[0] if A is not None else B.shape[0]
+    rc = lib().gemm_f16_lora_grad(_addr(dC), _addr(X), _addr(W), _addr(A), _addr(B), _addr(ids),
+                                  _addr(scales), _addr(dX), _addr(dA), _addr(dB), int(M), int(N),
+                                  int(K), int(R), int(adapters), int(N if lddc is None else lddc),
+                                  int(K if ldx is None else ldx), int(N if ldw is None else ldw),
+                                  int(R if lda is None else lda), int(N if ldb is None else ldb),
+                                  int(K if lddx is None else lddx), float(alpha), float(beta),
+                                  _stream(stream))
+    _check(rc, "gemm_f16_lora_grad")
+
+
+def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True, beta=0.0, T=None,
+                 H=None, I=None, E=None, ldx=None, ldy=None, stream=None):
+    """A mixture-of-experts layer on device fp16 operands, made for a few
+    tokens: Y_t := sum of topk experts' p*(silu(X_t*W1g)*(X_t*W1u))*W2 +
+    beta*Y_t, the experts and p from the router X_t*Wr.  Wr is (H, E), W1
+    (E, H, 2I), W2 (E, I, H); ids (int32) and probs (fp32), both (T, topk),
+    receive the choice."""
+    if T is None:
+        T = X.shape[0]
+    if H is None:
+        H = X.shape[1]
+    if E is None:
+        E = W2.shape[0]
+    if I is None:
+        I = W2.shape[1]
+    rc = lib().gemm_f16_moe(_addr(X), _addr(Wr), _addr(W1), _addr(W2), _addr(Y), _addr(ids),
+                            _addr(probs), int(T), int(H), int(I), int(E), int(topk),
+                            int(bool(renormalize)), int(H if ldx is None else ldx),
+                            int(H if ldy is None else ldy), float(beta), _stream(stream))
+    _check(rc, "gemm_f16_moe")
 
 
 def gemm_f16_host(A, B, C, alpha=1.0, beta=0.0, M=None, N=None, K=None, lda=None, ldb=None,

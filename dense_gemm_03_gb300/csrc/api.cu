@@ -71,6 +71,8 @@ struct StreamWs {
   size_t realigned_bytes = 0;
   void* split = nullptr;        // big/small tf32 parts of fp32 operands
   size_t split_bytes = 0;
+  void* routed = nullptr;       // scratch of the row-routed products
+  size_t routed_bytes = 0;
 };
 
 struct DevState {
@@ -1197,6 +1199,16 @@ int query_device(int* sm_count, DeviceStatus** status, unsigned long long* wait_
   return GEMM_OK;
 }
 
+int routed_scratch(cudaStream_t stream, size_t bytes, void** out) {
+  DevState* d = nullptr;
+  if (int rc = device_state(&d, nullptr)) return rc;
+  std::lock_guard<std::mutex> lk(g_mu);
+  StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
+  if (int rc = ensure_buffer(&w.routed, &w.routed_bytes, bytes)) return rc;
+  *out = w.routed;
+  return GEMM_OK;
+}
+
 int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
                    int box_cols, int box_rows) {
   return make_map_f16(map, ptr, rows, cols, ld, box_cols, box_rows);
@@ -1395,6 +1407,7 @@ int gemm_release(void) {
       if (kv.second.counters) cudaFree(kv.second.counters);
       if (kv.second.realigned) cudaFree(kv.second.realigned);
       if (kv.second.split) cudaFree(kv.second.split);
+      if (kv.second.routed) cudaFree(kv.second.routed);
     }
     d.ws.clear();
     for (cudaStream_t* st : {&d.copy_in, &d.copy_back}) {

@@ -292,6 +292,11 @@ cudaError_t launch_sgemm_ffma(bool vec, const SgemmArgs& args, cudaStream_t stre
 // on first use).  Returns a GEMM_* code.
 int query_device(int* sm_count, DeviceStatus** status, unsigned long long* wait_limit_ns);
 
+// Scratch of the row-routed products (adapters, experts) on `stream`, at least
+// `bytes` long and 256-byte aligned; kept per device and stream, freed by
+// gemm_release().  Returns a GEMM_* code.
+int routed_scratch(cudaStream_t stream, size_t bytes, void** out);
+
 // 2-D fp16 tensor map with 128-byte swizzle (rows x cols, row stride ld).
 int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
                    int box_cols, int box_rows);

@@ -140,6 +140,77 @@ int sgemm_f32_ld(const float* A, const float* B, float* C,
                  float alpha, float beta, cudaStream_t stream);
 
 /*
+ * Row-routed products: operators whose weights go by row of X.  Same types,
+ * layouts, streams, graphs, scratch and errors as above.
+ *
+ * A shared projection with low-rank adapters beside it,
+ *
+ *     C_i := alpha * (X_i * W + s[a] * (X_i * A[a]) * B[a]) + beta * C_i,
+ *
+ * a = ids[i] for every row i (rows in any order; an id outside [0, adapters)
+ * means no adapter: the row gets the shared projection alone, and no adapter's
+ * weights, whatever they hold, reach it).
+ *   X        M x K half, ldx >= K          W   K x N half, ldw >= N
+ *   A        adapters stacked densely: A[a] is K x R half with leading
+ *            dimension lda >= R, K*lda elements after A[a-1]
+ *   B        likewise, B[a] is R x N, ldb >= N, R*ldb elements apart
+ *   ids      M int32 on the device         R   0 .. 128 (else GEMM_ERR_ARG)
+ *   scales   `adapters` floats on the device, or NULL for all ones
+ * C is half with ldc >= N and overlaps no other operand.  Adapters of smaller
+ * rank are stacked with zero columns of A and zero rows of B.  Products and
+ * sums are fp32; s * X_i * A[a] is kept to at least 22 significant bits (its
+ * magnitude must stay within the half range, 65504); C is rounded once.
+ * R == 0 or adapters == 0 is gemm_f16_ld; alpha == 0 and beta == 0 as there.
+ */
+int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint16_t* A,
+                  const uint16_t* B, const int* ids, const float* scales, int M, int N, int K,
+                  int R, int adapters, int ldx, int ldw, int ldc, int lda, int ldb, float alpha,
+                  float beta, cudaStream_t stream);
+
+/*
+ * The gradients of gemm_f16_lora for a given dC (M x N half, lddc >= N), the
+ * shared W frozen.  With U_i = s[a] * dC_i * B[a]^T and V_i = s[a] * X_i * A[a]:
+ *
+ *     dX_i  := alpha * (dC_i * W^T + U_i * A[a]^T)         M x K half, lddx >= K
+ *     dA[a] := alpha * sum_{i of a} X_i^T * U_i + beta * dA[a]     K x R float
+ *     dB[a] := alpha * sum_{i of a} V_i^T * dC_i + beta * dB[a]    R x N float
+ *
+ * dA and dB are dense stacks (adapters x K x R, adapters x R x N) in fp32, to
+ * be accumulated over micro-batches with beta = 1 (beta == 0: not read); an
+ * adapter without rows gets beta times its old value.  dX, dA and dB may each
+ * be NULL (not wanted); then operands only they read may be NULL too.  Sums
+ * run in a fixed order: repeated calls are bitwise equal.
+ */
+int gemm_f16_lora_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, const uint16_t* A,
+                       const uint16_t* B, const int* ids, const float* scales, uint16_t* dX,
+                       float* dA, float* dB, int M, int N, int K, int R, int adapters, int lddc,
+                       int ldx, int ldw, int lda, int ldb, int lddx, float alpha, float beta,
+                       cudaStream_t stream);
+
+/*
+ * A whole mixture-of-experts layer, made for a few tokens (decoding):
+ *
+ *     l = X_t * Wr;  the topk experts of largest l (ties: the lowest index),
+ *     p = softmax(l) at them (divided by their sum when renormalize != 0),
+ *     Y_t := sum_k p_k * (silu(X_t * W1g[e_k]) .* (X_t * W1u[e_k])) * W2[e_k]
+ *            + beta * Y_t
+ *   X   T x H half, ldx >= H               Y   T x H half, ldy >= H
+ *   Wr  H x E half, dense                  W2  E x I x H half, dense
+ *   W1  E x H x 2I half, dense: I gate columns W1g, then I up columns W1u
+ *   ids, probs   T x topk int32 / float on the device: the chosen experts in
+ *                order of falling l, and p.  Each may be NULL.
+ * 1 <= topk <= min(E, 32), E <= 1024 (else GEMM_ERR_ARG).  A NaN logit counts
+ * as the largest.  Only chosen experts' weights are read, each once per block
+ * of tokens; a token's result depends on no other token and no expert it did
+ * not choose.  Sums are fp32 in a fixed order; the gated product is kept to at
+ * least 22 significant bits (magnitude within the half range); Y is rounded
+ * once.  H == 0 leaves nothing to do; I == 0 gives Y := beta * Y.
+ */
+int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_t* W1, const uint16_t* W2,
+                 uint16_t* Y, int* ids, float* probs, int T, int H, int I, int E, int topk,
+                 int renormalize, int ldx, int ldy, float beta, cudaStream_t stream);
+
+/*
  * Host-buffer forms: A, B, C are HOST pointers (pinned memory gives the
  * fastest copies and lets them overlap; pageable memory works).  On a
  * library-owned copy-in stream the call copies B, then A and C (C when

@@ -1,0 +1,342 @@
+"""A shared projection with low-rank adapters picked by row, and its gradients,
+through the public binding, against the 64-bit definition."""
+import numpy as np
+import pytest
+
+import routed_ref as ref
+from helpers import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dense_gemm_03_gb300 import build
+    build.build()
+
+
+def make_ids(t, rng, M, n, order):
+    if order == "none":
+        ids = np.full(M, -1)
+    elif order == "one":
+        ids = np.full(M, n - 1)
+    elif order == "mixed":
+        ids = rng.integers(-1, n, M)
+    elif order == "outside":       # ids that name no adapter, among ones that do
+        ids = rng.choice([-(2 ** 31), -7, -1, 0, n - 1, n, n + 1, 2 ** 31 - 1], M)
+    else:                          # runs of rows
+        ids = np.repeat(rng.integers(-1, n, M), rng.integers(1, max(2, 2 * M // (n + 1)), M))[:M]
+    return t.from_numpy(ids.astype(np.int32))
+
+
+def operands(t, seed, M, N, K, R, n, order, integers=False):
+    rng = np.random.default_rng(seed)
+    def draw(*shape, std=1.0):
+        x = rng.integers(-1, 2, shape) if integers else rng.normal(0, std, shape)
+        return t.from_numpy(x.astype(np.float16))
+    return dict(X=draw(M, K), W=draw(K, N, std=K ** -0.5), A=draw(n, K, R, std=K ** -0.5),
+                B=draw(n, R, N, std=R ** -0.5), ids=make_ids(t, rng, M, n, order),
+                scales=t.from_numpy((rng.choice([0.5, 1.0, -2.0], n) if integers
+                                     else rng.uniform(0.25, 2, n)).astype(np.float32)),
+                C0=draw(M, N), G=draw(M, N, std=0.1),
+                dA0=draw(n, K, R).float(), dB0=draw(n, R, N).float())
+
+
+def dev(o):
+    return {k: v.cuda() for k, v in o.items()}
+
+
+def sync(t):
+    import dense_gemm_03_gb300 as g
+    t.cuda.synchronize()
+    assert g.debug_status() == 0
+
+
+SHAPES = [
+    # M, N, K, R, adapters, ids
+    (1, 1, 1, 1, 1, "one"),
+    (1, 64, 64, 16, 2, "mixed"),
+    (1, 2048, 1024, 16, 4, "one"),
+    (2, 512, 256, 8, 3, "none"),
+    (3, 200, 100, 5, 3, "mixed"),          # rows of A off the 16-byte grid
+    (17, 256, 512, 16, 20, "mixed"),
+    (33, 136, 72, 8, 40, "mixed"),
+    (64, 512, 1024, 16, 32, "mixed"),
+    (64, 1032, 520, 64, 3, "outside"),
+    (127, 264, 1000, 24, 9, "mixed"),
+    (128, 384, 640, 128, 4, "mixed"),
+    (129, 257, 333, 33, 5, "runs"),        # nothing aligned
+    (130, 256, 256, 16, 130, "mixed"),     # more adapters in a tile than one pass takes
+    (200, 300, 96, 8, 1, "one"),
+    (256, 320, 128, 40, 300, "mixed"),
+    (300, 512, 256, 120, 7, "runs"),
+    (500, 1001, 512, 8, 5, "runs"),        # odd width
+    (513, 1024, 2048, 32, 8, "runs"),
+    (700, 520, 200, 16, 3, "none"),
+    (2049, 264, 320, 16, 6, "runs"),
+]
+
+
+@pytest.mark.parametrize("M,N,K,R,n,order", SHAPES)
+def test_forward(M, N, K, R, n, order):
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, 7 * M + N + K, M, N, K, R, n, order)
+    v = dev(o)
+    for alpha, beta, scales in ((1.0, 0.0, True), (1.5, -0.5, False)):
+        C = t.full_like(v["C0"], float("nan")) if beta == 0.0 else v["C0"].clone()
+        g.gemm_f16_lora(v["X"], v["W"], C, v["A"], v["B"], v["ids"],
+                        v["scales"] if scales else None, alpha, beta)
+        sync(t)
+        r, tol = ref.lora(o["X"], o["W"], o["C0"], o["A"], o["B"], o["ids"],
+                          o["scales"] if scales else None, alpha, beta)
+        ref.check(C.cpu(), r, tol, g.last_path())
+
+
+@pytest.mark.parametrize("M,N,K,R,n,order", [s for s in SHAPES if s[2] <= 640])
+def test_forward_integers_exact(M, N, K, R, n, order):
+    """Small integers: every sum is exact, so any lost, repeated or misplaced
+    term shows.  (Results beyond 2048 round; the sums before do not.)"""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M + N, M, N, K, R, n, order, integers=True)
+    v = dev(o)
+    C = v["C0"].clone()
+    g.gemm_f16_lora(v["X"], v["W"], C, v["A"], v["B"], v["ids"], v["scales"], 2.0, -1.0)
+    sync(t)
+    r, _ = ref.lora(o["X"], o["W"], o["C0"], o["A"], o["B"], o["ids"], o["scales"], 2.0, -1.0)
+    assert t.equal(C.cpu(), r.half()), g.last_path()
+
+
+@pytest.mark.parametrize("M,N,K,R,n,order", SHAPES)
+def test_grad(M, N, K, R, n, order):
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, 5 * M + N + K, M, N, K, R, n, order)
+    v = dev(o)
+    for alpha, beta, scales in ((1.0, 0.0, True), (0.5, 1.0, False)):
+        dX = t.full_like(v["X"], float("nan"))
+        dA, dB = v["dA0"].clone(), v["dB0"].clone()
+        if beta == 0.0:
+            dA.fill_(float("nan"))
+            dB.fill_(float("nan"))
+        g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"],
+                             v["scales"] if scales else None, dX, dA, dB, alpha, beta)
+        sync(t)
+        r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"],
+                          o["scales"] if scales else None, alpha, beta, o["dA0"], o["dB0"])
+        for name, got in (("dX", dX), ("dA", dA), ("dB", dB)):
+            ref.check(got.cpu(), *r[name], what=name + " " + g.last_path())
+
+
+@pytest.mark.parametrize("M,N,K,R,n,order", [s for s in SHAPES if s[2] <= 640 and s[0] <= 600])
+def test_grad_integers_exact(M, N, K, R, n, order):
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M * N, M, N, K, R, n, order, integers=True)
+    o["G"] = o["C0"]
+    v = dev(o)
+    dX = t.empty_like(v["X"])
+    dA, dB = v["dA0"].clone(), v["dB0"].clone()
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], dX, dA, dB,
+                         2.0, 1.0)
+    sync(t)
+    r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 2.0, 1.0,
+                      o["dA0"], o["dB0"])
+    assert t.equal(dX.cpu(), r["dX"][0].half()), g.last_path()
+    assert t.equal(dA.cpu(), r["dA"][0].float()) and t.equal(dB.cpu(), r["dB"][0].float())
+
+
+def test_grad_against_differences():
+    """dX, dA, dB are the derivatives of sum(G * C): C is linear in each of
+    them, so a central difference of the 64-bit forward along a direction equals
+    the gradient's product with it up to the gradient's own bound."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    M, N, K, R, n = 96, 160, 128, 16, 5
+    o = operands(t, 3, M, N, K, R, n, "mixed")
+    v = dev(o)
+    dX, dA, dB = t.empty_like(v["X"]), t.empty_like(v["dA0"]), t.empty_like(v["dB0"])
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], dX, dA, dB)
+    sync(t)
+    bounds = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0,
+                           o["dA0"], o["dB0"])
+    gen = t.Generator().manual_seed(4)
+
+    def loss(X, A, B):
+        Y, _ = ref.lora(X, o["W"], None, A, B, o["ids"], o["scales"], 1.0, 0.0)
+        return (o["G"].double() * Y).sum()
+
+    for name, got in (("X", dX), ("A", dA), ("B", dB)):
+        for _ in range(4):
+            base = {k: o[k].double() for k in "XAB"}
+            step = t.randn(base[name].shape, generator=gen, dtype=t.float64)
+            up, dn = dict(base), dict(base)
+            up[name], dn[name] = base[name] + step, base[name] - step
+            diff = float(loss(**up) - loss(**dn)) / 2
+            along = float((got.cpu().double() * step).sum())
+            tol = float((bounds["d" + name][1] * step.abs()).sum()) + 1e-9 * abs(diff)
+            assert abs(diff - along) <= tol, (name, diff, along, tol)
+
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_weights_of_other_adapters_do_not_reach_a_row(M):
+    """Adapters holding Inf and NaN change only their own rows, gradients
+    included; one that no row uses changes nothing."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    N, K, R, n = 264, 320, 16, 6
+    o = operands(t, 11, M, N, K, R, n, "mixed")
+    o["ids"][o["ids"] == 5] = 0
+    clean = {k: x.clone() for k, x in o.items()}
+    o["A"][2] = float("inf")
+    o["B"][3] = float("nan")
+    o["A"][5] = float("nan")
+    o["B"][5] = float("inf")
+    good = (o["ids"] != 2) & (o["ids"] != 3)
+    outs = []
+    for x in (dev(clean), dev(o)):
+        C, dX = t.empty_like(x["C0"]), t.empty_like(x["X"])
+        dA, dB = t.empty_like(x["dA0"]), t.empty_like(x["dB0"])
+        g.gemm_f16_lora(x["X"], x["W"], C, x["A"], x["B"], x["ids"], x["scales"])
+        g.gemm_f16_lora_grad(x["G"], x["X"], x["W"], x["A"], x["B"], x["ids"], x["scales"], dX, dA, dB)
+        sync(t)
+        outs.append([y.cpu() for y in (C, dX, dA, dB)])
+    (C, dX, dA, dB), (C2, dX2, dA2, dB2) = outs
+    assert t.equal(C[good], C2[good]) and t.equal(dX[good], dX2[good])
+    keep = [0, 1, 4, 5]
+    assert t.equal(dA[keep], dA2[keep]) and t.equal(dB[keep], dB2[keep])
+    assert (dA2[5] == 0).all() and (dB2[5] == 0).all()
+    if (o["ids"] == 2).any():
+        assert not t.isfinite(C2[o["ids"] == 2]).any()
+
+
+def test_infinite_row_stays_in_its_row():
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    M, N, K, R, n = 150, 128, 192, 16, 4
+    o = operands(t, 12, M, N, K, R, n, "mixed")
+    clean = dev(o)
+    o["X"][77, 5] = float("inf")
+    bad = dev(o)
+    C, C2 = t.empty_like(clean["C0"]), t.empty_like(clean["C0"])
+    g.gemm_f16_lora(clean["X"], clean["W"], C, clean["A"], clean["B"], clean["ids"], clean["scales"])
+    g.gemm_f16_lora(bad["X"], bad["W"], C2, bad["A"], bad["B"], bad["ids"], bad["scales"])
+    sync(t)
+    rows = [i for i in range(M) if i != 77]
+    assert t.equal(C[rows], C2[rows]) and not t.isfinite(C2[77]).any()
+
+
+@pytest.mark.parametrize("M,N,K,R,n,pad", [(50, 200, 136, 8, 3, 8), (50, 201, 133, 7, 3, 3),
+                                           (300, 264, 200, 16, 4, 8), (301, 263, 201, 9, 4, 5)])
+def test_leading_dimensions(M, N, K, R, n, pad):
+    """Sub-matrices of wider buffers; the columns beside them stay untouched."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M + pad, M, N, K, R, n, "mixed")
+
+    def wide(x):
+        w = t.full(x.shape[:-1] + (x.shape[-1] + pad,), float("nan"), dtype=x.dtype, device="cuda")
+        w[..., :x.shape[-1]] = x.cuda()
+        return w
+
+    X, W, C, A, B, G = (wide(o[k]) for k in ("X", "W", "C0", "A", "B", "G"))
+    ids, sc = o["ids"].cuda(), o["scales"].cuda()
+    g.gemm_f16_lora(X, W, C, A, B, ids, sc, 1.0, 0.5, M=M, N=N, K=K, R=R, adapters=n, ldx=K + pad,
+                    ldw=N + pad, ldc=N + pad, lda=R + pad, ldb=N + pad)
+    dX = t.full((M, K + pad), float("nan"), dtype=t.float16, device="cuda")
+    dA, dB = t.empty((n, K, R), device="cuda"), t.empty((n, R, N), device="cuda")
+    g.gemm_f16_lora_grad(G, X, W, A, B, ids, sc, dX, dA, dB, M=M, N=N, K=K, R=R, adapters=n,
+                         lddc=N + pad, ldx=K + pad, ldw=N + pad, lda=R + pad, ldb=N + pad,
+                         lddx=K + pad)
+    sync(t)
+    assert C[:, N:].isnan().all() and dX[:, K:].isnan().all()
+    ref.check(C[:, :N].cpu(), *ref.lora(o["X"], o["W"], o["C0"], o["A"], o["B"], o["ids"],
+                                        o["scales"], 1.0, 0.5))
+    r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0,
+                      o["dA0"], o["dB0"])
+    for name, got in (("dX", dX[:, :K]), ("dA", dA), ("dB", dB)):
+        ref.check(got.cpu(), *r[name], what=name)
+
+
+def test_empty_and_degenerate_calls():
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = dev(operands(t, 1, 20, 64, 32, 8, 3, "mixed"))
+    C = o["C0"].clone()
+    # no adapters at all: the plain projection, bit for bit
+    g.gemm_f16_lora(o["X"], o["W"], C, o["A"], o["B"], o["ids"], R=0)
+    D = t.empty_like(C)
+    g.gemm_f16(o["X"], o["W"], D)
+    sync(t)
+    assert t.equal(C, D)
+    # alpha == 0: C := beta C, the operands unread
+    C = o["C0"].clone()
+    bad = t.full_like(o["X"], float("nan"))
+    g.gemm_f16_lora(bad, o["W"], C, o["A"], o["B"], o["ids"], alpha=0.0, beta=0.5)
+    sync(t)
+    assert t.equal(C, (o["C0"].float() * 0.5).half())
+    # no rows: dA and dB are beta times what they were
+    dA, dB = t.ones_like(o["dA0"]), t.ones_like(o["dB0"])
+    g.gemm_f16_lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], None, None, dA, dB, 1.0,
+                         0.25, M=0)
+    sync(t)
+    assert (dA == 0.25).all() and (dB == 0.25).all()
+    # alpha == 0: dX := 0
+    dX = t.full_like(o["X"], float("nan"))
+    g.gemm_f16_lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], None, dX, dA, dB, 0.0, 0.0)
+    sync(t)
+    assert (dX == 0).all() and (dA == 0).all() and (dB == 0).all()
+
+
+def test_grad_parts_alone_equal_the_whole():
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = dev(operands(t, 21, 200, 256, 192, 16, 4, "runs"))
+    def outs():
+        return t.empty_like(o["X"]), t.empty_like(o["dA0"]), t.empty_like(o["dB0"])
+    dX, dA, dB = outs()
+    g.gemm_f16_lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], dX, dA, dB)
+    eX, eA, eB = outs()
+    g.gemm_f16_lora_grad(o["G"], None, o["W"], o["A"], o["B"], o["ids"], o["scales"], dX=eX)
+    g.gemm_f16_lora_grad(o["G"], o["X"], None, None, o["B"], o["ids"], o["scales"], dA=eA)
+    g.gemm_f16_lora_grad(o["G"], o["X"], None, o["A"], None, o["ids"], o["scales"], dB=eB)
+    sync(t)
+    assert t.equal(dX, eX) and t.equal(dA, eA) and t.equal(dB, eB)
+
+
+@pytest.mark.parametrize("M", [5, 64, 400])
+def test_streams_graphs_and_repeats(M):
+    """Repeated calls are bitwise equal, on another stream and from a graph."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = dev(operands(t, 31, M, 520, 1024, 16, 7, "mixed"))
+    t.cuda.synchronize()
+
+    def call(C, dX, dA, dB):
+        g.gemm_f16_lora(o["X"], o["W"], C, o["A"], o["B"], o["ids"], o["scales"])
+        g.gemm_f16_lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], dX, dA, dB)
+
+    def outs():
+        return [t.full_like(o[k], float("nan")) for k in ("C0", "X", "dA0", "dB0")]
+
+    first, second, third = outs(), outs(), outs()
+    call(*first)
+    t.cuda.synchronize()
+    s = t.cuda.Stream()
+    with t.cuda.stream(s):
+        call(*second)
+    s.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.stream(s):
+        call(*third)
+        s.synchronize()
+        with t.cuda.graph(graph, stream=s):
+            call(*third)
+    for x in third:
+        x.fill_(float("nan"))
+    for _ in range(3):
+        graph.replay()
+    sync(t)
+    for a, b, c in zip(first, second, third):
+        assert t.equal(a, b) and t.equal(a, c)
