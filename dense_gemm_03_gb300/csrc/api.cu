@@ -73,6 +73,8 @@ struct StreamWs {
   size_t split_bytes = 0;
   void* routed = nullptr;       // scratch of the row-routed products
   size_t routed_bytes = 0;
+  void* routed_zero = nullptr;  // its arrival counters, zero between calls
+  size_t routed_zero_bytes = 0;
 };
 
 struct DevState {
@@ -1199,14 +1201,41 @@ int query_device(int* sm_count, DeviceStatus** status, unsigned long long* wait_
   return GEMM_OK;
 }
 
-int routed_scratch(cudaStream_t stream, size_t bytes, void** out) {
+int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed,
+                   void** zeroed_out) {
   DevState* d = nullptr;
   if (int rc = device_state(&d, nullptr)) return rc;
   std::lock_guard<std::mutex> lk(g_mu);
   StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
   if (int rc = ensure_buffer(&w.routed, &w.routed_bytes, bytes)) return rc;
   *out = w.routed;
+  if (zeroed) {
+    if (!w.routed_zero || w.routed_zero_bytes < zeroed) {
+      if (int rc = ensure_buffer(&w.routed_zero, &w.routed_zero_bytes, zeroed)) return rc;
+      if (cudaMemsetAsync(w.routed_zero, 0, w.routed_zero_bytes, stream) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    }
+    *zeroed_out = w.routed_zero;
+  }
   return GEMM_OK;
+}
+
+int encode_map_f16_stack(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
+                         int depth, long long stride, int box_cols, int box_rows) {
+  EncodeTiledFn enc = nullptr;
+  if (int rc = encode_fn(&enc)) return rc;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(depth)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2,
+                                 static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows),
+                             1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
@@ -1408,6 +1437,7 @@ int gemm_release(void) {
       if (kv.second.realigned) cudaFree(kv.second.realigned);
       if (kv.second.split) cudaFree(kv.second.split);
       if (kv.second.routed) cudaFree(kv.second.routed);
+      if (kv.second.routed_zero) cudaFree(kv.second.routed_zero);
     }
     d.ws.clear();
     for (cudaStream_t* st : {&d.copy_in, &d.copy_back}) {

@@ -15,69 +15,18 @@
 #include <initializer_list>
 
 #include "gemm.h"
-#include "internal.h"
+#include "moe.h"
 
 namespace gb300 {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxExperts = 1024;
-constexpr int kMaxTopk = 32;
+constexpr int kMaxExperts = kMoeMaxExperts;
+constexpr int kMaxTopk = kMoeMaxTopk;
 
-__device__ __forceinline__ float h2f(uint16_t b) { return __half2float(__ushort_as_half(b)); }
-__device__ __forceinline__ uint16_t f2h(float x) { return __half_as_ushort(__float2half_rn(x)); }
-
-// Order-preserving key of a float: larger floats have larger keys, -0 and +0
-// the same one, NaN the largest.
-__device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) return 0xFFFFFFFFu;
-  const uint32_t u = __float_as_uint(x + 0.0f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-// One warp: the topk largest of logits[0, E) (ties: the lowest index), falling,
-// into ids and p[k] = softmax(logits) there.  `taken` holds E marks.
-__device__ void select_experts(const float* logits, uint8_t* taken, int E, int topk,
-                               int renormalize, int* ids, float* probs) {
-  const int lane = threadIdx.x & 31;
-  float sum = 0.0f, top = 0.0f, chosen = 0.0f;
-  for (int e = lane; e < E; e += 32) taken[e] = 0;
-  __syncwarp();
-  for (int k = 0; k < topk; ++k) {
-    uint32_t best = 0;
-    int arg = E;
-    for (int e = lane; e < E; e += 32)
-      if (!taken[e]) {
-        const uint32_t key = order_key(logits[e]);
-        if (arg == E || key > best) {
-          best = key;
-          arg = e;
-        }
-      }
-    const uint32_t most = __reduce_max_sync(0xffffffffu, arg < E ? best : 0u);
-    const uint32_t first =
-        __reduce_min_sync(0xffffffffu, (arg < E && best == most) ? static_cast<uint32_t>(arg)
-                                                                 : 0xFFFFFFFFu);
-    const int e = static_cast<int>(first);
-    if (k == 0) {
-      top = logits[e];
-      for (int j = lane; j < E; j += 32) sum += expf(logits[j] - top);
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    }
-    const float p = expf(logits[e] - top) / sum;
-    chosen += p;
-    if (lane == 0) {
-      taken[e] = 1;
-      ids[k] = e;
-      probs[k] = p;
-    }
-    __syncwarp();
-  }
-  if (renormalize)
-    for (int k = lane; k < topk; k += 32) probs[k] = probs[k] / chosen;
-  __syncwarp();
-}
+__device__ __forceinline__ float h2f(uint16_t b) { return moe_h2f(b); }
+__device__ __forceinline__ uint16_t f2h(float x) { return moe_f2h(x); }
 
 __global__ void __launch_bounds__(kThreads)
     moe_route_kernel(const uint16_t* __restrict__ X, long long ldx, const uint16_t* __restrict__ Wr,
@@ -195,16 +144,6 @@ int status_of(cudaError_t e) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-struct MoeArgs {
-  const uint16_t *X, *Wr, *W1, *W2;
-  uint16_t* Y;
-  int* ids;
-  float* probs;
-  int T, H, I, E, topk, renormalize;
-  int ldx, ldy;
-  float beta;
-};
-
 int moe_any(const MoeArgs& m, int sms, cudaStream_t stream) {
   const size_t pairs = static_cast<size_t>(m.T) * m.topk;
   const size_t id_bytes = round256(4 * pairs), h_bytes = round256(4 * pairs * m.I);
@@ -255,5 +194,5 @@ extern "C" int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_
   unsigned long long limit = 0;
   if (int rc = query_device(&sms, &st, &limit)) return rc;
   const MoeArgs m{X, Wr, W1, W2, Y, ids, probs, T, H, I, E, topk, renormalize, ldx, ldy, beta};
-  return moe_any(m, sms, stream);
+  return moe_stream_fits(m) ? moe_stream(m, sms, st, limit, stream) : moe_any(m, sms, stream);
 }

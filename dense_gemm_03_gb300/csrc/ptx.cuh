@@ -95,6 +95,21 @@ __device__ __forceinline__ bool wait_parity(uint32_t bar, uint32_t parity, uint6
   }
 }
 
+// A wait that does not give up early because another thread failed: used only
+// to let copies and MMAs already in flight finish before the CTA exits.
+__device__ __forceinline__ void settle_wait(uint32_t bar, uint32_t parity, DeviceStatus* st,
+                                            int where) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return;
+    if (globaltimer_ns() - t0 > 1000000000ull) {
+      if (atomicCAS(&st->code, 0, kStatusTimeout) == 0) st->where = where;
+      return;
+    }
+  }
+}
+
 // -------------------------------------------------------------------------
 // Proxy fences
 // -------------------------------------------------------------------------
@@ -124,6 +139,17 @@ __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(policy)
+      : "memory");
+}
+
+// A 3-D tile (a stack of matrices: x, y within matrix z), with an L2 policy.
+__device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap* map,
+                                                 uint32_t bar, int x, int y, int z,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
       : "memory");
 }
 
@@ -163,6 +189,32 @@ __device__ __forceinline__ unsigned long long ld_acquire_gpu_u64(const unsigned 
   unsigned long long v;
   asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(ptr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ unsigned int ld_acquire_gpu_u32(const unsigned int* ptr) {
+  unsigned int v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(ptr) : "memory");
+  return v;
+}
+
+// Waits until *ptr >= target (written by other resident CTAs with a release),
+// giving up like wait_parity.
+__device__ __forceinline__ bool wait_count(const unsigned int* ptr, unsigned int target,
+                                           uint64_t limit_ns, DeviceStatus* st, int where) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (ld_acquire_gpu_u32(ptr) >= target) return true;
+    if ((it & 63u) == 0) {
+      if (*reinterpret_cast<volatile int*>(&st->code) != 0) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > limit_ns) {
+        if (atomicCAS(&st->code, 0, kStatusTimeout) == 0) st->where = where;
+        return false;
+      }
+    }
+  }
 }
 
 // Brings the 128-byte line holding `ptr` into L2 (no registers written).
@@ -256,6 +308,27 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+
+// The same with 8 columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Waits for this warp's tcgen05.ld; the registers are operands, so that no use
+// of them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld2(uint32_t (&a)[8], uint32_t (&b)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                 "+r"(a[6]), "+r"(a[7]), "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]),
+                 "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_ld() {
