@@ -35,7 +35,6 @@ __global__ void __launch_bounds__(kThreads)
                      float* __restrict__ probs_out) {
   __shared__ float logits[kMaxExperts];
   __shared__ float part[kWarps][32];
-  __shared__ uint8_t taken[kMaxExperts];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int t = blockIdx.x; t < T; t += gridDim.x) {
     const uint16_t* x = X + static_cast<long long>(t) * ldx;
@@ -56,7 +55,7 @@ __global__ void __launch_bounds__(kThreads)
     if (warp == 0) {
       int* const id = ids + static_cast<long long>(t) * topk;
       float* const p = probs + static_cast<long long>(t) * topk;
-      select_experts(logits, taken, E, topk, renormalize, id, p);
+      select_experts(logits, E, topk, renormalize, id, p);
       for (int k = lane; k < topk; k += 32) {
         if (ids_out) ids_out[static_cast<long long>(t) * topk + k] = id[k];
         if (probs_out) probs_out[static_cast<long long>(t) * topk + k] = p[k];

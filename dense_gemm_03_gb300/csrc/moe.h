@@ -44,46 +44,57 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 // One warp: the topk largest of logits[0, E) (ties: the lowest index), falling,
 // into ids and p[k] = softmax(logits) there, divided by their sum when
-// `renormalize`.  `taken` holds E marks.
-__device__ __forceinline__ void select_experts(const float* logits, uint8_t* taken, int E, int topk,
+// `renormalize`.  The keys stay in registers, NR of 32 per lane (E <= 32 NR).
+template <int NR>
+__device__ __forceinline__ void select_experts(const float* logits, int E, int topk,
                                                int renormalize, int* ids, float* probs) {
   const int lane = threadIdx.x & 31;
-  float sum = 0.0f, top = 0.0f, chosen = 0.0f;
-  for (int e = lane; e < E; e += 32) taken[e] = 0;
-  __syncwarp();
+  uint32_t key[NR];
+#pragma unroll
+  for (int j = 0; j < NR; ++j)   // no logit has key 0
+    key[j] = lane + 32 * j < E ? order_key(logits[lane + 32 * j]) : 0u;
+  int mine = 0;                  // lane k: the k-th expert
   for (int k = 0; k < topk; ++k) {
     uint32_t best = 0;
-    int arg = E;
-    for (int e = lane; e < E; e += 32)
-      if (!taken[e]) {
-        const uint32_t key = order_key(logits[e]);
-        if (arg == E || key > best) {
-          best = key;
-          arg = e;
-        }
-      }
-    const uint32_t most = __reduce_max_sync(0xffffffffu, arg < E ? best : 0u);
-    const uint32_t first =
-        __reduce_min_sync(0xffffffffu, (arg < E && best == most) ? static_cast<uint32_t>(arg)
-                                                                 : 0xFFFFFFFFu);
-    const int e = static_cast<int>(first);
-    if (k == 0) {
-      top = logits[e];
-      for (int j = lane; j < E; j += 32) sum += expf(logits[j] - top);
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    }
-    const float p = expf(logits[e] - top) / sum;
-    chosen += p;
-    if (lane == 0) {
-      taken[e] = 1;
-      ids[k] = e;
-      probs[k] = p;
-    }
-    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < NR; ++j) best = max(best, key[j]);
+    const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+    uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = NR - 1; j >= 0; --j)
+      if (key[j] == most) at = static_cast<uint32_t>(lane + 32 * j);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, at);
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+      if (e == static_cast<uint32_t>(lane + 32 * j)) key[j] = 0u;
+    if (lane == k) mine = static_cast<int>(e);
   }
-  if (renormalize)
-    for (int k = lane; k < topk; k += 32) probs[k] = probs[k] / chosen;
+  const float top = logits[__shfl_sync(0xffffffffu, mine, 0)];
+  float sum = 0.0f;
+  for (int e = lane; e < E; e += 32) sum += expf(logits[e] - top);
+  float p = lane < topk ? expf(logits[mine] - top) : 0.0f;
+  float chosen = p;
+  for (int d = 16; d; d >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    chosen += __shfl_xor_sync(0xffffffffu, chosen, d);
+  }
+  p /= renormalize ? chosen : sum;
+  if (lane < topk) {
+    ids[lane] = mine;
+    probs[lane] = p;
+  }
   __syncwarp();
+}
+
+// The same for any E up to the layer's limit.
+__device__ __forceinline__ void select_experts(const float* logits, int E, int topk,
+                                               int renormalize, int* ids, float* probs) {
+  if (E <= 64)
+    select_experts<2>(logits, E, topk, renormalize, ids, probs);
+  else if (E <= 256)
+    select_experts<8>(logits, E, topk, renormalize, ids, probs);
+  else
+    select_experts<kMoeMaxExperts / 32>(logits, E, topk, renormalize, ids, probs);
 }
 
 }  // namespace gb300

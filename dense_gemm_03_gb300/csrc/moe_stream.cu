@@ -4,7 +4,7 @@
 //   moe_logits_kernel  l = x Wr as K slices over many CTAs; the CTA that ends a
 //                      block of four tokens adds the slices up in order, picks
 //                      the topk experts and writes ids and p.
-//   moe_stream_kernel  one CTA per SM, all resident (cooperative launch):
+//   moe_stream_kernel  one CTA per SM:
 //     up    hid = silu(x W1g) .* (x W1u) of every (token, expert) pair
 //     down  z = hid W2 per pair
 //     sum   y = sum_k p_k z_k + beta y
@@ -14,14 +14,18 @@
 // streaming the weights from HBM.  So the weights are the M operand: a unit is
 // 128 + 128 columns of an expert's matrix (gate and up columns j, or 256
 // columns of W2) in two TMEM accumulators, the expert's tokens the N operand
-// (N = 16..128), and a k-block is 64 rows of the matrix, 32 KB by TMA.  All
-// k-blocks of all units are shared out evenly: CTA c takes [c, c+1) * total /
-// CTAs, cut at unit boundaries into pieces.  A piece that is not a whole unit
-// publishes fp32 partial sums; the last piece of an up unit to arrive adds them
-// in k order (so the result does not depend on which that is), the sum step
-// does so for down units.  The weights do not depend on the grid-wide barrier
-// between up and down, so W2 streams into the ring across it; only the warps
-// that stage hid wait.
+// (N = 16..128), and a k-block is 64 rows of the matrix, 32 KB by TMA.
+//
+// Units are cut along K into chunks of equal length, numbered up first, and
+// CTAs take chunk numbers from a counter, in order: SMs stream at rates up to
+// 20% apart, and an equal share for each left the fast ones idle.  A unit's chunks publish fp32
+// partial sums; the last chunk of an up unit to arrive adds them in k order
+// (so the result does not depend on which that is), the sum step does so for
+// down units.  A down chunk waits until its own expert's hid is written, the
+// sum step for all down chunks; both wait only for chunks of lower numbers,
+// which running CTAs have taken and finish without waiting for later ones, so
+// no wait needs a CTA that has not started.  The weights do not depend on those
+// waits: W2 streams into the ring across them.
 //
 // hid is kept as two halves, hi + lo (22 significant bits), staged as separate
 // rows of the N operand and added up after the products, so the layer's only
@@ -47,6 +51,7 @@ constexpr int kMaxPairs = kBlockT * kMoeMaxTopk;
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteT = 4;                   // tokens per CTA
+constexpr int kMaxSplits = 16;
 constexpr int kRouteChunk = 512;             // rows of Wr staged against at a time
 
 struct RouteArgs {
@@ -69,7 +74,7 @@ __global__ void __launch_bounds__(kRouteThreads) moe_logits_kernel(const RouteAr
   __shared__ float xs[kRouteT][kRouteChunk];
   __shared__ float part[kRouteWarps][kRouteT][32];
   __shared__ int last;
-  extern __shared__ float logits[];          // [kRouteT][E], then the marks
+  extern __shared__ float logits[];          // [kRouteT][E]
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = blockIdx.x * kRouteThreads + threadIdx.x; i < a.nzero;
@@ -123,17 +128,19 @@ __global__ void __launch_bounds__(kRouteThreads) moe_logits_kernel(const RouteAr
   if (warp < nt) {
     const int t = t0 + warp;
     float* const l = logits + warp * a.E;
-    uint8_t* const taken = reinterpret_cast<uint8_t*>(logits + kRouteT * a.E) + warp * a.E;
     for (int j = lane; j < a.E; j += 32) {
-      float s = 0.0f;
-      for (int k = 0; k < a.splits; ++k)
-        s += __ldcg(a.part + (static_cast<long long>(k) * a.T + t) * a.E + j);
+      float v[kMaxSplits], s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxSplits; ++k)
+        v[k] = k < a.splits ? __ldcg(a.part + (static_cast<long long>(k) * a.T + t) * a.E + j) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxSplits; ++k) s += v[k];
       l[j] = s;
     }
     __syncwarp();
     int* const id = a.ids + static_cast<long long>(t) * a.topk;
     float* const p = a.probs + static_cast<long long>(t) * a.topk;
-    select_experts(l, taken, a.E, a.topk, a.renormalize, id, p);
+    select_experts(l, a.E, a.topk, a.renormalize, id, p);
     for (int k = lane; k < a.topk; k += 32) {
       if (a.ids_out) a.ids_out[static_cast<long long>(t) * a.topk + k] = id[k];
       if (a.probs_out) a.probs_out[static_cast<long long>(t) * a.topk + k] = p[k];
@@ -145,12 +152,15 @@ __global__ void __launch_bounds__(kRouteThreads) moe_logits_kernel(const RouteAr
 constexpr int kWeightBytes = 4 * 64 * 128;   // one k-block of a unit: 32 KB
 constexpr int kMaxStages = 8;
 constexpr int kLoaders = 4;                  // warps that stage token rows
-constexpr int kEpi = 4;                      // epilogue warps
-constexpr int kStreamWarps = 2 + kLoaders + kEpi;
+constexpr int kEpi = 4;                      // epilogue warps of one accumulator buffer
+constexpr int kStreamWarps = 2 + kLoaders + 2 * kEpi;
 constexpr int kStreamThreads = 32 * kStreamWarps;
 constexpr int kAccCols = 128;                // TMEM columns of one accumulator
 constexpr int kTmemCols = 512;               // two buffers of two accumulators
 constexpr int kSmemMax = 232448;
+constexpr int kQueue = 4;                    // chunk numbers on their way to the consumers
+constexpr int kBarBytes = 8 * (3 * kMaxStages + 5 + 2 * kQueue);
+constexpr int kFixedBytes = (kBarBytes + 4 * kQueue + 8 + 15) / 16 * 16;
 
 struct StreamArgs {
   const uint16_t* X;
@@ -164,68 +174,69 @@ struct StreamArgs {
   int up_tiles, up_kb, down_tiles, down_kb;
   int stages, stage_bytes;
   uint16_t* hid;           // [2][T * topk][I]: hi, lo
-  float* z;                // [T * topk][H], whole down units
-  float* part;             // [phase][CTA][first / last piece][acc][token][128]
-  int part_tokens;
-  unsigned int* counters;  // [up unit][4 epilogue warps]
-  unsigned int* bars;      // arrivals after up, after down
+  float* up_part;          // by unit and chunk: [acc][token][128]
+  float* z;                // [T * topk][chunk][H]
+  unsigned int* queue;     // chunks taken so far
+  unsigned int* done;      // down chunks finished, by epilogue warp
+  unsigned int* ready;     // [active expert] up units finished, by epilogue warp
+  unsigned int* counters;  // [up unit][epilogue warp] chunks arrived
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
 };
 
-// A CTA's share of a phase: k-blocks [beg, end) of the phase's tot = active
-// experts * tiles * kb.  The first `workers` CTAs have one, at least kMinKb
-// k-blocks long (none is empty, so the owners of a unit are consecutive CTAs).
-constexpr int kMinKb = 2;
-struct Phase {
-  long long tot, beg, end;
-  int tiles, kb, workers;
-};
-
-struct Piece {
-  int q, tile, kb0, kb1;
-  long long unit;
-};
-
-__device__ __forceinline__ Phase phase_of(long long active, int tiles, int kb, int cta, int ctas) {
-  Phase p;
-  p.tiles = tiles;
-  p.kb = kb;
-  p.tot = active * tiles * kb;
-  p.workers = static_cast<int>(min(static_cast<long long>(ctas), max(1ll, p.tot / kMinKb)));
-  p.beg = cta < p.workers ? cta * p.tot / p.workers : 0;
-  p.end = cta < p.workers ? (cta + 1) * p.tot / p.workers : 0;
-  return p;
+// Chunks per unit of `kb` k-blocks, for `active` experts of `tiles` units each
+// and `pairs` (token, expert) pairs.  A chunk has at least
+//   * 4 k-blocks (128 KB, ~2.8 us of an SM's share of HBM: publishing a chunk's
+//     sums and counting it in takes the two groups of epilogue warps about 2 us
+//     each; with 2 k-blocks they fell behind the stream by 10 us),
+//   * 1/8 of an SM's even share, so that the last ones to finish are short
+//     without the partial sums growing for nothing,
+//   * a quarter as many k-blocks as an expert has tokens: its partial sums,
+//     1 KB per token, then stay an eighth of its 32 KB k-blocks.
+__host__ __device__ inline int chunks_of(int active, int tiles, int kb, int pairs, int ctas) {
+  int len = active * tiles * kb / (8 * ctas);
+  if (len < 4) len = 4;
+  if (len < pairs / (4 * active)) len = pairs / (4 * active);
+  return len >= kb ? 1 : (kb + len - 1) / len;
 }
 
-__device__ __forceinline__ Piece piece_at(const Phase& p, long long x) {
-  Piece t;
-  t.unit = x / p.kb;
-  t.kb0 = static_cast<int>(x - t.unit * p.kb);
-  t.kb1 = static_cast<int>(min(static_cast<long long>(p.kb), t.kb0 + (p.end - x)));
-  t.q = static_cast<int>(t.unit / p.tiles);
-  t.tile = static_cast<int>(t.unit - static_cast<long long>(t.q) * p.tiles);
+// The chunks of a launch: [0, up) then [up, up + down).
+struct Work {
+  int up_tiles, up_kb, up_chunks, down_tiles, down_kb, down_chunks;
+  int up, total;
+};
+
+struct Chunk {
+  int down, unit, q, tile, c, kb0, kb1;
+};
+
+__device__ __forceinline__ Chunk chunk_at(const Work& w, int id) {
+  Chunk t;
+  t.down = id >= w.up;
+  if (t.down) id -= w.up;
+  const int n = t.down ? w.down_chunks : w.up_chunks, kb = t.down ? w.down_kb : w.up_kb;
+  const int tiles = t.down ? w.down_tiles : w.up_tiles;
+  t.unit = id / n;
+  t.c = id - t.unit * n;
+  t.kb0 = t.c * kb / n;
+  t.kb1 = (t.c + 1) * kb / n;
+  t.q = t.unit / tiles;
+  t.tile = t.unit - t.q * tiles;
   return t;
 }
 
-// The CTA whose share holds k-block x.
-__device__ __forceinline__ int owner_of(const Phase& p, long long x) {
-  return static_cast<int>(((x + 1) * p.workers - 1) / p.tot);
+__host__ __device__ inline int round_up(int x, int m) { return (x + m - 1) / m * m; }
+
+// Counts in at GPU scope after __syncwarp(): what the warp's lanes wrote before
+// is released with it (and acquired by whoever reads the count).
+__device__ __forceinline__ unsigned int add_acq_rel(unsigned int* p) {
+  unsigned int before;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(p) : "memory");
+  return before;
 }
 
-// Partial sums of CTA w for a unit that starts at k-block u0: its first piece
-// (slot 0) when its share starts inside the unit, else its last one (slot 1).
-__device__ __forceinline__ float* part_of(const StreamArgs& a, const Phase& p, int phase, int w,
-                                          int ctas, long long u0) {
-  const int slot = w * p.tot / p.workers > u0 ? 0 : 1;
-  return a.part + ((static_cast<long long>(phase) * ctas + w) * 2 + slot) *
-                      (2ll * a.part_tokens * 128);
-}
-
-__device__ __forceinline__ int round_up(int x, int m) { return (x + m - 1) / m * m; }
-
-__device__ __forceinline__ void arrive_release(unsigned int* bar) {
-  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
+__device__ __forceinline__ void add_release(unsigned int* p) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p) : "memory");
 }
 
 __global__ void __launch_bounds__(kStreamThreads, 1)
@@ -240,7 +251,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const int cta = blockIdx.x, ctas = gridDim.x;
   const int P = a.T * a.topk;
 
-  // after the ring: barriers, then the routing lists
+  // after the ring: barriers, the chunk queue, then the routing lists
   uint8_t* const tail = base_ptr + static_cast<size_t>(S) * a.stage_bytes;
   const uint32_t bars = base + static_cast<uint32_t>(S * a.stage_bytes);
   auto full_bar = [&](int s) { return bars + 8u * s; };                     // weights landed
@@ -249,16 +260,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   auto accf_bar = [&](uint32_t b) { return bars + 8u * (3 * kMaxStages + b); };
   auto acce_bar = [&](uint32_t b) { return bars + 8u * (3 * kMaxStages + 2 + b); };
   const uint32_t done_bar = bars + 8u * (3 * kMaxStages + 4);
-  constexpr int kBarBytes = 8 * (3 * kMaxStages + 5);
-  uint32_t* const misc = reinterpret_cast<uint32_t*>(tail + kBarBytes);     // TMEM address, active
-  uint16_t* const s_ids = reinterpret_cast<uint16_t*>(tail + kBarBytes + 8);   // expert of a pair
-  const int P2 = round_up(P, 2), E2 = round_up(a.E, 2);
-  uint16_t* const s_list = s_ids + P2;    // pairs by (expert, pair)
-  uint16_t* const s_pos = s_list + P2;    // place of a pair in s_list
-  uint16_t* const s_cnt = s_pos + P2;     // tokens of expert e
-  uint16_t* const s_off = s_cnt + E2;     // first place of expert e
-  uint16_t* const s_qi = s_off + E2;      // rank of expert e among the active ones
-  uint16_t* const s_act = s_qi + E2;      // active experts in order
+  auto qfull_bar = [&](int i) { return bars + 8u * (3 * kMaxStages + 5 + i); };
+  auto qempty_bar = [&](int i) { return bars + 8u * (3 * kMaxStages + 5 + kQueue + i); };
+  volatile int* const s_queue = reinterpret_cast<int*>(tail + kBarBytes);
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(tail + kBarBytes + 4 * kQueue);
+  uint16_t* const s_ids = reinterpret_cast<uint16_t*>(tail + kFixedBytes);   // expert of a pair
+  const int P8 = round_up(P, 8), E2 = round_up(a.E, 2);
+  uint16_t* const s_list = s_ids + P8;    // pairs by (expert, pair)
+  uint16_t* const s_pos = s_list + P8;    // place of a pair in s_list
+  uint16_t* const s_off = s_pos + P8;     // first place of expert e
+  uint16_t* const s_act = s_off + E2;     // active experts in order
+  int* const s_cnt = reinterpret_cast<int*>(s_act + E2);   // tokens of expert e
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -271,6 +283,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       mbar_init(acce_bar(b), static_cast<uint32_t>(kEpi));
     }
     mbar_init(done_bar, 1u);
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(qfull_bar(i), 1u);
+      mbar_init(qempty_bar(i), static_cast<uint32_t>(1 + kLoaders + 2 * kEpi));
+    }
     fence_barrier_init();
     fence_proxy_async_smem();
     prefetch_tensormap(&tm1);
@@ -280,22 +296,23 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     tmem_alloc(smem_addr(misc), kTmemCols);
     tmem_relinquish();
   }
+  for (int e = threadIdx.x; e < a.E; e += kStreamThreads) s_cnt[e] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(misc);
   griddep_wait();   // the routing kernel's ids, p and zeroed counters
+  int next_id = 0;  // warp 0, lane 0: the chunk taken last
+  if (threadIdx.x == 0) next_id = static_cast<int>(atomicAdd(a.queue, 1u));
 
-  // ---- lists: for every expert its pairs in order
-  for (int i = threadIdx.x; i < P2; i += kStreamThreads)
-    s_ids[i] = i < P ? static_cast<uint16_t>(__ldcg(a.ids + i)) : static_cast<uint16_t>(0xFFFFu);
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kStreamThreads) {
-    const uint32_t key = static_cast<uint32_t>(e) * 0x10001u;
-    uint32_t n = 0;
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(s_ids);
-    for (int i = 0; i < P2 / 2; ++i) n += __popc(__vcmpeq2(w[i], key));
-    s_cnt[e] = static_cast<uint16_t>(n / 16);
+  // ---- lists: every expert's pairs in order
+  for (int i = threadIdx.x; i < P8; i += kStreamThreads) {
+    int e = 0xFFFF;
+    if (i < P) {
+      e = __ldcg(a.ids + i);
+      atomicAdd(s_cnt + e, 1);
+    }
+    s_ids[i] = static_cast<uint16_t>(e);
   }
   __syncthreads();
   if (warp == 0) {
@@ -311,11 +328,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const unsigned int some = __ballot_sync(0xffffffffu, n > 0);
       if (e < a.E) {
         s_off[e] = static_cast<uint16_t>(off + incl - n);
-        if (n > 0) {
-          const int q = act + __popc(some & ((1u << lane) - 1u));
-          s_qi[e] = static_cast<uint16_t>(q);
-          s_act[q] = static_cast<uint16_t>(e);
-        }
+        if (n > 0)
+          s_act[act + __popc(some & ((1u << lane) - 1u))] = static_cast<uint16_t>(e);
       }
       off += __shfl_sync(0xffffffffu, incl, 31);
       act += __popc(some);
@@ -323,69 +337,106 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     if (lane == 0) misc[1] = static_cast<uint32_t>(act);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kStreamThreads) {
-    int left = s_cnt[e], pos = s_off[e];
-    for (int i = 0; left > 0; ++i)
-      if (s_ids[i] == e) {
-        s_list[pos] = static_cast<uint16_t>(i);
-        s_pos[i] = static_cast<uint16_t>(pos);
-        ++pos;
-        --left;
-      }
+  for (int i = threadIdx.x; i < P; i += kStreamThreads) {
+    // place: the expert's first one plus its pairs before this one
+    const uint32_t e = s_ids[i], key = e * 0x10001u;
+    uint32_t bits = 0;
+    int j = 0;
+    for (; j + 8 <= i; j += 8) {
+      const uint4 w = *reinterpret_cast<const uint4*>(s_ids + j);
+      bits += __popc(__vcmpeq2(w.x, key)) + __popc(__vcmpeq2(w.y, key)) +
+              __popc(__vcmpeq2(w.z, key)) + __popc(__vcmpeq2(w.w, key));
+    }
+    int pos = s_off[e] + static_cast<int>(bits >> 4);
+    for (; j < i; ++j) pos += s_ids[j] == e;
+    s_pos[i] = static_cast<uint16_t>(pos);
+    s_list[pos] = static_cast<uint16_t>(i);
   }
   __syncthreads();
   const int active = static_cast<int>(misc[1]);
-  const Phase up = phase_of(active, a.up_tiles, a.up_kb, cta, ctas);
-  const Phase down = phase_of(active, a.down_tiles, a.down_kb, cta, ctas);
+  Work w;
+  w.up_tiles = a.up_tiles;
+  w.up_kb = a.up_kb;
+  w.up_chunks = chunks_of(active, a.up_tiles, a.up_kb, P, ctas);
+  w.down_tiles = a.down_tiles;
+  w.down_kb = a.down_kb;
+  w.down_chunks = chunks_of(active, a.down_tiles, a.down_kb, P, ctas);
+  w.up = active * w.up_tiles * w.up_chunks;
+  w.total = w.up + active * w.down_tiles * w.down_chunks;
   const unsigned long long limit = a.wait_limit_ns;
   DeviceStatus* const st = a.status;
-  const unsigned int arrivals = static_cast<unsigned int>(kEpi * ctas);
+
+  // A consumer's next chunk number, -1 at the end (or when a wait gave up).
+  int qi = 0;
+  uint32_t qphase = 0;
+  auto next_chunk = [&]() -> int {   // one thread
+    if (!wait_parity(qfull_bar(qi), qphase, limit, st, 50)) return -1;
+    const int id = s_queue[qi];
+    mbar_arrive(qempty_bar(qi));
+    if (++qi == kQueue) {
+      qi = 0;
+      qphase ^= 1u;
+    }
+    return id;
+  };
+  auto next_chunk_warp = [&]() -> int {   // whole warp
+    int id = 0;
+    if (lane == 0) id = next_chunk();
+    return __shfl_sync(0xffffffffu, id, 0);
+  };
 
   if (warp == 0) {
-    // ---------------------------------------------------------- weights (TMA)
+    // ------------------------------------------- chunk numbers, weights (TMA)
     if (lane == 0) {
       const uint64_t policy = l2_evict_first_policy();
       int stage = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
-      for (int ph = 0; ph < 2 && ok; ++ph) {
-        const Phase& p = ph ? down : up;
-        for (long long x = p.beg; x < p.end && ok;) {
-          const Piece t = piece_at(p, x);
-          const int e = s_act[t.q];
-          // columns of the four boxes; one that lies past the matrix is skipped
-          int col[4], n = 0;
-          bool use[4];
-          for (int b = 0; b < 4; ++b) {
-            if (ph == 0) {
-              const int j = t.tile * 128 + (b & 1) * 64;
-              use[b] = j < a.I;
-              col[b] = (b >> 1) * a.I + j;
-            } else {
-              col[b] = t.tile * 256 + b * 64;
-              use[b] = col[b] < a.H;
-            }
-            n += use[b];
-          }
-          for (int kb = t.kb0; kb < t.kb1; ++kb) {
-            if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 40)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(n * 8192));
-            const uint32_t dst = base + static_cast<uint32_t>(stage * a.stage_bytes);
+      for (;;) {
+        const int id = ok && next_id < w.total ? next_id : -1;
+        if (!wait_parity(qempty_bar(qi), qphase ^ 1u, limit, st, 39)) break;
+        s_queue[qi] = id;
+        mbar_arrive(qfull_bar(qi));
+        if (++qi == kQueue) {
+          qi = 0;
+          qphase ^= 1u;
+        }
+        if (id < 0) break;
+        next_id = static_cast<int>(atomicAdd(a.queue, 1u));   // back by the end of this chunk
+        const Chunk t = chunk_at(w, id);
+        const int e = s_act[t.q];
+        // columns of the four boxes; one that lies past the matrix is skipped
+        int col[4], n = 0;
+        bool use[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-              if (use[b])
-                tma_load_3d_hint(dst + b * 8192, ph ? &tm2 : &tm1, full_bar(stage), col[b],
-                                 kb * 64, e, policy);
-            ++issued;
-            if (++stage == S) {
-              stage = 0;
-              phase ^= 1u;
-            }
+        for (int b = 0; b < 4; ++b) {
+          if (t.down) {
+            col[b] = t.tile * 256 + b * 64;
+            use[b] = col[b] < a.H;
+          } else {
+            const int j = t.tile * 128 + (b & 1) * 64;
+            use[b] = j < a.I;
+            col[b] = (b >> 1) * a.I + j;
           }
-          x += t.kb1 - t.kb0;
+          n += use[b];
+        }
+        const CUtensorMap* const tm = t.down ? &tm2 : &tm1;
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 40)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(n * 8192));
+          const uint32_t dst = base + static_cast<uint32_t>(stage * a.stage_bytes);
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (use[b])
+              tma_load_3d_hint(dst + b * 8192, tm, full_bar(stage), col[b], kb * 64, e, policy);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
       // loads still in flight must land before the CTA exits
@@ -400,48 +451,41 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       int stage = 0;
       uint32_t phase = 0, local = 0;
       bool ok = true;
-      for (int ph = 0; ph < 2 && ok; ++ph) {
-        const Phase& p = ph ? down : up;
-        for (long long x = p.beg; x < p.end && ok;) {
-          const Piece t = piece_at(p, x);
-          const int n = s_cnt[s_act[t.q]];
-          const int cols = ph ? 2 * round_up(n, 8) : round_up(n, 16);
-          const uint32_t idesc = make_idesc(0u, 128u, static_cast<uint32_t>(cols), 1u, 0u);
-          const uint32_t buf = local & 1u;
-          if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 42)) {
+      for (int id; ok && (id = next_chunk()) >= 0;) {
+        const Chunk t = chunk_at(w, id);
+        const int n = s_cnt[s_act[t.q]];
+        const int cols = t.down ? 2 * round_up(n, 8) : round_up(n, 16);
+        const uint32_t idesc = make_idesc(0u, 128u, static_cast<uint32_t>(cols), 1u, 0u);
+        const uint32_t buf = local & 1u;
+        if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 42)) break;
+        tc_fence_after();
+        const uint32_t d0 = tmem + buf * (2 * kAccCols);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wait_parity(full_bar(stage), phase, limit, st, 43) ||
+              !wait_parity(tok_bar(stage), phase, limit, st, 44)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t d0 = tmem + buf * (2 * kAccCols);
-          for (int kb = t.kb0; kb < t.kb1; ++kb) {
-            if (!wait_parity(full_bar(stage), phase, limit, st, 43) ||
-                !wait_parity(tok_bar(stage), phase, limit, st, 44)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t w0 = base + static_cast<uint32_t>(stage * a.stage_bytes);
-            const uint32_t x0 = w0 + kWeightBytes;
+          const uint32_t w0 = base + static_cast<uint32_t>(stage * a.stage_bytes);
+          const uint32_t x0 = w0 + kWeightBytes;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t bd = smem_desc_sw128(x0 + kk * 32, 16u, 1024u);
-              const uint32_t acc = (kb > t.kb0 || kk > 0) ? 1u : 0u;
-              mma_f16_ss(d0, smem_desc_sw128(w0 + kk * 2048, 8192u, 1024u), bd, idesc, acc);
-              mma_f16_ss(d0 + kAccCols, smem_desc_sw128(w0 + 16384 + kk * 2048, 8192u, 1024u), bd,
-                         idesc, acc);
-            }
-            mma_commit(empty_bar(stage));
-            if (++stage == S) {
-              stage = 0;
-              phase ^= 1u;
-            }
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t bd = smem_desc_sw128(x0 + kk * 32, 16u, 1024u);
+            const uint32_t acc = (kb > t.kb0 || kk > 0) ? 1u : 0u;
+            mma_f16_ss(d0, smem_desc_sw128(w0 + kk * 2048, 8192u, 1024u), bd, idesc, acc);
+            mma_f16_ss(d0 + kAccCols, smem_desc_sw128(w0 + 16384 + kk * 2048, 8192u, 1024u), bd,
+                       idesc, acc);
           }
-          if (!ok) break;
-          mma_commit(accf_bar(buf));
-          ++local;
-          x += t.kb1 - t.kb0;
+          mma_commit(empty_bar(stage));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
+        if (!ok) break;
+        mma_commit(accf_bar(buf));
+        ++local;
       }
       mma_commit(done_bar);
       settle_wait(done_bar, 0u, st, 45);
@@ -457,228 +501,246 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int stage = 0, seq = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int ph = 0; ph < 2 && ok; ++ph) {
-      if (ph == 1) {
-        // hid of every pair is written (by all CTAs)
-        if (lane == 0) ok = wait_count(a.bars, arrivals, limit, st, 46);
+    for (int id; ok && (id = next_chunk_warp()) >= 0;) {
+      const Chunk t = chunk_at(w, id);
+      const int e = s_act[t.q];
+      const int n = s_cnt[e], off = s_off[e], n8 = round_up(n, 8);
+      const int rows = t.down ? 2 * n : n;
+      const int K = t.down ? a.I : a.H;
+      if (t.down) {   // hid of the expert's pairs is written
+        if (lane == 0)
+          ok = wait_count(a.ready + t.q, static_cast<unsigned int>(kEpi * w.up_tiles), limit, st, 46);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        __syncwarp();
         if (!ok) break;
       }
-      const Phase& p = ph ? down : up;
-      const int K = ph ? a.I : a.H;
-      for (long long x = p.beg; x < p.end && ok;) {
-        const Piece t = piece_at(p, x);
-        const int e = s_act[t.q];
-        const int n = s_cnt[e], off = s_off[e], n8 = round_up(n, 8);
-        const int rows = ph ? 2 * n : n;
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++seq) {
-          if ((seq & (kLoaders - 1)) == l) {
-            if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 47)) {
-              ok = false;
-              break;
-            }
-            uint8_t* const dst = base_ptr + static_cast<size_t>(stage) * a.stage_bytes + kWeightBytes;
-            for (int i0 = 0; i0 < rows * 8; i0 += 32 * 4) {
-              uint4 v[4];
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++seq) {
+        if ((seq & (kLoaders - 1)) == l) {
+          if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 47)) {
+            ok = false;
+            break;
+          }
+          uint8_t* const dst = base_ptr + static_cast<size_t>(stage) * a.stage_bytes + kWeightBytes;
+          for (int i0 = 0; i0 < rows * 8; i0 += 32 * 4) {
+            uint4 v[4];
 #pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int i = i0 + 32 * u + lane;
-                const int r = i >> 3, k = kb * 64 + (i & 7) * 8;
-                v[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < rows && k < K) {
-                  if (ph == 0) {
-                    v[u] = __ldg(reinterpret_cast<const uint4*>(
-                        a.X + static_cast<long long>(s_list[off + r] / a.topk) * a.ldx + k));
-                  } else {
-                    const long long row = off + (r < n ? r : r - n + P);
-                    v[u] = __ldcg(reinterpret_cast<const uint4*>(a.hid + row * a.I + k));
-                  }
-                }
-              }
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const int i = i0 + 32 * u + lane;
-                const int r = i >> 3, c = i & 7;
-                if (r < rows) {
-                  const int rr = (ph && r >= n) ? r - n + n8 : r;
-                  *reinterpret_cast<uint4*>(dst + rr * 128 + ((c ^ (rr & 7)) << 4)) = v[u];
+            for (int u = 0; u < 4; ++u) {
+              const int i = i0 + 32 * u + lane;
+              const int r = i >> 3, k = kb * 64 + (i & 7) * 8;
+              v[u] = make_uint4(0u, 0u, 0u, 0u);
+              if (r < rows && k < K) {
+                if (t.down) {
+                  const long long row = off + (r < n ? r : r - n + P);
+                  v[u] = __ldcg(reinterpret_cast<const uint4*>(a.hid + row * a.I + k));
+                } else {
+                  v[u] = __ldg(reinterpret_cast<const uint4*>(
+                      a.X + static_cast<long long>(s_list[off + r] / a.topk) * a.ldx + k));
                 }
               }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tok_bar(stage));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int i = i0 + 32 * u + lane;
+              const int r = i >> 3, c = i & 7;
+              if (r < rows) {
+                const int rr = r >= n ? r - n + n8 : r;
+                *reinterpret_cast<uint4*>(dst + rr * 128 + ((c ^ (rr & 7)) << 4)) = v[u];
+              }
+            }
           }
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tok_bar(stage));
         }
-        x += t.kb1 - t.kb0;
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
   } else {
     // ---------------------------------------------------------- epilogue
     const int quad = warp & 3;                 // TMEM lanes 32 quad ..
     const int col = 32 * quad + lane;          // this thread's column of a 128-wide accumulator
+    const uint32_t buf = static_cast<uint32_t>(warp - 2 - kLoaders) / kEpi;   // every other chunk
     uint32_t local = 0;
-    bool ok = true;
-    for (int ph = 0; ph < 2 && ok; ++ph) {
-      const Phase& p = ph ? down : up;
-      for (long long x = p.beg; x < p.end;) {
-        const Piece t = piece_at(p, x);
-        const int e = s_act[t.q];
-        const int n = s_cnt[e], off = s_off[e], n8 = round_up(n, 8);
-        const uint32_t buf = local & 1u;
-        if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 48)) {
-          ok = false;
-          break;
+    for (int id; (id = next_chunk_warp()) >= 0; ++local) {
+      if ((local & 1u) != buf) continue;
+      const Chunk t = chunk_at(w, id);
+      const int e = s_act[t.q];
+      const int n = s_cnt[e], off = s_off[e], n8 = round_up(n, 8);
+      if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 48)) break;
+      tc_fence_after();
+      const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * (2 * kAccCols);
+      // hid of 8 tokens at column j
+      const int j = t.tile * 128 + col;
+      auto store_hid = [&](int r0, const float (&g)[8], const float (&u)[8]) {
+        if (j >= a.I) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (r0 + i < n) {
+            const float h = g[i] / (1.0f + expf(-g[i])) * u[i];
+            const uint16_t hi = moe_f2h(h);
+            // past the half range hi is infinite and stands alone
+            const uint16_t lo = (hi & 0x7FFFu) >= 0x7C00u ? 0 : moe_f2h(h - moe_h2f(hi));
+            const long long o = static_cast<long long>(off + r0 + i) * a.I + j;
+            a.hid[o] = hi;
+            a.hid[static_cast<long long>(P) * a.I + o] = lo;
+          }
+      };
+      float* const unit_part =
+          t.down ? nullptr
+                 : a.up_part + (static_cast<long long>(off) * w.up_tiles + t.tile * n) *
+                                   w.up_chunks * 256 + col;
+      for (int r0 = 0; r0 < n; r0 += 8) {
+        float v0[8], v1[8];
+        uint32_t g[8], h[8];
+        tmem_ld_32x32b_x8(d0 + r0, g);
+        tmem_ld_32x32b_x8(d0 + kAccCols + r0, h);
+        tmem_wait_ld2(g, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v0[i] = __uint_as_float(g[i]);
+          v1[i] = __uint_as_float(h[i]);
         }
-        tc_fence_after();
-        const uint32_t d0 =
-            tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * (2 * kAccCols);
-        const bool whole = t.kb0 == 0 && t.kb1 == p.kb;
-        const long long u0 = t.unit * p.kb;
-        // one chunk of 8 tokens of accumulator `acc`, hi and lo parts added
-        auto load8 = [&](int r0, float (&v0)[8], float (&v1)[8]) {
-          uint32_t g[8], h[8];
-          tmem_ld_32x32b_x8(d0 + r0, g);
-          tmem_ld_32x32b_x8(d0 + kAccCols + r0, h);
+        if (t.down) {
+          // hi and lo parts
+          tmem_ld_32x32b_x8(d0 + n8 + r0, g);
+          tmem_ld_32x32b_x8(d0 + kAccCols + n8 + r0, h);
           tmem_wait_ld2(g, h);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v0[i] = __uint_as_float(g[i]);
-            v1[i] = __uint_as_float(h[i]);
-          }
-          if (ph == 1) {
-            tmem_ld_32x32b_x8(d0 + n8 + r0, g);
-            tmem_ld_32x32b_x8(d0 + kAccCols + n8 + r0, h);
-            tmem_wait_ld2(g, h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              v0[i] += __uint_as_float(g[i]);
-              v1[i] += __uint_as_float(h[i]);
-            }
-          }
-        };
-        // hid of 8 tokens at column j
-        const int j = t.tile * 128 + col;
-        auto store_hid = [&](int r0, const float (&g)[8], const float (&u)[8]) {
-          if (j >= a.I) return;
+          const int c0 = t.tile * 256 + col;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (r0 + i < n) {
-              const float h = g[i] / (1.0f + expf(-g[i])) * u[i];
-              const uint16_t hi = moe_f2h(h);
-              const float rest = h - moe_h2f(hi);
-              // past the half range hi is infinite and stands alone
-              const uint16_t lo = (hi & 0x7FFFu) >= 0x7C00u ? 0 : moe_f2h(rest);
-              const long long o = static_cast<long long>(off + r0 + i) * a.I + j;
-              a.hid[o] = hi;
-              a.hid[static_cast<long long>(P) * a.I + o] = lo;
+              float* o = a.z + (static_cast<long long>(off + r0 + i) * w.down_chunks + t.c) * a.H;
+              if (c0 < a.H) __stcg(o + c0, v0[i] + __uint_as_float(g[i]));
+              if (c0 + 128 < a.H) __stcg(o + c0 + 128, v1[i] + __uint_as_float(h[i]));
             }
-        };
-        if (whole) {
-          for (int r0 = 0; r0 < n; r0 += 8) {
-            float v0[8], v1[8];
-            load8(r0, v0, v1);
-            if (ph == 0) {
-              store_hid(r0, v0, v1);
-            } else {
-              const int c0 = t.tile * 256 + col;
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (r0 + i < n) {
-                  float* o = a.z + static_cast<long long>(off + r0 + i) * a.H;
-                  if (c0 < a.H) __stcg(o + c0, v0[i]);
-                  if (c0 + 128 < a.H) __stcg(o + c0 + 128, v1[i]);
-                }
-            }
-          }
+        } else if (w.up_chunks == 1) {
+          store_hid(r0, v0, v1);
         } else {
-          float* const mine = part_of(a, p, ph, cta, ctas, u0) + col;
+          float* const mine = unit_part + t.c * n * 256;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (r0 + i < n) {
+              __stcg(mine + (r0 + i) * 128, v0[i]);
+              __stcg(mine + (n + r0 + i) * 128, v1[i]);
+            }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acce_bar(buf));   // the accumulators may be overwritten
+      if (t.down) {
+        if (lane == 0) add_release(a.done);
+        continue;
+      }
+      bool last = true;
+      if (w.up_chunks > 1) {
+        // the last of the unit's chunks to arrive adds them up in k order
+        unsigned int before = 0;
+        if (lane == 0) before = add_acq_rel(a.counters + t.unit * kEpi + quad);
+        last = __shfl_sync(0xffffffffu, before, 0) == static_cast<unsigned int>(w.up_chunks - 1);
+        __syncwarp();
+        if (last) {
           for (int r0 = 0; r0 < n; r0 += 8) {
-            float v0[8], v1[8];
-            load8(r0, v0, v1);
+            float v0[8] = {}, v1[8] = {};
+            if (n - r0 <= 2) {
+              // few tokens: the loads of eight chunks in flight
+              for (int c0 = 0; c0 < w.up_chunks; c0 += 8) {
+                float x[8][4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (r0 + i < n) {
-                __stcg(mine + (r0 + i) * 128, v0[i]);
-                __stcg(mine + (a.part_tokens + r0 + i) * 128, v1[i]);
-              }
-          }
-          if (ph == 0) {
-            // the last of the unit's pieces to arrive adds them up in k order
-            const int c0 = owner_of(p, u0), c1 = owner_of(p, u0 + p.kb - 1);
-            __threadfence();
-            __syncwarp();
-            unsigned int before = 0;
-            if (lane == 0) before = atomicAdd(a.counters + t.unit * kEpi + quad, 1u);
-            before = __shfl_sync(0xffffffffu, before, 0);
-            if (before == static_cast<unsigned int>(c1 - c0)) {
-              __threadfence();
-              for (int r0 = 0; r0 < n; r0 += 8) {
-                float v0[8] = {}, v1[8] = {};
-                for (int w = c0; w <= c1; ++w) {
-                  const float* src = part_of(a, p, ph, w, ctas, u0) + col;
+                for (int c = 0; c < 8; ++c) {
+                  const float* src = unit_part + static_cast<long long>(c0 + c) * n * 256;
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (r0 + i < n) {
-                      v0[i] += __ldcg(src + (r0 + i) * 128);
-                      v1[i] += __ldcg(src + (a.part_tokens + r0 + i) * 128);
-                    }
+                  for (int i = 0; i < 2; ++i) {
+                    const bool in = c0 + c < w.up_chunks && r0 + i < n;
+                    x[c][i] = in ? __ldcg(src + (r0 + i) * 128) : 0.0f;
+                    x[c][2 + i] = in ? __ldcg(src + (n + r0 + i) * 128) : 0.0f;
+                  }
                 }
-                store_hid(r0, v0, v1);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    v0[i] += x[c][i];
+                    v1[i] += x[c][2 + i];
+                  }
+              }
+            } else {
+#pragma unroll 2
+              for (int c = 0; c < w.up_chunks; ++c) {
+                const float* src = unit_part + static_cast<long long>(c) * n * 256;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (r0 + i < n) {
+                    v0[i] += __ldcg(src + (r0 + i) * 128);
+                    v1[i] += __ldcg(src + (n + r0 + i) * 128);
+                  }
               }
             }
+            store_hid(r0, v0, v1);
           }
+          __syncwarp();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acce_bar(buf));
-        ++local;
-        x += t.kb1 - t.kb0;
       }
-      // this warp's share of the phase is written
-      __threadfence();
-      __syncwarp();
-      if (ok && lane == 0) arrive_release(a.bars + ph);
+      if (last && lane == 0) add_release(a.ready + t.q);
     }
   }
 
-  // ---- sum: z of every pair is written; a warp per (token, 32 columns)
-  bool ready = true;
-  if (lane == 0) ready = wait_count(a.bars + 1, arrivals, limit, st, 49);
-  ready = __shfl_sync(0xffffffffu, ready ? 1 : 0, 0) != 0;
-  if (ready) {
-    const int strips = (a.H + 31) / 32;
-    for (int it = cta * kStreamWarps + warp; it < a.T * strips; it += ctas * kStreamWarps) {
+  // ---- sum: z of every pair is written.  `group` warps share a (token, 32
+  // columns) item, each with its own k; their terms meet in shared memory.
+  __syncthreads();   // the roles are done: the ring's memory is free, TMEM is read
+  bool* const s_ok = reinterpret_cast<bool*>(misc + 1);
+  if (threadIdx.x == 0)
+    *s_ok = wait_count(a.done, static_cast<unsigned int>(kEpi * (w.total - w.up)), limit, st, 49);
+  __syncthreads();
+  if (*s_ok) {
+    const int strips = (a.H + 31) / 32, items = a.T * strips;
+    int group = 1;   // 8 warps of the CTA take part
+    while (group < 8 && 2 * group * items <= 8 * ctas) group *= 2;
+    const int per = 8 / group;
+    float* const s_sum = reinterpret_cast<float*>(base_ptr);   // [8][32]
+    const int g = warp % group;
+    for (int it0 = cta * per; it0 < items; it0 += ctas * per) {
+      const int it = it0 + warp / group;
       const int t = it / strips, c = (it - t * strips) * 32 + lane;
-      const int tile = (it - t * strips) / 8;          // 256-column tile, uniform in the warp
-      const int in_tile = c - tile * 256;              // 0 .. 255
+      const bool mine = warp < 8 && it < items && c < a.H;
       float y = 0.0f;
-      for (int k = 0; k < a.topk; ++k) {
-        const int pair = t * a.topk + k, e = s_ids[pair], pos = s_pos[pair];
-        const long long u0 = (static_cast<long long>(s_qi[e]) * a.down_tiles + tile) * a.down_kb;
-        const int c0 = owner_of(down, u0), c1 = owner_of(down, u0 + a.down_kb - 1);
-        float z = 0.0f;
-        if (c0 == c1) {
-          if (c < a.H) z = __ldcg(a.z + static_cast<long long>(pos) * a.H + c);
-        } else {
-          const int r = pos - s_off[e];
-          for (int w = c0; w <= c1; ++w)
-            z += __ldcg(part_of(a, down, 1, w, ctas, u0) +
-                        ((in_tile >> 7) * a.part_tokens + r) * 128 + (in_tile & 127));
+      if (mine) {
+        for (int k0 = g; k0 < a.topk; k0 += 4 * group) {
+          float z[4], p[4];
+          const float* src[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int k = k0 + u * group;
+            const int pair = t * a.topk + min(k, a.topk - 1);
+            src[u] = a.z + static_cast<long long>(s_pos[pair]) * w.down_chunks * a.H + c;
+            p[u] = k < a.topk ? __ldcg(a.probs + pair) : 0.0f;
+            z[u] = k < a.topk ? __ldcg(src[u]) : 0.0f;
+          }
+          for (int ch = 1; ch < w.down_chunks; ++ch)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (k0 + u * group < a.topk) z[u] += __ldcg(src[u] + static_cast<long long>(ch) * a.H);
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (k0 + u * group < a.topk) y = fmaf(p[u], z[u], y);
         }
-        y = fmaf(__ldcg(a.probs + pair), z, y);
       }
-      if (c < a.H) {
+      if (group > 1) {
+        if (warp < 8) s_sum[warp * 32 + lane] = y;
+        __syncthreads();
+        if (g == 0 && mine)
+          for (int u = 1; u < group; ++u) y += s_sum[(warp + u) * 32 + lane];
+        __syncthreads();
+      }
+      if (g == 0 && mine) {
         uint16_t* o = a.Y + static_cast<long long>(t) * a.ldy + c;
         *o = moe_f2h(a.beta != 0.0f ? fmaf(a.beta, moe_h2f(*o), y) : y);
       }
     }
   }
-  __syncthreads();   // the epilogue warps have read TMEM, the MMAs are complete
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
@@ -691,7 +753,10 @@ bool moe_stream_fits(const MoeArgs& m) {
   const uintptr_t ptrs = reinterpret_cast<uintptr_t>(m.X) | reinterpret_cast<uintptr_t>(m.W1) |
                          reinterpret_cast<uintptr_t>(m.W2);
   // the rows of X, W1 (2I halves) and W2 (H) on the 16-byte grid
-  return (ptrs & 15u) == 0 && m.H % 8 == 0 && m.I % 8 == 0 && m.ldx % 8 == 0 && m.I > 0;
+  if ((ptrs & 15u) != 0 || m.H % 8 != 0 || m.I % 8 != 0 || m.ldx % 8 != 0 || m.I == 0) return false;
+  // k-blocks are counted in 32 bits
+  const long long kb = (m.H / 64 + 1ll) * (m.I / 64 + 1ll);
+  return kb * m.E < (1ll << 28);
 }
 
 int moe_stream(const MoeArgs& m, int sms, DeviceStatus* st, unsigned long long limit_ns,
@@ -728,13 +793,12 @@ int moe_stream(const MoeArgs& m, int sms, DeviceStatus* st, unsigned long long l
     s.up_kb = (m.H + 63) / 64;
     s.down_tiles = (m.H + 255) / 256;
     s.down_kb = (m.I + 63) / 64;
-    s.part_tokens = T;
     s.wait_limit_ns = limit_ns;
     s.status = st;
     // token rows of a stage: X rows padded to 16, or hi and lo rows padded to 8
     const int rows = std::max((T + 15) / 16 * 16, 2 * ((T + 7) / 8 * 8));
     s.stage_bytes = kWeightBytes + rows * 128;
-    const int lists = 8 * (3 * kMaxStages + 5) + 8 + 2 * (3 * (P + 1) + 4 * (m.E + 1));
+    const int lists = kFixedBytes + 2 * (3 * round_up(P, 8) + 2 * round_up(m.E, 2)) + 4 * m.E;
     s.stages = std::min(kMaxStages, (kSmemMax - 1024 - lists) / s.stage_bytes);
     if (s.stages < 2) return GEMM_ERR_ARG;
 
@@ -750,17 +814,25 @@ int moe_stream(const MoeArgs& m, int sms, DeviceStatus* st, unsigned long long l
     r.egroups = (m.E + 31) / 32;
     r.tblocks = (T + kRouteT - 1) / kRouteT;
     // K slices: about one CTA per SM in all, at most 16, none under 32 rows
-    const int want = std::max(1, std::min({sms / (r.egroups * r.tblocks), 16, m.H / 32}));
+    const int want = std::max(1, std::min({sms / (r.egroups * r.tblocks), kMaxSplits, m.H / 32}));
     r.rows_per_split = (m.H + want - 1) / want;
     r.splits = (m.H + r.rows_per_split - 1) / r.rows_per_split;
 
-    const long long units = 1ll * std::min(m.E, P) * s.up_tiles;
+    // most chunks of a unit over the numbers of experts that may be active
+    const int experts = std::min(m.E, P);
+    int up_chunks = 1, down_chunks = 1;
+    for (int n = 1; n <= experts; ++n) {
+      up_chunks = std::max(up_chunks, chunks_of(n, s.up_tiles, s.up_kb, P, sms));
+      down_chunks = std::max(down_chunks, chunks_of(n, s.down_tiles, s.down_kb, P, sms));
+    }
+    const long long units = 1ll * experts * s.up_tiles;
     const size_t b_part = round256(4 * static_cast<size_t>(r.splits) * T * m.E);
     const size_t b_ids = round256(4 * static_cast<size_t>(P));
     const size_t b_hid = round256(2 * 2 * static_cast<size_t>(P) * m.I);
-    const size_t b_z = round256(4 * static_cast<size_t>(P) * m.H);
-    const size_t b_ws = round256(4 * 2 * static_cast<size_t>(sms) * 2 * 2 * T * 128);
-    const size_t b_cnt = round256(4 * (static_cast<size_t>(units) * kEpi + 2));
+    const size_t b_z = round256(4 * static_cast<size_t>(P) * down_chunks * m.H);
+    const size_t b_ws = round256(4 * static_cast<size_t>(P) * s.up_tiles * up_chunks * 256);
+    const size_t n_zero = static_cast<size_t>(units) * kEpi + experts + 2;
+    const size_t b_cnt = round256(4 * n_zero);
     void *buf = nullptr, *zero = nullptr;
     if (int rc = routed_scratch(stream, b_part + 2 * b_ids + b_hid + b_z + b_ws + b_cnt, &buf,
                                 4 * static_cast<size_t>(kBlockT / kRouteT), &zero))
@@ -776,18 +848,20 @@ int moe_stream(const MoeArgs& m, int sms, DeviceStatus* st, unsigned long long l
     r.probs = reinterpret_cast<float*>(take(b_ids));
     s.hid = reinterpret_cast<uint16_t*>(take(b_hid));
     s.z = reinterpret_cast<float*>(take(b_z));
-    s.part = reinterpret_cast<float*>(take(b_ws));
-    s.bars = reinterpret_cast<unsigned int*>(take(b_cnt));
-    s.counters = s.bars + 2;
+    s.up_part = reinterpret_cast<float*>(take(b_ws));
+    s.queue = reinterpret_cast<unsigned int*>(take(b_cnt));
+    s.done = s.queue + 1;
+    s.ready = s.done + 1;
+    s.counters = s.ready + experts;
     s.ids = r.ids;
     s.probs = r.probs;
     r.counters = static_cast<unsigned int*>(zero);
-    r.zero = s.bars;
-    r.nzero = static_cast<int>(units * kEpi + 2);
+    r.zero = s.queue;
+    r.nzero = static_cast<int>(n_zero);
     r.ids_out = m.ids ? m.ids + static_cast<long long>(t0) * m.topk : nullptr;
     r.probs_out = m.probs ? m.probs + static_cast<long long>(t0) * m.topk : nullptr;
 
-    const size_t route_smem = static_cast<size_t>(kRouteT) * m.E * 5;
+    const size_t route_smem = 4 * static_cast<size_t>(kRouteT) * m.E;
     moe_logits_kernel<<<r.tblocks * r.egroups * r.splits, kRouteThreads, route_smem, stream>>>(r);
     if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
 
@@ -797,8 +871,8 @@ int moe_stream(const MoeArgs& m, int sms, DeviceStatus* st, unsigned long long l
     cfg.dynamicSmemBytes = static_cast<size_t>(s.stages) * s.stage_bytes + lists + 1024;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, moe_stream_kernel, tm1, tm2, s) != cudaSuccess)
