@@ -13,24 +13,19 @@
 // The path of this file serves every alignment: the shared product is the
 // library's half GEMM with a float result in scratch, and the kernels below
 // add the low-rank part to it in fp32.
-#include <cuda_fp16.h>
-
-#include <algorithm>
-#include <cstdint>
 #include <initializer_list>
 
-#include "gemm.h"
-#include "internal.h"
+#include "lora.h"
 
 namespace gb300 {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxRank = 128;
+constexpr int kMaxRank = kLoraMaxRank;
 
-__device__ __forceinline__ float h2f(uint16_t b) { return __half2float(__ushort_as_half(b)); }
-__device__ __forceinline__ uint16_t f2h(float x) { return __half_as_ushort(__float2half_rn(x)); }
+__device__ __forceinline__ float h2f(uint16_t b) { return lora_h2f(b); }
+__device__ __forceinline__ uint16_t f2h(float x) { return lora_f2h(x); }
 
 __device__ __forceinline__ float row_scale(const float* scales, int a) {
   return scales ? scales[a] : 1.0f;
@@ -216,23 +211,17 @@ int status_of(cudaError_t e) {
   return counted_launch(e) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+size_t round256(size_t x) { return lora_round256(x); }
+
+bool on16(const void* p, long long ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
+}
 
 bool misaligned(std::initializer_list<const void*> ptrs, size_t elem) {
   uintptr_t bits = 0;
   for (const void* p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);
   return (bits & (elem - 1)) != 0;
 }
-
-struct LoraArgs {
-  const uint16_t *X, *W, *A, *B;
-  const int* ids;
-  const float* scales;
-  int M, N, K, R, adapters;
-  int ldx, ldw, lda, ldb;
-  long long a_stride() const { return static_cast<long long>(K) * lda; }
-  long long b_stride() const { return static_cast<long long>(R) * ldb; }
-};
 
 int forward_any(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta, int sms,
                 cudaStream_t stream) {
@@ -333,6 +322,12 @@ int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint1
   unsigned long long limit = 0;
   if (int rc = query_device(&sms, &st, &limit)) return rc;
   const LoraArgs p{X, W, A, B, ids, scales, M, N, K, R, adapters, ldx, ldw, lda, ldb};
+  const LoraDevice d{sms, st, limit};
+  // TMA and 16-byte loads want every operand's rows on the 16-byte grid, and
+  // the ranks in groups of eight
+  if (M <= kLoraStreamRows && R % 8 == 0 && on16(X, ldx) && on16(W, ldw) && on16(A, lda) &&
+      on16(B, ldb))
+    return lora_stream(p, C, ldc, alpha, beta, d, stream);
   return forward_any(p, C, ldc, alpha, beta, sms, stream);
 }
 

@@ -1,0 +1,50 @@
+// lora.h -- what the files of the adapter products share.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "gemm.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace gb300 {
+
+constexpr int kLoraMaxRank = 128;
+
+struct LoraArgs {
+  const uint16_t *X, *W, *A, *B;
+  const int* ids;
+  const float* scales;
+  int M, N, K, R, adapters;
+  int ldx, ldw, lda, ldb;
+  long long a_stride() const { return static_cast<long long>(K) * lda; }
+  long long b_stride() const { return static_cast<long long>(R) * ldb; }
+};
+
+// What a launch needs to know of the device.
+struct LoraDevice {
+  int sms;
+  DeviceStatus* status;
+  unsigned long long wait_limit_ns;
+};
+
+// The forward for a few rows (M <= kLoraStreamRows): W streamed once.
+constexpr int kLoraStreamRows = 128;
+int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta,
+                const LoraDevice& d, cudaStream_t stream);
+
+__device__ __forceinline__ float lora_h2f(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+__device__ __forceinline__ uint16_t lora_f2h(float x) {
+  return __half_as_ushort(__float2half_rn(x));
+}
+__device__ __forceinline__ float2 lora_h2f2(uint32_t bits) {
+  __half2 h;
+  memcpy(&h, &bits, 4);
+  return __half22float2(h);
+}
+
+inline size_t lora_round256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace gb300

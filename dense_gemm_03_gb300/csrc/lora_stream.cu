@@ -1,0 +1,458 @@
+// lora_stream.cu -- the adapter product for a few rows (decoding), where the
+// time is that of streaming W (and the adapters) from HBM once.
+//
+//   lora_shrink_kernel   V = s X A by (row, K slice) on CUDA cores: at most 128
+//                        rows x K x R multiply-adds, nothing beside the bytes
+//   row_stream_kernel    X W as fp32 partial sums by (128 columns, K chunk): W
+//                        is the M operand of tcgen05.mma, the rows of X the N
+//                        operand, both by TMA.  It does not depend on the
+//                        shrink, which runs beside it on the same SMs
+//                        (programmatic launch).
+//   lora_combine_kernel  C = alpha (sum of the chunks + V B[a]) + beta C, the
+//                        chunks in k order, everything fp32, one rounding
+//
+// The low-rank product stays on CUDA cores here: each row has its own B[a], so
+// on the tensor cores it would be 128 rows of zeros per adapter for 2 R
+// multiply-adds per output that hide behind the loads of B anyway.
+//
+// Shared memory per ring stage: two 64-column boxes of 64 k-rows of W (128-byte
+// swizzle, MN-major: LBO 8 KB, SBO 1 KB), then the rows of X, 64 halves of k
+// each (K-major, SBO 1 KB).
+#include "lora.h"
+
+namespace gb300 {
+namespace {
+
+// ------------------------------------------------------------------- shrink
+constexpr int kShrinkThreads = 256;
+constexpr int kMaxSlices = 16;
+
+struct ShrinkArgs {
+  const uint16_t *X, *A;
+  const int* ids;
+  const float* scales;
+  float* V;              // [row][slice][R]
+  long long ldx, lda, a_stride;
+  int M, K, R, adapters;
+  int slices, len;       // K slices of `len` (the last may be shorter)
+};
+
+// One block per (row, slice): thread (k, v) multiplies x[k] with the eight
+// ranks 8v .. 8v + 7 of row k of A[a].
+__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const ShrinkArgs p) {
+  __shared__ float red[kShrinkThreads * 9];
+  __shared__ float red2[kShrinkThreads];
+  griddep_launch_dependents();
+  const int i = blockIdx.x / p.slices, slice = blockIdx.x - i * p.slices;
+  const int a = p.ids[i];
+  float* const out = p.V + (static_cast<long long>(i) * p.slices + slice) * p.R;
+  if (a < 0 || a >= p.adapters) {
+    for (int r = threadIdx.x; r < p.R; r += kShrinkThreads) out[r] = 0.0f;
+    return;
+  }
+  const int nv = p.R >> 3, step = kShrinkThreads / nv;   // k rows per pass
+  const int k0 = slice * p.len, k1 = min(p.K, k0 + p.len);
+  const int tk = threadIdx.x / nv, v = threadIdx.x - tk * nv;
+  float acc[8] = {};
+  if (tk < step) {
+    const uint16_t* x = p.X + static_cast<long long>(i) * p.ldx;
+    const uint16_t* f = p.A + static_cast<long long>(a) * p.a_stride + 8 * v;
+#pragma unroll 4
+    for (int k = k0 + tk; k < k1; k += step) {
+      const float xv = lora_h2f(__ldg(x + k));
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(f + static_cast<long long>(k) * p.lda));
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 c = lora_h2f2(h[j]);
+        acc[2 * j] = fmaf(xv, c.x, acc[2 * j]);
+        acc[2 * j + 1] = fmaf(xv, c.y, acc[2 * j + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[threadIdx.x * 9 + j] = acc[j];
+  __syncthreads();
+  // rank r: the `step` threads' terms in `parts` interleaved groups, then those
+  const int parts = kShrinkThreads / p.R;
+  const int r = threadIdx.x % p.R, part = threadIdx.x / p.R;
+  if (part < parts) {
+    float s = 0.0f;
+    for (int t = part; t < step; t += parts) s += red[(t * nv + (r >> 3)) * 9 + (r & 7)];
+    red2[part * p.R + r] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < p.R) {
+    float s = 0.0f;
+    for (int t = 0; t < parts; ++t) s += red2[t * p.R + threadIdx.x];
+    out[threadIdx.x] = (p.scales ? p.scales[a] : 1.0f) * s;
+  }
+}
+
+// ------------------------------------------------------------------- stream
+constexpr int kWBytes = 2 * 64 * 128;       // 128 columns of a k-block of W
+constexpr int kMaxStages = 12;
+constexpr int kEpi = 4;
+constexpr int kStreamThreads = 32 * (2 + kEpi);
+constexpr int kAccCols = 128;
+constexpr int kTmemCols = 2 * kAccCols;
+constexpr int kSmemMax = 232448;
+
+struct StreamArgs {
+  int M, N;
+  int kb, chunks, items;   // k-blocks, chunks per unit, units x chunks
+  int stages, stage_bytes, n_cols;
+  float* part;             // [unit][chunk][row][128]
+  unsigned long long wait_limit_ns;
+  DeviceStatus* status;
+};
+
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    row_stream_kernel(const __grid_constant__ CUtensorMap tmW,
+                      const __grid_constant__ CUtensorMap tmX, const StreamArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const int S = p.stages;
+  const int warp = warp_id_uniform(), lane = static_cast<int>(lane_id());
+  const uint32_t bars = base + static_cast<uint32_t>(S * p.stage_bytes);
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (kMaxStages + s); };
+  auto accf_bar = [&](uint32_t b) { return bars + 8u * (2 * kMaxStages + b); };
+  auto acce_bar = [&](uint32_t b) { return bars + 8u * (2 * kMaxStages + 2 + b); };
+  const uint32_t done_bar = bars + 8u * (2 * kMaxStages + 4);
+  constexpr int kBars = 2 * kMaxStages + 5;
+  uint8_t* const tmem_ptr = base_ptr + static_cast<size_t>(S) * p.stage_bytes + 8 * kBars;
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1u);
+      mbar_init(empty_bar(s), 1u);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1u);
+      mbar_init(acce_bar(b), static_cast<uint32_t>(kEpi));
+    }
+    mbar_init(done_bar, 1u);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_ptr), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+  const unsigned long long limit = p.wait_limit_ns;
+  DeviceStatus* const st = p.status;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t policy = l2_evict_first_policy();
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+        const int unit = it / p.chunks, c = it - unit * p.chunks;
+        const int n0 = unit * 128;
+        const bool two = n0 + 64 < p.N;      // the second box lies in the matrix
+        const uint32_t bytes =
+            static_cast<uint32_t>((two ? kWBytes : kWBytes / 2) + p.n_cols * 128);
+        for (int kb = c * p.kb / p.chunks; kb < (c + 1) * p.kb / p.chunks; ++kb) {
+          if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 60)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = base + static_cast<uint32_t>(stage * p.stage_bytes);
+          mbar_arrive_expect_tx(full_bar(stage), bytes);
+          tma_load_2d_hint(dst, &tmW, full_bar(stage), n0, kb * 64, policy);
+          if (two) tma_load_2d_hint(dst + 8192, &tmW, full_bar(stage), n0 + 64, kb * 64, policy);
+          tma_load_2d(dst + kWBytes, &tmX, full_bar(stage), kb * 64, 0);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      const uint32_t n = min(issued, static_cast<uint32_t>(S));
+      for (uint32_t i = issued - n; i < issued; ++i)
+        settle_wait(full_bar(static_cast<int>(i % S)), (i / S) & 1u, st, 61);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc(0u, 128u, static_cast<uint32_t>(p.n_cols), 1u, 0u);
+      int stage = 0;
+      uint32_t phase = 0, local = 0;
+      bool ok = true;
+      for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
+        const int c = it % p.chunks;
+        const int kb0 = c * p.kb / p.chunks, kb1 = (c + 1) * p.kb / p.chunks;
+        const uint32_t buf = local & 1u;
+        if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 62)) break;
+        tc_fence_after();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_parity(full_bar(stage), phase, limit, st, 63)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w0 = base + static_cast<uint32_t>(stage * p.stage_bytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss(tmem + buf * kAccCols, smem_desc_sw128(w0 + kk * 2048, 8192u, 1024u),
+                       smem_desc_sw128(w0 + kWBytes + kk * 32, 16u, 1024u), idesc,
+                       (kb > kb0 || kk > 0) ? 1u : 0u);
+          mma_commit(empty_bar(stage));
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit(accf_bar(buf));
+        ++local;
+      }
+      mma_commit(done_bar);
+      settle_wait(done_bar, 0u, st, 64);
+    }
+    __syncwarp();
+  } else {
+    const int quad = warp & 3;
+    uint32_t local = 0;
+    for (int it = blockIdx.x; it < p.items; it += gridDim.x, ++local) {
+      const uint32_t buf = local & 1u;
+      if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 65)) break;
+      tc_fence_after();
+      const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * kAccCols;
+      float* const out = p.part + static_cast<long long>(it) * p.M * 128 + 32 * quad + lane;
+      for (int r0 = 0; r0 < p.M; r0 += 16) {   // n_cols is a multiple of 16
+        uint32_t g[8], h[8];
+        tmem_ld_32x32b_x8(d0 + r0, g);
+        tmem_ld_32x32b_x8(d0 + r0 + 8, h);
+        tmem_wait_ld2(g, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (r0 + i < p.M) __stcg(out + (r0 + i) * 128, __uint_as_float(g[i]));
+          if (r0 + 8 + i < p.M) __stcg(out + (r0 + 8 + i) * 128, __uint_as_float(h[i]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acce_bar(buf));
+    }
+    // this kernel's end stands for the shrink's too (the combine waits for it)
+    griddep_wait();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ------------------------------------------------------------------ combine
+constexpr int kCombThreads = 128;
+
+struct CombineArgs {
+  const float *part, *V;
+  const uint16_t* B;
+  const int* ids;
+  uint16_t* C;
+  long long ldb, b_stride, ldc;
+  int M, N, R, adapters, chunks, slices;
+  float alpha, beta;
+  bool vec_c;              // rows of C on the 8-byte grid
+};
+
+// One block per (row, 512 columns), four columns a thread.
+__global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const CombineArgs p) {
+  __shared__ float vs[kLoraMaxRank];
+  const int strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
+  const int i = blockIdx.x / strips;
+  const int c = (blockIdx.x - i * strips) * 4 * kCombThreads + 4 * static_cast<int>(threadIdx.x);
+  const int a = p.ids[i];
+  const bool has = a >= 0 && a < p.adapters;
+  const bool whole = c + 4 <= p.N;
+  const uint16_t* const f = p.B + (has ? static_cast<long long>(a) * p.b_stride : 0) + c;
+  // nothing of the kernels before this one is read yet: bring this block's
+  // part of B[a] into L2
+  if (has && c < p.N && (threadIdx.x & 15) == 0)
+    for (int r = 0; r < p.R; ++r) prefetch_l2(f + r * p.ldb);
+  griddep_wait();
+  if (has)
+    for (int r = threadIdx.x; r < p.R; r += kCombThreads) {
+      const float* v = p.V + static_cast<long long>(i) * p.slices * p.R + r;
+      float s = 0.0f;
+      for (int k = 0; k < p.slices; ++k) s += __ldcg(v + k * p.R);
+      vs[r] = s;
+    }
+  __syncthreads();
+  if (c >= p.N) return;
+  const float* part = p.part + (static_cast<long long>(c >> 7) * p.chunks * p.M + i) * 128 + (c & 127);
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = 0; k < p.chunks; ++k) {
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(part + static_cast<long long>(k) * p.M * 128));
+    s.x += t.x;
+    s.y += t.y;
+    s.z += t.z;
+    s.w += t.w;
+  }
+  float o[4] = {s.x, s.y, s.z, s.w};
+  if (has) {
+    float l[4] = {};
+    if (whole) {
+#pragma unroll 8
+      for (int r = 0; r < p.R; ++r) {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(f + r * p.ldb));
+        const float2 b0 = lora_h2f2(b.x), b1 = lora_h2f2(b.y);
+        l[0] = fmaf(vs[r], b0.x, l[0]);
+        l[1] = fmaf(vs[r], b0.y, l[1]);
+        l[2] = fmaf(vs[r], b1.x, l[2]);
+        l[3] = fmaf(vs[r], b1.y, l[3]);
+      }
+    } else {
+      for (int r = 0; r < p.R; ++r)
+        for (int j = 0; j < p.N - c; ++j) l[j] = fmaf(vs[r], lora_h2f(f[r * p.ldb + j]), l[j]);
+    }
+    for (int j = 0; j < 4; ++j) o[j] += l[j];
+  }
+  uint16_t* const dst = p.C + static_cast<long long>(i) * p.ldc + c;
+  if (whole && p.vec_c) {
+    float old[4] = {};
+    if (p.beta != 0.0f) {
+      const uint2 b = *reinterpret_cast<const uint2*>(dst);
+      const float2 b0 = lora_h2f2(b.x), b1 = lora_h2f2(b.y);
+      old[0] = b0.x; old[1] = b0.y; old[2] = b1.x; old[3] = b1.y;
+    }
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      h[j] = lora_f2h(p.beta != 0.0f ? fmaf(p.alpha, o[j], p.beta * old[j]) : p.alpha * o[j]);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  } else {
+    for (int j = 0; j < 4 && c + j < p.N; ++j)
+      dst[j] = lora_f2h(p.beta != 0.0f ? fmaf(p.alpha, o[j], p.beta * lora_h2f(dst[j]))
+                                       : p.alpha * o[j]);
+  }
+}
+
+// Chunks per unit: the count whose rounds of chunks over the SMs, in k-block
+// times of an SM (16 KB at its share of HBM, ~0.36 us), and whose partial sums
+// (1 KB per row written and read, through L2 at about twice HBM's rate) take
+// least.
+int plan_chunks(int units, int kb, int M, int sms) {
+  int best = 1;
+  double best_t = 1e30;
+  for (int c = 1; c <= std::min(kb, 32); ++c) {
+    const long long rounds = (1ll * units * c + sms - 1) / sms;
+    const double t = static_cast<double>(rounds) * ((kb + c - 1) / c + 2) +
+                     1.9e-4 * units * c * M;
+    if (t < best_t) {
+      best_t = t;
+      best = c;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
+int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta,
+                const LoraDevice& d, cudaStream_t stream) {
+  const int units = (p.N + 127) / 128, kb = (p.K + 63) / 64;
+  const int rows = (p.M + 15) / 16 * 16;
+  CUtensorMap tmW{}, tmX{};
+  if (int rc = encode_map_f16(&tmW, p.W, p.K, p.N, p.ldw, 64, 64)) return rc;
+  if (int rc = encode_map_f16(&tmX, p.X, p.M, p.K, p.ldx, 64, rows)) return rc;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
+  static bool configured[64] = {};
+  if (dev < 64 && !configured[dev]) {
+    if (cudaFuncSetAttribute(row_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMax) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+    configured[dev] = true;
+  }
+  ShrinkArgs s{};
+  // about four blocks per SM in all, slices of at least 64
+  const int want = std::max(1, std::min({kMaxSlices, 4 * d.sms / p.M, p.K / 64}));
+  s.len = (p.K + want - 1) / want;
+  s.slices = (p.K + s.len - 1) / s.len;
+  StreamArgs t{};
+  t.M = p.M;
+  t.N = p.N;
+  t.kb = kb;
+  t.chunks = plan_chunks(units, kb, p.M, d.sms);
+  if (1ll * units * t.chunks > (1 << 30)) return GEMM_ERR_ARG;
+  t.items = units * t.chunks;
+  t.n_cols = rows;
+  t.stage_bytes = kWBytes + rows * 128;
+  t.stages = std::min(kMaxStages, (kSmemMax - 2048) / t.stage_bytes);
+  t.wait_limit_ns = d.wait_limit_ns;
+  t.status = d.status;
+
+  const size_t v_bytes = lora_round256(4 * static_cast<size_t>(p.M) * s.slices * p.R);
+  const size_t part_bytes = 4 * static_cast<size_t>(t.items) * p.M * 128;
+  void* buf = nullptr;
+  if (int rc = routed_scratch(stream, v_bytes + part_bytes, &buf)) return rc;
+  s.V = static_cast<float*>(buf);
+  t.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + v_bytes);
+  s.X = p.X;
+  s.A = p.A;
+  s.ids = p.ids;
+  s.scales = p.scales;
+  s.ldx = p.ldx;
+  s.lda = p.lda;
+  s.a_stride = p.a_stride();
+  s.M = p.M;
+  s.K = p.K;
+  s.R = p.R;
+  s.adapters = p.adapters;
+  lora_shrink_kernel<<<p.M * s.slices, kShrinkThreads, 0, stream>>>(s);
+  if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
+
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(t.items, d.sms)), 1, 1);
+  cfg.blockDim = dim3(kStreamThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(t.stages) * t.stage_bytes + 2048;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (counted_launch(cudaLaunchKernelEx(&cfg, row_stream_kernel, tmW, tmX, t)) != cudaSuccess)
+    return GEMM_ERR_CUDA;
+
+  CombineArgs c{};
+  c.part = t.part;
+  c.V = s.V;
+  c.B = p.B;
+  c.ids = p.ids;
+  c.C = C;
+  c.ldb = p.ldb;
+  c.b_stride = p.b_stride();
+  c.ldc = ldc;
+  c.M = p.M;
+  c.N = p.N;
+  c.R = p.R;
+  c.adapters = p.adapters;
+  c.chunks = t.chunks;
+  c.slices = s.slices;
+  c.alpha = alpha;
+  c.beta = beta;
+  c.vec_c = (reinterpret_cast<uintptr_t>(C) & 7u) == 0 && ldc % 4 == 0;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.M * ((p.N + 4 * kCombThreads - 1) / (4 * kCombThreads))), 1, 1);
+  cfg.blockDim = dim3(kCombThreads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  if (counted_launch(cudaLaunchKernelEx(&cfg, lora_combine_kernel, c)) != cudaSuccess)
+    return GEMM_ERR_CUDA;
+  set_last_path("lora.stream");
+  return GEMM_OK;
+}
+
+}  // namespace gb300
