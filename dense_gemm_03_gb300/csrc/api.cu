@@ -509,11 +509,16 @@ int check_common(const void* A, const void* B, const void* C, int M, int N, int 
 thread_local char t_path_buf[96];
 
 // Half-precision operands, fp32 accumulation; C is half (c_f32 false) or
-// float (c_f32 true).
+// float (c_f32 true).  `lora`: adapters beside the product, on CTA pairs
+// whatever path is forced; its B may be stored transposed.
 int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int M, int N, int K,
                   long long lda, long long ldb, long long ldc, float alpha, float beta,
-                  cudaStream_t stream) {
-  if (int rc = check_common(A, B, C, M, N, K, lda, ldb, ldc, alpha, 2)) return rc;
+                  cudaStream_t stream, const LoraCall* lora = nullptr) {
+  const bool trans_b = lora && lora->trans;
+  // rows and columns of B as it is stored
+  const int b_rows = trans_b ? N : K, b_cols = trans_b ? K : N;
+  if (int rc = check_common(A, B, C, M, N, K, lda, trans_b ? N : ldb, ldc, alpha, 2)) return rc;
+  if (trans_b && ldb < K) return GEMM_ERR_LD;
   if (c_f32 && (reinterpret_cast<uintptr_t>(C) & 3u)) return GEMM_ERR_ARG;
   if (M == 0 || N == 0) {
     t_last_path = "noop";
@@ -531,7 +536,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
   }
 
-  const int force = g_force_path.load();
+  const int force = lora ? 0 : g_force_path.load();
   int bn = N <= 64 ? 64 : (N <= 128 ? 128 : 256);
   // A single row of 256-wide tiles that cannot fill the SMs: narrower tiles
   // give more of them, so fewer K slices are needed.
@@ -553,10 +558,10 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   uint16_t* c_user = nullptr;   // the caller's C when the GEMM writes an aligned copy
   long long ldc_user = 0;
   if ((!a_tma || !b_tma || (!c_f32 && !c_tma)) && force != 2) {
-    const long long lda2 = (K + 7) / 8 * 8, ldb2 = (N + 7) / 8 * 8, ldc2 = (N + 7) / 8 * 8;
+    const long long lda2 = (K + 7) / 8 * 8, ldb2 = (b_cols + 7) / 8 * 8, ldc2 = (N + 7) / 8 * 8;
     auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t a_bytes = a_tma ? 0 : round256(static_cast<size_t>(M) * lda2 * 2);
-    const size_t b_bytes = b_tma ? 0 : round256(static_cast<size_t>(K) * ldb2 * 2);
+    const size_t b_bytes = b_tma ? 0 : round256(static_cast<size_t>(b_rows) * ldb2 * 2);
     const size_t c_bytes = (c_f32 || c_tma) ? 0 : round256(static_cast<size_t>(M) * ldc2 * 2);
     if (a_bytes + b_bytes + c_bytes <= (static_cast<size_t>(1) << 31)) {
       std::lock_guard<std::mutex> lk(g_mu);
@@ -579,7 +584,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
       }
       if (!b_tma) {
         uint16_t* dst = reinterpret_cast<uint16_t*>(buf);
-        add(RealignJob{B, ldb, dst, ldb2, K, N}, 1ll * K * ldb2 / 8);
+        add(RealignJob{B, ldb, dst, ldb2, b_rows, b_cols}, 1ll * b_rows * ldb2 / 8);
         B = dst;
         ldb = ldb2;
         buf += b_bytes;
@@ -606,7 +611,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   int epi = c_f32 ? kEpiF32 : ((c_tma && force != 2) ? kEpiTma : kEpiManual);
 
   TcArgs a{};
-  a.pdl = prepass;   // the realignment copy was launched just before
+  a.pdl = prepass || lora;   // the realignment copy (the adapters' shrink) was launched just before
   a.A = A;
   a.B = B;
   a.C = c_f32 ? nullptr : static_cast<uint16_t*>(C);
@@ -635,7 +640,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   // equal K slices instead.
   // Few tiles for many SMs: stream-K over all tiles when it beats half-width
   // whole-K units (few_sk; then one CTA per worker, no pairs).
-  const bool few = tiles * 2 <= d->sm_count && a.kb_total >= 8;
+  const bool few = !lora && tiles * 2 <= d->sm_count && a.kb_total >= 8;
   // Tall shapes (one column of 64-wide tiles): 64-row tiles (M = 64 MMAs)
   // double the tiles, so that whole-K units fill one wave without stream-K
   // partial sums.
@@ -815,7 +820,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   // that form (64-wide single-CTA tiles, 256-wide pairs, TMA epilogue)
   int kpb = 1;
   const int fk = g_stage_kblocks.load();
-  const bool two_ok = load == kLoadTma && epi == kEpiTma && !m64 &&
+  const bool two_ok = !lora && load == kLoadTma && epi == kEpiTma && !m64 &&
                       ((pair && bn == 256) || (!pair && bn == 64));
   if (fk == 2 && two_ok) {
     kpb = 2;
@@ -832,7 +837,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   CUtensorMap tmA{}, tmB{}, tmC{};
   if (load == kLoadTma) {
     if (int rc = make_map_f16(&tmA, A, M, K, lda, 64, am)) return rc;
-    if (int rc = make_map_f16(&tmB, B, K, N, ldb, 64, 64)) return rc;
+    if (int rc = make_map_f16(&tmB, B, b_rows, b_cols, ldb, 64, 64)) return rc;
   }
   if (epi == kEpiTma) {
     // epilogue staging tile: 32 rows (16 on 64-row tiles) x 32 halves, 64-byte swizzle
@@ -862,10 +867,25 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
                                : (epi == kEpiF32 ? "epi_f32" : (epi == kEpiTma ? "epi_tma" : "epi_manual")),
              kpb == 2 ? ".kb2" : "", cut, how);
     t_last_path = t_path_buf;
+    if (lora) {
+      const LoraTailArgs& x = lora->tail;
+      if (epi != kEpiTma) return GEMM_ERR_ARG;
+      CUtensorMap tmE{};
+      if (int rc = trans_b ? encode_map_f16_stack(&tmE, x.F, N, x.R, x.ldf, x.adapters, x.f_stride,
+                                                  64, 64)
+                           : encode_map_f16_stack(&tmE, x.F, x.R, N, x.ldf, x.adapters, x.f_stride,
+                                                  64, 32))
+        return rc;
+      if (launch_gemm_f16_tc_lora(trans_b, epi, tmA, tmB, tmC, tmE, x, a, grid, stream) !=
+          cudaSuccess)
+        return GEMM_ERR_CUDA;
+      return copy_back();
+    }
     if (launch_gemm_f16_tc_pair(bn, epi, tmA, tmB, tmC, a, grid, stream, kpb) != cudaSuccess)
       return GEMM_ERR_CUDA;
     return copy_back();
   }
+  if (lora) return GEMM_ERR_ARG;   // not a shape of the pair kernel
   const int grid = static_cast<int>(nw);
   const int bi = bn == 64 ? 0 : (bn == 128 ? 1 : 2);
   const char* rows = m64 ? ".m64" : (am == 32 ? ".a32" : (am == 64 ? ".a64" : (kpb == 2 ? ".kb2" : "")));
@@ -1199,6 +1219,12 @@ int query_device(int* sm_count, DeviceStatus** status, unsigned long long* wait_
   *status = d->status;
   *wait_limit_ns = static_cast<unsigned long long>(g_wait_limit_ns.load());
   return GEMM_OK;
+}
+
+int gemm_f16_lora_pair(const uint16_t* A, const uint16_t* B, uint16_t* C, int M, int N, int K,
+                       long long lda, long long ldb, long long ldc, float alpha, float beta,
+                       const LoraCall& lora, cudaStream_t stream) {
+  return gemm_f16_impl(A, B, C, false, M, N, K, lda, ldb, ldc, alpha, beta, stream, &lora);
 }
 
 int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed,

@@ -475,11 +475,50 @@ __device__ __forceinline__ void add_partials(uint32_t (&acc)[32], const float4* 
   }
 }
 
-template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1>
-__global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
+// The plain product: nothing is added to a tile's K loop, B is stored K x N.
+struct NoLora {
+  static constexpr bool kOn = false;
+  static constexpr bool kTransB = false;
+  static constexpr int kWarps = 0;
+};
+
+// Low-rank adapters picked by row, as more k-blocks of the same accumulators
+// (CTA pairs, TMA loads).  A tile's K loop goes on, after its last k-block,
+// over the adapters that occur in its 256 rows: for adapter a and 32 of its
+// ranks, the A part of a stage holds, for the rows of a, those entries of V in
+// two halves (32 hi, then 32 lo columns; zeros in other rows), and the B part
+// the adapter's 32 rows of N columns, which both halves are multiplied with.
+// Two more warps write the A part.  TRANSB: B operands are stored N x K and
+// N x R (the gradient's dC W^T + U A^T): K-major tiles of 64-row boxes.
+template <bool TRANSB>
+struct LoraTail {
+  static constexpr bool kOn = true;
+  static constexpr bool kTransB = TRANSB;
+  static constexpr int kWarps = 2;
+  CUtensorMap tmE;        // the adapters' B operand, a stack
+  LoraTailArgs a;
+};
+
+__device__ __forceinline__ bool lora_bad(const LoraTailArgs& a, int e) {
+  static_assert(kLoraBadParts == 4, "one 16-byte load");
+  const int4 b = *(reinterpret_cast<const int4*>(a.bad) + e);
+  return (b.x | b.y | b.z | b.w) != 0;
+}
+
+// The adapter of entry j of a tile's list, or -1 when it is left to the
+// epilogue (its weights are not all finite).
+__device__ __forceinline__ int lora_entry(const LoraTailArgs& a, int blk, int j) {
+  const int e = a.lists[static_cast<long long>(blk) * kLoraListStride + 1 + j];
+  return lora_bad(a, e) ? -1 : e;
+}
+
+template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1,
+          class LORA = NoLora>
+__global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
     gemm_f16_tc_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmC, const TcArgs p) {
+                       const __grid_constant__ CUtensorMap tmC, const TcArgs p,
+                       const __grid_constant__ LORA x) {
   using R = Roles<LOAD>;
   using L = Smem<BN, EPI, PAIR, AM, KPB>;
   using Cfg = typename L::Cfg;
@@ -489,6 +528,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
   static_assert(KPB == 1 || LOAD == kLoadTma, "two k-blocks per stage take TMA loads");
   constexpr int S = Cfg::kStages;
   static_assert(!PAIR || (LOAD == kLoadTma && EPI != kEpiPartial), "pair configuration");
+  static_assert(!LORA::kOn || (PAIR && BN == 256 && KPB == 1), "adapters run on 256-wide pairs");
   // MM = 64: 64-row tiles (tcgen05.mma with M = 64), whole-K units only, TMA
   // loads of 64 rows of A and the TMA epilogue
   static_assert(MM == 128 || (MM == 64 && AM == 64 && !PAIR && EPI == kEpiTma), "64-row tiles");
@@ -515,6 +555,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
   const uint32_t tmem_free_bar = bars + 8u * (2 * S + 5);   // epilogue warps done with TMEM
   // C sub-tile landed in staging tile b of epilogue warp w
   auto cfull_bar = [&](int w, int b) { return bars + 8u * (2 * S + 6 + L::kBufs * w + b); };
+  // adapters: the V tile of stage s is written (by the warps of both CTAs)
+  auto vfull_bar = [&](int s) { return base + static_cast<uint32_t>(L::kUsed) + 8u * s; };
   auto stage_a = [&](int s) { return base + static_cast<uint32_t>(s * Cfg::kStageBytes); };
   auto stage_b = [&](int s) { return stage_a(s) + kAB; };
 
@@ -531,6 +573,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
     mbar_init(tmem_free_bar, static_cast<uint32_t>(R::kEpiWarps));
     for (int w = 0; w < 8; ++w)
       for (int b = 0; b < L::kBufs; ++b) mbar_init(cfull_bar(w, b), 1u);
+    if constexpr (LORA::kOn)
+      for (int s = 0; s < S; ++s) mbar_init(vfull_bar(s), 2u * LORA::kWarps);
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -603,9 +647,13 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
                 tma_load_2d_pair(sa, &tmA, fb, k0, t.m0);
 #pragma unroll
                 for (int c = 0; c < Cfg::kBStageCols / 64; ++c)
-                  if (64 * c < bcols)
-                    tma_load_2d_pair(sb + c * kBBlockBytes, &tmB, fb,
-                                     t.n0 + static_cast<int>(rank) * bcols + 64 * c, k0);
+                  if (64 * c < bcols) {
+                    const int n = t.n0 + static_cast<int>(rank) * bcols + 64 * c;
+                    if constexpr (LORA::kTransB)
+                      tma_load_2d_pair(sb + c * kBBlockBytes, &tmB, fb, k0, n);
+                    else
+                      tma_load_2d_pair(sb + c * kBBlockBytes, &tmB, fb, n, k0);
+                  }
               }
             } else {
               mbar_arrive_expect_tx(full_bar(stage), bytes);
@@ -632,6 +680,43 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
             if (++stage == S) {
               stage = 0;
               phase ^= 1u;
+            }
+          }
+          if constexpr (LORA::kOn) {
+            if (!ok || t.kb1 != p.kb_total) continue;
+            const int blk = (t.m0 - static_cast<int>(rank) * BM) / (2 * BM);
+            const int n = x.a.lists[static_cast<long long>(blk) * kLoraListStride];
+            const int bcols = t.ncols / 2;
+            // a box: 64 columns of 32 ranks, or 64 rows of 64 (32 used)
+            constexpr uint32_t kBox = LORA::kTransB ? 8192u : 4096u;
+            for (int j = 0; j < n && ok; ++j) {
+              const int e = lora_entry(x.a, blk, j);
+              if (e < 0) continue;
+              for (int c32 = 0; c32 < x.a.chunks; ++c32) {
+                if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 18)) {
+                  ok = false;
+                  break;
+                }
+                const uint32_t fb = map_to_cta(full_bar(stage), 0);
+                if (leader)
+                  mbar_arrive_expect_tx(full_bar(stage),
+                                        2u * static_cast<uint32_t>((bcols + 63) / 64) * kBox);
+                const uint32_t sb = stage_b(stage);
+#pragma unroll
+                for (int c = 0; c < Cfg::kBStageCols / 64; ++c)
+                  if (64 * c < bcols) {
+                    const int n0 = t.n0 + static_cast<int>(rank) * bcols + 64 * c;
+                    if constexpr (LORA::kTransB)
+                      tma_load_3d_pair(sb + c * kBBlockBytes, &x.tmE, fb, 32 * c32, n0, e);
+                    else
+                      tma_load_3d_pair(sb + c * kBBlockBytes, &x.tmE, fb, n0, 32 * c32, e);
+                  }
+                ++issued;
+                if (++stage == S) {
+                  stage = 0;
+                  phase ^= 1u;
+                }
+              }
             }
           }
         }
@@ -698,8 +783,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
   } else if (warp == R::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc_full = make_idesc(0u, PAIR ? 2 * BM : MM, BN, 0u, 1u);
-      constexpr uint32_t idesc_half = make_idesc(0u, PAIR ? 2 * BM : MM, BN / 2, 0u, 1u);
+      constexpr uint32_t kBMajor = LORA::kTransB ? 0u : 1u;
+      constexpr uint32_t idesc_full = make_idesc(0u, PAIR ? 2 * BM : MM, BN, 0u, kBMajor);
+      constexpr uint32_t idesc_half = make_idesc(0u, PAIR ? 2 * BM : MM, BN / 2, 0u, kBMajor);
+      uint32_t vphase = 0;   // adapters: bit s is the parity of stage s's next V tile
       int stage = 0;
       uint32_t phase = 0, local = 0;
       bool ok = true;
@@ -723,7 +810,9 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < BK / kUmmaK; ++kk) {
               const uint64_t ad = smem_desc_sw128(a0 + kk * (kUmmaK * 2), 16u, 1024u);
-              const uint64_t bd = smem_desc_sw128(b0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u);
+              const uint64_t bd =
+                  LORA::kTransB ? smem_desc_sw128(b0 + kk * (kUmmaK * 2), 16u, 1024u)
+                                : smem_desc_sw128(b0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u);
               const uint32_t acc = (kb > t.kb0 || j > 0 || kk > 0) ? 1u : 0u;
               if (PAIR)
                 mma_f16_ss_pair(d_tmem, ad, bd, idesc, acc);
@@ -739,6 +828,39 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
           if (++stage == S) {
             stage = 0;
             phase ^= 1u;
+          }
+        }
+        if constexpr (LORA::kOn) {
+          if (ok && t.kb1 == p.kb_total) {
+            const int blk = t.m0 / (2 * BM);
+            const int n = x.a.lists[static_cast<long long>(blk) * kLoraListStride];
+            for (int j = 0; j < n && ok; ++j) {
+              if (lora_entry(x.a, blk, j) < 0) continue;
+              for (int c32 = 0; c32 < x.a.chunks; ++c32) {
+                if (!wait_parity(full_bar(stage), phase, limit, st, 19) ||
+                    !wait_parity_cluster(vfull_bar(stage), (vphase >> stage) & 1u, limit, st, 20)) {
+                  ok = false;
+                  break;
+                }
+                vphase ^= 1u << stage;
+                tc_fence_after();
+                const uint32_t a0 = stage_a(stage), b0 = a0 + kAB;
+                const int steps = (min(32, x.a.R - 32 * c32) + kUmmaK - 1) / kUmmaK;
+                for (int kk = 0; kk < steps; ++kk) {
+                  const uint64_t bd =
+                      LORA::kTransB ? smem_desc_sw128(b0 + kk * (kUmmaK * 2), 16u, 1024u)
+                                    : smem_desc_sw128(b0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u);
+                  const uint32_t av = a0 + kk * (kUmmaK * 2);
+                  mma_f16_ss_pair(d_tmem, smem_desc_sw128(av, 16u, 1024u), bd, idesc, 1u);
+                  mma_f16_ss_pair(d_tmem, smem_desc_sw128(av + 64, 16u, 1024u), bd, idesc, 1u);
+                }
+                mma_commit_pair_multicast(empty_bar(stage), 3);
+                if (++stage == S) {
+                  stage = 0;
+                  phase ^= 1u;
+                }
+              }
+            }
           }
         }
         if (!ok) break;
@@ -772,6 +894,79 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
       tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
     else
       tmem_dealloc(tmem_base, Cfg::kTmemCols);
+  } else if (LORA::kOn && warp >= R::kWarps) {
+    // ------------------------------------------------------------ adapters' V tiles
+    // Warp v writes rows 64v .. 64v + 63 of this CTA's 128; eight lanes share a
+    // row, four ranks each.  The stage sequence is followed k-block by k-block
+    // (a parity wait may not skip a phase).
+    if constexpr (LORA::kOn) {
+      const int v = warp - R::kWarps;
+      const int q = lane & 7, r0 = 64 * v + (lane >> 3);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      auto wait_empty = [&]() {
+        if (lane == 0) ok = wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 21);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      };
+      auto advance = [&]() {
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      UnitCursor cur = first_unit(p, worker);
+      Unit t;
+      while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
+        for (int kb = t.kb0; kb < t.kb1 && ok; ++kb) {
+          wait_empty();
+          advance();
+        }
+        if (!ok || t.kb1 != p.kb_total) continue;
+        const int blk = (t.m0 - static_cast<int>(rank) * BM) / (2 * BM);
+        const int n = x.a.lists[static_cast<long long>(blk) * kLoraListStride];
+        for (int j = 0; j < n && ok; ++j) {
+          const int e = lora_entry(x.a, blk, j);
+          if (e < 0) continue;
+          for (int c32 = 0; c32 < x.a.chunks && ok; ++c32) {
+            // the 16 rows' entries, on their way while the stage is waited for
+            float4 f[16];
+            const int r = 32 * c32 + 4 * q;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int row = t.m0 + r0 + 4 * i;
+              f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (row < p.M && r < x.a.ldv && x.a.ids[row] == e)
+                f[i] = __ldcg(reinterpret_cast<const float4*>(
+                    x.a.V + static_cast<long long>(row) * x.a.ldv + r));
+            }
+            wait_empty();
+            if (!ok) break;
+            uint8_t* const sa = base_ptr + stage * Cfg::kStageBytes;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int lr = r0 + 4 * i;
+              const uint32_t h0 = float2_to_half2_bits(f[i].x, f[i].y);
+              const uint32_t h1 = float2_to_half2_bits(f[i].z, f[i].w);
+              const float2 g0 = half2_bits_to_float2(h0), g1 = half2_bits_to_float2(h1);
+              // past the half range the leading half is infinite and stands alone
+              const float l0 = isinf(g0.x) ? 0.0f : f[i].x - g0.x;
+              const float l1 = isinf(g0.y) ? 0.0f : f[i].y - g0.y;
+              const float l2 = isinf(g1.x) ? 0.0f : f[i].z - g1.x;
+              const float l3 = isinf(g1.y) ? 0.0f : f[i].w - g1.y;
+              uint8_t* const rowp = sa + lr * 128 + (q & 1) * 8;
+              *reinterpret_cast<uint2*>(rowp + (((q >> 1) ^ (lr & 7)) << 4)) = make_uint2(h0, h1);
+              *reinterpret_cast<uint2*>(rowp + (((4 + (q >> 1)) ^ (lr & 7)) << 4)) =
+                  make_uint2(float2_to_half2_bits(l0, l1), float2_to_half2_bits(l2, l3));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_cta(vfull_bar(stage), 0));
+            advance();
+          }
+        }
+      }
+    }
   } else {
     // ------------------------------------------------------------ epilogue
     // The 32-column sub-chunks of a unit are shared out between the kParts
@@ -1003,6 +1198,29 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
               }
             }
           }
+          if constexpr (LORA::kOn) {
+            // a row whose adapter has weights that are not all finite: added here,
+            // so that no other row meets them (0 * Inf)
+            if (row < p.M) {
+              const int e = x.a.ids[row];
+              if (e >= 0 && e < x.a.adapters && lora_bad(x.a, e)) {
+                const float* v = x.a.V + static_cast<long long>(row) * x.a.ldv;
+                const uint16_t* f = x.a.F + static_cast<long long>(e) * x.a.f_stride;
+                for (int r = 0; r < x.a.R; ++r) {
+                  const float vr = v[r];
+#pragma unroll
+                  for (int i = 0; i < kSubCols; ++i)
+                    if (col0 + i < p.N) {
+                      const uint16_t w = LORA::kTransB
+                                             ? f[static_cast<long long>(col0 + i) * x.a.ldf + r]
+                                             : f[static_cast<long long>(r) * x.a.ldf + col0 + i];
+                      cur[i] = __float_as_uint(
+                          fmaf(vr, __half2float(__ushort_as_half(w)), __uint_as_float(cur[i])));
+                    }
+                }
+              }
+            }
+          }
           if (EPI == kEpiPartial) {
             if (row < p.M) {
               float* wrow = p.ws + (static_cast<long long>(t.split) * p.M + row) * p.ws_ld;
@@ -1190,33 +1408,43 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads, 1)
   // the MMA warp only after all epilogue warps have signalled tmem_free.
 }
 
-template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1>
-cudaError_t configure(int dev) {
+template <int BN, int LOAD, int EPI, bool PAIR, int AM, int MM, int KPB, class LORA>
+constexpr int smem_alloc() {
   using L = Smem<BN, EPI, PAIR, AM, KPB>;
+  constexpr int n = L::kAlloc + (LORA::kOn ? 8 * L::Cfg::kStages : 0);
+  static_assert(n <= 232448, "shared memory budget");
+  return n;
+}
+
+template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1,
+          class LORA = NoLora>
+cudaError_t configure(int dev) {
   static bool configured[64] = {};
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(gemm_f16_tc_kernel<BN, LOAD, EPI, PAIR, AM, MM, KPB>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               L::kAlloc);
+    const cudaError_t e = cudaFuncSetAttribute(
+        gemm_f16_tc_kernel<BN, LOAD, EPI, PAIR, AM, MM, KPB, LORA>,
+        cudaFuncAttributeMaxDynamicSharedMemorySize,
+        smem_alloc<BN, LOAD, EPI, PAIR, AM, MM, KPB, LORA>());
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
   return cudaSuccess;
 }
 
-template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1>
+template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1,
+          class LORA = NoLora>
 cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC,
-                       const TcArgs& args, int grid, cudaStream_t stream) {
-  using L = Smem<BN, EPI, PAIR, AM, KPB>;
+                       const TcArgs& args, int grid, cudaStream_t stream,
+                       const LORA& lora = LORA{}) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if ((e = configure<BN, LOAD, EPI, PAIR, AM, MM, KPB>(dev)) != cudaSuccess) return e;
+  if ((e = configure<BN, LOAD, EPI, PAIR, AM, MM, KPB, LORA>(dev)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(Roles<LOAD>::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.blockDim = dim3(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1, 1);
+  cfg.dynamicSmemBytes = smem_alloc<BN, LOAD, EPI, PAIR, AM, MM, KPB, LORA>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   unsigned int nattr = 0;
@@ -1234,8 +1462,8 @@ cudaError_t launch_one(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUt
   }
   cfg.attrs = nattr ? attr : nullptr;
   cfg.numAttrs = nattr;
-  e = cudaLaunchKernelEx(&cfg, gemm_f16_tc_kernel<BN, LOAD, EPI, PAIR, AM, MM, KPB>, tmA, tmB,
-                         tmC, args);
+  e = cudaLaunchKernelEx(&cfg, gemm_f16_tc_kernel<BN, LOAD, EPI, PAIR, AM, MM, KPB, LORA>, tmA, tmB,
+                         tmC, args, lora);
   if (e != cudaSuccess) return e;
   return counted_launch(cudaGetLastError());
 }

@@ -100,6 +100,38 @@ struct TcArgs {
   bool pdl;
 };
 
+// Low-rank adapters picked by row beside a GEMM on CTA pairs (256-row tiles):
+// what the kernel needs beside the product's own operands.
+constexpr int kLoraListStride = 257;   // a 256-row block's list: count, adapters
+constexpr int kLoraBadParts = 4;
+struct LoraTailArgs {
+  const float* V;        // [M][ldv] fp32, the rows' low-rank products; ldv % 4 == 0
+  int ldv;
+  const int* ids;        // [M]
+  const int* lists;      // [256-row block][kLoraListStride]: its distinct adapters
+  const int* bad;        // [adapters][kLoraBadParts]: nonzero when some weight of that
+                         // part of F[a] is not finite
+  const uint16_t* F;     // the adapters' B operand (for the bad ones)
+  long long ldf, f_stride;
+  int R, adapters, chunks;   // chunks of 32 ranks
+};
+// A call of the pair kernel with adapters: `trans` when B is stored N x K and
+// F[a] N x R (the gradient with respect to the left operand).
+struct LoraCall {
+  LoraTailArgs tail;
+  bool trans;
+};
+// C := alpha (A B + V F) + beta C through the pair kernel, after the
+// kernels on `stream` that write V, the lists and the marks.  Needs M > 128, N > 128, A, B and
+// F with rows on the 16-byte grid.  Returns a GEMM_* code.
+int gemm_f16_lora_pair(const uint16_t* A, const uint16_t* B, uint16_t* C, int M, int N, int K,
+                       long long lda, long long ldb, long long ldc, float alpha, float beta,
+                       const LoraCall& lora, cudaStream_t stream);
+cudaError_t launch_gemm_f16_tc_lora(bool trans, int epi_mode, const CUtensorMap& tmA,
+                                    const CUtensorMap& tmB, const CUtensorMap& tmC,
+                                    const CUtensorMap& tmE, const LoraTailArgs& tail,
+                                    const TcArgs& args, int grid, cudaStream_t stream);
+
 // Tensor-core fp16 GEMM (tcgen05).  Maps are ignored by the modes that do not
 // use them.  kpb: k-blocks per ring stage, 1, or 2 for 64-wide tiles with TMA
 // loads and epilogue.  Returns a cudaError_t from the launch.

@@ -246,6 +246,40 @@ int forward_any(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
   return GEMM_OK;
 }
 
+// Many rows: the low-rank products on the tensor cores, then the pair kernel
+// with the adapters as more k-blocks of its tiles.
+int forward_tiles(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta,
+                  const LoraDevice& d, cudaStream_t stream) {
+  LoraShrinkPlan s{};
+  s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, nullptr, 0};
+  s.njobs = 1;
+  s.ids = p.ids;
+  s.scales = p.scales;
+  s.M = p.M;
+  s.R = p.R;
+  s.adapters = p.adapters;
+  s.ldv = (p.R + 3) / 4 * 4;
+  s.check = p.B;
+  s.ld_check = p.ldb;
+  s.check_stride = p.b_stride();
+  s.check_rows = p.R;
+  s.check_cols = p.N;
+  void *buf = nullptr, *zero = nullptr;
+  if (int rc = routed_scratch(stream, lora_shrink_bytes(s, d.sms), &buf,
+                              4 * 8 * static_cast<size_t>((p.M + 127) / 128), &zero))
+    return rc;
+  if (int rc = lora_shrink(s, buf, static_cast<unsigned int*>(zero), d, stream)) return rc;
+  LoraCall call{};
+  call.trans = false;
+  call.tail = LoraTailArgs{s.job[0].V, s.ldv, p.ids, s.lists, s.bad, p.B, p.ldb, p.b_stride(),
+                           p.R, p.adapters, (p.R + 31) / 32};
+  if (int rc = gemm_f16_lora_pair(p.X, p.W, C, p.M, p.N, p.K, p.ldx, p.ldw, ldc, alpha, beta, call,
+                                  stream))
+    return rc;
+  set_last_path("lora.tiles");
+  return GEMM_OK;
+}
+
 int grad_any(const LoraArgs& p, const uint16_t* dC, int lddc, uint16_t* dX, int lddx, float* dA,
              float* dB, float alpha, float beta, int sms, cudaStream_t stream) {
   const long long ldd = (p.K + 3) / 4 * 4, ldt = (p.K + 7) / 8 * 8;
@@ -328,6 +362,8 @@ int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint1
   if (M <= kLoraStreamRows && R % 8 == 0 && on16(X, ldx) && on16(W, ldw) && on16(A, lda) &&
       on16(B, ldb))
     return lora_stream(p, C, ldc, alpha, beta, d, stream);
+  if (M > kLoraStreamRows && N > 128 && on16(X, ldx) && on16(W, ldw) && on16(A, lda) && on16(B, ldb))
+    return forward_tiles(p, C, ldc, alpha, beta, d, stream);
   return forward_any(p, C, ldc, alpha, beta, sms, stream);
 }
 

@@ -35,6 +35,36 @@ constexpr int kLoraStreamRows = 128;
 int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta,
                 const LoraDevice& d, cudaStream_t stream);
 
+// The low-rank products of many rows (lora_shrink.cu): V = s x F[a], F[a] a
+// C x R matrix, or R x C when k_major.
+struct LoraShrinkJob {
+  const uint16_t* x;
+  long long ldx;
+  int C;                  // columns of x
+  const uint16_t* F;
+  long long ldf, f_stride;
+  int k_major;
+  float* V;               // out: [M][ldv]
+  int tiles;
+};
+struct LoraShrinkPlan {
+  LoraShrinkJob job[2];
+  int njobs;
+  const int* ids;
+  const float* scales;
+  int M, R, adapters;
+  int ldv;                // R rounded up to 4
+  // weights to mark adapters by (NULL: neither marks nor lists are wanted)
+  const uint16_t* check;
+  long long ld_check, check_stride;
+  int check_rows, check_cols;
+  int *lists, *bad;       // out: LoraTailArgs::lists and bad
+};
+size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms);
+// `counters`: 8 words per 128 rows, zero before and after.
+int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const LoraDevice& d,
+                cudaStream_t stream);
+
 __device__ __forceinline__ float lora_h2f(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 __device__ __forceinline__ uint16_t lora_f2h(float x) {
   return __half_as_ushort(__float2half_rn(x));

@@ -1,0 +1,478 @@
+// lora_shrink.cu -- the low-rank products V = s X A[a] (and, for gradients,
+// U = s dC B[a]^T) of many rows on the tensor cores, with what the kernels
+// after it need: each 256-row block's distinct adapters, and which adapters
+// hold weights that are not finite.
+//
+// One CTA per (128 rows, K slice): the rows of x are the M operand, the
+// adapters that occur among them the N operand, RP columns each (the rank
+// rounded up to 16, 32, 64 or 128), 64 columns of TMEM at a time; a row keeps
+// the columns of its own adapter.  What binds is reading x once: 2 R
+// multiply-adds per half, where the tensor cores take ~280.  Slices make about
+// one CTA per SM; their partial sums are added by the last slice of a tile to
+// arrive, in slice order.
+//
+// The tensor cores truncate when they add to an fp32 accumulator, by up to
+// 2^-23 of it per 16 products of K, always toward zero.  The gradients of the
+// adapters are fp32, so a run of 128 products of K is the longest that stays in
+// TMEM; the runs are added up in registers, rounded to nearest.
+//
+// F[a] is stored along K (C x R: MN-major N operand) for V, or along the ranks
+// (R x C: K-major) for U.
+#include "lora.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int kThreads = 192;                // TMA, MMA, 4 epilogue warps
+constexpr int kStages = 4;
+constexpr int kXBytes = 128 * 128;           // 128 rows of a k-block
+constexpr int kFoldKb = 2;                   // k-blocks accumulated in TMEM
+constexpr int kSmemMax = 232448;
+
+struct Args {
+  LoraShrinkJob job[2];
+  int njobs;
+  const int* ids;
+  const float* scales;
+  int M, R, adapters, ldv;
+  int* lists;             // [256-row block][kLoraListStride]
+  int* bad;               // [adapters][kLoraBadParts]
+  const uint16_t* check;  // weights to look for non-finite ones in, rows x cols each
+  long long ld_check, check_stride;
+  int check_rows, check_cols;
+  int first_list, first_item[2];   // blocks: checks, lists, items of either job
+  int slices[2], kb[2];
+  float* part[2];         // [slice][M][ldv]
+  unsigned int* counters;
+  unsigned long long wait_limit_ns;
+  DeviceStatus* status;
+};
+
+// The distinct adapters of ids[0, n) in order of first occurrence into `list`;
+// returns their number.  slot[i]: place of row i's adapter, -1 for none.  All
+// kThreads threads; n <= 256.
+__device__ int distinct(const int* ids, int n, int adapters, int* s_id, int* list, int* slot,
+                        int* s_cnt) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int a = ids[i];
+    s_id[i] = a >= 0 && a < adapters ? a : -1;
+  }
+  if (threadIdx.x < 8) s_cnt[threadIdx.x] = 0;
+  __syncthreads();
+  // slot[i] := the first row with i's adapter, for now
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    int f = -1;
+    if (s_id[i] >= 0)
+      for (f = 0; s_id[f] != s_id[i];) ++f;
+    slot[i] = f;
+  }
+  __syncthreads();
+  // number the first rows (one warp, 32 rows at a time)
+  if (threadIdx.x < 32) {
+    int base = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      const bool first = i < n && slot[i] == i;
+      const unsigned int m = __ballot_sync(0xffffffffu, first);
+      if (first) {
+        const int k = base + __popc(m & ((1u << threadIdx.x) - 1u));
+        list[k] = s_id[i];
+        s_id[i] = ~k;   // its number, marked
+      }
+      base += __popc(m);
+    }
+    if (threadIdx.x == 0) s_cnt[0] = base;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (slot[i] >= 0) slot[i] = ~s_id[slot[i]];
+  __syncthreads();
+  return s_cnt[0];
+}
+
+// RP: columns of an adapter; COLS: columns of a pass (whole adapters).
+template <int RP>
+struct Cfg {
+  static constexpr int kCols = RP > 64 ? RP : 64;
+  static constexpr int kGroup = kCols / RP;            // adapters per pass
+  static constexpr int kNBytes = RP > 64 ? 16384 : 8192;   // MN-major: 64-column boxes
+  static constexpr int kStageBytes = kXBytes + kGroup * kNBytes;
+  static constexpr int kTmemCols = 2 * kCols;
+  static constexpr int kSmem = kStages * kStageBytes + 1024 + 8 * (2 * kStages + 5) + 16;
+  static_assert(kSmem <= kSmemMax, "shared memory budget");
+};
+
+template <int RP>
+__global__ void __launch_bounds__(kThreads, 1)
+    lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX0,
+                          const __grid_constant__ CUtensorMap tmF0,
+                          const __grid_constant__ CUtensorMap tmX1,
+                          const __grid_constant__ CUtensorMap tmF1, const Args p) {
+  using G = Cfg<RP>;
+  __shared__ int s_id[256], s_list[256], s_slot[256], s_cnt[8];
+  griddep_launch_dependents();
+  const int b = blockIdx.x;
+  if (b < p.first_list) {
+    // ---- a quarter of an adapter: are its weights finite (if a row uses it)
+    const int adapter = b / kLoraBadParts;
+    bool used = false;
+    for (int i = threadIdx.x; i < p.M; i += kThreads) used |= p.ids[i] == adapter;
+    int bad = 0;
+    if (__syncthreads_or(used)) {
+      const uint16_t* f = p.check + static_cast<long long>(adapter) * p.check_stride;
+      const int groups = (p.check_cols + 7) / 8;
+      const long long total = static_cast<long long>(p.check_rows) * groups;
+      const int part = b - adapter * kLoraBadParts;
+#pragma unroll 8
+      for (long long g = part * total / kLoraBadParts + threadIdx.x;
+           g < (part + 1) * total / kLoraBadParts; g += kThreads) {
+        const int r = static_cast<int>(g / groups), c = static_cast<int>(g % groups) * 8;
+        const uint16_t* q = f + static_cast<long long>(r) * p.ld_check + c;
+        if (c + 8 <= p.check_cols) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
+          // an exponent of all ones in either half
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) bad |= __vcmpgeu2(w[j] & 0x7FFF7FFFu, 0x7C007C00u) != 0u;
+        } else {
+          for (int j = 0; c + j < p.check_cols; ++j) bad |= (q[j] & 0x7FFFu) >= 0x7C00u;
+        }
+      }
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) p.bad[b] = bad;
+    return;
+  }
+  if (b < p.first_item[0]) {
+    // ---- the distinct adapters of a 256-row block
+    const int blk = b - p.first_list, row0 = blk * 256;
+    const int n = distinct(p.ids + row0, min(256, p.M - row0), p.adapters, s_id, s_list, s_slot,
+                           s_cnt);
+    int* const out = p.lists + static_cast<long long>(blk) * kLoraListStride;
+    for (int i = threadIdx.x; i < n; i += kThreads) out[1 + i] = s_list[i];
+    if (threadIdx.x == 0) out[0] = n;
+    return;
+  }
+  // ---- a product: rows [row0, row0 + 128), one K slice
+  const int which = p.njobs > 1 && b >= p.first_item[1] ? 1 : 0;
+  const LoraShrinkJob& job = p.job[which];
+  const CUtensorMap* const tmX = which ? &tmX1 : &tmX0;
+  const CUtensorMap* const tmF = which ? &tmF1 : &tmF0;
+  const int item = b - p.first_item[which], slices = p.slices[which];
+  const int tile = item / slices, slice = item - tile * slices;
+  const int row0 = tile * 128, rows = min(128, p.M - row0);
+  const int kb0 = slice * p.kb[which] / slices, kb1 = (slice + 1) * p.kb[which] / slices;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const uint32_t bars = base + kStages * G::kStageBytes;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto empty_bar = [&](int s) { return bars + 8u * (kStages + s); };
+  auto accf_bar = [&](uint32_t i) { return bars + 8u * (2 * kStages + i); };
+  auto acce_bar = [&](uint32_t i) { return bars + 8u * (2 * kStages + 2 + i); };
+  const uint32_t done_bar = bars + 8u * (2 * kStages + 4);
+  uint8_t* const tmem_ptr = base_ptr + kStages * G::kStageBytes + 8 * (2 * kStages + 5);
+  const int warp = warp_id_uniform(), lane = static_cast<int>(lane_id());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1u);
+      mbar_init(empty_bar(s), 1u);
+    }
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(accf_bar(i), 1u);
+      mbar_init(acce_bar(i), 4u);
+    }
+    mbar_init(done_bar, 1u);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_ptr), G::kTmemCols);
+    tmem_relinquish();
+  }
+  const int n = distinct(p.ids + row0, rows, p.adapters, s_id, s_list, s_slot, s_cnt);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
+  const int passes = (n + G::kGroup - 1) / G::kGroup;
+  const unsigned long long limit = p.wait_limit_ns;
+  DeviceStatus* const st = p.status;
+  const int fboxes = job.k_major ? 1 : (p.R + 63) / 64;
+  const uint32_t fbytes = job.k_major ? RP * 128u : fboxes * 8192u;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (int ps = 0; ps < passes && ok; ++ps) {
+        const int g0 = ps * G::kGroup, gn = min(G::kGroup, n - g0);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 70)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(full_bar(stage), kXBytes + gn * fbytes);
+          const uint32_t dst = base + stage * G::kStageBytes;
+          tma_load_2d(dst, tmX, full_bar(stage), kb * 64, row0);
+          for (int j = 0; j < gn; ++j) {
+            const uint32_t f = dst + kXBytes + j * G::kNBytes;
+            if (job.k_major) {
+              tma_load_3d(f, tmF, full_bar(stage), kb * 64, 0, s_list[g0 + j]);
+            } else {
+              for (int c = 0; c < fboxes; ++c)
+                tma_load_3d(f + c * 8192, tmF, full_bar(stage), 64 * c, kb * 64, s_list[g0 + j]);
+            }
+          }
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      const uint32_t left = min(issued, static_cast<uint32_t>(kStages));
+      for (uint32_t i = issued - left; i < issued; ++i)
+        settle_wait(full_bar(static_cast<int>(i % kStages)), (i / kStages) & 1u, st, 71);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = make_idesc(0u, 128u, RP, 0u, job.k_major ? 0u : 1u);
+      int stage = 0;
+      uint32_t phase = 0, local = 0;
+      bool ok = true;
+      for (int ps = 0; ps < passes && ok; ++ps) {
+        const int gn = min(G::kGroup, n - ps * G::kGroup);
+        for (int k0 = kb0; k0 < kb1 && ok; k0 += kFoldKb) {
+          const uint32_t buf = local & 1u;
+          if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 72)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          for (int kb = k0; kb < min(kb1, k0 + kFoldKb); ++kb) {
+            if (!wait_parity(full_bar(stage), phase, limit, st, 73)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t x0 = base + stage * G::kStageBytes, f0 = x0 + kXBytes;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ad = smem_desc_sw128(x0 + kk * 32, 16u, 1024u);
+              for (int j = 0; j < gn; ++j) {
+                const uint32_t f = f0 + j * G::kNBytes;
+                mma_f16_ss(tmem + buf * G::kCols + j * RP, ad,
+                           job.k_major ? smem_desc_sw128(f + kk * 32, 16u, 1024u)
+                                       : smem_desc_sw128(f + kk * 2048, 8192u, 1024u),
+                           idesc, (kb > k0 || kk > 0) ? 1u : 0u);
+              }
+            }
+            mma_commit(empty_bar(stage));
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          mma_commit(accf_bar(buf));
+          ++local;
+        }
+      }
+      mma_commit(done_bar);
+      settle_wait(done_bar, 0u, st, 74);
+    }
+    __syncwarp();
+  } else {
+    const int quad = warp & 3, lr = 32 * quad + lane;   // this thread's row of the tile
+    const bool in = lr < rows;
+    const int slot = in ? s_slot[lr] : -1;
+    const int row = row0 + lr;
+    float* const out = p.part[which] + (static_cast<long long>(slice) * p.M + row) * p.ldv;
+    if (in && slot < 0)
+      for (int r = 0; r < p.ldv; r += 4)
+        __stcg(reinterpret_cast<float4*>(out + r), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+    uint32_t local = 0;
+    bool ok = true;
+    for (int ps = 0; ps < passes && ok; ++ps) {
+      float acc[G::kCols];
+#pragma unroll
+      for (int i = 0; i < G::kCols; ++i) acc[i] = 0.0f;
+      for (int k0 = kb0; k0 < kb1; k0 += kFoldKb, ++local) {
+        const uint32_t buf = local & 1u;
+        if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 75)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * G::kCols;
+#pragma unroll
+        for (int c = 0; c < G::kCols; c += 16) {
+          uint32_t g[8], h[8];
+          tmem_ld_32x32b_x8(d0 + c, g);
+          tmem_ld_32x32b_x8(d0 + c + 8, h);
+          tmem_wait_ld2(g, h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            acc[c + i] += __uint_as_float(g[i]);
+            acc[c + 8 + i] += __uint_as_float(h[i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acce_bar(buf));
+      }
+      if (!ok) break;
+      const int mine = slot - ps * G::kGroup;
+      if (slot >= 0 && mine >= 0 && mine < G::kGroup) {
+        const float s = p.scales ? p.scales[s_list[slot]] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < G::kGroup; ++j)
+          if (mine == j)
+#pragma unroll
+            for (int r = 0; r < RP; r += 4)
+              if (r < p.ldv)
+                __stcg(reinterpret_cast<float4*>(out + r),
+                       make_float4(s * acc[j * RP + r], s * acc[j * RP + r + 1],
+                                   s * acc[j * RP + r + 2], s * acc[j * RP + r + 3]));
+      }
+    }
+    if (slices > 1) {
+      // the last slice of these 32 rows to arrive adds them up in slice order
+      unsigned int* const cnt = p.counters + ((which ? p.job[0].tiles : 0) + tile) * 4 + quad;
+      __syncwarp();
+      unsigned int before = 0;
+      if (lane == 0) {
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(cnt)
+                     : "memory");
+        if (before == static_cast<unsigned int>(slices - 1)) *cnt = 0u;   // for the next call
+      }
+      before = __shfl_sync(0xffffffffu, before, 0);
+      __syncwarp();
+      if (before == static_cast<unsigned int>(slices - 1)) {
+        // eight lanes a row: 16-byte pieces of consecutive rows
+        const int per = p.ldv / 4, total = max(0, min(32, rows - 32 * quad)) * per;
+        const float* src = p.part[which] + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
+        float* const dst = job.V + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
+        for (int i = lane; i < total; i += 32) {
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+          for (int k = 0; k < slices; ++k) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(
+                                        src + static_cast<long long>(k) * p.M * p.ldv) + i);
+            v.x += t.x;
+            v.y += t.y;
+            v.z += t.z;
+            v.w += t.w;
+          }
+          reinterpret_cast<float4*>(dst)[i] = v;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, G::kTmemCols);
+}
+
+template <int RP>
+int launch(const CUtensorMap* maps, const Args& a, int grid, cudaStream_t stream) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
+  static bool configured[64] = {};
+  if (dev < 64 && !configured[dev]) {
+    if (cudaFuncSetAttribute(lora_shrink_tc_kernel<RP>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<RP>::kSmem) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+    configured[dev] = true;
+  }
+  lora_shrink_tc_kernel<RP><<<grid, kThreads, Cfg<RP>::kSmem, stream>>>(maps[0], maps[1], maps[2],
+                                                                        maps[3], a);
+  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+int slices_of(int tiles, int kb, int sms) {
+  // about one CTA per SM, at least four k-blocks each
+  return std::max(1, std::min({sms / tiles, kb / 4, 16}));
+}
+
+}  // namespace
+
+size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms) {
+  size_t n = lora_round256(4 * static_cast<size_t>((p.M + 255) / 256) * kLoraListStride) +
+             lora_round256(4 * kLoraBadParts * static_cast<size_t>(p.adapters));
+  for (int j = 0; j < p.njobs; ++j) {
+    const int s = slices_of((p.M + 127) / 128, (p.job[j].C + 63) / 64, sms);
+    n += (s > 1 ? s + 1 : 1) * lora_round256(4 * static_cast<size_t>(p.M) * p.ldv);
+  }
+  return n;
+}
+
+int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const LoraDevice& d,
+                cudaStream_t stream) {
+  uint8_t* buf = static_cast<uint8_t*>(scratch);
+  auto take = [&](size_t bytes) {
+    uint8_t* const q = buf;
+    buf += lora_round256(bytes);
+    return q;
+  };
+  const int tiles = (p.M + 127) / 128, blocks = (p.M + 255) / 256;
+  const int rp = p.R <= 16 ? 16 : (p.R <= 32 ? 32 : (p.R <= 64 ? 64 : 128));
+  Args a{};
+  a.njobs = p.njobs;
+  a.ids = p.ids;
+  a.scales = p.scales;
+  a.M = p.M;
+  a.R = p.R;
+  a.adapters = p.adapters;
+  a.ldv = p.ldv;
+  p.lists = reinterpret_cast<int*>(take(4 * static_cast<size_t>(blocks) * kLoraListStride));
+  p.bad = reinterpret_cast<int*>(take(4 * kLoraBadParts * static_cast<size_t>(p.adapters)));
+  a.lists = p.lists;
+  a.bad = p.bad;
+  a.check = p.check;
+  a.ld_check = p.ld_check;
+  a.check_stride = p.check_stride;
+  a.check_rows = p.check_rows;
+  a.check_cols = p.check_cols;
+  a.counters = counters;
+  a.wait_limit_ns = d.wait_limit_ns;
+  a.status = d.status;
+  a.first_list = p.check ? kLoraBadParts * p.adapters : 0;
+  int grid = a.first_list + (p.check ? blocks : 0);
+  CUtensorMap maps[4] = {};
+  for (int j = 0; j < p.njobs; ++j) {
+    LoraShrinkJob& job = p.job[j];
+    job.tiles = tiles;
+    a.kb[j] = (job.C + 63) / 64;
+    a.slices[j] = slices_of(tiles, a.kb[j], d.sms);
+    const size_t v = 4 * static_cast<size_t>(p.M) * p.ldv;
+    job.V = reinterpret_cast<float*>(take(v));
+    a.part[j] = a.slices[j] > 1 ? reinterpret_cast<float*>(take(a.slices[j] * lora_round256(v)))
+                                : job.V;
+    a.first_item[j] = grid;
+    grid += tiles * a.slices[j];
+    if (int rc = encode_map_f16(&maps[2 * j], job.x, p.M, job.C, job.ldx, 64, 128)) return rc;
+    if (int rc = job.k_major ? encode_map_f16_stack(&maps[2 * j + 1], job.F, p.R, job.C, job.ldf,
+                                                    p.adapters, job.f_stride, 64, rp)
+                             : encode_map_f16_stack(&maps[2 * j + 1], job.F, job.C, p.R, job.ldf,
+                                                    p.adapters, job.f_stride, 64, 64))
+      return rc;
+    a.job[j] = job;
+  }
+  switch (rp) {
+    case 16: return launch<16>(maps, a, grid, stream);
+    case 32: return launch<32>(maps, a, grid, stream);
+    case 64: return launch<64>(maps, a, grid, stream);
+    default: return launch<128>(maps, a, grid, stream);
+  }
+}
+
+}  // namespace gb300
