@@ -541,6 +541,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   // A single row of 256-wide tiles that cannot fill the SMs: narrower tiles
   // give more of them, so fewer K slices are needed.
   if (bn == 256 && M <= kBM && 1ll * ((N + 255) / 256) * 2 <= d->sm_count) bn = 128;
+  if (lora) bn = 256;
   const bool a_tma = aligned16(A) && (lda * 2) % 16 == 0;
   const bool b_tma = aligned16(B) && (ldb * 2) % 16 == 0;
   // A TMA store writes whole 16-byte pieces of a row: when N is not a multiple
@@ -563,7 +564,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
     const size_t a_bytes = a_tma ? 0 : round256(static_cast<size_t>(M) * lda2 * 2);
     const size_t b_bytes = b_tma ? 0 : round256(static_cast<size_t>(b_rows) * ldb2 * 2);
     const size_t c_bytes = (c_f32 || c_tma) ? 0 : round256(static_cast<size_t>(M) * ldc2 * 2);
-    if (a_bytes + b_bytes + c_bytes <= (static_cast<size_t>(1) << 31)) {
+    if (lora || a_bytes + b_bytes + c_bytes <= (static_cast<size_t>(1) << 31)) {
       std::lock_guard<std::mutex> lk(g_mu);
       StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
       if (int rc = ensure_buffer(&w.realigned, &w.realigned_bytes, a_bytes + b_bytes + c_bytes))
@@ -675,7 +676,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   // large aligned shapes: each SM then stages half as much of B per MMA.
   int pair_slots = 0;
   const bool pair = splits == 1 && !few_sk && force != 6 && bn == 256 &&
-                    load == kLoadTma && a.tiles_m >= 2 &&
+                    load == kLoadTma && (a.tiles_m >= 2 || lora) &&
                     (pair_slots = tc_pair_max_clusters(epi)) > 0;
   // forced narrower pair tiles (the tile-family comparison)
   if (pair && !c_f32 && (force == 12 || force == 13)) {
@@ -869,7 +870,6 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
     t_last_path = t_path_buf;
     if (lora) {
       const LoraTailArgs& x = lora->tail;
-      if (epi != kEpiTma) return GEMM_ERR_ARG;
       CUtensorMap tmE{};
       if (int rc = trans_b ? encode_map_f16_stack(&tmE, x.F, N, x.R, x.ldf, x.adapters, x.f_stride,
                                                   64, 64)
@@ -885,7 +885,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
       return GEMM_ERR_CUDA;
     return copy_back();
   }
-  if (lora) return GEMM_ERR_ARG;   // not a shape of the pair kernel
+  if (lora) return GEMM_ERR_CUDA;   // no CTA pair fits on the device
   const int grid = static_cast<int>(nw);
   const int bi = bn == 64 ? 0 : (bn == 128 ? 1 : 2);
   const char* rows = m64 ? ".m64" : (am == 32 ? ".a32" : (am == 64 ? ".a64" : (kpb == 2 ? ".kb2" : "")));

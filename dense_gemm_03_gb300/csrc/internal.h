@@ -122,8 +122,8 @@ struct LoraCall {
   bool trans;
 };
 // C := alpha (A B + V F) + beta C through the pair kernel, after the
-// kernels on `stream` that write V, the lists and the marks.  Needs M > 128, N > 128, A, B and
-// F with rows on the 16-byte grid.  Returns a GEMM_* code.
+// kernels on `stream` that write V, the lists and the marks.  F has rows on the
+// 16-byte grid.  Returns a GEMM_* code.
 int gemm_f16_lora_pair(const uint16_t* A, const uint16_t* B, uint16_t* C, int M, int N, int K,
                        long long lda, long long ldb, long long ldc, float alpha, float beta,
                        const LoraCall& lora, cudaStream_t stream);

@@ -30,9 +30,12 @@ struct LoraDevice {
   unsigned long long wait_limit_ns;
 };
 
-// The forward for a few rows (M <= kLoraStreamRows): W streamed once.
+// The forward for a few rows (M <= kLoraStreamRows): W streamed once.  Every
+// operand has rows on the 16-byte grid; A has zero columns up to a multiple of
+// eight.
 constexpr int kLoraStreamRows = 128;
-int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta,
+size_t lora_stream_bytes(const LoraArgs& p, int sms);
+int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta, void* scratch,
                 const LoraDevice& d, cudaStream_t stream);
 
 // The low-rank products of many rows (lora_shrink.cu): V = s x F[a], F[a] a
@@ -64,6 +67,22 @@ size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms);
 // `counters`: 8 words per 128 rows, zero before and after.
 int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const LoraDevice& d,
                 cudaStream_t stream);
+
+// The adapters' gradients (lora_outer.cu): dA from X and U, dB from V and G;
+// either may be NULL.
+struct LoraOuter {
+  const uint16_t *X, *G;
+  long long ldx, ldg;
+  const float *U, *V;     // [M][ldv]
+  int ldv;
+  const int* ids;
+  float *dA, *dB;
+  int M, N, K, R, adapters;
+  float alpha, beta;
+};
+constexpr int kLoraMaxAdapters = 16384;   // of a gradient (its table of places)
+size_t lora_outer_bytes(const LoraOuter& o);
+int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStream_t stream);
 
 __device__ __forceinline__ float lora_h2f(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 __device__ __forceinline__ uint16_t lora_f2h(float x) {

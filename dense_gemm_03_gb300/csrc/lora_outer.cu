@@ -1,0 +1,538 @@
+// lora_outer.cu -- the adapters' gradients, sums over the rows of each adapter:
+//
+//   dA[a] = alpha sum X_i^T U_i + beta dA[a],  dB[a] = alpha sum V_i^T dC_i + beta dB[a]
+//
+// lora_outer_kernel: one item is (512 rows, an adapter that occurs in them, 256
+// columns of X or of dC, 32 ranks).  X (dC) is the M operand, as it lies in
+// memory (MN-major, 64 rows a k-block); the N operand is the rows' U (V) in two
+// halves, hi in columns 0 .. 31 and lo in 32 .. 63, so one product gives both
+// parts.  What binds is reading X and dC once per adapter in the rows (once in
+// all, when an adapter's rows lie together); the rest is small.  64-row blocks
+// without the adapter are skipped.  Items write fp32 partial sums, which
+// lora_outer_sum_kernel adds up in row order.
+//
+// U and V are fp32.  Every 64 rows they are scaled by a power of two that
+// brings their largest magnitude into [2^13, 2^14) before they are split, so
+// gradients of any size keep 22 significant bits relative to it; 64 rows are
+// also what is summed in TMEM (the tensor cores truncate, see lora_shrink.cu),
+// and the scale is taken back as those sums are added up in registers.
+//
+// Rows of other adapters in a block have zeros for U (V), and their part of X
+// (dC) is overwritten by zeros in shared memory, so that an Inf or NaN there
+// stays with its own adapter.
+#include "lora.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int kRange = 512;                  // rows of an item
+constexpr int kLoaders = 4;
+constexpr int kEpi = 4;
+constexpr int kThreads = 32 * (2 + kLoaders + kEpi);
+constexpr int kStages = 5;
+constexpr int kXBytes = 4 * 64 * 128;        // 64 rows x 256 columns
+constexpr int kVBytes = 64 * 128;            // 64 rows x (32 hi, 32 lo)
+constexpr int kStageBytes = kXBytes + kVBytes;
+constexpr int kTmemCols = 256;               // two buffers of two 64-column accumulators
+constexpr int kScales = 8;   // > blocks between the loaders and the epilogue: stages + 2 buffers
+constexpr int kMaxMasks = kLoraMaxAdapters;  // ranges x adapters of a launch
+constexpr int kGroupMasks = 32;              // masks per entry of the prefix
+constexpr int kBars = 3 * kStages + 5;
+constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * kBars + 8 + 4 * kScales;
+static_assert(kStages + 2 < kScales, "scales in flight");
+static_assert(kSmem + 16 + kMaxMasks + kMaxMasks / 8 + 64 <= 232448, "shared memory budget");
+
+struct Args {
+  const float* y[2];       // U, V: [M][ldv]
+  int cols[2], tiles[2];   // columns of X and dC, 256-column tiles (0: not wanted)
+  const int* ids;
+  int M, R, adapters, ldv, chunks, ranges, row0;
+  float* part;             // [present][tile columns and ranks as in dA, then as in dB]
+  long long part_stride, part_b;
+  int* table;              // [range][adapter]: place among the present ones, or -1
+  unsigned long long wait_limit_ns;
+  DeviceStatus* status;
+};
+
+struct Item {
+  int present, range, a, mask, src, tile, chunk;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    lora_outer_kernel(const __grid_constant__ CUtensorMap tmX,
+                      const __grid_constant__ CUtensorMap tmG, const Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  const uint32_t bars = base + kStages * kStageBytes;
+  auto full_bar = [&](int s) { return bars + 8u * s; };
+  auto tok_bar = [&](int s) { return bars + 8u * (kStages + s); };
+  auto empty_bar = [&](int s) { return bars + 8u * (2 * kStages + s); };
+  auto accf_bar = [&](uint32_t b) { return bars + 8u * (3 * kStages + b); };
+  auto acce_bar = [&](uint32_t b) { return bars + 8u * (3 * kStages + 2 + b); };
+  const uint32_t done_bar = bars + 8u * (3 * kStages + 4);
+  uint8_t* const tail = base_ptr + kStages * kStageBytes + 8 * kBars;
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(tail);            // TMEM address, present
+  volatile float* const s_scale = reinterpret_cast<float*>(tail + 8);
+  // [range][adapter] bytes: the 64-row blocks with the adapter; then, per 32 of
+  // them, how many nonzero ones come before
+  const int nmask = p.ranges * p.adapters;
+  const int words = (nmask + kGroupMasks - 1) / kGroupMasks * (kGroupMasks / 4);
+  uint32_t* const s_mask =
+      reinterpret_cast<uint32_t*>(base_ptr + (kSmem - 1024 + 15) / 16 * 16);
+  int* const s_prefix = reinterpret_cast<int*>(s_mask + words);
+  const int warp = warp_id_uniform(), lane = static_cast<int>(lane_id());
+  griddep_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full_bar(s), 1u);
+      mbar_init(tok_bar(s), 1u);
+      mbar_init(empty_bar(s), 1u);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(accf_bar(b), 1u);
+      mbar_init(acce_bar(b), static_cast<uint32_t>(kEpi));
+    }
+    mbar_init(done_bar, 1u);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(misc), kTmemCols);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < words; i += kThreads) s_mask[i] = 0u;
+  __syncthreads();
+  // ids is the caller's: nothing to wait for
+  const int rows = min(p.M - p.row0, p.ranges * kRange);
+  for (int i = threadIdx.x; i < rows; i += kThreads) {
+    const int a = __ldg(p.ids + p.row0 + i);
+    if (a >= 0 && a < p.adapters) {
+      const int m = i / kRange * p.adapters + a;
+      const uint32_t bit = 1u << (8 * (m & 3) + (i % kRange) / 64);
+      if (!(reinterpret_cast<volatile uint32_t*>(s_mask)[m >> 2] & bit)) atomicOr(s_mask + (m >> 2), bit);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int before = 0;
+    const int groups = words / (kGroupMasks / 4);
+    for (int g0 = 0; g0 < groups; g0 += 32) {
+      int n = 0;
+      if (g0 + lane < groups)
+        for (int w = 0; w < kGroupMasks / 4; ++w)
+          n += __popc(__vcmpgtu4(s_mask[(g0 + lane) * (kGroupMasks / 4) + w], 0u)) / 8;
+      int incl = n;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      if (g0 + lane < groups) s_prefix[g0 + lane] = before + incl - n;
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) misc[1] = static_cast<uint32_t>(before);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = reinterpret_cast<volatile uint32_t*>(misc)[0];
+  const int present = static_cast<int>(misc[1]);
+  const uint8_t* const mask_bytes = reinterpret_cast<const uint8_t*>(s_mask);
+  // the places of all masks, for the sum kernel
+  for (int m = blockIdx.x * kThreads + threadIdx.x; m < nmask; m += gridDim.x * kThreads) {
+    int place = -1;
+    if (mask_bytes[m]) {
+      const int g = m / kGroupMasks;
+      place = s_prefix[g];
+      for (int i = g * kGroupMasks; i < m; ++i) place += mask_bytes[i] != 0;
+    }
+    p.table[m] = place;
+  }
+  griddep_wait();   // U and V
+  const int all_tiles = p.tiles[0] + p.tiles[1];
+  const int per = all_tiles * p.chunks;
+  const long long items = 1ll * present * per;
+  auto item_at = [&](long long it) {
+    Item t;
+    t.present = static_cast<int>(it / per);
+    const int v = static_cast<int>(it - 1ll * t.present * per);
+    t.chunk = v / all_tiles;
+    const int tile = v - t.chunk * all_tiles;
+    t.src = tile < p.tiles[0] ? 0 : 1;
+    t.tile = t.src ? tile - p.tiles[0] : tile;
+    // the last group whose prefix does not pass the place, then within it
+    int lo = 0, hi = words / (kGroupMasks / 4) - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (s_prefix[mid] <= t.present)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    int left = t.present - s_prefix[lo], m = lo * kGroupMasks;
+    for (;; ++m)
+      if (mask_bytes[m] != 0 && left-- == 0) break;
+    t.range = m / p.adapters;
+    t.a = m - t.range * p.adapters;
+    t.mask = mask_bytes[m];
+    return t;
+  };
+  const unsigned long long limit = p.wait_limit_ns;
+  DeviceStatus* const st = p.status;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
+      bool ok = true;
+      for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const Item t = item_at(it);
+        const int left = p.cols[t.src] - t.tile * 256;
+        const int boxes = min(4, (left + 63) / 64);
+        const CUtensorMap* const tm = t.src ? &tmG : &tmX;
+        for (int m = t.mask; m && ok; m &= m - 1) {
+          const int row = p.row0 + t.range * kRange + (__ffs(m) - 1) * 64;
+          if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 80)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(boxes * 8192));
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(base + stage * kStageBytes + b * 8192, tm, full_bar(stage),
+                        t.tile * 256 + b * 64, row);
+          ++issued;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      const uint32_t n = min(issued, static_cast<uint32_t>(kStages));
+      for (uint32_t i = issued - n; i < issued; ++i)
+        settle_wait(full_bar(static_cast<int>(i % kStages)), (i / kStages) & 1u, st, 81);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc(0u, 128u, 64u, 1u, 1u);
+      int stage = 0;
+      uint32_t phase = 0, local = 0;
+      bool ok = true;
+      for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const Item t = item_at(it);
+        for (int m = t.mask; m; m &= m - 1) {
+          const uint32_t buf = local & 1u;
+          if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 82) ||
+              !wait_parity(full_bar(stage), phase, limit, st, 83) ||
+              !wait_parity(tok_bar(stage), phase, limit, st, 84)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d0 = tmem + buf * 128;
+          const uint32_t x0 = base + stage * kStageBytes, v0 = x0 + kXBytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t bd = smem_desc_sw128(v0 + kk * 2048, 8192u, 1024u);
+            mma_f16_ss(d0, smem_desc_sw128(x0 + kk * 2048, 8192u, 1024u), bd, idesc, kk > 0);
+            mma_f16_ss(d0 + 64, smem_desc_sw128(x0 + 16384 + kk * 2048, 8192u, 1024u), bd, idesc,
+                       kk > 0);
+          }
+          mma_commit(empty_bar(stage));
+          mma_commit(accf_bar(buf));
+          ++local;
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      mma_commit(done_bar);
+      settle_wait(done_bar, 0u, st, 85);
+    }
+    __syncwarp();
+  } else if (warp < 2 + kLoaders) {
+    // Loader l takes the blocks l, l + 4, ... of the CTA's sequence; eight lanes
+    // share a row, four ranks each.
+    const int l = warp - 2, q = lane & 7, r4 = lane >> 3;
+    int stage = 0;
+    uint32_t phase = 0, seq = 0;
+    bool ok = true;
+    for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const Item t = item_at(it);
+      const int rank = 32 * t.chunk + 4 * q;
+      const float* const y = p.y[t.src];
+      for (int m = t.mask; m; m &= m - 1, ++seq) {
+        if (static_cast<int>(seq & (kLoaders - 1)) == l) {
+          const int row0 = p.row0 + t.range * kRange + (__ffs(m) - 1) * 64 + r4;
+          float4 f[16];
+          uint32_t foreign = 0u;   // bit i: row 4 i + r4 of the block is another adapter's
+          float top = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int row = row0 + 4 * i;
+            if (row < p.M) {
+              if (__ldg(p.ids + row) != t.a)
+                foreign |= 1u << i;
+              else if (rank < p.ldv)
+                f[i] = __ldcg(reinterpret_cast<const float4*>(
+                    y + static_cast<long long>(row) * p.ldv + rank));
+            }
+          }
+          // the largest finite magnitude (an infinite entry stays infinite)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float v[4] = {fabsf(f[i].x), fabsf(f[i].y), fabsf(f[i].z), fabsf(f[i].w)};
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (v[c] < __int_as_float(0x7F800000)) top = fmaxf(top, v[c]);
+          }
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+          // top * 2^e in [2^13, 2^14); |e| <= 100, so that 2^e and 2^-e are normal
+          const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
+          const float up = __int_as_float((127 + e) << 23);
+          if (lane == 0) ok = wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 86);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane == 0) s_scale[seq & (kScales - 1)] = __int_as_float((127 - e) << 23);
+          uint8_t* const sx = base_ptr + stage * kStageBytes;
+          uint8_t* const sv = sx + kXBytes;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int lr = 4 * i + r4;
+            const float v[4] = {f[i].x * up, f[i].y * up, f[i].z * up, f[i].w * up};
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint16_t h0 = lora_f2h(v[2 * c]), h1 = lora_f2h(v[2 * c + 1]);
+              const uint16_t g0 =
+                  (h0 & 0x7FFFu) >= 0x7C00u ? 0 : lora_f2h(v[2 * c] - lora_h2f(h0));
+              const uint16_t g1 =
+                  (h1 & 0x7FFFu) >= 0x7C00u ? 0 : lora_f2h(v[2 * c + 1] - lora_h2f(h1));
+              hi[c] = h0 | (static_cast<uint32_t>(h1) << 16);
+              lo[c] = g0 | (static_cast<uint32_t>(g1) << 16);
+            }
+            uint8_t* const rowp = sv + lr * 128 + (q & 1) * 8;
+            *reinterpret_cast<uint2*>(rowp + (((q >> 1) ^ (lr & 7)) << 4)) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(rowp + (((4 + (q >> 1)) ^ (lr & 7)) << 4)) =
+                make_uint2(lo[0], lo[1]);
+          }
+          if (__any_sync(0xffffffffu, foreign != 0u)) {
+            // once the block has landed, zero the other adapters' rows of it
+            if (lane == 0) ok = wait_parity(full_bar(stage), phase, limit, st, 87);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            __syncwarp();
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (foreign >> i & 1u)
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                  *reinterpret_cast<uint4*>(sx + b * 8192 + (4 * i + r4) * 128 + 16 * q) =
+                      make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tok_bar(stage));
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    const int quad = warp & 3, col = 32 * quad + lane;
+    uint32_t local = 0;
+    bool ok = true;
+    for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
+      const Item t = item_at(it);
+      float acc0[32], acc1[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc0[i] = acc1[i] = 0.0f;
+      for (int n = __popc(t.mask); n > 0; --n, ++local) {
+        const uint32_t buf = local & 1u;
+        if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 88)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float down = s_scale[local & (kScales - 1)];
+        const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * 128;
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+          uint32_t g[8], h[8];
+          tmem_ld_32x32b_x8(d0 + c, g);
+          tmem_ld_32x32b_x8(d0 + 32 + c, h);
+          tmem_wait_ld2(g, h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc0[c + i] = fmaf(__uint_as_float(g[i]) + __uint_as_float(h[i]), down, acc0[c + i]);
+          tmem_ld_32x32b_x8(d0 + 64 + c, g);
+          tmem_ld_32x32b_x8(d0 + 96 + c, h);
+          tmem_wait_ld2(g, h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc1[c + i] = fmaf(__uint_as_float(g[i]) + __uint_as_float(h[i]), down, acc1[c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acce_bar(buf));
+      }
+      if (!ok) break;
+      const int C = p.cols[t.src], r0 = 32 * t.chunk, nr = min(32, p.R - r0);
+      float* const out = p.part + t.present * p.part_stride + (t.src ? p.part_b : 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = t.tile * 256 + h * 128 + col;
+        if (c < C) {
+#pragma unroll
+          for (int r = 0; r < 32; ++r)
+            if (r < nr)
+              __stcg(out + (t.src ? static_cast<long long>(r0 + r) * C + c
+                                  : static_cast<long long>(c) * p.R + r0 + r),
+                     h ? acc1[r] : acc0[r]);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+}
+
+// dA and dB := alpha * (the present ranges' partial sums in row order) + beta *
+// themselves.
+struct SumArgs {
+  const float* part;
+  long long part_stride, part_b, elems[2];   // elements per adapter of dA, dB
+  const int* table;
+  float* out[2];
+  int adapters, ranges;
+  float alpha, beta;
+};
+
+constexpr int kSumThreads = 256;
+
+__global__ void __launch_bounds__(kSumThreads) lora_outer_sum_kernel(const SumArgs p) {
+  griddep_wait();
+  const int a = blockIdx.y;
+  const long long na = p.out[0] ? p.elems[0] : 0, nb = p.out[1] ? p.elems[1] : 0;
+  for (long long i = 1ll * blockIdx.x * kSumThreads + threadIdx.x; i < na + nb;
+       i += 1ll * gridDim.x * kSumThreads) {
+    const int src = i < na ? 0 : 1;
+    const long long e = src ? i - na : i;
+    const float* part = p.part + (src ? p.part_b : 0) + e;
+    float s = 0.0f;
+    for (int r = 0; r < p.ranges; ++r) {
+      const int k = p.table[r * p.adapters + a];
+      if (k >= 0) s += __ldcg(part + k * p.part_stride);
+    }
+    float* o = p.out[src] + a * p.elems[src] + e;
+    *o = p.beta != 0.0f ? fmaf(p.alpha, s, p.beta * *o) : p.alpha * s;
+  }
+}
+
+// Ranges of one launch: the masks fit shared memory, the partial sums 2 GB.
+int ranges_of(const LoraOuter& o) {
+  const long long per = 4ll * std::min(o.adapters, kRange) * o.R * (o.K + o.N);
+  const long long fit = std::min<long long>(kMaxMasks / std::max(1, o.adapters),
+                                            (2ll << 30) / std::max(1ll, per));
+  return static_cast<int>(
+      std::max(1ll, std::min<long long>((o.M + kRange - 1) / kRange, fit)));
+}
+
+}  // namespace
+
+size_t lora_outer_bytes(const LoraOuter& o) {
+  const long long ranges = ranges_of(o);
+  return lora_round256(4 * static_cast<size_t>(ranges) * o.adapters) +
+         4 * static_cast<size_t>(ranges) * std::min(o.adapters, kRange) * o.R *
+             (static_cast<size_t>(o.K) + o.N);
+}
+
+int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStream_t stream) {
+  if (o.adapters > kMaxMasks) return GEMM_ERR_ARG;
+  CUtensorMap tmX{}, tmG{};
+  if (o.dA)
+    if (int rc = encode_map_f16(&tmX, o.X, o.M, o.K, o.ldx, 64, 64)) return rc;
+  if (o.dB)
+    if (int rc = encode_map_f16(&tmG, o.G, o.M, o.N, o.ldg, 64, 64)) return rc;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
+  static bool configured[64] = {};
+  if (dev < 64 && !configured[dev]) {
+    if (cudaFuncSetAttribute(lora_outer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             232448) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+    configured[dev] = true;
+  }
+  const int ranges = ranges_of(o);
+  Args a{};
+  a.y[0] = o.U;
+  a.y[1] = o.V;
+  a.cols[0] = o.K;
+  a.cols[1] = o.N;
+  a.tiles[0] = o.dA ? (o.K + 255) / 256 : 0;
+  a.tiles[1] = o.dB ? (o.N + 255) / 256 : 0;
+  a.ids = o.ids;
+  a.M = o.M;
+  a.R = o.R;
+  a.adapters = o.adapters;
+  a.ldv = o.ldv;
+  a.chunks = (o.R + 31) / 32;
+  a.table = static_cast<int*>(scratch);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
+                                    lora_round256(4 * static_cast<size_t>(ranges) * o.adapters));
+  a.part_b = 1ll * o.K * o.R;
+  a.part_stride = a.part_b + 1ll * o.R * o.N;
+  a.wait_limit_ns = d.wait_limit_ns;
+  a.status = d.status;
+  SumArgs s{};
+  s.part = a.part;
+  s.part_stride = a.part_stride;
+  s.part_b = a.part_b;
+  s.elems[0] = 1ll * o.K * o.R;
+  s.elems[1] = 1ll * o.R * o.N;
+  s.table = a.table;
+  s.out[0] = o.dA;
+  s.out[1] = o.dB;
+  s.adapters = o.adapters;
+  s.alpha = o.alpha;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  for (int r0 = 0; r0 * kRange < o.M; r0 += ranges) {
+    a.row0 = r0 * kRange;
+    a.ranges = std::min(ranges, (o.M + kRange - 1) / kRange - r0);
+    const int nmask = a.ranges * o.adapters;
+    const int words = (nmask + kGroupMasks - 1) / kGroupMasks * (kGroupMasks / 4);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(d.sms), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = kSmem + 16 + 4 * static_cast<size_t>(words + words / (kGroupMasks / 4));
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = r0 == 0 ? 1 : 0;   // a later slab waits for the sums of the one before
+    if (counted_launch(cudaLaunchKernelEx(&cfg, lora_outer_kernel, tmX, tmG, a)) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+    s.ranges = a.ranges;
+    s.beta = r0 == 0 ? o.beta : 1.0f;
+    const long long elems = (o.dA ? s.elems[0] : 0) + (o.dB ? s.elems[1] : 0);
+    const long long blocks = std::min<long long>((elems + kSumThreads - 1) / kSumThreads,
+                                                 std::max(1, 16 * d.sms / o.adapters));
+    cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, blocks)),
+                       static_cast<unsigned>(o.adapters), 1);
+    cfg.blockDim = dim3(kSumThreads, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    if (counted_launch(cudaLaunchKernelEx(&cfg, lora_outer_sum_kernel, s)) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+  }
+  return GEMM_OK;
+}
+
+}  // namespace gb300

@@ -262,7 +262,7 @@ struct CombineArgs {
   const int* ids;
   uint16_t* C;
   long long ldb, b_stride, ldc;
-  int M, N, R, adapters, chunks, slices;
+  int M, N, R, ldv, adapters, chunks, slices;   // ldv: ranks of V
   float alpha, beta;
   bool vec_c;              // rows of C on the 8-byte grid
 };
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
   griddep_wait();
   if (has)
     for (int r = threadIdx.x; r < p.R; r += kCombThreads) {
-      const float* v = p.V + static_cast<long long>(i) * p.slices * p.R + r;
+      const float* v = p.V + static_cast<long long>(i) * p.slices * p.ldv + r;
       float s = 0.0f;
-      for (int k = 0; k < p.slices; ++k) s += __ldcg(v + k * p.R);
+      for (int k = 0; k < p.slices; ++k) s += __ldcg(v + k * p.ldv);
       vs[r] = s;
     }
   __syncthreads();
@@ -361,7 +361,22 @@ int plan_chunks(int units, int kb, int M, int sms) {
 
 }  // namespace
 
-int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta,
+namespace {
+
+// K slices of the shrink: about four blocks per SM in all, at least 64 long.
+int shrink_slices(const LoraArgs& p, int sms) {
+  return std::max(1, std::min({kMaxSlices, 4 * sms / p.M, p.K / 64}));
+}
+
+}  // namespace
+
+size_t lora_stream_bytes(const LoraArgs& p, int sms) {
+  const int units = (p.N + 127) / 128, r8 = (p.R + 7) / 8 * 8;
+  return lora_round256(4 * static_cast<size_t>(p.M) * shrink_slices(p, sms) * r8) +
+         4 * static_cast<size_t>(units) * plan_chunks(units, (p.K + 63) / 64, p.M, sms) * p.M * 128;
+}
+
+int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta, void* scratch,
                 const LoraDevice& d, cudaStream_t stream) {
   const int units = (p.N + 127) / 128, kb = (p.K + 63) / 64;
   const int rows = (p.M + 15) / 16 * 16;
@@ -378,8 +393,7 @@ int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
     configured[dev] = true;
   }
   ShrinkArgs s{};
-  // about four blocks per SM in all, slices of at least 64
-  const int want = std::max(1, std::min({kMaxSlices, 4 * d.sms / p.M, p.K / 64}));
+  const int want = shrink_slices(p, d.sms), r8 = (p.R + 7) / 8 * 8;
   s.len = (p.K + want - 1) / want;
   s.slices = (p.K + s.len - 1) / s.len;
   StreamArgs t{};
@@ -395,12 +409,9 @@ int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
   t.wait_limit_ns = d.wait_limit_ns;
   t.status = d.status;
 
-  const size_t v_bytes = lora_round256(4 * static_cast<size_t>(p.M) * s.slices * p.R);
-  const size_t part_bytes = 4 * static_cast<size_t>(t.items) * p.M * 128;
-  void* buf = nullptr;
-  if (int rc = routed_scratch(stream, v_bytes + part_bytes, &buf)) return rc;
-  s.V = static_cast<float*>(buf);
-  t.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + v_bytes);
+  s.V = static_cast<float*>(scratch);
+  t.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
+                                    lora_round256(4 * static_cast<size_t>(p.M) * want * r8));
   s.X = p.X;
   s.A = p.A;
   s.ids = p.ids;
@@ -410,7 +421,7 @@ int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
   s.a_stride = p.a_stride();
   s.M = p.M;
   s.K = p.K;
-  s.R = p.R;
+  s.R = r8;
   s.adapters = p.adapters;
   lora_shrink_kernel<<<p.M * s.slices, kShrinkThreads, 0, stream>>>(s);
   if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
@@ -443,6 +454,7 @@ int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
   c.adapters = p.adapters;
   c.chunks = t.chunks;
   c.slices = s.slices;
+  c.ldv = r8;
   c.alpha = alpha;
   c.beta = beta;
   c.vec_c = (reinterpret_cast<uintptr_t>(C) & 7u) == 0 && ldc % 4 == 0;
@@ -451,7 +463,6 @@ int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
   cfg.dynamicSmemBytes = 0;
   if (counted_launch(cudaLaunchKernelEx(&cfg, lora_combine_kernel, c)) != cudaSuccess)
     return GEMM_ERR_CUDA;
-  set_last_path("lora.stream");
   return GEMM_OK;
 }
 

@@ -289,6 +289,19 @@ def test_empty_and_degenerate_calls():
     assert (dX == 0).all() and (dA == 0).all() and (dB == 0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(20, 64, 32), (300, 520, 264), (65, 129, 77)])
+def test_grad_without_adapters_is_the_projection_s(M, N, K):
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M, M, N, K, 8, 3, "none")
+    dX = t.full((M, K), float("nan"), dtype=t.float16, device="cuda")
+    g.gemm_f16_lora_grad(o["G"].cuda(), None, o["W"].cuda(), None, None, None, dX=dX, alpha=0.5, R=0,
+                         adapters=0)
+    sync(t)
+    r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], None, 0.5, 0.0, None, None)
+    ref.check(dX.cpu(), *r["dX"])
+
+
 def test_grad_parts_alone_equal_the_whole():
     import dense_gemm_03_gb300 as g
     t = torch()
