@@ -557,6 +557,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   auto cfull_bar = [&](int w, int b) { return bars + 8u * (2 * S + 6 + L::kBufs * w + b); };
   // adapters: the V tile of stage s is written (by the warps of both CTAs)
   auto vfull_bar = [&](int s) { return base + static_cast<uint32_t>(L::kUsed) + 8u * s; };
+  // adapters: stage s is free for a V tile (told by this CTA's producer)
+  auto vgo_bar = [&](int s) { return vfull_bar(S + s); };
   auto stage_a = [&](int s) { return base + static_cast<uint32_t>(s * Cfg::kStageBytes); };
   auto stage_b = [&](int s) { return stage_a(s) + kAB; };
 
@@ -574,7 +576,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
     for (int w = 0; w < 8; ++w)
       for (int b = 0; b < L::kBufs; ++b) mbar_init(cfull_bar(w, b), 1u);
     if constexpr (LORA::kOn)
-      for (int s = 0; s < S; ++s) mbar_init(vfull_bar(s), 2u * LORA::kWarps);
+      for (int s = 0; s < S; ++s) {
+        mbar_init(vfull_bar(s), 2u * LORA::kWarps);
+        mbar_init(vgo_bar(s), 1u);
+      }
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -697,6 +702,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
                   ok = false;
                   break;
                 }
+                mbar_arrive(vgo_bar(stage));
                 const uint32_t fb = map_to_cta(full_bar(stage), 0);
                 if (leader)
                   mbar_arrive_expect_tx(full_bar(stage),
@@ -897,32 +903,20 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   } else if (LORA::kOn && warp >= R::kWarps) {
     // ------------------------------------------------------------ adapters' V tiles
     // Warp v writes rows 64v .. 64v + 63 of this CTA's 128; eight lanes share a
-    // row, four ranks each.  The stage sequence is followed k-block by k-block
-    // (a parity wait may not skip a phase).
+    // row, four ranks each.  The ring goes round without these warps for most of
+    // a tile, so they count its stages and wait for the producer's word on the
+    // stages that are theirs (a wait for the parity of `empty` could meet it a
+    // whole round too late and never end).
     if constexpr (LORA::kOn) {
       const int v = warp - R::kWarps;
       const int q = lane & 7, r0 = 64 * v + (lane >> 3);
-      int stage = 0;
-      uint32_t phase = 0;
+      uint32_t count = 0, gophase = 0;   // stages passed; bit s: parity of vgo_bar(s)
       bool ok = true;
-      auto wait_empty = [&]() {
-        if (lane == 0) ok = wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 21);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      };
-      auto advance = [&]() {
-        if (++stage == S) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      };
       UnitCursor cur = first_unit(p, worker);
       Unit t;
       while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
-        for (int kb = t.kb0; kb < t.kb1 && ok; ++kb) {
-          wait_empty();
-          advance();
-        }
-        if (!ok || t.kb1 != p.kb_total) continue;
+        count += static_cast<uint32_t>(t.kb1 - t.kb0);
+        if (t.kb1 != p.kb_total) continue;
         const int blk = (t.m0 - static_cast<int>(rank) * BM) / (2 * BM);
         const int n = x.a.lists[static_cast<long long>(blk) * kLoraListStride];
         for (int j = 0; j < n && ok; ++j) {
@@ -940,8 +934,12 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
                 f[i] = __ldcg(reinterpret_cast<const float4*>(
                     x.a.V + static_cast<long long>(row) * x.a.ldv + r));
             }
-            wait_empty();
+            const int stage = static_cast<int>(count % S);
+            if (lane == 0) ok = wait_parity(vgo_bar(stage), (gophase >> stage) & 1u, limit, st, 21);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
+            gophase ^= 1u << stage;
+            ++count;
             uint8_t* const sa = base_ptr + stage * Cfg::kStageBytes;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -962,7 +960,6 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_cta(vfull_bar(stage), 0));
-            advance();
           }
         }
       }
@@ -1411,7 +1408,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
 template <int BN, int LOAD, int EPI, bool PAIR, int AM, int MM, int KPB, class LORA>
 constexpr int smem_alloc() {
   using L = Smem<BN, EPI, PAIR, AM, KPB>;
-  constexpr int n = L::kAlloc + (LORA::kOn ? 8 * L::Cfg::kStages : 0);
+  constexpr int n = L::kAlloc + (LORA::kOn ? 2 * 8 * L::Cfg::kStages : 0);
   static_assert(n <= 232448, "shared memory budget");
   return n;
 }
