@@ -505,12 +505,25 @@ __device__ __forceinline__ bool lora_bad(const LoraTailArgs& a, int e) {
   return (b.x | b.y | b.z | b.w) != 0;
 }
 
-// The adapter of entry j of a tile's list, or -1 when it is left to the
-// epilogue (its weights are not all finite).
-__device__ __forceinline__ int lora_entry(const LoraTailArgs& a, int blk, int j) {
-  const int e = a.lists[static_cast<long long>(blk) * kLoraListStride + 1 + j];
-  return lora_bad(a, e) ? -1 : e;
-}
+// Walks a tile's list, one usable entry ahead.  An adapter whose weights are not
+// all finite is left out: the epilogue adds it.
+struct LoraWalk {
+  const int* list;
+  int left;      // entries not looked at yet
+  int next;      // the next usable adapter, -1 at the end
+  __device__ __forceinline__ void start(const LoraTailArgs& a, int blk) {
+    list = a.lists + static_cast<long long>(blk) * kLoraListStride;
+    left = *list;
+    find(a);
+  }
+  __device__ __forceinline__ void find(const LoraTailArgs& a) {
+    next = -1;
+    while (next < 0 && left-- > 0) {
+      const int e = *++list;
+      if (!lora_bad(a, e)) next = e;
+    }
+  }
+};
 
 template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1,
           class LORA = NoLora>
@@ -559,6 +572,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   auto vfull_bar = [&](int s) { return base + static_cast<uint32_t>(L::kUsed) + 8u * s; };
   // adapters: stage s is free for a V tile (told by this CTA's producer)
   auto vgo_bar = [&](int s) { return vfull_bar(S + s); };
+  // adapters: whether a stage of the tile's adapters follows stage s (written by
+  // the producer before it arms the stage)
+  volatile uint32_t* const s_more =
+      reinterpret_cast<uint32_t*>(base_ptr + L::kUsed + 16 * S);
   auto stage_a = [&](int s) { return base + static_cast<uint32_t>(s * Cfg::kStageBytes); };
   auto stage_b = [&](int s) { return stage_a(s) + kAB; };
 
@@ -628,10 +645,20 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         UnitCursor cur = first_unit(p, worker);
         Unit t;
         while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
+          LoraWalk walk{};
           for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
             if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 1)) {
               ok = false;
               break;
+            }
+            if constexpr (LORA::kOn) {
+              // the list's first entries are fetched where the ring still holds
+              // loads in flight: two dependent reads, over a microsecond
+              if (t.kb1 == p.kb_total) {
+                if (kb == max(t.kb0, t.kb1 - 3))
+                  walk.start(x.a, (t.m0 - static_cast<int>(rank) * BM) / (2 * BM));
+                if (kb + 1 == t.kb1) s_more[stage] = walk.next >= 0;
+              }
             }
             // k-blocks of this stage (the unit's last stage may hold one)
             const int nk = KPB == 1 ? 1 : min(KPB, t.kb1 - kb);
@@ -689,20 +716,19 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           }
           if constexpr (LORA::kOn) {
             if (!ok || t.kb1 != p.kb_total) continue;
-            const int blk = (t.m0 - static_cast<int>(rank) * BM) / (2 * BM);
-            const int n = x.a.lists[static_cast<long long>(blk) * kLoraListStride];
             const int bcols = t.ncols / 2;
             // a box: 64 columns of 32 ranks, or 64 rows of 64 (32 used)
             constexpr uint32_t kBox = LORA::kTransB ? 8192u : 4096u;
-            for (int j = 0; j < n && ok; ++j) {
-              const int e = lora_entry(x.a, blk, j);
-              if (e < 0) continue;
+            while (ok && walk.next >= 0) {
+              const int e = walk.next;
+              walk.find(x.a);
               for (int c32 = 0; c32 < x.a.chunks; ++c32) {
                 if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 18)) {
                   ok = false;
                   break;
                 }
                 mbar_arrive(vgo_bar(stage));
+                s_more[stage] = c32 + 1 < x.a.chunks || walk.next >= 0;
                 const uint32_t fb = map_to_cta(full_bar(stage), 0);
                 if (leader)
                   mbar_arrive_expect_tx(full_bar(stage),
@@ -802,6 +828,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         const uint32_t buf = local & 1u, use = local >> 1;
         if (!wait_parity(acce_bar(buf), (use & 1u) ^ 1u, limit, st, 3)) break;
         tc_fence_after();
+        uint32_t more = 0;   // a stage of adapters follows
         const uint32_t idesc = t.ncols == BN ? idesc_full : idesc_half;
         const uint32_t d_tmem = tmem_base + buf * Cfg::kAccStride;
         for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
@@ -810,6 +837,9 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             break;
           }
           tc_fence_after();
+          if constexpr (LORA::kOn) {
+            if (kb + 1 == t.kb1 && t.kb1 == p.kb_total) more = s_more[stage];
+          }
           const int nk = KPB == 1 ? 1 : min(KPB, t.kb1 - kb);
           for (int j = 0; j < nk; ++j) {
             const uint32_t a0 = stage_a(stage) + j * Cfg::kKbBytes, b0 = a0 + kAB;
@@ -837,35 +867,29 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           }
         }
         if constexpr (LORA::kOn) {
-          if (ok && t.kb1 == p.kb_total) {
-            const int blk = t.m0 / (2 * BM);
-            const int n = x.a.lists[static_cast<long long>(blk) * kLoraListStride];
-            for (int j = 0; j < n && ok; ++j) {
-              if (lora_entry(x.a, blk, j) < 0) continue;
-              for (int c32 = 0; c32 < x.a.chunks; ++c32) {
-                if (!wait_parity(full_bar(stage), phase, limit, st, 19) ||
-                    !wait_parity_cluster(vfull_bar(stage), (vphase >> stage) & 1u, limit, st, 20)) {
-                  ok = false;
-                  break;
-                }
-                vphase ^= 1u << stage;
-                tc_fence_after();
-                const uint32_t a0 = stage_a(stage), b0 = a0 + kAB;
-                const int steps = (min(32, x.a.R - 32 * c32) + kUmmaK - 1) / kUmmaK;
-                for (int kk = 0; kk < steps; ++kk) {
-                  const uint64_t bd =
-                      LORA::kTransB ? smem_desc_sw128(b0 + kk * (kUmmaK * 2), 16u, 1024u)
-                                    : smem_desc_sw128(b0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u);
-                  const uint32_t av = a0 + kk * (kUmmaK * 2);
-                  mma_f16_ss_pair(d_tmem, smem_desc_sw128(av, 16u, 1024u), bd, idesc, 1u);
-                  mma_f16_ss_pair(d_tmem, smem_desc_sw128(av + 64, 16u, 1024u), bd, idesc, 1u);
-                }
-                mma_commit_pair_multicast(empty_bar(stage), 3);
-                if (++stage == S) {
-                  stage = 0;
-                  phase ^= 1u;
-                }
-              }
+          for (int c32 = 0; ok && more; c32 = c32 + 1 < x.a.chunks ? c32 + 1 : 0) {
+            if (!wait_parity(full_bar(stage), phase, limit, st, 19) ||
+                !wait_parity_cluster(vfull_bar(stage), (vphase >> stage) & 1u, limit, st, 20)) {
+              ok = false;
+              break;
+            }
+            vphase ^= 1u << stage;
+            more = s_more[stage];
+            tc_fence_after();
+            const uint32_t a0 = stage_a(stage), b0 = a0 + kAB;
+            const int steps = (min(32, x.a.R - 32 * c32) + kUmmaK - 1) / kUmmaK;
+            for (int kk = 0; kk < steps; ++kk) {
+              const uint64_t bd =
+                  LORA::kTransB ? smem_desc_sw128(b0 + kk * (kUmmaK * 2), 16u, 1024u)
+                                : smem_desc_sw128(b0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u);
+              const uint32_t av = a0 + kk * (kUmmaK * 2);
+              mma_f16_ss_pair(d_tmem, smem_desc_sw128(av, 16u, 1024u), bd, idesc, 1u);
+              mma_f16_ss_pair(d_tmem, smem_desc_sw128(av + 64, 16u, 1024u), bd, idesc, 1u);
+            }
+            mma_commit_pair_multicast(empty_bar(stage), 3);
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
             }
           }
         }
@@ -917,23 +941,33 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
         count += static_cast<uint32_t>(t.kb1 - t.kb0);
         if (t.kb1 != p.kb_total) continue;
-        const int blk = (t.m0 - static_cast<int>(rank) * BM) / (2 * BM);
-        const int n = x.a.lists[static_cast<long long>(blk) * kLoraListStride];
-        for (int j = 0; j < n && ok; ++j) {
-          const int e = lora_entry(x.a, blk, j);
-          if (e < 0) continue;
+        // the ids of this warp's rows, once per tile
+        int id[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = t.m0 + r0 + 4 * i;
+          id[i] = row < p.M ? __ldg(x.a.ids + row) : -1;
+        }
+        LoraWalk walk;
+        walk.start(x.a, (t.m0 - static_cast<int>(rank) * BM) / (2 * BM));
+        while (ok && walk.next >= 0) {
+          const int e = walk.next;
+          walk.find(x.a);
           for (int c32 = 0; c32 < x.a.chunks && ok; ++c32) {
             // the 16 rows' entries, on their way while the stage is waited for
+            // (all asked for, other adapters' dropped: a branch around each
+            // load would make 16 round trips of them)
             float4 f[16];
             const int r = 32 * c32 + 4 * q;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int row = t.m0 + r0 + 4 * i;
-              f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (row < p.M && r < x.a.ldv && x.a.ids[row] == e)
-                f[i] = __ldcg(reinterpret_cast<const float4*>(
-                    x.a.V + static_cast<long long>(row) * x.a.ldv + r));
+              const int row = min(t.m0 + r0 + 4 * i, p.M - 1);
+              f[i] = __ldcg(reinterpret_cast<const float4*>(
+                  x.a.V + static_cast<long long>(row) * x.a.ldv + min(r, x.a.ldv - 4)));
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (r >= x.a.ldv || id[i] != e) f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             const int stage = static_cast<int>(count % S);
             if (lane == 0) ok = wait_parity(vgo_bar(stage), (gophase >> stage) & 1u, limit, st, 21);
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -1074,6 +1108,14 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           for (int l = 0; l < 4; ++l) prefetch_l2(part + 8 * l);
         }
       }
+      // adapters: this row's, when the epilogue has to add it
+      int bad_e = -1;
+      if constexpr (LORA::kOn) {
+        if (finish && row < p.M) {
+          const int e = __ldg(x.a.ids + row);
+          if (e >= 0 && e < x.a.adapters && lora_bad(x.a, e)) bad_e = e;
+        }
+      }
       // C of the first sub-chunk is requested before the accumulator is ready.
       uint4 c_next[4];
       if (!kCs && EPI == kEpiTma && has_c && finish && !t.tail) load_c_sub(p, row, colw, c_next);
@@ -1198,23 +1240,20 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           if constexpr (LORA::kOn) {
             // a row whose adapter has weights that are not all finite: added here,
             // so that no other row meets them (0 * Inf)
-            if (row < p.M) {
-              const int e = x.a.ids[row];
-              if (e >= 0 && e < x.a.adapters && lora_bad(x.a, e)) {
-                const float* v = x.a.V + static_cast<long long>(row) * x.a.ldv;
-                const uint16_t* f = x.a.F + static_cast<long long>(e) * x.a.f_stride;
-                for (int r = 0; r < x.a.R; ++r) {
-                  const float vr = v[r];
+            if (bad_e >= 0) {
+              const float* v = x.a.V + static_cast<long long>(row) * x.a.ldv;
+              const uint16_t* f = x.a.F + static_cast<long long>(bad_e) * x.a.f_stride;
+              for (int r = 0; r < x.a.R; ++r) {
+                const float vr = v[r];
 #pragma unroll
-                  for (int i = 0; i < kSubCols; ++i)
-                    if (col0 + i < p.N) {
-                      const uint16_t w = LORA::kTransB
-                                             ? f[static_cast<long long>(col0 + i) * x.a.ldf + r]
-                                             : f[static_cast<long long>(r) * x.a.ldf + col0 + i];
-                      cur[i] = __float_as_uint(
-                          fmaf(vr, __half2float(__ushort_as_half(w)), __uint_as_float(cur[i])));
-                    }
-                }
+                for (int i = 0; i < kSubCols; ++i)
+                  if (col0 + i < p.N) {
+                    const uint16_t w = LORA::kTransB
+                                           ? f[static_cast<long long>(col0 + i) * x.a.ldf + r]
+                                           : f[static_cast<long long>(r) * x.a.ldf + col0 + i];
+                    cur[i] = __float_as_uint(
+                        fmaf(vr, __half2float(__ushort_as_half(w)), __uint_as_float(cur[i])));
+                  }
               }
             }
           }
@@ -1408,7 +1447,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
 template <int BN, int LOAD, int EPI, bool PAIR, int AM, int MM, int KPB, class LORA>
 constexpr int smem_alloc() {
   using L = Smem<BN, EPI, PAIR, AM, KPB>;
-  constexpr int n = L::kAlloc + (LORA::kOn ? 2 * 8 * L::Cfg::kStages : 0);
+  constexpr int n = L::kAlloc + (LORA::kOn ? (2 * 8 + 4) * L::Cfg::kStages : 0);
   static_assert(n <= 232448, "shared memory budget");
   return n;
 }

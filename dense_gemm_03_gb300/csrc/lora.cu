@@ -9,11 +9,11 @@
 // with a = ids[i]; a row whose id names no adapter (negative or >= adapters)
 // has only the shared projection, and no adapter's weights touch it.
 //
-//   up to 128 rows forward   lora_stream.cu: W streamed once
-//   more rows, gradients     lora_shrink.cu for V and U, the pair kernel of
-//                            gemm_f16_tc_kernel.cuh with the adapters as more
-//                            k-blocks of its tiles for C and dX,
-//                            lora_outer.cu for dA and dB
+//   V and U     lora_shrink.cu (up to 128 rows forward: in lora_stream.cu)
+//   C and dX    lora_stream.cu where the result has few tiles; else the pair
+//               kernel of gemm_f16_tc_kernel.cuh with the adapters as more
+//               k-blocks of its tiles
+//   dA and dB   lora_outer.cu
 // V and U are fp32; every sum is fp32; C and dX are rounded once.
 #include <initializer_list>
 
@@ -120,38 +120,48 @@ size_t counter_bytes(int M) { return 4 * 8 * static_cast<size_t>((M + 127) / 128
 
 int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const LoraDevice& d,
             cudaStream_t stream) {
-  const bool few = p.M <= kLoraStreamRows;
+  const bool chunks = lora_stream_suits(p.M, p.N, d.sms);
+  const bool few = p.M <= kLoraShrinkRows;   // the stream makes V itself
   // the pair kernel aligns W by itself
-  Aligned x(p.X, p.ldx, p.M, p.K, true), w(p.W, p.ldw, p.K, p.N, few);
+  Aligned x(p.X, p.ldx, p.M, p.K, true), w(p.W, p.ldw, p.K, p.N, chunks);
   Aligned a(p.A, p.lda, 1ll * p.adapters * p.K, p.R, true, few);
   Aligned b(p.B, p.ldb, 1ll * p.adapters * p.R, p.N, true);
   const size_t copies = x.bytes() + w.bytes() + a.bytes() + b.bytes();
   LoraShrinkPlan s = shrink_plan(p);
+  LoraStream t{};
   auto describe = [&]() {   // of the operands as they are by now
     s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, nullptr, 0};
     s.njobs = 1;
-    s.check = p.B;
-    s.ld_check = p.ldb;
-    s.check_stride = p.b_stride();
-    s.check_rows = p.R;
-    s.check_cols = p.N;
+    if (!chunks) {
+      s.check = p.B;
+      s.ld_check = p.ldb;
+      s.check_stride = p.b_stride();
+      s.check_rows = p.R;
+      s.check_cols = p.N;
+    }
+    t = LoraStream{p.X, p.W, C, p.ldx, p.ldw, ldc, p.M, p.N, p.K, p.R, p.adapters, 0, p.B, p.ldb,
+                   p.b_stride(), nullptr, s.ldv, p.A, p.lda, p.a_stride(), p.ids, p.scales, alpha,
+                   beta};
   };
   describe();
   void *buf = nullptr, *zero = nullptr;
-  const size_t need = copies + (few ? lora_stream_bytes(p, d.sms) : lora_shrink_bytes(s, d.sms));
+  const size_t shrink = few ? 0 : lora_shrink_bytes(s, d.sms);
+  const size_t need = copies + shrink + (chunks ? lora_stream_bytes(t, d.sms) : 0);
   if (int rc = routed_scratch(stream, need, &buf, counter_bytes(p.M), &zero)) return rc;
   uint8_t* const rest = static_cast<uint8_t*>(buf) + copies;
   if (int rc = align_operands({{x, &p.X, &p.ldx}, {w, &p.W, &p.ldw}, {a, &p.A, &p.lda},
                                {b, &p.B, &p.ldb}},
                               static_cast<uint8_t*>(buf), d.sms, stream))
     return rc;
-  if (few) {
-    if (int rc = lora_stream(p, C, ldc, alpha, beta, rest, d, stream)) return rc;
+  describe();
+  if (!few)
+    if (int rc = lora_shrink(s, rest, static_cast<unsigned int*>(zero), d, stream)) return rc;
+  if (chunks) {
+    t.V = few ? nullptr : s.job[0].V;
+    if (int rc = lora_stream(t, rest + shrink, d, stream)) return rc;
     set_last_path(copies ? "lora.stream.realigned" : "lora.stream");
     return GEMM_OK;
   }
-  describe();
-  if (int rc = lora_shrink(s, rest, static_cast<unsigned int*>(zero), d, stream)) return rc;
   LoraCall call{};
   call.trans = false;
   call.tail = LoraTailArgs{s.job[0].V, s.ldv, p.ids, s.lists, s.bad, p.B, p.ldb, p.b_stride(),
@@ -166,41 +176,53 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
 int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, float* dA, float* dB,
               float alpha, float beta, const LoraDevice& d, cudaStream_t stream) {
   const bool use_u = dX || dA, use_v = dB != nullptr;
+  const bool chunks = dX && lora_stream_suits(p.M, p.K, d.sms);
   Aligned g(G, ldg, p.M, p.N, true), x(p.X, p.ldx, p.M, p.K, dA || dB);
   Aligned a(p.A, p.lda, 1ll * p.adapters * p.K, p.R, dX || dB);
   Aligned b(p.B, p.ldb, 1ll * p.adapters * p.R, p.N, use_u);
-  const size_t copies = g.bytes() + x.bytes() + a.bytes() + b.bytes();
+  Aligned w(p.W, p.ldw, p.K, p.N, chunks);
+  const size_t copies = g.bytes() + x.bytes() + a.bytes() + b.bytes() + w.bytes();
   LoraShrinkPlan s = shrink_plan(p);
+  LoraStream t{};
   auto describe = [&]() {
     s.njobs = 0;
     if (use_u) s.job[s.njobs++] = LoraShrinkJob{G, ldg, p.N, p.B, p.ldb, p.b_stride(), 1, nullptr, 0};
     if (use_v)
       s.job[s.njobs++] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, nullptr, 0};
-    if (dX) {
+    if (dX && !chunks) {
       s.check = p.A;
       s.ld_check = p.lda;
       s.check_stride = p.a_stride();
       s.check_rows = p.K;
       s.check_cols = p.R;
     }
+    // any address for V: the stream makes none of its own
+    t = LoraStream{G, p.W, dX, ldg, p.ldw, lddx, p.M, p.K, p.N, p.R, p.adapters, 1, p.A, p.lda,
+                   p.a_stride(), p.scales ? p.scales : reinterpret_cast<const float*>(p.ids), s.ldv,
+                   nullptr, 0, 0, p.ids, nullptr, alpha, 0.0f};
   };
   describe();
   LoraOuter o{p.X, G, p.ldx, ldg, nullptr, nullptr, s.ldv, p.ids, dA, dB, p.M, p.N, p.K, p.R,
               p.adapters, alpha, beta};
   const bool outer = dA || dB;
   const size_t shrink_bytes = lora_shrink_bytes(s, d.sms);
+  const size_t stream_bytes = chunks ? lora_round256(lora_stream_bytes(t, d.sms)) : 0;
   void *buf = nullptr, *zero = nullptr;
-  if (int rc = routed_scratch(stream, copies + shrink_bytes + (outer ? lora_outer_bytes(o) : 0),
+  if (int rc = routed_scratch(stream, copies + shrink_bytes + stream_bytes +
+                                          (outer ? lora_outer_bytes(o) : 0),
                               &buf, counter_bytes(p.M), &zero))
     return rc;
   uint8_t* const rest = static_cast<uint8_t*>(buf) + copies;
   if (int rc = align_operands({{g, &G, &ldg}, {x, &p.X, &p.ldx}, {a, &p.A, &p.lda},
-                               {b, &p.B, &p.ldb}},
+                               {b, &p.B, &p.ldb}, {w, &p.W, &p.ldw}},
                               static_cast<uint8_t*>(buf), d.sms, stream))
     return rc;
   describe();
   if (int rc = lora_shrink(s, rest, static_cast<unsigned int*>(zero), d, stream)) return rc;
-  if (dX) {
+  if (chunks) {
+    t.V = s.job[0].V;
+    if (int rc = lora_stream(t, rest + shrink_bytes, d, stream)) return rc;
+  } else if (dX) {
     LoraCall call{};
     call.trans = true;
     call.tail = LoraTailArgs{s.job[0].V, s.ldv, p.ids, s.lists, s.bad, p.A, p.lda, p.a_stride(),
@@ -216,9 +238,10 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
     o.ldg = ldg;
     o.U = s.job[0].V;
     o.V = s.job[s.njobs - 1].V;
-    if (int rc = lora_outer(o, rest + shrink_bytes, d, stream)) return rc;
+    if (int rc = lora_outer(o, rest + shrink_bytes + stream_bytes, d, stream)) return rc;
   }
-  set_last_path(copies ? "lora_grad.tiles.realigned" : "lora_grad.tiles");
+  set_last_path(chunks ? (copies ? "lora_grad.stream.realigned" : "lora_grad.stream")
+                       : (copies ? "lora_grad.tiles.realigned" : "lora_grad.tiles"));
   return GEMM_OK;
 }
 

@@ -30,13 +30,32 @@ struct LoraDevice {
   unsigned long long wait_limit_ns;
 };
 
-// The forward for a few rows (M <= kLoraStreamRows): W streamed once.  Every
-// operand has rows on the 16-byte grid; A has zero columns up to a multiple of
-// eight.
-constexpr int kLoraStreamRows = 128;
-size_t lora_stream_bytes(const LoraArgs& p, int sms);
-int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta, void* scratch,
-                const LoraDevice& d, cudaStream_t stream);
+// C := alpha (X W + V F[a]) + beta C by K chunks with their sum in a kernel of
+// its own (lora_stream.cu): F[a] is R x N, or N x R when trans, and W then N x K.
+// V is given ([M][ldv]), or made here from A (up to kLoraShrinkRows rows; A has
+// zero columns up to a multiple of eight).  Operands have rows on the 16-byte
+// grid, except C.
+constexpr int kLoraShrinkRows = 128;
+struct LoraStream {
+  const uint16_t *X, *W;
+  uint16_t* C;
+  long long ldx, ldw, ldc;
+  int M, N, K, R, adapters, trans;
+  const uint16_t* F;
+  long long ldf, f_stride;
+  const float* V;
+  int ldv;
+  const uint16_t* A;
+  long long lda, a_stride;
+  const int* ids;
+  const float* scales;
+  float alpha, beta;
+};
+// Whether the chunks suit an M x N result better than whole 256 x 256 tiles on
+// CTA pairs: a few rows, or so few tiles that half the pairs would be idle.
+bool lora_stream_suits(int M, int N, int sms);
+size_t lora_stream_bytes(const LoraStream& p, int sms);
+int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStream_t stream);
 
 // The low-rank products of many rows (lora_shrink.cu): V = s x F[a], F[a] a
 // C x R matrix, or R x C when k_major.

@@ -270,17 +270,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           float4 f[16];
           uint32_t foreign = 0u;   // bit i: row 4 i + r4 of the block is another adapter's
           float top = 0.0f;
+          // all rows asked for, other adapters' dropped: a branch around each
+          // load would make 16 round trips of them
+          int id[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            id[i] = __ldg(p.ids + min(row0 + 4 * i, p.M - 1));
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            f[i] = __ldcg(reinterpret_cast<const float4*>(
+                y + static_cast<long long>(min(row0 + 4 * i, p.M - 1)) * p.ldv +
+                min(rank, p.ldv - 4)));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const int row = row0 + 4 * i;
-            if (row < p.M) {
-              if (__ldg(p.ids + row) != t.a)
-                foreign |= 1u << i;
-              else if (rank < p.ldv)
-                f[i] = __ldcg(reinterpret_cast<const float4*>(
-                    y + static_cast<long long>(row) * p.ldv + rank));
-            }
+            const bool in = row0 + 4 * i < p.M;
+            if (in && id[i] != t.a) foreign |= 1u << i;
+            if (!in || id[i] != t.a || rank >= p.ldv) f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           }
           // the largest finite magnitude (an infinite entry stays infinite)
 #pragma unroll
@@ -389,12 +394,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int h = 0; h < 2; ++h) {
         const int c = t.tile * 256 + h * 128 + col;
         if (c < C) {
+          if (t.src == 0 && p.R % 4 == 0) {
+            // nr is a multiple of four: 16-byte stores along the ranks
+            float* const o = out + static_cast<long long>(c) * p.R + r0;
 #pragma unroll
-          for (int r = 0; r < 32; ++r)
-            if (r < nr)
-              __stcg(out + (t.src ? static_cast<long long>(r0 + r) * C + c
-                                  : static_cast<long long>(c) * p.R + r0 + r),
-                     h ? acc1[r] : acc0[r]);
+            for (int r = 0; r < 32; r += 4)
+              if (r < nr)
+                __stcg(reinterpret_cast<float4*>(o + r),
+                       h ? make_float4(acc1[r], acc1[r + 1], acc1[r + 2], acc1[r + 3])
+                         : make_float4(acc0[r], acc0[r + 1], acc0[r + 2], acc0[r + 3]));
+          } else {
+#pragma unroll
+            for (int r = 0; r < 32; ++r)
+              if (r < nr)
+                __stcg(out + (t.src ? static_cast<long long>(r0 + r) * C + c
+                                    : static_cast<long long>(c) * p.R + r0 + r),
+                       h ? acc1[r] : acc0[r]);
+          }
         }
       }
     }
@@ -417,22 +433,47 @@ struct SumArgs {
 
 constexpr int kSumThreads = 256;
 
+// One block per (1024 elements of a slice of dA or dB, adapter); four elements
+// a thread, 256 apart.
 __global__ void __launch_bounds__(kSumThreads) lora_outer_sum_kernel(const SumArgs p) {
+  __shared__ int place[kSumThreads];   // present ranges, in order
+  __shared__ int count;
   griddep_wait();
   const int a = blockIdx.y;
-  const long long na = p.out[0] ? p.elems[0] : 0, nb = p.out[1] ? p.elems[1] : 0;
-  for (long long i = 1ll * blockIdx.x * kSumThreads + threadIdx.x; i < na + nb;
-       i += 1ll * gridDim.x * kSumThreads) {
-    const int src = i < na ? 0 : 1;
-    const long long e = src ? i - na : i;
-    const float* part = p.part + (src ? p.part_b : 0) + e;
-    float s = 0.0f;
-    for (int r = 0; r < p.ranges; ++r) {
-      const int k = p.table[r * p.adapters + a];
-      if (k >= 0) s += __ldcg(part + k * p.part_stride);
+  const long long blocks_a = p.out[0] ? (p.elems[0] + 4 * kSumThreads - 1) / (4 * kSumThreads) : 0;
+  const int src = blockIdx.x < blocks_a ? 0 : 1;
+  const long long e0 = (src ? blockIdx.x - blocks_a : blockIdx.x) * (4ll * kSumThreads) + threadIdx.x;
+  const long long n = p.elems[src];
+  const float* const part = p.part + (src ? p.part_b : 0);
+  float s[4] = {};
+  for (int r0 = 0; r0 < p.ranges; r0 += kSumThreads) {
+    // a warp at a time keeps the places in row order
+    if (threadIdx.x < 32) {
+      int k = 0;
+      for (int r = r0; r < min(p.ranges, r0 + kSumThreads); r += 32) {
+        const int i = r + static_cast<int>(threadIdx.x);
+        const int v = i < p.ranges ? p.table[i * p.adapters + a] : -1;
+        const unsigned int m = __ballot_sync(0xffffffffu, v >= 0);
+        if (v >= 0) place[k + __popc(m & ((1u << threadIdx.x) - 1u))] = v;
+        k += __popc(m);
+      }
+      if (threadIdx.x == 0) count = k;
     }
-    float* o = p.out[src] + a * p.elems[src] + e;
-    *o = p.beta != 0.0f ? fmaf(p.alpha, s, p.beta * *o) : p.alpha * s;
+    __syncthreads();
+#pragma unroll 2
+    for (int k = 0; k < count; ++k) {
+      const float* q = part + place[k] * p.part_stride;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (e0 + j * kSumThreads < n) s[j] += __ldcg(q + e0 + j * kSumThreads);
+    }
+    __syncthreads();
+  }
+  float* const o = p.out[src] + a * n;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const long long e = e0 + j * kSumThreads;
+    if (e < n) o[e] = p.beta != 0.0f ? fmaf(p.alpha, s[j], p.beta * o[e]) : p.alpha * s[j];
   }
 }
 
@@ -521,11 +562,11 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
       return GEMM_ERR_CUDA;
     s.ranges = a.ranges;
     s.beta = r0 == 0 ? o.beta : 1.0f;
-    const long long elems = (o.dA ? s.elems[0] : 0) + (o.dB ? s.elems[1] : 0);
-    const long long blocks = std::min<long long>((elems + kSumThreads - 1) / kSumThreads,
-                                                 std::max(1, 16 * d.sms / o.adapters));
-    cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, blocks)),
-                       static_cast<unsigned>(o.adapters), 1);
+    long long blocks = 0;
+    for (int i = 0; i < 2; ++i)
+      if (s.out[i]) blocks += (s.elems[i] + 4 * kSumThreads - 1) / (4 * kSumThreads);
+    if (blocks > 0x7fffffff) return GEMM_ERR_ARG;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(o.adapters), 1);
     cfg.blockDim = dim3(kSumThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;

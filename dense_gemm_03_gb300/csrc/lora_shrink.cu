@@ -24,10 +24,10 @@ namespace gb300 {
 namespace {
 
 constexpr int kThreads = 192;                // TMA, MMA, 4 epilogue warps
-constexpr int kStages = 4;
+constexpr int kMaxStages = 6;
+constexpr int kRing = 98304;                 // operand ring: two CTAs fit on an SM
 constexpr int kXBytes = 128 * 128;           // 128 rows of a k-block
 constexpr int kFoldKb = 2;                   // k-blocks accumulated in TMEM
-constexpr int kSmemMax = 232448;
 
 struct Args {
   LoraShrinkJob job[2];
@@ -48,46 +48,54 @@ struct Args {
   DeviceStatus* status;
 };
 
-// The distinct adapters of ids[0, n) in order of first occurrence into `list`;
-// returns their number.  slot[i]: place of row i's adapter, -1 for none.  All
-// kThreads threads; n <= 256.
-__device__ int distinct(const int* ids, int n, int adapters, int* s_id, int* list, int* slot,
-                        int* s_cnt) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int a = ids[i];
-    s_id[i] = a >= 0 && a < adapters ? a : -1;
+// The distinct adapters of ids[0, n), n <= 256, in order of first occurrence
+// within and among runs of 32 rows into `list`; returns their number.  slot[i]:
+// place of row i's adapter, -1 for none.  All kThreads threads; `first` has
+// room for 256 words, `cnt` for 10.
+__device__ int distinct(const int* ids, int n, int adapters, int* list, int* slot, int* first,
+                        int* cnt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int runs = (n + 31) / 32;
+  // every run by itself: its adapters and how many, each row's place among them
+  for (int g = warp; g < runs; g += kThreads / 32) {
+    const int i = 32 * g + lane;
+    int a = i < n ? __ldg(ids + i) : -1;
+    if (a >= adapters) a = -1;
+    const unsigned int same = __match_any_sync(0xffffffffu, a);
+    const unsigned int heads =
+        __ballot_sync(0xffffffffu, a >= 0 && (same & ((1u << lane) - 1u)) == 0u);
+    const int head = __ffs(same) - 1;
+    if (i < n) slot[i] = a < 0 ? -1 : __popc(heads & ((1u << head) - 1u));
+    if (heads >> lane & 1u) first[32 * g + __popc(heads & ((1u << lane) - 1u))] = a;
+    if (lane == 0) cnt[1 + g] = __popc(heads);
   }
-  if (threadIdx.x < 8) s_cnt[threadIdx.x] = 0;
   __syncthreads();
-  // slot[i] := the first row with i's adapter, for now
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    int f = -1;
-    if (s_id[i] >= 0)
-      for (f = 0; s_id[f] != s_id[i];) ++f;
-    slot[i] = f;
-  }
-  __syncthreads();
-  // number the first rows (one warp, 32 rows at a time)
-  if (threadIdx.x < 32) {
-    int base = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      const bool first = i < n && slot[i] == i;
-      const unsigned int m = __ballot_sync(0xffffffffu, first);
-      if (first) {
-        const int k = base + __popc(m & ((1u << threadIdx.x) - 1u));
-        list[k] = s_id[i];
-        s_id[i] = ~k;   // its number, marked
+  // one warp joins the runs: run g's adapters (a lane each) against the list so far
+  if (warp == 0) {
+    int total = 0;
+    for (int g = 0; g < runs; ++g) {
+      const int a = lane < cnt[1 + g] ? first[32 * g + lane] : -1;
+      int at = -1;
+      for (int k = 0; k < total; ++k)
+        if (list[k] == a) at = k;
+      const unsigned int fresh = __ballot_sync(0xffffffffu, a >= 0 && at < 0);
+      if (a >= 0) {
+        if (at < 0) {
+          at = total + __popc(fresh & ((1u << lane) - 1u));
+          list[at] = a;
+        }
+        first[32 * g + lane] = at;
       }
-      base += __popc(m);
+      total += __popc(fresh);
+      __syncwarp();
     }
-    if (threadIdx.x == 0) s_cnt[0] = base;
+    if (lane == 0) cnt[0] = total;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kThreads)
-    if (slot[i] >= 0) slot[i] = ~s_id[slot[i]];
+    if (slot[i] >= 0) slot[i] = first[(i & ~31) + slot[i]];
   __syncthreads();
-  return s_cnt[0];
+  return cnt[0];
 }
 
 // RP: columns of an adapter; COLS: columns of a pass (whole adapters).
@@ -96,27 +104,27 @@ struct Cfg {
   static constexpr int kCols = RP > 64 ? RP : 64;
   static constexpr int kGroup = kCols / RP;            // adapters per pass
   static constexpr int kNBytes = RP > 64 ? 16384 : 8192;   // MN-major: 64-column boxes
-  static constexpr int kStageBytes = kXBytes + kGroup * kNBytes;
   static constexpr int kTmemCols = 2 * kCols;
-  static constexpr int kSmem = kStages * kStageBytes + 1024 + 8 * (2 * kStages + 5) + 16;
-  static_assert(kSmem <= kSmemMax, "shared memory budget");
+  static constexpr int kSmem = kRing + 1024 + 8 * (2 * kMaxStages + 5) + 16;
+  static_assert(kRing / (kXBytes + kGroup * kNBytes) >= 2, "two stages");
 };
 
 template <int RP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX0,
                           const __grid_constant__ CUtensorMap tmF0,
                           const __grid_constant__ CUtensorMap tmX1,
                           const __grid_constant__ CUtensorMap tmF1, const Args p) {
   using G = Cfg<RP>;
-  __shared__ int s_id[256], s_list[256], s_slot[256], s_cnt[8];
+  __shared__ int s_first[256], s_list[256], s_slot[256], s_cnt[10];
   griddep_launch_dependents();
   const int b = blockIdx.x;
   if (b < p.first_list) {
     // ---- a quarter of an adapter: are its weights finite (if a row uses it)
     const int adapter = b / kLoraBadParts;
     bool used = false;
-    for (int i = threadIdx.x; i < p.M; i += kThreads) used |= p.ids[i] == adapter;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < p.M; i += kThreads) used |= __ldg(p.ids + i) == adapter;
     int bad = 0;
     if (__syncthreads_or(used)) {
       const uint16_t* f = p.check + static_cast<long long>(adapter) * p.check_stride;
@@ -146,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (b < p.first_item[0]) {
     // ---- the distinct adapters of a 256-row block
     const int blk = b - p.first_list, row0 = blk * 256;
-    const int n = distinct(p.ids + row0, min(256, p.M - row0), p.adapters, s_id, s_list, s_slot,
+    const int n = distinct(p.ids + row0, min(256, p.M - row0), p.adapters, s_list, s_slot, s_first,
                            s_cnt);
     int* const out = p.lists + static_cast<long long>(blk) * kLoraListStride;
     for (int i = threadIdx.x; i < n; i += kThreads) out[1 + i] = s_list[i];
@@ -167,16 +175,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t bars = base + kStages * G::kStageBytes;
+  const uint32_t bars = base + kRing;
   auto full_bar = [&](int s) { return bars + 8u * s; };
-  auto empty_bar = [&](int s) { return bars + 8u * (kStages + s); };
-  auto accf_bar = [&](uint32_t i) { return bars + 8u * (2 * kStages + i); };
-  auto acce_bar = [&](uint32_t i) { return bars + 8u * (2 * kStages + 2 + i); };
-  const uint32_t done_bar = bars + 8u * (2 * kStages + 4);
-  uint8_t* const tmem_ptr = base_ptr + kStages * G::kStageBytes + 8 * (2 * kStages + 5);
+  auto empty_bar = [&](int s) { return bars + 8u * (kMaxStages + s); };
+  auto accf_bar = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + i); };
+  auto acce_bar = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + 2 + i); };
+  const uint32_t done_bar = bars + 8u * (2 * kMaxStages + 4);
+  uint8_t* const tmem_ptr = base_ptr + kRing + 8 * (2 * kMaxStages + 5);
   const int warp = warp_id_uniform(), lane = static_cast<int>(lane_id());
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(full_bar(s), 1u);
       mbar_init(empty_bar(s), 1u);
     }
@@ -192,12 +200,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_addr(tmem_ptr), G::kTmemCols);
     tmem_relinquish();
   }
-  const int n = distinct(p.ids + row0, rows, p.adapters, s_id, s_list, s_slot, s_cnt);
+  const int n = distinct(p.ids + row0, rows, p.adapters, s_list, s_slot, s_first, s_cnt);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
   const int passes = (n + G::kGroup - 1) / G::kGroup;
+  // a stage holds the rows and as many adapters as a pass can have here
+  const uint32_t stage_bytes = kXBytes + min(max(n, 1), G::kGroup) * G::kNBytes;
+  const int S = min(kMaxStages, static_cast<int>(kRing / stage_bytes));
   const unsigned long long limit = p.wait_limit_ns;
   DeviceStatus* const st = p.status;
   const int fboxes = job.k_major ? 1 : (p.R + 63) / 64;
@@ -216,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(full_bar(stage), kXBytes + gn * fbytes);
-          const uint32_t dst = base + stage * G::kStageBytes;
+          const uint32_t dst = base + stage * stage_bytes;
           tma_load_2d(dst, tmX, full_bar(stage), kb * 64, row0);
           for (int j = 0; j < gn; ++j) {
             const uint32_t f = dst + kXBytes + j * G::kNBytes;
@@ -228,15 +239,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ++issued;
-          if (++stage == kStages) {
+          if (++stage == S) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      const uint32_t left = min(issued, static_cast<uint32_t>(kStages));
+      const uint32_t left = min(issued, static_cast<uint32_t>(S));
       for (uint32_t i = issued - left; i < issued; ++i)
-        settle_wait(full_bar(static_cast<int>(i % kStages)), (i / kStages) & 1u, st, 71);
+        settle_wait(full_bar(static_cast<int>(i % S)), (i / S) & 1u, st, 71);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
-            const uint32_t x0 = base + stage * G::kStageBytes, f0 = x0 + kXBytes;
+            const uint32_t x0 = base + stage * stage_bytes, f0 = x0 + kXBytes;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint64_t ad = smem_desc_sw128(x0 + kk * 32, 16u, 1024u);
@@ -273,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             mma_commit(empty_bar(stage));
-            if (++stage == kStages) {
+            if (++stage == S) {
               stage = 0;
               phase ^= 1u;
             }
@@ -399,7 +410,7 @@ int launch(const CUtensorMap* maps, const Args& a, int grid, cudaStream_t stream
 }
 
 int slices_of(int tiles, int kb, int sms) {
-  // about one CTA per SM, at least four k-blocks each
+  // about one CTA per SM and job, at least four k-blocks each
   return std::max(1, std::min({sms / tiles, kb / 4, 16}));
 }
 

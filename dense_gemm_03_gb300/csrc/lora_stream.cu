@@ -1,12 +1,14 @@
-// lora_stream.cu -- the adapter product for a few rows (decoding), where the
-// time is that of streaming W (and the adapters) from HBM once.
+// lora_stream.cu -- the adapter product (and dX) where whole output tiles would
+// leave SMs idle: a few rows (decoding), where the time is that of streaming W
+// and the adapters from HBM once, and small outputs with a long K.
 //
 //   lora_shrink_kernel   V = s X A by (row, K slice) on CUDA cores: at most 128
 //                        rows x K x R multiply-adds, nothing beside the bytes
-//   row_stream_kernel    X W as fp32 partial sums by (128 columns, K chunk): W
-//                        is the M operand of tcgen05.mma, the rows of X the N
-//                        operand, both by TMA.  It does not depend on the
-//                        shrink, which runs beside it on the same SMs
+//                        (more rows: lora_shrink.cu)
+//   row_stream_kernel    X W as fp32 partial sums by (256 rows, 128 columns, K
+//                        chunk): W is the M operand of tcgen05.mma, the rows of
+//                        X the N operand, both by TMA.  It does not depend on
+//                        the shrink, which runs beside it on the same SMs
 //                        (programmatic launch).
 //   lora_combine_kernel  C = alpha (sum of the chunks + V B[a]) + beta C, the
 //                        chunks in k order, everything fp32, one rounding
@@ -15,9 +17,14 @@
 // on the tensor cores it would be 128 rows of zeros per adapter for 2 R
 // multiply-adds per output that hide behind the loads of B anyway.
 //
+// Summing the chunks in a kernel of its own spreads that over all SMs: the pair
+// kernel's own K slices, added up by the last to finish, took 8 us longer at
+// 1000 x 1001 x 4096.
+//
 // Shared memory per ring stage: two 64-column boxes of 64 k-rows of W (128-byte
-// swizzle, MN-major: LBO 8 KB, SBO 1 KB), then the rows of X, 64 halves of k
-// each (K-major, SBO 1 KB).
+// swizzle, MN-major: LBO 8 KB, SBO 1 KB; or, for a W stored transposed, two
+// boxes of 64 rows, K-major, SBO 1 KB), then the rows of X, 64 halves of k each
+// (K-major, SBO 1 KB).
 #include "lora.h"
 
 namespace gb300 {
@@ -94,15 +101,15 @@ constexpr int kWBytes = 2 * 64 * 128;       // 128 columns of a k-block of W
 constexpr int kMaxStages = 12;
 constexpr int kEpi = 4;
 constexpr int kStreamThreads = 32 * (2 + kEpi);
-constexpr int kAccCols = 128;
-constexpr int kTmemCols = 2 * kAccCols;
+constexpr int kBlockRows = 256;             // rows of an item (N of the MMA)
 constexpr int kSmemMax = 232448;
 
 struct StreamArgs {
-  int M, N;
-  int kb, chunks, items;   // k-blocks, chunks per unit, units x chunks
-  int stages, stage_bytes, n_cols;
-  float* part;             // [unit][chunk][row][128]
+  int M, N, trans;
+  int kb, chunks, units, items;   // k-blocks, chunks, 128-column units, blocks x units x chunks
+  int stages, stage_bytes, n_cols, acc_cols;
+  int block_rows;          // rows of a block's partial sums: min(M, kBlockRows)
+  float* part;             // [block][unit][chunk][row][128]
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
 };
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     fence_proxy_async_smem();
   }
   if (warp == 1) {
-    tmem_alloc(smem_addr(tmem_ptr), kTmemCols);
+    tmem_alloc(smem_addr(tmem_ptr), 2 * p.acc_cols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -156,8 +163,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       uint32_t phase = 0, issued = 0;
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        const int unit = it / p.chunks, c = it - unit * p.chunks;
-        const int n0 = unit * 128;
+        const int c = it % p.chunks, n0 = it / p.chunks % p.units * 128;
+        const int row0 = it / p.chunks / p.units * kBlockRows;
         const bool two = n0 + 64 < p.N;      // the second box lies in the matrix
         const uint32_t bytes =
             static_cast<uint32_t>((two ? kWBytes : kWBytes / 2) + p.n_cols * 128);
@@ -168,9 +175,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           }
           const uint32_t dst = base + static_cast<uint32_t>(stage * p.stage_bytes);
           mbar_arrive_expect_tx(full_bar(stage), bytes);
-          tma_load_2d_hint(dst, &tmW, full_bar(stage), n0, kb * 64, policy);
-          if (two) tma_load_2d_hint(dst + 8192, &tmW, full_bar(stage), n0 + 64, kb * 64, policy);
-          tma_load_2d(dst + kWBytes, &tmX, full_bar(stage), kb * 64, 0);
+          // W evict-first when no other block of rows reads it
+          for (int b = 0; b <= two; ++b) {
+            const int n = n0 + 64 * b, cx = p.trans ? kb * 64 : n, cy = p.trans ? n : kb * 64;
+            if (p.M <= kBlockRows)
+              tma_load_2d_hint(dst + b * 8192, &tmW, full_bar(stage), cx, cy, policy);
+            else
+              tma_load_2d(dst + b * 8192, &tmW, full_bar(stage), cx, cy);
+          }
+          tma_load_2d(dst + kWBytes, &tmX, full_bar(stage), kb * 64, row0);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -185,7 +198,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = make_idesc(0u, 128u, static_cast<uint32_t>(p.n_cols), 1u, 0u);
+      const uint32_t idesc =
+          make_idesc(0u, 128u, static_cast<uint32_t>(p.n_cols), p.trans ? 0u : 1u, 0u);
       int stage = 0;
       uint32_t phase = 0, local = 0;
       bool ok = true;
@@ -204,7 +218,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           const uint32_t w0 = base + static_cast<uint32_t>(stage * p.stage_bytes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss(tmem + buf * kAccCols, smem_desc_sw128(w0 + kk * 2048, 8192u, 1024u),
+            mma_f16_ss(tmem + buf * p.acc_cols,
+                       p.trans ? smem_desc_sw128(w0 + kk * 32, 16u, 1024u)
+                               : smem_desc_sw128(w0 + kk * 2048, 8192u, 1024u),
                        smem_desc_sw128(w0 + kWBytes + kk * 32, 16u, 1024u), idesc,
                        (kb > kb0 || kk > 0) ? 1u : 0u);
           mma_commit(empty_bar(stage));
@@ -228,17 +244,19 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       const uint32_t buf = local & 1u;
       if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 65)) break;
       tc_fence_after();
-      const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * kAccCols;
-      float* const out = p.part + static_cast<long long>(it) * p.M * 128 + 32 * quad + lane;
-      for (int r0 = 0; r0 < p.M; r0 += 16) {   // n_cols is a multiple of 16
+      const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * p.acc_cols;
+      float* const out =
+          p.part + static_cast<long long>(it) * p.block_rows * 128 + 32 * quad + lane;
+      const int rows = min(kBlockRows, p.M - it / p.chunks / p.units * kBlockRows);
+      for (int r0 = 0; r0 < rows; r0 += 16) {   // n_cols is a multiple of 16
         uint32_t g[8], h[8];
         tmem_ld_32x32b_x8(d0 + r0, g);
         tmem_ld_32x32b_x8(d0 + r0 + 8, h);
         tmem_wait_ld2(g, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (r0 + i < p.M) __stcg(out + (r0 + i) * 128, __uint_as_float(g[i]));
-          if (r0 + 8 + i < p.M) __stcg(out + (r0 + 8 + i) * 128, __uint_as_float(h[i]));
+          if (r0 + i < rows) __stcg(out + (r0 + i) * 128, __uint_as_float(g[i]));
+          if (r0 + 8 + i < rows) __stcg(out + (r0 + 8 + i) * 128, __uint_as_float(h[i]));
         }
       }
       tc_fence_before();
@@ -250,64 +268,105 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) tmem_dealloc(tmem, 2 * p.acc_cols);
 }
 
 // ------------------------------------------------------------------ combine
 constexpr int kCombThreads = 128;
 
 struct CombineArgs {
-  const float *part, *V;
-  const uint16_t* B;
+  const float *part, *V;   // V: [row][slice][ldv]
+  const uint16_t* F;       // F[a]: R x N, or N x R
   const int* ids;
   uint16_t* C;
-  long long ldb, b_stride, ldc;
-  int M, N, R, ldv, adapters, chunks, slices;   // ldv: ranks of V
+  long long ldf, f_stride, ldc;
+  int M, N, R, ldv, adapters, chunks, slices, units, block_rows;
   float alpha, beta;
   bool vec_c;              // rows of C on the 8-byte grid
 };
 
 // One block per (row, 512 columns), four columns a thread.
+template <bool TRANS>
 __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const CombineArgs p) {
   __shared__ float vs[kLoraMaxRank];
   const int strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
   const int i = blockIdx.x / strips;
   const int c = (blockIdx.x - i * strips) * 4 * kCombThreads + 4 * static_cast<int>(threadIdx.x);
+  griddep_launch_dependents();
   const int a = p.ids[i];
   const bool has = a >= 0 && a < p.adapters;
   const bool whole = c + 4 <= p.N;
-  const uint16_t* const f = p.B + (has ? static_cast<long long>(a) * p.b_stride : 0) + c;
+  const uint16_t* const f = p.F + (has ? static_cast<long long>(a) * p.f_stride : 0) +
+                            (TRANS ? static_cast<long long>(c) * p.ldf : c);
   // nothing of the kernels before this one is read yet: bring this block's
-  // part of B[a] into L2
-  if (has && c < p.N && (threadIdx.x & 15) == 0)
-    for (int r = 0; r < p.R; ++r) prefetch_l2(f + r * p.ldb);
+  // part of F[a] into L2
+  if (has && c < p.N) {
+    if (TRANS) {
+      for (int j = 0; j < 4 && c + j < p.N; ++j) prefetch_l2(f + j * p.ldf);
+    } else if ((threadIdx.x & 15) == 0) {
+      for (int r = 0; r < p.R; ++r) prefetch_l2(f + r * p.ldf);
+    }
+  }
   griddep_wait();
   if (has)
     for (int r = threadIdx.x; r < p.R; r += kCombThreads) {
       const float* v = p.V + static_cast<long long>(i) * p.slices * p.ldv + r;
-      float s = 0.0f;
-      for (int k = 0; k < p.slices; ++k) s += __ldcg(v + k * p.ldv);
+      float t[kMaxSlices], s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxSlices; ++k) t[k] = k < p.slices ? __ldcg(v + k * p.ldv) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxSlices; ++k) s += t[k];
       vs[r] = s;
     }
   __syncthreads();
   if (c >= p.N) return;
-  const float* part = p.part + (static_cast<long long>(c >> 7) * p.chunks * p.M + i) * 128 + (c & 127);
+  const int blk = i / kBlockRows;
+  const long long chunk_elems = static_cast<long long>(p.block_rows) * 128;
+  const float* part = p.part + (static_cast<long long>(blk) * p.units + (c >> 7)) * p.chunks * chunk_elems +
+                      (i - blk * kBlockRows) * 128 + (c & 127);
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = 0; k < p.chunks; ++k) {
-    const float4 t = __ldcg(reinterpret_cast<const float4*>(part + static_cast<long long>(k) * p.M * 128));
-    s.x += t.x;
-    s.y += t.y;
-    s.z += t.z;
-    s.w += t.w;
+  for (int k0 = 0; k0 < p.chunks; k0 += 8) {
+    float4 t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      t[k] = k0 + k < p.chunks
+                 ? __ldcg(reinterpret_cast<const float4*>(part + (k0 + k) * chunk_elems))
+                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s.x += t[k].x;
+      s.y += t[k].y;
+      s.z += t[k].z;
+      s.w += t[k].w;
+    }
   }
   float o[4] = {s.x, s.y, s.z, s.w};
   if (has) {
     float l[4] = {};
-    if (whole) {
+    if (TRANS) {
+      const int r8 = p.R / 8 * 8;
+      for (int r = 0; r < r8; r += 8) {
+        uint4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = __ldg(reinterpret_cast<const uint4*>(f + (c + j < p.N ? j * p.ldf : 0) + r));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t h[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float2 b = lora_h2f2(h[u]);
+            l[j] = fmaf(vs[r + 2 * u], b.x, l[j]);
+            l[j] = fmaf(vs[r + 2 * u + 1], b.y, l[j]);
+          }
+        }
+      }
+      for (int r = r8; r < p.R; ++r)
+        for (int j = 0; j < 4 && c + j < p.N; ++j) l[j] = fmaf(vs[r], lora_h2f(f[j * p.ldf + r]), l[j]);
+    } else if (whole) {
 #pragma unroll 8
       for (int r = 0; r < p.R; ++r) {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(f + r * p.ldb));
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(f + r * p.ldf));
         const float2 b0 = lora_h2f2(b.x), b1 = lora_h2f2(b.y);
         l[0] = fmaf(vs[r], b0.x, l[0]);
         l[1] = fmaf(vs[r], b0.y, l[1]);
@@ -316,7 +375,7 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
       }
     } else {
       for (int r = 0; r < p.R; ++r)
-        for (int j = 0; j < p.N - c; ++j) l[j] = fmaf(vs[r], lora_h2f(f[r * p.ldb + j]), l[j]);
+        for (int j = 0; j < p.N - c; ++j) l[j] = fmaf(vs[r], lora_h2f(f[r * p.ldf + j]), l[j]);
     }
     for (int j = 0; j < 4; ++j) o[j] += l[j];
   }
@@ -341,16 +400,17 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
 }
 
 // Chunks per unit: the count whose rounds of chunks over the SMs, in k-block
-// times of an SM (16 KB at its share of HBM, ~0.36 us), and whose partial sums
-// (1 KB per row written and read, through L2 at about twice HBM's rate) take
-// least.
-int plan_chunks(int units, int kb, int M, int sms) {
+// times of an SM, and whose partial sums take least.  A k-block takes 0.36 us
+// (its 16 KB of W at an SM's share of HBM) or, for a full block of rows, as long
+// as its 48 KB from L2; the partial sums are 1 KB per row written and read,
+// through L2 at about twice HBM's rate.
+int plan_chunks(int units, int blocks, int kb, int rows, int sms) {
   int best = 1;
   double best_t = 1e30;
   for (int c = 1; c <= std::min(kb, 32); ++c) {
-    const long long rounds = (1ll * units * c + sms - 1) / sms;
+    const long long rounds = (1ll * units * blocks * c + sms - 1) / sms;
     const double t = static_cast<double>(rounds) * ((kb + c - 1) / c + 2) +
-                     1.9e-4 * units * c * M;
+                     1.9e-4 * units * blocks * c * rows;
     if (t < best_t) {
       best_t = t;
       best = c;
@@ -359,30 +419,49 @@ int plan_chunks(int units, int kb, int M, int sms) {
   return best;
 }
 
-}  // namespace
-
-namespace {
-
 // K slices of the shrink: about four blocks per SM in all, at least 64 long.
-int shrink_slices(const LoraArgs& p, int sms) {
+int shrink_slices(const LoraStream& p, int sms) {
   return std::max(1, std::min({kMaxSlices, 4 * sms / p.M, p.K / 64}));
 }
 
-}  // namespace
-
-size_t lora_stream_bytes(const LoraArgs& p, int sms) {
-  const int units = (p.N + 127) / 128, r8 = (p.R + 7) / 8 * 8;
-  return lora_round256(4 * static_cast<size_t>(p.M) * shrink_slices(p, sms) * r8) +
-         4 * static_cast<size_t>(units) * plan_chunks(units, (p.K + 63) / 64, p.M, sms) * p.M * 128;
+StreamArgs plan(const LoraStream& p, int sms) {
+  StreamArgs t{};
+  t.M = p.M;
+  t.N = p.N;
+  t.trans = p.trans;
+  t.kb = (p.K + 63) / 64;
+  t.units = (p.N + 127) / 128;
+  t.block_rows = std::min(p.M, kBlockRows);
+  const int blocks = (p.M + kBlockRows - 1) / kBlockRows;
+  t.chunks = plan_chunks(t.units, blocks, t.kb, t.block_rows, sms);
+  t.items = blocks * t.units * t.chunks;
+  t.n_cols = (t.block_rows + 15) / 16 * 16;
+  t.acc_cols = t.n_cols > 128 ? 256 : 128;
+  t.stage_bytes = kWBytes + t.n_cols * 128;
+  t.stages = std::min(kMaxStages, (kSmemMax - 2048) / t.stage_bytes);
+  return t;
 }
 
-int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta, void* scratch,
-                const LoraDevice& d, cudaStream_t stream) {
-  const int units = (p.N + 127) / 128, kb = (p.K + 63) / 64;
-  const int rows = (p.M + 15) / 16 * 16;
+}  // namespace
+
+bool lora_stream_suits(int M, int N, int sms) {
+  const long long tiles = static_cast<long long>((M + 255) / 256) * ((N + 255) / 256);
+  return M <= kLoraShrinkRows || 4 * tiles <= sms;
+}
+
+size_t lora_stream_bytes(const LoraStream& p, int sms) {
+  const StreamArgs t = plan(p, sms);
+  const size_t v = p.V ? 0 : 4 * static_cast<size_t>(p.M) * shrink_slices(p, sms) * ((p.R + 7) / 8 * 8);
+  return lora_round256(v) + 4 * static_cast<size_t>(t.items) * t.block_rows * 128;
+}
+
+int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStream_t stream) {
+  StreamArgs t = plan(p, d.sms);
   CUtensorMap tmW{}, tmX{};
-  if (int rc = encode_map_f16(&tmW, p.W, p.K, p.N, p.ldw, 64, 64)) return rc;
-  if (int rc = encode_map_f16(&tmX, p.X, p.M, p.K, p.ldx, 64, rows)) return rc;
+  if (int rc = p.trans ? encode_map_f16(&tmW, p.W, p.N, p.K, p.ldw, 64, 64)
+                       : encode_map_f16(&tmW, p.W, p.K, p.N, p.ldw, 64, 64))
+    return rc;
+  if (int rc = encode_map_f16(&tmX, p.X, p.M, p.K, p.ldx, 64, t.n_cols)) return rc;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
   static bool configured[64] = {};
@@ -392,39 +471,38 @@ int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
       return GEMM_ERR_CUDA;
     configured[dev] = true;
   }
-  ShrinkArgs s{};
-  const int want = shrink_slices(p, d.sms), r8 = (p.R + 7) / 8 * 8;
-  s.len = (p.K + want - 1) / want;
-  s.slices = (p.K + s.len - 1) / s.len;
-  StreamArgs t{};
-  t.M = p.M;
-  t.N = p.N;
-  t.kb = kb;
-  t.chunks = plan_chunks(units, kb, p.M, d.sms);
-  if (1ll * units * t.chunks > (1 << 30)) return GEMM_ERR_ARG;
-  t.items = units * t.chunks;
-  t.n_cols = rows;
-  t.stage_bytes = kWBytes + rows * 128;
-  t.stages = std::min(kMaxStages, (kSmemMax - 2048) / t.stage_bytes);
   t.wait_limit_ns = d.wait_limit_ns;
   t.status = d.status;
-
-  s.V = static_cast<float*>(scratch);
-  t.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
-                                    lora_round256(4 * static_cast<size_t>(p.M) * want * r8));
-  s.X = p.X;
-  s.A = p.A;
-  s.ids = p.ids;
-  s.scales = p.scales;
-  s.ldx = p.ldx;
-  s.lda = p.lda;
-  s.a_stride = p.a_stride();
-  s.M = p.M;
-  s.K = p.K;
-  s.R = r8;
-  s.adapters = p.adapters;
-  lora_shrink_kernel<<<p.M * s.slices, kShrinkThreads, 0, stream>>>(s);
-  if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
+  CombineArgs c{};
+  c.V = p.V;
+  c.ldv = p.ldv;
+  c.slices = 1;
+  uint8_t* rest = static_cast<uint8_t*>(scratch);
+  if (!p.V) {
+    ShrinkArgs s{};
+    const int want = shrink_slices(p, d.sms), r8 = (p.R + 7) / 8 * 8;
+    s.len = (p.K + want - 1) / want;
+    s.slices = (p.K + s.len - 1) / s.len;
+    s.V = reinterpret_cast<float*>(rest);
+    rest += lora_round256(4 * static_cast<size_t>(p.M) * want * r8);
+    s.X = p.X;
+    s.A = p.A;
+    s.ids = p.ids;
+    s.scales = p.scales;
+    s.ldx = p.ldx;
+    s.lda = p.lda;
+    s.a_stride = p.a_stride;
+    s.M = p.M;
+    s.K = p.K;
+    s.R = r8;
+    s.adapters = p.adapters;
+    lora_shrink_kernel<<<p.M * s.slices, kShrinkThreads, 0, stream>>>(s);
+    if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
+    c.V = s.V;
+    c.ldv = r8;
+    c.slices = s.slices;
+  }
+  t.part = reinterpret_cast<float*>(rest);
 
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -439,31 +517,30 @@ int lora_stream(const LoraArgs& p, uint16_t* C, int ldc, float alpha, float beta
   if (counted_launch(cudaLaunchKernelEx(&cfg, row_stream_kernel, tmW, tmX, t)) != cudaSuccess)
     return GEMM_ERR_CUDA;
 
-  CombineArgs c{};
   c.part = t.part;
-  c.V = s.V;
-  c.B = p.B;
+  c.F = p.F;
   c.ids = p.ids;
-  c.C = C;
-  c.ldb = p.ldb;
-  c.b_stride = p.b_stride();
-  c.ldc = ldc;
+  c.C = p.C;
+  c.ldf = p.ldf;
+  c.f_stride = p.f_stride;
+  c.ldc = p.ldc;
   c.M = p.M;
   c.N = p.N;
   c.R = p.R;
   c.adapters = p.adapters;
   c.chunks = t.chunks;
-  c.slices = s.slices;
-  c.ldv = r8;
-  c.alpha = alpha;
-  c.beta = beta;
-  c.vec_c = (reinterpret_cast<uintptr_t>(C) & 7u) == 0 && ldc % 4 == 0;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.M * ((p.N + 4 * kCombThreads - 1) / (4 * kCombThreads))), 1, 1);
+  c.units = t.units;
+  c.block_rows = t.block_rows;
+  c.alpha = p.alpha;
+  c.beta = p.beta;
+  c.vec_c = (reinterpret_cast<uintptr_t>(p.C) & 7u) == 0 && p.ldc % 4 == 0;
+  const long long blocks = 1ll * p.M * ((p.N + 4 * kCombThreads - 1) / (4 * kCombThreads));
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(kCombThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  if (counted_launch(cudaLaunchKernelEx(&cfg, lora_combine_kernel, c)) != cudaSuccess)
-    return GEMM_ERR_CUDA;
-  return GEMM_OK;
+  const cudaError_t e = p.trans ? cudaLaunchKernelEx(&cfg, lora_combine_kernel<true>, c)
+                                : cudaLaunchKernelEx(&cfg, lora_combine_kernel<false>, c);
+  return counted_launch(e) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 }  // namespace gb300
