@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kRange = 512;                  // rows of an item
 constexpr int kLoaders = 4;
-constexpr int kEpi = 4;
+constexpr int kEpi = 8;                      // epilogue warps: four per accumulator
 constexpr int kThreads = 32 * (2 + kLoaders + kEpi);
 constexpr int kStages = 5;
 constexpr int kXBytes = 4 * 64 * 128;        // 64 rows x 256 columns
@@ -43,8 +43,8 @@ static_assert(kStages + 2 < kScales, "scales in flight");
 static_assert(kSmem + 16 + kMaxMasks + kMaxMasks / 8 + 64 <= 232448, "shared memory budget");
 
 struct Args {
-  const float* y[2];       // U, V: [M][ldv]
-  int cols[2], tiles[2];   // columns of X and dC, 256-column tiles (0: not wanted)
+  const float *u, *v;      // [M][ldv]
+  int cols_x, cols_g, tiles_x, tiles_g;   // of X and dC, 256-column tiles (0: not wanted)
   const int* ids;
   int M, R, adapters, ldv, chunks, ranges, row0;
   float* part;             // [present][tile columns and ranks as in dA, then as in dB]
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.table[m] = place;
   }
   griddep_wait();   // U and V
-  const int all_tiles = p.tiles[0] + p.tiles[1];
+  const int all_tiles = p.tiles_x + p.tiles_g;
   const int per = all_tiles * p.chunks;
   const long long items = 1ll * present * per;
   auto item_at = [&](long long it) {
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v = static_cast<int>(it - 1ll * t.present * per);
     t.chunk = v / all_tiles;
     const int tile = v - t.chunk * all_tiles;
-    t.src = tile < p.tiles[0] ? 0 : 1;
-    t.tile = t.src ? tile - p.tiles[0] : tile;
+    t.src = tile < p.tiles_x ? 0 : 1;
+    t.tile = t.src ? tile - p.tiles_x : tile;
     // the last group whose prefix does not pass the place, then within it
     int lo = 0, hi = words / (kGroupMasks / 4) - 1;
     while (lo < hi) {
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
         const Item t = item_at(it);
-        const int left = p.cols[t.src] - t.tile * 256;
+        const int left = (t.src ? p.cols_g : p.cols_x) - t.tile * 256;
         const int boxes = min(4, (left + 63) / 64);
         const CUtensorMap* const tm = t.src ? &tmG : &tmX;
         for (int m = t.mask; m && ok; m &= m - 1) {
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
       const Item t = item_at(it);
       const int rank = 32 * t.chunk + 4 * q;
-      const float* const y = p.y[t.src];
+      const float* const y = t.src ? p.v : p.u;
       for (int m = t.mask; m; m &= m - 1, ++seq) {
         if (static_cast<int>(seq & (kLoaders - 1)) == l) {
           const int row0 = p.row0 + t.range * kRange + (__ffs(m) - 1) * 64 + r4;
@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int quad = warp & 3, col = 32 * quad + lane;
+    const int quad = warp & 3, half = (warp - 2 - kLoaders) / 4;
     uint32_t local = 0;
     bool ok = true;
     for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
       const Item t = item_at(it);
-      float acc0[32], acc1[32];
+      float acc[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc0[i] = acc1[i] = 0.0f;
+      for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
       for (int n = __popc(t.mask); n > 0; --n, ++local) {
         const uint32_t buf = local & 1u;
         if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 88)) {
@@ -366,51 +366,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const float down = s_scale[local & (kScales - 1)];
-        const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * 128;
-#pragma unroll
-        for (int c = 0; c < 32; c += 8) {
-          uint32_t g[8], h[8];
-          tmem_ld_32x32b_x8(d0 + c, g);
-          tmem_ld_32x32b_x8(d0 + 32 + c, h);
-          tmem_wait_ld2(g, h);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc0[c + i] = fmaf(__uint_as_float(g[i]) + __uint_as_float(h[i]), down, acc0[c + i]);
-          tmem_ld_32x32b_x8(d0 + 64 + c, g);
-          tmem_ld_32x32b_x8(d0 + 96 + c, h);
-          tmem_wait_ld2(g, h);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc1[c + i] = fmaf(__uint_as_float(g[i]) + __uint_as_float(h[i]), down, acc1[c + i]);
-        }
+        const uint32_t d0 =
+            tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * 128 + half * 64;
+        uint32_t hi[32], lo[32];
+        tmem_ld_32x32b_x32(d0, hi);
+        tmem_ld_32x32b_x32(d0 + 32, lo);
+        tmem_wait_ld32(hi, lo);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acce_bar(buf));
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          acc[i] = fmaf(__uint_as_float(hi[i]) + __uint_as_float(lo[i]), down, acc[i]);
       }
       if (!ok) break;
-      const int C = p.cols[t.src], r0 = 32 * t.chunk, nr = min(32, p.R - r0);
+      const int C = t.src ? p.cols_g : p.cols_x, r0 = 32 * t.chunk, nr = min(32, p.R - r0);
+      const int c = t.tile * 256 + half * 128 + 32 * quad + lane;
       float* const out = p.part + t.present * p.part_stride + (t.src ? p.part_b : 0);
+      if (c < C) {
+        if (t.src == 0 && p.R % 4 == 0) {
+          // nr is a multiple of four: 16-byte stores along the ranks
+          float* const o = out + static_cast<long long>(c) * p.R + r0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = t.tile * 256 + h * 128 + col;
-        if (c < C) {
-          if (t.src == 0 && p.R % 4 == 0) {
-            // nr is a multiple of four: 16-byte stores along the ranks
-            float* const o = out + static_cast<long long>(c) * p.R + r0;
+          for (int r = 0; r < 32; r += 4)
+            if (r < nr)
+              __stcg(reinterpret_cast<float4*>(o + r),
+                     make_float4(acc[r], acc[r + 1], acc[r + 2], acc[r + 3]));
+        } else {
 #pragma unroll
-            for (int r = 0; r < 32; r += 4)
-              if (r < nr)
-                __stcg(reinterpret_cast<float4*>(o + r),
-                       h ? make_float4(acc1[r], acc1[r + 1], acc1[r + 2], acc1[r + 3])
-                         : make_float4(acc0[r], acc0[r + 1], acc0[r + 2], acc0[r + 3]));
-          } else {
-#pragma unroll
-            for (int r = 0; r < 32; ++r)
-              if (r < nr)
-                __stcg(out + (t.src ? static_cast<long long>(r0 + r) * C + c
-                                    : static_cast<long long>(c) * p.R + r0 + r),
-                       h ? acc1[r] : acc0[r]);
-          }
+          for (int r = 0; r < 32; ++r)
+            if (r < nr)
+              __stcg(out + (t.src ? static_cast<long long>(r0 + r) * C + c
+                                  : static_cast<long long>(c) * p.R + r0 + r),
+                     acc[r]);
         }
       }
     }
@@ -424,9 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // themselves.
 struct SumArgs {
   const float* part;
-  long long part_stride, part_b, elems[2];   // elements per adapter of dA, dB
+  long long part_stride, part_b, elems_a, elems_b;   // elements per adapter of dA, dB
   const int* table;
-  float* out[2];
+  float *dA, *dB;
   int adapters, ranges;
   float alpha, beta;
 };
@@ -440,10 +428,10 @@ __global__ void __launch_bounds__(kSumThreads) lora_outer_sum_kernel(const SumAr
   __shared__ int count;
   griddep_wait();
   const int a = blockIdx.y;
-  const long long blocks_a = p.out[0] ? (p.elems[0] + 4 * kSumThreads - 1) / (4 * kSumThreads) : 0;
+  const long long blocks_a = p.dA ? (p.elems_a + 4 * kSumThreads - 1) / (4 * kSumThreads) : 0;
   const int src = blockIdx.x < blocks_a ? 0 : 1;
   const long long e0 = (src ? blockIdx.x - blocks_a : blockIdx.x) * (4ll * kSumThreads) + threadIdx.x;
-  const long long n = p.elems[src];
+  const long long n = src ? p.elems_b : p.elems_a;
   const float* const part = p.part + (src ? p.part_b : 0);
   float s[4] = {};
   for (int r0 = 0; r0 < p.ranges; r0 += kSumThreads) {
@@ -469,7 +457,7 @@ __global__ void __launch_bounds__(kSumThreads) lora_outer_sum_kernel(const SumAr
     }
     __syncthreads();
   }
-  float* const o = p.out[src] + a * n;
+  float* const o = (src ? p.dB : p.dA) + a * n;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const long long e = e0 + j * kSumThreads;
@@ -513,12 +501,12 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
   }
   const int ranges = ranges_of(o);
   Args a{};
-  a.y[0] = o.U;
-  a.y[1] = o.V;
-  a.cols[0] = o.K;
-  a.cols[1] = o.N;
-  a.tiles[0] = o.dA ? (o.K + 255) / 256 : 0;
-  a.tiles[1] = o.dB ? (o.N + 255) / 256 : 0;
+  a.u = o.U;
+  a.v = o.V;
+  a.cols_x = o.K;
+  a.cols_g = o.N;
+  a.tiles_x = o.dA ? (o.K + 255) / 256 : 0;
+  a.tiles_g = o.dB ? (o.N + 255) / 256 : 0;
   a.ids = o.ids;
   a.M = o.M;
   a.R = o.R;
@@ -536,11 +524,11 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
   s.part = a.part;
   s.part_stride = a.part_stride;
   s.part_b = a.part_b;
-  s.elems[0] = 1ll * o.K * o.R;
-  s.elems[1] = 1ll * o.R * o.N;
+  s.elems_a = 1ll * o.K * o.R;
+  s.elems_b = 1ll * o.R * o.N;
   s.table = a.table;
-  s.out[0] = o.dA;
-  s.out[1] = o.dB;
+  s.dA = o.dA;
+  s.dB = o.dB;
   s.adapters = o.adapters;
   s.alpha = o.alpha;
   cudaLaunchAttribute attr[1];
@@ -562,9 +550,9 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
       return GEMM_ERR_CUDA;
     s.ranges = a.ranges;
     s.beta = r0 == 0 ? o.beta : 1.0f;
-    long long blocks = 0;
-    for (int i = 0; i < 2; ++i)
-      if (s.out[i]) blocks += (s.elems[i] + 4 * kSumThreads - 1) / (4 * kSumThreads);
+    const long long blocks =
+        (s.dA ? (s.elems_a + 4 * kSumThreads - 1) / (4 * kSumThreads) : 0) +
+        (s.dB ? (s.elems_b + 4 * kSumThreads - 1) / (4 * kSumThreads) : 0);
     if (blocks > 0x7fffffff) return GEMM_ERR_ARG;
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(o.adapters), 1);
     cfg.blockDim = dim3(kSumThreads, 1, 1);
