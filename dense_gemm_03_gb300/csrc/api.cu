@@ -870,13 +870,15 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
     t_last_path = t_path_buf;
     if (lora) {
       const LoraTailArgs& x = lora->tail;
-      CUtensorMap tmE{};
+      CUtensorMap tmE{}, tmV{};
+      if (int rc = make_map_f16(&tmV, x.packed, M, 64 * x.chunks, 64ll * x.chunks, 64, 128))
+        return rc;
       if (int rc = trans_b ? encode_map_f16_stack(&tmE, x.F, N, x.R, x.ldf, x.adapters, x.f_stride,
                                                   64, 64)
                            : encode_map_f16_stack(&tmE, x.F, x.R, N, x.ldf, x.adapters, x.f_stride,
                                                   64, 32))
         return rc;
-      if (launch_gemm_f16_tc_lora(trans_b, epi, tmA, tmB, tmC, tmE, x, a, grid, stream) !=
+      if (launch_gemm_f16_tc_lora(trans_b, epi, tmA, tmB, tmC, tmE, tmV, x, a, grid, stream) !=
           cudaSuccess)
         return GEMM_ERR_CUDA;
       return copy_back();

@@ -8,10 +8,11 @@ namespace {
 
 template <bool TRANS>
 cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                   const CUtensorMap& e, const LoraTailArgs& tail, const TcArgs& args, int grid,
+                   const CUtensorMap& e, const CUtensorMap& v, const LoraTailArgs& tail, const TcArgs& args, int grid,
                    cudaStream_t s) {
   LoraTail<TRANS> x{};
   x.tmE = e;
+  x.tmV = v;
   x.a = tail;
   return epi == kEpiTma
              ? launch_one<256, kLoadTma, kEpiTma, true, 128, 128, 1, LoraTail<TRANS>>(a, b, c, args,
@@ -23,10 +24,11 @@ cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CU
 
 cudaError_t launch_gemm_f16_tc_lora(bool trans, int epi_mode, const CUtensorMap& tmA,
                                     const CUtensorMap& tmB, const CUtensorMap& tmC,
-                                    const CUtensorMap& tmE, const LoraTailArgs& tail,
+                                    const CUtensorMap& tmE, const CUtensorMap& tmV,
+                                    const LoraTailArgs& tail,
                                     const TcArgs& args, int grid, cudaStream_t stream) {
-  return trans ? launch<true>(epi_mode, tmA, tmB, tmC, tmE, tail, args, grid, stream)
-               : launch<false>(epi_mode, tmA, tmB, tmC, tmE, tail, args, grid, stream);
+  return trans ? launch<true>(epi_mode, tmA, tmB, tmC, tmE, tmV, tail, args, grid, stream)
+               : launch<false>(epi_mode, tmA, tmB, tmC, tmE, tmV, tail, args, grid, stream);
 }
 
 }  // namespace gb300

@@ -485,10 +485,13 @@ struct NoLora {
 // Low-rank adapters picked by row, as more k-blocks of the same accumulators
 // (CTA pairs, TMA loads).  A tile's K loop goes on, after its last k-block,
 // over the adapters that occur in its 256 rows: for adapter a and 32 of its
-// ranks, the A part of a stage holds, for the rows of a, those entries of V in
-// two halves (32 hi, then 32 lo columns; zeros in other rows), and the B part
-// the adapter's 32 rows of N columns, which both halves are multiplied with.
-// Two more warps write the A part.  TRANSB: B operands are stored N x K and
+// ranks, the A part of a stage holds the rows' entries of V in two halves (32
+// hi, then 32 lo columns), and the B part the adapter's 32 rows of N columns,
+// which both halves are multiplied with.  Both come by TMA; one more warp
+// overwrites the rows of other adapters by zeros, and another walks the tile's
+// list ahead of the producer, which would otherwise wait for two dependent
+// reads (several microseconds under load) at the end of every tile.
+// TRANSB: B operands are stored N x K and
 // N x R (the gradient's dC W^T + U A^T): K-major tiles of 64-row boxes.
 template <bool TRANSB>
 struct LoraTail {
@@ -496,6 +499,7 @@ struct LoraTail {
   static constexpr bool kTransB = TRANSB;
   static constexpr int kWarps = 2;
   CUtensorMap tmE;        // the adapters' B operand, a stack
+  CUtensorMap tmV;        // V in halves
   LoraTailArgs a;
 };
 
@@ -504,26 +508,6 @@ __device__ __forceinline__ bool lora_bad(const LoraTailArgs& a, int e) {
   const int4 b = *(reinterpret_cast<const int4*>(a.bad) + e);
   return (b.x | b.y | b.z | b.w) != 0;
 }
-
-// Walks a tile's list, one usable entry ahead.  An adapter whose weights are not
-// all finite is left out: the epilogue adds it.
-struct LoraWalk {
-  const int* list;
-  int left;      // entries not looked at yet
-  int next;      // the next usable adapter, -1 at the end
-  __device__ __forceinline__ void start(const LoraTailArgs& a, int blk) {
-    list = a.lists + static_cast<long long>(blk) * kLoraListStride;
-    left = *list;
-    find(a);
-  }
-  __device__ __forceinline__ void find(const LoraTailArgs& a) {
-    next = -1;
-    while (next < 0 && left-- > 0) {
-      const int e = *++list;
-      if (!lora_bad(a, e)) next = e;
-    }
-  }
-};
 
 template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1,
           class LORA = NoLora>
@@ -570,12 +554,17 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   auto cfull_bar = [&](int w, int b) { return bars + 8u * (2 * S + 6 + L::kBufs * w + b); };
   // adapters: the V tile of stage s is written (by the warps of both CTAs)
   auto vfull_bar = [&](int s) { return base + static_cast<uint32_t>(L::kUsed) + 8u * s; };
-  // adapters: stage s is free for a V tile (told by this CTA's producer)
-  auto vgo_bar = [&](int s) { return vfull_bar(S + s); };
+  // adapters: this CTA's part of the V tile of stage s has landed
+  auto vland_bar = [&](int s) { return vfull_bar(S + s); };
+  // adapters: entries of the tiles' lists on their way to the producer
+  constexpr int kQ = 8;
+  auto qfull_bar = [&](int i) { return vfull_bar(2 * S + i); };
+  auto qempty_bar = [&](int i) { return vfull_bar(2 * S + kQ + i); };
   // adapters: whether a stage of the tile's adapters follows stage s (written by
   // the producer before it arms the stage)
   volatile uint32_t* const s_more =
-      reinterpret_cast<uint32_t*>(base_ptr + L::kUsed + 16 * S);
+      reinterpret_cast<uint32_t*>(base_ptr + L::kUsed + 16 * S + 16 * kQ);
+  volatile int* const s_queue = reinterpret_cast<int*>(base_ptr + L::kUsed + 20 * S + 16 * kQ);
   auto stage_a = [&](int s) { return base + static_cast<uint32_t>(s * Cfg::kStageBytes); };
   auto stage_b = [&](int s) { return stage_a(s) + kAB; };
 
@@ -594,8 +583,13 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       for (int b = 0; b < L::kBufs; ++b) mbar_init(cfull_bar(w, b), 1u);
     if constexpr (LORA::kOn)
       for (int s = 0; s < S; ++s) {
-        mbar_init(vfull_bar(s), 2u * LORA::kWarps);
-        mbar_init(vgo_bar(s), 1u);
+        mbar_init(vfull_bar(s), 2u);
+        mbar_init(vland_bar(s), 1u);
+      }
+    if constexpr (LORA::kOn)
+      for (int i = 0; i < kQ; ++i) {
+        mbar_init(qfull_bar(i), 1u);
+        mbar_init(qempty_bar(i), 1u);
       }
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -642,22 +636,34 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         uint32_t phase = 0, issued = 0;
         bool ok = true;
         const uint64_t evict_first = l2_evict_first_policy();
+        int qi = 0;
+        uint32_t qphase = 0;
+        auto pop_entry = [&](int& e) {
+          if (!wait_parity(qfull_bar(qi), qphase, limit, st, 22)) return false;
+          e = s_queue[qi];
+          mbar_arrive(qempty_bar(qi));
+          if (++qi == kQ) {
+            qi = 0;
+            qphase ^= 1u;
+          }
+          return true;
+        };
         UnitCursor cur = first_unit(p, worker);
         Unit t;
         while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
-          LoraWalk walk{};
+          int next_e = -1;   // adapters: the next of the tile's list
           for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
             if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 1)) {
               ok = false;
               break;
             }
             if constexpr (LORA::kOn) {
-              // the list's first entries are fetched where the ring still holds
-              // loads in flight: two dependent reads, over a microsecond
-              if (t.kb1 == p.kb_total) {
-                if (kb == max(t.kb0, t.kb1 - 3))
-                  walk.start(x.a, (t.m0 - static_cast<int>(rank) * BM) / (2 * BM));
-                if (kb + 1 == t.kb1) s_more[stage] = walk.next >= 0;
+              if (kb + 1 == t.kb1 && t.kb1 == p.kb_total) {
+                if (!pop_entry(next_e)) {
+                  ok = false;
+                  break;
+                }
+                s_more[stage] = next_e >= 0;
               }
             }
             // k-blocks of this stage (the unit's last stage may hold one)
@@ -719,16 +725,20 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             const int bcols = t.ncols / 2;
             // a box: 64 columns of 32 ranks, or 64 rows of 64 (32 used)
             constexpr uint32_t kBox = LORA::kTransB ? 8192u : 4096u;
-            while (ok && walk.next >= 0) {
-              const int e = walk.next;
-              walk.find(x.a);
+            while (ok && next_e >= 0) {
+              const int e = next_e;
+              if (!pop_entry(next_e)) {
+                ok = false;
+                break;
+              }
               for (int c32 = 0; c32 < x.a.chunks; ++c32) {
                 if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 18)) {
                   ok = false;
                   break;
                 }
-                mbar_arrive(vgo_bar(stage));
-                s_more[stage] = c32 + 1 < x.a.chunks || walk.next >= 0;
+                s_more[stage] = c32 + 1 < x.a.chunks || next_e >= 0;
+                mbar_arrive_expect_tx(vland_bar(stage), static_cast<uint32_t>(kABytes));
+                tma_load_2d(stage_a(stage), &x.tmV, vland_bar(stage), 64 * c32, t.m0);
                 const uint32_t fb = map_to_cta(full_bar(stage), 0);
                 if (leader)
                   mbar_arrive_expect_tx(full_bar(stage),
@@ -926,76 +936,80 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       tmem_dealloc(tmem_base, Cfg::kTmemCols);
   } else if (LORA::kOn && warp >= R::kWarps) {
     // ------------------------------------------------------------ adapters' V tiles
-    // Warp v writes rows 64v .. 64v + 63 of this CTA's 128; eight lanes share a
-    // row, four ranks each.  The ring goes round without these warps for most of
-    // a tile, so they count its stages and wait for the producer's word on the
-    // stages that are theirs (a wait for the parity of `empty` could meet it a
-    // whole round too late and never end).
+    // The first of these warps hands the usable entries of each tile's list, and
+    // -1 after them, to the producer.  The second clears other adapters' rows of
+    // the V tiles (four rows a lane).  The ring goes round without it for most of
+    // a tile, so it counts the stages and waits for the V tile of a stage that
+    // is its own (a wait for the parity of `empty` could meet it a whole round
+    // too late and never end).
     if constexpr (LORA::kOn) {
-      const int v = warp - R::kWarps;
-      const int q = lane & 7, r0 = 64 * v + (lane >> 3);
-      uint32_t count = 0, gophase = 0;   // stages passed; bit s: parity of vgo_bar(s)
+      const bool walker = warp == R::kWarps;
+      uint32_t count = 0, landphase = 0;   // stages passed; bit s: parity of vland_bar(s)
+      int qi = 0;
+      uint32_t qphase = 0;
       bool ok = true;
+      auto push_entry = [&](int e) {
+        if (lane == 0) ok = wait_parity(qempty_bar(qi), qphase ^ 1u, limit, st, 23);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (ok && lane == 0) {
+          s_queue[qi] = e;
+          mbar_arrive(qfull_bar(qi));
+        }
+        if (++qi == kQ) {
+          qi = 0;
+          qphase ^= 1u;
+        }
+      };
+      auto clear_rows = [&](int e, const int (&id)[4]) {
+        for (int c32 = 0; c32 < x.a.chunks && ok; ++c32, ++count) {
+          const int stage = static_cast<int>(count % S);
+          if (lane == 0) ok = wait_parity(vland_bar(stage), (landphase >> stage) & 1u, limit, st, 21);
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          __syncwarp();
+          if (!ok) return;
+          landphase ^= 1u << stage;
+          uint8_t* const sa = base_ptr + stage * Cfg::kStageBytes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (id[i] != e)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)   // chunks in an order that spreads the banks
+                *reinterpret_cast<uint4*>(sa + (32 * i + lane) * 128 + (((c + lane) & 7) << 4)) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_cta(vfull_bar(stage), 0));
+        }
+      };
       UnitCursor cur = first_unit(p, worker);
       Unit t;
       while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
         count += static_cast<uint32_t>(t.kb1 - t.kb0);
         if (t.kb1 != p.kb_total) continue;
-        // the ids of this warp's rows, once per tile
-        int id[16];
+        int id[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int row = t.m0 + r0 + 4 * i;
-          id[i] = row < p.M ? __ldg(x.a.ids + row) : -1;
+        for (int i = 0; i < 4; ++i) {
+          const int row = t.m0 + 32 * i + lane;
+          id[i] = !walker && row < p.M ? __ldg(x.a.ids + row) : -1;
         }
-        LoraWalk walk;
-        walk.start(x.a, (t.m0 - static_cast<int>(rank) * BM) / (2 * BM));
-        while (ok && walk.next >= 0) {
-          const int e = walk.next;
-          walk.find(x.a);
-          for (int c32 = 0; c32 < x.a.chunks && ok; ++c32) {
-            // the 16 rows' entries, on their way while the stage is waited for
-            // (all asked for, other adapters' dropped: a branch around each
-            // load would make 16 round trips of them)
-            float4 f[16];
-            const int r = 32 * c32 + 4 * q;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int row = min(t.m0 + r0 + 4 * i, p.M - 1);
-              f[i] = __ldcg(reinterpret_cast<const float4*>(
-                  x.a.V + static_cast<long long>(row) * x.a.ldv + min(r, x.a.ldv - 4)));
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (r >= x.a.ldv || id[i] != e) f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            const int stage = static_cast<int>(count % S);
-            if (lane == 0) ok = wait_parity(vgo_bar(stage), (gophase >> stage) & 1u, limit, st, 21);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok) break;
-            gophase ^= 1u << stage;
-            ++count;
-            uint8_t* const sa = base_ptr + stage * Cfg::kStageBytes;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int lr = r0 + 4 * i;
-              const uint32_t h0 = float2_to_half2_bits(f[i].x, f[i].y);
-              const uint32_t h1 = float2_to_half2_bits(f[i].z, f[i].w);
-              const float2 g0 = half2_bits_to_float2(h0), g1 = half2_bits_to_float2(h1);
-              // past the half range the leading half is infinite and stands alone
-              const float l0 = isinf(g0.x) ? 0.0f : f[i].x - g0.x;
-              const float l1 = isinf(g0.y) ? 0.0f : f[i].y - g0.y;
-              const float l2 = isinf(g1.x) ? 0.0f : f[i].z - g1.x;
-              const float l3 = isinf(g1.y) ? 0.0f : f[i].w - g1.y;
-              uint8_t* const rowp = sa + lr * 128 + (q & 1) * 8;
-              *reinterpret_cast<uint2*>(rowp + (((q >> 1) ^ (lr & 7)) << 4)) = make_uint2(h0, h1);
-              *reinterpret_cast<uint2*>(rowp + (((4 + (q >> 1)) ^ (lr & 7)) << 4)) =
-                  make_uint2(float2_to_half2_bits(l0, l1), float2_to_half2_bits(l2, l3));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_cta(vfull_bar(stage), 0));
+        const int* const list =
+            x.a.lists + static_cast<long long>((t.m0 - static_cast<int>(rank) * BM) / (2 * BM)) *
+                            kLoraListStride;
+        const int n = list[0];
+        // 32 entries at a time, an adapter with weights that are not all finite
+        // left out (the epilogue adds it)
+        for (int j0 = 0; j0 < n && ok; j0 += 32) {
+          const int mine = j0 + lane < n ? list[1 + j0 + lane] : -1;
+          const bool usable = mine >= 0 && !lora_bad(x.a, mine);
+          for (unsigned int todo = __ballot_sync(0xffffffffu, usable); todo && ok; todo &= todo - 1) {
+            const int e = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
+            if (walker)
+              push_entry(e);
+            else
+              clear_rows(e, id);
           }
         }
+        if (walker && ok) push_entry(-1);
       }
     }
   } else {
@@ -1447,7 +1461,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
 template <int BN, int LOAD, int EPI, bool PAIR, int AM, int MM, int KPB, class LORA>
 constexpr int smem_alloc() {
   using L = Smem<BN, EPI, PAIR, AM, KPB>;
-  constexpr int n = L::kAlloc + (LORA::kOn ? (2 * 8 + 4) * L::Cfg::kStages : 0);
+  constexpr int n = L::kAlloc + (LORA::kOn ? 20 * L::Cfg::kStages + 20 * 8 : 0);
   static_assert(n <= 232448, "shared memory budget");
   return n;
 }

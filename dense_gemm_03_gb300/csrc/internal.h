@@ -105,7 +105,8 @@ struct TcArgs {
 constexpr int kLoraListStride = 257;   // a 256-row block's list: count, adapters
 constexpr int kLoraBadParts = 4;
 struct LoraTailArgs {
-  const float* V;        // [M][ldv] fp32, the rows' low-rank products; ldv % 4 == 0
+  const float* V;        // [M][ldv] fp32, the rows' low-rank products
+  const uint16_t* packed;   // the same as halves, [M][chunk][32 hi, 32 lo]
   int ldv;
   const int* ids;        // [M]
   const int* lists;      // [256-row block][kLoraListStride]: its distinct adapters
@@ -129,7 +130,8 @@ int gemm_f16_lora_pair(const uint16_t* A, const uint16_t* B, uint16_t* C, int M,
                        const LoraCall& lora, cudaStream_t stream);
 cudaError_t launch_gemm_f16_tc_lora(bool trans, int epi_mode, const CUtensorMap& tmA,
                                     const CUtensorMap& tmB, const CUtensorMap& tmC,
-                                    const CUtensorMap& tmE, const LoraTailArgs& tail,
+                                    const CUtensorMap& tmE, const CUtensorMap& tmV,
+                                    const LoraTailArgs& tail,
                                     const TcArgs& args, int grid, cudaStream_t stream);
 
 // Tensor-core fp16 GEMM (tcgen05).  Maps are ignored by the modes that do not

@@ -116,7 +116,7 @@ LoraShrinkPlan shrink_plan(const LoraArgs& p) {
   return s;
 }
 
-size_t counter_bytes(int M) { return 4 * 8 * static_cast<size_t>((M + 127) / 128); }
+size_t counter_bytes(int M) { return 4 * 2 * static_cast<size_t>((M + 127) / 128); }
 
 int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const LoraDevice& d,
             cudaStream_t stream) {
@@ -130,7 +130,7 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
   LoraShrinkPlan s = shrink_plan(p);
   LoraStream t{};
   auto describe = [&]() {   // of the operands as they are by now
-    s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, nullptr, 0};
+    s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, chunks ? 0 : kLoraPacked};
     s.njobs = 1;
     if (!chunks) {
       s.check = p.B;
@@ -164,7 +164,7 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
   }
   LoraCall call{};
   call.trans = false;
-  call.tail = LoraTailArgs{s.job[0].V, s.ldv, p.ids, s.lists, s.bad, p.B, p.ldb, p.b_stride(),
+  call.tail = LoraTailArgs{s.job[0].V, s.job[0].packed, s.ldv, p.ids, s.lists, s.bad, p.B, p.ldb, p.b_stride(),
                            p.R, p.adapters, (p.R + 31) / 32};
   if (int rc = gemm_f16_lora_pair(p.X, p.W, C, p.M, p.N, p.K, p.ldx, p.ldw, ldc, alpha, beta, call,
                                   stream))
@@ -186,9 +186,12 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   LoraStream t{};
   auto describe = [&]() {
     s.njobs = 0;
-    if (use_u) s.job[s.njobs++] = LoraShrinkJob{G, ldg, p.N, p.B, p.ldb, p.b_stride(), 1, nullptr, 0};
+    if (use_u)
+      s.job[s.njobs++] = LoraShrinkJob{G, ldg, p.N, p.B, p.ldb, p.b_stride(), 1,
+                                       (dX && !chunks ? kLoraPacked : 0) | (dA ? kLoraScaled : 0)};
     if (use_v)
-      s.job[s.njobs++] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, nullptr, 0};
+      s.job[s.njobs++] =
+          LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, kLoraScaled};
     if (dX && !chunks) {
       s.check = p.A;
       s.ld_check = p.lda;
@@ -202,7 +205,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
                    nullptr, 0, 0, p.ids, nullptr, alpha, 0.0f};
   };
   describe();
-  LoraOuter o{p.X, G, p.ldx, ldg, nullptr, nullptr, s.ldv, p.ids, dA, dB, p.M, p.N, p.K, p.R,
+  LoraOuter o{p.X, G, p.ldx, ldg, nullptr, nullptr, p.ids, dA, dB, p.M, p.N, p.K, p.R,
               p.adapters, alpha, beta};
   const bool outer = dA || dB;
   const size_t shrink_bytes = lora_shrink_bytes(s, d.sms);
@@ -225,7 +228,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   } else if (dX) {
     LoraCall call{};
     call.trans = true;
-    call.tail = LoraTailArgs{s.job[0].V, s.ldv, p.ids, s.lists, s.bad, p.A, p.lda, p.a_stride(),
+    call.tail = LoraTailArgs{s.job[0].V, s.job[0].packed, s.ldv, p.ids, s.lists, s.bad, p.A, p.lda, p.a_stride(),
                              p.R, p.adapters, (p.R + 31) / 32};
     if (int rc = gemm_f16_lora_pair(G, p.W, dX, p.M, p.K, p.N, ldg, p.ldw, lddx, alpha, 0.0f, call,
                                     stream))
@@ -236,8 +239,8 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
     o.ldx = p.ldx;
     o.G = G;
     o.ldg = ldg;
-    o.U = s.job[0].V;
-    o.V = s.job[s.njobs - 1].V;
+    o.U = dA ? &s.job[0] : nullptr;
+    o.V = dB ? &s.job[s.njobs - 1] : nullptr;
     if (int rc = lora_outer(o, rest + shrink_bytes + stream_bytes, d, stream)) return rc;
   }
   set_last_path(chunks ? (copies ? "lora_grad.stream.realigned" : "lora_grad.stream")
@@ -260,7 +263,7 @@ int plain_dx(const LoraArgs& p, const uint16_t* G, int ldg, uint16_t* dX, int ld
   LoraCall call{};
   call.trans = true;
   // any mapped matrix for the adapters' tensor map: no tile reads it
-  call.tail = LoraTailArgs{nullptr, 4, none, lists, nullptr, reinterpret_cast<uint16_t*>(buf), 8,
+  call.tail = LoraTailArgs{nullptr, reinterpret_cast<uint16_t*>(buf), 4, none, lists, nullptr, reinterpret_cast<uint16_t*>(buf), 8,
                            8, 1, 1, 1};
   if (int rc = gemm_f16_lora_pair(G, p.W, dX, p.M, p.K, p.N, ldg, p.ldw, lddx, alpha, 0.0f, call,
                                   stream))

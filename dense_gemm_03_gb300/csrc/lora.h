@@ -66,9 +66,15 @@ struct LoraShrinkJob {
   const uint16_t* F;
   long long ldf, f_stride;
   int k_major;
+  int want;               // kLoraPacked, kLoraScaled
   float* V;               // out: [M][ldv]
+  // out: V as hi and lo halves, [M][chunk of 32 ranks][32 hi, 32 lo]; scaled by
+  // a power of two per 128 rows, whose inverses are unscale[]
+  uint16_t *packed, *scaled;
+  float* unscale;
   int tiles;
 };
+constexpr int kLoraPacked = 1, kLoraScaled = 2;
 struct LoraShrinkPlan {
   LoraShrinkJob job[2];
   int njobs;
@@ -83,7 +89,7 @@ struct LoraShrinkPlan {
   int *lists, *bad;       // out: LoraTailArgs::lists and bad
 };
 size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms);
-// `counters`: 8 words per 128 rows, zero before and after.
+// `counters`: 2 words per 128 rows, zero before and after.
 int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const LoraDevice& d,
                 cudaStream_t stream);
 
@@ -92,8 +98,7 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const 
 struct LoraOuter {
   const uint16_t *X, *G;
   long long ldx, ldg;
-  const float *U, *V;     // [M][ldv]
-  int ldv;
+  const LoraShrinkJob *U, *V;   // their scaled halves
   const int* ids;
   float *dA, *dB;
   int M, N, K, R, adapters;

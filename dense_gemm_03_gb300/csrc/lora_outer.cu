@@ -11,11 +11,9 @@
 // without the adapter are skipped.  Items write fp32 partial sums, which
 // lora_outer_sum_kernel adds up in row order.
 //
-// U and V are fp32.  Every 64 rows they are scaled by a power of two that
-// brings their largest magnitude into [2^13, 2^14) before they are split, so
-// gradients of any size keep 22 significant bits relative to it; 64 rows are
-// also what is summed in TMEM (the tensor cores truncate, see lora_shrink.cu),
-// and the scale is taken back as those sums are added up in registers.
+// U and V come scaled by a power of two per 128 rows (lora_shrink.cu); 64 rows
+// are what is summed in TMEM (the tensor cores truncate, see there), and the
+// scale is taken back as those sums are added up in registers.
 //
 // Rows of other adapters in a block have zeros for U (V), and their part of X
 // (dC) is overwritten by zeros in shared memory, so that an Inf or NaN there
@@ -34,19 +32,17 @@ constexpr int kXBytes = 4 * 64 * 128;        // 64 rows x 256 columns
 constexpr int kVBytes = 64 * 128;            // 64 rows x (32 hi, 32 lo)
 constexpr int kStageBytes = kXBytes + kVBytes;
 constexpr int kTmemCols = 256;               // two buffers of two 64-column accumulators
-constexpr int kScales = 8;   // > blocks between the loaders and the epilogue: stages + 2 buffers
 constexpr int kMaxMasks = kLoraMaxAdapters;  // ranges x adapters of a launch
 constexpr int kGroupMasks = 32;              // masks per entry of the prefix
 constexpr int kBars = 3 * kStages + 5;
-constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * kBars + 8 + 4 * kScales;
-static_assert(kStages + 2 < kScales, "scales in flight");
+constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * kBars + 8;
 static_assert(kSmem + 16 + kMaxMasks + kMaxMasks / 8 + 64 <= 232448, "shared memory budget");
 
 struct Args {
-  const float *u, *v;      // [M][ldv]
+  const float *unscale_u, *unscale_v;   // by 128 rows
   int cols_x, cols_g, tiles_x, tiles_g;   // of X and dC, 256-column tiles (0: not wanted)
   const int* ids;
-  int M, R, adapters, ldv, chunks, ranges, row0;
+  int M, R, adapters, chunks, ranges, row0;
   float* part;             // [present][tile columns and ranks as in dA, then as in dB]
   long long part_stride, part_b;
   int* table;              // [range][adapter]: place among the present ones, or -1
@@ -60,7 +56,9 @@ struct Item {
 
 __global__ void __launch_bounds__(kThreads, 1)
     lora_outer_kernel(const __grid_constant__ CUtensorMap tmX,
-                      const __grid_constant__ CUtensorMap tmG, const Args p) {
+                      const __grid_constant__ CUtensorMap tmG,
+                      const __grid_constant__ CUtensorMap tmU,
+                      const __grid_constant__ CUtensorMap tmV, const Args p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -74,7 +72,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t done_bar = bars + 8u * (3 * kStages + 4);
   uint8_t* const tail = base_ptr + kStages * kStageBytes + 8 * kBars;
   uint32_t* const misc = reinterpret_cast<uint32_t*>(tail);            // TMEM address, present
-  volatile float* const s_scale = reinterpret_cast<float*>(tail + 8);
   // [range][adapter] bytes: the 64-row blocks with the adapter; then, per 32 of
   // them, how many nonzero ones come before
   const int nmask = p.ranges * p.adapters;
@@ -198,7 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(boxes * 8192));
+          mbar_arrive_expect_tx(full_bar(stage), static_cast<uint32_t>(boxes * 8192 + kVBytes));
+          tma_load_2d(base + stage * kStageBytes + kXBytes, t.src ? &tmV : &tmU, full_bar(stage),
+                      64 * t.chunk, row);
           for (int b = 0; b < boxes; ++b)
             tma_load_2d(base + stage * kStageBytes + b * 8192, tm, full_bar(stage),
                         t.tile * 256 + b * 64, row);
@@ -254,93 +253,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp < 2 + kLoaders) {
-    // Loader l takes the blocks l, l + 4, ... of the CTA's sequence; eight lanes
-    // share a row, four ranks each.
-    const int l = warp - 2, q = lane & 7, r4 = lane >> 3;
+    // Warp l of these takes the blocks l, l + 4, ... of the CTA's sequence and
+    // clears the rows of other adapters (a lane has two rows).
+    const int l = warp - 2;
     int stage = 0;
     uint32_t phase = 0, seq = 0;
     bool ok = true;
     for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
       const Item t = item_at(it);
-      const int rank = 32 * t.chunk + 4 * q;
-      const float* const y = t.src ? p.v : p.u;
       for (int m = t.mask; m; m &= m - 1, ++seq) {
         if (static_cast<int>(seq & (kLoaders - 1)) == l) {
-          const int row0 = p.row0 + t.range * kRange + (__ffs(m) - 1) * 64 + r4;
-          float4 f[16];
-          uint32_t foreign = 0u;   // bit i: row 4 i + r4 of the block is another adapter's
-          float top = 0.0f;
-          // all rows asked for, other adapters' dropped: a branch around each
-          // load would make 16 round trips of them
-          int id[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            id[i] = __ldg(p.ids + min(row0 + 4 * i, p.M - 1));
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            f[i] = __ldcg(reinterpret_cast<const float4*>(
-                y + static_cast<long long>(min(row0 + 4 * i, p.M - 1)) * p.ldv +
-                min(rank, p.ldv - 4)));
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const bool in = row0 + 4 * i < p.M;
-            if (in && id[i] != t.a) foreign |= 1u << i;
-            if (!in || id[i] != t.a || rank >= p.ldv) f[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          }
-          // the largest finite magnitude (an infinite entry stays infinite)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float v[4] = {fabsf(f[i].x), fabsf(f[i].y), fabsf(f[i].z), fabsf(f[i].w)};
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (v[c] < __int_as_float(0x7F800000)) top = fmaxf(top, v[c]);
-          }
-          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-          // top * 2^e in [2^13, 2^14); |e| <= 100, so that 2^e and 2^-e are normal
-          const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
-          const float up = __int_as_float((127 + e) << 23);
-          if (lane == 0) ok = wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 86);
+          const int row = p.row0 + t.range * kRange + (__ffs(m) - 1) * 64 + lane;
+          const bool f0 = row < p.M && __ldg(p.ids + row) != t.a;
+          const bool f1 = row + 32 < p.M && __ldg(p.ids + row + 32) != t.a;
+          const bool mixed = __any_sync(0xffffffffu, f0 || f1);
+          // a block of one adapter only passes through, but not before its stage
+          // is free: two arrivals in one phase would hide one from the MMA warp
+          if (lane == 0)
+            ok = wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 86) &&
+                 (!mixed || wait_parity(full_bar(stage), phase, limit, st, 87));
           ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          if (lane == 0) s_scale[seq & (kScales - 1)] = __int_as_float((127 - e) << 23);
-          uint8_t* const sx = base_ptr + stage * kStageBytes;
-          uint8_t* const sv = sx + kXBytes;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int lr = 4 * i + r4;
-            const float v[4] = {f[i].x * up, f[i].y * up, f[i].z * up, f[i].w * up};
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint16_t h0 = lora_f2h(v[2 * c]), h1 = lora_f2h(v[2 * c + 1]);
-              const uint16_t g0 =
-                  (h0 & 0x7FFFu) >= 0x7C00u ? 0 : lora_f2h(v[2 * c] - lora_h2f(h0));
-              const uint16_t g1 =
-                  (h1 & 0x7FFFu) >= 0x7C00u ? 0 : lora_f2h(v[2 * c + 1] - lora_h2f(h1));
-              hi[c] = h0 | (static_cast<uint32_t>(h1) << 16);
-              lo[c] = g0 | (static_cast<uint32_t>(g1) << 16);
-            }
-            uint8_t* const rowp = sv + lr * 128 + (q & 1) * 8;
-            *reinterpret_cast<uint2*>(rowp + (((q >> 1) ^ (lr & 7)) << 4)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(rowp + (((4 + (q >> 1)) ^ (lr & 7)) << 4)) =
-                make_uint2(lo[0], lo[1]);
-          }
-          if (__any_sync(0xffffffffu, foreign != 0u)) {
-            // once the block has landed, zero the other adapters' rows of it
-            if (lane == 0) ok = wait_parity(full_bar(stage), phase, limit, st, 87);
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            __syncwarp();
-            if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (foreign >> i & 1u)
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                  *reinterpret_cast<uint4*>(sx + b * 8192 + (4 * i + r4) * 128 + 16 * q) =
-                      make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
           __syncwarp();
+          if (!ok) break;
+          if (mixed) {
+            uint8_t* const sx = base_ptr + stage * kStageBytes;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (i ? f1 : f0)
+                for (int b = 0; b < 5; ++b)   // four boxes of X or dC, then U or V
+#pragma unroll
+                  for (int c = 0; c < 8; ++c)
+                    *reinterpret_cast<uint4*>(sx + b * 8192 + (32 * i + lane) * 128 +
+                                              (((c + lane) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
           if (lane == 0) mbar_arrive(tok_bar(stage));
         }
         if (++stage == kStages) {
@@ -358,14 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float acc[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
-      for (int n = __popc(t.mask); n > 0; --n, ++local) {
+      for (int m = t.mask; m; m &= m - 1, ++local) {
         const uint32_t buf = local & 1u;
         if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 88)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float down = s_scale[local & (kScales - 1)];
+        const int blk = t.range * (kRange / 64) + __ffs(m) - 1;
+        const float down = __ldg((t.src ? p.unscale_v : p.unscale_u) + (p.row0 / 64 + blk) / 2);
         const uint32_t d0 =
             tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * 128 + half * 64;
         uint32_t hi[32], lo[32];
@@ -501,8 +449,16 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
   }
   const int ranges = ranges_of(o);
   Args a{};
-  a.u = o.U;
-  a.v = o.V;
+  CUtensorMap tmU{}, tmV{};
+  const int chunks = (o.R + 31) / 32;
+  if (o.dA) {
+    if (int rc = encode_map_f16(&tmU, o.U->scaled, o.M, 64 * chunks, 64ll * chunks, 64, 64)) return rc;
+    a.unscale_u = o.U->unscale;
+  }
+  if (o.dB) {
+    if (int rc = encode_map_f16(&tmV, o.V->scaled, o.M, 64 * chunks, 64ll * chunks, 64, 64)) return rc;
+    a.unscale_v = o.V->unscale;
+  }
   a.cols_x = o.K;
   a.cols_g = o.N;
   a.tiles_x = o.dA ? (o.K + 255) / 256 : 0;
@@ -511,8 +467,7 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
   a.M = o.M;
   a.R = o.R;
   a.adapters = o.adapters;
-  a.ldv = o.ldv;
-  a.chunks = (o.R + 31) / 32;
+  a.chunks = chunks;
   a.table = static_cast<int*>(scratch);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
                                     lora_round256(4 * static_cast<size_t>(ranges) * o.adapters));
@@ -546,7 +501,7 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = r0 == 0 ? 1 : 0;   // a later slab waits for the sums of the one before
-    if (counted_launch(cudaLaunchKernelEx(&cfg, lora_outer_kernel, tmX, tmG, a)) != cudaSuccess)
+    if (counted_launch(cudaLaunchKernelEx(&cfg, lora_outer_kernel, tmX, tmG, tmU, tmV, a)) != cudaSuccess)
       return GEMM_ERR_CUDA;
     s.ranges = a.ranges;
     s.beta = r0 == 0 ? o.beta : 1.0f;

@@ -9,7 +9,12 @@
 // the columns of its own adapter.  What binds is reading x once: 2 R
 // multiply-adds per half, where the tensor cores take ~280.  Slices make about
 // one CTA per SM; their partial sums are added by the last slice of a tile to
-// arrive, in slice order.
+// arrive, in slice order, which also writes V as the tensor cores take it: two
+// halves per entry, hi + lo (22 significant bits), 32 ranks' hi and then their
+// lo as 64 columns, so that the kernels after this one load it by TMA.  For the
+// adapters' gradients it is first scaled, 128 rows at a time, by the power of
+// two that brings its largest finite magnitude into [2^13, 2^14): gradients of
+// any size keep their bits.
 //
 // The tensor cores truncate when they add to an fp32 accumulator, by up to
 // 2^-23 of it per 16 products of K, always toward zero.  The gradients of the
@@ -43,6 +48,7 @@ struct Args {
   int first_list, first_item[2];   // blocks: checks, lists, items of either job
   int slices[2], kb[2];
   float* part[2];         // [slice][M][ldv]
+  int chunks;             // of 32 ranks
   unsigned int* counters;
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
@@ -109,6 +115,22 @@ struct Cfg {
   static_assert(kRing / (kXBytes + kGroup * kNBytes) >= 2, "two stages");
 };
 
+// Four entries as hi halves at o and lo halves 32 further; past the half range
+// hi is infinite and stands alone.
+__device__ __forceinline__ void store_split(uint16_t* o, float4 v) {
+  const __half2 h0 = __floats2half2_rn(v.x, v.y), h1 = __floats2half2_rn(v.z, v.w);
+  const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+  const __half2 l0 = __floats2half2_rn(isinf(f0.x) ? 0.0f : v.x - f0.x, isinf(f0.y) ? 0.0f : v.y - f0.y);
+  const __half2 l1 = __floats2half2_rn(isinf(f1.x) ? 0.0f : v.z - f1.x, isinf(f1.y) ? 0.0f : v.w - f1.y);
+  uint32_t b[4];
+  memcpy(b, &h0, 4);
+  memcpy(b + 1, &h1, 4);
+  memcpy(b + 2, &l0, 4);
+  memcpy(b + 3, &l1, 4);
+  *reinterpret_cast<uint2*>(o) = make_uint2(b[0], b[1]);
+  *reinterpret_cast<uint2*>(o + 32) = make_uint2(b[2], b[3]);
+}
+
 template <int RP>
 __global__ void __launch_bounds__(kThreads, 2)
     lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX0,
@@ -117,6 +139,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                           const __grid_constant__ CUtensorMap tmF1, const Args p) {
   using G = Cfg<RP>;
   __shared__ int s_first[256], s_list[256], s_slot[256], s_cnt[10];
+  __shared__ float s_top[4];
+  __shared__ int s_last;
   griddep_launch_dependents();
   const int b = blockIdx.x;
   if (b < p.first_list) {
@@ -352,38 +376,59 @@ __global__ void __launch_bounds__(kThreads, 2)
                                    s * acc[j * RP + r + 2], s * acc[j * RP + r + 3]));
       }
     }
-    if (slices > 1) {
-      // the last slice of these 32 rows to arrive adds them up in slice order
-      unsigned int* const cnt = p.counters + ((which ? p.job[0].tiles : 0) + tile) * 4 + quad;
-      __syncwarp();
-      unsigned int before = 0;
-      if (lane == 0) {
-        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                     : "=r"(before)
-                     : "l"(cnt)
-                     : "memory");
-        if (before == static_cast<unsigned int>(slices - 1)) *cnt = 0u;   // for the next call
-      }
-      before = __shfl_sync(0xffffffffu, before, 0);
-      __syncwarp();
-      if (before == static_cast<unsigned int>(slices - 1)) {
-        // eight lanes a row: 16-byte pieces of consecutive rows
-        const int per = p.ldv / 4, total = max(0, min(32, rows - 32 * quad)) * per;
-        const float* src = p.part[which] + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
-        float* const dst = job.V + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
-        for (int i = lane; i < total; i += 32) {
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // the last slice of the tile to arrive finishes it (the four warps meet at
+    // barrier 1; they all get here, whatever waits gave up)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp == 2 && lane == 0) {
+      unsigned int* const cnt = p.counters + (which ? p.job[0].tiles : 0) + tile;
+      unsigned int before;
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(cnt) : "memory");
+      s_last = before == static_cast<unsigned int>(slices - 1);
+      if (s_last) *cnt = 0u;   // for the next call
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (s_last) {
+      const int nrow = max(0, min(32, rows - 32 * quad));
+      const int per = p.ldv / 4;
+      const float* src = p.part[which] + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
+      float* const dst = job.V + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
+      float top = 0.0f;
+      for (int i = lane; i < nrow * per; i += 32) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-          for (int k = 0; k < slices; ++k) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(
-                                        src + static_cast<long long>(k) * p.M * p.ldv) + i);
-            v.x += t.x;
-            v.y += t.y;
-            v.z += t.z;
-            v.w += t.w;
-          }
-          reinterpret_cast<float4*>(dst)[i] = v;
+        for (int k = 0; k < slices; ++k) {
+          const float4 t = __ldcg(reinterpret_cast<const float4*>(
+                                      src + static_cast<long long>(k) * p.M * p.ldv) + i);
+          v.x += t.x;
+          v.y += t.y;
+          v.z += t.z;
+          v.w += t.w;
         }
+        reinterpret_cast<float4*>(dst)[i] = v;
+        const float m[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (m[j] < __int_as_float(0x7F800000)) top = fmaxf(top, m[j]);
+      }
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      if (lane == 0) s_top[quad] = top;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+      // |e| <= 100, so that 2^e and 2^-e are normal
+      const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
+      const float up = __int_as_float((127 + e) << 23);
+      if (job.scaled && warp == 2 && lane == 0) job.unscale[tile] = __int_as_float((127 - e) << 23);
+      // eight lanes a row and chunk, four ranks each
+      const int q = lane & 7;
+      for (int i = lane >> 3; i < nrow * p.chunks; i += 4) {
+        const int r = i / p.chunks, c = i - r * p.chunks, rank = 32 * c + 4 * q;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (rank < p.ldv) v = *reinterpret_cast<const float4*>(dst + r * p.ldv + rank);
+        const long long o =
+            ((static_cast<long long>(row0) + 32 * quad + r) * p.chunks + c) * 64 + 4 * q;
+        if (job.packed) store_split(job.packed + o, v);
+        if (job.scaled)
+          store_split(job.scaled + o, make_float4(up * v.x, up * v.y, up * v.z, up * v.w));
       }
     }
   }
@@ -422,6 +467,10 @@ size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms) {
   for (int j = 0; j < p.njobs; ++j) {
     const int s = slices_of((p.M + 127) / 128, (p.job[j].C + 63) / 64, sms);
     n += (s > 1 ? s + 1 : 1) * lora_round256(4 * static_cast<size_t>(p.M) * p.ldv);
+    const size_t packed = lora_round256(2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M);
+    if (p.job[j].want & kLoraPacked) n += packed;
+    if (p.job[j].want & kLoraScaled)
+      n += packed + lora_round256(4 * static_cast<size_t>((p.M + 127) / 128));
   }
   return n;
 }
@@ -444,6 +493,7 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const 
   a.R = p.R;
   a.adapters = p.adapters;
   a.ldv = p.ldv;
+  a.chunks = (p.R + 31) / 32;
   p.lists = reinterpret_cast<int*>(take(4 * static_cast<size_t>(blocks) * kLoraListStride));
   p.bad = reinterpret_cast<int*>(take(4 * kLoraBadParts * static_cast<size_t>(p.adapters)));
   a.lists = p.lists;
@@ -468,6 +518,12 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const 
     job.V = reinterpret_cast<float*>(take(v));
     a.part[j] = a.slices[j] > 1 ? reinterpret_cast<float*>(take(a.slices[j] * lora_round256(v)))
                                 : job.V;
+    const size_t packed = 2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M;
+    if (job.want & kLoraPacked) job.packed = reinterpret_cast<uint16_t*>(take(packed));
+    if (job.want & kLoraScaled) {
+      job.scaled = reinterpret_cast<uint16_t*>(take(packed));
+      job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(tiles)));
+    }
     a.first_item[j] = grid;
     grid += tiles * a.slices[j];
     if (int rc = encode_map_f16(&maps[2 * j], job.x, p.M, job.C, job.ldx, 64, 128)) return rc;
