@@ -612,6 +612,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   int epi = c_f32 ? kEpiF32 : ((c_tma && force != 2) ? kEpiTma : kEpiManual);
 
   TcArgs a{};
+  a.wait_operands = prepass;
   a.pdl = prepass || lora;   // the realignment copy (the adapters' shrink) was launched just before
   a.A = A;
   a.B = B;

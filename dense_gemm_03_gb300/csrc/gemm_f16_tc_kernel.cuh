@@ -619,7 +619,9 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   // everything above touched only this CTA's shared and tensor memory; from
   // here on global memory is read and written, once a pre-pass launched just
   // before this kernel has completed
-  griddep_wait();
+  // (with adapters only their own warps and the epilogue read or overwrite what
+  // the kernels before this one touch, unless the operands are copies)
+  if (!LORA::kOn || p.wait_operands || warp >= R::kEpiWarp0) griddep_wait();
   // a copy-back kernel launched after this one may be scheduled now (it waits
   // for this kernel's completion before reading anything this kernel writes)
   griddep_launch_dependents();

@@ -92,6 +92,8 @@ struct TcArgs {
   // streamed once -- loaded evict-first, so it does not push out of L2 lines
   // that are still useful (or dirty lines that would be written back)
   int stream_a, stream_b;
+  // adapters: A, B or C was copied by the kernel launched just before
+  int wait_operands;
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
   // host only: the launch directly follows this call's pre-pass kernel on the

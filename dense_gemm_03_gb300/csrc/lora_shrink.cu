@@ -8,7 +8,7 @@
 // rounded up to 16, 32, 64 or 128), 64 columns of TMEM at a time; a row keeps
 // the columns of its own adapter.  What binds is reading x once: 2 R
 // multiply-adds per half, where the tensor cores take ~280.  Slices make about
-// one CTA per SM; their partial sums are added by the last slice of a tile to
+// two CTAs per SM; their partial sums are added by the last slice of a tile to
 // arrive, in slice order, which also writes V as the tensor cores take it: two
 // halves per entry, hi + lo (22 significant bits), 32 ranks' hi and then their
 // lo as 64 columns, so that the kernels after this one load it by TMA.  For the
@@ -454,9 +454,13 @@ int launch(const CUtensorMap* maps, const Args& a, int grid, cudaStream_t stream
   return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-int slices_of(int tiles, int kb, int sms) {
-  // about one CTA per SM and job, at least four k-blocks each
-  return std::max(1, std::min({sms / tiles, kb / 4, 16}));
+// K slices of a job: the CTAs of all jobs, checks and lists about fill the two
+// places an SM has, at least four k-blocks a slice.
+int slices_of(const LoraShrinkPlan& p, int j, int sms) {
+  const int tiles = (p.M + 127) / 128, kb = (p.job[j].C + 63) / 64;
+  const long long extra = p.check ? 1ll * kLoraBadParts * p.adapters + (p.M + 255) / 256 : 0;
+  const long long room = std::max<long long>(2 * sms - extra, sms) / p.njobs;
+  return static_cast<int>(std::max(1ll, std::min<long long>({room / tiles, kb / 4, 16})));
 }
 
 }  // namespace
@@ -465,7 +469,7 @@ size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms) {
   size_t n = lora_round256(4 * static_cast<size_t>((p.M + 255) / 256) * kLoraListStride) +
              lora_round256(4 * kLoraBadParts * static_cast<size_t>(p.adapters));
   for (int j = 0; j < p.njobs; ++j) {
-    const int s = slices_of((p.M + 127) / 128, (p.job[j].C + 63) / 64, sms);
+    const int s = slices_of(p, j, sms);
     n += (s > 1 ? s + 1 : 1) * lora_round256(4 * static_cast<size_t>(p.M) * p.ldv);
     const size_t packed = lora_round256(2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M);
     if (p.job[j].want & kLoraPacked) n += packed;
@@ -513,7 +517,7 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const 
     LoraShrinkJob& job = p.job[j];
     job.tiles = tiles;
     a.kb[j] = (job.C + 63) / 64;
-    a.slices[j] = slices_of(tiles, a.kb[j], d.sms);
+    a.slices[j] = slices_of(p, j, d.sms);
     const size_t v = 4 * static_cast<size_t>(p.M) * p.ldv;
     job.V = reinterpret_cast<float*>(take(v));
     a.part[j] = a.slices[j] > 1 ? reinterpret_cast<float*>(take(a.slices[j] * lora_round256(v)))

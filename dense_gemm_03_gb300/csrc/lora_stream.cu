@@ -25,6 +25,8 @@
 // swizzle, MN-major: LBO 8 KB, SBO 1 KB; or, for a W stored transposed, two
 // boxes of 64 rows, K-major, SBO 1 KB), then the rows of X, 64 halves of k each
 // (K-major, SBO 1 KB).
+#include <type_traits>
+
 #include "lora.h"
 
 namespace gb300 {
@@ -285,22 +287,28 @@ struct CombineArgs {
   bool vec_c;              // rows of C on the 8-byte grid
 };
 
-// One block per (row, 512 columns), four columns a thread.
-template <bool TRANS>
+// One block per (RB rows, 512 columns), four columns a thread.  Rows of one
+// adapter share the loads of F[a] (the rows of a prompt do; at RB = 1, 1500 x
+// 1000 outputs of rank 24 read 72 MB of it from L2 and took 26 us).
+template <bool TRANS, int RB>
 __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const CombineArgs p) {
-  __shared__ float vs[kLoraMaxRank];
-  const int strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
-  const int i = blockIdx.x / strips;
-  const int c = (blockIdx.x - i * strips) * 4 * kCombThreads + 4 * static_cast<int>(threadIdx.x);
+  __shared__ float vs[RB][kLoraMaxRank];
   griddep_launch_dependents();
-  const int a = p.ids[i];
-  const bool has = a >= 0 && a < p.adapters;
+  const int strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
+  const int i0 = blockIdx.x / strips * RB;
+  const int c = blockIdx.x % strips * 4 * kCombThreads + 4 * static_cast<int>(threadIdx.x);
   const bool whole = c + 4 <= p.N;
-  const uint16_t* const f = p.F + (has ? static_cast<long long>(a) * p.f_stride : 0) +
-                            (TRANS ? static_cast<long long>(c) * p.ldf : c);
+  int id[RB];
+#pragma unroll
+  for (int j = 0; j < RB; ++j) {
+    id[j] = i0 + j < p.M ? __ldg(p.ids + i0 + j) : -1;
+    if (id[j] >= p.adapters) id[j] = -1;
+  }
+  const long long f0 = TRANS ? static_cast<long long>(c) * p.ldf : c;
   // nothing of the kernels before this one is read yet: bring this block's
-  // part of F[a] into L2
-  if (has && c < p.N) {
+  // part of the first row's F[a] into L2
+  if (id[0] >= 0 && c < p.N) {
+    const uint16_t* const f = p.F + id[0] * p.f_stride + f0;
     if (TRANS) {
       for (int j = 0; j < 4 && c + j < p.N; ++j) prefetch_l2(f + j * p.ldf);
     } else if ((threadIdx.x & 15) == 0) {
@@ -308,94 +316,120 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
     }
   }
   griddep_wait();
-  if (has)
-    for (int r = threadIdx.x; r < p.R; r += kCombThreads) {
-      const float* v = p.V + static_cast<long long>(i) * p.slices * p.ldv + r;
-      float t[kMaxSlices], s = 0.0f;
-#pragma unroll
-      for (int k = 0; k < kMaxSlices; ++k) t[k] = k < p.slices ? __ldcg(v + k * p.ldv) : 0.0f;
-#pragma unroll
-      for (int k = 0; k < kMaxSlices; ++k) s += t[k];
-      vs[r] = s;
+  for (int e = threadIdx.x; e < RB * p.R; e += kCombThreads) {
+    const int j = e / p.R, r = e - j * p.R;
+    float s = 0.0f;
+    if (i0 + j < p.M) {
+      const float* v = p.V + static_cast<long long>(i0 + j) * p.slices * p.ldv + r;
+#pragma unroll 8
+      for (int k = 0; k < p.slices; ++k) s += __ldcg(v + k * p.ldv);
     }
+    vs[j][r] = s;
+  }
   __syncthreads();
   if (c >= p.N) return;
-  const int blk = i / kBlockRows;
   const long long chunk_elems = static_cast<long long>(p.block_rows) * 128;
-  const float* part = p.part + (static_cast<long long>(blk) * p.units + (c >> 7)) * p.chunks * chunk_elems +
-                      (i - blk * kBlockRows) * 128 + (c & 127);
-  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int k0 = 0; k0 < p.chunks; k0 += 8) {
-    float4 t[8];
+  const int blk = i0 / kBlockRows;   // RB divides kBlockRows
+  const float* const part =
+      p.part + (static_cast<long long>(blk) * p.units + (c >> 7)) * p.chunks * chunk_elems +
+      (i0 - blk * kBlockRows) * 128 + (c & 127);
+  float o[RB][4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      t[k] = k0 + k < p.chunks
-                 ? __ldcg(reinterpret_cast<const float4*>(part + (k0 + k) * chunk_elems))
-                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j = 0; j < RB; ++j)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      s.x += t[k].x;
-      s.y += t[k].y;
-      s.z += t[k].z;
-      s.w += t[k].w;
-    }
-  }
-  float o[4] = {s.x, s.y, s.z, s.w};
-  if (has) {
-    float l[4] = {};
+    for (int u = 0; u < 4; ++u) o[j][u] = 0.0f;
+#pragma unroll 2
+  for (int k = 0; k < p.chunks; ++k)
+#pragma unroll
+    for (int j = 0; j < RB; ++j)
+      if (i0 + j < p.M) {
+        const float4 t = __ldcg(reinterpret_cast<const float4*>(part + k * chunk_elems + j * 128));
+        o[j][0] += t.x;
+        o[j][1] += t.y;
+        o[j][2] += t.z;
+        o[j][3] += t.w;
+      }
+  unsigned int todo = 0;
+#pragma unroll
+  for (int j = 0; j < RB; ++j) todo |= static_cast<unsigned int>(id[j] >= 0) << j;
+  while (todo) {
+    int a = -1;
+    unsigned int mine = 0;   // the rows of the first open row's adapter
+#pragma unroll
+    for (int j = 0; j < RB; ++j)
+      if (todo >> j & 1u) {
+        if (a < 0) a = id[j];
+        if (id[j] == a) mine |= 1u << j;
+      }
+    todo &= ~mine;
+    const uint16_t* const f = p.F + a * p.f_stride + f0;
+    auto add = [&](int r, const float (&w)[4]) {
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+        if (RB == 1 || (mine >> j & 1u))
+#pragma unroll
+          for (int u = 0; u < 4; ++u) o[j][u] = fmaf(vs[j][r], w[u], o[j][u]);
+    };
+    int r = 0;
     if (TRANS) {
-      const int r8 = p.R / 8 * 8;
-      for (int r = 0; r < r8; r += 8) {
+      for (; r + 8 <= p.R; r += 8) {
         uint4 w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = __ldg(reinterpret_cast<const uint4*>(f + (c + j < p.N ? j * p.ldf : 0) + r));
+        for (int u = 0; u < 4; ++u)
+          w[u] = __ldg(reinterpret_cast<const uint4*>(f + (c + u < p.N ? u * p.ldf : 0) + r));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t h[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        for (int h = 0; h < 4; ++h) {
+          float2 b[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float2 b = lora_h2f2(h[u]);
-            l[j] = fmaf(vs[r + 2 * u], b.x, l[j]);
-            l[j] = fmaf(vs[r + 2 * u + 1], b.y, l[j]);
-          }
+          for (int u = 0; u < 4; ++u)
+            b[u] = lora_h2f2(h == 0 ? w[u].x : (h == 1 ? w[u].y : (h == 2 ? w[u].z : w[u].w)));
+          const float lo[4] = {b[0].x, b[1].x, b[2].x, b[3].x};
+          const float hi[4] = {b[0].y, b[1].y, b[2].y, b[3].y};
+          add(r + 2 * h, lo);
+          add(r + 2 * h + 1, hi);
         }
       }
-      for (int r = r8; r < p.R; ++r)
-        for (int j = 0; j < 4 && c + j < p.N; ++j) l[j] = fmaf(vs[r], lora_h2f(f[j * p.ldf + r]), l[j]);
     } else if (whole) {
 #pragma unroll 8
-      for (int r = 0; r < p.R; ++r) {
+      for (; r < p.R; ++r) {
         const uint2 b = __ldg(reinterpret_cast<const uint2*>(f + r * p.ldf));
         const float2 b0 = lora_h2f2(b.x), b1 = lora_h2f2(b.y);
-        l[0] = fmaf(vs[r], b0.x, l[0]);
-        l[1] = fmaf(vs[r], b0.y, l[1]);
-        l[2] = fmaf(vs[r], b1.x, l[2]);
-        l[3] = fmaf(vs[r], b1.y, l[3]);
+        const float w[4] = {b0.x, b0.y, b1.x, b1.y};
+        add(r, w);
       }
-    } else {
-      for (int r = 0; r < p.R; ++r)
-        for (int j = 0; j < p.N - c; ++j) l[j] = fmaf(vs[r], lora_h2f(f[r * p.ldf + j]), l[j]);
     }
-    for (int j = 0; j < 4; ++j) o[j] += l[j];
-  }
-  uint16_t* const dst = p.C + static_cast<long long>(i) * p.ldc + c;
-  if (whole && p.vec_c) {
-    float old[4] = {};
-    if (p.beta != 0.0f) {
-      const uint2 b = *reinterpret_cast<const uint2*>(dst);
-      const float2 b0 = lora_h2f2(b.x), b1 = lora_h2f2(b.y);
-      old[0] = b0.x; old[1] = b0.y; old[2] = b1.x; old[3] = b1.y;
-    }
-    uint32_t h[4];
+    for (; r < p.R; ++r) {   // ranks past a multiple of eight, the ragged last columns
+      float w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      h[j] = lora_f2h(p.beta != 0.0f ? fmaf(p.alpha, o[j], p.beta * old[j]) : p.alpha * o[j]);
-    *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  } else {
-    for (int j = 0; j < 4 && c + j < p.N; ++j)
-      dst[j] = lora_f2h(p.beta != 0.0f ? fmaf(p.alpha, o[j], p.beta * lora_h2f(dst[j]))
-                                       : p.alpha * o[j]);
+      for (int u = 0; u < 4; ++u)
+        w[u] = c + u < p.N ? lora_h2f(TRANS ? f[u * p.ldf + r] : f[r * p.ldf + u]) : 0.0f;
+      add(r, w);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RB; ++j) {
+    if (i0 + j >= p.M) break;
+    uint16_t* const dst = p.C + static_cast<long long>(i0 + j) * p.ldc + c;
+    if (whole && p.vec_c) {
+      float2 old0 = make_float2(0.0f, 0.0f), old1 = old0;
+      if (p.beta != 0.0f) {
+        const uint2 b = *reinterpret_cast<const uint2*>(dst);
+        old0 = lora_h2f2(b.x);
+        old1 = lora_h2f2(b.y);
+      }
+      const float old[4] = {old0.x, old0.y, old1.x, old1.y};
+      uint32_t h[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        h[u] = lora_f2h(p.beta != 0.0f ? fmaf(p.alpha, o[j][u], p.beta * old[u]) : p.alpha * o[j][u]);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c + u < p.N)
+          dst[u] = lora_f2h(p.beta != 0.0f ? fmaf(p.alpha, o[j][u], p.beta * lora_h2f(dst[u]))
+                                           : p.alpha * o[j][u]);
+    }
   }
 }
 
@@ -534,12 +568,21 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   c.alpha = p.alpha;
   c.beta = p.beta;
   c.vec_c = (reinterpret_cast<uintptr_t>(p.C) & 7u) == 0 && p.ldc % 4 == 0;
-  const long long blocks = 1ll * p.M * ((p.N + 4 * kCombThreads - 1) / (4 * kCombThreads));
+  // as many rows a block as leave about two blocks per SM
+  const long long strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
+  const int rb = p.M * strips >= 16ll * d.sms ? 8 : (p.M * strips >= 8ll * d.sms ? 4 : 1);
+  const long long blocks = (p.M + rb - 1) / rb * strips;
+  if (blocks > 0x7fffffff) return GEMM_ERR_ARG;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(kCombThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  const cudaError_t e = p.trans ? cudaLaunchKernelEx(&cfg, lora_combine_kernel<true>, c)
-                                : cudaLaunchKernelEx(&cfg, lora_combine_kernel<false>, c);
+  auto launch = [&](auto trans) {
+    constexpr bool T = decltype(trans)::value;
+    return rb == 8   ? cudaLaunchKernelEx(&cfg, lora_combine_kernel<T, 8>, c)
+           : rb == 4 ? cudaLaunchKernelEx(&cfg, lora_combine_kernel<T, 4>, c)
+                     : cudaLaunchKernelEx(&cfg, lora_combine_kernel<T, 1>, c);
+  };
+  const cudaError_t e = p.trans ? launch(std::true_type{}) : launch(std::false_type{});
   return counted_launch(e) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
