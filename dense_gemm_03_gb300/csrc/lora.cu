@@ -116,8 +116,6 @@ LoraShrinkPlan shrink_plan(const LoraArgs& p) {
   return s;
 }
 
-size_t counter_bytes(int M) { return 4 * 2 * static_cast<size_t>((M + 127) / 128); }
-
 int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const LoraDevice& d,
             cudaStream_t stream) {
   const bool chunks = lora_stream_suits(p.M, p.N, d.sms);
@@ -131,7 +129,8 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
   LoraStream t{};
   auto describe = [&]() {   // of the operands as they are by now
     s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, chunks ? 0 : kLoraPacked};
-    s.njobs = 1;
+    s.njobs = s.all_jobs = 1;
+    s.min_c = p.K;
     if (!chunks) {
       s.check = p.B;
       s.ld_check = p.ldb;
@@ -144,10 +143,10 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
                    beta};
   };
   describe();
-  void *buf = nullptr, *zero = nullptr;
-  const size_t shrink = few ? 0 : lora_shrink_bytes(s, d.sms);
+  void* buf = nullptr;
+  const size_t shrink = few ? 0 : lora_shrink_bytes(s);
   const size_t need = copies + shrink + (chunks ? lora_stream_bytes(t, d.sms) : 0);
-  if (int rc = routed_scratch(stream, need, &buf, counter_bytes(p.M), &zero)) return rc;
+  if (int rc = routed_scratch(stream, need, &buf)) return rc;
   uint8_t* const rest = static_cast<uint8_t*>(buf) + copies;
   if (int rc = align_operands({{x, &p.X, &p.ldx}, {w, &p.W, &p.ldw}, {a, &p.A, &p.lda},
                                {b, &p.B, &p.ldb}},
@@ -155,7 +154,7 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
     return rc;
   describe();
   if (!few)
-    if (int rc = lora_shrink(s, rest, static_cast<unsigned int*>(zero), d, stream)) return rc;
+    if (int rc = lora_shrink(s, rest, d, stream)) return rc;
   if (chunks) {
     t.V = few ? nullptr : s.job[0].V;
     if (int rc = lora_stream(t, rest + shrink, d, stream)) return rc;
@@ -186,6 +185,8 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   LoraStream t{};
   auto describe = [&]() {
     s.njobs = 0;
+    s.all_jobs = 2;
+    s.min_c = std::min(p.N, p.K);
     if (use_u)
       s.job[s.njobs++] = LoraShrinkJob{G, ldg, p.N, p.B, p.ldb, p.b_stride(), 1,
                                        (dX && !chunks ? kLoraPacked : 0) | (dA ? kLoraScaled : 0)};
@@ -208,12 +209,12 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   LoraOuter o{p.X, G, p.ldx, ldg, nullptr, nullptr, p.ids, dA, dB, p.M, p.N, p.K, p.R,
               p.adapters, alpha, beta};
   const bool outer = dA || dB;
-  const size_t shrink_bytes = lora_shrink_bytes(s, d.sms);
+  const size_t shrink_bytes = lora_shrink_bytes(s);
   const size_t stream_bytes = chunks ? lora_round256(lora_stream_bytes(t, d.sms)) : 0;
-  void *buf = nullptr, *zero = nullptr;
+  void* buf = nullptr;
   if (int rc = routed_scratch(stream, copies + shrink_bytes + stream_bytes +
                                           (outer ? lora_outer_bytes(o) : 0),
-                              &buf, counter_bytes(p.M), &zero))
+                              &buf))
     return rc;
   uint8_t* const rest = static_cast<uint8_t*>(buf) + copies;
   if (int rc = align_operands({{g, &G, &ldg}, {x, &p.X, &p.ldx}, {a, &p.A, &p.lda},
@@ -221,7 +222,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
                               static_cast<uint8_t*>(buf), d.sms, stream))
     return rc;
   describe();
-  if (int rc = lora_shrink(s, rest, static_cast<unsigned int*>(zero), d, stream)) return rc;
+  if (int rc = lora_shrink(s, rest, d, stream)) return rc;
   if (chunks) {
     t.V = s.job[0].V;
     if (int rc = lora_stream(t, rest + shrink_bytes, d, stream)) return rc;

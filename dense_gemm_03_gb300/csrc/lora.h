@@ -78,6 +78,7 @@ constexpr int kLoraPacked = 1, kLoraScaled = 2;
 struct LoraShrinkPlan {
   LoraShrinkJob job[2];
   int njobs;
+  int all_jobs, min_c;    // jobs the operator can have, the least C among them
   const int* ids;
   const float* scales;
   int M, R, adapters;
@@ -88,10 +89,8 @@ struct LoraShrinkPlan {
   int check_rows, check_cols;
   int *lists, *bad;       // out: LoraTailArgs::lists and bad
 };
-size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms);
-// `counters`: 2 words per 128 rows, zero before and after.
-int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const LoraDevice& d,
-                cudaStream_t stream);
+size_t lora_shrink_bytes(const LoraShrinkPlan& p);
+int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStream_t stream);
 
 // The adapters' gradients (lora_outer.cu): dA from X and U, dB from V and G;
 // either may be NULL.

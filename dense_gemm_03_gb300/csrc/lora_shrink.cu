@@ -5,16 +5,17 @@
 //
 // One CTA per (128 rows, K slice): the rows of x are the M operand, the
 // adapters that occur among them the N operand, RP columns each (the rank
-// rounded up to 16, 32, 64 or 128), 64 columns of TMEM at a time; a row keeps
-// the columns of its own adapter.  What binds is reading x once: 2 R
-// multiply-adds per half, where the tensor cores take ~280.  Slices make about
-// two CTAs per SM; their partial sums are added by the last slice of a tile to
-// arrive, in slice order, which also writes V as the tensor cores take it: two
-// halves per entry, hi + lo (22 significant bits), 32 ranks' hi and then their
-// lo as 64 columns, so that the kernels after this one load it by TMA.  For the
-// adapters' gradients it is first scaled, 128 rows at a time, by the power of
-// two that brings its largest finite magnitude into [2^13, 2^14): gradients of
-// any size keep their bits.
+// rounded up to 16, 32, 64 or 128), a few of them at a time; a row keeps the
+// columns of its own adapter.  What binds is reading x once: 2 R
+// multiply-adds per half, where the tensor cores take ~280.  The K slices of a
+// tile are a cluster: each leaves its partial sums in its own shared memory and
+// adds up its share of the rows from all of them, in slice order (through global
+// memory and a counter, the last slice alone took 8 us to add up eight).  The
+// same step writes V as the tensor cores take it: two halves per entry, hi + lo
+// (22 significant bits), 32 ranks' hi and then their lo as 64 columns, so that
+// the kernels after this one load it by TMA.  For the adapters' gradients it is
+// first scaled, 128 rows at a time, by the power of two that brings its largest
+// finite magnitude into [2^13, 2^14): gradients of any size keep their bits.
 //
 // The tensor cores truncate when they add to an fp32 accumulator, by up to
 // 2^-23 of it per 16 products of K, always toward zero.  The gradients of the
@@ -30,7 +31,7 @@ namespace {
 
 constexpr int kThreads = 192;                // TMA, MMA, 4 epilogue warps
 constexpr int kMaxStages = 6;
-constexpr int kRing = 98304;                 // operand ring: two CTAs fit on an SM
+constexpr int kMaxSlices = 8;                // a portable cluster
 constexpr int kXBytes = 128 * 128;           // 128 rows of a k-block
 constexpr int kFoldKb = 2;                   // k-blocks accumulated in TMEM
 
@@ -45,11 +46,9 @@ struct Args {
   const uint16_t* check;  // weights to look for non-finite ones in, rows x cols each
   long long ld_check, check_stride;
   int check_rows, check_cols;
-  int first_list, first_item[2];   // blocks: checks, lists, items of either job
-  int slices[2], kb[2];
-  float* part[2];         // [slice][M][ldv]
+  int first_list, end_list, first_item[2];   // blocks: checks, lists, items of either job
+  int slices, kb[2];
   int chunks;             // of 32 ranks
-  unsigned int* counters;
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
 };
@@ -104,16 +103,34 @@ __device__ int distinct(const int* ids, int n, int adapters, int* list, int* slo
   return cnt[0];
 }
 
-// RP: columns of an adapter; COLS: columns of a pass (whole adapters).
+// RP: columns of an adapter.
 template <int RP>
 struct Cfg {
-  static constexpr int kCols = RP > 64 ? RP : 64;
+  static constexpr int kCols = RP > 32 ? RP : 32;      // columns of a pass: whole adapters
   static constexpr int kGroup = kCols / RP;            // adapters per pass
   static constexpr int kNBytes = RP > 64 ? 16384 : 8192;   // MN-major: 64-column boxes
-  static constexpr int kTmemCols = 2 * kCols;
-  static constexpr int kSmem = kRing + 1024 + 8 * (2 * kMaxStages + 5) + 16;
+  static constexpr int kTmemCols = 2 * kCols < 64 ? 64 : 2 * kCols;
+  // operand ring and the tile's partial sums: two CTAs fit on an SM up to rank 64
+  static constexpr int kRing = RP > 32 ? 65536 : 81920;
+  static constexpr int kSums = 128 * RP * 4;
+  static constexpr int kSmem = kRing + kSums + 1024 + 8 * (2 * kMaxStages + 5) + 16;
   static_assert(kRing / (kXBytes + kGroup * kNBytes) >= 2, "two stages");
+  static_assert(kRing >= kSums, "the ring holds the tile's sums");
 };
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster_f(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 // Four entries as hi halves at o and lo halves 32 further; past the half range
 // hi is infinite and stands alone.
@@ -139,15 +156,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                           const __grid_constant__ CUtensorMap tmF1, const Args p) {
   using G = Cfg<RP>;
   __shared__ int s_first[256], s_list[256], s_slot[256], s_cnt[10];
-  __shared__ float s_top[4];
-  __shared__ int s_last;
+  __shared__ float s_top[kThreads / 32 + 1];
   griddep_launch_dependents();
   const int b = blockIdx.x;
   if (b < p.first_list) {
     // ---- a quarter of an adapter: are its weights finite (if a row uses it)
     const int adapter = b / kLoraBadParts;
     bool used = false;
-#pragma unroll 8
+#pragma unroll 16
     for (int i = threadIdx.x; i < p.M; i += kThreads) used |= __ldg(p.ids + i) == adapter;
     int bad = 0;
     if (__syncthreads_or(used)) {
@@ -155,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int groups = (p.check_cols + 7) / 8;
       const long long total = static_cast<long long>(p.check_rows) * groups;
       const int part = b - adapter * kLoraBadParts;
-#pragma unroll 8
+#pragma unroll 16
       for (long long g = part * total / kLoraBadParts + threadIdx.x;
            g < (part + 1) * total / kLoraBadParts; g += kThreads) {
         const int r = static_cast<int>(g / groups), c = static_cast<int>(g % groups) * 8;
@@ -175,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x == 0) p.bad[b] = bad;
     return;
   }
-  if (b < p.first_item[0]) {
+  if (b < p.end_list) {
     // ---- the distinct adapters of a 256-row block
     const int blk = b - p.first_list, row0 = blk * 256;
     const int n = distinct(p.ids + row0, min(256, p.M - row0), p.adapters, s_list, s_slot, s_first,
@@ -185,12 +201,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x == 0) out[0] = n;
     return;
   }
+  if (b < p.first_item[0]) return;   // fills up the lists' last cluster
   // ---- a product: rows [row0, row0 + 128), one K slice
   const int which = p.njobs > 1 && b >= p.first_item[1] ? 1 : 0;
   const LoraShrinkJob& job = p.job[which];
   const CUtensorMap* const tmX = which ? &tmX1 : &tmX0;
   const CUtensorMap* const tmF = which ? &tmF1 : &tmF0;
-  const int item = b - p.first_item[which], slices = p.slices[which];
+  const int item = b - p.first_item[which], slices = p.slices;
   const int tile = item / slices, slice = item - tile * slices;
   const int row0 = tile * 128, rows = min(128, p.M - row0);
   const int kb0 = slice * p.kb[which] / slices, kb1 = (slice + 1) * p.kb[which] / slices;
@@ -199,13 +216,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t bars = base + kRing;
+  const uint32_t bars = base + G::kRing + G::kSums;
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (kMaxStages + s); };
   auto accf_bar = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + i); };
   auto acce_bar = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + 2 + i); };
   const uint32_t done_bar = bars + 8u * (2 * kMaxStages + 4);
-  uint8_t* const tmem_ptr = base_ptr + kRing + 8 * (2 * kMaxStages + 5);
+  float* const sums = reinterpret_cast<float*>(base_ptr + G::kRing);   // [128][ldv]
+  uint8_t* const tmem_ptr = base_ptr + G::kRing + G::kSums + 8 * (2 * kMaxStages + 5);
   const int warp = warp_id_uniform(), lane = static_cast<int>(lane_id());
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -232,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int passes = (n + G::kGroup - 1) / G::kGroup;
   // a stage holds the rows and as many adapters as a pass can have here
   const uint32_t stage_bytes = kXBytes + min(max(n, 1), G::kGroup) * G::kNBytes;
-  const int S = min(kMaxStages, static_cast<int>(kRing / stage_bytes));
+  const int S = min(kMaxStages, static_cast<int>(G::kRing / stage_bytes));
   const unsigned long long limit = p.wait_limit_ns;
   DeviceStatus* const st = p.status;
   const int fboxes = job.k_major ? 1 : (p.R + 63) / 64;
@@ -326,11 +344,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int quad = warp & 3, lr = 32 * quad + lane;   // this thread's row of the tile
     const bool in = lr < rows;
     const int slot = in ? s_slot[lr] : -1;
-    const int row = row0 + lr;
-    float* const out = p.part[which] + (static_cast<long long>(slice) * p.M + row) * p.ldv;
-    if (in && slot < 0)
+    float* const out = sums + lr * p.ldv;
+    if (slot < 0)
       for (int r = 0; r < p.ldv; r += 4)
-        __stcg(reinterpret_cast<float4*>(out + r), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        *reinterpret_cast<float4*>(out + r) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     uint32_t local = 0;
     bool ok = true;
     for (int ps = 0; ps < passes && ok; ++ps) {
@@ -371,70 +388,80 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int r = 0; r < RP; r += 4)
               if (r < p.ldv)
-                __stcg(reinterpret_cast<float4*>(out + r),
-                       make_float4(s * acc[j * RP + r], s * acc[j * RP + r + 1],
-                                   s * acc[j * RP + r + 2], s * acc[j * RP + r + 3]));
-      }
-    }
-    // the last slice of the tile to arrive finishes it (the four warps meet at
-    // barrier 1; they all get here, whatever waits gave up)
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (warp == 2 && lane == 0) {
-      unsigned int* const cnt = p.counters + (which ? p.job[0].tiles : 0) + tile;
-      unsigned int before;
-      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(cnt) : "memory");
-      s_last = before == static_cast<unsigned int>(slices - 1);
-      if (s_last) *cnt = 0u;   // for the next call
-    }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (s_last) {
-      const int nrow = max(0, min(32, rows - 32 * quad));
-      const int per = p.ldv / 4;
-      const float* src = p.part[which] + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
-      float* const dst = job.V + (static_cast<long long>(row0) + 32 * quad) * p.ldv;
-      float top = 0.0f;
-      for (int i = lane; i < nrow * per; i += 32) {
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int k = 0; k < slices; ++k) {
-          const float4 t = __ldcg(reinterpret_cast<const float4*>(
-                                      src + static_cast<long long>(k) * p.M * p.ldv) + i);
-          v.x += t.x;
-          v.y += t.y;
-          v.z += t.z;
-          v.w += t.w;
-        }
-        reinterpret_cast<float4*>(dst)[i] = v;
-        const float m[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (m[j] < __int_as_float(0x7F800000)) top = fmaxf(top, m[j]);
-      }
-      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      if (lane == 0) s_top[quad] = top;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-      // |e| <= 100, so that 2^e and 2^-e are normal
-      const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
-      const float up = __int_as_float((127 + e) << 23);
-      if (job.scaled && warp == 2 && lane == 0) job.unscale[tile] = __int_as_float((127 - e) << 23);
-      // eight lanes a row and chunk, four ranks each
-      const int q = lane & 7;
-      for (int i = lane >> 3; i < nrow * p.chunks; i += 4) {
-        const int r = i / p.chunks, c = i - r * p.chunks, rank = 32 * c + 4 * q;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (rank < p.ldv) v = *reinterpret_cast<const float4*>(dst + r * p.ldv + rank);
-        const long long o =
-            ((static_cast<long long>(row0) + 32 * quad + r) * p.chunks + c) * 64 + 4 * q;
-        if (job.packed) store_split(job.packed + o, v);
-        if (job.scaled)
-          store_split(job.scaled + o, make_float4(up * v.x, up * v.y, up * v.z, up * v.w));
+                *reinterpret_cast<float4*>(out + r) =
+                    make_float4(s * acc[j * RP + r], s * acc[j * RP + r + 1],
+                                s * acc[j * RP + r + 2], s * acc[j * RP + r + 3]);
       }
     }
   }
+  __syncwarp();
+  cluster_sync();   // every slice's sums are in its shared memory; its ring is idle
+  // this CTA's share of the tile's rows: the slices added up in order
+  const int share = 128 / slices, r0 = slice * share;
+  const int per = p.ldv / 4, total = max(0, min(share, rows - r0)) * per;
+  float4* const mine = reinterpret_cast<float4*>(base_ptr);   // [share][ldv]
+  float4* const vout =
+      reinterpret_cast<float4*>(job.V + (static_cast<long long>(row0) + r0) * p.ldv);
+  const uint32_t sums_addr = base + G::kRing + r0 * p.ldv * 4;
+  float top = 0.0f;
+  for (int i = threadIdx.x; i < total; i += kThreads) {
+    float4 t[kMaxSlices];
+#pragma unroll
+    for (int k = 0; k < kMaxSlices; ++k)
+      if (k < slices) t[k] = ld_cluster_f4(map_to_cta(sums_addr + 16 * i, k));
+    float4 v = t[0];
+#pragma unroll
+    for (int k = 1; k < kMaxSlices; ++k)
+      if (k < slices) {
+        v.x += t[k].x;
+        v.y += t[k].y;
+        v.z += t[k].z;
+        v.w += t[k].w;
+      }
+    mine[i] = v;
+    vout[i] = v;
+    const float m[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (m[j] < __int_as_float(0x7F800000)) top = fmaxf(top, m[j]);
+  }
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+  if (lane == 0) s_top[warp] = top;
   __syncthreads();
+  float up = 1.0f;
+  if (job.scaled) {
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, s_top[w]);
+      s_top[kThreads / 32] = top;
+    }
+    __syncwarp();
+    cluster_sync();   // every slice's largest magnitude is known
+    for (int k = 0; k < slices; ++k)
+      top = fmaxf(k ? top : 0.0f, ld_cluster_f(map_to_cta(smem_addr(s_top + kThreads / 32), k)));
+    // |e| <= 100, so that 2^e and 2^-e are normal
+    const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
+    up = __int_as_float((127 + e) << 23);
+    if (slice == 0 && threadIdx.x == 0) job.unscale[tile] = __int_as_float((127 - e) << 23);
+  }
+  if (job.packed || job.scaled) {
+    // eight threads a row and chunk, four ranks each
+    const int q = threadIdx.x & 7, nrow = total / per;
+    for (int i = threadIdx.x >> 3; i < nrow * p.chunks; i += kThreads / 8) {
+      const int r = i / p.chunks, c = i - r * p.chunks, piece = 8 * c + q;
+      const float4 v =
+          piece < per ? mine[r * per + piece] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const long long o =
+          ((static_cast<long long>(row0) + r0 + r) * p.chunks + c) * 64 + 4 * q;
+      if (job.packed) store_split(job.packed + o, v);
+      if (job.scaled)
+        store_split(job.scaled + o, make_float4(up * v.x, up * v.y, up * v.z, up * v.w));
+    }
+  }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, G::kTmemCols);
+  // no CTA leaves while another may still read its shared memory
+  __syncwarp();
+  cluster_sync();
 }
 
 template <int RP>
@@ -449,28 +476,45 @@ int launch(const CUtensorMap* maps, const Args& a, int grid, cudaStream_t stream
       return GEMM_ERR_CUDA;
     configured[dev] = true;
   }
-  lora_shrink_tc_kernel<RP><<<grid, kThreads, Cfg<RP>::kSmem, stream>>>(maps[0], maps[1], maps[2],
-                                                                        maps[3], a);
-  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg<RP>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.slices);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_shrink_tc_kernel<RP>, maps[0], maps[1],
+                                           maps[2], maps[3], a);
+  return counted_launch(e) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-// K slices of a job: the CTAs of all jobs, checks and lists about fill the two
-// places an SM has, at least four k-blocks a slice.
-int slices_of(const LoraShrinkPlan& p, int j, int sms) {
-  const int tiles = (p.M + 127) / 128, kb = (p.job[j].C + 63) / 64;
-  const long long extra = p.check ? 1ll * kLoraBadParts * p.adapters + (p.M + 255) / 256 : 0;
-  const long long room = std::max<long long>(2 * sms - extra, sms) / p.njobs;
-  return static_cast<int>(std::max(1ll, std::min<long long>({room / tiles, kb / 4, 16})));
+// K slices of a tile: with them the CTAs of all jobs, checks and lists about
+// fill the two places an SM has, at least two k-blocks a slice.  Counted for all
+// the jobs that the operator can have, so that a gradient asked for alone has
+// the bits it has beside the others.
+int slices_of(const LoraShrinkPlan& p, int sms) {
+  const int tiles = (p.M + 127) / 128;
+  const long long extra = 1ll * kLoraBadParts * p.adapters + (p.M + 255) / 256;
+  const long long room = std::max<long long>((p.R > 64 ? 1 : 2) * sms - extra, sms);
+  int s = 1;
+  while (2 * s <= kMaxSlices && 2ll * s * tiles * p.all_jobs <= room &&
+         4 * s <= (p.min_c + 63) / 64)
+    s *= 2;
+  return s;
 }
 
 }  // namespace
 
-size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms) {
+size_t lora_shrink_bytes(const LoraShrinkPlan& p) {
   size_t n = lora_round256(4 * static_cast<size_t>((p.M + 255) / 256) * kLoraListStride) +
              lora_round256(4 * kLoraBadParts * static_cast<size_t>(p.adapters));
   for (int j = 0; j < p.njobs; ++j) {
-    const int s = slices_of(p, j, sms);
-    n += (s > 1 ? s + 1 : 1) * lora_round256(4 * static_cast<size_t>(p.M) * p.ldv);
+    n += lora_round256(4 * static_cast<size_t>(p.M) * p.ldv);
     const size_t packed = lora_round256(2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M);
     if (p.job[j].want & kLoraPacked) n += packed;
     if (p.job[j].want & kLoraScaled)
@@ -479,8 +523,7 @@ size_t lora_shrink_bytes(const LoraShrinkPlan& p, int sms) {
   return n;
 }
 
-int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const LoraDevice& d,
-                cudaStream_t stream) {
+int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStream_t stream) {
   uint8_t* buf = static_cast<uint8_t*>(scratch);
   auto take = [&](size_t bytes) {
     uint8_t* const q = buf;
@@ -507,21 +550,18 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const 
   a.check_stride = p.check_stride;
   a.check_rows = p.check_rows;
   a.check_cols = p.check_cols;
-  a.counters = counters;
   a.wait_limit_ns = d.wait_limit_ns;
   a.status = d.status;
   a.first_list = p.check ? kLoraBadParts * p.adapters : 0;
-  int grid = a.first_list + (p.check ? blocks : 0);
+  a.slices = slices_of(p, d.sms);
+  a.end_list = a.first_list + (p.check ? blocks : 0);
+  int grid = (a.end_list + a.slices - 1) / a.slices * a.slices;   // whole clusters
   CUtensorMap maps[4] = {};
   for (int j = 0; j < p.njobs; ++j) {
     LoraShrinkJob& job = p.job[j];
     job.tiles = tiles;
     a.kb[j] = (job.C + 63) / 64;
-    a.slices[j] = slices_of(p, j, d.sms);
-    const size_t v = 4 * static_cast<size_t>(p.M) * p.ldv;
-    job.V = reinterpret_cast<float*>(take(v));
-    a.part[j] = a.slices[j] > 1 ? reinterpret_cast<float*>(take(a.slices[j] * lora_round256(v)))
-                                : job.V;
+    job.V = reinterpret_cast<float*>(take(4 * static_cast<size_t>(p.M) * p.ldv));
     const size_t packed = 2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M;
     if (job.want & kLoraPacked) job.packed = reinterpret_cast<uint16_t*>(take(packed));
     if (job.want & kLoraScaled) {
@@ -529,7 +569,7 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, unsigned int* counters, const 
       job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(tiles)));
     }
     a.first_item[j] = grid;
-    grid += tiles * a.slices[j];
+    grid += tiles * a.slices;
     if (int rc = encode_map_f16(&maps[2 * j], job.x, p.M, job.C, job.ldx, 64, 128)) return rc;
     if (int rc = job.k_major ? encode_map_f16_stack(&maps[2 * j + 1], job.F, p.R, job.C, job.ldf,
                                                     p.adapters, job.f_stride, 64, rp)

@@ -287,8 +287,112 @@ struct CombineArgs {
   bool vec_c;              // rows of C on the 8-byte grid
 };
 
-// One block per (RB rows, 512 columns), four columns a thread.  Rows of one
-// adapter share the loads of F[a] (the rows of a prompt do; at RB = 1, 1500 x
+// Few rows: one block per (row, 128 VEC columns), VEC columns a thread (four
+// when that still fills the SMs; a thread then takes them with one load).  All
+// that it waits for are three rounds of loads -- the id, then the first ranks of
+// F[a] (which no kernel before it writes), then V's slices and the chunks
+// together -- and little code: with everything unrolled, 2048 columns of one row
+// took 13 us here instead of 6.
+constexpr int kAhead = 16;
+
+template <bool TRANS, int VEC>
+__global__ void __launch_bounds__(kCombThreads) lora_combine_row_kernel(const CombineArgs p) {
+  static_assert(VEC == 1 || (VEC == 4 && !TRANS), "four columns are one load along a row of F");
+  __shared__ float raw[kMaxSlices * kLoraMaxRank];
+  __shared__ float vs[kLoraMaxRank];
+  griddep_launch_dependents();
+  const int strips = (p.N + kCombThreads * VEC - 1) / (kCombThreads * VEC);
+  const int i = blockIdx.x / strips;
+  const int t = threadIdx.x, c = ((blockIdx.x - i * strips) * kCombThreads + t) * VEC;
+  const int a = __ldg(p.ids + i);
+  const bool has = a >= 0 && a < p.adapters, mine = has && c < p.N;
+  const uint16_t* const f =
+      p.F + (mine ? a * p.f_stride + (TRANS ? static_cast<long long>(c) * p.ldf : c) : 0);
+  const long long step = TRANS ? 1 : p.ldf;
+  const bool whole = c + VEC <= p.N;
+  auto load = [&](int r, uint16_t (&w)[VEC]) {
+    if (VEC == 4 && whole) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(f + r * step));
+      memcpy(w, &q, sizeof(w));
+    } else {
+#pragma unroll
+      for (int u = 0; u < VEC; ++u) w[u] = c + u < p.N ? __ldg(f + r * step + u) : 0;
+    }
+  };
+  uint16_t b[kAhead][VEC];
+  if (mine) {
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r)
+      if (r < p.R) load(r, b[r]);
+  }
+  griddep_wait();
+  if (has) {
+    const float* const v = p.V + static_cast<long long>(i) * p.slices * p.ldv;
+    for (int e = t; e < p.slices * p.ldv; e += kCombThreads) raw[e] = __ldcg(v + e);
+  }
+  const long long chunk_elems = static_cast<long long>(p.block_rows) * 128;
+  const int blk = i / kBlockRows;
+  const float* const part =
+      p.part +
+      (static_cast<long long>(blk) * p.units + min(c >> 7, p.units - 1)) * p.chunks * chunk_elems +
+      (i - blk * kBlockRows) * 128 + (c & 127);
+  float s[VEC] = {};
+#pragma unroll 4
+  for (int k = 0; k < p.chunks; ++k) {
+    if (VEC == 4) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(part + k * chunk_elems));
+      s[0] += q.x;
+      s[VEC > 1 ? 1 : 0] += VEC > 1 ? q.y : 0.0f;
+      s[VEC > 2 ? 2 : 0] += VEC > 2 ? q.z : 0.0f;
+      s[VEC > 3 ? 3 : 0] += VEC > 3 ? q.w : 0.0f;
+    } else {
+      s[0] += __ldcg(part + k * chunk_elems);
+    }
+  }
+  __syncthreads();
+  if (has && t < p.R) {
+    float x = 0.0f;
+    for (int k = 0; k < p.slices; ++k) x += raw[k * p.ldv + t];
+    vs[t] = x;
+  }
+  __syncthreads();
+  if (c >= p.N) return;
+  if (has) {
+    float l[VEC] = {};
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r)
+      if (r < p.R)
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) l[u] = fmaf(vs[r], lora_h2f(b[r][u]), l[u]);
+#pragma unroll 4
+    for (int r = kAhead; r < p.R; ++r) {
+      uint16_t w[VEC];
+      load(r, w);
+#pragma unroll
+      for (int u = 0; u < VEC; ++u) l[u] = fmaf(vs[r], lora_h2f(w[u]), l[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < VEC; ++u) s[u] += l[u];
+  }
+  uint16_t* const dst = p.C + static_cast<long long>(i) * p.ldc + c;
+  uint16_t h[VEC];
+#pragma unroll
+  for (int u = 0; u < VEC; ++u)
+    if (c + u < p.N)
+      h[u] = lora_f2h(p.beta != 0.0f ? fmaf(p.alpha, s[u], p.beta * lora_h2f(dst[u])) : p.alpha * s[u]);
+  if (VEC == 4 && whole && p.vec_c) {
+    uint2 q;
+    memcpy(&q, h, sizeof(q));
+    *reinterpret_cast<uint2*>(dst) = q;
+  } else {
+#pragma unroll
+    for (int u = 0; u < VEC; ++u)
+      if (c + u < p.N) dst[u] = h[u];
+  }
+}
+
+// More rows: one block per (RB rows, 512 columns), four columns a thread.  Rows of one
+// adapter share the loads of F[a] (the rows of a prompt do; row by row, 1500 x
 // 1000 outputs of rank 24 read 72 MB of it from L2 and took 26 us).
 template <bool TRANS, int RB>
 __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const CombineArgs p) {
@@ -366,7 +470,7 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
     auto add = [&](int r, const float (&w)[4]) {
 #pragma unroll
       for (int j = 0; j < RB; ++j)
-        if (RB == 1 || (mine >> j & 1u))
+        if (mine >> j & 1u)
 #pragma unroll
           for (int u = 0; u < 4; ++u) o[j][u] = fmaf(vs[j][r], w[u], o[j][u]);
     };
@@ -568,10 +672,11 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   c.alpha = p.alpha;
   c.beta = p.beta;
   c.vec_c = (reinterpret_cast<uintptr_t>(p.C) & 7u) == 0 && p.ldc % 4 == 0;
-  // as many rows a block as leave about two blocks per SM
+  // as many rows a block as leave about two blocks per SM; else by single rows
   const long long strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
   const int rb = p.M * strips >= 16ll * d.sms ? 8 : (p.M * strips >= 8ll * d.sms ? 4 : 1);
-  const long long blocks = (p.M + rb - 1) / rb * strips;
+  const bool wide = !p.trans && p.M * strips >= d.sms;   // four columns a thread
+  const long long blocks = rb > 1 ? (p.M + rb - 1) / rb * strips : p.M * (wide ? strips : t.units);
   if (blocks > 0x7fffffff) return GEMM_ERR_ARG;
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(kCombThreads, 1, 1);
@@ -580,7 +685,8 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
     constexpr bool T = decltype(trans)::value;
     return rb == 8   ? cudaLaunchKernelEx(&cfg, lora_combine_kernel<T, 8>, c)
            : rb == 4 ? cudaLaunchKernelEx(&cfg, lora_combine_kernel<T, 4>, c)
-                     : cudaLaunchKernelEx(&cfg, lora_combine_kernel<T, 1>, c);
+                     : wide    ? cudaLaunchKernelEx(&cfg, lora_combine_row_kernel<false, 4>, c)
+                     : cudaLaunchKernelEx(&cfg, lora_combine_row_kernel<T, 1>, c);
   };
   const cudaError_t e = p.trans ? launch(std::true_type{}) : launch(std::false_type{});
   return counted_launch(e) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
