@@ -120,8 +120,10 @@ def _addr(x):
         return None
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(x, "ctypes"):                      # numpy array
         return x.ctypes.data
     raise TypeError("expected a tensor, an array or an address, got %r" % type(x))
@@ -222,27 +224,26 @@ def sgemm_f32(A, B, C, alpha=1.0, beta=0.0, M=None, N=None, K=None, lda=None, ld
     _check(rc, "sgemm_f32")
 
 
-def _adapter_dims(A, R, adapters):
-    if adapters is None:
-        adapters = A.shape[0]
-    if R is None:
-        R = A.shape[2]
-    return int(R), int(adapters)
-
-
 def gemm_f16_lora(X, W, C, A, B, ids, scales=None, alpha=1.0, beta=0.0, M=None, N=None, K=None,
                   R=None, adapters=None, ldx=None, ldw=None, ldc=None, lda=None, ldb=None,
                   stream=None):
     """C_i := alpha*(X_i*W + s[a]*(X_i*A[a])*B[a]) + beta*C_i with a = ids[i]
     (int32; outside [0, adapters): no adapter) on device fp16 operands; A is
     (adapters, K, R), B (adapters, R, N), scales fp32 or None for ones."""
-    M, N, K = _dims(X, W, M, N, K)
-    R, adapters = _adapter_dims(A, R, adapters)
+    # (a tensor's shape is asked for once: it costs a third of a microsecond)
+    if M is None or K is None:
+        m, k = X.shape
+        M, K = m if M is None else M, k if K is None else K
+    if N is None:
+        N = W.shape[1]
+    if R is None or adapters is None:
+        n, _, r = A.shape
+        R, adapters = r if R is None else R, n if adapters is None else adapters
     rc = lib().gemm_f16_lora(_addr(X), _addr(W), _addr(C), _addr(A), _addr(B), _addr(ids),
-                             _addr(scales), M, N, K, R, adapters, int(K if ldx is None else ldx),
-                             int(N if ldw is None else ldw), int(N if ldc is None else ldc),
-                             int(R if lda is None else lda), int(N if ldb is None else ldb),
-                             float(alpha), float(beta), _stream(stream))
+                             _addr(scales), M, N, K, R, adapters, K if ldx is None else ldx,
+                             N if ldw is None else ldw, N if ldc is None else ldc,
+                             R if lda is None else lda, N if ldb is None else ldb,
+                             alpha, beta, _stream(stream))
     _check(rc, "gemm_f16_lora")
 
 
@@ -252,23 +253,20 @@ def gemm_f16_lora_grad(dC, X, W, A, B, ids, scales=None, dX=None, dA=None, dB=No
     """Gradients of gemm_f16_lora, W frozen: dX (M, K) fp16, and dA
     (adapters, K, R), dB (adapters, R, N) fp32, which are accumulated onto
     beta times their old values.  Any of the three may be None."""
-    if N is None:
-        N = dC.shape[1]
-    if M is None:
-        M = dC.shape[0]
+    if M is None or N is None:
+        m, n = dC.shape
+        M, N = m if M is None else M, n if N is None else N
     if K is None:
         K = W.shape[0] if W is not None else X.shape[1]
-    if R is None:
-        R = A.shape[2] if A is not None else B.shape[1]
-    if adapters is None:
-        adapters = A.shape[0] if A is not None else B.shape[0]
+    if R is None or adapters is None:
+        n, _, r = A.shape if A is not None else (B.shape[0], None, B.shape[1])
+        R, adapters = r if R is None else R, n if adapters is None else adapters
     rc = lib().gemm_f16_lora_grad(_addr(dC), _addr(X), _addr(W), _addr(A), _addr(B), _addr(ids),
-                                  _addr(scales), _addr(dX), _addr(dA), _addr(dB), int(M), int(N),
-                                  int(K), int(R), int(adapters), int(N if lddc is None else lddc),
-                                  int(K if ldx is None else ldx), int(N if ldw is None else ldw),
-                                  int(R if lda is None else lda), int(N if ldb is None else ldb),
-                                  int(K if lddx is None else lddx), float(alpha), float(beta),
-                                  _stream(stream))
+                                  _addr(scales), _addr(dX), _addr(dA), _addr(dB), M, N, K, R,
+                                  adapters, N if lddc is None else lddc,
+                                  K if ldx is None else ldx, N if ldw is None else ldw,
+                                  R if lda is None else lda, N if ldb is None else ldb,
+                                  K if lddx is None else lddx, alpha, beta, _stream(stream))
     _check(rc, "gemm_f16_lora_grad")
 
 
@@ -279,18 +277,16 @@ def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True,
     beta*Y_t, the experts and p from the router X_t*Wr.  Wr is (H, E), W1
     (E, H, 2I), W2 (E, I, H); ids (int32) and probs (fp32), both (T, topk),
     receive the choice."""
-    if T is None:
-        T = X.shape[0]
-    if H is None:
-        H = X.shape[1]
-    if E is None:
-        E = W2.shape[0]
-    if I is None:
-        I = W2.shape[1]
+    if T is None or H is None:
+        t, h = X.shape
+        T, H = t if T is None else T, h if H is None else H
+    if E is None or I is None:
+        e, i, _ = W2.shape
+        E, I = e if E is None else E, i if I is None else I
     rc = lib().gemm_f16_moe(_addr(X), _addr(Wr), _addr(W1), _addr(W2), _addr(Y), _addr(ids),
-                            _addr(probs), int(T), int(H), int(I), int(E), int(topk),
-                            int(bool(renormalize)), int(H if ldx is None else ldx),
-                            int(H if ldy is None else ldy), float(beta), _stream(stream))
+                            _addr(probs), T, H, I, E, topk, bool(renormalize),
+                            H if ldx is None else ldx, H if ldy is None else ldy, beta,
+                            _stream(stream))
     _check(rc, "gemm_f16_moe")
 
 

@@ -48,6 +48,8 @@ struct Args {
   int check_rows, check_cols;
   int first_list, end_list, first_item[2];   // blocks: checks, lists, items of either job
   int slices, kb[2];
+  int ring;               // bytes of the operand ring: twice as many when every
+                          // CTA can have an SM for itself
   int chunks;             // of 32 ranks
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
@@ -113,7 +115,7 @@ struct Cfg {
   // operand ring and the tile's partial sums: two CTAs fit on an SM up to rank 64
   static constexpr int kRing = RP > 32 ? 65536 : 81920;
   static constexpr int kSums = 128 * RP * 4;
-  static constexpr int kSmem = kRing + kSums + 1024 + 8 * (2 * kMaxStages + 5) + 16;
+  static constexpr int kSmem = kSums + 1024 + 8 * (2 * kMaxStages + 5) + 16;   // beside it
   static_assert(kRing / (kXBytes + kGroup * kNBytes) >= 2, "two stages");
   static_assert(kRing >= kSums, "the ring holds the tile's sums");
 };
@@ -216,14 +218,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
-  const uint32_t bars = base + G::kRing + G::kSums;
+  const uint32_t bars = base + p.ring + G::kSums;
   auto full_bar = [&](int s) { return bars + 8u * s; };
   auto empty_bar = [&](int s) { return bars + 8u * (kMaxStages + s); };
   auto accf_bar = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + i); };
   auto acce_bar = [&](uint32_t i) { return bars + 8u * (2 * kMaxStages + 2 + i); };
   const uint32_t done_bar = bars + 8u * (2 * kMaxStages + 4);
-  float* const sums = reinterpret_cast<float*>(base_ptr + G::kRing);   // [128][ldv]
-  uint8_t* const tmem_ptr = base_ptr + G::kRing + G::kSums + 8 * (2 * kMaxStages + 5);
+  float* const sums = reinterpret_cast<float*>(base_ptr + p.ring);   // [128][ldv]
+  uint8_t* const tmem_ptr = base_ptr + p.ring + G::kSums + 8 * (2 * kMaxStages + 5);
   const int warp = warp_id_uniform(), lane = static_cast<int>(lane_id());
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int passes = (n + G::kGroup - 1) / G::kGroup;
   // a stage holds the rows and as many adapters as a pass can have here
   const uint32_t stage_bytes = kXBytes + min(max(n, 1), G::kGroup) * G::kNBytes;
-  const int S = min(kMaxStages, static_cast<int>(G::kRing / stage_bytes));
+  const int S = min(kMaxStages, static_cast<int>(p.ring / stage_bytes));
   const unsigned long long limit = p.wait_limit_ns;
   DeviceStatus* const st = p.status;
   const int fboxes = job.k_major ? 1 : (p.R + 63) / 64;
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float4* const mine = reinterpret_cast<float4*>(base_ptr);   // [share][ldv]
   float4* const vout =
       reinterpret_cast<float4*>(job.V + (static_cast<long long>(row0) + r0) * p.ldv);
-  const uint32_t sums_addr = base + G::kRing + r0 * p.ldv * 4;
+  const uint32_t sums_addr = base + p.ring + r0 * p.ldv * 4;
   float top = 0.0f;
   for (int i = threadIdx.x; i < total; i += kThreads) {
     float4 t[kMaxSlices];
@@ -465,21 +467,23 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <int RP>
-int launch(const CUtensorMap* maps, const Args& a, int grid, cudaStream_t stream) {
+int launch(const CUtensorMap* maps, Args a, int grid, int sms, cudaStream_t stream) {
+  a.ring = grid <= sms ? 2 * Cfg<RP>::kRing : Cfg<RP>::kRing;
+  static_assert(2 * Cfg<RP>::kRing + Cfg<RP>::kSmem <= 232448, "shared memory budget");
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
   static bool configured[64] = {};
   if (dev < 64 && !configured[dev]) {
     if (cudaFuncSetAttribute(lora_shrink_tc_kernel<RP>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<RP>::kSmem) != cudaSuccess)
+                             2 * Cfg<RP>::kRing + Cfg<RP>::kSmem) != cudaSuccess)
       return GEMM_ERR_CUDA;
     configured[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<RP>::kSmem;
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.ring) + Cfg<RP>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -579,10 +583,10 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStrea
     a.job[j] = job;
   }
   switch (rp) {
-    case 16: return launch<16>(maps, a, grid, stream);
-    case 32: return launch<32>(maps, a, grid, stream);
-    case 64: return launch<64>(maps, a, grid, stream);
-    default: return launch<128>(maps, a, grid, stream);
+    case 16: return launch<16>(maps, a, grid, d.sms, stream);
+    case 32: return launch<32>(maps, a, grid, d.sms, stream);
+    case 64: return launch<64>(maps, a, grid, d.sms, stream);
+    default: return launch<128>(maps, a, grid, d.sms, stream);
   }
 }
 

@@ -11,7 +11,10 @@
 //                        the shrink, which runs beside it on the same SMs
 //                        (programmatic launch).
 //   lora_combine_kernel  C = alpha (sum of the chunks + V B[a]) + beta C, the
-//                        chunks in k order, everything fp32, one rounding
+//                        chunks in k order, everything fp32, one rounding.  Up
+//                        to kFusedRows rows the last chunk of a column strip to
+//                        arrive does this for the strip instead, with the same
+//                        sums: one launch less.
 //
 // The low-rank product stays on CUDA cores here: each row has its own B[a], so
 // on the tensor cores it would be 128 rows of zeros per adapter for 2 R
@@ -44,6 +47,8 @@ struct ShrinkArgs {
   long long ldx, lda, a_stride;
   int M, K, R, adapters;
   int slices, len;       // K slices of `len` (the last may be shorter)
+  unsigned int* zero;    // counters of the stream kernel
+  int nzero;
 };
 
 // One block per (row, slice): thread (k, v) multiplies x[k] with the eight
@@ -52,6 +57,9 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const Shrin
   __shared__ float red[kShrinkThreads * 9];
   __shared__ float red2[kShrinkThreads];
   griddep_launch_dependents();
+  for (int z = blockIdx.x * kShrinkThreads + threadIdx.x; z < p.nzero;
+       z += gridDim.x * kShrinkThreads)
+    p.zero[z] = 0u;
   const int i = blockIdx.x / p.slices, slice = blockIdx.x - i * p.slices;
   const int a = p.ids[i];
   float* const out = p.V + (static_cast<long long>(i) * p.slices + slice) * p.R;
@@ -104,7 +112,22 @@ constexpr int kMaxStages = 12;
 constexpr int kEpi = 4;
 constexpr int kStreamThreads = 32 * (2 + kEpi);
 constexpr int kBlockRows = 256;             // rows of an item (N of the MMA)
+// Rows up to which the stream kernel finishes the product itself: a warp has the
+// rows of its strip one after another, about 2 us each, where the kernel of its
+// own takes 5 us for all.
+constexpr int kFusedRows = 2;
 constexpr int kSmemMax = 232448;
+
+struct CombineArgs {
+  const float *part, *V;   // V: [row][slice][ldv]
+  const uint16_t* F;       // F[a]: R x N, or N x R
+  const int* ids;
+  uint16_t* C;
+  long long ldf, f_stride, ldc;
+  int M, N, R, ldv, adapters, chunks, slices, units, block_rows;
+  float alpha, beta;
+  bool vec_c;              // rows of C on the 8-byte grid
+};
 
 struct StreamArgs {
   int M, N, trans;
@@ -114,8 +137,47 @@ struct StreamArgs {
   float* part;             // [block][unit][chunk][row][128]
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
+  // fused: the rest of the product, chunks arrived by [unit][epilogue warp]
+  CombineArgs comb;
+  unsigned int* counters;
 };
 
+// Fused: columns c = 128 unit + 32 quad + lane of all rows, by one warp.
+__device__ __forceinline__ void finish_strip(const StreamArgs& p, int unit, int quad, int lane) {
+  const CombineArgs& q = p.comb;
+  const int c = unit * 128 + 32 * quad + lane;
+  for (int i = 0; i < p.M; ++i) {
+    const int a = __ldg(q.ids + i);
+    const bool has = a >= 0 && a < q.adapters;
+    float s = 0.0f;
+    const float* const part =
+        p.part + (static_cast<long long>(unit) * p.chunks * p.M + i) * 128 + 32 * quad + lane;
+#pragma unroll 8
+    for (int k = 0; k < p.chunks; ++k) s += __ldcg(part + static_cast<long long>(k) * p.M * 128);
+    if (has) {
+      const float* const v = q.V + static_cast<long long>(i) * q.slices * q.ldv;
+      const uint16_t* const f = q.F + a * q.f_stride + min(c, p.N - 1);
+      float l = 0.0f;
+      for (int r0 = 0; r0 < q.R; r0 += 32) {   // a lane sums the slices of one rank
+        float x = 0.0f;
+        if (r0 + lane < q.R)
+#pragma unroll 8
+          for (int k = 0; k < q.slices; ++k) x += __ldcg(v + k * q.ldv + r0 + lane);
+        const int n = min(32, q.R - r0);
+#pragma unroll 16
+        for (int r = 0; r < n; ++r)
+          l = fmaf(__shfl_sync(0xffffffffu, x, r), lora_h2f(__ldg(f + (r0 + r) * q.ldf)), l);
+      }
+      s += l;
+    }
+    if (c < p.N) {
+      uint16_t* const dst = q.C + static_cast<long long>(i) * q.ldc + c;
+      *dst = lora_f2h(q.beta != 0.0f ? fmaf(q.alpha, s, q.beta * lora_h2f(*dst)) : q.alpha * s);
+    }
+  }
+}
+
+template <bool FUSED>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     row_stream_kernel(const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmX, const StreamArgs p) {
@@ -242,6 +304,15 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else {
     const int quad = warp & 3;
     uint32_t local = 0;
+    if (FUSED) {
+      // the strip's first rows of B[a] into L2 (no kernel before writes them)
+      const int c = static_cast<int>(blockIdx.x) / p.chunks * 128 + 64 * (quad & 1);
+      const int a = __ldg(p.comb.ids);
+      if (quad < 2 && c < p.N && a >= 0 && a < p.comb.adapters)
+        for (int r = lane; r < p.comb.R; r += 32)
+          prefetch_l2(p.comb.F + a * p.comb.f_stride + r * p.comb.ldf + c);
+      griddep_wait();   // V, and the counters at zero
+    }
     for (int it = blockIdx.x; it < p.items; it += gridDim.x, ++local) {
       const uint32_t buf = local & 1u;
       if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 65)) break;
@@ -264,9 +335,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acce_bar(buf));
+      if (FUSED) {
+        const int unit = it / p.chunks;   // one block of rows
+        unsigned int before = 0;
+        if (lane == 0)
+          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                       : "=r"(before)
+                       : "l"(p.counters + unit * kEpi + quad)
+                       : "memory");
+        before = __shfl_sync(0xffffffffu, before, 0);
+        __syncwarp();
+        if (before == static_cast<unsigned int>(p.chunks - 1)) finish_strip(p, unit, quad, lane);
+      }
     }
     // this kernel's end stands for the shrink's too (the combine waits for it)
-    griddep_wait();
+    if (!FUSED) griddep_wait();
   }
   __syncthreads();
   tc_fence_after();
@@ -275,17 +358,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 
 // ------------------------------------------------------------------ combine
 constexpr int kCombThreads = 128;
-
-struct CombineArgs {
-  const float *part, *V;   // V: [row][slice][ldv]
-  const uint16_t* F;       // F[a]: R x N, or N x R
-  const int* ids;
-  uint16_t* C;
-  long long ldf, f_stride, ldc;
-  int M, N, R, ldv, adapters, chunks, slices, units, block_rows;
-  float alpha, beta;
-  bool vec_c;              // rows of C on the 8-byte grid
-};
 
 // Few rows: one block per (row, 128 VEC columns), VEC columns a thread (four
 // when that still fills the SMs; a thread then takes them with one load).  All
@@ -590,7 +662,8 @@ bool lora_stream_suits(int M, int N, int sms) {
 size_t lora_stream_bytes(const LoraStream& p, int sms) {
   const StreamArgs t = plan(p, sms);
   const size_t v = p.V ? 0 : 4 * static_cast<size_t>(p.M) * shrink_slices(p, sms) * ((p.R + 7) / 8 * 8);
-  return lora_round256(v) + 4 * static_cast<size_t>(t.items) * t.block_rows * 128;
+  return lora_round256(v) + lora_round256(4 * static_cast<size_t>(t.units) * kEpi) +
+         4 * static_cast<size_t>(t.items) * t.block_rows * 128;
 }
 
 int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStream_t stream) {
@@ -604,7 +677,9 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
   static bool configured[64] = {};
   if (dev < 64 && !configured[dev]) {
-    if (cudaFuncSetAttribute(row_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(row_stream_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMax) != cudaSuccess ||
+        cudaFuncSetAttribute(row_stream_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemMax) != cudaSuccess)
       return GEMM_ERR_CUDA;
     configured[dev] = true;
@@ -616,6 +691,7 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   c.ldv = p.ldv;
   c.slices = 1;
   uint8_t* rest = static_cast<uint8_t*>(scratch);
+  const bool fused = !p.V && p.M <= kFusedRows;
   if (!p.V) {
     ShrinkArgs s{};
     const int want = shrink_slices(p, d.sms), r8 = (p.R + 7) / 8 * 8;
@@ -634,6 +710,12 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
     s.K = p.K;
     s.R = r8;
     s.adapters = p.adapters;
+    if (fused) {
+      s.nzero = t.units * kEpi;
+      s.zero = reinterpret_cast<unsigned int*>(rest);
+      rest += lora_round256(4 * static_cast<size_t>(s.nzero));
+      t.counters = s.zero;
+    }
     lora_shrink_kernel<<<p.M * s.slices, kShrinkThreads, 0, stream>>>(s);
     if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
     c.V = s.V;
@@ -641,20 +723,6 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
     c.slices = s.slices;
   }
   t.part = reinterpret_cast<float*>(rest);
-
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(t.items, d.sms)), 1, 1);
-  cfg.blockDim = dim3(kStreamThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(t.stages) * t.stage_bytes + 2048;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (counted_launch(cudaLaunchKernelEx(&cfg, row_stream_kernel, tmW, tmX, t)) != cudaSuccess)
-    return GEMM_ERR_CUDA;
-
   c.part = t.part;
   c.F = p.F;
   c.ids = p.ids;
@@ -672,6 +740,23 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   c.alpha = p.alpha;
   c.beta = p.beta;
   c.vec_c = (reinterpret_cast<uintptr_t>(p.C) & 7u) == 0 && p.ldc % 4 == 0;
+  t.comb = c;
+
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(t.items, d.sms)), 1, 1);
+  cfg.blockDim = dim3(kStreamThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(t.stages) * t.stage_bytes + 2048;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t es = fused ? cudaLaunchKernelEx(&cfg, row_stream_kernel<true>, tmW, tmX, t)
+                               : cudaLaunchKernelEx(&cfg, row_stream_kernel<false>, tmW, tmX, t);
+  if (counted_launch(es) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (fused) return GEMM_OK;
+
   // as many rows a block as leave about two blocks per SM; else by single rows
   const long long strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
   const int rb = p.M * strips >= 16ll * d.sms ? 8 : (p.M * strips >= 8ll * d.sms ? 4 : 1);
