@@ -130,7 +130,7 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
   auto describe = [&]() {   // of the operands as they are by now
     s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, chunks ? 0 : kLoraPacked};
     s.njobs = s.all_jobs = 1;
-    s.min_c = p.K;
+    s.max_c = p.K;
     if (!chunks) {
       s.check = p.B;
       s.ld_check = p.ldb;
@@ -186,7 +186,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   auto describe = [&]() {
     s.njobs = 0;
     s.all_jobs = 2;
-    s.min_c = std::min(p.N, p.K);
+    s.max_c = std::max(p.N, p.K);
     if (use_u)
       s.job[s.njobs++] = LoraShrinkJob{G, ldg, p.N, p.B, p.ldb, p.b_stride(), 1,
                                        (dX && !chunks ? kLoraPacked : 0) | (dA ? kLoraScaled : 0)};

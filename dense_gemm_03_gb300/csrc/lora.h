@@ -78,7 +78,7 @@ constexpr int kLoraPacked = 1, kLoraScaled = 2;
 struct LoraShrinkPlan {
   LoraShrinkJob job[2];
   int njobs;
-  int all_jobs, min_c;    // jobs the operator can have, the least C among them
+  int all_jobs, max_c;    // jobs the operator can have, the largest C among them
   const int* ids;
   const float* scales;
   int M, R, adapters;

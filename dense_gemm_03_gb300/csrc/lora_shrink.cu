@@ -108,15 +108,15 @@ __device__ int distinct(const int* ids, int n, int adapters, int* list, int* slo
 // RP: columns of an adapter.
 template <int RP>
 struct Cfg {
-  static constexpr int kCols = RP > 32 ? RP : 32;      // columns of a pass: whole adapters
-  static constexpr int kGroup = kCols / RP;            // adapters per pass
+  static constexpr int kCols = RP > 64 ? RP : 64;      // columns of a pass: whole adapters
+  static constexpr int kGroup = kCols / RP;            // most adapters per pass
   static constexpr int kNBytes = RP > 64 ? 16384 : 8192;   // MN-major: 64-column boxes
-  static constexpr int kTmemCols = 2 * kCols < 64 ? 64 : 2 * kCols;
+  static constexpr int kTmemCols = 2 * kCols;
   // operand ring and the tile's partial sums: two CTAs fit on an SM up to rank 64
   static constexpr int kRing = RP > 32 ? 65536 : 81920;
   static constexpr int kSums = 128 * RP * 4;
   static constexpr int kSmem = kSums + 1024 + 8 * (2 * kMaxStages + 5) + 16;   // beside it
-  static_assert(kRing / (kXBytes + kGroup * kNBytes) >= 2, "two stages");
+  static_assert(kRing / (kXBytes + kNBytes) >= 2, "two stages");
   static_assert(kRing >= kSums, "the ring holds the tile's sums");
 };
 
@@ -249,9 +249,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
-  const int passes = (n + G::kGroup - 1) / G::kGroup;
-  // a stage holds the rows and as many adapters as a pass can have here
-  const uint32_t stage_bytes = kXBytes + min(max(n, 1), G::kGroup) * G::kNBytes;
+  // adapters of a pass: as many as leave the ring two stages; a stage holds the
+  // rows and as many adapters as a pass can have here
+  const int group = min(min(max(n, 1), G::kGroup), (p.ring / 2 - kXBytes) / G::kNBytes);
+  const int passes = (n + group - 1) / group;
+  const uint32_t stage_bytes = kXBytes + group * G::kNBytes;
   const int S = min(kMaxStages, static_cast<int>(p.ring / stage_bytes));
   const unsigned long long limit = p.wait_limit_ns;
   DeviceStatus* const st = p.status;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t phase = 0, issued = 0;
       bool ok = true;
       for (int ps = 0; ps < passes && ok; ++ps) {
-        const int g0 = ps * G::kGroup, gn = min(G::kGroup, n - g0);
+        const int g0 = ps * group, gn = min(group, n - g0);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 70)) {
             ok = false;
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       uint32_t phase = 0, local = 0;
       bool ok = true;
       for (int ps = 0; ps < passes && ok; ++ps) {
-        const int gn = min(G::kGroup, n - ps * G::kGroup);
+        const int gn = min(group, n - ps * group);
         for (int k0 = kb0; k0 < kb1 && ok; k0 += kFoldKb) {
           const uint32_t buf = local & 1u;
           if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 72)) {
@@ -381,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive(acce_bar(buf));
       }
       if (!ok) break;
-      const int mine = slot - ps * G::kGroup;
-      if (slot >= 0 && mine >= 0 && mine < G::kGroup) {
+      const int mine = slot - ps * group;
+      if (slot >= 0 && mine >= 0 && mine < group) {
         const float s = p.scales ? p.scales[s_list[slot]] : 1.0f;
 #pragma unroll
         for (int j = 0; j < G::kGroup; ++j)
@@ -498,16 +500,17 @@ int launch(const CUtensorMap* maps, Args a, int grid, int sms, cudaStream_t stre
 }
 
 // K slices of a tile: with them the CTAs of all jobs, checks and lists about
-// fill the two places an SM has, at least two k-blocks a slice.  Counted for all
-// the jobs that the operator can have, so that a gradient asked for alone has
-// the bits it has beside the others.
+// fill the two places an SM has, at least two k-blocks a slice for the longer
+// job (slices of the other may be empty).  Counted for all the jobs that the
+// operator can have, so that a gradient asked for alone has the bits it has
+// beside the others.
 int slices_of(const LoraShrinkPlan& p, int sms) {
   const int tiles = (p.M + 127) / 128;
   const long long extra = 1ll * kLoraBadParts * p.adapters + (p.M + 255) / 256;
   const long long room = std::max<long long>((p.R > 64 ? 1 : 2) * sms - extra, sms);
   int s = 1;
   while (2 * s <= kMaxSlices && 2ll * s * tiles * p.all_jobs <= room &&
-         4 * s <= (p.min_c + 63) / 64)
+         4 * s <= (p.max_c + 63) / 64)
     s *= 2;
   return s;
 }
