@@ -119,7 +119,7 @@ LoraShrinkPlan shrink_plan(const LoraArgs& p) {
 int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const LoraDevice& d,
             cudaStream_t stream) {
   const bool chunks = lora_stream_suits(p.M, p.N, d.sms);
-  const bool few = p.M <= kLoraShrinkRows;   // the stream makes V itself
+  const bool few = chunks && lora_stream_shrinks(p.M, p.K, p.R);   // the stream makes V itself
   // the pair kernel aligns W by itself
   Aligned x(p.X, p.ldx, p.M, p.K, true), w(p.W, p.ldw, p.K, p.N, chunks);
   Aligned a(p.A, p.lda, 1ll * p.adapters * p.K, p.R, true, few);

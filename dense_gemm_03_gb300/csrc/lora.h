@@ -32,10 +32,9 @@ struct LoraDevice {
 
 // C := alpha (X W + V F[a]) + beta C by K chunks with their sum in a kernel of
 // its own (lora_stream.cu): F[a] is R x N, or N x R when trans, and W then N x K.
-// V is given ([M][ldv]), or made here from A (up to kLoraShrinkRows rows; A has
+// V is given ([M][ldv]), or made here from A (lora_stream_shrinks; A then has
 // zero columns up to a multiple of eight).  Operands have rows on the 16-byte
 // grid, except C.
-constexpr int kLoraShrinkRows = 128;
 struct LoraStream {
   const uint16_t *X, *W;
   uint16_t* C;
@@ -54,6 +53,8 @@ struct LoraStream {
 // Whether the chunks suit an M x N result better than whole 256 x 256 tiles on
 // CTA pairs: a few rows, or so few tiles that half the pairs would be idle.
 bool lora_stream_suits(int M, int N, int sms);
+// Whether it makes V itself better than lora_shrink does.
+bool lora_stream_shrinks(int M, int K, int R);
 size_t lora_stream_bytes(const LoraStream& p, int sms);
 int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStream_t stream);
 

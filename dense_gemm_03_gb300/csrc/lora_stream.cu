@@ -116,6 +116,7 @@ constexpr int kBlockRows = 256;             // rows of an item (N of the MMA)
 // rows of its strip one after another, about 2 us each, where the kernel of its
 // own takes 5 us for all.
 constexpr int kFusedRows = 2;
+constexpr int kFewRows = 128;               // rows of a decoding batch
 constexpr int kSmemMax = 232448;
 
 struct CombineArgs {
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_row_kernel(const Co
 // 1000 outputs of rank 24 read 72 MB of it from L2 and took 26 us).
 template <bool TRANS, int RB>
 __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const CombineArgs p) {
-  __shared__ float vs[RB][kLoraMaxRank];
+  __shared__ __align__(16) float vs[RB][kLoraMaxRank];
   griddep_launch_dependents();
   const int strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
   const int i0 = blockIdx.x / strips * RB;
@@ -492,15 +493,15 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
     }
   }
   griddep_wait();
-  for (int e = threadIdx.x; e < RB * p.R; e += kCombThreads) {
-    const int j = e / p.R, r = e - j * p.R;
-    float s = 0.0f;
-    if (i0 + j < p.M) {
-      const float* v = p.V + static_cast<long long>(i0 + j) * p.slices * p.ldv + r;
-#pragma unroll 8
-      for (int k = 0; k < p.slices; ++k) s += __ldcg(v + k * p.ldv);
-    }
-    vs[j][r] = s;
+  // V by 16-byte pieces (one slice), the ranks past R up to a multiple of four
+  // with it (they are zero)
+  const int per = p.ldv / 4;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < RB * per; e += kCombThreads) {
+    const int j = e / per, r = (e - j * per) * 4;
+    const int row = min(i0 + j, p.M - 1);
+    *reinterpret_cast<float4*>(&vs[j][r]) =
+        __ldcg(reinterpret_cast<const float4*>(p.V + static_cast<long long>(row) * p.ldv + r));
   }
   __syncthreads();
   if (c >= p.N) return;
@@ -539,47 +540,69 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
       }
     todo &= ~mine;
     const uint16_t* const f = p.F + a * p.f_stride + f0;
-    auto add = [&](int r, const float (&w)[4]) {
+    // four ranks at a time: w[k][u] is rank r + k of column c + u; a row's four
+    // entries of V are one load from shared memory
+    auto add4 = [&](int r, const float (&w)[4][4]) {
 #pragma unroll
       for (int j = 0; j < RB; ++j)
-        if (mine >> j & 1u)
+        if (mine >> j & 1u) {
+          const float4 v = *reinterpret_cast<const float4*>(&vs[j][r]);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) o[j][u] = fmaf(vs[j][r], w[u], o[j][u]);
+          for (int u = 0; u < 4; ++u) {
+            o[j][u] = fmaf(v.x, w[0][u], o[j][u]);
+            o[j][u] = fmaf(v.y, w[1][u], o[j][u]);
+            o[j][u] = fmaf(v.z, w[2][u], o[j][u]);
+            o[j][u] = fmaf(v.w, w[3][u], o[j][u]);
+          }
+        }
     };
     int r = 0;
     if (TRANS) {
+#pragma unroll 2
       for (; r + 8 <= p.R; r += 8) {
-        uint4 w[4];
+        uint4 q[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          w[u] = __ldg(reinterpret_cast<const uint4*>(f + (c + u < p.N ? u * p.ldf : 0) + r));
+          q[u] = __ldg(reinterpret_cast<const uint4*>(f + (c + u < p.N ? u * p.ldf : 0) + r));
+        float w[4][4];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          float2 b[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            b[u] = lora_h2f2(h == 0 ? w[u].x : (h == 1 ? w[u].y : (h == 2 ? w[u].z : w[u].w)));
-          const float lo[4] = {b[0].x, b[1].x, b[2].x, b[3].x};
-          const float hi[4] = {b[0].y, b[1].y, b[2].y, b[3].y};
-          add(r + 2 * h, lo);
-          add(r + 2 * h + 1, hi);
+        for (int u = 0; u < 4; ++u) {
+          const float2 b0 = lora_h2f2(q[u].x), b1 = lora_h2f2(q[u].y);
+          w[0][u] = b0.x; w[1][u] = b0.y; w[2][u] = b1.x; w[3][u] = b1.y;
         }
+        add4(r, w);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 b0 = lora_h2f2(q[u].z), b1 = lora_h2f2(q[u].w);
+          w[0][u] = b0.x; w[1][u] = b0.y; w[2][u] = b1.x; w[3][u] = b1.y;
+        }
+        add4(r + 4, w);
       }
     } else if (whole) {
-#pragma unroll 8
-      for (; r < p.R; ++r) {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(f + r * p.ldf));
-        const float2 b0 = lora_h2f2(b.x), b1 = lora_h2f2(b.y);
-        const float w[4] = {b0.x, b0.y, b1.x, b1.y};
-        add(r, w);
+#pragma unroll 2
+      for (; r + 4 <= p.R; r += 4) {
+        uint2 q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = __ldg(reinterpret_cast<const uint2*>(f + (r + k) * p.ldf));
+        float w[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 b0 = lora_h2f2(q[k].x), b1 = lora_h2f2(q[k].y);
+          w[k][0] = b0.x; w[k][1] = b0.y; w[k][2] = b1.x; w[k][3] = b1.y;
+        }
+        add4(r, w);
       }
     }
-    for (; r < p.R; ++r) {   // ranks past a multiple of eight, the ragged last columns
-      float w[4];
+    for (; r < p.R; r += 4) {   // the last ranks, the ragged last columns
+      float w[4][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        w[u] = c + u < p.N ? lora_h2f(TRANS ? f[u * p.ldf + r] : f[r * p.ldf + u]) : 0.0f;
-      add(r, w);
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          w[k][u] = c + u < p.N && r + k < p.R
+                        ? lora_h2f(TRANS ? f[u * p.ldf + r + k] : f[(r + k) * p.ldf + u])
+                        : 0.0f;
+      add4(r, w);
     }
   }
 #pragma unroll
@@ -656,7 +679,14 @@ StreamArgs plan(const LoraStream& p, int sms) {
 
 bool lora_stream_suits(int M, int N, int sms) {
   const long long tiles = static_cast<long long>((M + 255) / 256) * ((N + 255) / 256);
-  return M <= kLoraShrinkRows || 4 * tiles <= sms;
+  return M <= kFewRows || 4 * tiles <= sms;
+}
+
+// By rows: each row's adapter is read from L2 by itself, 2 K R bytes, whatever
+// the other rows have; on the tensor cores 128 rows read each of theirs once,
+// but with many adapters among them in many passes.
+bool lora_stream_shrinks(int M, int K, int R) {
+  return M <= kFewRows || (M <= 2 * kFewRows && 1ll * M * K * R <= (1ll << 24));
 }
 
 size_t lora_stream_bytes(const LoraStream& p, int sms) {
@@ -759,7 +789,10 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
 
   // as many rows a block as leave about two blocks per SM; else by single rows
   const long long strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
-  const int rb = p.M * strips >= 16ll * d.sms ? 8 : (p.M * strips >= 8ll * d.sms ? 4 : 1);
+  const int rb = c.slices > 1                     ? 1
+                 : p.M * strips >= 16ll * d.sms ? 8
+                 : p.M * strips >= 8ll * d.sms  ? 4
+                                                : 1;
   const bool wide = !p.trans && p.M * strips >= d.sms;   // four columns a thread
   const long long blocks = rb > 1 ? (p.M + rb - 1) / rb * strips : p.M * (wide ? strips : t.units);
   if (blocks > 0x7fffffff) return GEMM_ERR_ARG;
