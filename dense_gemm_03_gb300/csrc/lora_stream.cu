@@ -20,9 +20,11 @@
 // on the tensor cores it would be 128 rows of zeros per adapter for 2 R
 // multiply-adds per output that hide behind the loads of B anyway.
 //
-// Summing the chunks in a kernel of its own spreads that over all SMs: the pair
-// kernel's own K slices, added up by the last to finish, took 8 us longer at
-// 1000 x 1001 x 4096.
+// Summing the chunks in a kernel of its own spreads that over all SMs: as K
+// slices of the pair kernel, added up by the last to finish, 1000 x 1001 x 4096
+// took 55 us instead of 31.  What bounds: at 64 x 4096 x 4096 W streams in 10.5
+// of 18.5 us (34 MB, 0.48 of the measured HBM rate over its whole launch), the
+// rest is the chain of three kernels; at one row the chain is all.
 //
 // Shared memory per ring stage: two 64-column boxes of 64 k-rows of W (128-byte
 // swizzle, MN-major: LBO 8 KB, SBO 1 KB; or, for a W stored transposed, two
