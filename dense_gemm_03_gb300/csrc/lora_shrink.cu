@@ -159,6 +159,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   using G = Cfg<RP>;
   __shared__ int s_first[256], s_list[256], s_slot[256], s_cnt[10];
   __shared__ float s_top[kThreads / 32 + 1];
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&tmX0);
+    prefetch_tensormap(&tmF0);
+    if (p.njobs > 1) {
+      prefetch_tensormap(&tmX1);
+      prefetch_tensormap(&tmF1);
+    }
+  }
   griddep_launch_dependents();
   const int b = blockIdx.x;
   if (b < p.first_list) {

@@ -11,10 +11,7 @@
 //                        the shrink, which runs beside it on the same SMs
 //                        (programmatic launch).
 //   lora_combine_kernel  C = alpha (sum of the chunks + V B[a]) + beta C, the
-//                        chunks in k order, everything fp32, one rounding.  Up
-//                        to kFusedRows rows the last chunk of a column strip to
-//                        arrive does this for the strip instead, with the same
-//                        sums: one launch less.
+//                        chunks in k order, everything fp32, one rounding
 //
 // The low-rank product stays on CUDA cores here: each row has its own B[a], so
 // on the tensor cores it would be 128 rows of zeros per adapter for 2 R
@@ -49,8 +46,6 @@ struct ShrinkArgs {
   long long ldx, lda, a_stride;
   int M, K, R, adapters;
   int slices, len;       // K slices of `len` (the last may be shorter)
-  unsigned int* zero;    // counters of the stream kernel
-  int nzero;
 };
 
 // One block per (row, slice): thread (k, v) multiplies x[k] with the eight
@@ -59,9 +54,6 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const Shrin
   __shared__ float red[kShrinkThreads * 9];
   __shared__ float red2[kShrinkThreads];
   griddep_launch_dependents();
-  for (int z = blockIdx.x * kShrinkThreads + threadIdx.x; z < p.nzero;
-       z += gridDim.x * kShrinkThreads)
-    p.zero[z] = 0u;
   const int i = blockIdx.x / p.slices, slice = blockIdx.x - i * p.slices;
   const int a = p.ids[i];
   float* const out = p.V + (static_cast<long long>(i) * p.slices + slice) * p.R;
@@ -114,10 +106,6 @@ constexpr int kMaxStages = 12;
 constexpr int kEpi = 4;
 constexpr int kStreamThreads = 32 * (2 + kEpi);
 constexpr int kBlockRows = 256;             // rows of an item (N of the MMA)
-// Rows up to which the stream kernel finishes the product itself: a warp has the
-// rows of its strip one after another, about 2 us each, where the kernel of its
-// own takes 5 us for all.
-constexpr int kFusedRows = 2;
 constexpr int kFewRows = 128;               // rows of a decoding batch
 constexpr int kSmemMax = 232448;
 
@@ -140,47 +128,8 @@ struct StreamArgs {
   float* part;             // [block][unit][chunk][row][128]
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
-  // fused: the rest of the product, chunks arrived by [unit][epilogue warp]
-  CombineArgs comb;
-  unsigned int* counters;
 };
 
-// Fused: columns c = 128 unit + 32 quad + lane of all rows, by one warp.
-__device__ __forceinline__ void finish_strip(const StreamArgs& p, int unit, int quad, int lane) {
-  const CombineArgs& q = p.comb;
-  const int c = unit * 128 + 32 * quad + lane;
-  for (int i = 0; i < p.M; ++i) {
-    const int a = __ldg(q.ids + i);
-    const bool has = a >= 0 && a < q.adapters;
-    float s = 0.0f;
-    const float* const part =
-        p.part + (static_cast<long long>(unit) * p.chunks * p.M + i) * 128 + 32 * quad + lane;
-#pragma unroll 8
-    for (int k = 0; k < p.chunks; ++k) s += __ldcg(part + static_cast<long long>(k) * p.M * 128);
-    if (has) {
-      const float* const v = q.V + static_cast<long long>(i) * q.slices * q.ldv;
-      const uint16_t* const f = q.F + a * q.f_stride + min(c, p.N - 1);
-      float l = 0.0f;
-      for (int r0 = 0; r0 < q.R; r0 += 32) {   // a lane sums the slices of one rank
-        float x = 0.0f;
-        if (r0 + lane < q.R)
-#pragma unroll 8
-          for (int k = 0; k < q.slices; ++k) x += __ldcg(v + k * q.ldv + r0 + lane);
-        const int n = min(32, q.R - r0);
-#pragma unroll 16
-        for (int r = 0; r < n; ++r)
-          l = fmaf(__shfl_sync(0xffffffffu, x, r), lora_h2f(__ldg(f + (r0 + r) * q.ldf)), l);
-      }
-      s += l;
-    }
-    if (c < p.N) {
-      uint16_t* const dst = q.C + static_cast<long long>(i) * q.ldc + c;
-      *dst = lora_f2h(q.beta != 0.0f ? fmaf(q.alpha, s, q.beta * lora_h2f(*dst)) : q.alpha * s);
-    }
-  }
-}
-
-template <bool FUSED>
 __global__ void __launch_bounds__(kStreamThreads, 1)
     row_stream_kernel(const __grid_constant__ CUtensorMap tmW,
                       const __grid_constant__ CUtensorMap tmX, const StreamArgs p) {
@@ -211,6 +160,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     mbar_init(done_bar, 1u);
     fence_barrier_init();
     fence_proxy_async_smem();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_ptr), 2 * p.acc_cols);
@@ -307,15 +258,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else {
     const int quad = warp & 3;
     uint32_t local = 0;
-    if (FUSED) {
-      // the strip's first rows of B[a] into L2 (no kernel before writes them)
-      const int c = static_cast<int>(blockIdx.x) / p.chunks * 128 + 64 * (quad & 1);
-      const int a = __ldg(p.comb.ids);
-      if (quad < 2 && c < p.N && a >= 0 && a < p.comb.adapters)
-        for (int r = lane; r < p.comb.R; r += 32)
-          prefetch_l2(p.comb.F + a * p.comb.f_stride + r * p.comb.ldf + c);
-      griddep_wait();   // V, and the counters at zero
-    }
     for (int it = blockIdx.x; it < p.items; it += gridDim.x, ++local) {
       const uint32_t buf = local & 1u;
       if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 65)) break;
@@ -338,21 +280,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acce_bar(buf));
-      if (FUSED) {
-        const int unit = it / p.chunks;   // one block of rows
-        unsigned int before = 0;
-        if (lane == 0)
-          asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                       : "=r"(before)
-                       : "l"(p.counters + unit * kEpi + quad)
-                       : "memory");
-        before = __shfl_sync(0xffffffffu, before, 0);
-        __syncwarp();
-        if (before == static_cast<unsigned int>(p.chunks - 1)) finish_strip(p, unit, quad, lane);
-      }
     }
     // this kernel's end stands for the shrink's too (the combine waits for it)
-    if (!FUSED) griddep_wait();
+    griddep_wait();
   }
   __syncthreads();
   tc_fence_after();
@@ -654,9 +584,10 @@ int plan_chunks(int units, int blocks, int kb, int rows, int sms) {
   return best;
 }
 
-// K slices of the shrink: about four blocks per SM in all, at least 64 long.
+// K slices of the shrink: about four blocks per SM in all, at least 64 long; one
+// where several rows of a block of the sum kernel can share an adapter.
 int shrink_slices(const LoraStream& p, int sms) {
-  return std::max(1, std::min({kMaxSlices, 4 * sms / p.M, p.K / 64}));
+  return p.M > 2 * kFewRows ? 1 : std::max(1, std::min({kMaxSlices, 4 * sms / p.M, p.K / 64}));
 }
 
 StreamArgs plan(const LoraStream& p, int sms) {
@@ -673,7 +604,10 @@ StreamArgs plan(const LoraStream& p, int sms) {
   t.n_cols = (t.block_rows + 15) / 16 * 16;
   t.acc_cols = t.n_cols > 128 ? 256 : 128;
   t.stage_bytes = kWBytes + t.n_cols * 128;
-  t.stages = std::min(kMaxStages, (kSmemMax - 2048) / t.stage_bytes);
+  // beside the blocks of the shrink by rows (10 KB each, four on an SM) where it
+  // runs: with the whole shared memory this kernel's CTAs started only as those
+  // ended, 3 us later
+  t.stages = std::min(kMaxStages, ((p.V ? kSmemMax : kSmemMax - 49152) - 2048) / t.stage_bytes);
   return t;
 }
 
@@ -685,17 +619,17 @@ bool lora_stream_suits(int M, int N, int sms) {
 }
 
 // By rows: each row's adapter is read from L2 by itself, 2 K R bytes, whatever
-// the other rows have; on the tensor cores 128 rows read each of theirs once,
-// but with many adapters among them in many passes.
+// the other rows have: 10 us for 2^25 multiply-adds, what the tensor cores take
+// with a few adapters among 128 rows; with many they make many passes (300 rows
+// of 4096 over 32 adapters of rank 16 in no order: 70 us).
 bool lora_stream_shrinks(int M, int K, int R) {
-  return M <= kFewRows || (M <= 2 * kFewRows && 1ll * M * K * R <= (1ll << 24));
+  return M <= kFewRows || (M <= 4 * kFewRows && 1ll * M * K * R <= (1ll << 25));
 }
 
 size_t lora_stream_bytes(const LoraStream& p, int sms) {
   const StreamArgs t = plan(p, sms);
   const size_t v = p.V ? 0 : 4 * static_cast<size_t>(p.M) * shrink_slices(p, sms) * ((p.R + 7) / 8 * 8);
-  return lora_round256(v) + lora_round256(4 * static_cast<size_t>(t.units) * kEpi) +
-         4 * static_cast<size_t>(t.items) * t.block_rows * 128;
+  return lora_round256(v) + 4 * static_cast<size_t>(t.items) * t.block_rows * 128;
 }
 
 int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStream_t stream) {
@@ -709,9 +643,7 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
   static bool configured[64] = {};
   if (dev < 64 && !configured[dev]) {
-    if (cudaFuncSetAttribute(row_stream_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemMax) != cudaSuccess ||
-        cudaFuncSetAttribute(row_stream_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(row_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemMax) != cudaSuccess)
       return GEMM_ERR_CUDA;
     configured[dev] = true;
@@ -723,7 +655,6 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   c.ldv = p.ldv;
   c.slices = 1;
   uint8_t* rest = static_cast<uint8_t*>(scratch);
-  const bool fused = !p.V && p.M <= kFusedRows;
   if (!p.V) {
     ShrinkArgs s{};
     const int want = shrink_slices(p, d.sms), r8 = (p.R + 7) / 8 * 8;
@@ -742,12 +673,6 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
     s.K = p.K;
     s.R = r8;
     s.adapters = p.adapters;
-    if (fused) {
-      s.nzero = t.units * kEpi;
-      s.zero = reinterpret_cast<unsigned int*>(rest);
-      rest += lora_round256(4 * static_cast<size_t>(s.nzero));
-      t.counters = s.zero;
-    }
     lora_shrink_kernel<<<p.M * s.slices, kShrinkThreads, 0, stream>>>(s);
     if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
     c.V = s.V;
@@ -772,7 +697,6 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   c.alpha = p.alpha;
   c.beta = p.beta;
   c.vec_c = (reinterpret_cast<uintptr_t>(p.C) & 7u) == 0 && p.ldc % 4 == 0;
-  t.comb = c;
 
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -784,10 +708,8 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t es = fused ? cudaLaunchKernelEx(&cfg, row_stream_kernel<true>, tmW, tmX, t)
-                               : cudaLaunchKernelEx(&cfg, row_stream_kernel<false>, tmW, tmX, t);
-  if (counted_launch(es) != cudaSuccess) return GEMM_ERR_CUDA;
-  if (fused) return GEMM_OK;
+  if (counted_launch(cudaLaunchKernelEx(&cfg, row_stream_kernel, tmW, tmX, t)) != cudaSuccess)
+    return GEMM_ERR_CUDA;
 
   // as many rows a block as leave about two blocks per SM; else by single rows
   const long long strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
