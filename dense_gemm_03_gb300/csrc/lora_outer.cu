@@ -9,7 +9,8 @@
 // parts.  What binds is reading X and dC once per adapter in the rows (once in
 // all, when an adapter's rows lie together); the rest is small.  64-row blocks
 // without the adapter are skipped.  Items write fp32 partial sums, which
-// lora_outer_sum_kernel adds up in row order.
+// lora_outer_sum_kernel adds up in row order; up to 512 rows in all (one range)
+// they write the gradients themselves (256 x 1024 x 1024: 23.4 -> 22.0 us).
 //
 // U and V come scaled by a power of two per 128 rows (lora_shrink.cu); 64 rows
 // are what is summed in TMEM (the tensor cores truncate, see there), and the
@@ -46,6 +47,10 @@ struct Args {
   float* part;             // [present][tile columns and ranks as in dA, then as in dB]
   long long part_stride, part_b;
   int* table;              // [range][adapter]: place among the present ones, or -1
+  // one range (direct): the gradients themselves
+  float *dA, *dB;
+  float alpha, beta;
+  int direct;
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
 };
@@ -137,8 +142,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = reinterpret_cast<volatile uint32_t*>(misc)[0];
   const int present = static_cast<int>(misc[1]);
   const uint8_t* const mask_bytes = reinterpret_cast<const uint8_t*>(s_mask);
-  // the places of all masks, for the sum kernel
-  for (int m = blockIdx.x * kThreads + threadIdx.x; m < nmask; m += gridDim.x * kThreads) {
+  // the places of all masks, for the sum kernel; or, with one range, the
+  // gradients of adapters without rows
+  if (p.direct) {
+    for (int a = 0; a < p.adapters; ++a) {
+      if (mask_bytes[a]) continue;
+      for (int src = 0; src < 2; ++src) {
+        float* const o = src ? p.dB : p.dA;
+        if (!o) continue;
+        const long long n = 1ll * (src ? p.cols_g : p.cols_x) * p.R;
+        for (long long i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads)
+          o[a * n + i] = p.beta != 0.0f ? p.beta * o[a * n + i] : 0.0f;
+      }
+    }
+  }
+  for (int m = blockIdx.x * kThreads + threadIdx.x; m < nmask && !p.direct;
+       m += gridDim.x * kThreads) {
     int place = -1;
     if (mask_bytes[m]) {
       const int g = m / kGroupMasks;
@@ -330,9 +349,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const int C = t.src ? p.cols_g : p.cols_x, r0 = 32 * t.chunk, nr = min(32, p.R - r0);
       const int c = t.tile * 256 + half * 128 + 32 * quad + lane;
-      float* const out = p.part + t.present * p.part_stride + (t.src ? p.part_b : 0);
+      float* const out =
+          p.direct ? (t.src ? p.dB : p.dA) + static_cast<long long>(t.a) * C * p.R
+                   : p.part + t.present * p.part_stride + (t.src ? p.part_b : 0);
       if (c < C) {
-        if (t.src == 0 && p.R % 4 == 0) {
+        if (p.direct) {
+#pragma unroll
+          for (int r = 0; r < 32; ++r)
+            if (r < nr) {
+              float* const o = out + (t.src ? static_cast<long long>(r0 + r) * C + c
+                                            : static_cast<long long>(c) * p.R + r0 + r);
+              *o = p.beta != 0.0f ? fmaf(p.alpha, acc[r], p.beta * *o) : p.alpha * acc[r];
+            }
+        } else if (t.src == 0 && p.R % 4 == 0) {
           // nr is a multiple of four: 16-byte stores along the ranks
           float* const o = out + static_cast<long long>(c) * p.R + r0;
 #pragma unroll
@@ -425,6 +454,7 @@ int ranges_of(const LoraOuter& o) {
 }  // namespace
 
 size_t lora_outer_bytes(const LoraOuter& o) {
+  if (o.M <= kRange) return 0;
   const long long ranges = ranges_of(o);
   return lora_round256(4 * static_cast<size_t>(ranges) * o.adapters) +
          4 * static_cast<size_t>(ranges) * std::min(o.adapters, kRange) * o.R *
@@ -468,13 +498,18 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
   a.R = o.R;
   a.adapters = o.adapters;
   a.chunks = chunks;
-  a.table = static_cast<int*>(scratch);
+  a.table = static_cast<int*>(scratch);   // unused, like part, when direct
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) +
                                     lora_round256(4 * static_cast<size_t>(ranges) * o.adapters));
   a.part_b = 1ll * o.K * o.R;
   a.part_stride = a.part_b + 1ll * o.R * o.N;
   a.wait_limit_ns = d.wait_limit_ns;
   a.status = d.status;
+  a.dA = o.dA;
+  a.dB = o.dB;
+  a.alpha = o.alpha;
+  a.beta = o.beta;
+  a.direct = o.M <= kRange;
   SumArgs s{};
   s.part = a.part;
   s.part_stride = a.part_stride;
@@ -503,6 +538,7 @@ int lora_outer(const LoraOuter& o, void* scratch, const LoraDevice& d, cudaStrea
     cfg.numAttrs = r0 == 0 ? 1 : 0;   // a later slab waits for the sums of the one before
     if (counted_launch(cudaLaunchKernelEx(&cfg, lora_outer_kernel, tmX, tmG, tmU, tmV, a)) != cudaSuccess)
       return GEMM_ERR_CUDA;
+    if (a.direct) return GEMM_OK;
     s.ranges = a.ranges;
     s.beta = r0 == 0 ? o.beta : 1.0f;
     const long long blocks =

@@ -711,7 +711,7 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   if (counted_launch(cudaLaunchKernelEx(&cfg, row_stream_kernel, tmW, tmX, t)) != cudaSuccess)
     return GEMM_ERR_CUDA;
 
-  // as many rows a block as leave about two blocks per SM; else by single rows
+  // as many rows a block as leave a few blocks per SM; else by single rows
   const long long strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);
   const int rb = c.slices > 1                     ? 1
                  : p.M * strips >= 16ll * d.sms ? 8
