@@ -186,17 +186,17 @@ struct StreamArgs {
 
 // Chunks per unit of `kb` k-blocks, for `active` experts of `tiles` units each
 // and `pairs` (token, expert) pairs.  A chunk has at least
-//   * 4 k-blocks (128 KB, ~2.8 us of an SM's share of HBM: publishing a chunk's
-//     sums and counting it in takes the two groups of epilogue warps about 2 us
-//     each; with 2 k-blocks they fell behind the stream by 10 us),
 //   * 1/8 of an SM's even share, so that the last ones to finish are short
 //     without the partial sums growing for nothing,
-//   * a quarter as many k-blocks as an expert has tokens: its partial sums,
-//     1 KB per token, then stay an eighth of its 32 KB k-blocks.
+//   * 4 k-blocks (128 KB, ~2.8 us of an SM's share of HBM): publishing a chunk's
+//     sums and counting it in takes the two groups of epilogue warps about 2 us
+//     each (with 2 k-blocks they fell behind the stream by 10 us),
+//   * and one more for each token an expert has, for the 1 KB of sums per token
+//     written and read back (a quarter of a k-block per token instead: 64 tokens
+//     at 8 experts of 4096 x 1408, top 2, 110 us against 72).
 __host__ __device__ inline int chunks_of(int active, int tiles, int kb, int pairs, int ctas) {
-  int len = active * tiles * kb / (8 * ctas);
-  if (len < 4) len = 4;
-  if (len < pairs / (4 * active)) len = pairs / (4 * active);
+  const int share = active * tiles * kb / (8 * ctas), least = 4 + pairs / active;
+  const int len = share > least ? share : least;
   return len >= kb ? 1 : (kb + len - 1) / len;
 }
 
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                   }
               }
             } else {
-#pragma unroll 2
+#pragma unroll 4
               for (int c = 0; c < w.up_chunks; ++c) {
                 const float* src = unit_part + static_cast<long long>(c) * n * 256;
 #pragma unroll
