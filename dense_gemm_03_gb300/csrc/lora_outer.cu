@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int quad = warp & 3, half = (warp - 2 - kLoaders) / 4;
+    const bool vec_a = !p.direct || (reinterpret_cast<uintptr_t>(p.dA) & 15u) == 0;
     uint32_t local = 0;
     bool ok = true;
     for (long long it = blockIdx.x; it < items && ok; it += gridDim.x) {
@@ -353,29 +354,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.direct ? (t.src ? p.dB : p.dA) + static_cast<long long>(t.a) * C * p.R
                    : p.part + t.present * p.part_stride + (t.src ? p.part_b : 0);
       if (c < C) {
-        if (p.direct) {
-#pragma unroll
-          for (int r = 0; r < 32; ++r)
-            if (r < nr) {
-              float* const o = out + (t.src ? static_cast<long long>(r0 + r) * C + c
-                                            : static_cast<long long>(c) * p.R + r0 + r);
-              *o = p.beta != 0.0f ? fmaf(p.alpha, acc[r], p.beta * *o) : p.alpha * acc[r];
-            }
-        } else if (t.src == 0 && p.R % 4 == 0) {
+        auto value = [&](float x, const float* old) {
+          if (!p.direct) return x;
+          return p.beta != 0.0f ? fmaf(p.alpha, x, p.beta * *old) : p.alpha * x;
+        };
+        if (t.src == 0 && p.R % 4 == 0 && vec_a) {
           // nr is a multiple of four: 16-byte stores along the ranks
           float* const o = out + static_cast<long long>(c) * p.R + r0;
 #pragma unroll
           for (int r = 0; r < 32; r += 4)
             if (r < nr)
               __stcg(reinterpret_cast<float4*>(o + r),
-                     make_float4(acc[r], acc[r + 1], acc[r + 2], acc[r + 3]));
+                     make_float4(value(acc[r], o + r), value(acc[r + 1], o + r + 1),
+                                 value(acc[r + 2], o + r + 2), value(acc[r + 3], o + r + 3)));
         } else {
 #pragma unroll
           for (int r = 0; r < 32; ++r)
-            if (r < nr)
-              __stcg(out + (t.src ? static_cast<long long>(r0 + r) * C + c
-                                  : static_cast<long long>(c) * p.R + r0 + r),
-                     acc[r]);
+            if (r < nr) {
+              float* const o = out + (t.src ? static_cast<long long>(r0 + r) * C + c
+                                            : static_cast<long long>(c) * p.R + r0 + r);
+              __stcg(o, value(acc[r], o));
+            }
         }
       }
     }

@@ -313,8 +313,18 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_row_kernel(const Co
   const bool has = a >= 0 && a < p.adapters, mine = has && c < p.N;
   const uint16_t* const f =
       p.F + (mine ? a * p.f_stride + (TRANS ? static_cast<long long>(c) * p.ldf : c) : 0);
-  const long long step = TRANS ? 1 : p.ldf;
+  const long long step = p.ldf;
   const bool whole = c + VEC <= p.N;
+  // ranks r .. r + 7 of this thread's column (TRANS): one load where they are there
+  auto load8 = [&](int r, uint16_t (&w)[8]) {
+    if (r + 8 <= p.R) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(f + r));
+      memcpy(w, &q, sizeof(w));
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) w[u] = r + u < p.R ? __ldg(f + r + u) : 0;
+    }
+  };
   auto load = [&](int r, uint16_t (&w)[VEC]) {
     if (VEC == 4 && whole) {
       const uint2 q = __ldg(reinterpret_cast<const uint2*>(f + r * step));
@@ -326,9 +336,20 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_row_kernel(const Co
   };
   uint16_t b[kAhead][VEC];
   if (mine) {
+    if (TRANS) {
 #pragma unroll
-    for (int r = 0; r < kAhead; ++r)
-      if (r < p.R) load(r, b[r]);
+      for (int r = 0; r < kAhead; r += 8)
+        if (r < p.R) {
+          uint16_t w[8];
+          load8(r, w);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) b[r + u][0] = w[u];
+        }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kAhead; ++r)
+        if (r < p.R) load(r, b[r]);
+    }
   }
   griddep_wait();
   if (has) {
@@ -369,12 +390,23 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_row_kernel(const Co
       if (r < p.R)
 #pragma unroll
         for (int u = 0; u < VEC; ++u) l[u] = fmaf(vs[r], lora_h2f(b[r][u]), l[u]);
-#pragma unroll 4
-    for (int r = kAhead; r < p.R; ++r) {
-      uint16_t w[VEC];
-      load(r, w);
+    if (TRANS) {
+#pragma unroll 2
+      for (int r = kAhead; r < p.R; r += 8) {
+        uint16_t w[8];
+        load8(r, w);
 #pragma unroll
-      for (int u = 0; u < VEC; ++u) l[u] = fmaf(vs[r], lora_h2f(w[u]), l[u]);
+        for (int u = 0; u < 8; ++u)
+          if (r + u < p.R) l[0] = fmaf(vs[r + u], lora_h2f(w[u]), l[0]);
+      }
+    } else {
+#pragma unroll 4
+      for (int r = kAhead; r < p.R; ++r) {
+        uint16_t w[VEC];
+        load(r, w);
+#pragma unroll
+        for (int u = 0; u < VEC; ++u) l[u] = fmaf(vs[r], lora_h2f(w[u]), l[u]);
+      }
     }
 #pragma unroll
     for (int u = 0; u < VEC; ++u) s[u] += l[u];
