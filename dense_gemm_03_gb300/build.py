@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgemm.so")
 SOURCES = ["api.cu", "gemm_f16_tc.cu", "gemm_f16_pair_narrow.cu", "gemm_f16_f32out.cu",
            "gemm_f16_skinny.cu", "sgemm_ffma.cu", "sgemm_split.cu", "aux_kernels.cu",
-           "splitk_static.cu", "lora.cu", "lora_stream.cu", "lora_shrink.cu", "lora_outer.cu", "gemm_f16_lora.cu", "moe.cu", "moe_stream.cu"]
+           "splitk_static.cu", "lora.cu", "lora_stream.cu", "lora_rows.cu", "lora_shrink.cu", "lora_outer.cu", "gemm_f16_lora.cu", "moe.cu", "moe_stream.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -9,7 +9,8 @@
 // with a = ids[i]; a row whose id names no adapter (negative or >= adapters)
 // has only the shared projection, and no adapter's weights touch it.
 //
-//   V and U     lora_shrink.cu (up to 128 rows forward: in lora_stream.cu)
+//   V and U     lora_shrink.cu on the tensor cores; lora_rows.cu for a few rows
+//               forward, or few rows over many adapters
 //   C and dX    lora_stream.cu where the result has few tiles; else the pair
 //               kernel of gemm_f16_tc_kernel.cuh with the adapters as more
 //               k-blocks of its tiles
@@ -131,6 +132,7 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
     s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, chunks ? 0 : kLoraPacked};
     s.njobs = s.all_jobs = 1;
     s.max_c = p.K;
+    s.macs = 1ll * p.M * p.K * p.R;
     if (!chunks) {
       s.check = p.B;
       s.ld_check = p.ldb;
@@ -176,8 +178,15 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
               float alpha, float beta, const LoraDevice& d, cudaStream_t stream) {
   const bool use_u = dX || dA, use_v = dB != nullptr;
   const bool chunks = dX && lora_stream_suits(p.M, p.K, d.sms);
+  // by rows where the result's dX (if any) does not need the lists of tiles;
+  // the rule goes by sizes alone, so that a gradient asked for alone has the bits
+  // it has beside the others
+  LoraShrinkPlan rule = shrink_plan(p);
+  rule.max_c = std::max(p.N, p.K);
+  rule.macs = 1ll * p.M * (1ll * p.N + p.K) * p.R;
+  const bool by_rows = lora_stream_suits(p.M, p.K, d.sms) && lora_rows_suit(rule);
   Aligned g(G, ldg, p.M, p.N, true), x(p.X, p.ldx, p.M, p.K, dA || dB);
-  Aligned a(p.A, p.lda, 1ll * p.adapters * p.K, p.R, dX || dB);
+  Aligned a(p.A, p.lda, 1ll * p.adapters * p.K, p.R, dX || dB, by_rows);
   Aligned b(p.B, p.ldb, 1ll * p.adapters * p.R, p.N, use_u);
   Aligned w(p.W, p.ldw, p.K, p.N, chunks);
   const size_t copies = g.bytes() + x.bytes() + a.bytes() + b.bytes() + w.bytes();
@@ -187,6 +196,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
     s.njobs = 0;
     s.all_jobs = 2;
     s.max_c = std::max(p.N, p.K);
+    s.macs = 1ll * p.M * (1ll * p.N + p.K) * p.R;
     if (use_u)
       s.job[s.njobs++] = LoraShrinkJob{G, ldg, p.N, p.B, p.ldb, p.b_stride(), 1,
                                        (dX && !chunks ? kLoraPacked : 0) | (dA ? kLoraScaled : 0)};
@@ -209,7 +219,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   LoraOuter o{p.X, G, p.ldx, ldg, nullptr, nullptr, p.ids, dA, dB, p.M, p.N, p.K, p.R,
               p.adapters, alpha, beta};
   const bool outer = dA || dB;
-  const size_t shrink_bytes = lora_shrink_bytes(s);
+  const size_t shrink_bytes = by_rows ? lora_rows_bytes(s, d.sms) : lora_shrink_bytes(s);
   const size_t stream_bytes = chunks ? lora_round256(lora_stream_bytes(t, d.sms)) : 0;
   void* buf = nullptr;
   if (int rc = routed_scratch(stream, copies + shrink_bytes + stream_bytes +
@@ -222,7 +232,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
                               static_cast<uint8_t*>(buf), d.sms, stream))
     return rc;
   describe();
-  if (int rc = lora_shrink(s, rest, d, stream)) return rc;
+  if (int rc = by_rows ? lora_rows(s, rest, d, stream) : lora_shrink(s, rest, d, stream)) return rc;
   if (chunks) {
     t.V = s.job[0].V;
     if (int rc = lora_stream(t, rest + shrink_bytes, d, stream)) return rc;

@@ -79,7 +79,8 @@ constexpr int kLoraPacked = 1, kLoraScaled = 2;
 struct LoraShrinkPlan {
   LoraShrinkJob job[2];
   int njobs;
-  int all_jobs, max_c;    // jobs the operator can have, the largest C among them
+  int all_jobs, max_c;    // jobs the operator can have, the largest C among them,
+  long long macs;         // and the multiply-adds of all of them
   const int* ids;
   const float* scales;
   int M, R, adapters;
@@ -92,6 +93,32 @@ struct LoraShrinkPlan {
 };
 size_t lora_shrink_bytes(const LoraShrinkPlan& p);
 int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStream_t stream);
+
+// The same row by row (lora_rows.cu), without lists and marks.  F's rows along K
+// (not k_major) have zero columns up to a multiple of eight.
+bool lora_rows_suit(const LoraShrinkPlan& p);
+size_t lora_rows_bytes(const LoraShrinkPlan& p, int sms);
+int lora_rows(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStream_t stream);
+// Its first kernel: V as [row][slice][R], R a multiple of eight.
+constexpr int kLoraRowSlices = 16;
+struct LoraRowsJob {
+  const uint16_t* x;
+  long long ldx;
+  int C;
+  const uint16_t* F;
+  long long ldf, f_stride;
+  int k_major;
+  float* V;
+  int ranks;              // of F where k_major (0: R)
+};
+struct LoraRows {
+  LoraRowsJob job[2];
+  int njobs, slices;
+  const int* ids;
+  const float* scales;
+  int M, R, adapters;
+};
+cudaError_t launch_lora_rows(const LoraRows& p, cudaStream_t stream);
 
 // The adapters' gradients (lora_outer.cu): dA from X and U, dB from V and G;
 // either may be NULL.
@@ -116,6 +143,29 @@ __device__ __forceinline__ float2 lora_h2f2(uint32_t bits) {
   __half2 h;
   memcpy(&h, &bits, 4);
   return __half22float2(h);
+}
+
+// Four entries as hi halves at o and lo halves 32 further; past the half range
+// hi is infinite and stands alone.
+__device__ __forceinline__ void lora_store_split(uint16_t* o, float4 v) {
+  const __half2 h0 = __floats2half2_rn(v.x, v.y), h1 = __floats2half2_rn(v.z, v.w);
+  const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+  const __half2 l0 = __floats2half2_rn(isinf(f0.x) ? 0.0f : v.x - f0.x, isinf(f0.y) ? 0.0f : v.y - f0.y);
+  const __half2 l1 = __floats2half2_rn(isinf(f1.x) ? 0.0f : v.z - f1.x, isinf(f1.y) ? 0.0f : v.w - f1.y);
+  uint32_t b[4];
+  memcpy(b, &h0, 4);
+  memcpy(b + 1, &h1, 4);
+  memcpy(b + 2, &l0, 4);
+  memcpy(b + 3, &l1, 4);
+  *reinterpret_cast<uint2*>(o) = make_uint2(b[0], b[1]);
+  *reinterpret_cast<uint2*>(o + 32) = make_uint2(b[2], b[3]);
+}
+
+// The power of two that brings a largest finite magnitude `top` into [2^13,
+// 2^14): its exponent, at most 100 either way, so that it and its inverse are
+// normal.
+__device__ __forceinline__ int lora_scale_exponent(float top) {
+  return top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
 }
 
 inline size_t lora_round256(size_t x) { return (x + 255) / 256 * 256; }

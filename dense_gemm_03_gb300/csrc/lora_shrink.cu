@@ -134,22 +134,6 @@ __device__ __forceinline__ float ld_cluster_f(uint32_t addr) {
   return v;
 }
 
-// Four entries as hi halves at o and lo halves 32 further; past the half range
-// hi is infinite and stands alone.
-__device__ __forceinline__ void store_split(uint16_t* o, float4 v) {
-  const __half2 h0 = __floats2half2_rn(v.x, v.y), h1 = __floats2half2_rn(v.z, v.w);
-  const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-  const __half2 l0 = __floats2half2_rn(isinf(f0.x) ? 0.0f : v.x - f0.x, isinf(f0.y) ? 0.0f : v.y - f0.y);
-  const __half2 l1 = __floats2half2_rn(isinf(f1.x) ? 0.0f : v.z - f1.x, isinf(f1.y) ? 0.0f : v.w - f1.y);
-  uint32_t b[4];
-  memcpy(b, &h0, 4);
-  memcpy(b + 1, &h1, 4);
-  memcpy(b + 2, &l0, 4);
-  memcpy(b + 3, &l1, 4);
-  *reinterpret_cast<uint2*>(o) = make_uint2(b[0], b[1]);
-  *reinterpret_cast<uint2*>(o + 32) = make_uint2(b[2], b[3]);
-}
-
 template <int RP>
 __global__ void __launch_bounds__(kThreads, 2)
     lora_shrink_tc_kernel(const __grid_constant__ CUtensorMap tmX0,
@@ -450,8 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     cluster_sync();   // every slice's largest magnitude is known
     for (int k = 0; k < slices; ++k)
       top = fmaxf(k ? top : 0.0f, ld_cluster_f(map_to_cta(smem_addr(s_top + kThreads / 32), k)));
-    // |e| <= 100, so that 2^e and 2^-e are normal
-    const int e = top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
+    const int e = lora_scale_exponent(top);
     up = __int_as_float((127 + e) << 23);
     if (slice == 0 && threadIdx.x == 0) job.unscale[tile] = __int_as_float((127 - e) << 23);
   }
@@ -464,9 +447,9 @@ __global__ void __launch_bounds__(kThreads, 2)
           piece < per ? mine[r * per + piece] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       const long long o =
           ((static_cast<long long>(row0) + r0 + r) * p.chunks + c) * 64 + 4 * q;
-      if (job.packed) store_split(job.packed + o, v);
+      if (job.packed) lora_store_split(job.packed + o, v);
       if (job.scaled)
-        store_split(job.scaled + o, make_float4(up * v.x, up * v.y, up * v.z, up * v.w));
+        lora_store_split(job.scaled + o, make_float4(up * v.x, up * v.y, up * v.z, up * v.w));
     }
   }
   tc_fence_after();

@@ -2,9 +2,7 @@
 // leave SMs idle: a few rows (decoding), where the time is that of streaming W
 // and the adapters from HBM once, and small outputs with a long K.
 //
-//   lora_shrink_kernel   V = s X A by (row, K slice) on CUDA cores: at most 128
-//                        rows x K x R multiply-adds, nothing beside the bytes
-//                        (more rows: lora_shrink.cu)
+//   (lora_rows.cu)       V = s X A by (row, K slice) on CUDA cores
 //   row_stream_kernel    X W as fp32 partial sums by (256 rows, 128 columns, K
 //                        chunk): W is the M operand of tcgen05.mma, the rows of
 //                        X the N operand, both by TMA.  It does not depend on
@@ -33,72 +31,6 @@
 
 namespace gb300 {
 namespace {
-
-// ------------------------------------------------------------------- shrink
-constexpr int kShrinkThreads = 256;
-constexpr int kMaxSlices = 16;
-
-struct ShrinkArgs {
-  const uint16_t *X, *A;
-  const int* ids;
-  const float* scales;
-  float* V;              // [row][slice][R]
-  long long ldx, lda, a_stride;
-  int M, K, R, adapters;
-  int slices, len;       // K slices of `len` (the last may be shorter)
-};
-
-// One block per (row, slice): thread (k, v) multiplies x[k] with the eight
-// ranks 8v .. 8v + 7 of row k of A[a].
-__global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const ShrinkArgs p) {
-  __shared__ float red[kShrinkThreads * 9];
-  __shared__ float red2[kShrinkThreads];
-  griddep_launch_dependents();
-  const int i = blockIdx.x / p.slices, slice = blockIdx.x - i * p.slices;
-  const int a = p.ids[i];
-  float* const out = p.V + (static_cast<long long>(i) * p.slices + slice) * p.R;
-  if (a < 0 || a >= p.adapters) {
-    for (int r = threadIdx.x; r < p.R; r += kShrinkThreads) out[r] = 0.0f;
-    return;
-  }
-  const int nv = p.R >> 3, step = kShrinkThreads / nv;   // k rows per pass
-  const int k0 = slice * p.len, k1 = min(p.K, k0 + p.len);
-  const int tk = threadIdx.x / nv, v = threadIdx.x - tk * nv;
-  float acc[8] = {};
-  if (tk < step) {
-    const uint16_t* x = p.X + static_cast<long long>(i) * p.ldx;
-    const uint16_t* f = p.A + static_cast<long long>(a) * p.a_stride + 8 * v;
-#pragma unroll 4
-    for (int k = k0 + tk; k < k1; k += step) {
-      const float xv = lora_h2f(__ldg(x + k));
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(f + static_cast<long long>(k) * p.lda));
-      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 c = lora_h2f2(h[j]);
-        acc[2 * j] = fmaf(xv, c.x, acc[2 * j]);
-        acc[2 * j + 1] = fmaf(xv, c.y, acc[2 * j + 1]);
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) red[threadIdx.x * 9 + j] = acc[j];
-  __syncthreads();
-  // rank r: the `step` threads' terms in `parts` interleaved groups, then those
-  const int parts = kShrinkThreads / p.R;
-  const int r = threadIdx.x % p.R, part = threadIdx.x / p.R;
-  if (part < parts) {
-    float s = 0.0f;
-    for (int t = part; t < step; t += parts) s += red[(t * nv + (r >> 3)) * 9 + (r & 7)];
-    red2[part * p.R + r] = s;
-  }
-  __syncthreads();
-  if (threadIdx.x < p.R) {
-    float s = 0.0f;
-    for (int t = 0; t < parts; ++t) s += red2[t * p.R + threadIdx.x];
-    out[threadIdx.x] = (p.scales ? p.scales[a] : 1.0f) * s;
-  }
-}
 
 // ------------------------------------------------------------------- stream
 constexpr int kWBytes = 2 * 64 * 128;       // 128 columns of a k-block of W
@@ -303,7 +235,7 @@ constexpr int kAhead = 16;
 template <bool TRANS, int VEC>
 __global__ void __launch_bounds__(kCombThreads) lora_combine_row_kernel(const CombineArgs p) {
   static_assert(VEC == 1 || (VEC == 4 && !TRANS), "four columns are one load along a row of F");
-  __shared__ float raw[kMaxSlices * kLoraMaxRank];
+  __shared__ float raw[kLoraRowSlices * kLoraMaxRank];
   __shared__ float vs[kLoraMaxRank];
   griddep_launch_dependents();
   const int strips = (p.N + kCombThreads * VEC - 1) / (kCombThreads * VEC);
@@ -619,7 +551,8 @@ int plan_chunks(int units, int blocks, int kb, int rows, int sms) {
 // K slices of the shrink: about four blocks per SM in all, at least 64 long; one
 // where several rows of a block of the sum kernel can share an adapter.
 int shrink_slices(const LoraStream& p, int sms) {
-  return p.M > 2 * kFewRows ? 1 : std::max(1, std::min({kMaxSlices, 4 * sms / p.M, p.K / 64}));
+  return p.M > 2 * kFewRows ? 1
+                            : std::max(1, std::min({kLoraRowSlices, 4 * sms / p.M, p.K / 64}));
 }
 
 StreamArgs plan(const LoraStream& p, int sms) {
@@ -688,28 +621,22 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   c.slices = 1;
   uint8_t* rest = static_cast<uint8_t*>(scratch);
   if (!p.V) {
-    ShrinkArgs s{};
-    const int want = shrink_slices(p, d.sms), r8 = (p.R + 7) / 8 * 8;
-    s.len = (p.K + want - 1) / want;
-    s.slices = (p.K + s.len - 1) / s.len;
-    s.V = reinterpret_cast<float*>(rest);
-    rest += lora_round256(4 * static_cast<size_t>(p.M) * want * r8);
-    s.X = p.X;
-    s.A = p.A;
-    s.ids = p.ids;
-    s.scales = p.scales;
-    s.ldx = p.ldx;
-    s.lda = p.lda;
-    s.a_stride = p.a_stride;
-    s.M = p.M;
-    s.K = p.K;
-    s.R = r8;
-    s.adapters = p.adapters;
-    lora_shrink_kernel<<<p.M * s.slices, kShrinkThreads, 0, stream>>>(s);
-    if (counted_launch(cudaGetLastError()) != cudaSuccess) return GEMM_ERR_CUDA;
-    c.V = s.V;
+    const int slices = shrink_slices(p, d.sms), r8 = (p.R + 7) / 8 * 8;
+    float* const v = reinterpret_cast<float*>(rest);
+    rest += lora_round256(4 * static_cast<size_t>(p.M) * slices * r8);
+    LoraRows rows{};
+    rows.job[0] = LoraRowsJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride, 0, v};
+    rows.njobs = 1;
+    rows.slices = slices;
+    rows.ids = p.ids;
+    rows.scales = p.scales;
+    rows.M = p.M;
+    rows.R = r8;
+    rows.adapters = p.adapters;
+    if (launch_lora_rows(rows, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+    c.V = v;
     c.ldv = r8;
-    c.slices = s.slices;
+    c.slices = slices;
   }
   t.part = reinterpret_cast<float*>(rest);
   c.part = t.part;
