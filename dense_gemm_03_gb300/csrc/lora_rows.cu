@@ -3,7 +3,8 @@
 // have.  For decoding batches this hides behind the stream of W; for the
 // gradients of a few rows over many adapters it replaces the tensor-core shrink
 // (lora_shrink.cu), which passes once over its rows for every few adapters among
-// them (49 rows over 29 adapters of rank 32: 110 us of passes against 8).
+// them (dA, dB and dX of 49 rows over 29 adapters of rank 32, 4096 x 4096: 105 us that
+// way, 41 this way).
 //
 //   lora_rows_kernel  (row, K slice, job): F[a] stored along K (thread (k, v):
 //                     ranks 8v .. 8v + 7 of row k) or along the ranks (a warp

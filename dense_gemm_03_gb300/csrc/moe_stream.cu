@@ -45,7 +45,6 @@ namespace gb300 {
 namespace {
 
 constexpr int kBlockT = 64;                  // most tokens per launch
-constexpr int kMaxPairs = kBlockT * kMoeMaxTopk;
 
 // ------------------------------------------------------------------ routing
 constexpr int kRouteThreads = 256;
@@ -193,9 +192,12 @@ struct StreamArgs {
 //     each (with 2 k-blocks they fell behind the stream by 10 us),
 //   * and one more for each token an expert has, for the 1 KB of sums per token
 //     written and read back (a quarter of a k-block per token instead: 64 tokens
-//     at 8 experts of 4096 x 1408, top 2, 110 us against 72).
+//     at 8 experts of 4096 x 1408, top 2, 110 us against 72), but for at most a
+//     third of the unit, so that a few busy experts still reach every SM (60
+//     tokens at 6 experts of 3008 x 1600, top 4, 103 us without, 82 with it).
 __host__ __device__ inline int chunks_of(int active, int tiles, int kb, int pairs, int ctas) {
-  const int share = active * tiles * kb / (8 * ctas), least = 4 + pairs / active;
+  const int share = active * tiles * kb / (8 * ctas);
+  const int tokens = pairs / active, least = 4 + (tokens < kb / 3 ? tokens : kb / 3);
   const int len = share > least ? share : least;
   return len >= kb ? 1 : (kb + len - 1) / len;
 }
