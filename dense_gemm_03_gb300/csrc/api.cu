@@ -1250,7 +1250,7 @@ int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed,
 }
 
 int encode_map_f16_stack(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
-                         int depth, long long stride, int box_cols, int box_rows) {
+                         int depth, long long stride, int box_cols, int box_rows, int swizzle) {
   EncodeTiledFn enc = nullptr;
   if (int rc = encode_fn(&enc)) return rc;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
@@ -1262,8 +1262,10 @@ int encode_map_f16_stack(CUtensorMap* map, const void* ptr, int rows, int cols, 
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims,
                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         swizzle == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                         : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                         : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

@@ -336,10 +336,11 @@ int query_device(int* sm_count, DeviceStatus** status, unsigned long long* wait_
 int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed = 0,
                    void** zeroed_out = nullptr);
 // Tensor map of a stack of `depth` fp16 matrices (rows x cols, leading
-// dimension ld, `stride` elements apart), 128-byte swizzle, boxes of box_cols x
-// box_rows of one matrix; what lies outside a matrix reads as zero.
+// dimension ld, `stride` elements apart), 128-, 64- or 32-byte swizzle, boxes of
+// box_cols x box_rows of one matrix; what lies outside a matrix reads as zero.
 int encode_map_f16_stack(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
-                         int depth, long long stride, int box_cols, int box_rows);
+                         int depth, long long stride, int box_cols, int box_rows,
+                         int swizzle = 128);
 
 // 2-D fp16 tensor map with 128-byte swizzle (rows x cols, row stride ld).
 int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,

@@ -130,9 +130,9 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
   LoraStream t{};
   auto describe = [&]() {   // of the operands as they are by now
     s.job[0] = LoraShrinkJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride(), 0, chunks ? 0 : kLoraPacked};
-    s.njobs = s.all_jobs = 1;
+    s.njobs = 1;
     s.max_c = p.K;
-    s.macs = 1ll * p.M * p.K * p.R;
+    s.sum_c = p.K;
     if (!chunks) {
       s.check = p.B;
       s.ld_check = p.ldb;
@@ -183,7 +183,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   // it has beside the others
   LoraShrinkPlan rule = shrink_plan(p);
   rule.max_c = std::max(p.N, p.K);
-  rule.macs = 1ll * p.M * (1ll * p.N + p.K) * p.R;
+  rule.sum_c = 1ll * p.N + p.K;
   const bool by_rows = lora_stream_suits(p.M, p.K, d.sms) && lora_rows_suit(rule);
   Aligned g(G, ldg, p.M, p.N, true), x(p.X, p.ldx, p.M, p.K, dA || dB);
   Aligned a(p.A, p.lda, 1ll * p.adapters * p.K, p.R, dX || dB, by_rows);
@@ -194,9 +194,8 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   LoraStream t{};
   auto describe = [&]() {
     s.njobs = 0;
-    s.all_jobs = 2;
     s.max_c = std::max(p.N, p.K);
-    s.macs = 1ll * p.M * (1ll * p.N + p.K) * p.R;
+    s.sum_c = 1ll * p.N + p.K;
     if (use_u)
       s.job[s.njobs++] = LoraShrinkJob{G, ldg, p.N, p.B, p.ldb, p.b_stride(), 1,
                                        (dX && !chunks ? kLoraPacked : 0) | (dA ? kLoraScaled : 0)};

@@ -79,8 +79,8 @@ constexpr int kLoraPacked = 1, kLoraScaled = 2;
 struct LoraShrinkPlan {
   LoraShrinkJob job[2];
   int njobs;
-  int all_jobs, max_c;    // jobs the operator can have, the largest C among them,
-  long long macs;         // and the multiply-adds of all of them
+  int max_c;              // of all the jobs that the operator can have
+  long long sum_c;
   const int* ids;
   const float* scales;
   int M, R, adapters;

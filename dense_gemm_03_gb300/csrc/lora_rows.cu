@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kPackThreads) lora_pack_kernel(const PackArgs 
 
 // K slices: about four blocks per SM in all, at least 64 long for the longer job.
 int slices_of(const LoraShrinkPlan& p, int sms) {
-  return std::max(1, std::min({kLoraRowSlices, 4 * sms / (p.M * p.all_jobs), p.max_c / 64}));
+  return std::max(1, std::min({kLoraRowSlices, static_cast<int>(4ll * sms * p.max_c / (p.M * p.sum_c)), p.max_c / 64}));
 }
 
 }  // namespace
@@ -188,7 +188,8 @@ bool lora_rows_suit(const LoraShrinkPlan& p) {
   const int at_once = p.R <= 16 ? 4 : (p.R <= 32 ? 2 : 1);
   const int most = std::min({p.adapters, p.M, 128});
   const long long iterations = 1ll * ((most + at_once - 1) / at_once) * ((p.max_c + 511) / 512);
-  return p.M <= 1024 && iterations >= 24 && p.macs <= std::min(iterations << 20, 1ll << 26);
+  return p.M <= 1024 && iterations >= 24 &&
+         p.M * p.sum_c * p.R <= std::min(iterations << 20, 1ll << 26);
 }
 
 size_t lora_rows_bytes(const LoraShrinkPlan& p, int sms) {

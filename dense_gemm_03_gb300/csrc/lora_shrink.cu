@@ -23,7 +23,9 @@
 // TMEM; the runs are added up in registers, rounded to nearest.
 //
 // F[a] is stored along K (C x R: MN-major N operand) for V, or along the ranks
-// (R x C: K-major) for U.
+// (R x C: K-major) for U.  Along K a rank of 16 or 32 is staged as rows of 32 or
+// 64 bytes: in 128-byte rows, mostly padding, only two stages fitted beside four
+// adapters.
 #include "lora.h"
 
 namespace gb300 {
@@ -46,7 +48,9 @@ struct Args {
   const uint16_t* check;  // weights to look for non-finite ones in, rows x cols each
   long long ld_check, check_stride;
   int check_rows, check_cols;
-  int first_list, end_list, first_item[2];   // blocks: checks, lists, items of either job
+  // blocks: items of the first job, of the second, lists, checks (the short ones
+  // last: items start one to an SM)
+  int first_item, first_list, first_check;
   int slices, kb[2];
   int ring;               // bytes of the operand ring: twice as many when every
                           // CTA can have an SM for itself
@@ -110,7 +114,7 @@ template <int RP>
 struct Cfg {
   static constexpr int kCols = RP > 64 ? RP : 64;      // columns of a pass: whole adapters
   static constexpr int kGroup = kCols / RP;            // most adapters per pass
-  static constexpr int kNBytes = RP > 64 ? 16384 : 8192;   // MN-major: 64-column boxes
+  static constexpr int kNBytes = 128 * RP;             // an adapter's k-block
   static constexpr int kTmemCols = 2 * kCols;
   // operand ring and the tile's partial sums: two CTAs fit on an SM up to rank 64
   static constexpr int kRing = RP > 32 ? 65536 : 81920;
@@ -153,22 +157,25 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   griddep_launch_dependents();
   const int b = blockIdx.x;
-  if (b < p.first_list) {
+  if (b >= p.first_check) {
     // ---- a quarter of an adapter: are its weights finite (if a row uses it)
-    const int adapter = b / kLoraBadParts;
+    const int check = b - p.first_check, adapter = check / kLoraBadParts;
+    if (adapter >= p.adapters) return;   // fills up the last cluster
     bool used = false;
 #pragma unroll 16
     for (int i = threadIdx.x; i < p.M; i += kThreads) used |= __ldg(p.ids + i) == adapter;
     int bad = 0;
     if (__syncthreads_or(used)) {
       const uint16_t* f = p.check + static_cast<long long>(adapter) * p.check_stride;
-      const int groups = (p.check_cols + 7) / 8;
-      const long long total = static_cast<long long>(p.check_rows) * groups;
-      const int part = b - adapter * kLoraBadParts;
+      const int groups = (p.check_cols + 7) / 8, part = check - adapter * kLoraBadParts;
+      const int end = static_cast<int>((part + 1ll) * p.check_rows / kLoraBadParts);
+      // thread t takes 16-byte pieces t, t + kThreads, ... of the rows' pieces
+      int r = static_cast<int>(1ll * part * p.check_rows / kLoraBadParts) + threadIdx.x / groups;
+      int g = threadIdx.x % groups;
+      const int dr = kThreads / groups, dg = kThreads % groups;
 #pragma unroll 16
-      for (long long g = part * total / kLoraBadParts + threadIdx.x;
-           g < (part + 1) * total / kLoraBadParts; g += kThreads) {
-        const int r = static_cast<int>(g / groups), c = static_cast<int>(g % groups) * 8;
+      for (; r < end; r += dr + (g + dg >= groups), g += g + dg >= groups ? dg - groups : dg) {
+        const int c = 8 * g;
         const uint16_t* q = f + static_cast<long long>(r) * p.ld_check + c;
         if (c + 8 <= p.check_cols) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(q));
@@ -182,10 +189,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) p.bad[b] = bad;
+    if (threadIdx.x == 0) p.bad[check] = bad;
     return;
   }
-  if (b < p.end_list) {
+  if (b >= p.first_list) {
     // ---- the distinct adapters of a 256-row block
     const int blk = b - p.first_list, row0 = blk * 256;
     const int n = distinct(p.ids + row0, min(256, p.M - row0), p.adapters, s_list, s_slot, s_first,
@@ -195,13 +202,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (threadIdx.x == 0) out[0] = n;
     return;
   }
-  if (b < p.first_item[0]) return;   // fills up the lists' last cluster
   // ---- a product: rows [row0, row0 + 128), one K slice
-  const int which = p.njobs > 1 && b >= p.first_item[1] ? 1 : 0;
+  const int which = b >= p.first_item ? 1 : 0;
   const LoraShrinkJob& job = p.job[which];
   const CUtensorMap* const tmX = which ? &tmX1 : &tmX0;
   const CUtensorMap* const tmF = which ? &tmF1 : &tmF0;
-  const int item = b - p.first_item[which], slices = p.slices;
+  const int item = b - which * p.first_item, slices = p.slices;
   const int tile = item / slices, slice = item - tile * slices;
   const int row0 = tile * 128, rows = min(128, p.M - row0);
   const int kb0 = slice * p.kb[which] / slices, kb1 = (slice + 1) * p.kb[which] / slices;
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const unsigned long long limit = p.wait_limit_ns;
   DeviceStatus* const st = p.status;
   const int fboxes = job.k_major ? 1 : (p.R + 63) / 64;
-  const uint32_t fbytes = job.k_major ? RP * 128u : fboxes * 8192u;
+  const uint32_t fbytes = job.k_major || RP <= 64 ? RP * 128u : fboxes * 8192u;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -317,6 +323,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint32_t f = f0 + j * G::kNBytes;
                 mma_f16_ss(tmem + buf * G::kCols + j * RP, ad,
                            job.k_major ? smem_desc_sw128(f + kk * 32, 16u, 1024u)
+                           : RP == 16  ? smem_desc_sw32(f + kk * 512, 2048u, 256u)
+                           : RP == 32  ? smem_desc_sw64(f + kk * 1024, 4096u, 512u)
                                        : smem_desc_sw128(f + kk * 2048, 8192u, 1024u),
                            idesc, (kb > k0 || kk > 0) ? 1u : 0u);
               }
@@ -492,15 +500,16 @@ int launch(const CUtensorMap* maps, Args a, int grid, int sms, cudaStream_t stre
 
 // K slices of a tile: with them the CTAs of all jobs, checks and lists about
 // fill the two places an SM has, at least two k-blocks a slice for the longer
-// job (slices of the other may be empty).  Counted for all the jobs that the
-// operator can have, so that a gradient asked for alone has the bits it has
+// job (slices of the other may be empty, and its CTAs count by their length: 1949
+// x 384 x 5568 of rank 24, 24 adapters, 96 -> 92 us).  Counted for all the jobs that
+// the operator can have, so that a gradient asked for alone has the bits it has
 // beside the others.
 int slices_of(const LoraShrinkPlan& p, int sms) {
   const int tiles = (p.M + 127) / 128;
   const long long extra = 1ll * kLoraBadParts * p.adapters + (p.M + 255) / 256;
   const long long room = std::max<long long>((p.R > 64 ? 1 : 2) * sms - extra, sms);
   int s = 1;
-  while (2 * s <= kMaxSlices && 2ll * s * tiles * p.all_jobs <= room &&
+  while (2 * s <= kMaxSlices && 2 * s * tiles * p.sum_c <= room * p.max_c &&
          4 * s <= (p.max_c + 63) / 64)
     s *= 2;
   return s;
@@ -550,10 +559,12 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStrea
   a.check_cols = p.check_cols;
   a.wait_limit_ns = d.wait_limit_ns;
   a.status = d.status;
-  a.first_list = p.check ? kLoraBadParts * p.adapters : 0;
   a.slices = slices_of(p, d.sms);
-  a.end_list = a.first_list + (p.check ? blocks : 0);
-  int grid = (a.end_list + a.slices - 1) / a.slices * a.slices;   // whole clusters
+  a.first_item = tiles * a.slices;
+  a.first_list = p.njobs * a.first_item;
+  a.first_check = a.first_list + (p.check ? blocks : 0);
+  int grid = a.first_check + (p.check ? kLoraBadParts * p.adapters : 0);
+  grid = (grid + a.slices - 1) / a.slices * a.slices;   // whole clusters
   CUtensorMap maps[4] = {};
   for (int j = 0; j < p.njobs; ++j) {
     LoraShrinkJob& job = p.job[j];
@@ -566,13 +577,12 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStrea
       job.scaled = reinterpret_cast<uint16_t*>(take(packed));
       job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(tiles)));
     }
-    a.first_item[j] = grid;
-    grid += tiles * a.slices;
     if (int rc = encode_map_f16(&maps[2 * j], job.x, p.M, job.C, job.ldx, 64, 128)) return rc;
     if (int rc = job.k_major ? encode_map_f16_stack(&maps[2 * j + 1], job.F, p.R, job.C, job.ldf,
                                                     p.adapters, job.f_stride, 64, rp)
                              : encode_map_f16_stack(&maps[2 * j + 1], job.F, job.C, p.R, job.ldf,
-                                                    p.adapters, job.f_stride, 64, 64))
+                                                    p.adapters, job.f_stride, std::min(rp, 64), 64,
+                                                    2 * std::min(rp, 64)))
       return rc;
     a.job[j] = job;
   }

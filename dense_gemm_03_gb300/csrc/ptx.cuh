@@ -536,6 +536,19 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo_
   return d;
 }
 
+// The same with 32-byte swizzle (mode 6): rows of 32 bytes, 8-row groups of 256
+// bytes.
+__device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr, uint32_t lbo_bytes,
+                                                   uint32_t sbo_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(6) << 61;
+  return d;
+}
+
 // Instruction descriptor for kind::f16 / kind::tf32:
 //   bits 4-5  D format (1 = f32)      bits 7-9  A format   bits 10-12 B format
 //   bit 15    A major (0 = K-major)   bit 16    B major (1 = MN-major)
