@@ -552,19 +552,16 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   const uint32_t tmem_free_bar = bars + 8u * (2 * S + 5);   // epilogue warps done with TMEM
   // C sub-tile landed in staging tile b of epilogue warp w
   auto cfull_bar = [&](int w, int b) { return bars + 8u * (2 * S + 6 + L::kBufs * w + b); };
+  constexpr int kQ = 8;
   // adapters: the V tile of stage s is written (by the warps of both CTAs)
   auto vfull_bar = [&](int s) { return base + static_cast<uint32_t>(L::kUsed) + 8u * s; };
   // adapters: this CTA's part of the V tile of stage s has landed
   auto vland_bar = [&](int s) { return vfull_bar(S + s); };
-  // adapters: entries of the tiles' lists on their way to the producer
-  constexpr int kQ = 8;
+  // adapters: entries of the tiles' lists on their way to the producer and the
+  // MMA thread of the leader
   auto qfull_bar = [&](int i) { return vfull_bar(2 * S + i); };
   auto qempty_bar = [&](int i) { return vfull_bar(2 * S + kQ + i); };
-  // adapters: whether a stage of the tile's adapters follows stage s (written by
-  // the producer before it arms the stage)
-  volatile uint32_t* const s_more =
-      reinterpret_cast<uint32_t*>(base_ptr + L::kUsed + 16 * S + 16 * kQ);
-  volatile int* const s_queue = reinterpret_cast<int*>(base_ptr + L::kUsed + 20 * S + 16 * kQ);
+  volatile int* const s_queue = reinterpret_cast<int*>(base_ptr + L::kUsed + 16 * S + 16 * kQ);
   auto stage_a = [&](int s) { return base + static_cast<uint32_t>(s * Cfg::kStageBytes); };
   auto stage_b = [&](int s) { return stage_a(s) + kAB; };
 
@@ -589,7 +586,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
     if constexpr (LORA::kOn)
       for (int i = 0; i < kQ; ++i) {
         mbar_init(qfull_bar(i), 1u);
-        mbar_init(qempty_bar(i), 1u);
+        mbar_init(qempty_bar(i), leader ? 2u : 1u);
       }
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -606,6 +603,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   if (LOAD == kLoadTma && warp == 0 && lane == 0) {
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
+    if constexpr (LORA::kOn) {
+      prefetch_tensormap(&x.tmV);
+      prefetch_tensormap(&x.tmE);
+    }
   }
   if ((EPI == kEpiTma || EPI == kEpiF32Tma) && warp == R::kEpiWarp0 && lane == 0)
     prefetch_tensormap(&tmC);
@@ -630,6 +631,18 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   const unsigned long long limit = p.wait_limit_ns;
   DeviceStatus* const st = p.status;
 
+  // adapters: the next entry of the queue (one thread of each that reads it)
+  auto pop_entry = [&](int& qi, uint32_t& qphase, int where, int& e) {
+    if (!wait_parity(qfull_bar(qi), qphase, limit, st, where)) return false;
+    e = s_queue[qi];
+    mbar_arrive(qempty_bar(qi));
+    if (++qi == kQ) {
+      qi = 0;
+      qphase ^= 1u;
+    }
+    return true;
+  };
+
   if (warp < R::kProdWarps) {
     // ------------------------------------------------------------ producer
     if (LOAD == kLoadTma) {
@@ -640,33 +653,13 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         const uint64_t evict_first = l2_evict_first_policy();
         int qi = 0;
         uint32_t qphase = 0;
-        auto pop_entry = [&](int& e) {
-          if (!wait_parity(qfull_bar(qi), qphase, limit, st, 22)) return false;
-          e = s_queue[qi];
-          mbar_arrive(qempty_bar(qi));
-          if (++qi == kQ) {
-            qi = 0;
-            qphase ^= 1u;
-          }
-          return true;
-        };
         UnitCursor cur = first_unit(p, worker);
         Unit t;
         while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
-          int next_e = -1;   // adapters: the next of the tile's list
           for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
             if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 1)) {
               ok = false;
               break;
-            }
-            if constexpr (LORA::kOn) {
-              if (kb + 1 == t.kb1 && t.kb1 == p.kb_total) {
-                if (!pop_entry(next_e)) {
-                  ok = false;
-                  break;
-                }
-                s_more[stage] = next_e >= 0;
-              }
             }
             // k-blocks of this stage (the unit's last stage may hold one)
             const int nk = KPB == 1 ? 1 : min(KPB, t.kb1 - kb);
@@ -727,18 +720,12 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             const int bcols = t.ncols / 2;
             // a box: 64 columns of 32 ranks, or 64 rows of 64 (32 used)
             constexpr uint32_t kBox = LORA::kTransB ? 8192u : 4096u;
-            while (ok && next_e >= 0) {
-              const int e = next_e;
-              if (!pop_entry(next_e)) {
-                ok = false;
-                break;
-              }
+            for (int e; ok && (ok = pop_entry(qi, qphase, 22, e)) && e >= 0;) {
               for (int c32 = 0; c32 < x.a.chunks; ++c32) {
                 if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 18)) {
                   ok = false;
                   break;
                 }
-                s_more[stage] = c32 + 1 < x.a.chunks || next_e >= 0;
                 mbar_arrive_expect_tx(vland_bar(stage), static_cast<uint32_t>(kABytes));
                 tma_load_2d(stage_a(stage), &x.tmV, vland_bar(stage), 64 * c32, t.m0);
                 const uint32_t fb = map_to_cta(full_bar(stage), 0);
@@ -831,6 +818,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       constexpr uint32_t idesc_full = make_idesc(0u, PAIR ? 2 * BM : MM, BN, 0u, kBMajor);
       constexpr uint32_t idesc_half = make_idesc(0u, PAIR ? 2 * BM : MM, BN / 2, 0u, kBMajor);
       uint32_t vphase = 0;   // adapters: bit s is the parity of stage s's next V tile
+      int qi = 0;
+      uint32_t qphase = 0;
       int stage = 0;
       uint32_t phase = 0, local = 0;
       bool ok = true;
@@ -840,7 +829,6 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         const uint32_t buf = local & 1u, use = local >> 1;
         if (!wait_parity(acce_bar(buf), (use & 1u) ^ 1u, limit, st, 3)) break;
         tc_fence_after();
-        uint32_t more = 0;   // a stage of adapters follows
         const uint32_t idesc = t.ncols == BN ? idesc_full : idesc_half;
         const uint32_t d_tmem = tmem_base + buf * Cfg::kAccStride;
         for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
@@ -849,9 +837,6 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             break;
           }
           tc_fence_after();
-          if constexpr (LORA::kOn) {
-            if (kb + 1 == t.kb1 && t.kb1 == p.kb_total) more = s_more[stage];
-          }
           const int nk = KPB == 1 ? 1 : min(KPB, t.kb1 - kb);
           for (int j = 0; j < nk; ++j) {
             const uint32_t a0 = stage_a(stage) + j * Cfg::kKbBytes, b0 = a0 + kAB;
@@ -879,17 +864,23 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           }
         }
         if constexpr (LORA::kOn) {
-          for (int c32 = 0; ok && more; c32 = c32 + 1 < x.a.chunks ? c32 + 1 : 0) {
+          int c32 = x.a.chunks;   // of the entry in hand: all done
+          while (ok && t.kb1 == p.kb_total) {
+            if (c32 == x.a.chunks) {
+              int e;
+              if (!(ok = pop_entry(qi, qphase, 24, e)) || e < 0) break;
+              c32 = 0;
+            }
             if (!wait_parity(full_bar(stage), phase, limit, st, 19) ||
                 !wait_parity_cluster(vfull_bar(stage), (vphase >> stage) & 1u, limit, st, 20)) {
               ok = false;
               break;
             }
             vphase ^= 1u << stage;
-            more = s_more[stage];
             tc_fence_after();
             const uint32_t a0 = stage_a(stage), b0 = a0 + kAB;
             const int steps = (min(32, x.a.R - 32 * c32) + kUmmaK - 1) / kUmmaK;
+            ++c32;
             for (int kk = 0; kk < steps; ++kk) {
               const uint64_t bd =
                   LORA::kTransB ? smem_desc_sw128(b0 + kk * (kUmmaK * 2), 16u, 1024u)
@@ -939,11 +930,14 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   } else if (LORA::kOn && warp >= R::kWarps) {
     // ------------------------------------------------------------ adapters' V tiles
     // The first of these warps hands the usable entries of each tile's list, and
-    // -1 after them, to the producer.  The second clears other adapters' rows of
-    // the V tiles (four rows a lane).  The ring goes round without it for most of
-    // a tile, so it counts the stages and waits for the V tile of a stage that
-    // is its own (a wait for the parity of `empty` could meet it a whole round
-    // too late and never end).
+    // -1 after them, to the producer and the MMA thread.  The second clears other
+    // adapters' rows of the V tiles (four rows a lane).  The ring goes round
+    // without it for most of a tile, so it counts the stages and waits for the V
+    // tile of a stage that is its own (a wait for the parity of `empty` could meet
+    // it a whole round too late and never end).  A release to the other CTA
+    // takes 0.7 us, against 0.15 to clear a tile, so only the peer makes one (the
+    // leader too: a prompt of 4096 rows, 4096 x 4096, rank 32 over 8 adapters, 108
+    // us against 105; one for several tiles, or from a warp of its own: slower).
     if constexpr (LORA::kOn) {
       const bool walker = warp == R::kWarps;
       uint32_t count = 0, landphase = 0;   // stages passed; bit s: parity of vland_bar(s)
@@ -980,7 +974,12 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
                     make_uint4(0u, 0u, 0u, 0u);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_cta(vfull_bar(stage), 0));
+          if (lane == 0) {
+            if (leader)
+              mbar_arrive(vfull_bar(stage));
+            else
+              mbar_arrive_cluster(map_to_cta(vfull_bar(stage), 0));
+          }
         }
       };
       UnitCursor cur = first_unit(p, worker);
@@ -997,11 +996,11 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         const int* const list =
             x.a.lists + static_cast<long long>((t.m0 - static_cast<int>(rank) * BM) / (2 * BM)) *
                             kLoraListStride;
-        const int n = list[0];
+        const int n = list[0], head = list[1 + lane];   // (written up to n)
         // 32 entries at a time, an adapter with weights that are not all finite
         // left out (the epilogue adds it)
         for (int j0 = 0; j0 < n && ok; j0 += 32) {
-          const int mine = j0 + lane < n ? list[1 + j0 + lane] : -1;
+          const int mine = j0 + lane >= n ? -1 : j0 == 0 ? head : list[1 + j0 + lane];
           const bool usable = mine >= 0 && !lora_bad(x.a, mine);
           for (unsigned int todo = __ballot_sync(0xffffffffu, usable); todo && ok; todo &= todo - 1) {
             const int e = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
@@ -1463,7 +1462,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
 template <int BN, int LOAD, int EPI, bool PAIR, int AM, int MM, int KPB, class LORA>
 constexpr int smem_alloc() {
   using L = Smem<BN, EPI, PAIR, AM, KPB>;
-  constexpr int n = L::kAlloc + (LORA::kOn ? 20 * L::Cfg::kStages + 20 * 8 : 0);
+  constexpr int n = L::kAlloc + (LORA::kOn ? 16 * L::Cfg::kStages + 20 * 8 : 0);
   static_assert(n <= 232448, "shared memory budget");
   return n;
 }
