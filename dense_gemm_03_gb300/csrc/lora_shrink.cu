@@ -12,7 +12,7 @@
 // adds up its share of the rows from all of them, in slice order (through global
 // memory and a counter, the last slice alone took 8 us to add up eight).  The
 // same step writes V as the tensor cores take it: two halves per entry, hi + lo
-// (22 significant bits), 32 ranks' hi and then their lo as 64 columns, so that
+// (22 significant bits or 2^-25), 32 ranks' hi and then their lo as 64 columns, so that
 // the kernels after this one load it by TMA.  For the adapters' gradients it is
 // first scaled, 128 rows at a time, by the power of two that brings its largest
 // finite magnitude into [2^13, 2^14): gradients of any size keep their bits.

@@ -18,7 +18,7 @@
 // Summing the chunks in a kernel of its own spreads that over all SMs: as K
 // slices of the pair kernel, added up by the last to finish, 1000 x 1001 x 4096
 // took 55 us instead of 31.  What bounds: at 64 x 4096 x 4096 W streams in 10.5
-// of 18.5 us (34 MB, 0.48 of the measured HBM rate over its whole launch), the
+// of 15.6 us (34 MB, 0.48 of the measured HBM rate over its whole launch), the
 // rest is the chain of three kernels; at one row the chain is all.
 //
 // Shared memory per ring stage: two 64-column boxes of 64 k-rows of W (128-byte

@@ -27,7 +27,7 @@
 // no wait needs a CTA that has not started.  The weights do not depend on those
 // waits: W2 streams into the ring across them.
 //
-// hid is kept as two halves, hi + lo (22 significant bits), staged as separate
+// hid is kept as two halves, hi + lo (22 significant bits or 2^-25), staged as separate
 // rows of the N operand and added up after the products, so the layer's only
 // rounding to half is that of Y.  A token's columns never mix with another's,
 // and a pair's partial results are read only for its own token.

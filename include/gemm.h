@@ -158,8 +158,9 @@ int sgemm_f32_ld(const float* A, const float* B, float* C,
  *   scales   `adapters` floats on the device, or NULL for all ones
  * C is half with ldc >= N and overlaps no other operand.  Adapters of smaller
  * rank are stacked with zero columns of A and zero rows of B.  Products and
- * sums are fp32; s * X_i * A[a] is kept to at least 22 significant bits (its
- * magnitude must stay within the half range, 65504); C is rounded once.
+ * sums are fp32; s * X_i * A[a] is kept to 22 significant bits or 2^-25,
+ * whichever is coarser (its magnitude must stay within the half range, 65504);
+ * C is rounded once.
  * R == 0 or adapters == 0 is gemm_f16_ld; alpha == 0 and beta == 0 as there.
  */
 int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint16_t* A,
@@ -202,9 +203,9 @@ int gemm_f16_lora_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W,
  * 1 <= topk <= min(E, 32), E <= 1024 (else GEMM_ERR_ARG).  A NaN logit counts
  * as the largest.  Only chosen experts' weights are read, each once per block
  * of tokens; a token's result depends on no other token and no expert it did
- * not choose.  Sums are fp32 in a fixed order; the gated product is kept to at
- * least 22 significant bits (magnitude within the half range); Y is rounded
- * once.  H == 0 leaves nothing to do; I == 0 gives Y := beta * Y.
+ * not choose.  Sums are fp32 in a fixed order; the gated product is kept to 22
+ * significant bits or 2^-25, whichever is coarser (magnitude within the half
+ * range); Y is rounded once.  H == 0 leaves nothing to do; I == 0 gives Y := beta * Y.
  */
 int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_t* W1, const uint16_t* W2,
                  uint16_t* Y, int* ids, float* probs, int T, int H, int I, int E, int topk,
