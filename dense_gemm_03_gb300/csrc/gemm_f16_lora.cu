@@ -8,8 +8,8 @@ namespace {
 
 template <bool TRANS>
 cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                   const CUtensorMap& e, const CUtensorMap& v, const LoraTailArgs& tail, const TcArgs& args, int grid,
-                   cudaStream_t s) {
+                   const CUtensorMap& e, const CUtensorMap& v, const LoraTailArgs& tail,
+                   const TcArgs& args, int grid, cudaStream_t s) {
   LoraTail<TRANS> x{};
   x.tmE = e;
   x.tmV = v;

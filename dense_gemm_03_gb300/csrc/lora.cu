@@ -273,8 +273,8 @@ int plain_dx(const LoraArgs& p, const uint16_t* G, int ldg, uint16_t* dX, int ld
   LoraCall call{};
   call.trans = true;
   // any mapped matrix for the adapters' tensor map: no tile reads it
-  call.tail = LoraTailArgs{nullptr, reinterpret_cast<uint16_t*>(buf), 4, none, lists, nullptr, reinterpret_cast<uint16_t*>(buf), 8,
-                           8, 1, 1, 1};
+  const uint16_t* const any = reinterpret_cast<const uint16_t*>(buf);
+  call.tail = LoraTailArgs{nullptr, any, 4, none, lists, nullptr, any, 8, 8, 1, 1, 1};
   if (int rc = gemm_f16_lora_pair(G, p.W, dX, p.M, p.K, p.N, ldg, p.ldw, lddx, alpha, 0.0f, call,
                                   stream))
     return rc;

@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kPackThreads) lora_pack_kernel(const PackArgs 
 
 // K slices: about four blocks per SM in all, at least 64 long for the longer job.
 int slices_of(const LoraShrinkPlan& p, int sms) {
-  return std::max(1, std::min({kLoraRowSlices, static_cast<int>(4ll * sms * p.max_c / (p.M * p.sum_c)), p.max_c / 64}));
+  const int fill = static_cast<int>(4ll * sms * p.max_c / (p.M * p.sum_c));
+  return std::max(1, std::min({kLoraRowSlices, fill, p.max_c / 64}));
 }
 
 }  // namespace

@@ -318,6 +318,70 @@ def test_grad_parts_alone_equal_the_whole():
     assert t.equal(dX, eX) and t.equal(dA, eA) and t.equal(dB, eB)
 
 
+MANY = [
+    # M, N, K, R, adapters: more adapters among few rows than one pass of the
+    # tensor cores takes
+    (70, 520, 1000, 24, 40),
+    (49, 333, 777, 12, 29),
+    (600, 264, 1536, 40, 64),
+    (130, 72, 4096, 64, 50),
+    (7, 2048, 4096, 128, 9),
+]
+
+
+@pytest.mark.parametrize("M,N,K,R,n", MANY)
+def test_grad_of_many_adapters(M, N, K, R, n):
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M * n, M, N, K, R, n, "mixed")
+    v = dev(o)
+    def outs():
+        return t.full_like(v["X"], float("nan")), v["dA0"].clone(), v["dB0"].clone()
+    dX, dA, dB = outs()
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], dX, dA, dB,
+                         0.5, -1.0)
+    eX, eA, eB = outs()
+    g.gemm_f16_lora_grad(v["G"], None, v["W"], v["A"], v["B"], v["ids"], v["scales"], dX=eX, alpha=0.5)
+    g.gemm_f16_lora_grad(v["G"], v["X"], None, None, v["B"], v["ids"], v["scales"], dA=eA, alpha=0.5,
+                         beta=-1.0)
+    g.gemm_f16_lora_grad(v["G"], v["X"], None, v["A"], None, v["ids"], v["scales"], dB=eB, alpha=0.5,
+                         beta=-1.0)
+    sync(t)
+    r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 0.5, -1.0,
+                      o["dA0"], o["dB0"])
+    for name, got, alone in (("dX", dX, eX), ("dA", dA, eA), ("dB", dB, eB)):
+        ref.check(got.cpu(), *r[name], what=name + " " + g.last_path())
+        assert t.equal(got, alone), name
+
+
+@pytest.mark.parametrize("M,N,K,R,n", MANY[:4])
+def test_grad_of_many_adapters_apart(M, N, K, R, n):
+    """What is not finite in one adapter or one row stays with it."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M + n, M, N, K, R, n, "mixed")
+    o["ids"][0], o["ids"][1] = 3, 5
+    clean, dirty = dev(o), dev({k: v.clone() for k, v in o.items()})
+    dirty["A"][5, 1, 2], dirty["B"][5, 0, 1] = float("inf"), float("nan")
+    dirty["X"][0, 7], dirty["G"][0, 5] = float("nan"), float("-inf")
+    got = []
+    for v in (clean, dirty):
+        out = [t.empty_like(v["X"]), t.empty_like(v["dA0"]), t.empty_like(v["dB0"])]
+        g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], *out)
+        got.append(out)
+    sync(t)
+    rows = clean["ids"] != 5
+    rows[0] = False
+    others = t.tensor([a for a in range(n) if a not in (3, 5)], device="cuda")
+    assert t.equal(got[0][0][rows], got[1][0][rows])
+    for c, e in zip(got[0][1:], got[1][1:]):
+        assert e[others].isfinite().all()
+        ref_scale = c[others].abs().max()
+        # the rows of a block share a power of two, which the row that is not
+        # finite no longer raises: equal but for the parts it keeps
+        assert ((c[others] - e[others]).abs() <= 2.0 ** -20 * ref_scale).all()
+
+
 @pytest.mark.parametrize("M", [5, 64, 400])
 def test_streams_graphs_and_repeats(M):
     """Repeated calls are bitwise equal, on another stream and from a graph."""
