@@ -42,6 +42,7 @@
 #include <initializer_list>
 #include <mutex>
 #include <unordered_map>
+#include <vector>
 
 #include "gemm.h"
 #include "internal.h"
@@ -58,23 +59,24 @@ constexpr int kBM = 128;
 constexpr int kBK = 64;
 constexpr int kHostBlocks = 4;   // row blocks of the pipelined host-buffer forms
 
+// A library-owned device buffer that grows.
+struct Buffer {
+  void* ptr = nullptr;
+  size_t bytes = 0;
+  bool captured = false;        // a CUDA graph may hold its address
+};
+
 // Scratch of one stream: fp32 partial sums (split-K or tail tiles) and the
 // tail-tile arrival counters.  Kernels on one stream run in order, so giving
 // each stream its own scratch keeps concurrent streams apart.
 struct StreamWs {
-  void* ptr = nullptr;
-  size_t bytes = 0;
-  void* counters = nullptr;     // unsigned long long[]
-  size_t counter_bytes = 0;
+  Buffer parts;
+  Buffer counters;              // unsigned long long[]
   unsigned int epoch = 0;       // launches that used the counters
-  void* realigned = nullptr;    // aligned copies of unaligned operands
-  size_t realigned_bytes = 0;
-  void* split = nullptr;        // big/small tf32 parts of fp32 operands
-  size_t split_bytes = 0;
-  void* routed = nullptr;       // scratch of the row-routed products
-  size_t routed_bytes = 0;
-  void* routed_zero = nullptr;  // its arrival counters, zero between calls
-  size_t routed_zero_bytes = 0;
+  Buffer realigned;             // aligned copies of unaligned operands
+  Buffer split;                 // big/small tf32 parts of fp32 operands
+  Buffer routed;                // scratch of the row-routed products
+  Buffer routed_zero;           // its arrival counters, zero between calls
 };
 
 struct DevState {
@@ -84,10 +86,9 @@ struct DevState {
   int l2_bytes = 0;
   DeviceStatus* status = nullptr;
   std::unordered_map<uintptr_t, StreamWs> ws;   // per stream
-  void* flush = nullptr;        // L2 flush buffer
-  size_t flush_bytes = 0;
-  void* host_buf[3] = {nullptr, nullptr, nullptr};  // staging for the host-buffer forms
-  size_t host_bytes[3] = {0, 0, 0};
+  std::vector<void*> outgrown;  // buffers that captured graphs may still use
+  Buffer flush;                 // L2 flush buffer
+  Buffer host_buf[3];           // staging for the host-buffer forms
   // host forms: copy-in and copy-back streams, and per row block an "in"
   // event (operands on the device) and a "done" event (block computed), plus
   // the call's entry and exit events
@@ -156,22 +157,40 @@ int device_state(DevState** out, int* dev_out) {
   return GEMM_OK;
 }
 
-// Grows a library-owned device buffer (synchronising the device before a
-// buffer that may be in use is replaced).
-int ensure_buffer(void** buf, size_t* have, size_t need) {
-  if (*have >= need && *buf) return GEMM_OK;
-  if (*buf) {
-    if (cudaDeviceSynchronize() != cudaSuccess) return GEMM_ERR_CUDA;
-    cudaFree(*buf);
-    *buf = nullptr;
-    *have = 0;
+// Grows a library-owned device buffer for a call on `stream`.  One whose address
+// a captured graph may hold is kept until gemm_release() -- replays go on using
+// it -- and outgrown by at least half, so that what is kept stays within three
+// times the largest; any other is freed once the device is idle.
+int ensure_buffer(DevState* d, Buffer* b, size_t need, cudaStream_t stream) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) {
+    cudaGetLastError();   // the legacy stream beside a capture: not part of it
+    capture = cudaStreamCaptureStatusNone;
+  }
+  const bool capturing = capture != cudaStreamCaptureStatusNone;
+  if (b->bytes >= need && b->ptr) {
+    b->captured |= capturing;
+    return GEMM_OK;
   }
   size_t sz = std::max(need, static_cast<size_t>(1) << 20);
-  if (cudaMalloc(buf, sz) != cudaSuccess) {
-    *buf = nullptr;
-    return GEMM_ERR_CUDA;
+  if (b->ptr && b->captured) {
+    d->outgrown.push_back(b->ptr);
+    sz = std::max(sz, b->bytes + b->bytes / 2);
+  } else if (b->ptr) {
+    if (cudaDeviceSynchronize() != cudaSuccess) return GEMM_ERR_CUDA;
+    cudaFree(b->ptr);
   }
-  *have = sz;
+  *b = Buffer{};
+  if (cudaMalloc(&b->ptr, sz) != cudaSuccess) {
+    cudaGetLastError();
+    sz = need;
+    if (cudaMalloc(&b->ptr, sz) != cudaSuccess) {
+      *b = Buffer{};
+      return GEMM_ERR_CUDA;
+    }
+  }
+  b->bytes = sz;
+  b->captured = capturing;
   return GEMM_OK;
 }
 
@@ -183,13 +202,14 @@ int stream_scratch(DevState* d, cudaStream_t stream, size_t bytes, size_t counte
                    StreamWs** out) {
   StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
   if (bytes) {
-    if (int rc = ensure_buffer(&w.ptr, &w.bytes, bytes)) return rc;
+    if (int rc = ensure_buffer(d, &w.parts, bytes, stream)) return rc;
   }
   if (counters) {
     const size_t cb = counters * sizeof(unsigned long long);
-    if (w.counter_bytes < cb || !w.counters) {
-      if (int rc = ensure_buffer(&w.counters, &w.counter_bytes, cb)) return rc;
-      if (cudaMemsetAsync(w.counters, 0, w.counter_bytes, stream) != cudaSuccess)
+    const void* const before = w.counters.ptr;
+    if (int rc = ensure_buffer(d, &w.counters, cb, stream)) return rc;
+    if (w.counters.ptr != before) {
+      if (cudaMemsetAsync(w.counters.ptr, 0, w.counters.bytes, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
       w.epoch = 0;
     }
@@ -567,9 +587,8 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
     if (lora || a_bytes + b_bytes + c_bytes <= (static_cast<size_t>(1) << 31)) {
       std::lock_guard<std::mutex> lk(g_mu);
       StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
-      if (int rc = ensure_buffer(&w.realigned, &w.realigned_bytes, a_bytes + b_bytes + c_bytes))
-        return rc;
-      uint8_t* buf = static_cast<uint8_t*>(w.realigned);
+      if (int rc = ensure_buffer(d, &w.realigned, a_bytes + b_bytes + c_bytes, stream)) return rc;
+      uint8_t* buf = static_cast<uint8_t*>(w.realigned.ptr);
       RealignBatch batch{};
       auto add = [&](const RealignJob& j, long long groups) {
         batch.job[batch.n] = j;
@@ -711,8 +730,8 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
     std::lock_guard<std::mutex> lk(g_mu);
     StreamWs* w = nullptr;
     if (int rc = stream_scratch(d, stream, need, static_cast<size_t>(parts) * 8, &w)) return rc;
-    a.tail_ws = static_cast<float*>(w->ptr);
-    a.tail_counters = static_cast<unsigned long long*>(w->counters);
+    a.tail_ws = static_cast<float*>(w->parts.ptr);
+    a.tail_counters = static_cast<unsigned long long*>(w->counters.ptr);
     a.epoch = ++w->epoch;
     if (a.epoch == 0) a.epoch = ++w->epoch;   // 0 marks never-used counters
     return GEMM_OK;
@@ -963,8 +982,8 @@ int sgemm_f32_device(const float* A, const float* B, float* C, int M, int N, int
       {
         std::lock_guard<std::mutex> lk(g_mu);
         StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
-        if (int rc = ensure_buffer(&w.split, &w.split_bytes, need)) return rc;
-        buf = static_cast<uint8_t*>(w.split);
+        if (int rc = ensure_buffer(d, &w.split, need, stream)) return rc;
+        buf = static_cast<uint8_t*>(w.split.ptr);
       }
       Tf32Args t{};
       t.pdl = true;   // the split pre-pass was launched just before
@@ -1067,8 +1086,8 @@ int sgemm_f32_device(const float* A, const float* B, float* C, int M, int N, int
         StreamWs* w = nullptr;
         if (int rc = stream_scratch(d, stream, wneed, static_cast<size_t>(sliced) * 16, &w))
           return rc;
-        t.part_ws = static_cast<float4*>(w->ptr);
-        t.counters = static_cast<unsigned long long*>(w->counters);
+        t.part_ws = static_cast<float4*>(w->parts.ptr);
+        t.counters = static_cast<unsigned long long*>(w->counters.ptr);
         t.epoch = ++w->epoch;
         if (t.epoch == 0) t.epoch = ++w->epoch;   // 0 marks never-used counters
         return GEMM_OK;
@@ -1148,13 +1167,13 @@ int host_form(const T* A, const T* B, T* C, int M, int N, int K, int lda, int ld
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (read_ab) {
-      if (int rc = ensure_buffer(&d->host_buf[0], &d->host_bytes[0], ba)) return rc;
-      if (int rc = ensure_buffer(&d->host_buf[1], &d->host_bytes[1], bb)) return rc;
-      dA = static_cast<T*>(d->host_buf[0]);
-      dB = static_cast<T*>(d->host_buf[1]);
+      if (int rc = ensure_buffer(d, &d->host_buf[0], ba, stream)) return rc;
+      if (int rc = ensure_buffer(d, &d->host_buf[1], bb, stream)) return rc;
+      dA = static_cast<T*>(d->host_buf[0].ptr);
+      dB = static_cast<T*>(d->host_buf[1].ptr);
     }
-    if (int rc = ensure_buffer(&d->host_buf[2], &d->host_bytes[2], bc)) return rc;
-    dC = static_cast<T*>(d->host_buf[2]);
+    if (int rc = ensure_buffer(d, &d->host_buf[2], bc, stream)) return rc;
+    dC = static_cast<T*>(d->host_buf[2].ptr);
     for (cudaStream_t* st : {&d->copy_in, &d->copy_back})
       if (!*st && cudaStreamCreateWithFlags(st, cudaStreamNonBlocking) != cudaSuccess)
         return GEMM_ERR_CUDA;
@@ -1236,15 +1255,15 @@ int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed,
   if (int rc = device_state(&d, nullptr)) return rc;
   std::lock_guard<std::mutex> lk(g_mu);
   StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
-  if (int rc = ensure_buffer(&w.routed, &w.routed_bytes, bytes)) return rc;
-  *out = w.routed;
+  if (int rc = ensure_buffer(d, &w.routed, bytes, stream)) return rc;
+  *out = w.routed.ptr;
   if (zeroed) {
-    if (!w.routed_zero || w.routed_zero_bytes < zeroed) {
-      if (int rc = ensure_buffer(&w.routed_zero, &w.routed_zero_bytes, zeroed)) return rc;
-      if (cudaMemsetAsync(w.routed_zero, 0, w.routed_zero_bytes, stream) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    }
-    *zeroed_out = w.routed_zero;
+    const void* const before = w.routed_zero.ptr;
+    if (int rc = ensure_buffer(d, &w.routed_zero, zeroed, stream)) return rc;
+    if (w.routed_zero.ptr != before &&
+        cudaMemsetAsync(w.routed_zero.ptr, 0, w.routed_zero.bytes, stream) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+    *zeroed_out = w.routed_zero.ptr;
   }
   return GEMM_OK;
 }
@@ -1353,9 +1372,9 @@ int gemm_l2_flush(size_t bytes, cudaStream_t stream) {
   const size_t n = bytes ? bytes : 2 * static_cast<size_t>(d->l2_bytes);
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    if (int rc = ensure_buffer(&d->flush, &d->flush_bytes, n)) return rc;
+    if (int rc = ensure_buffer(d, &d->flush, n, stream)) return rc;
   }
-  return cudaMemsetAsync(d->flush, 0, n, stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  return cudaMemsetAsync(d->flush.ptr, 0, n, stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 int gemm_force_path(int path) {
@@ -1448,29 +1467,26 @@ int gemm_release(void) {
   int rc = GEMM_OK;
   for (int dev = 0; dev < kMaxDevices; ++dev) {
     DevState& d = g_dev[dev];
-    void** bufs[4] = {&d.flush, &d.host_buf[0], &d.host_buf[1], &d.host_buf[2]};
-    size_t* sizes[4] = {&d.flush_bytes, &d.host_bytes[0], &d.host_bytes[1], &d.host_bytes[2]};
-    bool any = !d.ws.empty();
-    for (void** b : bufs) any = any || *b != nullptr;
+    Buffer* bufs[4] = {&d.flush, &d.host_buf[0], &d.host_buf[1], &d.host_buf[2]};
+    bool any = !d.ws.empty() || !d.outgrown.empty();
+    for (Buffer* b : bufs) any = any || b->ptr != nullptr;
     if (!any) continue;
     if (cudaSetDevice(dev) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
       rc = GEMM_ERR_CUDA;
       continue;
     }
-    for (int i = 0; i < 4; ++i) {
-      if (*bufs[i]) cudaFree(*bufs[i]);
-      *bufs[i] = nullptr;
-      *sizes[i] = 0;
-    }
-    for (auto& kv : d.ws) {
-      if (kv.second.ptr) cudaFree(kv.second.ptr);
-      if (kv.second.counters) cudaFree(kv.second.counters);
-      if (kv.second.realigned) cudaFree(kv.second.realigned);
-      if (kv.second.split) cudaFree(kv.second.split);
-      if (kv.second.routed) cudaFree(kv.second.routed);
-      if (kv.second.routed_zero) cudaFree(kv.second.routed_zero);
-    }
+    auto drop = [](Buffer* b) {
+      if (b->ptr) cudaFree(b->ptr);
+      *b = Buffer{};
+    };
+    for (Buffer* b : bufs) drop(b);
+    for (auto& kv : d.ws)
+      for (Buffer* b : {&kv.second.parts, &kv.second.counters, &kv.second.realigned,
+                        &kv.second.split, &kv.second.routed, &kv.second.routed_zero})
+        drop(b);
     d.ws.clear();
+    for (void* p : d.outgrown) cudaFree(p);
+    d.outgrown.clear();
     for (cudaStream_t* st : {&d.copy_in, &d.copy_back}) {
       if (*st) cudaStreamDestroy(*st);
       *st = nullptr;

@@ -50,7 +50,12 @@
  *   Graphs     a call may be captured in a CUDA graph on `stream` once the
  *              same shape has run on that stream outside the capture (so
  *              that no scratch has to be allocated inside it); replays give
- *              the same results as direct calls.
+ *              the same results as direct calls, also after larger calls on
+ *              the stream (scratch that a graph was captured with is kept
+ *              until gemm_release(), after which the graph must not be
+ *              replayed).  A replay uses the scratch of the stream it was
+ *              captured on: it must not run at the same time as calls on that
+ *              stream or other graphs captured there.
  *   Errors     a negative return code (below) and nothing enqueued, except
  *              GEMM_ERR_CUDA, which reports a failed launch.  Kernels never
  *              trap: a wait that runs past its time limit sets a device
@@ -376,8 +381,8 @@ long long gemm_launch_count(void);
 const char* gemm_strerror(int code);
 
 /* Frees every library-owned device buffer on every device (workspace,
- * host-form staging buffers, L2-flush buffer).  Synchronises each device
- * that has such buffers. */
+ * host-form staging buffers, L2-flush buffer), those that captured graphs use
+ * among them.  Synchronises each device that has such buffers. */
 int gemm_release(void);
 
 #ifdef __cplusplus

@@ -1,0 +1,100 @@
+"""The library's scratch under programs that share it: graphs captured on a
+stream beside larger calls on it, and host threads on one stream."""
+import pytest
+
+from helpers import torch
+from test_gpu_lora import operands as lora_operands
+from test_gpu_moe import operands as moe_operands
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dense_gemm_03_gb300 import build
+    build.build()
+
+
+def lora_call(t, M, N, K, R, n, seed, grad=False):
+    """A call on `M` rows: (run(), its outputs)."""
+    import dense_gemm_03_gb300 as g
+    o = {k: v.cuda() for k, v in lora_operands(t, seed, M, N, K, R, n, "mixed").items()}
+    if not grad:
+        C = t.full_like(o["C0"], float("nan"))
+        return (lambda: g.gemm_f16_lora(o["X"], o["W"], C, o["A"], o["B"], o["ids"], o["scales"])), [C]
+    out = [t.full_like(o["X"], float("nan")), t.full_like(o["dA0"], float("nan")),
+           t.full_like(o["dB0"], float("nan"))]
+    return (lambda: g.gemm_f16_lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"],
+                                         o["scales"], *out)), out
+
+
+def moe_call(t, T, H, I, E, k, seed):
+    import dense_gemm_03_gb300 as g
+    o = {n: v.cuda() for n, v in moe_operands(t, seed, T, H, I, E).items()}
+    Y = t.full_like(o["Y0"], float("nan"))
+    return (lambda: g.gemm_f16_moe(o["X"], o["Wr"], o["W1"], o["W2"], Y, k)), [Y]
+
+
+def gemm_call(t, M, N, K, seed):
+    import dense_gemm_03_gb300 as g
+    gen = t.Generator(device="cuda").manual_seed(seed)
+    A, B = (t.randn(s, generator=gen, device="cuda").half() for s in ((M, K), (K, N)))
+    C = t.full((M, N), float("nan"), dtype=t.float16, device="cuda")
+    return (lambda: g.gemm_f16(A, B, C)), [C]
+
+
+KINDS = {
+    # small call, then one that needs more of the same scratch
+    "decode": (lambda t: lora_call(t, 8, 1024, 2048, 16, 6, 51),
+               lambda t: lora_call(t, 1500, 1001, 2048, 8, 6, 52)),
+    "tiles": (lambda t: lora_call(t, 2300, 1290, 512, 16, 6, 53),
+              lambda t: lora_call(t, 3000, 1930, 1032, 40, 6, 54)),
+    "grad": (lambda t: lora_call(t, 40, 512, 1024, 16, 6, 55, True),
+             lambda t: lora_call(t, 2500, 1288, 1032, 16, 6, 56, True)),
+    "moe": (lambda t: moe_call(t, 3, 512, 256, 16, 4, 57),
+            lambda t: moe_call(t, 64, 2048, 1024, 32, 8, 58)),
+    "dense": (lambda t: gemm_call(t, 300, 501, 3000, 59),
+              lambda t: gemm_call(t, 2000, 2601, 4096, 60)),
+}
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_a_graph_outlives_larger_calls_on_its_stream(kind):
+    """Replays of a graph give its results, and write nowhere else, after calls
+    on the same stream that outgrew the scratch it was captured with."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    g.release()
+    small, large = (f(t) for f in KINDS[kind])
+    run, outs = small
+    s = t.cuda.Stream()
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.stream(s):
+        run()
+        s.synchronize()
+        want = [x.clone() for x in outs]
+        s.synchronize()
+        with t.cuda.graph(graph, stream=s):
+            run()
+        large[0]()
+        s.synchronize()
+        want_large = [x.clone() for x in large[1]]
+    t.cuda.synchronize()
+    # whatever the larger call freed may go to these
+    mine = [t.full((n,), 7.0, device="cuda") for n in [1 << 18] * 8 + [1 << 22] * 4]
+    for _ in range(3):
+        for x in outs:
+            x.fill_(float("nan"))
+        t.cuda.synchronize()
+        graph.replay()
+        t.cuda.synchronize()
+        assert all(t.equal(a, b) for a, b in zip(want, outs))
+    with t.cuda.stream(s):
+        large[0]()
+    t.cuda.synchronize()
+    assert g.debug_status() == 0
+    assert all(t.equal(a, b) for a, b in zip(want_large, large[1]))
+    assert all(bool((x == 7.0).all()) for x in mine)
+    del graph
+    g.release()
