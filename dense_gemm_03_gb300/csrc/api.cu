@@ -133,6 +133,13 @@ int device_state(DevState** out, int* dev_out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_DEVICE;
+  // a host thread that has not used CUDA yet has no current context, which the
+  // driver's tensor-map encoder needs
+  thread_local int bound = -1;
+  if (dev != bound) {
+    if (cudaSetDevice(dev) != cudaSuccess) return GEMM_ERR_CUDA;
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lk(g_mu);
   DevState& d = g_dev[dev];
   if (!d.init) {

@@ -98,3 +98,39 @@ def test_a_graph_outlives_larger_calls_on_its_stream(kind):
     assert all(bool((x == 7.0).all()) for x in mine)
     del graph
     g.release()
+
+
+@pytest.mark.parametrize("kind", ["decode", "tiles", "grad", "moe", "f16", "f32"])
+def test_first_call_of_a_host_thread(kind):
+    """A thread whose first use of CUDA is a call of the library."""
+    import threading
+
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    dt = t.float32 if kind == "f32" else t.float16
+    A, B = (t.randn(256, 256, device="cuda").to(dt) for _ in range(2))
+    C = t.empty_like(A)
+    run, out = {"f16": lambda: (lambda: g.gemm_f16(A, B, C), [C]),
+                "f32": lambda: (lambda: g.sgemm_f32(A, B, C), [C])}.get(
+                    kind, lambda: KINDS[kind][0](t))()
+    run()
+    t.cuda.synchronize()
+    want = [x.clone() for x in out]
+    for x in out:
+        x.fill_(float("nan"))
+    t.cuda.synchronize()
+    errors = []
+
+    def work():
+        try:
+            run()
+        except Exception as e:      # reported on the main thread
+            errors.append(repr(e))
+
+    th = threading.Thread(target=work)
+    th.start()
+    th.join()
+    t.cuda.synchronize()
+    assert not errors, errors
+    assert g.debug_status() == 0
+    assert all(t.equal(a, b) for a, b in zip(want, out))
