@@ -79,13 +79,35 @@ struct StreamWs {
   Buffer routed_zero;           // its arrival counters, zero between calls
 };
 
+// What tells streams apart: the handle, and the stream's id where one handle
+// (cudaStreamPerThread) names another stream in each host thread.
+struct StreamKey {
+  uintptr_t handle;
+  unsigned long long id;
+  bool operator==(const StreamKey& o) const { return handle == o.handle && id == o.id; }
+};
+struct StreamKeyHash {
+  size_t operator()(const StreamKey& k) const {
+    return std::hash<unsigned long long>{}(k.handle ^ (k.id * 0x9E3779B97F4A7C15ull));
+  }
+};
+
+StreamKey stream_key(cudaStream_t stream) {
+  StreamKey k{reinterpret_cast<uintptr_t>(stream), 0};
+  if (stream == cudaStreamPerThread && cudaStreamGetId(stream, &k.id) != cudaSuccess) {
+    cudaGetLastError();
+    k.id = 0;
+  }
+  return k;
+}
+
 struct DevState {
   bool init = false;
   int err = 0;
   int sm_count = 0;
   int l2_bytes = 0;
   DeviceStatus* status = nullptr;
-  std::unordered_map<uintptr_t, StreamWs> ws;   // per stream
+  std::unordered_map<StreamKey, StreamWs, StreamKeyHash> ws;
   std::vector<void*> outgrown;  // buffers that captured graphs may still use
   Buffer flush;                 // L2 flush buffer
   Buffer host_buf[3];           // staging for the host-buffer forms
@@ -207,7 +229,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // arrival counters (fresh counters start at zero).  Caller holds g_mu.
 int stream_scratch(DevState* d, cudaStream_t stream, size_t bytes, size_t counters,
                    StreamWs** out) {
-  StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
+  StreamWs& w = d->ws[stream_key(stream)];
   if (bytes) {
     if (int rc = ensure_buffer(d, &w.parts, bytes, stream)) return rc;
   }
@@ -593,7 +615,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
     const size_t c_bytes = (c_f32 || c_tma) ? 0 : round256(static_cast<size_t>(M) * ldc2 * 2);
     if (lora || a_bytes + b_bytes + c_bytes <= (static_cast<size_t>(1) << 31)) {
       std::lock_guard<std::mutex> lk(g_mu);
-      StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
+      StreamWs& w = d->ws[stream_key(stream)];
       if (int rc = ensure_buffer(d, &w.realigned, a_bytes + b_bytes + c_bytes, stream)) return rc;
       uint8_t* buf = static_cast<uint8_t*>(w.realigned.ptr);
       RealignBatch batch{};
@@ -988,7 +1010,7 @@ int sgemm_f32_device(const float* A, const float* B, float* C, int M, int N, int
       uint8_t* buf = nullptr;
       {
         std::lock_guard<std::mutex> lk(g_mu);
-        StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
+        StreamWs& w = d->ws[stream_key(stream)];
         if (int rc = ensure_buffer(d, &w.split, need, stream)) return rc;
         buf = static_cast<uint8_t*>(w.split.ptr);
       }
@@ -1261,7 +1283,7 @@ int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed,
   DevState* d = nullptr;
   if (int rc = device_state(&d, nullptr)) return rc;
   std::lock_guard<std::mutex> lk(g_mu);
-  StreamWs& w = d->ws[reinterpret_cast<uintptr_t>(stream)];
+  StreamWs& w = d->ws[stream_key(stream)];
   if (int rc = ensure_buffer(d, &w.routed, bytes, stream)) return rc;
   *out = w.routed.ptr;
   if (zeroed) {

@@ -1,5 +1,7 @@
 """The library's scratch under programs that share it: graphs captured on a
 stream beside larger calls on it, and host threads on one stream."""
+import threading
+
 import pytest
 
 from helpers import torch
@@ -21,18 +23,19 @@ def lora_call(t, M, N, K, R, n, seed, grad=False):
     o = {k: v.cuda() for k, v in lora_operands(t, seed, M, N, K, R, n, "mixed").items()}
     if not grad:
         C = t.full_like(o["C0"], float("nan"))
-        return (lambda: g.gemm_f16_lora(o["X"], o["W"], C, o["A"], o["B"], o["ids"], o["scales"])), [C]
+        return (lambda **k: g.gemm_f16_lora(o["X"], o["W"], C, o["A"], o["B"], o["ids"], o["scales"],
+                                            **k)), [C]
     out = [t.full_like(o["X"], float("nan")), t.full_like(o["dA0"], float("nan")),
            t.full_like(o["dB0"], float("nan"))]
-    return (lambda: g.gemm_f16_lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"],
-                                         o["scales"], *out)), out
+    return (lambda **k: g.gemm_f16_lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"],
+                                             o["scales"], *out, **k)), out
 
 
 def moe_call(t, T, H, I, E, k, seed):
     import dense_gemm_03_gb300 as g
     o = {n: v.cuda() for n, v in moe_operands(t, seed, T, H, I, E).items()}
     Y = t.full_like(o["Y0"], float("nan"))
-    return (lambda: g.gemm_f16_moe(o["X"], o["Wr"], o["W1"], o["W2"], Y, k)), [Y]
+    return (lambda **s: g.gemm_f16_moe(o["X"], o["Wr"], o["W1"], o["W2"], Y, k, **s)), [Y]
 
 
 def gemm_call(t, M, N, K, seed):
@@ -40,7 +43,7 @@ def gemm_call(t, M, N, K, seed):
     gen = t.Generator(device="cuda").manual_seed(seed)
     A, B = (t.randn(s, generator=gen, device="cuda").half() for s in ((M, K), (K, N)))
     C = t.full((M, N), float("nan"), dtype=t.float16, device="cuda")
-    return (lambda: g.gemm_f16(A, B, C)), [C]
+    return (lambda **k: g.gemm_f16(A, B, C, **k)), [C]
 
 
 KINDS = {
@@ -103,8 +106,6 @@ def test_a_graph_outlives_larger_calls_on_its_stream(kind):
 @pytest.mark.parametrize("kind", ["decode", "tiles", "grad", "moe", "f16", "f32"])
 def test_first_call_of_a_host_thread(kind):
     """A thread whose first use of CUDA is a call of the library."""
-    import threading
-
     import dense_gemm_03_gb300 as g
     t = torch()
     dt = t.float32 if kind == "f32" else t.float16
@@ -134,3 +135,57 @@ def test_first_call_of_a_host_thread(kind):
     assert not errors, errors
     assert g.debug_status() == 0
     assert all(t.equal(a, b) for a, b in zip(want, out))
+
+
+PER_THREAD = 2      # the handle cudaStreamPerThread
+
+
+@pytest.mark.parametrize("shared", [False])
+def test_host_threads(shared):
+    """Threads that call different operators, all on one stream or each on its
+    per-thread stream (one handle value for all of them), get the bits each call
+    gives alone; the scratch grows meanwhile."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    makers = [lambda i: lora_call(t, 8 + i, 1024, 2048, 16, 6, 100 + i),
+              lambda i: lora_call(t, 300 + 300 * i, 512, 1024, 16, 6, 110 + i, True),
+              lambda i: moe_call(t, 2 + 5 * i, 512, 256, 16, 4, 120 + i),
+              lambda i: moe_call(t, 40 + i, 1024, 512, 32, 4, 130 + i),
+              lambda i: lora_call(t, 2300, 1290, 256 + 256 * i, 16, 6, 140 + i),
+              lambda i: gemm_call(t, 300, 501, 1500 * (1 + i), 150 + i)]
+    jobs = [[m(i) for i in range(4)] for m in makers]
+    want = []
+    for calls in jobs:
+        for run, _ in calls:
+            run()
+        t.cuda.synchronize()
+        want.append([[x.clone() for x in out] for _, out in calls])
+        for _, out in calls:
+            for x in out:
+                x.fill_(float("nan"))
+    t.cuda.synchronize()
+    g.release()
+    s = t.cuda.Stream()
+    handle = s.cuda_stream if shared else PER_THREAD
+    errors, gate = [], threading.Barrier(len(jobs))
+
+    def work(calls):
+        try:
+            gate.wait()
+            for _ in range(12):
+                for run, _ in calls:
+                    run(stream=handle)
+        except Exception as e:      # reported on the main thread
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    t.cuda.synchronize()
+    assert not errors, errors
+    assert g.debug_status() == 0
+    for calls, refs in zip(jobs, want):
+        for (_, out), ref in zip(calls, refs):
+            assert all(t.equal(a, b) for a, b in zip(out, ref))
