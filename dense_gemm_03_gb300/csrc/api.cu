@@ -41,6 +41,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <mutex>
+#include <thread>
 #include <unordered_map>
 #include <vector>
 
@@ -108,6 +109,9 @@ struct DevState {
   int l2_bytes = 0;
   DeviceStatus* status = nullptr;
   std::unordered_map<StreamKey, StreamWs, StreamKeyHash> ws;
+  // held by a call from taking its scratch to its last launch (stream_call);
+  // never erased
+  std::unordered_map<StreamKey, std::recursive_mutex, StreamKeyHash> calls;
   std::vector<void*> outgrown;  // buffers that captured graphs may still use
   Buffer flush;                 // L2 flush buffer
   Buffer host_buf[3];           // staging for the host-buffer forms
@@ -184,6 +188,19 @@ int device_state(DevState** out, int* dev_out) {
   *out = &d;
   if (dev_out) *dev_out = dev;
   return GEMM_OK;
+}
+
+// Held by a call from taking its stream's scratch to its last launch: two host
+// threads on one stream would otherwise launch their kernels in between each
+// other's, over the same scratch.  Taken before g_mu, and again by a call within
+// a call.
+std::unique_lock<std::recursive_mutex> stream_call(DevState* d, cudaStream_t stream) {
+  std::recursive_mutex* m = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    m = &d->calls[stream_key(stream)];
+  }
+  return std::unique_lock<std::recursive_mutex>(*m);
 }
 
 // Grows a library-owned device buffer for a call on `stream`.  One whose address
@@ -575,6 +592,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   }
   DevState* d = nullptr;
   if (int rc = device_state(&d, nullptr)) return rc;
+  const auto call = stream_call(d, stream);
 
   if (alpha == 0.0f || K == 0) {
     t_last_path = c_f32 ? "f16f32.scale" : "f16.scale";
@@ -970,6 +988,7 @@ int sgemm_f32_device(const float* A, const float* B, float* C, int M, int N, int
   }
   DevState* d = nullptr;
   if (int rc = device_state(&d, nullptr)) return rc;
+  const auto call = stream_call(d, stream);
   if (alpha == 0.0f || K == 0) {
     t_last_path = "f32.scale";
     return launch_scale_f32(C, ldc, M, N, beta, scale_grid(*d, 1ll * M * N), stream) == cudaSuccess
@@ -1278,6 +1297,13 @@ int gemm_f16_lora_pair(const uint16_t* A, const uint16_t* B, uint16_t* C, int M,
   return gemm_f16_impl(A, B, C, false, M, N, K, lda, ldb, ldc, alpha, beta, stream, &lora);
 }
 
+int lock_stream(cudaStream_t stream, std::unique_lock<std::recursive_mutex>* call) {
+  DevState* d = nullptr;
+  if (int rc = device_state(&d, nullptr)) return rc;
+  *call = stream_call(d, stream);
+  return GEMM_OK;
+}
+
 int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed,
                    void** zeroed_out) {
   DevState* d = nullptr;
@@ -1490,7 +1516,23 @@ const char* gemm_strerror(int code) {
 
 int gemm_release(void) {
   std::lock_guard<std::mutex> host_lk(g_host_mu);
-  std::lock_guard<std::mutex> lk(g_mu);
+  // no call is between taking its scratch and its last launch (one that is may
+  // be about to take g_mu)
+  std::unique_lock<std::mutex> lk(g_mu);
+  std::vector<std::unique_lock<std::recursive_mutex>> held;
+  for (bool all = false; !all;) {
+    all = true;
+    for (DevState& d : g_dev)
+      for (auto& kv : d.calls) {
+        held.emplace_back(kv.second, std::try_to_lock);
+        all = all && held.back().owns_lock();
+      }
+    if (all) break;
+    held.clear();
+    lk.unlock();
+    std::this_thread::yield();
+    lk.lock();
+  }
   int prev = 0;
   if (cudaGetDevice(&prev) != cudaSuccess) return GEMM_ERR_CUDA;
   int rc = GEMM_OK;

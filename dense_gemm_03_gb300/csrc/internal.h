@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <mutex>
 
 namespace gb300 {
 
@@ -327,6 +328,10 @@ cudaError_t launch_sgemm_ffma(bool vec, const SgemmArgs& args, cudaStream_t stre
 // Current device: SM count, status word and wait limit (library set-up done
 // on first use).  Returns a GEMM_* code.
 int query_device(int* sm_count, DeviceStatus** status, unsigned long long* wait_limit_ns);
+
+// To be held from the first routed_scratch() of a call to its last launch.
+// Returns a GEMM_* code.
+int lock_stream(cudaStream_t stream, std::unique_lock<std::recursive_mutex>* call);
 
 // Scratch of the row-routed products (adapters, experts) on `stream`, at least
 // `bytes` long and 256-byte aligned; kept per device and stream, freed by

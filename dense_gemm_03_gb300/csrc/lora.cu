@@ -305,6 +305,8 @@ int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint1
   DeviceStatus* st = nullptr;
   unsigned long long limit = 0;
   if (int rc = query_device(&sms, &st, &limit)) return rc;
+  std::unique_lock<std::recursive_mutex> call;
+  if (int rc = lock_stream(stream, &call)) return rc;
   const LoraArgs p{X, W, A, B, ids, scales, M, N, K, R, adapters, ldx, ldw, lda, ldb};
   return forward(p, C, ldc, alpha, beta, LoraDevice{sms, st, limit}, stream);
 }
@@ -358,6 +360,8 @@ int gemm_f16_lora_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W,
     }
     return GEMM_OK;
   }
+  std::unique_lock<std::recursive_mutex> call;
+  if (int rc = lock_stream(stream, &call)) return rc;
   const LoraArgs p{X, W, A, B, ids, scales, M, N, K, R, adapters, ldx, ldw, lda, ldb};
   const LoraDevice d{sms, st, limit};
   if (!grads) return plain_dx(p, dC, lddc, dX, lddx, alpha, d, stream);

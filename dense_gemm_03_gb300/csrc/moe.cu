@@ -192,6 +192,8 @@ extern "C" int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_
   DeviceStatus* st = nullptr;
   unsigned long long limit = 0;
   if (int rc = query_device(&sms, &st, &limit)) return rc;
+  std::unique_lock<std::recursive_mutex> call;
+  if (int rc = lock_stream(stream, &call)) return rc;
   const MoeArgs m{X, Wr, W1, W2, Y, ids, probs, T, H, I, E, topk, renormalize, ldx, ldy, beta};
   return moe_stream_fits(m) ? moe_stream(m, sms, st, limit, stream) : moe_any(m, sms, stream);
 }

@@ -39,6 +39,9 @@
  *   Streams    work is enqueued on `stream` (NULL = the legacy default
  *              stream) and the call returns without synchronising.  Calls on
  *              different streams that write the same C race.
+ *   Threads    any host threads may call at any time, also on one stream (the
+ *              kernels of a call stay together there) or each on its
+ *              cudaStreamPerThread.
  *   Scratch    some shapes split K over several thread blocks and need an
  *              fp32 workspace (few tiles with a long K: stream-K for half
  *              operands, K slices for fp32 ones; the forced split paths);

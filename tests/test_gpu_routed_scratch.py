@@ -140,7 +140,7 @@ def test_first_call_of_a_host_thread(kind):
 PER_THREAD = 2      # the handle cudaStreamPerThread
 
 
-@pytest.mark.parametrize("shared", [False])
+@pytest.mark.parametrize("shared", [True, False])
 def test_host_threads(shared):
     """Threads that call different operators, all on one stream or each on its
     per-thread stream (one handle value for all of them), get the bits each call
@@ -189,3 +189,32 @@ def test_host_threads(shared):
     for calls, refs in zip(jobs, want):
         for (_, out), ref in zip(calls, refs):
             assert all(t.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_release_beside_calls():
+    """gemm_release() waits for calls in progress on other threads, and they go
+    on after it."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    run, out = lora_call(t, 16, 512, 1024, 16, 4, 160)
+    run()
+    t.cuda.synchronize()
+    want = out[0].clone()
+    s, stop, errors = t.cuda.Stream(), threading.Event(), []
+
+    def work():
+        try:
+            while not stop.is_set():
+                run(stream=s.cuda_stream)
+        except Exception as e:
+            errors.append(repr(e))
+
+    th = threading.Thread(target=work)
+    th.start()
+    for _ in range(20):
+        g.release()
+    stop.set()
+    th.join()
+    t.cuda.synchronize()
+    assert not errors, errors
+    assert g.debug_status() == 0 and t.equal(want, out[0])
