@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       reinterpret_cast<uint32_t*>(base_ptr + (kSmem - 1024 + 15) / 16 * 16);
   int* const s_prefix = reinterpret_cast<int*>(s_mask + words);
   const int warp = warp_id_uniform(), lane = static_cast<int>(lane_id());
-  griddep_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -104,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tmem_alloc(smem_addr(misc), kTmemCols);
     tmem_relinquish();
+    griddep_launch_dependents();
   }
   for (int i = threadIdx.x; i < words; i += kThreads) s_mask[i] = 0u;
   __syncthreads();

@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       prefetch_tensormap(&tmF1);
     }
   }
-  griddep_launch_dependents();
   const int b = blockIdx.x;
+  if (b >= p.first_list) griddep_launch_dependents();
   if (b >= p.first_check) {
     // ---- a quarter of an adapter: are its weights finite (if a row uses it)
     const int check = b - p.first_check, adapter = check / kLoraBadParts;
@@ -241,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_ptr), G::kTmemCols);
     tmem_relinquish();
+    // only now: the next kernel holds its tensor memory until this one ends
+    griddep_launch_dependents();
   }
   const int n = distinct(p.ids + row0, rows, p.adapters, s_list, s_slot, s_first, s_cnt);
   tc_fence_before();

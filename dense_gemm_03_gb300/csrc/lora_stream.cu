@@ -79,7 +79,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   const uint32_t done_bar = bars + 8u * (2 * kMaxStages + 4);
   constexpr int kBars = 2 * kMaxStages + 5;
   uint8_t* const tmem_ptr = base_ptr + static_cast<size_t>(S) * p.stage_bytes + 8 * kBars;
-  griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1u);
@@ -98,6 +97,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   if (warp == 1) {
     tmem_alloc(smem_addr(tmem_ptr), 2 * p.acc_cols);
     tmem_relinquish();
+    // only now: a kernel after the next one (the sums) allocates tensor memory and
+    // holds it until this one ends
+    griddep_launch_dependents();
   }
   tc_fence_before();
   __syncthreads();
