@@ -109,7 +109,7 @@ struct LoraRowsJob {
   long long ldf, f_stride;
   int k_major;
   float* V;
-  int ranks;              // of F where k_major (0: R)
+  int ranks;              // of F; V's other columns are zero
 };
 struct LoraRows {
   LoraRowsJob job[2];

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraRows p) {
   if (threadIdx.x < p.R) {
     float s = 0.0f;
     for (int t = 0; t < parts; ++t) s += red2[t * p.R + threadIdx.x];
-    out[threadIdx.x] = scale * s;
+    out[threadIdx.x] = static_cast<int>(threadIdx.x) < job.ranks ? scale * s : 0.0f;
   }
 }
 
@@ -172,13 +172,10 @@ int slices_of(const LoraShrinkPlan& p, int sms) {
 }  // namespace
 
 cudaError_t launch_lora_rows(const LoraRows& p, cudaStream_t stream) {
-  LoraRows q = p;
-  for (int j = 0; j < q.njobs; ++j)
-    if (q.job[j].ranks == 0) q.job[j].ranks = q.R;
   if (p.njobs == 1 && !p.job[0].k_major)
-    lora_rows_kernel<true><<<p.M * p.slices, kThreads, 0, stream>>>(q);
+    lora_rows_kernel<true><<<p.M * p.slices, kThreads, 0, stream>>>(p);
   else
-    lora_rows_kernel<false><<<p.M * p.slices * p.njobs, kThreads, 0, stream>>>(q);
+    lora_rows_kernel<false><<<p.M * p.slices * p.njobs, kThreads, 0, stream>>>(p);
   return counted_launch(cudaGetLastError());
 }
 

@@ -393,10 +393,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (mine == j)
 #pragma unroll
             for (int r = 0; r < RP; r += 4)
-              if (r < p.ldv)
+              if (r < p.ldv) {
+                // the ranks past R are products with zeros, which an Inf or NaN
+                // of x makes NaN
+                auto value = [&](int i) { return i < p.R ? s * acc[j * RP + i] : 0.0f; };
                 *reinterpret_cast<float4*>(out + r) =
-                    make_float4(s * acc[j * RP + r], s * acc[j * RP + r + 1],
-                                s * acc[j * RP + r + 2], s * acc[j * RP + r + 3]);
+                    make_float4(value(r), value(r + 1), value(r + 2), value(r + 3));
+              }
       }
     }
   }

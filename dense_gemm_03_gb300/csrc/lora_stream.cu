@@ -627,7 +627,7 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
     float* const v = reinterpret_cast<float*>(rest);
     rest += lora_round256(4 * static_cast<size_t>(p.M) * slices * r8);
     LoraRows rows{};
-    rows.job[0] = LoraRowsJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride, 0, v};
+    rows.job[0] = LoraRowsJob{p.X, p.ldx, p.K, p.A, p.lda, p.a_stride, 0, v, p.R};
     rows.njobs = 1;
     rows.slices = slices;
     rows.ids = p.ids;

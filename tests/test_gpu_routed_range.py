@@ -1,0 +1,51 @@
+"""The range of the row-routed products' intermediates: V, U and the gated rows
+past the half range and far below it, adapters of very different magnitude side
+by side, and infinities, which come out as the formula gives them.
+
+u = 2^-24 as in routed_ref.  An intermediate is kept to 2^-22 of itself or, of
+the largest entry of its row, to 2^-14 (LoRA's V and U on CTA pairs), or of
+the largest entry of the rows or columns that share a scale to 2^-37 (two halves
+whose sum is scaled so that the largest lies in [2^13, 2^14): steps of 2^-24)."""
+import pytest
+
+import routed_ref as ref
+from helpers import torch
+from test_gpu_lora import dev, operands, sync
+from test_gpu_moe import operands as moe_operands
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from dense_gemm_03_gb300 import build
+    build.build()
+
+
+# tiles, chunks with V by the shrink, chunks with V by rows
+LORA_SIZES = [(2300, 1288, 1100, "tiles"), (1300, 264, 320, "stream"), (300, 264, 320, "stream"),
+              (40, 264, 320, "stream")]
+
+
+@pytest.mark.parametrize("M,N,K,path", LORA_SIZES)
+@pytest.mark.parametrize("R", [6, 33, 64])
+def test_ranks_past_the_last_stay_zero(M, N, K, path, R):
+    """A row of X with an infinity, all weights positive: every output of the row
+    is +Inf, whatever the rank is padded to."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M + R, M, N, K, R, 3, "mixed")
+    o["ids"][[3, 17]] = 1
+    for k in "WAB":
+        o[k] = o[k].abs() + 2.0 ** -10
+    o["X"][3, 7], o["G"][17, 5] = float("inf"), float("inf")
+    v = dev(o)
+    C, dX = t.empty_like(v["C0"]), t.empty_like(v["X"])
+    g.gemm_f16_lora(v["X"], v["W"], C, v["A"], v["B"], v["ids"], v["scales"])
+    assert path in g.last_path()
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], dX)
+    assert path in g.last_path()
+    sync(t)
+    assert (C[3] == float("inf")).all() and (dX[17] == float("inf")).all()
+    C[3], dX[17] = 0.0, 0.0
+    assert C.isfinite().all() and dX.isfinite().all()
