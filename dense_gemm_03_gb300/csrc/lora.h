@@ -161,6 +161,10 @@ __device__ __forceinline__ void lora_store_split(uint16_t* o, float4 v) {
   *reinterpret_cast<uint2*>(o + 32) = make_uint2(b[2], b[3]);
 }
 
+// The two halves' products with the same factors.  Where those hold an infinity
+// the hi part is the result; lo, of either sign or zero, would make it NaN.
+__device__ __forceinline__ float lora_join(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
+
 // The power of two that brings a largest finite magnitude `top` into [2^13,
 // 2^14): its exponent, at most 100 either way, so that it and its inverse are
 // normal.

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(acce_bar(buf));
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          acc[i] = fmaf(__uint_as_float(hi[i]) + __uint_as_float(lo[i]), down, acc[i]);
+          acc[i] = fmaf(lora_join(__uint_as_float(hi[i]), __uint_as_float(lo[i])), down, acc[i]);
       }
       if (!ok) break;
       const int C = t.src ? p.cols_g : p.cols_x, r0 = 32 * t.chunk, nr = min(32, p.R - r0);

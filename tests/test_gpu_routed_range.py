@@ -22,6 +22,15 @@ def _built():
     build.build()
 
 
+def same_where_not_finite(got, want, what=""):
+    """got has want's infinities and NaN, and is finite elsewhere."""
+    t = torch()
+    got, want = got.double(), want.double()
+    fin = want.isfinite()
+    assert t.equal(got.isfinite(), fin), "%s: finite in other places" % what
+    assert t.equal(got[~fin].nan_to_num(0.0, 1.0, -1.0), want[~fin].nan_to_num(0.0, 1.0, -1.0)), what
+
+
 # tiles, chunks with V by the shrink, chunks with V by rows
 LORA_SIZES = [(2300, 1288, 1100, "tiles"), (1300, 264, 320, "stream"), (300, 264, 320, "stream"),
               (40, 264, 320, "stream")]
@@ -49,3 +58,25 @@ def test_ranks_past_the_last_stay_zero(M, N, K, path, R):
     assert (C[3] == float("inf")).all() and (dX[17] == float("inf")).all()
     C[3], dX[17] = 0.0, 0.0
     assert C.isfinite().all() and dX.isfinite().all()
+
+
+@pytest.mark.parametrize("M,N,K,n", [(2300, 1288, 1096, 4), (300, 264, 320, 4), (49, 333, 777, 29)])
+def test_infinite_entries_in_gradients(M, N, K, n):
+    """An infinity in a row of X or of dC: dA and dB are infinite or NaN where
+    the formula is (a part of U or V that is zero must not make it NaN)."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M + N, M, N, K, 16, n, "mixed")
+    o["ids"][[3, 17]] = t.tensor([1, 2], dtype=t.int32)
+    o["X"][3, 7], o["G"][17, 5] = float("inf"), float("-inf")
+    v = dev(o)
+    dA, dB = t.empty_like(v["dA0"]), t.empty_like(v["dB0"])
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], None, dA, dB)
+    sync(t)
+    r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0,
+                      o["dA0"], o["dB0"])
+    for name, got in (("dA", dA), ("dB", dB)):
+        want, tol = r[name]
+        same_where_not_finite(got.cpu(), want, name)
+        fin = want.isfinite()
+        ref.check(got.cpu()[fin], want[fin], tol[fin], name)
