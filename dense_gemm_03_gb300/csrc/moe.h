@@ -34,6 +34,10 @@ __device__ __forceinline__ uint16_t moe_f2h(float x) {
   return __half_as_ushort(__float2half_rn(x));
 }
 
+// The two halves' products with the same weights.  Where those hold an infinity
+// the hi part is the result; lo, of either sign or zero, would make it NaN.
+__device__ __forceinline__ float moe_join(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
+
 // Order-preserving key of a float: larger floats have larger keys, -0 and +0
 // the same one, NaN the largest.
 __device__ __forceinline__ uint32_t order_key(float x) {

@@ -615,8 +615,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
           for (int i = 0; i < 8; ++i)
             if (r0 + i < n) {
               float* o = a.z + (static_cast<long long>(off + r0 + i) * w.down_chunks + t.c) * a.H;
-              if (c0 < a.H) __stcg(o + c0, v0[i] + __uint_as_float(g[i]));
-              if (c0 + 128 < a.H) __stcg(o + c0 + 128, v1[i] + __uint_as_float(h[i]));
+              if (c0 < a.H) __stcg(o + c0, moe_join(v0[i], __uint_as_float(g[i])));
+              if (c0 + 128 < a.H) __stcg(o + c0 + 128, moe_join(v1[i], __uint_as_float(h[i])));
             }
         } else if (w.up_chunks == 1) {
           store_hid(r0, v0, v1);

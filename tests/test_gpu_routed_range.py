@@ -80,3 +80,52 @@ def test_infinite_entries_in_gradients(M, N, K, n):
         same_where_not_finite(got.cpu(), want, name)
         fin = want.isfinite()
         ref.check(got.cpu()[fin], want[fin], tol[fin], name)
+
+
+def moe_exact(o, topk):
+    """(Y, tol) of the renormalised layer with the gated rows kept to 2^-22 of
+    themselves or 2^-37 of a row's largest."""
+    t = torch()
+    X, Wr = o["X"].double(), o["Wr"].double()
+    T, H = X.shape
+    I = o["W2"].shape[1]
+    l = X @ Wr
+    dl = ((H + 8) * ref.U2 * (X.abs() @ Wr.abs())).amax(1)
+    ids = t.sort(l, dim=1, descending=True, stable=True).indices[:, :topk]
+    p = t.gather(t.softmax(l, dim=1), 1, ids)
+    p = p / p.sum(1, keepdim=True)
+    Y, tol = t.zeros(T, H, dtype=t.float64), t.zeros(T, H, dtype=t.float64)
+    for i in range(T):
+        for k in range(topk):
+            w1, w2 = o["W1"][ids[i, k]].double(), o["W2"][ids[i, k]].double()
+            gu, terms = X[i] @ w1, X[i].abs() @ w1.abs()
+            g, u = gu[:I], gu[I:]
+            e = (H + 8) * ref.U2 * terms
+            s = g * t.sigmoid(g)
+            h = s * u
+            eh = 1.1 * e[:I] * (u.abs() + e[I:]) + s.abs() * e[I:] + 2.0 ** -20 * h.abs()
+            eh = eh + 2.0 ** -22 * h.abs() + 2.0 ** -37 * h.abs().max()
+            ep = p[i, k] * (4 * dl[i] + 2.0 ** -20 + Wr.shape[1] * ref.U2)
+            Y[i] += p[i, k] * (h @ w2)
+            th = h.abs() @ w2.abs()
+            tol[i] += p[i, k] * (eh @ w2.abs() + (I + topk + 8) * ref.U2 * th) + ep * th
+    return ids, Y, tol + ref.HALF * Y.abs() + ref.TINY
+
+
+@pytest.mark.parametrize("H,I", [(256, 192), (257, 129)])
+def test_moe_infinite_weights(H, I):
+    """Infinities in W2: the tokens of that expert are infinite or NaN where the
+    formula is."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    T, E, topk = 9, 4, 2
+    o = moe_operands(t, 81, T, H, I, E)
+    o["W2"][1, 5, 7], o["W2"][2, I - 1, H - 1] = float("inf"), float("-inf")
+    v = {k: x.cuda() for k, x in o.items()}
+    Y = t.empty_like(v["Y0"])
+    g.gemm_f16_moe(v["X"], v["Wr"], v["W1"], v["W2"], Y, topk)
+    sync(t)
+    _, want, tol = moe_exact(o, topk)
+    same_where_not_finite(Y.cpu(), want)
+    fin = want.isfinite()
+    ref.check(Y.cpu()[fin], want[fin], tol[fin])
