@@ -70,7 +70,7 @@ struct LoraShrinkJob {
   int want;               // kLoraPacked, kLoraScaled
   float* V;               // out: [M][ldv]
   // out: V as hi and lo halves, [M][chunk of 32 ranks][32 hi, 32 lo]; scaled by
-  // a power of two per 128 rows, whose inverses are unscale[]
+  // a power of two for each adapter of 128 rows, whose inverses are unscale[M]
   uint16_t *packed, *scaled;
   float* unscale;
   int tiles;
@@ -166,10 +166,20 @@ __device__ __forceinline__ void lora_store_split(uint16_t* o, float4 v) {
 __device__ __forceinline__ float lora_join(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }
 
 // The power of two that brings a largest finite magnitude `top` into [2^13,
-// 2^14): its exponent, at most 100 either way, so that it and its inverse are
-// normal.
+// 2^14): its exponent, at most 126 either way, so that it and its inverse are
+// normal (below 2^-112 the largest scaled magnitude is less, and has bits enough).
 __device__ __forceinline__ int lora_scale_exponent(float top) {
-  return top > 0.0f ? max(-100, min(100, 13 - ilogbf(top))) : 0;
+  return top > 0.0f ? max(-126, min(126, 13 - ilogbf(top))) : 0;
+}
+__device__ __forceinline__ float lora_power(int e) { return __int_as_float((127 + e) << 23); }
+// The largest finite magnitude of four, as bits that order like it.
+__device__ __forceinline__ unsigned int lora_top_bits(float4 v) {
+  const float m[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (m[j] < __int_as_float(0x7F800000)) top = fmaxf(top, m[j]);
+  return __float_as_uint(top);
 }
 
 inline size_t lora_round256(size_t x) { return (x + 255) / 256 * 256; }

@@ -12,9 +12,10 @@
 // lora_outer_sum_kernel adds up in row order; up to 512 rows in all (one range)
 // they write the gradients themselves (256 x 1024 x 1024: 23.4 -> 22.0 us).
 //
-// U and V come scaled by a power of two per 128 rows (lora_shrink.cu); 64 rows
-// are what is summed in TMEM (the tensor cores truncate, see there), and the
-// scale is taken back as those sums are added up in registers.
+// U and V come scaled by a power of two for each adapter of 128 rows
+// (lora_shrink.cu); 64 rows are what is summed in TMEM (the tensor cores
+// truncate, see there), and the scale is taken back as those sums are added up in
+// registers.
 //
 // Rows of other adapters in a block have zeros for U (V), and their part of X
 // (dC) is overwritten by zeros in shared memory, so that an Inf or NaN there
@@ -36,11 +37,15 @@ constexpr int kTmemCols = 256;               // two buffers of two 64-column acc
 constexpr int kMaxMasks = kLoraMaxAdapters;  // ranges x adapters of a launch
 constexpr int kGroupMasks = 32;              // masks per entry of the prefix
 constexpr int kBars = 3 * kStages + 5;
-constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * kBars + 8;
+constexpr int kScales = 16;                  // blocks' scales on their way to the epilogue
+// (a loader writes one before it waits for the block's stage: four blocks on from
+// one whose stage was free, while the epilogue has two left)
+static_assert(kScales >= kLoaders + kStages + 2, "places of scales still to be read");
+constexpr int kSmem = 1024 + kStages * kStageBytes + 8 * kBars + 8 + 4 * kScales;
 static_assert(kSmem + 16 + kMaxMasks + kMaxMasks / 8 + 64 <= 232448, "shared memory budget");
 
 struct Args {
-  const float *unscale_u, *unscale_v;   // by 128 rows
+  const float *unscale_u, *unscale_v;   // by row
   int cols_x, cols_g, tiles_x, tiles_g;   // of X and dC, 256-column tiles (0: not wanted)
   const int* ids;
   int M, R, adapters, chunks, ranges, row0;
@@ -77,6 +82,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t done_bar = bars + 8u * (3 * kStages + 4);
   uint8_t* const tail = base_ptr + kStages * kStageBytes + 8 * kBars;
   uint32_t* const misc = reinterpret_cast<uint32_t*>(tail);            // TMEM address, present
+  volatile float* const s_down = reinterpret_cast<float*>(misc + 2);   // [kScales], by block
   // [range][adapter] bytes: the 64-row blocks with the adapter; then, per 32 of
   // them, how many nonzero ones come before
   const int nmask = p.ranges * p.adapters;
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(empty_bar(s), 1u);
     }
     for (uint32_t b = 0; b < 2; ++b) {
-      mbar_init(accf_bar(b), 1u);
+      mbar_init(accf_bar(b), 2u);   // the products, and the MMA thread for the scale
       mbar_init(acce_bar(b), static_cast<uint32_t>(kEpi));
     }
     mbar_init(done_bar, 1u);
@@ -260,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit(empty_bar(stage));
           mma_commit(accf_bar(buf));
+          mbar_arrive(accf_bar(buf));
           ++local;
           if (++stage == kStages) {
             stage = 0;
@@ -272,8 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp < 2 + kLoaders) {
-    // Warp l of these takes the blocks l, l + 4, ... of the CTA's sequence and
-    // clears the rows of other adapters (a lane has two rows).
+    // Warp l of these takes the blocks l, l + 4, ... of the CTA's sequence, clears
+    // the rows of other adapters (a lane has two rows) and hands on the scale of
+    // the adapter's rows, which is that of the first of them.
     const int l = warp - 2;
     int stage = 0;
     uint32_t phase = 0, seq = 0;
@@ -286,6 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool f0 = row < p.M && __ldg(p.ids + row) != t.a;
           const bool f1 = row + 32 < p.M && __ldg(p.ids + row + 32) != t.a;
           const bool mixed = __any_sync(0xffffffffu, f0 || f1);
+          const unsigned int own0 = __ballot_sync(0xffffffffu, row < p.M && !f0);
+          const unsigned int own1 = __ballot_sync(0xffffffffu, row + 32 < p.M && !f1);
+          if (lane == 0)
+            s_down[seq % kScales] =
+                __ldg((t.src ? p.unscale_v : p.unscale_u) + row +
+                      (own0 ? __ffs(own0) - 1 : 31 + __ffs(own1)));
           // a block of one adapter only passes through, but not before its stage
           // is free: two arrivals in one phase would hide one from the MMA warp
           if (lane == 0)
@@ -332,8 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const int blk = t.range * (kRange / 64) + __ffs(m) - 1;
-        const float down = __ldg((t.src ? p.unscale_v : p.unscale_u) + (p.row0 / 64 + blk) / 2);
+        const float down = s_down[local % kScales];
         const uint32_t d0 =
             tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * 128 + half * 64;
         uint32_t hi[32], lo[32];

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kThreads) lora_rows_kernel(const LoraRows p) {
 }
 
 struct PackArgs {
+  const int* ids;
   const float* part[2];    // [row][slice][r8]
   float* V[2];             // [row][ldv]
   uint16_t* scaled[2];     // may be NULL
@@ -115,16 +116,22 @@ struct PackArgs {
 constexpr int kPackThreads = 512;
 
 __global__ void __launch_bounds__(kPackThreads) lora_pack_kernel(const PackArgs p) {
-  __shared__ float s_top[kPackThreads / 32];
+  __shared__ int s_ids[128], s_exp[128];
+  __shared__ unsigned int s_top[128];   // by row: largest finite magnitude
   griddep_launch_dependents();
   const int which = blockIdx.y, row0 = blockIdx.x * 128, rows = min(128, p.M - row0);
   const float* const part = (which ? p.part[1] : p.part[0]) +
                             static_cast<long long>(row0) * p.slices * p.r8;
   float* const V = (which ? p.V[1] : p.V[0]) + static_cast<long long>(row0) * p.ldv;
   uint16_t* const scaled = which ? p.scaled[1] : p.scaled[0];
+  float* const unscale = (which ? p.unscale[1] : p.unscale[0]) + row0;
+  for (int i = threadIdx.x; i < rows; i += kPackThreads) {
+    s_ids[i] = __ldg(p.ids + row0 + i);
+    s_top[i] = 0u;
+  }
+  __syncthreads();
   griddep_wait();
   const int per = p.ldv / 4;
-  float top = 0.0f;
   for (int i = threadIdx.x; i < rows * per; i += kPackThreads) {
     const int r = i / per, q = i - r * per;
     const float* src = part + static_cast<long long>(r) * p.slices * p.r8 + 4 * q;
@@ -138,26 +145,34 @@ __global__ void __launch_bounds__(kPackThreads) lora_pack_kernel(const PackArgs 
       v.w += t.w;
     }
     reinterpret_cast<float4*>(V)[i] = v;
-    const float m[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (m[j] < __int_as_float(0x7F800000)) top = fmaxf(top, m[j]);
+    if (scaled) atomicMax(s_top + r, lora_top_bits(v));
   }
   if (!scaled) return;
-  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
   __syncthreads();
-  for (int w = 0; w < kPackThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-  const int e = lora_scale_exponent(top);
-  const float up = __int_as_float((127 + e) << 23);
-  if (threadIdx.x == 0)
-    (which ? p.unscale[1] : p.unscale[0])[blockIdx.x] = __int_as_float((127 - e) << 23);
+  // a row's scale goes by the largest magnitude of all rows of its adapter here:
+  // four threads a row, each a quarter of the rows
+  static_assert(kPackThreads == 4 * 128, "four threads a row");
+  {
+    const int r = threadIdx.x >> 2;
+    unsigned int top = 0u;
+    if (r < rows)
+      for (int i = threadIdx.x & 3; i < rows; i += 4)
+        if (s_ids[i] == s_ids[r]) top = max(top, s_top[i]);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    if (r < rows && (threadIdx.x & 3) == 0) {
+      s_exp[r] = lora_scale_exponent(__uint_as_float(top));
+      unscale[r] = lora_power(-s_exp[r]);
+    }
+  }
+  __syncthreads();
   // eight threads a row and chunk, four ranks each
   const int q = threadIdx.x & 7;
   for (int i = threadIdx.x >> 3; i < rows * p.chunks; i += kPackThreads / 8) {
     const int r = i / p.chunks, c = i - r * p.chunks, piece = 8 * c + q;
     const float4 v = piece < per ? reinterpret_cast<const float4*>(V)[r * per + piece]
                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float up = lora_power(s_exp[r]);
     lora_store_split(scaled + ((static_cast<long long>(row0) + r) * p.chunks + c) * 64 + 4 * q,
                      make_float4(up * v.x, up * v.y, up * v.z, up * v.w));
   }
@@ -213,6 +228,7 @@ int lora_rows(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStream_
   rows.R = r8;
   rows.adapters = p.adapters;
   PackArgs k{};
+  k.ids = p.ids;
   k.M = p.M;
   k.slices = rows.slices;
   k.r8 = r8;
@@ -227,7 +243,7 @@ int lora_rows(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStream_
     job.tiles = tiles;
     if (job.want & kLoraScaled) {
       job.scaled = reinterpret_cast<uint16_t*>(take(2 * 64 * static_cast<size_t>(k.chunks) * p.M));
-      job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(tiles)));
+      job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(p.M)));
     }
     k.part[j] = part;
     k.V[j] = job.V;

@@ -14,8 +14,9 @@
 // same step writes V as the tensor cores take it: two halves per entry, hi + lo
 // (22 significant bits or 2^-25), 32 ranks' hi and then their lo as 64 columns, so that
 // the kernels after this one load it by TMA.  For the adapters' gradients it is
-// first scaled, 128 rows at a time, by the power of two that brings its largest
-// finite magnitude into [2^13, 2^14): gradients of any size keep their bits.
+// first scaled, each adapter of the 128 rows by itself, by the power of two that
+// brings its largest finite magnitude into [2^13, 2^14): gradients of any size
+// keep their bits, whatever the rows of other adapters hold.
 //
 // The tensor cores truncate when they add to an fp32 accumulator, by up to
 // 2^-23 of it per 16 products of K, always toward zero.  The gradients of the
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                           const __grid_constant__ CUtensorMap tmF1, const Args p) {
   using G = Cfg<RP>;
   __shared__ int s_first[256], s_list[256], s_slot[256], s_cnt[10];
-  __shared__ float s_top[kThreads / 32 + 1];
+  __shared__ unsigned int s_top[128];   // by slot: largest finite magnitude
   if (threadIdx.x == 0) {
     prefetch_tensormap(&tmX0);
     prefetch_tensormap(&tmF0);
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // only now: the next kernel holds its tensor memory until this one ends
     griddep_launch_dependents();
   }
+  if (job.scaled && threadIdx.x < 128) s_top[threadIdx.x] = 0u;
   const int n = distinct(p.ids + row0, rows, p.adapters, s_list, s_slot, s_first, s_cnt);
   tc_fence_before();
   __syncthreads();
@@ -412,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   float4* const vout =
       reinterpret_cast<float4*>(job.V + (static_cast<long long>(row0) + r0) * p.ldv);
   const uint32_t sums_addr = base + p.ring + r0 * p.ldv * 4;
-  float top = 0.0f;
   for (int i = threadIdx.x; i < total; i += kThreads) {
     float4 t[kMaxSlices];
 #pragma unroll
@@ -429,28 +430,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     mine[i] = v;
     vout[i] = v;
-    const float m[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (m[j] < __int_as_float(0x7F800000)) top = fmaxf(top, m[j]);
   }
-  top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-  float up = 1.0f;
+  int* const s_exp = s_first;   // by slot: the exponent of its scale
   if (job.scaled) {
-    if (threadIdx.x == 0) {
-      for (int w = 1; w < kThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-      s_top[kThreads / 32] = top;
+    for (int i = threadIdx.x; i < total; i += kThreads) {   // this thread's own
+      const int slot = s_slot[r0 + i / per];
+      if (slot >= 0) atomicMax(s_top + slot, lora_top_bits(mine[i]));
     }
     __syncwarp();
-    cluster_sync();   // every slice's largest magnitude is known
-    for (int k = 0; k < slices; ++k)
-      top = fmaxf(k ? top : 0.0f, ld_cluster_f(map_to_cta(smem_addr(s_top + kThreads / 32), k)));
-    const int e = lora_scale_exponent(top);
-    up = __int_as_float((127 + e) << 23);
-    if (slice == 0 && threadIdx.x == 0) job.unscale[tile] = __int_as_float((127 - e) << 23);
+    cluster_sync();   // every slice's largest magnitudes are known
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      float t[kMaxSlices], top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxSlices; ++k)
+        t[k] = k < slices ? ld_cluster_f(map_to_cta(smem_addr(s_top + i), k)) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kMaxSlices; ++k) top = fmaxf(top, t[k]);
+      s_exp[i] = lora_scale_exponent(top);
+    }
   }
+  __syncthreads();
   if (job.packed || job.scaled) {
     // eight threads a row and chunk, four ranks each
     const int q = threadIdx.x & 7, nrow = total / per;
@@ -461,8 +460,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       const long long o =
           ((static_cast<long long>(row0) + r0 + r) * p.chunks + c) * 64 + 4 * q;
       if (job.packed) lora_store_split(job.packed + o, v);
-      if (job.scaled)
+      if (job.scaled) {
+        const int slot = s_slot[r0 + r], e = slot < 0 ? 0 : s_exp[slot];
+        const float up = lora_power(e);
         lora_store_split(job.scaled + o, make_float4(up * v.x, up * v.y, up * v.z, up * v.w));
+        if (c == 0 && q == 0) job.unscale[row0 + r0 + r] = lora_power(-e);
+      }
     }
   }
   tc_fence_after();
@@ -530,7 +533,7 @@ size_t lora_shrink_bytes(const LoraShrinkPlan& p) {
     const size_t packed = lora_round256(2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M);
     if (p.job[j].want & kLoraPacked) n += packed;
     if (p.job[j].want & kLoraScaled)
-      n += packed + lora_round256(4 * static_cast<size_t>((p.M + 127) / 128));
+      n += packed + lora_round256(4 * static_cast<size_t>(p.M));
   }
   return n;
 }
@@ -580,7 +583,7 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStrea
     if (job.want & kLoraPacked) job.packed = reinterpret_cast<uint16_t*>(take(packed));
     if (job.want & kLoraScaled) {
       job.scaled = reinterpret_cast<uint16_t*>(take(packed));
-      job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(tiles)));
+      job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(p.M)));
     }
     if (int rc = encode_map_f16(&maps[2 * j], job.x, p.M, job.C, job.ldx, 64, 128)) return rc;
     if (int rc = job.k_major ? encode_map_f16_stack(&maps[2 * j + 1], job.F, p.R, job.C, job.ldf,

@@ -82,6 +82,43 @@ def test_infinite_entries_in_gradients(M, N, K, n):
         ref.check(got.cpu()[fin], want[fin], tol[fin], name)
 
 
+@pytest.mark.parametrize("M,N,K,n", [(2300, 1288, 1096, 4), (1100, 264, 320, 6), (300, 264, 320, 4),
+                                     (49, 333, 777, 29)])
+def test_adapters_of_different_magnitude(M, N, K, n):
+    """Neighbouring rows whose adapters' scales are 2^-60 to 2^60: each adapter's
+    gradients within its own bound."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, M + 3 * N, M, N, K, 16, n, "mixed")
+    o["scales"] = t.tensor([2.0 ** (-60 + 120 * i / (n - 1)) for i in range(n)])
+    v = dev(o)
+    dA, dB = t.empty_like(v["dA0"]), t.empty_like(v["dB0"])
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], None, dA, dB)
+    sync(t)
+    r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0,
+                      o["dA0"], o["dB0"])
+    ref.check(dA.cpu(), *r["dA"], what="dA")
+    ref.check(dB.cpu(), *r["dB"], what="dB")
+
+
+@pytest.mark.parametrize("exponent", [-120, -40, 100])
+def test_gradients_of_any_magnitude(exponent):
+    """U and V from 2^-120 to 2^100 (fp32's range, not half's)."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = operands(t, 300 + exponent, 300, 264, 320, 16, 4, "mixed")
+    o["scales"] = t.full((4,), 2.0 ** exponent)
+    v = dev(o)
+    dA, dB = t.empty_like(v["dA0"]), t.empty_like(v["dB0"])
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], None, dA, dB)
+    sync(t)
+    r = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0,
+                      o["dA0"], o["dB0"])
+    # (below 2^-126 the results are denormal: one of their steps more)
+    ref.check(dA.cpu(), r["dA"][0], r["dA"][1] + 2.0 ** -149)
+    ref.check(dB.cpu(), r["dB"][0], r["dB"][1] + 2.0 ** -149)
+
+
 def moe_exact(o, topk):
     """(Y, tol) of the renormalised layer with the gated rows kept to 2^-22 of
     themselves or 2^-37 of a row's largest."""
