@@ -503,10 +503,10 @@ struct LoraTail {
   LoraTailArgs a;
 };
 
-__device__ __forceinline__ bool lora_bad(const LoraTailArgs& a, int e) {
+__device__ __forceinline__ int lora_marks(const LoraTailArgs& a, int e) {
   static_assert(kLoraBadParts == 4, "one 16-byte load");
   const int4 b = *(reinterpret_cast<const int4*>(a.bad) + e);
-  return (b.x | b.y | b.z | b.w) != 0;
+  return b.x | b.y | b.z | b.w;
 }
 
 template <int BN, int LOAD, int EPI, bool PAIR, int AM = 128, int MM = 128, int KPB = 1,
@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         // left out (the epilogue adds it)
         for (int j0 = 0; j0 < n && ok; j0 += 32) {
           const int mine = j0 + lane >= n ? -1 : j0 == 0 ? head : list[1 + j0 + lane];
-          const bool usable = mine >= 0 && !lora_bad(x.a, mine);
+          const bool usable = mine >= 0 && (lora_marks(x.a, mine) & 1) == 0;
           for (unsigned int todo = __ballot_sync(0xffffffffu, usable); todo && ok; todo &= todo - 1) {
             const int e = __shfl_sync(0xffffffffu, mine, __ffs(todo) - 1);
             if (walker)
@@ -1123,12 +1123,19 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           for (int l = 0; l < 4; ++l) prefetch_l2(part + 8 * l);
         }
       }
-      // adapters: this row's, when the epilogue has to add it
+      // adapters: this row's, when the epilogue has to add it (its weights are not
+      // all finite, or the row is past the halves' range), or what the halves of a
+      // small row left out
       int bad_e = -1;
+      bool rest_only = false;
       if constexpr (LORA::kOn) {
         if (finish && row < p.M) {
           const int e = __ldg(x.a.ids + row);
-          if (e >= 0 && e < x.a.adapters && lora_bad(x.a, e)) bad_e = e;
+          if (e >= 0 && e < x.a.adapters) {
+            const int marks = lora_marks(x.a, e), apart = x.a.apart[row];
+            rest_only = (marks & 1) == 0 && apart == 2;
+            if ((marks & 1) || apart == 1 || (rest_only && marks != 0)) bad_e = e;
+          }
         }
       }
       // C of the first sub-chunk is requested before the accumulator is ready.
@@ -1253,22 +1260,62 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             }
           }
           if constexpr (LORA::kOn) {
-            // a row whose adapter has weights that are not all finite: added here,
-            // so that no other row meets them (0 * Inf)
+            // a row whose adapter has weights that are not all finite (added here,
+            // so that no other row meets them: 0 * Inf), or whose V its halves do
+            // not hold
             if (bad_e >= 0) {
-              const float* v = x.a.V + static_cast<long long>(row) * x.a.ldv;
+              const float* const v0 = x.a.V + static_cast<long long>(row) * x.a.ldv;
+              auto v = [&](int r) {
+                const float y = v0[r];
+                if (!rest_only) return y;
+                if (!(fabsf(y) < 0x1p-11f)) return 0.0f;   // not finite: in its hi half
+                const float rest = y - __half2float(__float2half_rn(y));
+                return rest - __half2float(__float2half_rn(rest));
+              };
               const uint16_t* f = x.a.F + static_cast<long long>(bad_e) * x.a.f_stride;
-              for (int r = 0; r < x.a.R; ++r) {
-                const float vr = v[r];
+              auto add = [&](int i, float vr, uint32_t bits) {
+                cur[i] = __float_as_uint(fmaf(
+                    vr, __half2float(__ushort_as_half(static_cast<uint16_t>(bits & 0xFFFFu))),
+                    __uint_as_float(cur[i])));
+              };
+              // eight weights at a time, along the ranks or the columns
+              for (int r = 0; r < x.a.R; r += LORA::kTransB ? 8 : 1) {
+                if constexpr (LORA::kTransB) {
+                  const bool whole = r + 8 <= x.a.R;
+                  float vr[8];
 #pragma unroll
-                for (int i = 0; i < kSubCols; ++i)
-                  if (col0 + i < p.N) {
-                    const uint16_t w = LORA::kTransB
-                                           ? f[static_cast<long long>(col0 + i) * x.a.ldf + r]
-                                           : f[static_cast<long long>(r) * x.a.ldf + col0 + i];
-                    cur[i] = __float_as_uint(
-                        fmaf(vr, __half2float(__ushort_as_half(w)), __uint_as_float(cur[i])));
-                  }
+                  for (int k = 0; k < 8; ++k) vr[k] = r + k < x.a.R ? v(r + k) : 0.0f;
+#pragma unroll
+                  for (int i = 0; i < kSubCols; ++i)
+                    if (col0 + i < p.N) {
+                      const uint16_t* w = f + static_cast<long long>(col0 + i) * x.a.ldf + r;
+                      if (whole) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4*>(w));
+                        const uint32_t b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) add(i, vr[k], b[k / 2] >> (16 * (k & 1)));
+                      } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                          if (r + k < x.a.R) add(i, vr[k], w[k]);
+                      }
+                    }
+                } else {
+                  const float vr = v(r);
+                  const uint16_t* w = f + static_cast<long long>(r) * x.a.ldf + col0;
+#pragma unroll
+                  for (int i = 0; i < kSubCols; i += 8)
+                    if (col0 + i + 8 <= p.N) {
+                      const uint4 q = __ldg(reinterpret_cast<const uint4*>(w + i));
+                      const uint32_t b[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                      for (int k = 0; k < 8; ++k) add(i + k, vr, b[k / 2] >> (16 * (k & 1)));
+                    } else {
+#pragma unroll
+                      for (int k = 0; k < 8; ++k)
+                        if (col0 + i + k < p.N) add(i + k, vr, w[i + k]);
+                    }
+                }
               }
             }
           }

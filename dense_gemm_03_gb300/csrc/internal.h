@@ -110,11 +110,13 @@ constexpr int kLoraBadParts = 4;
 struct LoraTailArgs {
   const float* V;        // [M][ldv] fp32, the rows' low-rank products
   const uint16_t* packed;   // the same as halves, [M][chunk][32 hi, 32 lo]
+  const uint8_t* apart;     // [M] 1: past the half range, packed is zero and V added in
+                            // fp32; 2: what packed leaves out is, where weights are large
   int ldv;
   const int* ids;        // [M]
   const int* lists;      // [256-row block][kLoraListStride]: its distinct adapters
-  const int* bad;        // [adapters][kLoraBadParts]: nonzero when some weight of that
-                         // part of F[a] is not finite
+  const int* bad;        // [adapters][kLoraBadParts], of the weights of that part of F[a]:
+                         // 1 when some are not finite, 2 when some are large
   const uint16_t* F;     // the adapters' B operand (for the bad ones)
   long long ldf, f_stride;
   int R, adapters, chunks;   // chunks of 32 ranks

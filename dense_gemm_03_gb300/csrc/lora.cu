@@ -16,6 +16,7 @@
 //               k-blocks of its tiles
 //   dA and dB   lora_outer.cu
 // V and U are fp32; every sum is fp32; C and dX are rounded once.
+#include <cmath>
 #include <initializer_list>
 
 #include "lora.h"
@@ -117,6 +118,11 @@ LoraShrinkPlan shrink_plan(const LoraArgs& p) {
   return s;
 }
 
+// See lora_shrink.cu on rows with small entries.
+float large_weight(int R, float alpha) {
+  return 1.0f / (std::fabs(alpha) * std::sqrt(static_cast<float>(R)));
+}
+
 int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const LoraDevice& d,
             cudaStream_t stream) {
   const bool chunks = lora_stream_suits(p.M, p.N, d.sms);
@@ -139,6 +145,7 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
       s.check_stride = p.b_stride();
       s.check_rows = p.R;
       s.check_cols = p.N;
+      s.large = large_weight(p.R, alpha);
     }
     t = LoraStream{p.X, p.W, C, p.ldx, p.ldw, ldc, p.M, p.N, p.K, p.R, p.adapters, 0, p.B, p.ldb,
                    p.b_stride(), nullptr, s.ldv, p.A, p.lda, p.a_stride(), p.ids, p.scales, alpha,
@@ -165,8 +172,8 @@ int forward(LoraArgs p, uint16_t* C, int ldc, float alpha, float beta, const Lor
   }
   LoraCall call{};
   call.trans = false;
-  call.tail = LoraTailArgs{s.job[0].V, s.job[0].packed, s.ldv, p.ids, s.lists, s.bad, p.B, p.ldb, p.b_stride(),
-                           p.R, p.adapters, (p.R + 31) / 32};
+  call.tail = LoraTailArgs{s.job[0].V, s.job[0].packed, s.job[0].apart, s.ldv, p.ids, s.lists, s.bad,
+                           p.B, p.ldb, p.b_stride(), p.R, p.adapters, (p.R + 31) / 32};
   if (int rc = gemm_f16_lora_pair(p.X, p.W, C, p.M, p.N, p.K, p.ldx, p.ldw, ldc, alpha, beta, call,
                                   stream))
     return rc;
@@ -208,6 +215,7 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
       s.check_stride = p.a_stride();
       s.check_rows = p.K;
       s.check_cols = p.R;
+      s.large = large_weight(p.R, alpha);
     }
     // any address for V: the stream makes none of its own
     t = LoraStream{G, p.W, dX, ldg, p.ldw, lddx, p.M, p.K, p.N, p.R, p.adapters, 1, p.A, p.lda,
@@ -238,8 +246,8 @@ int gradients(LoraArgs p, const uint16_t* G, int ldg, uint16_t* dX, int lddx, fl
   } else if (dX) {
     LoraCall call{};
     call.trans = true;
-    call.tail = LoraTailArgs{s.job[0].V, s.job[0].packed, s.ldv, p.ids, s.lists, s.bad, p.A, p.lda, p.a_stride(),
-                             p.R, p.adapters, (p.R + 31) / 32};
+    call.tail = LoraTailArgs{s.job[0].V, s.job[0].packed, s.job[0].apart, s.ldv, p.ids, s.lists,
+                             s.bad, p.A, p.lda, p.a_stride(), p.R, p.adapters, (p.R + 31) / 32};
     if (int rc = gemm_f16_lora_pair(G, p.W, dX, p.M, p.K, p.N, ldg, p.ldw, lddx, alpha, 0.0f, call,
                                     stream))
       return rc;
@@ -274,7 +282,7 @@ int plain_dx(const LoraArgs& p, const uint16_t* G, int ldg, uint16_t* dX, int ld
   call.trans = true;
   // any mapped matrix for the adapters' tensor map: no tile reads it
   const uint16_t* const any = reinterpret_cast<const uint16_t*>(buf);
-  call.tail = LoraTailArgs{nullptr, any, 4, none, lists, nullptr, any, 8, 8, 1, 1, 1};
+  call.tail = LoraTailArgs{nullptr, any, nullptr, 4, none, lists, nullptr, any, 8, 8, 1, 1, 1};
   if (int rc = gemm_f16_lora_pair(G, p.W, dX, p.M, p.K, p.N, ldg, p.ldw, lddx, alpha, 0.0f, call,
                                   stream))
     return rc;

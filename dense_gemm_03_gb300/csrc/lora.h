@@ -72,6 +72,7 @@ struct LoraShrinkJob {
   // out: V as hi and lo halves, [M][chunk of 32 ranks][32 hi, 32 lo]; scaled by
   // a power of two for each adapter of 128 rows, whose inverses are unscale[M]
   uint16_t *packed, *scaled;
+  uint8_t* apart;         // beside packed: LoraTailArgs::apart
   float* unscale;
   int tiles;
 };
@@ -89,6 +90,7 @@ struct LoraShrinkPlan {
   const uint16_t* check;
   long long ld_check, check_stride;
   int check_rows, check_cols;
+  float large;            // magnitude past which a weight counts as large
   int *lists, *bad;       // out: LoraTailArgs::lists and bad
 };
 size_t lora_shrink_bytes(const LoraShrinkPlan& p);

@@ -13,7 +13,14 @@
 // memory and a counter, the last slice alone took 8 us to add up eight).  The
 // same step writes V as the tensor cores take it: two halves per entry, hi + lo
 // (22 significant bits or 2^-25), 32 ranks' hi and then their lo as 64 columns, so that
-// the kernels after this one load it by TMA.  For the adapters' gradients it is
+// the kernels after this one load it by TMA.  For C and dX these share an
+// accumulator with the rest of the product and so have no scale: a row with an
+// entry past the half range has zeros instead, a mark, and is added in fp32 from V.
+// One whose largest entry is below 2^-11 (2^-25 is more than 2^-14 of it) is marked
+// as well: what its halves leave out matters, and is added, only where weights are
+// large.  alpha times the sum over R ranks is then off by about alpha sqrt(R) max|F|
+// 2^-25, which is below the result's own rounding while alpha sqrt(R) max|F| <= 1.
+// For the adapters' gradients it is
 // first scaled, each adapter of the 128 rows by itself, by the power of two that
 // brings its largest finite magnitude into [2^13, 2^14): gradients of any size
 // keep their bits, whatever the rows of other adapters hold.
@@ -49,6 +56,7 @@ struct Args {
   const uint16_t* check;  // weights to look for non-finite ones in, rows x cols each
   long long ld_check, check_stride;
   int check_rows, check_cols;
+  uint32_t large;         // twice: bits of the largest half that is not large
   // blocks: items of the first job, of the second, lists, checks (the short ones
   // last: items start one to an SM)
   int first_item, first_list, first_check;
@@ -159,13 +167,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int b = blockIdx.x;
   if (b >= p.first_list) griddep_launch_dependents();
   if (b >= p.first_check) {
-    // ---- a quarter of an adapter: are its weights finite (if a row uses it)
+    // ---- a quarter of an adapter (if a row uses it): are its weights finite, are
+    // some large
     const int check = b - p.first_check, adapter = check / kLoraBadParts;
     if (adapter >= p.adapters) return;   // fills up the last cluster
     bool used = false;
 #pragma unroll 16
     for (int i = threadIdx.x; i < p.M; i += kThreads) used |= __ldg(p.ids + i) == adapter;
     int bad = 0;
+    unsigned int big = 0u;
     if (__syncthreads_or(used)) {
       const uint16_t* f = p.check + static_cast<long long>(adapter) * p.check_stride;
       const int groups = (p.check_cols + 7) / 8, part = check - adapter * kLoraBadParts;
@@ -183,14 +193,21 @@ __global__ void __launch_bounds__(kThreads, 2)
           // an exponent of all ones in either half
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) bad |= __vcmpgeu2(w[j] & 0x7FFF7FFFu, 0x7C007C00u) != 0u;
+          for (int j = 0; j < 4; ++j) {
+            bad |= __vcmpgeu2(w[j] & 0x7FFF7FFFu, 0x7C007C00u) != 0u;
+            big |= __vcmpgtu2(w[j] & 0x7FFF7FFFu, p.large);
+          }
         } else {
-          for (int j = 0; c + j < p.check_cols; ++j) bad |= (q[j] & 0x7FFFu) >= 0x7C00u;
+          for (int j = 0; c + j < p.check_cols; ++j) {
+            bad |= (q[j] & 0x7FFFu) >= 0x7C00u;
+            big |= (q[j] & 0x7FFFu) > (p.large & 0xFFFFu);
+          }
         }
       }
     }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) p.bad[check] = bad;
+    big = __syncthreads_or(big != 0u);
+    if (threadIdx.x == 0) p.bad[check] = (bad ? 1 : 0) | (big ? 2 : 0);
     return;
   }
   if (b >= p.first_list) {
@@ -459,7 +476,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           piece < per ? mine[r * per + piece] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       const long long o =
           ((static_cast<long long>(row0) + r0 + r) * p.chunks + c) * 64 + 4 * q;
-      if (job.packed) lora_store_split(job.packed + o, v);
+      if (job.packed) {
+        // the row's largest finite magnitude, by the eight threads
+        unsigned int top = 0u;
+        for (int j = q; j < per; j += 8) top = max(top, lora_top_bits(mine[r * per + j]));
+        for (int d = 4; d; d >>= 1)
+          top = max(top, __shfl_xor_sync(0xFFu << (lane & 24), top, d));
+        const float t = __uint_as_float(top);
+        const bool past = t >= 65520.0f;   // rounds to infinity
+        lora_store_split(job.packed + o, past ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : v);
+        if (c == 0 && q == 0)
+          job.apart[row0 + r0 + r] = past ? 1 : (t > 0.0f && t < 0x1p-11f ? 2 : 0);
+      }
       if (job.scaled) {
         const int slot = s_slot[r0 + r], e = slot < 0 ? 0 : s_exp[slot];
         const float up = lora_power(e);
@@ -531,7 +559,7 @@ size_t lora_shrink_bytes(const LoraShrinkPlan& p) {
   for (int j = 0; j < p.njobs; ++j) {
     n += lora_round256(4 * static_cast<size_t>(p.M) * p.ldv);
     const size_t packed = lora_round256(2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M);
-    if (p.job[j].want & kLoraPacked) n += packed;
+    if (p.job[j].want & kLoraPacked) n += packed + lora_round256(p.M);
     if (p.job[j].want & kLoraScaled)
       n += packed + lora_round256(4 * static_cast<size_t>(p.M));
   }
@@ -565,6 +593,8 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStrea
   a.check_stride = p.check_stride;
   a.check_rows = p.check_rows;
   a.check_cols = p.check_cols;
+  const uint32_t large = __half_as_ushort(__float2half_rz(std::min(p.large, 65504.0f)));
+  a.large = large * 0x10001u;
   a.wait_limit_ns = d.wait_limit_ns;
   a.status = d.status;
   a.slices = slices_of(p, d.sms);
@@ -580,7 +610,10 @@ int lora_shrink(LoraShrinkPlan& p, void* scratch, const LoraDevice& d, cudaStrea
     a.kb[j] = (job.C + 63) / 64;
     job.V = reinterpret_cast<float*>(take(4 * static_cast<size_t>(p.M) * p.ldv));
     const size_t packed = 2 * 64 * static_cast<size_t>((p.R + 31) / 32) * p.M;
-    if (job.want & kLoraPacked) job.packed = reinterpret_cast<uint16_t*>(take(packed));
+    if (job.want & kLoraPacked) {
+      job.packed = reinterpret_cast<uint16_t*>(take(packed));
+      job.apart = take(static_cast<size_t>(p.M));
+    }
     if (job.want & kLoraScaled) {
       job.scaled = reinterpret_cast<uint16_t*>(take(packed));
       job.unscale = reinterpret_cast<float*>(take(4 * static_cast<size_t>(p.M)));

@@ -166,9 +166,11 @@ int sgemm_f32_ld(const float* A, const float* B, float* C,
  *   scales   `adapters` floats on the device, or NULL for all ones
  * C is half with ldc >= N and overlaps no other operand.  Adapters of smaller
  * rank are stacked with zero columns of A and zero rows of B.  Products and
- * sums are fp32; s * X_i * A[a] is kept to 22 significant bits or 2^-25,
- * whichever is coarser (its magnitude must stay within the half range, 65504);
- * C is rounded once.
+ * sums are fp32; V_i = s * X_i * A[a] is kept to 22 significant bits or 2^-25,
+ * whichever is coarser, and in fp32 where that would show: rows with an entry
+ * past the half range (65504), and rows whose entries are all below 2^-11 when
+ * |alpha| * sqrt(R) * max|B[a]| > 1 (with large results, these rows cost more:
+ * they are added outside the tensor cores).  C is rounded once.
  * R == 0 or adapters == 0 is gemm_f16_ld; alpha == 0 and beta == 0 as there.
  */
 int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint16_t* A,
@@ -188,7 +190,10 @@ int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint1
  * be accumulated over micro-batches with beta = 1 (beta == 0: not read); an
  * adapter without rows gets beta times its old value.  dX, dA and dB may each
  * be NULL (not wanted); then operands only they read may be NULL too.  Sums
- * run in a fixed order: repeated calls are bitwise equal.
+ * run in a fixed order: repeated calls are bitwise equal.  For dX, U_i is kept
+ * like V_i above (with max|A[a]|); for dA and dB, U_i and V_i are kept to 22
+ * significant bits or 2^-37 of the largest entry of the same adapter among 128
+ * rows (rows 128 j .. 128 j + 127), whichever is coarser.
  */
 int gemm_f16_lora_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, const uint16_t* A,
                        const uint16_t* B, const int* ids, const float* scales, uint16_t* dX,

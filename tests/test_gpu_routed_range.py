@@ -2,10 +2,12 @@
 past the half range and far below it, adapters of very different magnitude side
 by side, and infinities, which come out as the formula gives them.
 
-u = 2^-24 as in routed_ref.  An intermediate is kept to 2^-22 of itself or, of
-the largest entry of its row, to 2^-14 (LoRA's V and U on CTA pairs), or of
-the largest entry of the rows or columns that share a scale to 2^-37 (two halves
-whose sum is scaled so that the largest lies in [2^13, 2^14): steps of 2^-24)."""
+u = 2^-24 as in routed_ref.  V and U on CTA pairs are kept to 2^-22 of themselves
+or 2^-25 where that is below the result's own rounding, else to 2^-14 of the
+largest entry of their row; in the sums of dA and dB, and the gated rows of the
+experts, to 2^-22 of themselves or 2^-37 of the largest entry that shares their
+scale (two halves whose sum is scaled so that the largest lies in [2^13, 2^14):
+steps of 2^-24)."""
 import pytest
 
 import routed_ref as ref
@@ -117,6 +119,117 @@ def test_gradients_of_any_magnitude(exponent):
     # (below 2^-126 the results are denormal: one of their steps more)
     ref.check(dA.cpu(), r["dA"][0], r["dA"][1] + 2.0 ** -149)
     ref.check(dB.cpu(), r["dB"][0], r["dB"][1] + 2.0 ** -149)
+
+
+def kept(V, F):
+    """The bound on V F of V's representation: 2^-22 of itself, or 2^-14 of its
+    row's largest entry below the half's normal steps (2^-25)."""
+    top = V.abs().amax(1, keepdim=True)
+    return (2.0 ** -22 * V.abs() + (2.0 ** -14 * top).clamp(max=2.0 ** -25)) @ F.abs()
+
+
+@pytest.mark.parametrize("M,N,K,path", LORA_SIZES)
+@pytest.mark.parametrize("up", [20, 9, 0, -8, -12, -16, -20])
+def test_forward_range(M, N, K, path, up):
+    """V about 2^up, B about 2^-up, so that V B is about 1; every other column has
+    nothing else."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    R, n = 12, 3
+    o = operands(t, M + up, M, N, K, R, n, "mixed")
+    o["W"][:, ::2] = 0
+    o["scales"] = t.full((n,), 2.0 ** up)
+    o["B"] = (o["B"].float() * 2.0 ** min(-up, 14)).half()
+    v = dev(o)
+    C = t.empty_like(v["C0"])
+    g.gemm_f16_lora(v["X"], v["W"], C, v["A"], v["B"], v["ids"], v["scales"])
+    assert path in g.last_path()
+    sync(t)
+    r, tol = ref.lora(o["X"], o["W"], None, o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0)
+    for a in range(n):
+        rows = o["ids"] == a
+        tol[rows] += kept(2.0 ** up * o["X"][rows].double() @ o["A"][a].double(), o["B"][a].double())
+    ref.check(C.cpu(), r, tol)
+
+
+@pytest.mark.parametrize("M,N,K,path", LORA_SIZES)
+@pytest.mark.parametrize("up,down", [(14, -13), (12, -12), (0, 0), (-13, 13), (-18, 18)])
+def test_dx_range(M, N, K, path, up, down):
+    """dC about 2^up with alpha 2^down: loss scaling, and its contrary; every other
+    column of dX has the adapters' part alone."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    R, n = 16, 3
+    o = operands(t, M + up, M, N, K, R, n, "mixed")
+    o["W"][::2] = 0
+    o["G"] = (o["G"].float().clamp(-0.35, 0.35) * 10 * 2.0 ** up).half()   # below 65504
+    o["B"] = o["B"] * 4
+    v = dev(o)
+    dX = t.empty_like(v["X"])
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], dX,
+                         alpha=2.0 ** down)
+    assert path in g.last_path()
+    sync(t)
+    r, tol = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"],
+                           2.0 ** down, 0.0, None, None)["dX"]
+    for a in range(n):
+        rows = o["ids"] == a
+        U = float(o["scales"][a]) * o["G"][rows].double() @ o["B"][a].double().t()
+        tol[rows] += 2.0 ** down * kept(U, o["A"][a].double().t())
+    ref.check(dX.cpu(), r, tol)
+
+
+@pytest.mark.parametrize("M,N,K,path", LORA_SIZES)
+@pytest.mark.parametrize("up", [-11, -16, -22])
+def test_small_gradients_without_scaling(M, N, K, path, up):
+    """dC about 2^up with alpha 1 and weights of the usual size: what U is kept to,
+    2^-25, is below the result's own rounding (2^-25 as well, where it is small)."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    R, n = 16, 3
+    o = operands(t, M - up, M, N, K, R, n, "mixed")
+    o["G"] = (o["G"].float() * 10 * 2.0 ** up).half()
+    o["G"][5, 3] = float("inf")                       # in a row of small entries
+    o["W"][::2] = 0
+    v = dev(o)
+    dX = t.empty_like(v["X"])
+    g.gemm_f16_lora_grad(v["G"], v["X"], v["W"], v["A"], v["B"], v["ids"], v["scales"], dX)
+    assert path in g.last_path()
+    sync(t)
+    r, tol = ref.lora_grad(o["G"], o["X"], o["W"], o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0,
+                           None, None)["dX"]
+    for a in range(n):
+        rows = o["ids"] == a
+        tol[rows] += 2.0 ** -25 * o["A"][a].double().abs().sum(1)
+    rows = t.arange(M) != 5
+    ref.check(dX.cpu()[rows], r[rows], tol[rows])
+    assert not dX[5].isfinite().any() or int(o["ids"][5]) < 0
+
+
+def test_rows_of_either_range_side_by_side():
+    """In one tile: rows past the half range, far below it and between, with an
+    adapter that is not finite among them."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    M, N, K, R, n = 2300, 1288, 1096, 40, 5
+    o = operands(t, 71, M, N, K, R, n, "mixed")
+    up = [18, 0, -12, -20, 0]
+    o["scales"] = t.tensor([2.0 ** e for e in up])
+    for a in range(n):
+        o["B"][a] = (o["B"][a].float() * 2.0 ** min(-up[a], 14)).half()
+    o["B"][4, 3, 5] = float("inf")
+    v = dev(o)
+    C, dX = t.empty_like(v["C0"]), t.empty_like(v["X"])
+    g.gemm_f16_lora(v["X"], v["W"], C, v["A"], v["B"], v["ids"], v["scales"], 1.0, 0.0)
+    sync(t)
+    r, tol = ref.lora(o["X"], o["W"], None, o["A"], o["B"], o["ids"], o["scales"], 1.0, 0.0)
+    for a in range(n):
+        rows = o["ids"] == a
+        tol[rows] += kept(2.0 ** up[a] * o["X"][rows].double() @ o["A"][a].double(),
+                          o["B"][a].double()).nan_to_num(0.0)
+    same_where_not_finite(C.cpu(), r)
+    fin = r.isfinite()
+    ref.check(C.cpu()[fin], r[fin], tol[fin])
 
 
 def moe_exact(o, topk):
