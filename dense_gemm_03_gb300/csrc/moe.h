@@ -34,6 +34,38 @@ __device__ __forceinline__ uint16_t moe_f2h(float x) {
   return __half_as_ushort(__float2half_rn(x));
 }
 
+// |x| as bits that order like it, or 0 for an infinity or NaN.
+__device__ __forceinline__ unsigned int moe_finite_bits(float x) {
+  const unsigned int b = __float_as_uint(x) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? b : 0u;
+}
+// The power of two that brings a magnitude (its bits) into [2^13, 2^14), at most
+// 2^126 either way, so that it and its inverse are normal; and that inverse.
+__device__ __forceinline__ float moe_scale(unsigned int top) {
+  return __int_as_float(min(253, 127 + 13 + 127 - static_cast<int>(top >> 23)) << 23);
+}
+__device__ __forceinline__ float moe_unscale(float up) {
+  return __int_as_float((254 << 23) - __float_as_int(up));
+}
+
+// Four entries times `up` as halves, hi and what it leaves out; an infinite hi
+// stands alone.
+__device__ __forceinline__ void moe_split4(float4 v, float up, uint2& hi, uint2& lo) {
+  const float x[4] = {up * v.x, up * v.y, up * v.z, up * v.w};
+  uint32_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2 hh = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    const float2 f = __half22float2(hh);
+    const __half2 ll = __floats2half2_rn(isinf(f.x) ? 0.0f : x[2 * i] - f.x,
+                                         isinf(f.y) ? 0.0f : x[2 * i + 1] - f.y);
+    memcpy(h + i, &hh, 4);
+    memcpy(l + i, &ll, 4);
+  }
+  hi = make_uint2(h[0], h[1]);
+  lo = make_uint2(l[0], l[1]);
+}
+
 // The two halves' products with the same weights.  Where those hold an infinity
 // the hi part is the result; lo, of either sign or zero, would make it NaN.
 __device__ __forceinline__ float moe_join(float hi, float lo) { return isinf(hi) ? hi : hi + lo; }

@@ -27,10 +27,13 @@
 // no wait needs a CTA that has not started.  The weights do not depend on those
 // waits: W2 streams into the ring across them.
 //
-// hid is kept as two halves, hi + lo (22 significant bits or 2^-25), staged as separate
-// rows of the N operand and added up after the products, so the layer's only
-// rounding to half is that of Y.  A token's columns never mix with another's,
-// and a pair's partial results are read only for its own token.
+// hid is fp32.  For the second product each pair's row is scaled by the power of
+// two that brings its largest finite magnitude into [2^13, 2^14) and staged as two
+// halves, hi + lo (22 significant bits or 2^-37 of the largest), separate rows of
+// the N operand whose products are added up and scaled back after it: the layer's
+// only rounding to half is that of Y, and a gated row of any size has its bits.  A
+// token's columns never mix with another's, and a pair's partial results are read
+// only for its own token.
 //
 // Shared memory per ring stage: four 64-column boxes of 64 k-rows (128-byte
 // swizzle, MN-major: LBO 8 KB to the next 64 columns, SBO 1 KB to the next 8
@@ -159,7 +162,11 @@ constexpr int kTmemCols = 512;               // two buffers of two accumulators
 constexpr int kSmemMax = 232448;
 constexpr int kQueue = 4;                    // chunk numbers on their way to the consumers
 constexpr int kBarBytes = 8 * (3 * kMaxStages + 5 + 2 * kQueue);
-constexpr int kFixedBytes = (kBarBytes + 4 * kQueue + 8 + 15) / 16 * 16;
+constexpr int kTopPad = 8;                   // words to a row's magnitude: in one sector the
+                                             // maxima of eight rows took 0.6 us longer
+constexpr int kScales = 8;                   // chunks whose rows' scales are kept
+static_assert(kScales > kQueue, "the chunk an epilogue warp is at, and a queue of later ones");
+constexpr int kFixedBytes = (kBarBytes + 4 * kQueue + 8 + 4 * kScales * kBlockT + 15) / 16 * 16;
 
 struct StreamArgs {
   const uint16_t* X;
@@ -172,7 +179,8 @@ struct StreamArgs {
   float beta;
   int up_tiles, up_kb, down_tiles, down_kb;
   int stages, stage_bytes;
-  uint16_t* hid;           // [2][T * topk][I]: hi, lo
+  float* hid;              // [T * topk][I]
+  unsigned int* top;       // [T * topk][kTopPad]: the rows' largest finite magnitude, as bits
   float* up_part;          // by unit and chunk: [acc][token][128]
   float* z;                // [T * topk][chunk][H]
   unsigned int* queue;     // chunks taken so far
@@ -266,6 +274,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   auto qempty_bar = [&](int i) { return bars + 8u * (3 * kMaxStages + 5 + kQueue + i); };
   volatile int* const s_queue = reinterpret_cast<int*>(tail + kBarBytes);
   uint32_t* const misc = reinterpret_cast<uint32_t*>(tail + kBarBytes + 4 * kQueue);
+  // by chunk: what takes the scale of a row of hid back
+  volatile float* const s_down = reinterpret_cast<float*>(misc + 2);   // [kScales][kBlockT]
   uint16_t* const s_ids = reinterpret_cast<uint16_t*>(tail + kFixedBytes);   // expert of a pair
   const int P8 = round_up(P, 8), E2 = round_up(a.E, 2);
   uint16_t* const s_list = s_ids + P8;    // pairs by (expert, pair)
@@ -281,7 +291,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       mbar_init(empty_bar(s), 1u);
     }
     for (uint32_t b = 0; b < 2; ++b) {
-      mbar_init(accf_bar(b), 1u);
+      mbar_init(accf_bar(b), 2u);   // the products, and the MMA thread for the scales
       mbar_init(acce_bar(b), static_cast<uint32_t>(kEpi));
     }
     mbar_init(done_bar, 1u);
@@ -487,6 +497,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         }
         if (!ok) break;
         mma_commit(accf_bar(buf));
+        mbar_arrive(accf_bar(buf));
         ++local;
       }
       mma_commit(done_bar);
@@ -496,25 +507,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else if (warp < 2 + kLoaders) {
     // ---------------------------------------------------------- token rows
     // Loader l stages the k-blocks l, l + 4, ... of the CTA's sequence: rows
-    // of X for up; for down the hi rows of hid, then (from the next multiple
-    // of 8) the lo rows.  Rows past them are left as they are: their columns
-    // of the product are never read.
+    // of X for up; for down the hi parts of the rows of hid, then (from the next
+    // multiple of 8) the lo parts.  Rows past them are left as they are: their
+    // columns of the product are never read.
     const int l = warp - 2;
-    int stage = 0, seq = 0;
+    int stage = 0, seq = 0, place = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int id; ok && (id = next_chunk_warp()) >= 0;) {
+    for (int id; ok && (id = next_chunk_warp()) >= 0; ++place) {
       const Chunk t = chunk_at(w, id);
       const int e = s_act[t.q];
       const int n = s_cnt[e], off = s_off[e], n8 = round_up(n, 8);
-      const int rows = t.down ? 2 * n : n;
-      const int K = t.down ? a.I : a.H;
+      unsigned int top[2] = {};   // of rows lane and lane + 32 (kBlockT in all)
       if (t.down) {   // hid of the expert's pairs is written
         if (lane == 0)
           ok = wait_count(a.ready + t.q, static_cast<unsigned int>(kEpi * w.up_tiles), limit, st, 46);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         __syncwarp();
         if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (lane + 32 * u < n) top[u] = __ldcg(a.top + (off + lane + 32 * u) * kTopPad);
       }
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++seq) {
         if ((seq & (kLoaders - 1)) == l) {
@@ -523,30 +536,60 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             break;
           }
           uint8_t* const dst = base_ptr + static_cast<size_t>(stage) * a.stage_bytes + kWeightBytes;
-          for (int i0 = 0; i0 < rows * 8; i0 += 32 * 4) {
-            uint4 v[4];
+          if (t.down) {
+            // four entries at a time
+            for (int i0 = 0; i0 < n * 16; i0 += 32 * 4) {
+              float4 v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int i = i0 + 32 * u + lane;
-              const int r = i >> 3, k = kb * 64 + (i & 7) * 8;
-              v[u] = make_uint4(0u, 0u, 0u, 0u);
-              if (r < rows && k < K) {
-                if (t.down) {
-                  const long long row = off + (r < n ? r : r - n + P);
-                  v[u] = __ldcg(reinterpret_cast<const uint4*>(a.hid + row * a.I + k));
-                } else {
-                  v[u] = __ldg(reinterpret_cast<const uint4*>(
-                      a.X + static_cast<long long>(s_list[off + r] / a.topk) * a.ldx + k));
+              for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u + lane;
+                const int r = i >> 4, k = kb * 64 + (i & 15) * 4;
+                v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (r < n && k < a.I)
+                  v[u] = __ldcg(reinterpret_cast<const float4*>(
+                      a.hid + static_cast<long long>(off + r) * a.I + k));
+              }
+              // (not before the loads: the compiler would wait for top first)
+              asm volatile("" : "+r"(top[0]), "+r"(top[1]));
+              const float mine = moe_scale(i0 < 512 ? top[0] : top[1]);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u + lane;
+                const int r = i >> 4, c = i & 15;
+                // (rows i0 / 16 .. i0 / 16 + 7 are on one side of 32)
+                const float up = __shfl_sync(0xffffffffu, mine, r & 31);
+                if (r < n) {
+                  uint2 hi, lo;
+                  moe_split4(v[u], up, hi, lo);
+                  // n8 is a multiple of 8
+                  uint8_t* const o = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + 8 * (c & 1);
+                  *reinterpret_cast<uint2*>(o) = hi;
+                  *reinterpret_cast<uint2*>(o + n8 * 128) = lo;
                 }
               }
             }
+            if (kb == t.kb0)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int i = i0 + 32 * u + lane;
-              const int r = i >> 3, c = i & 7;
-              if (r < rows) {
-                const int rr = r >= n ? r - n + n8 : r;
-                *reinterpret_cast<uint4*>(dst + rr * 128 + ((c ^ (rr & 7)) << 4)) = v[u];
+              for (int u = 0; u < 2; ++u)
+                s_down[place % kScales * kBlockT + lane + 32 * u] =
+                    moe_unscale(moe_scale(top[u]));
+          } else {
+            for (int i0 = 0; i0 < n * 8; i0 += 32 * 4) {
+              uint4 v[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u + lane;
+                const int r = i >> 3, k = kb * 64 + (i & 7) * 8;
+                v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < n && k < a.H)
+                  v[u] = __ldg(reinterpret_cast<const uint4*>(
+                      a.X + static_cast<long long>(s_list[off + r] / a.topk) * a.ldx + k));
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const int i = i0 + 32 * u + lane;
+                const int r = i >> 3, c = i & 7;
+                if (r < n) *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) = v[u];
               }
             }
           }
@@ -574,21 +617,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 48)) break;
       tc_fence_after();
       const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16) + buf * (2 * kAccCols);
-      // hid of 8 tokens at column j
+      // hid of 8 tokens at column j, and the largest of the warp's columns
       const int j = t.tile * 128 + col;
       auto store_hid = [&](int r0, const float (&g)[8], const float (&u)[8]) {
-        if (j >= a.I) return;
+        unsigned int top = 0u;   // lane i: of token r0 + i
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (r0 + i < n) {
-            const float h = g[i] / (1.0f + expf(-g[i])) * u[i];
-            const uint16_t hi = moe_f2h(h);
-            // past the half range hi is infinite and stands alone
-            const uint16_t lo = (hi & 0x7FFFu) >= 0x7C00u ? 0 : moe_f2h(h - moe_h2f(hi));
-            const long long o = static_cast<long long>(off + r0 + i) * a.I + j;
-            a.hid[o] = hi;
-            a.hid[static_cast<long long>(P) * a.I + o] = lo;
+          if (r0 + i < n) {   // for all lanes or none
+            float h = 0.0f;
+            if (j < a.I) {
+              h = g[i] / (1.0f + expf(-g[i])) * u[i];
+              a.hid[static_cast<long long>(off + r0 + i) * a.I + j] = h;
+            }
+            const unsigned int most = __reduce_max_sync(0xffffffffu, moe_finite_bits(h));
+            if (lane == i) top = most;
           }
+        if (lane < 8 && top != 0u) atomicMax(a.top + (off + r0 + lane) * kTopPad, top);
       };
       float* const unit_part =
           t.down ? nullptr
@@ -614,9 +658,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (r0 + i < n) {
+              const float down = s_down[local % kScales * kBlockT + r0 + i];
               float* o = a.z + (static_cast<long long>(off + r0 + i) * w.down_chunks + t.c) * a.H;
-              if (c0 < a.H) __stcg(o + c0, moe_join(v0[i], __uint_as_float(g[i])));
-              if (c0 + 128 < a.H) __stcg(o + c0 + 128, moe_join(v1[i], __uint_as_float(h[i])));
+              if (c0 < a.H) __stcg(o + c0, down * moe_join(v0[i], __uint_as_float(g[i])));
+              if (c0 + 128 < a.H)
+                __stcg(o + c0 + 128, down * moe_join(v1[i], __uint_as_float(h[i])));
             }
         } else if (w.up_chunks == 1) {
           store_hid(r0, v0, v1);
@@ -830,10 +876,10 @@ int moe_stream(const MoeArgs& m, int sms, DeviceStatus* st, unsigned long long l
     const long long units = 1ll * experts * s.up_tiles;
     const size_t b_part = round256(4 * static_cast<size_t>(r.splits) * T * m.E);
     const size_t b_ids = round256(4 * static_cast<size_t>(P));
-    const size_t b_hid = round256(2 * 2 * static_cast<size_t>(P) * m.I);
+    const size_t b_hid = round256(4 * static_cast<size_t>(P) * m.I);
     const size_t b_z = round256(4 * static_cast<size_t>(P) * down_chunks * m.H);
     const size_t b_ws = round256(4 * static_cast<size_t>(P) * s.up_tiles * up_chunks * 256);
-    const size_t n_zero = static_cast<size_t>(units) * kEpi + experts + 2;
+    const size_t n_zero = static_cast<size_t>(units) * kEpi + experts + kTopPad * (P + 1);
     const size_t b_cnt = round256(4 * n_zero);
     void *buf = nullptr, *zero = nullptr;
     if (int rc = routed_scratch(stream, b_part + 2 * b_ids + b_hid + b_z + b_ws + b_cnt, &buf,
@@ -848,12 +894,13 @@ int moe_stream(const MoeArgs& m, int sms, DeviceStatus* st, unsigned long long l
     r.part = reinterpret_cast<float*>(take(b_part));
     r.ids = reinterpret_cast<int*>(take(b_ids));
     r.probs = reinterpret_cast<float*>(take(b_ids));
-    s.hid = reinterpret_cast<uint16_t*>(take(b_hid));
+    s.hid = reinterpret_cast<float*>(take(b_hid));
     s.z = reinterpret_cast<float*>(take(b_z));
     s.up_part = reinterpret_cast<float*>(take(b_ws));
     s.queue = reinterpret_cast<unsigned int*>(take(b_cnt));
     s.done = s.queue + 1;
-    s.ready = s.done + 1;
+    s.top = s.queue + kTopPad;
+    s.ready = s.top + kTopPad * P;
     s.counters = s.ready + experts;
     s.ids = r.ids;
     s.probs = r.probs;

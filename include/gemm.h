@@ -217,8 +217,8 @@ int gemm_f16_lora_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W,
  * as the largest.  Only chosen experts' weights are read, each once per block
  * of tokens; a token's result depends on no other token and no expert it did
  * not choose.  Sums are fp32 in a fixed order; the gated product is kept to 22
- * significant bits or 2^-25, whichever is coarser (magnitude within the half
- * range); Y is rounded once.  H == 0 leaves nothing to do; I == 0 gives Y := beta * Y.
+ * significant bits or 2^-37 of the largest of its row (a token at an expert),
+ * whichever is coarser; Y is rounded once.  H == 0 leaves nothing to do; I == 0 gives Y := beta * Y.
  */
 int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_t* W1, const uint16_t* W2,
                  uint16_t* Y, int* ids, float* probs, int T, int H, int I, int E, int topk,

@@ -262,6 +262,32 @@ def moe_exact(o, topk):
     return ids, Y, tol + ref.HALF * Y.abs() + ref.TINY
 
 
+@pytest.mark.parametrize("T,H,I,E,topk", [(1, 512, 256, 16, 4), (5, 512, 256, 8, 2),
+                                          (40, 264, 712, 3, 2), (64, 256, 192, 1, 1),
+                                          (6, 257, 129, 8, 2)])
+@pytest.mark.parametrize("up", [9, 4, 0, -7, -12])
+def test_moe_range(T, H, I, E, topk, up):
+    """Gate and up of about 2^up: gated rows from 2^-25 to 2^18, tokens of
+    different magnitude side by side; W2 makes the result about 1."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = moe_operands(t, T + H + up, T, H, I, E)
+    o["Wr"] = t.zeros_like(o["Wr"])
+    o["Wr"][0] = t.arange(E, 0, -1).half()            # a choice no rounding changes
+    o["X"] = (o["X"].float() * t.tensor([1.0, 0.25, 1.0, 0.0625])[t.arange(T) % 4, None]).half()
+    o["X"][:, 0] = 1.0
+    o["W1"][:, 0] = 0
+    o["W1"] = (o["W1"].float() * 2.0 ** up).half()
+    o["W2"] = (o["W2"].float() * 2.0 ** max(min(-2 * up, 14), -10)).half()
+    v = {k: x.cuda() for k, x in o.items()}
+    Y, ids = t.empty_like(v["Y0"]), t.empty((T, topk), dtype=t.int32, device="cuda")
+    g.gemm_f16_moe(v["X"], v["Wr"], v["W1"], v["W2"], Y, topk, ids=ids)
+    sync(t)
+    want_ids, want, tol = moe_exact(o, topk)
+    assert t.equal(ids.cpu().long(), want_ids)
+    ref.check(Y.cpu(), want, tol, g.last_path())
+
+
 @pytest.mark.parametrize("H,I", [(256, 192), (257, 129)])
 def test_moe_infinite_weights(H, I):
     """Infinities in W2: the tokens of that expert are infinite or NaN where the
