@@ -129,6 +129,55 @@ def _addr(x):
     raise TypeError("expected a tensor, an array or an address, got %r" % type(x))
 
 
+_dtype_names = {}
+
+
+def _dtype_name(x):
+    name = _dtype_names.get(x.dtype)
+    if name is None:
+        name = _dtype_names[x.dtype] = str(x.dtype).rpartition(".")[2]
+    return name
+
+
+def _typed(x, dtype, n, name):
+    """The address of an operand without a leading dimension: n dense elements of
+    `dtype`.  An address is taken at its word."""
+    try:                                          # the usual tensor, in little time
+        if _dtype_names[x.dtype] == dtype and x.is_contiguous() and x.numel() >= n:
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    if x is None or isinstance(x, int):
+        return x
+    if _dtype_name(x) != dtype:
+        raise TypeError("%s is %s, not %s" % (name, _dtype_name(x), dtype))
+    if not _dense(x) or (x.numel() if hasattr(x, "numel") else x.size) < n:
+        raise ValueError("%s is not %d dense elements" % (name, n))
+    return _addr(x)
+
+
+def _dense(x):
+    return x.is_contiguous() if hasattr(x, "is_contiguous") else x.flags.c_contiguous
+
+
+def _stack(x, ld, name):
+    """The address of stacked matrices, dense unless a leading dimension is given."""
+    try:
+        if ld is not None or x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    if x is None or isinstance(x, int):
+        return x
+    if ld is None and not _dense(x):
+        raise ValueError("%s is not dense (a permuted view?)" % name)
+    return _addr(x)
+
+
+def _differ(what, a, b):
+    raise ValueError("%s: %d and %d" % (what, a, b))
+
+
 _current_stream = None
 
 
@@ -154,7 +203,7 @@ def _current_stream_fn():
 
 def _stream(stream):
     if stream is None:
-        return _current_stream_fn()()
+        return (_current_stream or _current_stream_fn())()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -231,16 +280,26 @@ def gemm_f16_lora(X, W, C, A, B, ids, scales=None, alpha=1.0, beta=0.0, M=None, 
     (int32; outside [0, adapters): no adapter) on device fp16 operands; A is
     (adapters, K, R), B (adapters, R, N), scales fp32 or None for ones."""
     # (a tensor's shape is asked for once: it costs a third of a microsecond)
+    whole = K is None                 # no sub-matrix: the shapes have one K
     if M is None or K is None:
         m, k = X.shape
         M, K = m if M is None else M, k if K is None else K
     if N is None:
-        N = W.shape[1]
+        k, N = W.shape
+        if k != K and whole:
+            _differ("K of W and X", k, K)
     if R is None or adapters is None:
-        n, _, r = A.shape
+        n, k, r = A.shape
         R, adapters = r if R is None else R, n if adapters is None else adapters
-    rc = lib().gemm_f16_lora(_addr(X), _addr(W), _addr(C), _addr(A), _addr(B), _addr(ids),
-                             _addr(scales), M, N, K, R, adapters, K if ldx is None else ldx,
+        if k != K and whole:
+            _differ("K of A and X", k, K)
+    try:
+        x, w, c = X.data_ptr(), W.data_ptr(), C.data_ptr()
+    except AttributeError:
+        x, w, c = _addr(X), _addr(W), _addr(C)
+    rc = lib().gemm_f16_lora(x, w, c, _stack(A, lda, "A"), _stack(B, ldb, "B"),
+                             _typed(ids, "int32", M, "ids"),
+                             _typed(scales, "float32", adapters, "scales"), M, N, K, R, adapters, K if ldx is None else ldx,
                              N if ldw is None else ldw, N if ldc is None else ldc,
                              R if lda is None else lda, N if ldb is None else ldb,
                              alpha, beta, _stream(stream))
@@ -256,13 +315,19 @@ def gemm_f16_lora_grad(dC, X, W, A, B, ids, scales=None, dX=None, dA=None, dB=No
     if M is None or N is None:
         m, n = dC.shape
         M, N = m if M is None else M, n if N is None else N
+    whole = K is None
     if K is None:
         K = W.shape[0] if W is not None else X.shape[1]
     if R is None or adapters is None:
-        n, _, r = A.shape if A is not None else (B.shape[0], None, B.shape[1])
+        n, k, r = A.shape if A is not None else (B.shape[0], K, B.shape[1])
         R, adapters = r if R is None else R, n if adapters is None else adapters
-    rc = lib().gemm_f16_lora_grad(_addr(dC), _addr(X), _addr(W), _addr(A), _addr(B), _addr(ids),
-                                  _addr(scales), _addr(dX), _addr(dA), _addr(dB), M, N, K, R,
+        if k != K and whole:
+            _differ("K of A and W", k, K)
+    rc = lib().gemm_f16_lora_grad(_addr(dC), _addr(X), _addr(W), _stack(A, lda, "A"),
+                                  _stack(B, ldb, "B"), _typed(ids, "int32", M, "ids"),
+                                  _typed(scales, "float32", adapters, "scales"), _addr(dX),
+                                  _typed(dA, "float32", adapters * K * R, "dA"),
+                                  _typed(dB, "float32", adapters * R * N, "dB"), M, N, K, R,
                                   adapters, N if lddc is None else lddc,
                                   K if ldx is None else ldx, N if ldw is None else ldw,
                                   R if lda is None else lda, N if ldb is None else ldb,
@@ -281,10 +346,14 @@ def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True,
         t, h = X.shape
         T, H = t if T is None else T, h if H is None else H
     if E is None or I is None:
-        e, i, _ = W2.shape
+        e, i, h = W2.shape
         E, I = e if E is None else E, i if I is None else I
-    rc = lib().gemm_f16_moe(_addr(X), _addr(Wr), _addr(W1), _addr(W2), _addr(Y), _addr(ids),
-                            _addr(probs), T, H, I, E, topk, bool(renormalize),
+        if h != H:
+            _differ("H of W2 and X", h, H)
+    rc = lib().gemm_f16_moe(_addr(X), _stack(Wr, None, "Wr"), _stack(W1, None, "W1"),
+                            _stack(W2, None, "W2"), _addr(Y),
+                            _typed(ids, "int32", T * topk, "ids"),
+                            _typed(probs, "float32", T * topk, "probs"), T, H, I, E, topk, bool(renormalize),
                             H if ldx is None else ldx, H if ldy is None else ldy, beta,
                             _stream(stream))
     _check(rc, "gemm_f16_moe")
