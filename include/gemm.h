@@ -215,10 +215,13 @@ int gemm_f16_lora_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W,
  *                order of falling l, and p.  Each may be NULL.
  * 1 <= topk <= min(E, 32), E <= 1024 (else GEMM_ERR_ARG).  A NaN logit counts
  * as the largest.  Only chosen experts' weights are read, each once per block
- * of tokens; a token's result depends on no other token and no expert it did
- * not choose.  Sums are fp32 in a fixed order; the gated product is kept to 22
- * significant bits or 2^-37 of the largest of its row (a token at an expert),
- * whichever is coarser; Y is rounded once.  H == 0 leaves nothing to do; I == 0 gives Y := beta * Y.
+ * of tokens; no value of another token, or of an expert that it did not choose,
+ * enters a token's sums.  Sums are fp32, in an order that is fixed for a batch
+ * but goes by its size and by how many experts it takes: the same token in
+ * another batch may differ in the last bits and, where two logits are that
+ * close, in its choice.  The gated product is kept to 22 significant bits or
+ * 2^-37 of the largest of its row (a token at an expert), whichever is coarser;
+ * Y is rounded once.  H == 0 leaves nothing to do; I == 0 gives Y := beta * Y.
  */
 int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_t* W1, const uint16_t* W2,
                  uint16_t* Y, int* ids, float* probs, int T, int H, int I, int E, int topk,

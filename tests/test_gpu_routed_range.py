@@ -305,3 +305,65 @@ def test_moe_infinite_weights(H, I):
     same_where_not_finite(Y.cpu(), want)
     fin = want.isfinite()
     ref.check(Y.cpu()[fin], want[fin], tol[fin])
+
+
+@pytest.mark.parametrize("T,H,I,E", [(24, 2560, 1408, 16), (40, 2816, 640, 64)])
+def test_moe_tokens_do_not_mix_in_units_of_many_chunks(T, H, I, E):
+    """Tokens of Inf and NaN beside others, in experts whose matrices are cut into
+    many chunks: the others stay within the bound they have alone (what they
+    choose leaves other chunks, so bits may differ)."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    o = moe_operands(t, 91 + T, T, H, I, E)
+    o["Wr"] = (o["Wr"].float() * 4).half()
+    o["X"][5, 3], o["X"][9] = float("inf"), float("nan")
+    v = {k: x.cuda() for k, x in o.items()}
+    Y, ids = t.empty_like(v["Y0"]), t.empty((T, 2), dtype=t.int32, device="cuda")
+    g.gemm_f16_moe(v["X"], v["Wr"], v["W1"], v["W2"], Y, 2, ids=ids)
+    sync(t)
+    rows = [i for i in range(T) if i not in (5, 9)]
+    o["X"] = o["X"][rows]
+    want_ids, want, tol = moe_exact(o, 2)
+    same = (ids.cpu()[rows].long() == want_ids).all(1)
+    assert int(same.sum()) >= len(rows) - 1           # a near tie may go either way
+    ref.check(Y.cpu()[rows][same], want[same], tol[same])
+    assert Y[9].isnan().all()
+
+
+@pytest.mark.parametrize("T,H,I,E", [(1, 128, 96, 4), (5, 2560, 640, 3), (33, 264, 200, 2),
+                                     (64, 1024, 1024, 1), (5, 130, 97, 3)])
+def test_moe_integers_exact(T, H, I, E):
+    """Gated rows of 15 to 17 bits whose differences are the result: every sum is
+    exact, and the half that their upper 11 bits leave out is needed."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    gen = t.Generator().manual_seed(T + H)
+
+    def ints(lo, hi, *shape):
+        return t.randint(lo, hi + 1, shape, generator=gen).double()
+
+    X = ints(-1, 1, T, H)
+    X[:, 0] = 1
+    Wr = t.zeros(H, E, dtype=t.float64)
+    Wr[1] = t.arange(E, dtype=t.float64)
+    W1 = t.zeros(E, H, 2 * I, dtype=t.float64)
+    W1[:, 0, :I], W1[:, 0, I:] = 210, 190             # silu(x) = x in fp32 from about 20 on
+    for k in range(2, min(H, 34)):
+        W1[:, k] = ints(-1, 1, E, 2 * I)
+    W1[:, H - 1] = ints(-2, 2, E, 2 * I)
+    W2 = t.zeros(E, I, H, dtype=t.float64)
+    for e in range(E):
+        a, b = (t.randint(0, I, (H,), generator=gen) for _ in range(2))
+        W2[e, a, t.arange(H)] += 1
+        W2[e, b, t.arange(H)] -= 1
+    e = (X @ Wr).argmax(1)
+    gu = (X[:, None] @ W1[e])[:, 0]
+    assert gu.min() > 100
+    want = ((gu[:, :I] * gu[:, I:])[:, None] @ W2[e])[:, 0]
+    v = [x.half().cuda() for x in (X, Wr, W1, W2)]
+    Y = t.empty((T, H), dtype=t.float16, device="cuda")
+    ids = t.empty((T, 1), dtype=t.int32, device="cuda")
+    g.gemm_f16_moe(*v, Y, 1, ids=ids)
+    sync(t)
+    assert t.equal(ids.cpu()[:, 0].long(), e)
+    assert t.equal(Y.cpu(), want.half()), g.last_path()
