@@ -297,13 +297,13 @@ def gemm_f16_lora(X, W, C, A, B, ids, scales=None, alpha=1.0, beta=0.0, M=None, 
         x, w, c = X.data_ptr(), W.data_ptr(), C.data_ptr()
     except AttributeError:
         x, w, c = _addr(X), _addr(W), _addr(C)
-    rc = lib().gemm_f16_lora(x, w, c, _stack(A, lda, "A"), _stack(B, ldb, "B"),
-                             _typed(ids, "int32", M, "ids"),
-                             _typed(scales, "float32", adapters, "scales"), M, N, K, R, adapters, K if ldx is None else ldx,
-                             N if ldw is None else ldw, N if ldc is None else ldc,
-                             R if lda is None else lda, N if ldb is None else ldb,
-                             alpha, beta, _stream(stream))
-    _check(rc, "gemm_f16_lora")
+    call = (_lib or lib()).gemm_f16_lora
+    rc = call(x, w, c, _stack(A, lda, "A"), _stack(B, ldb, "B"), _typed(ids, "int32", M, "ids"),
+              _typed(scales, "float32", adapters, "scales"), M, N, K, R, adapters,
+              K if ldx is None else ldx, N if ldw is None else ldw, N if ldc is None else ldc,
+              R if lda is None else lda, N if ldb is None else ldb, alpha, beta, _stream(stream))
+    if rc:
+        _check(rc, "gemm_f16_lora")
 
 
 def gemm_f16_lora_grad(dC, X, W, A, B, ids, scales=None, dX=None, dA=None, dB=None, alpha=1.0,
@@ -353,8 +353,8 @@ def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True,
     rc = lib().gemm_f16_moe(_addr(X), _stack(Wr, None, "Wr"), _stack(W1, None, "W1"),
                             _stack(W2, None, "W2"), _addr(Y),
                             _typed(ids, "int32", T * topk, "ids"),
-                            _typed(probs, "float32", T * topk, "probs"), T, H, I, E, topk, bool(renormalize),
-                            H if ldx is None else ldx, H if ldy is None else ldy, beta,
+                            _typed(probs, "float32", T * topk, "probs"), T, H, I, E, topk,
+                            bool(renormalize), H if ldx is None else ldx, H if ldy is None else ldy, beta,
                             _stream(stream))
     _check(rc, "gemm_f16_moe")
 

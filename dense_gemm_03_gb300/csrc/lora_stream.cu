@@ -588,7 +588,11 @@ bool lora_stream_suits(int M, int N, int sms) {
 // By rows: each row's adapter is read from L2 by itself, 2 K R bytes, whatever
 // the other rows have: 10 us for 2^25 multiply-adds, what the tensor cores take
 // with a few adapters among 128 rows; with many they make many passes (300 rows
-// of 4096 over 32 adapters of rank 16 in no order: 70 us).
+// of 4096 over 32 adapters of rank 16 in no order: 70 us).  Up to 128 rows by rows
+// whatever K R is: a call of 128 x 4096 x 8192 at rank 128 takes 69 us with one
+// adapter (43 with the tensor cores) and 110 with 32 in no order (272), one of
+// 128 x 4096 x 4096 at rank 16 17 us with either (17 and 81).  How many adapters
+// there are only the device knows.
 bool lora_stream_shrinks(int M, int K, int R) {
   return M <= kFewRows || (M <= 4 * kFewRows && 1ll * M * K * R <= (1ll << 25));
 }
