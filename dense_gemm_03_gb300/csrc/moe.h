@@ -48,8 +48,8 @@ __device__ __forceinline__ float moe_unscale(float up) {
   return __int_as_float((254 << 23) - __float_as_int(up));
 }
 
-// Four entries times `up` as halves, hi and what it leaves out; an infinite hi
-// stands alone.
+// Four entries times `up` as halves, hi and what it leaves out; a hi that is not
+// finite stands alone.
 __device__ __forceinline__ void moe_split4(float4 v, float up, uint2& hi, uint2& lo) {
   const float x[4] = {up * v.x, up * v.y, up * v.z, up * v.w};
   uint32_t h[2], l[2];
@@ -57,10 +57,10 @@ __device__ __forceinline__ void moe_split4(float4 v, float up, uint2& hi, uint2&
   for (int i = 0; i < 2; ++i) {
     const __half2 hh = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
     const float2 f = __half22float2(hh);
-    const __half2 ll = __floats2half2_rn(isinf(f.x) ? 0.0f : x[2 * i] - f.x,
-                                         isinf(f.y) ? 0.0f : x[2 * i + 1] - f.y);
+    const __half2 ll = __floats2half2_rn(x[2 * i] - f.x, x[2 * i + 1] - f.y);
     memcpy(h + i, &hh, 4);
     memcpy(l + i, &ll, 4);
+    l[i] &= __hlt2_mask(__habs2(hh), __half2half2(__ushort_as_half(0x7C00)));
   }
   hi = make_uint2(h[0], h[1]);
   lo = make_uint2(l[0], l[1]);

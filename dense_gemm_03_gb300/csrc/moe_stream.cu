@@ -622,16 +622,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
       auto store_hid = [&](int r0, const float (&g)[8], const float (&u)[8]) {
         unsigned int top = 0u;   // lane i: of token r0 + i
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (r0 + i < n) {   // for all lanes or none
-            float h = 0.0f;
-            if (j < a.I) {
-              h = g[i] / (1.0f + expf(-g[i])) * u[i];
-              a.hid[static_cast<long long>(off + r0 + i) * a.I + j] = h;
-            }
-            const unsigned int most = __reduce_max_sync(0xffffffffu, moe_finite_bits(h));
-            if (lane == i) top = most;
+        for (int i = 0; i < 8; ++i) {
+          // for all lanes or none: one jump past the code of tokens that are not
+          // there (a jump for each fetched 0.7 us of code at one token)
+          if (r0 + i >= n) break;
+          float h = 0.0f;
+          if (j < a.I) {
+            h = g[i] / (1.0f + expf(-g[i])) * u[i];
+            a.hid[static_cast<long long>(off + r0 + i) * a.I + j] = h;
           }
+          const unsigned int most = __reduce_max_sync(0xffffffffu, moe_finite_bits(h));
+          if (lane == i) top = most;
+        }
         if (lane < 8 && top != 0u) atomicMax(a.top + (off + r0 + lane) * kTopPad, top);
       };
       float* const unit_part =

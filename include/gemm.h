@@ -188,7 +188,8 @@ int gemm_f16_lora(const uint16_t* X, const uint16_t* W, uint16_t* C, const uint1
  *
  * dA and dB are dense stacks (adapters x K x R, adapters x R x N) in fp32, to
  * be accumulated over micro-batches with beta = 1 (beta == 0: not read); an
- * adapter without rows gets beta times its old value.  dX, dA and dB may each
+ * adapter without rows gets beta times its old value.  At most 16384 adapters
+ * (else GEMM_ERR_ARG).  dX, dA and dB may each
  * be NULL (not wanted); then operands only they read may be NULL too.  Sums
  * run in a fixed order: repeated calls are bitwise equal.  For dX, U_i is kept
  * like V_i above (with max|A[a]|); for dA and dB, U_i and V_i are kept to 22
