@@ -252,9 +252,10 @@ int stream_scratch(DevState* d, cudaStream_t stream, size_t bytes, size_t counte
   }
   if (counters) {
     const size_t cb = counters * sizeof(unsigned long long);
-    const void* const before = w.counters.ptr;
+    // (another size: a larger buffer may lie where the one before it was)
+    const size_t before = w.counters.bytes;
     if (int rc = ensure_buffer(d, &w.counters, cb, stream)) return rc;
-    if (w.counters.ptr != before) {
+    if (w.counters.bytes != before) {
       if (cudaMemsetAsync(w.counters.ptr, 0, w.counters.bytes, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
       w.epoch = 0;
@@ -1313,9 +1314,9 @@ int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed,
   if (int rc = ensure_buffer(d, &w.routed, bytes, stream)) return rc;
   *out = w.routed.ptr;
   if (zeroed) {
-    const void* const before = w.routed_zero.ptr;
+    const size_t before = w.routed_zero.bytes;
     if (int rc = ensure_buffer(d, &w.routed_zero, zeroed, stream)) return rc;
-    if (w.routed_zero.ptr != before &&
+    if (w.routed_zero.bytes != before &&
         cudaMemsetAsync(w.routed_zero.ptr, 0, w.routed_zero.bytes, stream) != cudaSuccess)
       return GEMM_ERR_CUDA;
     *zeroed_out = w.routed_zero.ptr;

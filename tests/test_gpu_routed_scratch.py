@@ -219,3 +219,33 @@ def test_release_beside_calls():
     t.cuda.synchronize()
     assert not errors, errors
     assert g.debug_status() == 0 and t.equal(want, out[0])
+
+
+def test_counters_that_grow_start_at_zero():
+    """Tiles' arrival counters: a call with more split tiles than the first buffer
+    has counters for, after one whose counts that buffer held (the larger buffer
+    may lie at the same address)."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    g.release()
+    s = t.cuda.Stream()
+    prev, prev_splits = g.force_path(g.PATH_SPLITK), g.force_splits(2)
+    K = 128
+    try:
+        for M, N in ((256, 256), (64, 256 * 16400), (256, 512)):
+            gen = t.Generator(device="cuda").manual_seed(M + N)
+            A, B = (t.randint(-1, 2, shape, generator=gen, device="cuda", dtype=t.float16)
+                    for shape in ((M, K), (K, N)))
+            C = t.full((M, N), float("nan"), dtype=t.float16, device="cuda")
+            t.cuda.synchronize()
+            g.gemm_f16(A, B, C, stream=s)
+            assert ".splitk" in g.last_path()
+            s.synchronize()
+            assert g.debug_status() == 0
+            cols = t.randint(0, N, (512,), generator=gen, device="cuda")
+            want = A.float() @ B[:, cols].float()
+            assert t.equal(C[:, cols], want.half()) and not C.isnan().any()
+    finally:
+        g.force_path(prev)
+        g.force_splits(prev_splits)
+        g.release()
