@@ -16,7 +16,8 @@ import threading
 
 __all__ = [
     "GemmError", "lib", "library_path", "gemm_f16", "gemm_f16_f32out", "f32_to_f16",
-    "sgemm_f32", "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe", "gemm_f16_host",
+    "sgemm_f32", "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe", "gemm_f16_trans",
+    "gemm_f16_trans_f32out", "gemm_f16_glu", "gemm_f16_glu_grad", "gemm_f16_host",
     "sgemm_f32_host", "gemm_f16_splitk_noalloc", "l2_flush", "force_path", "force_splits", "stage_kblocks",
     "set_wait_limit_ns",
     "debug_status", "last_path", "launch_count", "plan_stream_k", "release", "EXPORTS",
@@ -34,8 +35,12 @@ EXPORTS = (
     "gemm_debug_status", "gemm_last_path", "gemm_strerror", "gemm_release",
     "gemm_f16_splitk_noalloc", "gemm_launch_count", "gemm_plan_stream_k", "gemm_f16_f32out",
     "gemm_f32_to_f16", "gemm_debug_wait_probe", "gemm_plan_tf32_slices", "gemm_stage_kblocks",
-    "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe",
+    "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe", "gemm_f16_trans",
+    "gemm_f16_trans_f32out", "gemm_f16_glu", "gemm_f16_glu_grad",
 )
+
+# Activations of a gate, by the names the calls take.
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 PATH_AUTO, PATH_TMA, PATH_MANUAL, PATH_SPLITK, PATH_F32_SCALAR = 0, 1, 2, 3, 4
 
@@ -83,6 +88,14 @@ def lib():
             L.gemm_f16_lora_grad.argtypes = [vp] * 10 + [i] * 11 + [f, f, vp]
             L.gemm_f16_moe.restype = i
             L.gemm_f16_moe.argtypes = [vp] * 7 + [i] * 8 + [f, vp]
+            for name in ("gemm_f16_trans", "gemm_f16_trans_f32out"):
+                fn = getattr(L, name)
+                fn.restype = i
+                fn.argtypes = [i, i] + [vp] * 3 + [i] * 6 + [f, f, vp]
+            L.gemm_f16_glu.restype = i
+            L.gemm_f16_glu.argtypes = [vp] * 3 + [i] * 7 + [vp]
+            L.gemm_f16_glu_grad.restype = i
+            L.gemm_f16_glu_grad.argtypes = [vp] * 6 + [i] * 10 + [f, vp]
             L.gemm_f16_splitk_noalloc.restype = i
             L.gemm_f16_splitk_noalloc.argtypes = [vp, vp, vp, i, i, i, i, i, i, f, f, i, vp]
             L.gemm_l2_flush.restype = i
@@ -357,6 +370,93 @@ def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True,
                             bool(renormalize), H if ldx is None else ldx, H if ldy is None else ldy, beta,
                             _stream(stream))
     _check(rc, "gemm_f16_moe")
+
+
+def _act(act):
+    if isinstance(act, str):
+        try:
+            return ACTIVATIONS[act]
+        except KeyError:
+            raise ValueError("unknown activation %r" % act) from None
+    return act
+
+
+def _trans(name, A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc, stream):
+    whole = K is None
+    if M is None or K is None:
+        m, k = A.shape
+        if trans_a:
+            m, k = k, m
+        M, K = m if M is None else M, k if K is None else K
+    if N is None:
+        k, N = B.shape
+        if trans_b:
+            k, N = N, k
+        if k != K and whole:
+            _differ("K of B and A", k, K)
+    rc = getattr(_lib or lib(), name)(
+        bool(trans_a), bool(trans_b), _addr(A), _addr(B), _addr(C), M, N, K,
+        (M if trans_a else K) if lda is None else lda, (K if trans_b else N) if ldb is None else ldb,
+        N if ldc is None else ldc, alpha, beta, _stream(stream))
+    if rc:
+        _check(rc, name)
+
+
+def gemm_f16_trans(A, B, C, trans_a=False, trans_b=False, alpha=1.0, beta=0.0, M=None, N=None,
+                   K=None, lda=None, ldb=None, ldc=None, stream=None):
+    """C := alpha*op(A)*op(B) + beta*C on device fp16 operands: A is (M, K), or
+    (K, M) with trans_a; B (K, N), or (N, K) with trans_b."""
+    _trans("gemm_f16_trans", A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc, stream)
+
+
+def gemm_f16_trans_f32out(A, B, C, trans_a=False, trans_b=False, alpha=1.0, beta=0.0, M=None,
+                          N=None, K=None, lda=None, ldb=None, ldc=None, stream=None):
+    """As gemm_f16_trans with an fp32 C."""
+    _trans("gemm_f16_trans_f32out", A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc,
+           stream)
+
+
+def _glu_dims(X, W, M, N, K):
+    whole = K is None
+    if M is None or K is None:
+        m, k = X.shape
+        M, K = m if M is None else M, k if K is None else K
+    if N is None:
+        k, n2 = W.shape
+        if k != K and whole:
+            _differ("K of W and X", k, K)
+        if n2 % 2:
+            raise ValueError("W has %d columns: a gate and an up column for each output" % n2)
+        N = n2 // 2
+    return M, N, K
+
+
+def gemm_f16_glu(X, W, C, act="silu", M=None, N=None, K=None, ldx=None, ldw=None, ldc=None,
+                 stream=None):
+    """C := f(X*Wg) .* (X*Wu) on device fp16 operands; W is (K, 2N), N gate
+    columns, then N up columns.  act: "silu", "gelu", "gelu_tanh" or "relu"."""
+    M, N, K = _glu_dims(X, W, M, N, K)
+    rc = (_lib or lib()).gemm_f16_glu(_addr(X), _addr(W), _addr(C), M, N, K, _act(act),
+                                      K if ldx is None else ldx, 2 * N if ldw is None else ldw,
+                                      N if ldc is None else ldc, _stream(stream))
+    if rc:
+        _check(rc, "gemm_f16_glu")
+
+
+def gemm_f16_glu_grad(dC, X, W, dGU, dX=None, dW=None, act="silu", beta=0.0, M=None, N=None,
+                      K=None, lddc=None, ldx=None, ldw=None, lddgu=None, lddx=None, lddw=None,
+                      stream=None):
+    """Gradients of gemm_f16_glu: dGU (M, 2N), the gate's and up columns' before
+    the product; dX (M, K) and dW (K, 2N), which is added onto beta times its old
+    value.  All fp16; dX and dW may be None."""
+    M, N, K = _glu_dims(X, W, M, N, K)
+    rc = (_lib or lib()).gemm_f16_glu_grad(
+        _addr(dC), _addr(X), _addr(W), _addr(dGU), _addr(dX), _addr(dW), M, N, K, _act(act),
+        N if lddc is None else lddc, K if ldx is None else ldx, 2 * N if ldw is None else ldw,
+        2 * N if lddgu is None else lddgu, K if lddx is None else lddx,
+        2 * N if lddw is None else lddw, beta, _stream(stream))
+    if rc:
+        _check(rc, "gemm_f16_glu_grad")
 
 
 def gemm_f16_host(A, B, C, alpha=1.0, beta=0.0, M=None, N=None, K=None, lda=None, ldb=None,

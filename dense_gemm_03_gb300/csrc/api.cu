@@ -1298,6 +1298,182 @@ int gemm_f16_lora_pair(const uint16_t* A, const uint16_t* B, uint16_t* C, int M,
   return gemm_f16_impl(A, B, C, false, M, N, K, lda, ldb, ldc, alpha, beta, stream, &lora);
 }
 
+// The variants of the pair kernel (PairCall in internal.h): 256 x 256 tiles (256 x
+// 128 gated outputs) whatever the shape; the last, partial wave of tiles as two K
+// slices or two half-width units each, as in gemm_f16_impl.
+int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
+  DevState* d = nullptr;
+  if (int rc = device_state(&d, nullptr)) return rc;
+  const auto call = stream_call(d, stream);
+  const int M = q.M, N = q.N, K = q.K;
+  const uint16_t *A = q.A, *B = q.B;
+  long long lda = q.lda, ldb = q.ldb, ldc = q.ldc;
+  GateArgs g = q.g;
+  uint16_t* C = q.c_f32 ? nullptr : static_cast<uint16_t*>(q.C);
+  const int a_rows = q.trans_a ? K : M, a_cols = q.trans_a ? M : K;
+  const int b_rows = q.trans_b ? N : K;
+  int b_cols = q.trans_b ? K : (q.gate ? g.up + N : N);
+
+  // operands off the 16-byte grid are copied, a gate's columns and those it gates
+  // apart; so is a half C (the gradient's two are written with predicated stores)
+  const bool a_ok = aligned16(A) && lda % 8 == 0;
+  const bool b_ok = aligned16(B) && ldb % 8 == 0 && (!q.gate || g.up % 8 == 0);
+  const bool c_ok = q.c_f32 || (aligned16(C) && ldc % 8 == 0 && N % 8 == 0);
+  const bool dc_ok = q.gate != 2 || (aligned16(g.dC) && g.lddc % 8 == 0 && aligned16(g.dU));
+  const bool copy_c = !c_ok && q.gate != 2;
+  const long long lda2 = (a_cols + 7) / 8 * 8, n8 = (N + 7) / 8 * 8;
+  const long long ldb2 = q.gate ? 2 * n8 : (b_cols + 7) / 8 * 8;
+  auto round256 = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t a_bytes = a_ok ? 0 : round256(static_cast<size_t>(a_rows) * lda2 * 2);
+  const size_t b_bytes = b_ok ? 0 : round256(static_cast<size_t>(b_rows) * ldb2 * 2);
+  const size_t c_bytes = copy_c ? round256(static_cast<size_t>(M) * n8 * 2) : 0;
+  uint16_t* c_user = nullptr;
+  long long ldc_user = 0;
+  bool prepass = false;
+  if (a_bytes + b_bytes + c_bytes) {
+    uint8_t* buf = nullptr;
+    {
+      std::lock_guard<std::mutex> lk(g_mu);
+      StreamWs& w = d->ws[stream_key(stream)];
+      if (int rc = ensure_buffer(d, &w.realigned, a_bytes + b_bytes + c_bytes, stream)) return rc;
+      buf = static_cast<uint8_t*>(w.realigned.ptr);
+    }
+    RealignBatch batch{};
+    auto add = [&](const uint16_t* src, long long lds, uint16_t* dst, long long ldd, int rows,
+                   int cols) {
+      batch.job[batch.n] = RealignJob{src, lds, dst, ldd, rows, cols, (cols + 7) / 8 * 8};
+      batch.end[batch.n] = (batch.n ? batch.end[batch.n - 1] : 0) +
+                           scale_grid(*d, 1ll * rows * ((cols + 7) / 8));
+      ++batch.n;
+    };
+    if (a_bytes) {
+      uint16_t* const dst = reinterpret_cast<uint16_t*>(buf);
+      add(A, lda, dst, lda2, a_rows, a_cols);
+      A = dst;
+      lda = lda2;
+      buf += a_bytes;
+    }
+    if (b_bytes) {
+      uint16_t* const dst = reinterpret_cast<uint16_t*>(buf);
+      if (q.gate) {
+        add(B, ldb, dst, ldb2, b_rows, N);
+        add(B + g.up, ldb, dst + n8, ldb2, b_rows, N);
+        g.up = static_cast<int>(n8);
+        b_cols = static_cast<int>(2 * n8);
+      } else {
+        add(B, ldb, dst, ldb2, b_rows, b_cols);
+      }
+      B = dst;
+      ldb = ldb2;
+      buf += b_bytes;
+    }
+    if (c_bytes) {
+      uint16_t* const dst = reinterpret_cast<uint16_t*>(buf);
+      if (q.beta != 0.0f) add(C, ldc, dst, n8, M, N);
+      c_user = C;
+      ldc_user = ldc;
+      C = dst;
+      ldc = n8;
+    }
+    if (batch.n > 0) {
+      if (launch_realign_f16(batch, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+      prepass = true;
+    }
+  }
+  const bool vec_c = q.c_f32 && aligned16(q.C) && ldc % 4 == 0;
+  const int epi = q.c_f32 ? (vec_c && N % 4 == 0 ? kEpiF32Tma : kEpiF32)
+                          : ((c_ok || copy_c) && dc_ok ? kEpiTma : kEpiManual);
+  const int bn_out = q.gate ? 128 : 256;
+
+  TcArgs a{};
+  a.wait_operands = 1;
+  a.pdl = prepass || q.follows;
+  a.A = A;
+  a.B = B;
+  a.C = C;
+  a.Cf = q.c_f32 ? static_cast<float*>(q.C) : nullptr;
+  a.vec_c = vec_c;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.lda = lda;
+  a.ldb = ldb;
+  a.ldc = ldc;
+  a.alpha = q.alpha;
+  a.beta = q.beta;
+  a.tiles_m = (M + 2 * kBM - 1) / (2 * kBM);
+  a.tiles_n = (N + bn_out - 1) / bn_out;
+  a.kb_total = (K + kBK - 1) / kBK;
+  a.splits = 1;
+  a.kb_per_split = a.kb_total;
+  a.group_m = 8;
+  a.wait_limit_ns = static_cast<unsigned long long>(g_wait_limit_ns.load());
+  a.status = d->status;
+  const long long tiles = 1ll * a.tiles_m * a.tiles_n;
+  if (tiles * 4 > 0x7fffffffll) return GEMM_ERR_ARG;
+  const long long slots = tc_pair_max_clusters(epi);
+  if (slots <= 0) return GEMM_ERR_CUDA;
+  a.dp_tiles = static_cast<int>(tiles);
+  a.tail_splits = 1;
+  a.tail_kb_per_split = a.kb_total;
+  long long workers = std::min(tiles, slots);
+  const char* cut = "";
+  const long long rem = tiles % slots;
+  const int first_kb = tail_first_slice(tiles, slots, a.kb_total);
+  if (first_kb > 0) {
+    a.dp_tiles = static_cast<int>(tiles - rem);
+    a.tail_splits = 2;
+    a.tail_kb_per_split = first_kb;
+    a.tail_first = 1;
+    workers = slots;
+    const size_t need = sizeof(float) * static_cast<size_t>(rem) * 2 * 2 * kBM * 256;
+    std::lock_guard<std::mutex> lk(g_mu);
+    StreamWs* w = nullptr;
+    if (int rc = stream_scratch(d, stream, need, static_cast<size_t>(rem) * 2 * 8, &w)) return rc;
+    a.tail_ws = static_cast<float*>(w->parts.ptr);
+    a.tail_counters = static_cast<unsigned long long*>(w->counters.ptr);
+    a.epoch = ++w->epoch;
+    if (a.epoch == 0) a.epoch = ++w->epoch;   // 0 marks never-used counters
+    cut = ".ktail";
+  } else if (rem > 0 && 2 * rem <= slots) {
+    a.dp_tiles = static_cast<int>(tiles - rem);
+    a.tail_splits = 2;
+    a.tail_halves = 1;
+    workers = std::min<long long>(slots, a.dp_tiles > 0 ? slots : 2 * rem);
+    cut = ".halves";
+  }
+  a.num_units = static_cast<int>(a.dp_tiles + (tiles - a.dp_tiles) * a.tail_splits);
+
+  CUtensorMap tmA{}, tmB{}, tmC{}, tmU{};
+  if (int rc = make_map_f16(&tmA, A, a_rows, a_cols, lda, 64, q.trans_a ? 64 : kBM)) return rc;
+  if (int rc = make_map_f16(&tmB, B, b_rows, b_cols, ldb, 64, 64)) return rc;
+  if (epi == kEpiTma) {
+    if (int rc = make_map_f16(&tmC, C, M, N, ldc, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
+    if (q.gate == 2)
+      if (int rc = make_map_f16(&tmU, g.dU, M, N, ldc, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
+  } else if (epi == kEpiF32Tma) {
+    if (int rc = make_map_f32(&tmC, a.Cf, M, N, ldc, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
+  }
+  const int grid = 2 * static_cast<int>(std::min<long long>(a.num_units, workers));
+  snprintf(t_path_buf, sizeof(t_path_buf), "f16.tc.pair.%s%s%s%s%s%s%s%s",
+           q.trans_a ? "ta." : "", q.trans_b ? "tb." : "", q.scaled ? "scaled." : "",
+           q.gate == 2 ? "gate_grad." : (q.gate ? "gate." : ""),
+           epi == kEpiF32Tma ? "epi_f32_tma"
+                             : (epi == kEpiF32 ? "epi_f32" : (epi == kEpiTma ? "epi_tma" : "epi_manual")),
+           cut, prepass ? ".realigned" : "", c_user ? ".c" : "");
+  t_last_path = t_path_buf;
+  const cudaError_t e =
+      q.gate || q.scaled
+          ? launch_gemm_f16_tc_gate(q.gate, q.scaled, epi, tmA, tmB, tmC, tmU, g, a, grid, stream)
+          : launch_gemm_f16_tc_trans(q.trans_a, q.trans_b, epi, tmA, tmB, tmC, a, grid, stream);
+  if (e != cudaSuccess) return GEMM_ERR_CUDA;
+  if (!c_user) return GEMM_OK;
+  const RealignJob j{C, ldc, c_user, ldc_user, M, N};
+  return launch_unalign_f16(j, scale_grid(*d, 1ll * M * (N / 8 + 2)), stream) == cudaSuccess
+             ? GEMM_OK
+             : GEMM_ERR_CUDA;
+}
+
 int lock_stream(cudaStream_t stream, std::unique_lock<std::recursive_mutex>* call) {
   DevState* d = nullptr;
   if (int rc = device_state(&d, nullptr)) return rc;

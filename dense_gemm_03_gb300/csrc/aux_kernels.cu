@@ -100,7 +100,7 @@ __device__ __forceinline__ uint4 shift_bytes(uint4 lo, uint4 hi, uint32_t m) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// dst[r][c] = src[r][c] for c < cols, 0 for cols <= c < ldd (ldd % 8 == 0,
+// dst[r][c] = src[r][c] for c < cols, 0 for cols <= c < width (width % 8 == 0,
 // dst 16-byte aligned).  One thread writes 8 halves.  A fully valid source
 // piece at any 2-byte alignment is read as the (at most two) 16-byte-aligned
 // blocks that contain it -- blocks that hold at least one element of the
@@ -108,8 +108,9 @@ __device__ __forceinline__ uint4 shift_bytes(uint4 lo, uint4 hi, uint32_t m) {
 // place; the ragged end of a row uses element loads.
 __device__ __forceinline__ void realign_rows(const uint16_t* __restrict__ src, long long lds,
                                              uint16_t* __restrict__ dst, long long ldd, int rows,
-                                             int cols, long long block, long long nblocks) {
-  const long long groups = ldd / 8;
+                                             int cols, long long width, long long block,
+                                             long long nblocks) {
+  const long long groups = width / 8;
   const long long total = static_cast<long long>(rows) * groups;
   for (long long g = block * blockDim.x + threadIdx.x; g < total; g += nblocks * blockDim.x) {
     const int r = static_cast<int>(g / groups);
@@ -142,7 +143,8 @@ __global__ void realign_f16_kernel(const RealignBatch b) {
   while (i + 1 < b.n && static_cast<int>(blockIdx.x) >= b.end[i]) ++i;
   const int first = i ? b.end[i - 1] : 0;
   const RealignJob& j = b.job[i];
-  realign_rows(j.src, j.lds, j.dst, j.ldd, j.rows, j.cols, blockIdx.x - first, b.end[i] - first);
+  realign_rows(j.src, j.lds, j.dst, j.ldd, j.rows, j.cols, j.width ? j.width : j.ldd,
+               blockIdx.x - first, b.end[i] - first);
   // this block's copies are issued: the GEMM launched next may be scheduled
   // (it waits for this kernel's completion before reading the copies)
   griddep_launch_dependents();

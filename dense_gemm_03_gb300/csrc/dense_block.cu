@@ -1,0 +1,257 @@
+// dense_block.cu -- the gated block of a dense model, its gradients, and products
+// with transposed operands: argument checks, alignment copies and path choice.
+//
+//   glu       C := f(X Wg) .* (X Wu),  W = [Wg Wu]
+//   gradient  G = X Wg and U = X Wu again (one gated product whose epilogue reads dC),
+//             dG = dC .* U .* f'(G), dU = dC .* f(G), dGU = [dG dU];
+//             dX := dGU W^T, dW := X^T dGU + beta dW
+//   trans     C := alpha op(A) op(B) + beta C
+//
+// Two ways for each product: whole 256 x 256 tiles on CTA pairs
+// (gemm_f16_tc_kernel.cuh), or, where a few rows or few tiles would leave SMs idle, fp32
+// partial sums by K chunks with their sum in a kernel of its own (lora_stream.cu,
+// stream_sum.cu).  Sums are fp32; every result is rounded once.
+#include "gemm.h"
+#include "lora.h"
+#include "operands.h"
+#include "stream.h"
+
+namespace gb300 {
+namespace {
+
+bool known_act(int act) {
+  return act == GEMM_ACT_SILU || act == GEMM_ACT_GELU || act == GEMM_ACT_GELU_TANH ||
+         act == GEMM_ACT_RELU;
+}
+
+int blank(uint16_t* C, long long ldc, int M, int N, float beta, const LoraDevice& d,
+          cudaStream_t stream) {
+  return launch_scale_f16(C, ldc, M, N, beta, 8 * d.sms, stream) == cudaSuccess ? GEMM_OK
+                                                                               : GEMM_ERR_CUDA;
+}
+
+// The streamed form: op(X) op(W) with `cols` columns, then the sum `s` (its parts are
+// filled in here).
+int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ldw, bool trans_w,
+             int M, int cols, int K, StreamSum s, const LoraDevice& d, cudaStream_t stream,
+             bool* copied) {
+  Aligned x(X, ldx, trans_x ? K : M, trans_x ? M : K, true);
+  Aligned w(W, ldw, trans_w ? cols : K, trans_w ? K : cols, true);
+  const size_t copies = x.bytes() + w.bytes();
+  RowStream r{X, W, ldx, ldw, M, cols, K, trans_x, trans_w};
+  s.parts = row_stream_parts(r, d.sms);
+  void* buf = nullptr;
+  if (int rc = routed_scratch(stream, copies + s.parts.bytes, &buf)) return rc;
+  if (int rc = align_operands({{x, &X, &ldx}, {w, &W, &ldw}}, static_cast<uint8_t*>(buf), d.sms,
+                              stream))
+    return rc;
+  r.X = X;
+  r.W = W;
+  r.ldx = ldx;
+  r.ldw = ldw;
+  s.parts.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + copies);
+  if (int rc = row_stream(r, s.parts, d, stream)) return rc;
+  *copied = copies != 0;
+  return stream_sum(s, d, stream);
+}
+
+struct GluArgs {
+  const uint16_t *X, *W;
+  int M, N, K, ldx, ldw, act;
+};
+
+// gate 1: C := f(G) .* U; gate 2: C = dGU.
+int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, int lddc,
+          const LoraDevice& d, cudaStream_t stream) {
+  GateArgs g{};
+  g.act = p.act;
+  g.up = p.N;
+  g.dC = dC;
+  g.lddc = lddc;
+  g.dU = gate == 2 ? C + p.N : nullptr;
+  if (lora_stream_suits(p.M, 2 * p.N, d.sms)) {
+    StreamSum s{};
+    s.C = C;
+    s.ldc = ldc;
+    s.M = p.M;
+    s.N = p.N;
+    s.gate = gate;
+    s.g = g;
+    bool copied = false;
+    if (int rc = streamed(p.X, p.ldx, false, p.W, p.ldw, false, p.M, 2 * p.N, p.K, s, d, stream,
+                          &copied))
+      return rc;
+    set_last_path(copied ? "glu.stream.realigned" : "glu.stream");
+    return GEMM_OK;
+  }
+  PairCall q{};
+  q.A = p.X;
+  q.B = p.W;
+  q.C = C;
+  q.M = p.M;
+  q.N = p.N;
+  q.K = p.K;
+  q.lda = p.ldx;
+  q.ldb = p.ldw;
+  q.ldc = ldc;
+  q.alpha = 1.0f;
+  q.gate = gate;
+  q.g = g;
+  return gemm_f16_pair(q, stream);
+}
+
+// C := alpha op(A) op(B) + beta C, checked, with M, N, K > 0 and alpha != 0.
+int transposed(const uint16_t* A, const uint16_t* B, void* C, bool f32, bool ta, bool tb, int M,
+               int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
+               const LoraDevice& d, cudaStream_t stream) {
+  if (lora_stream_suits(M, N, d.sms)) {
+    StreamSum s{};
+    s.C = C;
+    s.ldc = ldc;
+    s.M = M;
+    s.N = N;
+    s.alpha = alpha;
+    s.beta = beta;
+    s.f32 = f32;
+    bool copied = false;
+    if (int rc = streamed(A, lda, ta, B, ldb, tb, M, N, K, s, d, stream, &copied)) return rc;
+    set_last_path(copied ? "trans.stream.realigned" : "trans.stream");
+    return GEMM_OK;
+  }
+  PairCall q{};
+  q.A = A;
+  q.B = B;
+  q.C = C;
+  q.c_f32 = f32;
+  q.M = M;
+  q.N = N;
+  q.K = K;
+  q.lda = lda;
+  q.ldb = ldb;
+  q.ldc = ldc;
+  q.alpha = alpha;
+  q.beta = beta;
+  q.trans_a = ta;
+  q.trans_b = tb;
+  return gemm_f16_pair(q, stream);
+}
+
+int device(LoraDevice* d) { return query_device(&d->sms, &d->status, &d->wait_limit_ns); }
+
+int trans_entry(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, void* C, bool f32,
+                int M, int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
+                cudaStream_t stream) {
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
+  if ((trans_a != 0 && trans_a != 1) || (trans_b != 0 && trans_b != 1)) return GEMM_ERR_ARG;
+  if (!trans_a && !trans_b)
+    return f32 ? gemm_f16_f32out(A, B, static_cast<float*>(C), M, N, K, lda, ldb, ldc, alpha, beta,
+                                 stream)
+               : gemm_f16_ld(A, B, static_cast<uint16_t*>(C), M, N, K, lda, ldb, ldc, alpha, beta,
+                             stream);
+  if (M == 0 || N == 0) {
+    set_last_path("noop");
+    return GEMM_OK;
+  }
+  if (ldc < N || (K > 0 && (lda < (trans_a ? M : K) || ldb < (trans_b ? K : N)))) return GEMM_ERR_LD;
+  const bool some = K > 0 && alpha != 0.0f;
+  if (!C || (some && (!A || !B))) return GEMM_ERR_NULL;
+  if (misaligned({A, B}, 2) || misaligned({C}, f32 ? 4 : 2)) return GEMM_ERR_ARG;
+  LoraDevice d{};
+  if (int rc = device(&d)) return rc;
+  std::unique_lock<std::recursive_mutex> call;
+  if (int rc = lock_stream(stream, &call)) return rc;
+  if (!some) {
+    set_last_path("trans.scale");
+    if (!f32) return blank(static_cast<uint16_t*>(C), ldc, M, N, beta, d, stream);
+    return launch_scale_f32(static_cast<float*>(C), ldc, M, N, beta, 8 * d.sms, stream) == cudaSuccess
+               ? GEMM_OK
+               : GEMM_ERR_CUDA;
+  }
+  return transposed(A, B, C, f32, trans_a != 0, trans_b != 0, M, N, K, lda, ldb, ldc, alpha, beta, d,
+                    stream);
+}
+
+}  // namespace
+}  // namespace gb300
+
+using namespace gb300;
+
+extern "C" {
+
+int gemm_f16_trans(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, uint16_t* C,
+                   int M, int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
+                   cudaStream_t stream) {
+  return trans_entry(trans_a, trans_b, A, B, C, false, M, N, K, lda, ldb, ldc, alpha, beta, stream);
+}
+
+int gemm_f16_trans_f32out(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, float* C,
+                          int M, int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
+                          cudaStream_t stream) {
+  return trans_entry(trans_a, trans_b, A, B, C, true, M, N, K, lda, ldb, ldc, alpha, beta, stream);
+}
+
+int gemm_f16_glu(const uint16_t* X, const uint16_t* W, uint16_t* C, int M, int N, int K, int act,
+                 int ldx, int ldw, int ldc, cudaStream_t stream) {
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
+  if (!known_act(act) || N > GEMM_GLU_MAX_N) return GEMM_ERR_ARG;
+  if (M == 0 || N == 0) {
+    set_last_path("noop");
+    return GEMM_OK;
+  }
+  if (ldc < N || (K > 0 && (ldx < K || ldw < 2 * N))) return GEMM_ERR_LD;
+  if (!C || (K > 0 && (!X || !W))) return GEMM_ERR_NULL;
+  if (misaligned({X, W, C}, 2)) return GEMM_ERR_ARG;
+  LoraDevice d{};
+  if (int rc = device(&d)) return rc;
+  std::unique_lock<std::recursive_mutex> call;
+  if (int rc = lock_stream(stream, &call)) return rc;
+  if (K == 0) {
+    set_last_path("glu.blank");
+    return blank(C, ldc, M, N, 0.0f, d, stream);
+  }
+  return gated(GluArgs{X, W, M, N, K, ldx, ldw, act}, 1, C, ldc, nullptr, 0, d, stream);
+}
+
+int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, uint16_t* dGU,
+                      uint16_t* dX, uint16_t* dW, int M, int N, int K, int act, int lddc, int ldx,
+                      int ldw, int lddgu, int lddx, int lddw, float beta, cudaStream_t stream) {
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
+  if (!known_act(act) || N > GEMM_GLU_MAX_N) return GEMM_ERR_ARG;
+  const bool want_gu = M > 0 && N > 0;   // dGU has elements, and every product some
+  const bool want_dx = dX && M > 0 && K > 0, want_dw = dW && N > 0 && K > 0;
+  if (!want_gu && !want_dx && !want_dw) {
+    set_last_path("noop");
+    return GEMM_OK;
+  }
+  const bool some = want_gu && K > 0;
+  if ((want_gu && lddgu < 2 * N) || (some && (lddc < N || ldx < K || ldw < 2 * N)) ||
+      (want_dx && lddx < K) || (want_dw && lddw < 2 * N))
+    return GEMM_ERR_LD;
+  if ((want_gu && !dGU) || (some && (!dC || !X || !W))) return GEMM_ERR_NULL;
+  if (misaligned({dC, X, W, dGU, dX, dW}, 2)) return GEMM_ERR_ARG;
+  LoraDevice d{};
+  if (int rc = device(&d)) return rc;
+  std::unique_lock<std::recursive_mutex> call;
+  if (int rc = lock_stream(stream, &call)) return rc;
+  if (!some) {   // no sums: zeros, and dW as beta leaves it
+    set_last_path("glu_grad.blank");
+    if (want_gu)
+      if (int rc = blank(dGU, lddgu, M, 2 * N, 0.0f, d, stream)) return rc;
+    if (want_dx)
+      if (int rc = blank(dX, lddx, M, K, 0.0f, d, stream)) return rc;
+    return want_dw ? blank(dW, lddw, K, 2 * N, beta, d, stream) : GEMM_OK;
+  }
+  if (int rc = gated(GluArgs{X, W, M, N, K, ldx, ldw, act}, 2, dGU, lddgu, dC, lddc, d, stream))
+    return rc;
+  if (want_dx)
+    if (int rc = transposed(dGU, W, dX, false, false, true, M, K, 2 * N, lddgu, ldw, lddx, 1.0f,
+                            0.0f, d, stream))
+      return rc;
+  if (want_dw)
+    if (int rc = transposed(X, dGU, dW, false, true, false, K, 2 * N, M, ldx, lddgu, lddw, 1.0f,
+                            beta, d, stream))
+      return rc;
+  return GEMM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,73 @@
+// gate.cuh -- the activations of a gated block, f(g) and f'(g) in fp32.
+//
+//   silu       f = g s,             s = 1 / (1 + e^-g);      f' = s (1 + g (1 - s))
+//   gelu       f = g P,             P = erfc(-g / sqrt 2) / 2;   f' = P + g phi(g)
+//   gelu_tanh  f = g s,             s = 1 / (1 + e^-2z) = (1 + tanh z) / 2,
+//              z = sqrt(2/pi) (g + 0.044715 g^3);           f' = s + 2 g z' s (1 - s)
+//   relu       f = max(g, 0);                                f' = 1 for g > 0, else 0
+// Both forms of s are exact in the tails (no difference of near-equal numbers): a
+// large negative g makes e^-g infinite and s zero.  1 - s is taken as e^-g s, which
+// keeps its bits where s is near 1.  A NaN stays a NaN.
+#pragma once
+#include <type_traits>
+
+#include "gemm.h"
+
+namespace gb300 {
+
+// s = 1 / (1 + e^-x) and 1 - s.  e^-x past the largest float: s = 0 and 1 - s = 1.
+__device__ __forceinline__ float gate_logistic(float x, float& rest) {
+  const float e = __expf(-x);
+  const float s = __fdividef(1.0f, 1.0f + e);   // 0 past 2^126
+  rest = e < 0x1p60f ? e * s : 1.0f;
+  return s;
+}
+
+constexpr float kGeluC = 0.7978845608028654f;    // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// f(g), and f'(g) into d.
+template <int ACT>
+__device__ __forceinline__ float gate_both(float g, float& d) {
+  if (ACT == GEMM_ACT_SILU) {
+    float rest;
+    const float s = gate_logistic(g, rest);
+    d = s * fmaf(g, rest, 1.0f);
+    return g * s;
+  }
+  if (ACT == GEMM_ACT_GELU) {
+    const float P = 0.5f * erfcf(-0.7071067811865476f * g);
+    d = fmaf(g, 0.3989422804014327f * __expf(-0.5f * g * g), P);
+    return g * P;
+  }
+  if (ACT == GEMM_ACT_GELU_TANH) {
+    const float g2 = g * g;
+    float rest;
+    const float s = gate_logistic(2.0f * kGeluC * g * fmaf(kGeluA, g2, 1.0f), rest);
+    const float dz = 2.0f * kGeluC * fmaf(3.0f * kGeluA, g2, 1.0f);
+    // past any use of the product dz could overflow: s or 1 - s is zero there
+    d = fabsf(g) > 16.0f ? s : fmaf(g * dz, s * rest, s);
+    return g * s;
+  }
+  d = g > 0.0f || g != g ? 1.0f : 0.0f;
+  return g > 0.0f || g != g ? g : 0.0f;
+}
+
+template <int ACT>
+__device__ __forceinline__ float gate_value(float g) {
+  float d;
+  return gate_both<ACT>(g, d);
+}
+
+// fn(constant) with the constant the activation `act` is.
+template <class F>
+__device__ __forceinline__ void gate_dispatch(int act, F&& fn) {
+  switch (act) {
+    case GEMM_ACT_SILU: fn(std::integral_constant<int, GEMM_ACT_SILU>{}); break;
+    case GEMM_ACT_GELU: fn(std::integral_constant<int, GEMM_ACT_GELU>{}); break;
+    case GEMM_ACT_GELU_TANH: fn(std::integral_constant<int, GEMM_ACT_GELU_TANH>{}); break;
+    default: fn(std::integral_constant<int, GEMM_ACT_RELU>{}); break;
+  }
+}
+
+}  // namespace gb300

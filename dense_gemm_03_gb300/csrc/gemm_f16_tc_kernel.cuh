@@ -46,6 +46,7 @@
 // Epilogue staging tile: 32 rows x 32 halves, 64-byte swizzle: row r at r*64 B,
 //            16-byte chunk c stored at chunk (c ^ ((r / 2) % 4)).
 #pragma once
+#include "gate.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -475,11 +476,40 @@ __device__ __forceinline__ void add_partials(uint32_t (&acc)[32], const float4* 
   }
 }
 
-// The plain product: nothing is added to a tile's K loop, B is stored K x N.
+// The plain product: nothing is added to a tile's K loop, A is stored M x K, B
+// K x N.
 struct NoLora {
   static constexpr bool kOn = false;
-  static constexpr bool kTransB = false;
+  static constexpr bool kTransA = false;   // A is stored K x M (an MN-major operand)
+  static constexpr bool kTransB = false;   // B is stored N x K (a K-major operand)
+  static constexpr int kGate = 0;          // 1: gated product, 2: its gradient
+  static constexpr bool kScaled = false;   // results scaled by row and column
   static constexpr int kWarps = 0;
+};
+
+// Operands stored transposed (CTA pairs, TMA loads).  A stage's part of A is then
+// two blocks of 64 (k) rows x 64 halves, like B's.
+template <bool TRANSA, bool TRANSB>
+struct Transposed : NoLora {
+  static constexpr bool kTransA = TRANSA;
+  static constexpr bool kTransB = TRANSB;
+};
+
+// Gated products (CTA pairs, TMA loads): B is K x 2 up, the gate's columns and,
+// `up` columns on, those it gates.  A 256-wide tile takes 128 columns of each:
+// CTA 0 of the pair stages the gate's, CTA 1 the others (B's halves of one MMA), so
+// the operand traffic and the main loop are those of the plain product, and G
+// and U of an output sit in the same TMEM lane, 128 columns apart, where the
+// epilogue joins them: C = f(G) .* U, or with GATE == 2 the gradients dG = dC .* U .*
+// f'(G) to C and dU = dC .* f(G) to dU.  p.N counts output columns.
+// SCALED: results (G and U, or the plain product's) are multiplied by sx[row] and
+// sw[column of B].
+template <int GATE, bool SCALED>
+struct Gated : NoLora {
+  static constexpr int kGate = GATE;
+  static constexpr bool kScaled = SCALED;
+  CUtensorMap tmU;        // GATE == 2: dU, as tmC is dG
+  GateArgs a;
 };
 
 // Low-rank adapters picked by row, as more k-blocks of the same accumulators
@@ -494,7 +524,7 @@ struct NoLora {
 // TRANSB: B operands are stored N x K and
 // N x R (the gradient's dC W^T + U A^T): K-major tiles of 64-row boxes.
 template <bool TRANSB>
-struct LoraTail {
+struct LoraTail : NoLora {
   static constexpr bool kOn = true;
   static constexpr bool kTransB = TRANSB;
   static constexpr int kWarps = 2;
@@ -526,6 +556,12 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   constexpr int S = Cfg::kStages;
   static_assert(!PAIR || (LOAD == kLoadTma && EPI != kEpiPartial), "pair configuration");
   static_assert(!LORA::kOn || (PAIR && BN == 256 && KPB == 1), "adapters run on 256-wide pairs");
+  constexpr int kGate = LORA::kGate;
+  static_assert(!(LORA::kTransA || LORA::kTransB || kGate || LORA::kScaled) ||
+                    (PAIR && BN == 256 && KPB == 1),
+                "transposed operands and gates run on 256-wide pairs");
+  static_assert(!kGate || EPI == kEpiTma || EPI == kEpiManual, "gated results are halves");
+  constexpr int kBn = kGate ? BN / 2 : BN;   // output columns of a tile
   // MM = 64: 64-row tiles (tcgen05.mma with M = 64), whole-K units only, TMA
   // loads of 64 rows of A and the TMA epilogue
   static_assert(MM == 128 || (MM == 64 && AM == 64 && !PAIR && EPI == kEpiTma), "64-row tiles");
@@ -655,7 +691,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         uint32_t qphase = 0;
         UnitCursor cur = first_unit(p, worker);
         Unit t;
-        while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
+        while (ok && next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, t)) {
           for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
             if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 1)) {
               ok = false;
@@ -665,7 +701,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             const int nk = KPB == 1 ? 1 : min(KPB, t.kb1 - kb);
             // B columns this CTA gives the MMA (a half-width unit needs half of
             // them), staged in whole 64-column boxes
-            const int bcols = PAIR ? t.ncols / 2 : t.ncols;
+            const int bcols = PAIR && !kGate ? t.ncols / 2 : t.ncols;
             const uint32_t bytes =
                 static_cast<uint32_t>(nk * (kAB + ((bcols + 63) / 64) * kBBlockBytes));
             if (PAIR) {
@@ -677,11 +713,18 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
               for (int j = 0; j < nk; ++j) {
                 const uint32_t sa = stage_a(stage) + j * Cfg::kKbBytes, sb = sa + kAB;
                 const int k0 = (kb + j) * BK;
-                tma_load_2d_pair(sa, &tmA, fb, k0, t.m0);
+                if constexpr (LORA::kTransA) {
+                  tma_load_2d_pair(sa, &tmA, fb, t.m0, k0);
+                  tma_load_2d_pair(sa + kBBlockBytes, &tmA, fb, t.m0 + 64, k0);
+                } else {
+                  tma_load_2d_pair(sa, &tmA, fb, k0, t.m0);
+                }
+                int first = t.n0 + static_cast<int>(rank) * bcols;
+                if constexpr (kGate != 0) first = t.n0 + (leader ? 0 : x.a.up);
 #pragma unroll
                 for (int c = 0; c < Cfg::kBStageCols / 64; ++c)
                   if (64 * c < bcols) {
-                    const int n = t.n0 + static_cast<int>(rank) * bcols + 64 * c;
+                    const int n = first + 64 * c;
                     if constexpr (LORA::kTransB)
                       tma_load_2d_pair(sb + c * kBBlockBytes, &tmB, fb, k0, n);
                     else
@@ -815,8 +858,9 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
       constexpr uint32_t kBMajor = LORA::kTransB ? 0u : 1u;
-      constexpr uint32_t idesc_full = make_idesc(0u, PAIR ? 2 * BM : MM, BN, 0u, kBMajor);
-      constexpr uint32_t idesc_half = make_idesc(0u, PAIR ? 2 * BM : MM, BN / 2, 0u, kBMajor);
+      constexpr uint32_t kAMajor = LORA::kTransA ? 1u : 0u;
+      constexpr uint32_t idesc_full = make_idesc(0u, PAIR ? 2 * BM : MM, BN, kAMajor, kBMajor);
+      constexpr uint32_t idesc_half = make_idesc(0u, PAIR ? 2 * BM : MM, BN / 2, kAMajor, kBMajor);
       uint32_t vphase = 0;   // adapters: bit s is the parity of stage s's next V tile
       int qi = 0;
       uint32_t qphase = 0;
@@ -825,11 +869,11 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       bool ok = true;
       UnitCursor cur = first_unit(p, worker);
       Unit t;
-      while (ok && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t)) {
+      while (ok && next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, t)) {
         const uint32_t buf = local & 1u, use = local >> 1;
         if (!wait_parity(acce_bar(buf), (use & 1u) ^ 1u, limit, st, 3)) break;
         tc_fence_after();
-        const uint32_t idesc = t.ncols == BN ? idesc_full : idesc_half;
+        const uint32_t idesc = t.ncols == kBn ? idesc_full : idesc_half;
         const uint32_t d_tmem = tmem_base + buf * Cfg::kAccStride;
         for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
           if (!wait_parity(full_bar(stage), phase, limit, st, 4)) {
@@ -842,7 +886,9 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             const uint32_t a0 = stage_a(stage) + j * Cfg::kKbBytes, b0 = a0 + kAB;
 #pragma unroll
             for (int kk = 0; kk < BK / kUmmaK; ++kk) {
-              const uint64_t ad = smem_desc_sw128(a0 + kk * (kUmmaK * 2), 16u, 1024u);
+              const uint64_t ad =
+                  LORA::kTransA ? smem_desc_sw128(a0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u)
+                                : smem_desc_sw128(a0 + kk * (kUmmaK * 2), 16u, 1024u);
               const uint64_t bd =
                   LORA::kTransB ? smem_desc_sw128(b0 + kk * (kUmmaK * 2), 16u, 1024u)
                                 : smem_desc_sw128(b0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u);
@@ -1019,7 +1065,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
     // warps of each TMEM lane quadrant: part h takes chunks [lo, hi) (the first
     // part takes the odd one of a 224-wide tile).  kSubs: most chunks of a warp.
     constexpr int kParts = R::kEpiWarps / 4;
-    constexpr int kSubs = (BN / kSubCols + kParts - 1) / kParts;
+    constexpr int kSubs = (kBn / kSubCols + kParts - 1) / kParts;
     const int ew = warp - R::kEpiWarp0;   // 0 .. kEpiWarps-1
     const int q = warp & 3;               // TMEM lane quadrant -> rows 32q .. 32q+31
     // Tile rows per lane quadrant: 32 (row 32q + l in TMEM lane 32q + l), or
@@ -1082,13 +1128,168 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       for (int j = 0; j < NB; ++j)
         if (kTc * j < wc && cw + kTc * j < p.N) load_c_sub_tma(j, cw + kTc * j, r0);
     };
+    // scales of this thread's row and of a sub-chunk's columns (the same for every
+    // lane: broadcast loads)
+    [[maybe_unused]] float sx_row = 1.0f;
+    [[maybe_unused]] auto scales_of = [&](int col0, int ncols, float (&s)[kSubCols]) {
+      if constexpr (LORA::kScaled) {
+#pragma unroll
+        for (int i = 0; i < kSubCols; ++i)
+          s[i] = x.a.sw && col0 + i < ncols ? __ldg(x.a.sw + col0 + i) : 1.0f;
+      }
+    };
+    // a gate's gradient: dC of one row for a sub-chunk, read into registers
+    [[maybe_unused]] uint4 dc_next[4];
+    [[maybe_unused]] auto load_dc = [&](int r, int col0, uint4 (&dst)[4]) {
+      if constexpr (kGate == 2) {
+        const uint4* src =
+            reinterpret_cast<const uint4*>(x.a.dC + static_cast<long long>(r) * x.a.lddc + col0);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          dst[g] = (r < p.M && col0 + 8 * g < p.N) ? __ldcs(src + g) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // 32 x 32 results (this lane's row) to columns col0.. of dst: through a staging
+    // tile, by TMA or with predicated element stores
+    [[maybe_unused]] auto store_sub = [&](const CUtensorMap* tm, uint16_t* dst, long long ld,
+                                          int col0, int row0, const uint32_t (&v)[32]) {
+      const uint32_t b = EPI == kEpiTma ? nstore & 1u : 0u;
+      uint8_t* const sptr = sptr0 + b * kEpiBufBytes;
+      if (EPI == kEpiTma && lane == 0) bulk_wait_group_read<1>();   // the tile's last store has read it
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<uint4*>(sptr + sw64_chunk(lane, g)) =
+            epilogue8(v + 8 * g, make_uint4(0u, 0u, 0u, 0u), false, 1.0f, 0.0f);
+      if (EPI == kEpiTma) {
+        fence_proxy_async_smem();   // generic writes -> TMA store reads
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(tm, sbuf0 + b * kEpiBufBytes, col0, row0);
+          bulk_commit_group();
+        }
+        ++nstore;
+      } else {
+        __syncwarp();
+        uint16_t o[32];
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+          o[r] = *reinterpret_cast<const uint16_t*>(sptr + sw64_elem(r, lane));
+        uint16_t* const out = dst + static_cast<long long>(row0) * ld + col0 + lane;
+#pragma unroll
+        for (int r = 0; r < 32; ++r)
+          if (row0 + r < p.M && col0 + lane < p.N) out[static_cast<long long>(r) * ld] = o[r];
+        __syncwarp();
+      }
+    };
+    // Joins G and U of this warp's columns of a finished unit.
+    [[maybe_unused]] auto gated_epilogue = [&](const Unit& u, int tail_part, uint32_t tbase,
+                                               int wcol0, int nsub, int colw, int row0, int row) {
+      if constexpr (kGate != 0) {
+        // a sub-chunk of the accumulator at TMEM column wcol0 + off: of a shared
+        // tile the sum of every slice's, in slice order, this one's from TMEM
+        auto sums = [&](int off, uint32_t (&acc)[32], uint32_t (&own)[32]) {
+          tmem_ld_32x32b_x32(tbase + off, own);
+          tmem_wait_regs(own);
+          const float4* part =
+              tail_partials(p, tail_part, 0, BN) + 32 * q + lane + (wcol0 + off) / 4 * BM;
+          for (int s2 = 0; s2 < u.npieces; ++s2, part += BN / 4 * BM) {
+            if (s2 != u.split) {
+              add_partials(acc, part, s2 == 0);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                acc[i] = s2 == 0 ? own[i]
+                                 : __float_as_uint(__uint_as_float(acc[i]) + __uint_as_float(own[i]));
+            }
+          }
+        };
+        for (int k = 0; k < nsub; ++k) {
+          const int col0 = colw + kSubCols * k;
+          if (col0 >= p.N) break;
+          uint32_t ga[32], ua[32];
+          if (u.tail) {
+            uint32_t own[32];
+            sums(kSubCols * k, ga, own);
+            sums(kSubCols * k + u.ncols, ua, own);
+          } else {
+            tmem_ld_32x32b_x32(tbase + kSubCols * k, ga);
+            tmem_ld_32x32b_x32(tbase + kSubCols * k + u.ncols, ua);
+            tmem_wait_ld32(ga, ua);
+          }
+          if constexpr (LORA::kScaled) {
+            float s[kSubCols];
+            scales_of(col0, p.N, s);
+#pragma unroll
+            for (int i = 0; i < kSubCols; ++i)
+              ga[i] = __float_as_uint(__uint_as_float(ga[i]) * sx_row * s[i]);
+            scales_of(p.N + col0, 2 * p.N, s);
+#pragma unroll
+            for (int i = 0; i < kSubCols; ++i)
+              ua[i] = __float_as_uint(__uint_as_float(ua[i]) * sx_row * s[i]);
+          }
+          if constexpr (kGate == 1) {
+            gate_dispatch(x.a.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                ga[i] = __float_as_uint(gate_value<decltype(act)::value>(__uint_as_float(ga[i])) *
+                                        __uint_as_float(ua[i]));
+            });
+            store_sub(&tmC, p.C, p.ldc, col0, row0, ga);
+          } else {
+            uint4 dc[4];
+            if (EPI == kEpiTma) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) dc[g] = dc_next[g];
+              if (k + 1 < nsub && col0 + kSubCols < p.N) load_dc(row, col0 + kSubCols, dc_next);
+            } else {
+              // column-wise (coalesced) through the staging tile
+              const uint16_t* const src =
+                  x.a.dC + static_cast<long long>(row0) * x.a.lddc + col0 + lane;
+              uint16_t v[32];
+#pragma unroll
+              for (int r = 0; r < 32; ++r)
+                v[r] = row0 + r < p.M && col0 + lane < p.N
+                           ? __ldg(src + static_cast<long long>(r) * x.a.lddc)
+                           : static_cast<uint16_t>(0);
+#pragma unroll
+              for (int r = 0; r < 32; ++r)
+                *reinterpret_cast<uint16_t*>(sptr0 + sw64_elem(r, lane)) = v[r];
+              __syncwarp();
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                dc[g] = *reinterpret_cast<const uint4*>(sptr0 + sw64_chunk(lane, g));
+            }
+            gate_dispatch(x.a.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const uint4 c4 = dc[i / 8];
+                const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
+                const float2 c2 = half2_bits_to_float2(w[(i % 8) / 2]);
+                const float c[2] = {c2.x, c2.y};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float df;
+                  const float f =
+                      gate_both<decltype(act)::value>(__uint_as_float(ga[i + j]), df);
+                  ga[i + j] = __float_as_uint(c[j] * __uint_as_float(ua[i + j]) * df);
+                  ua[i + j] = __float_as_uint(c[j] * f);
+                }
+              }
+            });
+            store_sub(&tmC, p.C, p.ldc, col0, row0, ga);
+            store_sub(&x.tmU, x.a.dU, p.ldc, col0, row0, ua);
+          }
+        }
+      }
+    };
     UnitCursor cur = first_unit(p, worker);
     Unit t, tn;
-    bool have = next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t);
+    bool have = next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, t);
     if (kCs && have) load_c_head(t);
     while (have) {
       // kCs looks one unit ahead (its C tile is loaded during the next main loop)
-      const bool have_next = kCs && next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, tn);
+      const bool have_next = kCs && next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, tn);
       const uint32_t buf = local & 1u, use = local >> 1;
       const int row0 = t.m0 + kQRows * q;
       // tail bookkeeping is per CTA: the rows of one CTA of a pair form their own part
@@ -1120,7 +1321,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           const float4* part =
               tail_partials(p, tail_part, s2, BN) + (wcol0 / 4 + lane) * BM + 32 * q;
 #pragma unroll
-          for (int l = 0; l < 4; ++l) prefetch_l2(part + 8 * l);
+          for (int l = 0; l < 4; ++l) {
+            prefetch_l2(part + 8 * l);
+            if (kGate != 0) prefetch_l2(part + t.ncols / 4 * BM + 8 * l);
+          }
         }
       }
       // adapters: this row's, when the epilogue has to add it (its weights are not
@@ -1141,6 +1345,11 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       // C of the first sub-chunk is requested before the accumulator is ready.
       uint4 c_next[4];
       if (!kCs && EPI == kEpiTma && has_c && finish && !t.tail) load_c_sub(p, row, colw, c_next);
+      if constexpr (LORA::kScaled)
+        sx_row = x.a.sx && finish && row < p.M ? __ldg(x.a.sx + row) : 1.0f;
+      if constexpr (kGate == 2) {
+        if (EPI == kEpiTma && finish) load_dc(row, colw, dc_next);
+      }
       if (!wait_parity(accf_bar(buf), use & 1u, limit, st, 5)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
@@ -1165,12 +1374,15 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           // Publish this slice's partial sums, then count the slice in; the last
           // slice to arrive finishes the tile.
           float4* mine = tail_partials(p, tail_part, t.split, BN) + 32 * q + lane;
-          for (int k = 0; k < kSubs; ++k) {
-            if (k >= nsub || colw + kSubCols * k >= p.N) break;
+          for (int k = 0; k < (kGate ? 2 : 1) * kSubs; ++k) {
+            // (a gate's chunks, then those it gates)
+            const int kc = k < kSubs ? k : k - kSubs, col = kSubCols * kc;
+            const int off = k < kSubs ? col : col + t.ncols;
+            if (kc >= nsub || colw + col >= p.N) continue;
             uint32_t acc[32];
-            tmem_ld_32x32b_x32(tbase + kSubCols * k, acc);
+            tmem_ld_32x32b_x32(tbase + off, acc);
             tmem_wait_regs(acc);
-            const int cq0 = (wcol0 + kSubCols * k) / 4;
+            const int cq0 = (wcol0 + off) / 4;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               __stcg(mine + (cq0 + i) * BM,
@@ -1214,7 +1426,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         for (int b = 0; b < NB; ++b) ok_c = wait_c_sub(b) && ok_c;
         if (!ok_c) break;
       }
-      if (finish) {
+      if constexpr (kGate != 0) {
+        if (finish) gated_epilogue(t, tail_part, tbase, wcol0, nsub, colw, row0, row);
+      }
+      if (kGate == 0 && finish) {
         uint32_t acc_a[32], acc_b[32];
         if (!t.tail) {
           tmem_ld_32x32b_x32(tbase, acc_a);
@@ -1318,6 +1533,13 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
                 }
               }
             }
+          }
+          if constexpr (LORA::kScaled) {
+            float s[kSubCols];
+            scales_of(col0, p.N, s);
+#pragma unroll
+            for (int i = 0; i < kSubCols; ++i)
+              cur[i] = __float_as_uint(__uint_as_float(cur[i]) * sx_row * s[i]);
           }
           if (EPI == kEpiPartial) {
             if (row < p.M) {
@@ -1483,7 +1705,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         t = tn;
         have = have_next;
       } else {
-        have = next_unit(p, cur, worker, nworkers, BN, bm_tile, rank, t);
+        have = next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, t);
       }
     }
     // C loads still in flight (a wait above gave up) must land before exit

@@ -139,6 +139,45 @@ cudaError_t launch_gemm_f16_tc_lora(bool trans, int epi_mode, const CUtensorMap&
                                     const LoraTailArgs& tail,
                                     const TcArgs& args, int grid, cudaStream_t stream);
 
+// What a gated or scaled product needs beside the product's own operands.
+struct GateArgs {
+  int act;             // GEMM_ACT_*
+  int up;              // columns of B from a gate's to the one it gates
+  const uint16_t* dC;  // gradient: M x N, rows lddc apart
+  long long lddc;
+  uint16_t* dU;        // gradient: beside C (dG), the same leading dimension
+  const float *sx, *sw;   // scales by row and by column of B (NULL: ones)
+};
+// Variants of the pair kernel: operands stored transposed (half or float C) ...
+cudaError_t launch_gemm_f16_tc_trans(bool trans_a, bool trans_b, int epi_mode,
+                                     const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                     const CUtensorMap& tmC, const TcArgs& args, int grid,
+                                     cudaStream_t stream);
+// ... gated products (gate 1), their gradient (gate 2), and products scaled by row and
+// column (gate 0 or 1); tmU: dU's map (gate 2).
+cudaError_t launch_gemm_f16_tc_gate(int gate, bool scaled, int epi_mode, const CUtensorMap& tmA,
+                                    const CUtensorMap& tmB, const CUtensorMap& tmC,
+                                    const CUtensorMap& tmU, const GateArgs& gate_args,
+                                    const TcArgs& args, int grid, cudaStream_t stream);
+// A product through one of those variants.  op(A) is M x K, op(B) K x N; with
+// `gate` B is K x (up + N) and C the gated result (gate 1), or dG with dU beside it
+// (gate 2).  C is float when c_f32.  Rows of A and B, and of a half C, that are off
+// the 16-byte grid are copied.  Returns a GEMM_* code.
+struct PairCall {
+  const uint16_t *A, *B;
+  void* C;
+  bool c_f32;
+  int M, N, K;
+  long long lda, ldb, ldc;
+  float alpha, beta;
+  bool trans_a, trans_b;
+  int gate;
+  bool scaled;
+  GateArgs g;
+  bool follows;        // launched right after a kernel of the same call
+};
+int gemm_f16_pair(const PairCall& call, cudaStream_t stream);
+
 // Tensor-core fp16 GEMM (tcgen05).  Maps are ignored by the modes that do not
 // use them.  kpb: k-blocks per ring stage, 1, or 2 for 64-wide tiles with TMA
 // loads and epilogue.  Returns a cudaError_t from the launch.
@@ -199,13 +238,15 @@ cudaError_t launch_splitk_reduce_f16(const float* ws, long long ws_ld, int split
                                      int grid, cudaStream_t stream);
 
 // Copies a rows x cols half matrix with any leading dimension and alignment
-// into a 16-byte-aligned one with ldd = cols rounded up to 8 (zero padding).
+// into a 16-byte-aligned one with ldd = cols rounded up to 8 (zero padding), or
+// into `width` columns (a multiple of 8, at least cols) of one with a larger ldd.
 struct RealignJob {
   const uint16_t* src;
   long long lds;
   uint16_t* dst;
   long long ldd;
   int rows, cols;
+  long long width = 0;   // 0: ldd
 };
 // One launch for up to three copies: blocks [end[i-1], end[i]) copy jobs[i].
 struct RealignBatch {

@@ -1,0 +1,203 @@
+// stream_sum.cu -- adds up the fp32 partial sums of a streamed product (few rows,
+// or few tiles with a long K) in chunk order and finishes the result: alpha and
+// beta, scales by row and column, a gate, or a gate's gradient.
+//
+// One block per (row, 128 VEC columns); a thread takes VEC neighbouring columns
+// (four, by 16-byte loads, when that still fills the SMs).  Bound by the latency of two
+// dependent steps, the stream's end and one round of loads: every chunk's are
+// issued before the first is added.
+#include "gate.cuh"
+#include "stream.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kBlockRows = 256;   // of a block of partial sums
+
+template <int VEC>
+__device__ __forceinline__ void load_part(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 4) {
+    const float4 q = __ldcg(reinterpret_cast<const float4*>(p));
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  } else {
+    v[0] = __ldcg(p);
+  }
+}
+
+// The sums of columns c .. c + VEC - 1 of row `row` (columns of the stream; a block's
+// last columns may lie past N, inside its unit).
+template <int VEC>
+__device__ __forceinline__ void add_chunks(const StreamParts& p, int row, int c, float (&s)[VEC]) {
+  const int blk = row / kBlockRows;
+  const long long step = static_cast<long long>(p.block_rows) * 128;
+  const float* src = p.part +
+                     (static_cast<long long>(blk) * p.units + (c >> 7)) * p.chunks * step +
+                     (row - blk * kBlockRows) * 128 + (c & 127);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) s[i] = 0.0f;
+  int k = 0;
+  for (; k + 8 <= p.chunks; k += 8, src += 8 * step) {
+    float v[8][VEC];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) load_part<VEC>(src + u * step, v[u]);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] += v[u][i];
+  }
+  float v[7][VEC];
+#pragma unroll
+  for (int u = 0; u < 7; ++u)
+    if (k + u < p.chunks) load_part<VEC>(src + u * step, v[u]);
+#pragma unroll
+  for (int u = 0; u < 7; ++u)
+    if (k + u < p.chunks)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] += v[u][i];
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_half(const uint16_t* p, bool vec, int n, float (&v)[VEC]) {
+  if (VEC == 4 && vec) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    const float2 a = lora_h2f2(q.x), b = lora_h2f2(q.y);
+    v[0] = a.x; v[VEC > 1 ? 1 : 0] = a.y; v[VEC > 2 ? 2 : 0] = b.x; v[VEC > 3 ? 3 : 0] = b.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = i < n ? lora_h2f(p[i]) : 0.0f;
+  }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_half(uint16_t* p, bool vec, int n, const float (&v)[VEC]) {
+  if (VEC == 4 && vec) {
+    uint2 q;
+    q.x = lora_f2h(v[0]) | static_cast<uint32_t>(lora_f2h(v[VEC > 1 ? 1 : 0])) << 16;
+    q.y = lora_f2h(v[VEC > 2 ? 2 : 0]) | static_cast<uint32_t>(lora_f2h(v[VEC > 3 ? 3 : 0])) << 16;
+    *reinterpret_cast<uint2*>(p) = q;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (i < n) p[i] = lora_f2h(v[i]);
+  }
+}
+
+// vec: the results' rows (and dC's) are on the grid of VEC elements.
+template <int GATE, bool F32, bool SCALED, int VEC>
+__global__ void __launch_bounds__(kThreads) stream_sum_kernel(const StreamSum p, bool vec) {
+  griddep_launch_dependents();
+  const int strips = (p.N + kThreads * VEC - 1) / (kThreads * VEC);
+  const int row = blockIdx.x / strips;
+  const int c = ((blockIdx.x - row * strips) * kThreads + static_cast<int>(threadIdx.x)) * VEC;
+  const int n = min(VEC, p.N - c);   // columns that exist
+  griddep_wait();
+  if (n <= 0) return;
+  const bool v = vec && n == VEC;
+  const long long at = row * p.ldc + c;
+  float s[VEC], u[VEC];
+  add_chunks<VEC>(p.parts, row, c, s);
+  if constexpr (GATE != 0) add_chunks<VEC>(p.parts, row, p.N + c, u);
+  if constexpr (SCALED) {
+    const float sx = p.g.sx ? __ldg(p.g.sx + row) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      s[i] = s[i] * sx * (p.g.sw && i < n ? __ldg(p.g.sw + c + i) : 1.0f);
+      if constexpr (GATE != 0) u[i] = u[i] * sx * (p.g.sw && i < n ? __ldg(p.g.sw + p.N + c + i) : 1.0f);
+    }
+  }
+  if constexpr (GATE == 0) {
+    if constexpr (F32) {
+      float* const dst = static_cast<float*>(p.C) + at;
+      if (VEC == 4 && v) {
+        float4 old = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p.beta != 0.0f) old = *reinterpret_cast<const float4*>(dst);
+        const float o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          s[i] = p.beta != 0.0f ? fmaf(p.alpha, s[i], p.beta * o[i]) : p.alpha * s[i];
+        *reinterpret_cast<float4*>(dst) = make_float4(s[0], s[VEC > 1 ? 1 : 0], s[VEC > 2 ? 2 : 0],
+                                                      s[VEC > 3 ? 3 : 0]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          if (i < n) dst[i] = p.beta != 0.0f ? fmaf(p.alpha, s[i], p.beta * dst[i]) : p.alpha * s[i];
+      }
+    } else {
+      uint16_t* const dst = static_cast<uint16_t*>(p.C) + at;
+      float old[VEC];
+      if (p.beta != 0.0f) load_half<VEC>(dst, v, n, old);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        s[i] = p.beta != 0.0f ? fmaf(p.alpha, s[i], p.beta * old[i]) : p.alpha * s[i];
+      store_half<VEC>(dst, v, n, s);
+    }
+  } else if constexpr (GATE == 1) {
+    gate_dispatch(p.g.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s[i] = gate_value<decltype(act)::value>(s[i]) * u[i];
+    });
+    store_half<VEC>(static_cast<uint16_t*>(p.C) + at, v, n, s);
+  } else {
+    float dc[VEC];
+    load_half<VEC>(p.g.dC + row * p.g.lddc + c, v, n, dc);
+    gate_dispatch(p.g.act, [&](auto act) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        float df;
+        const float f = gate_both<decltype(act)::value>(s[i], df);
+        s[i] = dc[i] * u[i] * df;
+        u[i] = dc[i] * f;
+      }
+    });
+    store_half<VEC>(static_cast<uint16_t*>(p.C) + at, v, n, s);
+    store_half<VEC>(p.g.dU + at, v, n, u);
+  }
+}
+
+template <int GATE, bool F32, bool SCALED>
+cudaError_t launch(const StreamSum& s, const LoraDevice& d, cudaStream_t stream) {
+  // four columns a thread where that still gives the SMs a block each, and where U's
+  // columns lie on the same grid as G's
+  const long long strips4 = (s.N + 4 * kThreads - 1) / (4 * kThreads);
+  const bool wide = s.M * strips4 >= d.sms && (GATE == 0 || s.N % 4 == 0);
+  const long long strips = wide ? strips4 : (s.N + kThreads - 1) / kThreads;
+  const long long blocks = s.M * strips;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const uintptr_t elem = F32 ? 16 : 8;
+  uintptr_t bits = reinterpret_cast<uintptr_t>(s.C);
+  bool vec = s.ldc % 4 == 0;
+  if (GATE == 2) {
+    bits |= reinterpret_cast<uintptr_t>(s.g.dC) | reinterpret_cast<uintptr_t>(s.g.dU);
+    vec = vec && s.g.lddc % 4 == 0;
+  }
+  vec = vec && bits % elem == 0;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return wide ? cudaLaunchKernelEx(&cfg, stream_sum_kernel<GATE, F32, SCALED, 4>, s, vec)
+              : cudaLaunchKernelEx(&cfg, stream_sum_kernel<GATE, F32, SCALED, 1>, s, vec);
+}
+
+}  // namespace
+
+int stream_sum(const StreamSum& s, const LoraDevice& d, cudaStream_t stream) {
+  cudaError_t e = cudaErrorInvalidValue;
+  if (s.gate == 0)
+    e = s.scaled ? launch<0, false, true>(s, d, stream)
+        : s.f32  ? launch<0, true, false>(s, d, stream)
+                 : launch<0, false, false>(s, d, stream);
+  else if (s.gate == 1)
+    e = s.scaled ? launch<1, false, true>(s, d, stream) : launch<1, false, false>(s, d, stream);
+  else if (!s.scaled)
+    e = launch<2, false, false>(s, d, stream);
+  return counted_launch(e) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+}  // namespace gb300

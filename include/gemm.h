@@ -229,6 +229,65 @@ int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_t* W1, cons
                  int renormalize, int ldx, int ldy, float beta, cudaStream_t stream);
 
 /*
+ * Dense block: the gated projections of a model's feed-forward block, their
+ * gradients, products with transposed operands, and products in 8-bit integers.
+ * Same types, layouts, streams, graphs, scratch and errors as above; results overlap
+ * no operand.
+ *
+ * C := alpha * op(A) * op(B) + beta * C with op(A) = A, or A^T where trans_a is 1;
+ * likewise B (another value: GEMM_ERR_ARG).  M, N, K are those of op(A) (M x K) and
+ * op(B) (K x N): with trans_a A is stored K x M, lda >= M; with trans_b B is stored
+ * N x K, ldb >= K.  The gradients of C = X * W are products of this kind: dX = dC * W^T
+ * and dW = X^T * dC (in float, beta = 1 adds up micro-batches).  Otherwise as
+ * gemm_f16_ld and gemm_f16_f32out, which do the work when neither is transposed.
+ */
+int gemm_f16_trans(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, uint16_t* C,
+                   int M, int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
+                   cudaStream_t stream);
+int gemm_f16_trans_f32out(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, float* C,
+                          int M, int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
+                          cudaStream_t stream);
+
+/* Activations of a gate: f(g) = g / (1 + e^-g); g times the normal distribution
+ * function; its approximation g / (1 + e^-2z), z = sqrt(2/pi) (g + 0.044715 g^3); max(g, 0). */
+#define GEMM_ACT_NONE       -1   /* gemm_i8 only: no gate */
+#define GEMM_ACT_SILU        0
+#define GEMM_ACT_GELU        1
+#define GEMM_ACT_GELU_TANH   2
+#define GEMM_ACT_RELU        3
+#define GEMM_GLU_MAX_N  (1 << 29)   /* most output columns of a gate */
+
+/*
+ * C := f(X * Wg) .* (X * Wu), both projections, the activation and the product in
+ * one pass over W = [Wg Wu].
+ *   X  M x K half, ldx >= K       W  K x 2N half: N gate columns, then N up columns,
+ *   C  M x N half, ldc >= N          ldw >= 2N
+ * act is GEMM_ACT_SILU ... GEMM_ACT_RELU, N at most GEMM_GLU_MAX_N (else GEMM_ERR_ARG).
+ * Both sums, f and the product are fp32; C is rounded once.  K == 0: C := 0.
+ */
+int gemm_f16_glu(const uint16_t* X, const uint16_t* W, uint16_t* C, int M, int N, int K, int act,
+                 int ldx, int ldw, int ldc, cudaStream_t stream);
+
+/*
+ * The gradients of gemm_f16_glu for a given dC (M x N half, lddc >= N).  G = X * Wg and
+ * U = X * Wu are computed again (nothing is kept from the forward call):
+ *
+ *     dGU := [dC .* U .* f'(G),  dC .* f(G)]     M x 2N half, lddgu >= 2N
+ *     dX  := dGU * W^T                           M x K half, lddx >= K
+ *     dW  := X^T * dGU + beta * dW               K x 2N half, lddw >= 2N
+ *
+ * dGU is computed in fp32 and rounded to half once; dX and dW are products of what it
+ * then holds (entries past the half range are infinite, small ones rounded to the
+ * half's 2^-24 grid: scale the loss, as in any training in half), summed in fp32 and
+ * rounded once.  dX and dW may each be NULL (not wanted); dGU may not.  For a dW in
+ * float call gemm_f16_trans_f32out on X and dGU.  f'(0) is 0 for GEMM_ACT_RELU.
+ * K == 0: dGU := 0.
+ */
+int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, uint16_t* dGU,
+                      uint16_t* dX, uint16_t* dW, int M, int N, int K, int act, int lddc, int ldx,
+                      int ldw, int lddgu, int lddx, int lddw, float beta, cudaStream_t stream);
+
+/*
  * Host-buffer forms: A, B, C are HOST pointers (pinned memory gives the
  * fastest copies and lets them overlap; pageable memory works).  On a
  * library-owned copy-in stream the call copies B, then A and C (C when

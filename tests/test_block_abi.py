@@ -1,0 +1,87 @@
+"""Argument checks of the dense block's entry points: no GPU is touched."""
+import pytest
+
+import dense_gemm_03_gb300 as g
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.fixture(scope="module")
+def L():
+    from dense_gemm_03_gb300 import build
+    build.build()
+    return g.lib()
+
+
+@pytest.mark.parametrize("name", ["gemm_f16_trans", "gemm_f16_trans_f32out"])
+def test_trans_refusals(L, name):
+    f = getattr(L, name)
+    def call(ta, tb, M, N, K, lda, ldb, ldc, A=16, B=16, C=16):
+        return f(ta, tb, A, B, C, M, N, K, lda, ldb, ldc, 1.0, 0.0, None)
+    assert call(1, 0, -1, 4, 4, 4, 4, 4) == -2
+    assert call(1, 0, 4, 4, -1, 4, 4, 4) == -2
+    assert call(2, 0, 4, 4, 4, 4, 4, 4) == -7
+    assert call(0, -1, 4, 4, 4, 4, 4, 4) == -7
+    assert call(1, 0, 8, 4, 4, 7, 4, 4) == -3      # A is K x M
+    assert call(0, 1, 4, 4, 8, 8, 7, 4) == -3      # B is N x K
+    assert call(1, 1, 4, 4, 8, 4, 7, 4) == -3
+    assert call(1, 0, 4, 4, 4, 4, 4, 3) == -3
+    assert call(0, 0, 4, 4, 4, 3, 4, 4) == -3      # as gemm_f16_ld
+    assert call(1, 0, 4, 4, 4, 4, 4, 4, A=None) == -1
+    assert call(1, 0, 4, 4, 4, 4, 4, 4, C=None) == -1
+    assert call(1, 0, 4, 4, 4, 4, 4, 4, A=17) == -7
+    assert call(1, 0, 4, 4, 4, 4, 4, 4, C=17) == -7
+    assert call(1, 0, 0, 4, 4, 0, 4, 4, A=None, B=None, C=None) == 0
+    assert call(1, 0, 4, 0, 4, 4, 0, 0, A=None, B=None, C=None) == 0
+
+
+def test_glu_refusals(L):
+    def call(M, N, K, act=0, ldx=8, ldw=16, ldc=8, X=16, W=16, C=16):
+        return L.gemm_f16_glu(X, W, C, M, N, K, act, ldx, ldw, ldc, None)
+    assert call(-1, 8, 8) == -2 and call(8, -8, 8) == -2 and call(8, 8, -8) == -2
+    assert call(8, 8, 8, act=-1) == -7 and call(8, 8, 8, act=4) == -7
+    assert call(8, (1 << 29) + 1, 8, ldw=BIG, ldc=BIG) == -7
+    assert call(8, 8, 8, ldx=7) == -3 and call(8, 8, 8, ldw=15) == -3 and call(8, 8, 8, ldc=7) == -3
+    for missing in ("X", "W", "C"):
+        assert call(8, 8, 8, **{missing: None}) == -1
+        assert call(8, 8, 8, **{missing: 17}) == -7
+    assert call(8, 8, 0, C=None) == -1
+    assert call(0, 8, 8, X=None, W=None, C=None) == 0
+
+
+def test_glu_grad_refusals(L):
+    ok = dict(dC=16, X=16, W=16, dGU=16, dX=16, dW=16, M=8, N=8, K=8, act=0, lddc=8, ldx=8, ldw=16,
+              lddgu=16, lddx=8, lddw=16, beta=0.0)
+    def call(**k):
+        return L.gemm_f16_glu_grad(*{**ok, **k}.values(), None)
+    for name in ("M", "N", "K"):
+        assert call(**{name: -1}) == -2
+    assert call(act=-1) == -7 and call(act=4) == -7 and call(N=(1 << 29) + 1) == -7
+    for name in ("lddc", "ldx", "ldw", "lddgu", "lddx", "lddw"):
+        assert call(**{name: ok[name] - 1}) == -3
+    for name in ("dC", "X", "W", "dGU"):
+        assert call(**{name: None}) == -1
+    for name in ("dC", "X", "W", "dGU", "dX", "dW"):
+        assert call(**{name: 17}) == -7
+    assert call(dGU=None, dX=None, dW=None) == -1
+    # not wanted: their leading dimensions are not looked at
+    assert call(dX=None, dW=None, lddx=0, lddw=0, dC=17) == -7
+    assert call(M=0, dC=None, X=None, W=None, dGU=None, dX=None, dW=None) == 0
+    assert call(M=0, dW=None, dC=None, X=None, W=None, dGU=None) == 0
+
+
+def test_binding_shapes(L):
+    torch = pytest.importorskip("torch")
+    z = lambda *s: torch.zeros(*s, dtype=torch.float16)
+    with pytest.raises(ValueError, match="K of W and X"):
+        g.gemm_f16_glu(z(2, 8), z(9, 8), z(2, 4))
+    with pytest.raises(ValueError, match="columns"):
+        g.gemm_f16_glu(z(2, 8), z(8, 7), z(2, 4))
+    with pytest.raises(ValueError, match="activation"):
+        g.gemm_f16_glu(z(2, 8), z(8, 8), z(2, 4), "tanh")
+    with pytest.raises(ValueError, match="K of W and X"):
+        g.gemm_f16_glu_grad(z(2, 4), z(2, 8), z(9, 8), z(2, 8))
+    with pytest.raises(ValueError, match="K of B and A"):
+        g.gemm_f16_trans(z(8, 2), z(9, 4), z(2, 4), True)
+    with pytest.raises(g.GemmError):
+        g.gemm_f16_glu(16, 16, 16, M=-1, N=1, K=1)
