@@ -17,7 +17,7 @@ import threading
 __all__ = [
     "GemmError", "lib", "library_path", "gemm_f16", "gemm_f16_f32out", "f32_to_f16",
     "sgemm_f32", "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe", "gemm_f16_trans",
-    "gemm_f16_trans_f32out", "gemm_f16_glu", "gemm_f16_glu_grad", "gemm_f16_host",
+    "gemm_f16_trans_f32out", "gemm_f16_glu", "gemm_f16_glu_grad", "gemm_i8", "f16_to_i8", "gemm_f16_host",
     "sgemm_f32_host", "gemm_f16_splitk_noalloc", "l2_flush", "force_path", "force_splits", "stage_kblocks",
     "set_wait_limit_ns",
     "debug_status", "last_path", "launch_count", "plan_stream_k", "release", "EXPORTS",
@@ -36,7 +36,7 @@ EXPORTS = (
     "gemm_f16_splitk_noalloc", "gemm_launch_count", "gemm_plan_stream_k", "gemm_f16_f32out",
     "gemm_f32_to_f16", "gemm_debug_wait_probe", "gemm_plan_tf32_slices", "gemm_stage_kblocks",
     "gemm_f16_lora", "gemm_f16_lora_grad", "gemm_f16_moe", "gemm_f16_trans",
-    "gemm_f16_trans_f32out", "gemm_f16_glu", "gemm_f16_glu_grad",
+    "gemm_f16_trans_f32out", "gemm_f16_glu", "gemm_f16_glu_grad", "gemm_i8", "gemm_f16_to_i8",
 )
 
 # Activations of a gate, by the names the calls take.
@@ -96,6 +96,10 @@ def lib():
             L.gemm_f16_glu.argtypes = [vp] * 3 + [i] * 7 + [vp]
             L.gemm_f16_glu_grad.restype = i
             L.gemm_f16_glu_grad.argtypes = [vp] * 6 + [i] * 10 + [f, vp]
+            L.gemm_i8.restype = i
+            L.gemm_i8.argtypes = [vp] * 5 + [i] * 7 + [f, vp]
+            L.gemm_f16_to_i8.restype = i
+            L.gemm_f16_to_i8.argtypes = [vp] * 3 + [i] * 4 + [vp]
             L.gemm_f16_splitk_noalloc.restype = i
             L.gemm_f16_splitk_noalloc.argtypes = [vp, vp, vp, i, i, i, i, i, i, f, f, i, vp]
             L.gemm_l2_flush.restype = i
@@ -457,6 +461,59 @@ def gemm_f16_glu_grad(dC, X, W, dGU, dX=None, dW=None, act="silu", beta=0.0, M=N
         2 * N if lddw is None else lddw, beta, _stream(stream))
     if rc:
         _check(rc, "gemm_f16_glu_grad")
+
+
+def _int8(x, name):
+    """The address of a matrix of 8-bit integers."""
+    try:
+        if _dtype_names[x.dtype] == "int8":
+            return x.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    if x is None or isinstance(x, int):
+        return x
+    if _dtype_name(x) != "int8":
+        raise TypeError("%s is %s, not int8" % (name, _dtype_name(x)))
+    return _addr(x)
+
+
+def gemm_i8(X, W, C, sx=None, sw=None, act=None, beta=0.0, M=None, N=None, K=None, ldx=None,
+            ldw=None, ldc=None, stream=None):
+    """C := sx[i]*sw[n]*(X*W) + beta*C on device int8 operands, sx and sw fp32 or
+    None for ones, C fp16.  With an activation W is (K, 2N), sw has 2N scales and
+    C := f(G) .* U of the scaled gate and up products."""
+    whole = K is None
+    if M is None or K is None:
+        m, k = X.shape
+        M, K = m if M is None else M, k if K is None else K
+    if N is None:
+        k, N = W.shape
+        if k != K and whole:
+            _differ("K of W and X", k, K)
+        if act is not None:
+            if N % 2:
+                raise ValueError("W has %d columns: a gate and an up column for each output" % N)
+            N //= 2
+    cols = N if act is None else 2 * N
+    rc = (_lib or lib()).gemm_i8(
+        _int8(X, "X"), _int8(W, "W"), _addr(C), _typed(sx, "float32", M, "sx"),
+        _typed(sw, "float32", cols, "sw"), M, N, K, -1 if act is None else _act(act),
+        K if ldx is None else ldx, cols if ldw is None else ldw, N if ldc is None else ldc, beta,
+        _stream(stream))
+    if rc:
+        _check(rc, "gemm_i8")
+
+
+def f16_to_i8(X, Q, scales, M=None, K=None, ldx=None, ldq=None, stream=None):
+    """scales[i] := max|X_i| / 127 (fp32), Q_i := X_i / scales[i] to the nearest int8."""
+    if M is None or K is None:
+        m, k = X.shape
+        M, K = m if M is None else M, k if K is None else K
+    rc = (_lib or lib()).gemm_f16_to_i8(_addr(X), _int8(Q, "Q"), _typed(scales, "float32", M, "scales"),
+                                        M, K, K if ldx is None else ldx, K if ldq is None else ldq,
+                                        _stream(stream))
+    if rc:
+        _check(rc, "gemm_f16_to_i8")
 
 
 def gemm_f16_host(A, B, C, alpha=1.0, beta=0.0, M=None, N=None, K=None, lda=None, ldb=None,

@@ -1419,7 +1419,8 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   long long workers = std::min(tiles, slots);
   const char* cut = "";
   const long long rem = tiles % slots;
-  const int first_kb = tail_first_slice(tiles, slots, a.kb_total);
+  // (float results are folded by whole K)
+  const int first_kb = q.c_f32 ? 0 : tail_first_slice(tiles, slots, a.kb_total);
   if (first_kb > 0) {
     a.dp_tiles = static_cast<int>(tiles - rem);
     a.tail_splits = 2;
@@ -1523,6 +1524,12 @@ int encode_map_f16_stack(CUtensorMap* map, const void* ptr, int rows, int cols, 
 int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
                    int box_cols, int box_rows) {
   return make_map_f16(map, ptr, rows, cols, ld, box_cols, box_rows);
+}
+
+int encode_map_i8(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld, int box_cols,
+                  int box_rows) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, rows, cols, ld, box_cols, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }

@@ -38,7 +38,7 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   Aligned x(X, ldx, trans_x ? K : M, trans_x ? M : K, true);
   Aligned w(W, ldw, trans_w ? cols : K, trans_w ? K : cols, true);
   const size_t copies = x.bytes() + w.bytes();
-  RowStream r{X, W, ldx, ldw, M, cols, K, trans_x, trans_w};
+  RowStream r{X, W, ldx, ldw, M, cols, K, trans_x, trans_w, s.f32};
   s.parts = row_stream_parts(r, d.sms);
   void* buf = nullptr;
   if (int rc = routed_scratch(stream, copies + s.parts.bytes, &buf)) return rc;

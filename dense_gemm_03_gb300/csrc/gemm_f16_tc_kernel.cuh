@@ -484,13 +484,22 @@ struct NoLora {
   static constexpr bool kTransB = false;   // B is stored N x K (a K-major operand)
   static constexpr int kGate = 0;          // 1: gated product, 2: its gradient
   static constexpr bool kScaled = false;   // results scaled by row and column
+  static constexpr bool kFold = false;     // long sums folded into registers
   static constexpr int kWarps = 0;
 };
 
+// With kFold the accumulator holds kFoldKb k-blocks at most; the epilogue warps add
+// these parts up in registers, rounding to nearest.  The tensor core's own additions
+// truncate: over 8192 products the sums drift by 9e-6 of their norm, folded every
+// 1024 by 1e-6.
+constexpr int kFoldKb = 16;
+
 // Operands stored transposed (CTA pairs, TMA loads).  A stage's part of A is then
-// two blocks of 64 (k) rows x 64 halves, like B's.
-template <bool TRANSA, bool TRANSB>
+// two blocks of 64 (k) rows x 64 halves, like B's.  FOLD: float results of long sums
+// (gradients over the tokens of a batch), units of whole K only.
+template <bool TRANSA, bool TRANSB, bool FOLD>
 struct Transposed : NoLora {
+  static constexpr bool kFold = FOLD;
   static constexpr bool kTransA = TRANSA;
   static constexpr bool kTransB = TRANSB;
 };
@@ -560,6 +569,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   static_assert(!(LORA::kTransA || LORA::kTransB || kGate || LORA::kScaled) ||
                     (PAIR && BN == 256 && KPB == 1),
                 "transposed operands and gates run on 256-wide pairs");
+  static_assert(!LORA::kFold || (PAIR && KPB == 1 && (EPI == kEpiF32 || EPI == kEpiF32Tma)),
+                "long sums of float results");
   static_assert(!kGate || EPI == kEpiTma || EPI == kEpiManual, "gated results are halves");
   constexpr int kBn = kGate ? BN / 2 : BN;   // output columns of a tile
   // MM = 64: 64-row tiles (tcgen05.mma with M = 64), whole-K units only, TMA
@@ -870,12 +881,27 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       UnitCursor cur = first_unit(p, worker);
       Unit t;
       while (ok && next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, t)) {
-        const uint32_t buf = local & 1u, use = local >> 1;
-        if (!wait_parity(acce_bar(buf), (use & 1u) ^ 1u, limit, st, 3)) break;
+        uint32_t buf = local & 1u;
+        if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 3)) break;
         tc_fence_after();
         const uint32_t idesc = t.ncols == kBn ? idesc_full : idesc_half;
-        const uint32_t d_tmem = tmem_base + buf * Cfg::kAccStride;
+        uint32_t d_tmem = tmem_base + buf * Cfg::kAccStride;
+        int first_kb = t.kb0;   // of the accumulator in hand
         for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
+          if constexpr (LORA::kFold) {
+            if (kb - first_kb == kFoldKb) {   // this part is the epilogue's now
+              mma_commit_pair_multicast(accf_bar(buf), 3);
+              ++local;
+              buf = local & 1u;
+              if (!wait_parity(acce_bar(buf), ((local >> 1) & 1u) ^ 1u, limit, st, 25)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              d_tmem = tmem_base + buf * Cfg::kAccStride;
+              first_kb = kb;
+            }
+          }
           if (!wait_parity(full_bar(stage), phase, limit, st, 4)) {
             ok = false;
             break;
@@ -892,7 +918,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
               const uint64_t bd =
                   LORA::kTransB ? smem_desc_sw128(b0 + kk * (kUmmaK * 2), 16u, 1024u)
                                 : smem_desc_sw128(b0 + kk * (kUmmaK * 128), kBBlockBytes, 1024u);
-              const uint32_t acc = (kb > t.kb0 || j > 0 || kk > 0) ? 1u : 0u;
+              const uint32_t acc = (kb > first_kb || j > 0 || kk > 0) ? 1u : 0u;
               if (PAIR)
                 mma_f16_ss_pair(d_tmem, ad, bd, idesc, acc);
               else
@@ -1350,12 +1376,50 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       if constexpr (kGate == 2) {
         if (EPI == kEpiTma && finish) load_dc(row, colw, dc_next);
       }
-      if (!wait_parity(accf_bar(buf), use & 1u, limit, st, 5)) break;
-      tc_fence_after();
+      // kFold: this row's sums, every part of the accumulator added as it comes
+      [[maybe_unused]] float sum[LORA::kFold ? kSubs * kSubCols : 1];
+      if constexpr (LORA::kFold) {
+#pragma unroll
+        for (int i = 0; i < kSubs * kSubCols; ++i) sum[i] = 0.0f;
+        bool ok = true;
+        for (int kb = t.kb0; kb < t.kb1; kb += kFoldKb) {
+          const uint32_t b = local & 1u;
+          ok = wait_parity(accf_bar(b), (local >> 1) & 1u, limit, st, 5);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t part = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                b * Cfg::kAccStride + static_cast<uint32_t>(wcol0);
+          if (finish)
+#pragma unroll
+            for (int k = 0; k < kSubs; ++k)
+              if (k < nsub && colw + kSubCols * k < p.N) {
+#pragma unroll
+                for (int c = 0; c < kSubCols; c += 16) {
+                  uint32_t v[8], w[8];
+                  tmem_ld_32x32b_x8(part + kSubCols * k + c, v);
+                  tmem_ld_32x32b_x8(part + kSubCols * k + c + 8, w);
+                  tmem_wait_ld2(v, w);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    sum[kSubCols * k + c + i] += __uint_as_float(v[i]);
+                    sum[kSubCols * k + c + 8 + i] += __uint_as_float(w[i]);
+                  }
+                }
+              }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_cta(acce_bar(b), 0));
+          ++local;
+        }
+        if (!ok) break;
+      } else {
+        if (!wait_parity(accf_bar(buf), use & 1u, limit, st, 5)) break;
+        tc_fence_after();
+      }
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                              buf * Cfg::kAccStride + static_cast<uint32_t>(wcol0);
 
-      if (EPI != kEpiPartial && t.tail && finish) {
+      if (EPI != kEpiPartial && !LORA::kFold && t.tail && finish) {
         unsigned long long* cnt = p.tail_counters + tail_part * kTailCounters + h * 4 + q;
         // If every other slice of the tile has already published, this one
         // finishes the tile straight from TMEM and need not publish.
@@ -1431,7 +1495,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       }
       if (kGate == 0 && finish) {
         uint32_t acc_a[32], acc_b[32];
-        if (!t.tail) {
+        if (!LORA::kFold && !t.tail) {
           tmem_ld_32x32b_x32(tbase, acc_a);
           tmem_wait_regs(acc_a);
         }
@@ -1442,14 +1506,19 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           const int col0 = colw + kSubCols * k;
           if (k >= nsub || col0 >= p.N) break;
           const bool more = k + 1 < nsub && col0 + kSubCols < p.N;
-          if (more && !t.tail) tmem_ld_32x32b_x32(tbase + kSubCols * (k + 1), nxt);   // in flight
+          if constexpr (LORA::kFold) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) cur[i] = __float_as_uint(sum[kSubCols * k + i]);
+          } else {
+            if (more && !t.tail) tmem_ld_32x32b_x32(tbase + kSubCols * (k + 1), nxt);   // in flight
+          }
           uint4 c_cur[4];
           if (!kCs && EPI == kEpiTma) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) c_cur[g] = c_next[g];
             if (has_c && more) load_c_sub(p, row, col0 + kSubCols, c_next);
           }
-          if (EPI != kEpiPartial && t.tail) {
+          if (EPI != kEpiPartial && !LORA::kFold && t.tail) {
             // cur := sum of every slice's partial sums in slice order; this
             // slice's own term is still in TMEM (bit-identical to what it
             // published), so only the other slices are read back.
@@ -1687,19 +1756,21 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
               if (row0 + r < p.M && col_ok) cout[static_cast<long long>(r) * p.ldc] = o[r];
             __syncwarp();
           }
-          if (more && !t.tail) tmem_wait_regs(nxt);
+          if (!LORA::kFold && more && !t.tail) tmem_wait_regs(nxt);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      // the accumulator may be overwritten (with pairs: counted on the leader)
-      if (lane == 0) {
-        if (PAIR)
-          mbar_arrive_cluster(map_to_cta(acce_bar(buf), 0));
-        else
-          mbar_arrive(acce_bar(buf));
+      if constexpr (!LORA::kFold) {
+        tc_fence_before();
+        __syncwarp();
+        // the accumulator may be overwritten (with pairs: counted on the leader)
+        if (lane == 0) {
+          if (PAIR)
+            mbar_arrive_cluster(map_to_cta(acce_bar(buf), 0));
+          else
+            mbar_arrive(acce_bar(buf));
+        }
+        ++local;
       }
-      ++local;
       if (kCs) {
         if (have_next) load_c_head(tn);
         t = tn;

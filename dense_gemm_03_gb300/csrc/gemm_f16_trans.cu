@@ -9,14 +9,15 @@ namespace {
 template <bool TA, bool TB>
 cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
                    const TcArgs& args, int grid, cudaStream_t s) {
-  using T = Transposed<TA, TB>;
+  using T = Transposed<TA, TB, false>;
+  using F = Transposed<TA, TB, true>;
   switch (epi) {
     case kEpiTma:
       return launch_one<256, kLoadTma, kEpiTma, true, 128, 128, 1, T>(a, b, c, args, grid, s);
     case kEpiF32Tma:
-      return launch_one<256, kLoadTma, kEpiF32Tma, true, 128, 128, 1, T>(a, b, c, args, grid, s);
+      return launch_one<256, kLoadTma, kEpiF32Tma, true, 128, 128, 1, F>(a, b, c, args, grid, s);
     case kEpiF32:
-      return launch_one<256, kLoadTma, kEpiF32, true, 128, 128, 1, T>(a, b, c, args, grid, s);
+      return launch_one<256, kLoadTma, kEpiF32, true, 128, 128, 1, F>(a, b, c, args, grid, s);
     default:
       return cudaErrorInvalidValue;
   }

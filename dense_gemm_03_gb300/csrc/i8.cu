@@ -1,0 +1,421 @@
+// i8.cu -- products in 8-bit integers with a scale for each token and channel, and the
+// rounding of tokens to 8 bits: argument checks, path choice and the kernels that
+// turn rows of halves into rows of integers and back.
+//
+//   product    S = X W exactly as integers, C := sx[i] sw[n] S + beta C, or gated
+//   tokens     a = max_k |X[i,k]|, scale[i] = a / 127, Q[i,k] = round(127 X[i,k] / a)
+//
+// Few rows or few tiles: i8_stream.cu (bytes to halves on their way to the tensor
+// cores) and stream_sum.cu.  Else both operands become halves in scratch, read back
+// from L2 by the pair kernel (gemm_f16_tc_kernel.cuh), whose epilogue scales.
+#include <cuda_fp16.h>
+
+#include "gemm.h"
+#include "lora.h"
+#include "operands.h"
+#include "stream.h"
+
+namespace gb300 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------- integers to halves
+// dst[r][c] = src[r][c] for c < cols, 0 for cols <= c < width (a multiple of 16); one
+// thread 16 elements, dst rows on the 16-byte grid.
+struct SpreadJob {
+  const int8_t* src;
+  long long lds;
+  void* dst;
+  long long ldd;
+  int rows, cols, width;
+};
+constexpr int kSpreadJobs = 3;
+struct SpreadBatch {
+  SpreadJob job[kSpreadJobs];
+  int end[kSpreadJobs];   // blocks [end[i-1], end[i]) do job i
+  int n;
+};
+
+// 16 bytes at any address, of which `n` belong to the row.
+__device__ __forceinline__ uint4 load16(const int8_t* p, int n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  if (n >= 16 && (a & 15u) == 0) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (n >= 16) {
+    // the one or two aligned blocks that hold the piece (each holds bytes of it)
+    const uint32_t m = static_cast<uint32_t>(a & 15u);
+    const uint4* const blk = reinterpret_cast<const uint4*>(a - m);
+    const uint4 lo = __ldg(blk), hi = __ldg(blk + 1);
+    const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    const uint32_t sh = (m & 3u) * 8u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (static_cast<int>(m >> 2) == q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(v[q + i], v[q + i + 1 < 8 ? q + i + 1 : 7], sh);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(p + i))) << (8 * (i & 3));
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// HALVES: as halves (every 8-bit integer is one), else as bytes on the 16-byte grid.
+template <bool HALVES>
+__global__ void __launch_bounds__(kThreads) spread_i8_kernel(const SpreadBatch b) {
+  griddep_launch_dependents();
+  int i = 0;
+  while (i + 1 < b.n && static_cast<int>(blockIdx.x) >= b.end[i]) ++i;
+  const int first = i ? b.end[i - 1] : 0;
+  const SpreadJob& j = b.job[i];
+  const int groups = j.width / 16;
+  const long long total = static_cast<long long>(j.rows) * groups;
+  for (long long g = (blockIdx.x - first) * static_cast<long long>(kThreads) + threadIdx.x; g < total;
+       g += static_cast<long long>(b.end[i] - first) * kThreads) {
+    const int r = static_cast<int>(g / groups), c = static_cast<int>(g - static_cast<long long>(r) * groups) * 16;
+    const uint4 q = load16(j.src + r * j.lds + c, j.cols - c);
+    const long long at = r * j.ldd + c;
+    if constexpr (!HALVES) {
+      *reinterpret_cast<uint4*>(static_cast<int8_t*>(j.dst) + at) = q;
+    } else {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {   // byte q + 128 -> 1024 + it -> q (see i8_stream.cu)
+        const uint32_t u = w[k] ^ 0x80808080u;
+        const uint32_t v[2] = {__byte_perm(u, 0x64646464u, 0x4140), __byte_perm(u, 0x64646464u, 0x4342)};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          __half2 h;
+          memcpy(&h, &v[e], 4);
+          h = __hsub2(h, off);
+          memcpy(&o[2 * k + e], &h, 4);
+        }
+      }
+      uint4* const dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.dst) + at);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+int spread(SpreadBatch& b, bool halves, int sms, cudaStream_t stream) {
+  int blocks = 0;
+  for (int i = 0; i < b.n; ++i) {
+    const long long want = (1ll * b.job[i].rows * (b.job[i].width / 16) + kThreads - 1) / kThreads;
+    blocks += static_cast<int>(std::max(1ll, std::min<long long>(want, 16ll * sms)));
+    b.end[i] = blocks;
+  }
+  if (halves)
+    spread_i8_kernel<true><<<blocks, kThreads, 0, stream>>>(b);
+  else
+    spread_i8_kernel<false><<<blocks, kThreads, 0, stream>>>(b);
+  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// ------------------------------------------------------------ tokens to bytes
+// T threads a row, V groups of eight elements a thread kept in registers between the
+// two passes over them (V == 0: a row too long for that, read twice).  Groups lie on
+// Q's 8-byte grid, so that stores are whole; a row's first and last may be ragged.
+//
+// The maximum is taken over the bits of |x|, which order like the values, infinities
+// above them and NaNs above those.  The quotient 127 x / a is x times the rounded 127 / a
+// (off by less than 2^-15), rounded to the nearest integer by adding 1.5 2^23; where it
+// comes within 2^-13 of a tie the division decides: 127 x is exact, and a quotient that is
+// no tie is further from one than its rounding.
+template <int T, int V>
+__global__ void __launch_bounds__(T < 256 ? 256 : T)
+    to_i8_kernel(const uint16_t* __restrict__ X, int8_t* __restrict__ Q, float* __restrict__ scales,
+                 int M, int K, long long ldx, long long ldq) {
+  constexpr int kRowsPerBlock = T < 256 ? 256 / T : 1;
+  __shared__ uint32_t top[32];
+  const int t = static_cast<int>(threadIdx.x) % T;
+  const int row = blockIdx.x * kRowsPerBlock + static_cast<int>(threadIdx.x) / T;
+  const bool there = row < M;   // (uniform over a warp)
+  const uint16_t* const x = X + (there ? row * ldx : 0);
+  int8_t* const q = Q + (there ? row * ldq : 0);
+  const int md = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 7u);
+  const int groups = there ? (K + md + 7) / 8 : 0;
+  auto load = [&](int j) {
+    const int e0 = 8 * j - md;
+    if (e0 >= 0 && e0 + 8 <= K) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(x + e0);
+      const uint32_t m = static_cast<uint32_t>(a & 15u);
+      const uint4* const blk = reinterpret_cast<const uint4*>(a - m);
+      const uint4 lo = __ldcs(blk);
+      if (m == 0) return lo;
+      const uint4 hi = __ldcs(blk + 1);   // (holds elements of the group)
+      const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      const uint32_t sh = (m & 3u) * 8u;
+      uint32_t o[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (static_cast<int>(m >> 2) == s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = __funnelshift_r(w[s + i], w[s + i + 1 < 8 ? s + i + 1 : 7], sh);
+      return make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = e0 + i >= 0 && e0 + i < K ? __ldg(x + e0 + i) : 0u;
+    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  };
+  uint32_t m2 = 0u;
+  auto look = [&](uint4 v) {
+    constexpr uint32_t kAbs = 0x7FFF7FFFu;
+    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
+  };
+  uint4 kept[V > 0 ? V : 1];
+  if constexpr (V > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) kept[i] = t + T * i < groups ? load(t + T * i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < V; ++i) look(kept[i]);
+  } else {
+    for (int j = t; j < groups; j += T) look(load(j));
+  }
+  uint32_t bits = max(m2 & 0xFFFFu, m2 >> 16);
+  bits = __reduce_max_sync(0xffffffffu, bits);
+  if constexpr (T > 32) {
+    const int warp = static_cast<int>(threadIdx.x) / 32;
+    if ((threadIdx.x & 31) == 0) top[warp] = bits;
+    __syncthreads();
+    bits = top[0];
+#pragma unroll
+    for (int i = 1; i < T / 32; ++i) bits = max(bits, top[i]);
+  }
+  if (!there) return;
+  const float a = lora_h2f(static_cast<uint16_t>(bits));
+  const bool finite = bits < 0x7C00u;
+  if (t == 0) scales[row] = __fdiv_rn(a, 127.0f);
+  const float inv = bits != 0u && finite ? __fdiv_rn(127.0f, a) : 0.0f;
+  auto put = [&](int j, uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    constexpr float kMagic = 12582912.0f;   // 1.5 2^23: the integer is in the low bits
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = lora_h2f2(w[i]);
+      f[2 * i] = finite ? h.x : 0.0f;
+      f[2 * i + 1] = finite ? h.y : 0.0f;
+    }
+    uint32_t b[8];
+    float off = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float n = fmaf(f[i], inv, kMagic);
+      b[i] = __float_as_uint(n);
+      off = fmaxf(off, fabsf(fmaf(f[i], inv, kMagic - n)));
+    }
+    if (off > 0.5f - 0x1p-13f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        b[i] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * f[i], a), kMagic));
+    }
+    const int e0 = 8 * j - md;
+    if (e0 >= 0 && e0 + 8 <= K) {
+      const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+      const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+      *reinterpret_cast<uint2*>(q + e0) = make_uint2(lo, hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e0 + i >= 0 && e0 + i < K) q[e0 + i] = static_cast<int8_t>(b[i] & 0xFFu);
+    }
+  };
+  if constexpr (V > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (t + T * i < groups) put(t + T * i, kept[i]);
+  } else {
+    for (int j = t; j < groups; j += T) put(j, load(j));
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) zero_floats_kernel(float* p, int n) {
+  for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) p[i] = 0.0f;
+}
+
+int device(LoraDevice* d) { return query_device(&d->sms, &d->status, &d->wait_limit_ns); }
+
+struct I8Args {
+  const int8_t *X, *W;
+  const float *sx, *sw;
+  uint16_t* C;
+  int M, N, K, act, ldx, ldw, ldc;
+  float beta;
+  bool gated() const { return act != GEMM_ACT_NONE; }
+  int cols() const { return gated() ? 2 * N : N; }
+};
+
+bool on_grid(const int8_t* p, int ld) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 16 == 0;
+}
+
+int streamed(const I8Args& p, const GateArgs& g, const LoraDevice& d, cudaStream_t stream) {
+  I8Stream r{p.X, p.W, p.ldx, p.ldw, p.M, p.cols(), p.K};
+  StreamSum s{};
+  s.parts = i8_stream_parts(r, d.sms);
+  const bool copy_x = !on_grid(p.X, p.ldx), copy_w = !on_grid(p.W, p.ldw);
+  const int kx = (p.K + 15) / 16 * 16, kw = (p.cols() + 15) / 16 * 16;
+  const size_t x_bytes = copy_x ? lora_round256(static_cast<size_t>(p.M) * kx) : 0;
+  const size_t w_bytes = copy_w ? lora_round256(static_cast<size_t>(p.K) * kw) : 0;
+  void* buf = nullptr;
+  if (int rc = routed_scratch(stream, x_bytes + w_bytes + s.parts.bytes, &buf)) return rc;
+  uint8_t* at = static_cast<uint8_t*>(buf);
+  SpreadBatch b{};
+  if (copy_x) {
+    b.job[b.n++] = SpreadJob{p.X, p.ldx, at, kx, p.M, p.K, kx};
+    r.X = reinterpret_cast<int8_t*>(at);
+    r.ldx = kx;
+  }
+  at += x_bytes;
+  if (copy_w) {
+    b.job[b.n++] = SpreadJob{p.W, p.ldw, at, kw, p.K, p.cols(), kw};
+    r.W = reinterpret_cast<int8_t*>(at);
+    r.ldw = kw;
+  }
+  at += w_bytes;
+  if (b.n)
+    if (int rc = spread(b, false, d.sms, stream)) return rc;
+  s.parts.part = reinterpret_cast<float*>(at);
+  if (int rc = i8_stream(r, s.parts, d, b.n > 0, stream)) return rc;
+  s.C = p.C;
+  s.ldc = p.ldc;
+  s.M = p.M;
+  s.N = p.N;
+  s.alpha = 1.0f;
+  s.beta = p.beta;
+  s.gate = p.gated();
+  s.scaled = true;
+  s.g = g;
+  if (int rc = stream_sum(s, d, stream)) return rc;
+  set_last_path(b.n ? "i8.stream.realigned" : "i8.stream");
+  return GEMM_OK;
+}
+
+int tiled(const I8Args& p, GateArgs g, const LoraDevice& d, cudaStream_t stream) {
+  // the gate's columns and those it gates apart, each from a 16-byte boundary
+  const bool apart = p.gated() && p.N % 8 != 0;
+  const int kx = (p.K + 15) / 16 * 16, n16 = (p.N + 15) / 16 * 16;
+  const int kw = apart ? 2 * n16 : (p.cols() + 15) / 16 * 16;
+  const size_t x_bytes = lora_round256(2 * static_cast<size_t>(p.M) * kx);
+  const size_t w_bytes = lora_round256(2 * static_cast<size_t>(p.K) * kw);
+  void* buf = nullptr;
+  if (int rc = routed_scratch(stream, x_bytes + w_bytes, &buf)) return rc;
+  uint16_t* const x = static_cast<uint16_t*>(buf);
+  uint16_t* const w = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(buf) + x_bytes);
+  SpreadBatch b{};
+  b.job[b.n++] = SpreadJob{p.X, p.ldx, x, kx, p.M, p.K, kx};
+  if (apart) {
+    b.job[b.n++] = SpreadJob{p.W, p.ldw, w, kw, p.K, p.N, n16};
+    b.job[b.n++] = SpreadJob{p.W + p.N, p.ldw, w + n16, kw, p.K, p.N, n16};
+  } else {
+    b.job[b.n++] = SpreadJob{p.W, p.ldw, w, kw, p.K, p.cols(), kw};
+  }
+  if (int rc = spread(b, true, d.sms, stream)) return rc;
+  PairCall q{};
+  q.A = x;
+  q.B = w;
+  q.C = p.C;
+  q.M = p.M;
+  q.N = p.N;
+  q.K = p.K;
+  q.lda = kx;
+  q.ldb = kw;
+  q.ldc = p.ldc;
+  q.alpha = 1.0f;
+  q.beta = p.beta;
+  q.gate = p.gated();
+  q.scaled = true;
+  q.g = g;
+  q.g.up = apart ? n16 : p.N;
+  q.follows = true;
+  return gemm_f16_pair(q, stream);
+}
+
+}  // namespace
+}  // namespace gb300
+
+using namespace gb300;
+
+extern "C" {
+
+int gemm_i8(const int8_t* X, const int8_t* W, uint16_t* C, const float* sx, const float* sw, int M,
+            int N, int K, int act, int ldx, int ldw, int ldc, float beta, cudaStream_t stream) {
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
+  const bool gated = act != GEMM_ACT_NONE;
+  if (act < GEMM_ACT_NONE || act > GEMM_ACT_RELU || (gated && (beta != 0.0f || N > GEMM_GLU_MAX_N)))
+    return GEMM_ERR_ARG;
+  if (M == 0 || N == 0) {
+    set_last_path("noop");
+    return GEMM_OK;
+  }
+  if (ldc < N || (K > 0 && (ldx < K || ldw < (gated ? 2 * N : N)))) return GEMM_ERR_LD;
+  if (!C || (K > 0 && (!X || !W))) return GEMM_ERR_NULL;
+  if (misaligned({C}, 2) || misaligned({sx, sw}, 4)) return GEMM_ERR_ARG;
+  LoraDevice d{};
+  if (int rc = device(&d)) return rc;
+  std::unique_lock<std::recursive_mutex> call;
+  if (int rc = lock_stream(stream, &call)) return rc;
+  if (K == 0) {
+    set_last_path("i8.scale");
+    return launch_scale_f16(C, ldc, M, N, beta, 8 * d.sms, stream) == cudaSuccess ? GEMM_OK
+                                                                                 : GEMM_ERR_CUDA;
+  }
+  const I8Args p{X, W, sx, sw, C, M, N, K, act, ldx, ldw, ldc, beta};
+  GateArgs g{};
+  g.act = act;
+  g.up = N;
+  g.sx = sx;
+  g.sw = sw;
+  return lora_stream_suits(M, p.cols(), d.sms) ? streamed(p, g, d, stream) : tiled(p, g, d, stream);
+}
+
+int gemm_f16_to_i8(const uint16_t* X, int8_t* Q, float* scales, int M, int K, int ldx, int ldq,
+                   cudaStream_t stream) {
+  if (M < 0 || K < 0) return GEMM_ERR_DIM;
+  if (M == 0) {
+    set_last_path("noop");
+    return GEMM_OK;
+  }
+  if (K > 0 && (ldx < K || ldq < K)) return GEMM_ERR_LD;
+  if (!scales || (K > 0 && (!X || !Q))) return GEMM_ERR_NULL;
+  if (misaligned({X}, 2) || misaligned({scales}, 4)) return GEMM_ERR_ARG;
+  LoraDevice d{};
+  if (int rc = device(&d)) return rc;
+  if (K == 0) {
+    set_last_path("to_i8.blank");
+    zero_floats_kernel<<<d.sms, kThreads, 0, stream>>>(scales, M);
+    return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  }
+  set_last_path("to_i8");
+  // groups of a row: at most, when Q's rows leave its 8-byte grid
+  const bool grid8 = (reinterpret_cast<uintptr_t>(Q) & 7u) == 0 && ldq % 8 == 0;
+  const int groups = grid8 ? (K - 1) / 8 + 1 : K / 8 + 2;
+  auto launch = [&](auto kernel, int threads, int rows) {
+    kernel<<<(M - 1) / rows + 1, threads, 0, stream>>>(X, Q, scales, M, K, ldx, ldq);
+  };
+  if (groups <= 32)
+    launch(to_i8_kernel<32, 1>, 256, 8);
+  else if (groups <= 64)
+    launch(to_i8_kernel<32, 2>, 256, 8);
+  else if (groups <= 128)
+    launch(to_i8_kernel<32, 4>, 256, 8);
+  else if (groups <= 256)
+    launch(to_i8_kernel<256, 1>, 256, 1);
+  else if (groups <= 512)
+    launch(to_i8_kernel<256, 2>, 256, 1);
+  else if (groups <= 1024)
+    launch(to_i8_kernel<256, 4>, 256, 1);
+  else if (groups <= 4096)
+    launch(to_i8_kernel<1024, 4>, 1024, 1);
+  else
+    launch(to_i8_kernel<1024, 0>, 1024, 1);
+  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -393,5 +393,8 @@ int encode_map_f16_stack(CUtensorMap* map, const void* ptr, int rows, int cols, 
 // 2-D fp16 tensor map with 128-byte swizzle (rows x cols, row stride ld).
 int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
                    int box_cols, int box_rows);
+// 2-D map of bytes, no swizzle.
+int encode_map_i8(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld, int box_cols,
+                  int box_rows);
 
 }  // namespace gb300

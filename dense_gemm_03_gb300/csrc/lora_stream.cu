@@ -547,10 +547,12 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
 // (its 16 KB of W at an SM's share of HBM) or, for a full block of rows, as long
 // as its 48 KB from L2; the partial sums are 1 KB per row written and read,
 // through L2 at about twice HBM's rate.
-int plan_chunks(int units, int blocks, int kb, int rows, int sms) {
-  int best = 1;
+}  // namespace
+
+int plan_chunks(int units, int blocks, int kb, int rows, int sms, int least) {
+  int best = least;
   double best_t = 1e30;
-  for (int c = 1; c <= std::min(kb, 32); ++c) {
+  for (int c = least; c <= std::max(least, std::min(kb, 32)); ++c) {
     const long long rounds = (1ll * units * blocks * c + sms - 1) / sms;
     const double t = static_cast<double>(rounds) * ((kb + c - 1) / c + 2) +
                      1.9e-4 * units * blocks * c * rows;
@@ -562,6 +564,8 @@ int plan_chunks(int units, int blocks, int kb, int rows, int sms) {
   return best;
 }
 
+namespace {
+
 // K slices of the shrink: about four blocks per SM in all, at least 64 long; one
 // where several rows of a block of the sum kernel can share an adapter.
 int shrink_slices(const LoraStream& p, int sms) {
@@ -569,7 +573,7 @@ int shrink_slices(const LoraStream& p, int sms) {
                             : std::max(1, std::min({kLoraRowSlices, 4 * sms / p.M, p.K / 64}));
 }
 
-StreamArgs plan_stream(int M, int N, int K, bool trans, bool trans_x, int sms) {
+StreamArgs plan_stream(int M, int N, int K, bool trans, bool trans_x, int sms, bool fold = false) {
   StreamArgs t{};
   t.M = M;
   t.N = N;
@@ -579,7 +583,8 @@ StreamArgs plan_stream(int M, int N, int K, bool trans, bool trans_x, int sms) {
   t.units = (N + 127) / 128;
   t.block_rows = std::min(M, kBlockRows);
   const int blocks = (M + kBlockRows - 1) / kBlockRows;
-  t.chunks = plan_chunks(t.units, blocks, t.kb, t.block_rows, sms);
+  t.chunks = plan_chunks(t.units, blocks, t.kb, t.block_rows, sms,
+                         fold ? (K + kFoldDepth - 1) / kFoldDepth : 1);
   t.items = blocks * t.units * t.chunks;
   t.n_cols = (t.block_rows + 15) / 16 * 16;
   t.acc_cols = t.n_cols > 128 ? 256 : 128;
@@ -665,14 +670,14 @@ int launch_stream(StreamArgs t, const uint16_t* W, long long ldw, const uint16_t
 }  // namespace
 
 StreamParts row_stream_parts(const RowStream& p, int sms) {
-  const StreamArgs t = plan_stream(p.M, p.N, p.K, p.trans_w, p.trans_x, sms);
+  const StreamArgs t = plan_stream(p.M, p.N, p.K, p.trans_w, p.trans_x, sms, p.fold);
   return StreamParts{nullptr, t.chunks, t.units, t.block_rows,
-                     4 * static_cast<size_t>(t.items) * t.block_rows * 128};
+                     4 * static_cast<size_t>(t.items) * t.block_rows * 128, kBlockRows};
 }
 
 int row_stream(const RowStream& p, const StreamParts& parts, const LoraDevice& d,
                cudaStream_t stream) {
-  StreamArgs t = plan_stream(p.M, p.N, p.K, p.trans_w, p.trans_x, d.sms);
+  StreamArgs t = plan_stream(p.M, p.N, p.K, p.trans_w, p.trans_x, d.sms, p.fold);
   t.part = parts.part;
   return launch_stream(t, p.W, p.ldw, p.X, p.ldx, p.K, false, d, stream);
 }

@@ -13,7 +13,6 @@ namespace gb300 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBlockRows = 256;   // of a block of partial sums
 
 template <int VEC>
 __device__ __forceinline__ void load_part(const float* p, float (&v)[VEC]) {
@@ -29,11 +28,11 @@ __device__ __forceinline__ void load_part(const float* p, float (&v)[VEC]) {
 // last columns may lie past N, inside its unit).
 template <int VEC>
 __device__ __forceinline__ void add_chunks(const StreamParts& p, int row, int c, float (&s)[VEC]) {
-  const int blk = row / kBlockRows;
+  const int blk = row / p.block;
   const long long step = static_cast<long long>(p.block_rows) * 128;
   const float* src = p.part +
                      (static_cast<long long>(blk) * p.units + (c >> 7)) * p.chunks * step +
-                     (row - blk * kBlockRows) * 128 + (c & 127);
+                     (row - blk * p.block) * 128 + (c & 127);
 #pragma unroll
   for (int i = 0; i < VEC; ++i) s[i] = 0.0f;
   int k = 0;

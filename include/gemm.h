@@ -288,6 +288,40 @@ int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, 
                       int ldw, int lddgu, int lddx, int lddw, float beta, cudaStream_t stream);
 
 /*
+ * The product in 8-bit integers, with a scale for each token and each channel:
+ *
+ *     C[i,n] := sx[i] * sw[n] * sum_k X[i,k] * W[k,n] + beta * C[i,n]
+ *
+ * or, with an activation, gated: W is K x 2N (N gate columns, then N up columns), sw
+ * has 2N scales, and C := f(G) .* U of the scaled products G and U; beta is then 0
+ * (else GEMM_ERR_ARG).
+ *   X   M x K int8, ldx >= K         W   K x N (K x 2N) int8, ldw >= N (2N)
+ *   sx  M floats, sw  N (2N) floats, on the device; each may be NULL: ones
+ *   C   M x N half, ldc >= N         act GEMM_ACT_NONE ... GEMM_ACT_RELU
+ * X and W may lie at any address.  Products are exact; so is each sum as long as its
+ * partial sums stay below 2^24 in magnitude (whatever the values for K <= 1024, and in
+ * practice far beyond; else it is rounded as in gemm_f16).  (sum * sx) * sw, f and the
+ * gate's product are fp32; C is rounded once.  K == 0: C := beta * C.
+ */
+int gemm_i8(const int8_t* X, const int8_t* W, uint16_t* C, const float* sx, const float* sw, int M,
+            int N, int K, int act, int ldx, int ldw, int ldc, float beta, cudaStream_t stream);
+
+/*
+ * Tokens rounded to 8 bits: with a = max_k |X[i,k]|,
+ *
+ *     scales[i] := a / 127,     Q[i,k] := 127 X[i,k] / a to the nearest integer
+ *
+ * (ties to even, exactly), so that scales[i] * Q[i,k] is X[i,k] to within scales[i] / 2
+ * and the rounding of scales[i].  A row of zeros has scale 0 and zeros; one that holds an
+ * infinity or a NaN has that scale (NaN when it holds both) and zeros, and makes its
+ * row of a product NaN.
+ *   X  M x K half, ldx >= K    Q  M x K int8 at any address, ldq >= K    scales  M floats
+ * K == 0: the scales are 0.
+ */
+int gemm_f16_to_i8(const uint16_t* X, int8_t* Q, float* scales, int M, int K, int ldx, int ldq,
+                   cudaStream_t stream);
+
+/*
  * Host-buffer forms: A, B, C are HOST pointers (pinned memory gives the
  * fastest copies and lets them overlap; pageable memory works).  On a
  * library-owned copy-in stream the call copies B, then A and C (C when

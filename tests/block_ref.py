@@ -80,6 +80,44 @@ def glu_grad(dC, X, W, act):
     return ref, half_round(ref) + torch.cat([tG, tU], 1)
 
 
+def i8_sums(X, W):
+    """The integer sums and their bound: exact where no partial sum can reach 2^24."""
+    X, W = d(X), d(W)
+    S, t = X @ W, X.abs() @ W.abs()
+    return S, sum_tol(X.shape[1], t) * (t >= 2.0 ** 24)
+
+
+def i8(X, W, sx, sw, act=None, beta=0.0, C0=None):
+    """(ref, tol) of the scaled 8-bit product; two roundings of each scaled sum."""
+    S, e = i8_sums(X, W)
+    s = (d(sx) if sx is not None else torch.ones(X.shape[0], dtype=torch.float64))[:, None] * \
+        (d(sw) if sw is not None else torch.ones(W.shape[1], dtype=torch.float64))[None, :]
+    S, e = S * s, e * s + U2 * (S * s).abs()
+    if act is not None:
+        N = W.shape[1] // 2
+        return joined(act, S[:, :N], S[:, N:], e[:, :N], e[:, N:])
+    if beta:
+        S, e = S + beta * d(C0), e + U2 * (S.abs() + abs(beta) * d(C0).abs())
+    return S, half_round(S) + e
+
+
+def to_i8(X):
+    """(Q, scales): the exact rounding, in integers (a half is a multiple of 2^-24)."""
+    n = (d(X) * 2.0 ** 24).numpy().astype(object)
+    Q = torch.zeros(X.shape, dtype=torch.int8)
+    for i, row in enumerate(n):
+        row = [int(v) for v in row]
+        a = max((abs(v) for v in row), default=0)
+        if a:
+            for k, v in enumerate(row):
+                q, r = divmod(2 * 127 * abs(v) + a, 2 * a)     # nearest, ties up
+                if r == 0 and q % 2:
+                    q -= 1                                     # ties to even
+                Q[i, k] = q if v >= 0 else -q
+    a = X.abs().float().amax(1) if X.shape[1] else torch.zeros(X.shape[0])
+    return Q, a / torch.full_like(a, 127.0)
+
+
 def product(A, B, alpha=1.0, beta=0.0, C0=None, f32=False):
     """(ref, tol) of alpha A B + beta C0."""
     A, B = d(A), d(B)

@@ -85,3 +85,52 @@ def test_binding_shapes(L):
         g.gemm_f16_trans(z(8, 2), z(9, 4), z(2, 4), True)
     with pytest.raises(g.GemmError):
         g.gemm_f16_glu(16, 16, 16, M=-1, N=1, K=1)
+
+
+def test_i8_refusals(L):
+    def call(M, N, K, act=-1, ldx=8, ldw=16, ldc=8, beta=0.0, X=1, W=1, C=16, sx=None, sw=None):
+        return L.gemm_i8(X, W, C, sx, sw, M, N, K, act, ldx, ldw, ldc, beta, None)
+    assert call(-1, 8, 8) == -2 and call(8, -8, 8) == -2 and call(8, 8, -8) == -2
+    assert call(8, 8, 8, act=-2) == -7 and call(8, 8, 8, act=4) == -7
+    assert call(8, 8, 8, act=0, beta=0.5) == -7
+    assert call(8, (1 << 29) + 1, 8, act=0, ldw=BIG, ldc=BIG) == -7
+    assert call(8, 8, 8, ldx=7) == -3 and call(8, 8, 8, ldw=7) == -3 and call(8, 8, 8, ldc=7) == -3
+    assert call(8, 8, 8, act=0, ldw=15) == -3
+    for missing in ("X", "W", "C"):
+        assert call(8, 8, 8, **{missing: None}) == -1
+    assert call(8, 8, 8, C=17) == -7 and call(8, 8, 8, sx=6) == -7 and call(8, 8, 8, sw=6) == -7
+    assert call(0, 8, 8, X=None, W=None, C=None) == 0
+
+
+def test_to_i8_refusals(L):
+    def call(M, K, ldx=8, ldq=8, X=16, Q=1, scales=16):
+        return L.gemm_f16_to_i8(X, Q, scales, M, K, ldx, ldq, None)
+    assert call(-1, 8) == -2 and call(8, -1) == -2
+    assert call(8, 8, ldx=7) == -3 and call(8, 8, ldq=7) == -3
+    for missing in ("X", "Q", "scales"):
+        assert call(8, 8, **{missing: None}) == -1
+    assert call(8, 0, scales=None) == -1
+    assert call(8, 8, X=17) == -7 and call(8, 8, scales=18) == -7
+    assert call(0, 8, X=None, Q=None, scales=None) == 0
+
+
+def test_i8_binding(L):
+    torch = pytest.importorskip("torch")
+    q = lambda *s: torch.zeros(*s, dtype=torch.int8)
+    c = torch.zeros(2, 4, dtype=torch.float16)
+    with pytest.raises(TypeError, match="X is float16"):
+        g.gemm_i8(c, q(4, 4), c)
+    with pytest.raises(TypeError, match="W is uint8"):
+        g.gemm_i8(q(2, 4), torch.zeros(4, 4, dtype=torch.uint8), c)
+    with pytest.raises(TypeError, match="sx is float16"):
+        g.gemm_i8(q(2, 4), q(4, 4), c, torch.zeros(2, dtype=torch.float16))
+    with pytest.raises(ValueError, match="sw is not 8 dense"):
+        g.gemm_i8(q(2, 4), q(4, 8), c, None, torch.zeros(4), "silu")
+    with pytest.raises(ValueError, match="K of W and X"):
+        g.gemm_i8(q(2, 4), q(5, 4), c)
+    with pytest.raises(ValueError, match="columns"):
+        g.gemm_i8(q(2, 4), q(4, 7), c, act="relu")
+    with pytest.raises(TypeError, match="Q is float16"):
+        g.f16_to_i8(c, c, torch.zeros(2))
+    with pytest.raises(ValueError, match="scales is not 2 dense"):
+        g.f16_to_i8(c, q(2, 4), torch.zeros(1))
