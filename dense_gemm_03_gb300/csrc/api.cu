@@ -486,6 +486,23 @@ struct MapCache {
 };
 thread_local MapCache t_maps;
 
+// The same for encode_map_3d.
+struct MapKey3 {
+  const void* ptr;
+  int elem;
+  MapDims size, stride, box;
+  bool operator==(const MapKey3& o) const {
+    return ptr == o.ptr && elem == o.elem && std::equal(size.d, size.d + 3, o.size.d) &&
+           std::equal(stride.d, stride.d + 3, o.stride.d) && std::equal(box.d, box.d + 3, o.box.d);
+  }
+};
+struct MapCache3 {
+  MapKey3 key[kMapCache];
+  CUtensorMap map[kMapCache];
+  int used = 0, next = 0;
+};
+thread_local MapCache3 t_maps3;
+
 // Width of the CTA-pair tiles: 256 unless forced (paths 12 / 13: 224 / 192).
 // Measured on GB300 (same-box A/B, alpha 1.5 beta 0.5): a k-block of a
 // 256 x 224 or 256 x 192 pair tile takes as long as one of a 256 x 256 tile,
@@ -1526,10 +1543,37 @@ int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long l
   return make_map_f16(map, ptr, rows, cols, ld, box_cols, box_rows);
 }
 
-int encode_map_i8(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld, int box_cols,
-                  int box_rows) {
-  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, rows, cols, ld, box_cols, box_rows,
-                  CU_TENSOR_MAP_SWIZZLE_NONE);
+int encode_map_3d(CUtensorMap* map, int elem, const void* ptr, MapDims size, MapDims stride,
+                  MapDims box) {
+  const MapKey3 k{ptr, elem, size, stride, box};
+  MapCache3& c = t_maps3;
+  for (int i = 0; i < c.used; ++i)
+    if (c.key[i] == k) {
+      *map = c.map[i];
+      return GEMM_OK;
+    }
+  EncodeTiledFn enc = nullptr;
+  if (int rc = encode_fn(&enc)) return rc;
+  const cuuint32_t rank = size.d[2] ? 3 : 2;
+  cuuint64_t dims[3], strides[2];
+  cuuint32_t boxes[3];
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  for (int i = 0; i < 3; ++i) {
+    dims[i] = static_cast<cuuint64_t>(size.d[i]);
+    boxes[i] = static_cast<cuuint32_t>(box.d[i]);
+  }
+  for (int i = 0; i < 2; ++i) strides[i] = static_cast<cuuint64_t>(stride.d[i]) * elem;
+  const CUresult r = enc(
+      map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
+      const_cast<void*>(ptr), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      box.d[0] * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return GEMM_ERR_CUDA;
+  const int slot = c.used < kMapCache ? c.used++ : c.next;
+  c.next = (slot + 1) % kMapCache;
+  c.key[slot] = k;
+  c.map[slot] = *map;
+  return GEMM_OK;
 }
 
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }

@@ -8,9 +8,8 @@
 //   trans     C := alpha op(A) op(B) + beta C
 //
 // Two ways for each product: whole 256 x 256 tiles on CTA pairs
-// (gemm_f16_tc_kernel.cuh), or, where a few rows or few tiles would leave SMs idle, fp32
-// partial sums by K chunks with their sum in a kernel of its own (lora_stream.cu,
-// stream_sum.cu).  Sums are fp32; every result is rounded once.
+// (gemm_f16_tc_kernel.cuh), or, where a few rows or few tiles would leave SMs idle,
+// K cut into chunks (narrow_stream.cu).  Sums are fp32; every result is rounded once.
 #include "gemm.h"
 #include "lora.h"
 #include "operands.h"
@@ -38,20 +37,20 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   Aligned x(X, ldx, trans_x ? K : M, trans_x ? M : K, true);
   Aligned w(W, ldw, trans_w ? cols : K, trans_w ? K : cols, true);
   const size_t copies = x.bytes() + w.bytes();
-  RowStream r{X, W, ldx, ldw, M, cols, K, trans_x, trans_w, s.f32};
-  s.parts = row_stream_parts(r, d.sms);
+  const bool cluster = narrow_cluster_suits(false, M, s.N, K, s.gate, s.f32, d.sms);
+  NarrowStream p{X, W, ldx, ldw, K, trans_x, trans_w, false};
+  if (!cluster) s.parts = narrow_parts(p, M, cols, s.f32, d.sms);
   void* buf = nullptr;
-  if (int rc = routed_scratch(stream, copies + s.parts.bytes, &buf)) return rc;
+  if (copies + s.parts.bytes)
+    if (int rc = routed_scratch(stream, copies + s.parts.bytes, &buf)) return rc;
   if (int rc = align_operands({{x, &X, &ldx}, {w, &W, &ldw}}, static_cast<uint8_t*>(buf), d.sms,
                               stream))
     return rc;
-  r.X = X;
-  r.W = W;
-  r.ldx = ldx;
-  r.ldw = ldw;
-  s.parts.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + copies);
-  if (int rc = row_stream(r, s.parts, d, stream)) return rc;
   *copied = copies != 0;
+  p = NarrowStream{X, W, ldx, ldw, K, trans_x, trans_w, false};
+  if (cluster) return narrow_cluster(p, s, d, *copied, stream);
+  s.parts.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + copies);
+  if (int rc = narrow_partial(p, M, cols, s.f32, s.parts, d, *copied, stream)) return rc;
   return stream_sum(s, d, stream);
 }
 

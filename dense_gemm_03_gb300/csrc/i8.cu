@@ -5,12 +5,13 @@
 //   product    S = X W exactly as integers, C := sx[i] sw[n] S + beta C, or gated
 //   tokens     a = max_k |X[i,k]|, scale[i] = a / 127, Q[i,k] = round(127 X[i,k] / a)
 //
-// Few rows or few tiles: i8_stream.cu (bytes to halves on their way to the tensor
-// cores) and stream_sum.cu.  Else both operands become halves in scratch, read back
+// Few rows or few tiles: narrow_stream.cu (bytes to halves on their way to the tensor
+// cores).  Else both operands become halves in scratch, read back
 // from L2 by the pair kernel (gemm_f16_tc_kernel.cuh), whose epilogue scales.
 #include <cuda_fp16.h>
 
 #include "gemm.h"
+#include "i8_convert.cuh"
 #include "lora.h"
 #include "operands.h"
 #include "stream.h"
@@ -80,24 +81,8 @@ __global__ void __launch_bounds__(kThreads) spread_i8_kernel(const SpreadBatch b
     if constexpr (!HALVES) {
       *reinterpret_cast<uint4*>(static_cast<int8_t*>(j.dst) + at) = q;
     } else {
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-      uint32_t o[8];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {   // byte q + 128 -> 1024 + it -> q (see i8_stream.cu)
-        const uint32_t u = w[k] ^ 0x80808080u;
-        const uint32_t v[2] = {__byte_perm(u, 0x64646464u, 0x4140), __byte_perm(u, 0x64646464u, 0x4342)};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          __half2 h;
-          memcpy(&h, &v[e], 4);
-          h = __hsub2(h, off);
-          memcpy(&o[2 * k + e], &h, 4);
-        }
-      }
       uint4* const dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(j.dst) + at);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      i8_halves16(q, dst[0], dst[1]);
     }
   }
 }
@@ -122,10 +107,13 @@ int spread(SpreadBatch& b, bool halves, int sms, cudaStream_t stream) {
 // Q's 8-byte grid, so that stores are whole; a row's first and last may be ragged.
 //
 // The maximum is taken over the bits of |x|, which order like the values, infinities
-// above them and NaNs above those.  The quotient 127 x / a is x times the rounded 127 / a
-// (off by less than 2^-15), rounded to the nearest integer by adding 1.5 2^23; where it
-// comes within 2^-13 of a tie the division decides: 127 x is exact, and a quotient that is
-// no tie is further from one than its rounding.
+// above them and NaNs above those.  127 x / a is x times 127 / a, the latter rounded up,
+// and rounds to an integer as 1.5 2^23 is added (one rounding, of the exact product).
+// That is exact.  With significands X and A below 2^11, 127 x / a - (k + 1/2) is zero or at
+// least 2^-19 of the quotient, and the product is off by at most 2^-23 of it.  A tie, 254 x
+// = (2k + 1) a, has 127 among the factors of 2k + 1 or of A.  2k + 1 = 127 is x = a / 2,
+// whose product is 63.5 or a little more and rounds to 64, the even one; rows whose A is a
+// multiple of 127 divide instead (127 x is exact, and so is a tie's quotient).
 template <int T, int V>
 __global__ void __launch_bounds__(T < 256 ? 256 : T)
     to_i8_kernel(const uint16_t* __restrict__ X, int8_t* __restrict__ Q, float* __restrict__ scales,
@@ -191,29 +179,23 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T)
   const float a = lora_h2f(static_cast<uint16_t>(bits));
   const bool finite = bits < 0x7C00u;
   if (t == 0) scales[row] = __fdiv_rn(a, 127.0f);
-  const float inv = bits != 0u && finite ? __fdiv_rn(127.0f, a) : 0.0f;
+  const float inv = bits != 0u && finite ? __fdiv_ru(127.0f, a) : 0.0f;
+  const uint32_t significand = (bits & 0x3FFu) | (bits >= 0x400u ? 0x400u : 0u);
+  const bool divide = finite && bits != 0u && significand % 127u == 0u;
   auto put = [&](int j, uint4 v) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     constexpr float kMagic = 12582912.0f;   // 1.5 2^23: the integer is in the low bits
-    float f[8];
+    if (!finite) v = make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t b[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 h = lora_h2f2(w[i]);
-      f[2 * i] = finite ? h.x : 0.0f;
-      f[2 * i + 1] = finite ? h.y : 0.0f;
-    }
-    uint32_t b[8];
-    float off = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float n = fmaf(f[i], inv, kMagic);
-      b[i] = __float_as_uint(n);
-      off = fmaxf(off, fabsf(fmaf(f[i], inv, kMagic - n)));
-    }
-    if (off > 0.5f - 0x1p-13f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        b[i] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * f[i], a), kMagic));
+      b[2 * i] = __float_as_uint(fmaf(h.x, inv, kMagic));
+      b[2 * i + 1] = __float_as_uint(fmaf(h.y, inv, kMagic));
+      if (divide) {
+        b[2 * i] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * h.x, a), kMagic));
+        b[2 * i + 1] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * h.y, a), kMagic));
+      }
     }
     const int e0 = 8 * j - md;
     if (e0 >= 0 && e0 + 8 <= K) {
@@ -256,33 +238,33 @@ bool on_grid(const int8_t* p, int ld) {
 }
 
 int streamed(const I8Args& p, const GateArgs& g, const LoraDevice& d, cudaStream_t stream) {
-  I8Stream r{p.X, p.W, p.ldx, p.ldw, p.M, p.cols(), p.K};
+  NarrowStream r{p.X, p.W, p.ldx, p.ldw, p.K, false, false, true};
   StreamSum s{};
-  s.parts = i8_stream_parts(r, d.sms);
+  const bool cluster = narrow_cluster_suits(true, p.M, p.N, p.K, p.gated(), false, d.sms);
+  if (!cluster) s.parts = narrow_parts(r, p.M, p.cols(), false, d.sms);
   const bool copy_x = !on_grid(p.X, p.ldx), copy_w = !on_grid(p.W, p.ldw);
   const int kx = (p.K + 15) / 16 * 16, kw = (p.cols() + 15) / 16 * 16;
   const size_t x_bytes = copy_x ? lora_round256(static_cast<size_t>(p.M) * kx) : 0;
   const size_t w_bytes = copy_w ? lora_round256(static_cast<size_t>(p.K) * kw) : 0;
   void* buf = nullptr;
-  if (int rc = routed_scratch(stream, x_bytes + w_bytes + s.parts.bytes, &buf)) return rc;
+  if (x_bytes + w_bytes + s.parts.bytes)
+    if (int rc = routed_scratch(stream, x_bytes + w_bytes + s.parts.bytes, &buf)) return rc;
   uint8_t* at = static_cast<uint8_t*>(buf);
   SpreadBatch b{};
   if (copy_x) {
     b.job[b.n++] = SpreadJob{p.X, p.ldx, at, kx, p.M, p.K, kx};
-    r.X = reinterpret_cast<int8_t*>(at);
+    r.X = at;
     r.ldx = kx;
   }
   at += x_bytes;
   if (copy_w) {
     b.job[b.n++] = SpreadJob{p.W, p.ldw, at, kw, p.K, p.cols(), kw};
-    r.W = reinterpret_cast<int8_t*>(at);
+    r.W = at;
     r.ldw = kw;
   }
   at += w_bytes;
   if (b.n)
     if (int rc = spread(b, false, d.sms, stream)) return rc;
-  s.parts.part = reinterpret_cast<float*>(at);
-  if (int rc = i8_stream(r, s.parts, d, b.n > 0, stream)) return rc;
   s.C = p.C;
   s.ldc = p.ldc;
   s.M = p.M;
@@ -292,7 +274,13 @@ int streamed(const I8Args& p, const GateArgs& g, const LoraDevice& d, cudaStream
   s.gate = p.gated();
   s.scaled = true;
   s.g = g;
-  if (int rc = stream_sum(s, d, stream)) return rc;
+  if (cluster) {
+    if (int rc = narrow_cluster(r, s, d, b.n > 0, stream)) return rc;
+  } else {
+    s.parts.part = reinterpret_cast<float*>(at);
+    if (int rc = narrow_partial(r, p.M, p.cols(), false, s.parts, d, b.n > 0, stream)) return rc;
+    if (int rc = stream_sum(s, d, stream)) return rc;
+  }
   set_last_path(b.n ? "i8.stream.realigned" : "i8.stream");
   return GEMM_OK;
 }

@@ -393,8 +393,13 @@ int encode_map_f16_stack(CUtensorMap* map, const void* ptr, int rows, int cols, 
 // 2-D fp16 tensor map with 128-byte swizzle (rows x cols, row stride ld).
 int encode_map_f16(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld,
                    int box_cols, int box_rows);
-// 2-D map of bytes, no swizzle.
-int encode_map_i8(CUtensorMap* map, const void* ptr, int rows, int cols, long long ld, int box_cols,
-                  int box_rows);
+// Map of two dimensions (the third's size 0) or three over elements of `elem` bytes (1: bytes, 2:
+// halves): sizes, the strides of the second and third dimension in elements, and the box;
+// its rows are 64 or 128 bytes, swizzled over that width.
+struct MapDims {
+  long long d[3];
+};
+int encode_map_3d(CUtensorMap* map, int elem, const void* ptr, MapDims size, MapDims stride,
+                  MapDims box);
 
 }  // namespace gb300

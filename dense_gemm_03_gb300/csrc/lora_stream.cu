@@ -24,11 +24,7 @@
 // Shared memory per ring stage: two 64-column boxes of 64 k-rows of W (128-byte
 // swizzle, MN-major: LBO 8 KB, SBO 1 KB; or, for a W stored transposed, two
 // boxes of 64 rows, K-major, SBO 1 KB), then the rows of X, 64 halves of k each
-// (K-major, SBO 1 KB), or, for an X stored K x M, boxes of 64 k-rows of 64 of its
-// rows (MN-major).
-//
-// The stream is also that of other products with few rows or few tiles (row_stream),
-// whose chunks stream_sum.cu adds up.
+// (K-major, SBO 1 KB).
 #include <type_traits>
 
 #include "lora.h"
@@ -58,9 +54,9 @@ struct CombineArgs {
 };
 
 struct StreamArgs {
-  int M, N, trans, trans_x;   // W stored N x K; X stored K x M
+  int M, N, trans;
   int kb, chunks, units, items;   // k-blocks, chunks, 128-column units, blocks x units x chunks
-  int stages, stage_bytes, x_bytes, n_cols, acc_cols;
+  int stages, stage_bytes, n_cols, acc_cols;
   int block_rows;          // rows of a block's partial sums: min(M, kBlockRows)
   float* part;             // [block][unit][chunk][row][128]
   unsigned long long wait_limit_ns;
@@ -124,7 +120,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const int row0 = it / p.chunks / p.units * kBlockRows;
         const bool two = n0 + 64 < p.N;      // the second box lies in the matrix
         const uint32_t bytes =
-            static_cast<uint32_t>((two ? kWBytes : kWBytes / 2) + p.x_bytes);
+            static_cast<uint32_t>((two ? kWBytes : kWBytes / 2) + p.n_cols * 128);
         for (int kb = c * p.kb / p.chunks; kb < (c + 1) * p.kb / p.chunks; ++kb) {
           if (!wait_parity(empty_bar(stage), phase ^ 1u, limit, st, 60)) {
             ok = false;
@@ -140,11 +136,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             else
               tma_load_2d(dst + b * 8192, &tmW, full_bar(stage), cx, cy);
           }
-          if (p.trans_x)
-            for (int b = 0; b < p.x_bytes; b += 8192)
-              tma_load_2d(dst + kWBytes + b, &tmX, full_bar(stage), row0 + b / 128, kb * 64);
-          else
-            tma_load_2d(dst + kWBytes, &tmX, full_bar(stage), kb * 64, row0);
+          tma_load_2d(dst + kWBytes, &tmX, full_bar(stage), kb * 64, row0);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -160,8 +152,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc =
-          make_idesc(0u, 128u, static_cast<uint32_t>(p.n_cols), p.trans ? 0u : 1u,
-                     p.trans_x ? 1u : 0u);
+          make_idesc(0u, 128u, static_cast<uint32_t>(p.n_cols), p.trans ? 0u : 1u, 0u);
       int stage = 0;
       uint32_t phase = 0, local = 0;
       bool ok = true;
@@ -183,9 +174,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             mma_f16_ss(tmem + buf * p.acc_cols,
                        p.trans ? smem_desc_sw128(w0 + kk * 32, 16u, 1024u)
                                : smem_desc_sw128(w0 + kk * 2048, 8192u, 1024u),
-                       p.trans_x ? smem_desc_sw128(w0 + kWBytes + kk * 2048, 8192u, 1024u)
-                                 : smem_desc_sw128(w0 + kWBytes + kk * 32, 16u, 1024u),
-                       idesc,
+                       smem_desc_sw128(w0 + kWBytes + kk * 32, 16u, 1024u), idesc,
                        (kb > kb0 || kk > 0) ? 1u : 0u);
           mma_commit(empty_bar(stage));
           if (++stage == S) {
@@ -573,29 +562,20 @@ int shrink_slices(const LoraStream& p, int sms) {
                             : std::max(1, std::min({kLoraRowSlices, 4 * sms / p.M, p.K / 64}));
 }
 
-StreamArgs plan_stream(int M, int N, int K, bool trans, bool trans_x, int sms, bool fold = false) {
+StreamArgs plan(const LoraStream& p, int sms) {
   StreamArgs t{};
-  t.M = M;
-  t.N = N;
-  t.trans = trans;
-  t.trans_x = trans_x;
-  t.kb = (K + 63) / 64;
-  t.units = (N + 127) / 128;
-  t.block_rows = std::min(M, kBlockRows);
-  const int blocks = (M + kBlockRows - 1) / kBlockRows;
-  t.chunks = plan_chunks(t.units, blocks, t.kb, t.block_rows, sms,
-                         fold ? (K + kFoldDepth - 1) / kFoldDepth : 1);
+  t.M = p.M;
+  t.N = p.N;
+  t.trans = p.trans;
+  t.kb = (p.K + 63) / 64;
+  t.units = (p.N + 127) / 128;
+  t.block_rows = std::min(p.M, kBlockRows);
+  const int blocks = (p.M + kBlockRows - 1) / kBlockRows;
+  t.chunks = plan_chunks(t.units, blocks, t.kb, t.block_rows, sms);
   t.items = blocks * t.units * t.chunks;
   t.n_cols = (t.block_rows + 15) / 16 * 16;
   t.acc_cols = t.n_cols > 128 ? 256 : 128;
-  t.x_bytes = trans_x ? (t.n_cols + 63) / 64 * 8192 : t.n_cols * 128;
-  t.stage_bytes = kWBytes + t.x_bytes;
-  t.stages = std::min(kMaxStages, (kSmemMax - 2048) / t.stage_bytes);
-  return t;
-}
-
-StreamArgs plan(const LoraStream& p, int sms) {
-  StreamArgs t = plan_stream(p.M, p.N, p.K, p.trans != 0, false, sms);
+  t.stage_bytes = kWBytes + t.n_cols * 128;
   // beside the blocks of the shrink by rows (10 KB each, four on an SM) where it
   // runs: with the whole shared memory this kernel's CTAs started only as those
   // ended, 3 us later
@@ -628,19 +608,13 @@ size_t lora_stream_bytes(const LoraStream& p, int sms) {
   return lora_round256(v) + 4 * static_cast<size_t>(t.items) * t.block_rows * 128;
 }
 
-namespace {
-
-// The stream over W (K x N, or N x K) and X (M x K, or K x M); `early`: it may start
-// before the kernel launched just before it ends.
-int launch_stream(StreamArgs t, const uint16_t* W, long long ldw, const uint16_t* X, long long ldx,
-                  int K, bool early, const LoraDevice& d, cudaStream_t stream) {
+int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStream_t stream) {
+  StreamArgs t = plan(p, d.sms);
   CUtensorMap tmW{}, tmX{};
-  if (int rc = t.trans ? encode_map_f16(&tmW, W, t.N, K, ldw, 64, 64)
-                       : encode_map_f16(&tmW, W, K, t.N, ldw, 64, 64))
+  if (int rc = p.trans ? encode_map_f16(&tmW, p.W, p.N, p.K, p.ldw, 64, 64)
+                       : encode_map_f16(&tmW, p.W, p.K, p.N, p.ldw, 64, 64))
     return rc;
-  if (int rc = t.trans_x ? encode_map_f16(&tmX, X, K, t.M, ldx, 64, 64)
-                         : encode_map_f16(&tmX, X, t.M, K, ldx, 64, t.n_cols))
-    return rc;
+  if (int rc = encode_map_f16(&tmX, p.X, p.M, p.K, p.ldx, 64, t.n_cols)) return rc;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
   static bool configured[64] = {};
@@ -652,38 +626,6 @@ int launch_stream(StreamArgs t, const uint16_t* W, long long ldw, const uint16_t
   }
   t.wait_limit_ns = d.wait_limit_ns;
   t.status = d.status;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min(t.items, d.sms)), 1, 1);
-  cfg.blockDim = dim3(kStreamThreads, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(t.stages) * t.stage_bytes + 2048;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = early ? 1 : 0;
-  return counted_launch(cudaLaunchKernelEx(&cfg, row_stream_kernel, tmW, tmX, t)) == cudaSuccess
-             ? GEMM_OK
-             : GEMM_ERR_CUDA;
-}
-
-}  // namespace
-
-StreamParts row_stream_parts(const RowStream& p, int sms) {
-  const StreamArgs t = plan_stream(p.M, p.N, p.K, p.trans_w, p.trans_x, sms, p.fold);
-  return StreamParts{nullptr, t.chunks, t.units, t.block_rows,
-                     4 * static_cast<size_t>(t.items) * t.block_rows * 128, kBlockRows};
-}
-
-int row_stream(const RowStream& p, const StreamParts& parts, const LoraDevice& d,
-               cudaStream_t stream) {
-  StreamArgs t = plan_stream(p.M, p.N, p.K, p.trans_w, p.trans_x, d.sms, p.fold);
-  t.part = parts.part;
-  return launch_stream(t, p.W, p.ldw, p.X, p.ldx, p.K, false, d, stream);
-}
-
-int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStream_t stream) {
-  StreamArgs t = plan(p, d.sms);
   CombineArgs c{};
   c.V = p.V;
   c.ldv = p.ldv;
@@ -730,10 +672,14 @@ int lora_stream(const LoraStream& p, void* scratch, const LoraDevice& d, cudaStr
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(t.items, d.sms)), 1, 1);
+  cfg.blockDim = dim3(kStreamThreads, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(t.stages) * t.stage_bytes + 2048;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (int rc = launch_stream(t, p.W, p.ldw, p.X, p.ldx, p.K, true, d, stream)) return rc;
+  if (counted_launch(cudaLaunchKernelEx(&cfg, row_stream_kernel, tmW, tmX, t)) != cudaSuccess)
+    return GEMM_ERR_CUDA;
 
   // as many rows a block as leave a few blocks per SM; else by single rows
   const long long strips = (p.N + 4 * kCombThreads - 1) / (4 * kCombThreads);

@@ -1,6 +1,6 @@
-// stream.h -- products with few rows or few tiles as fp32 partial sums by K chunks
-// (row_stream in lora_stream.cu for halves, i8_stream.cu for 8-bit integers) and
-// the kernel that adds them up and finishes the result (stream_sum.cu).
+// stream.h -- products with few rows or few tiles: as one kernel where a wave of
+// clusters covers them, else as fp32 partial sums by K chunks (narrow_stream.cu) and the
+// kernel that adds them up and finishes the result (stream_sum.cu).
 #pragma once
 
 #include <cstddef>
@@ -21,28 +21,21 @@ struct StreamParts {
 // Chunks per unit (of `kb` steps of 16 KB of W each): see lora_stream.cu.
 int plan_chunks(int units, int blocks, int kb, int rows, int sms, int least = 1);
 
-// X (M x K, or K x M) times W (K x N, or N x K), rows on the 16-byte grid.
-struct RowStream {
-  const uint16_t *X, *W;
-  long long ldx, ldw;
-  int M, N, K;
-  bool trans_x, trans_w;
-  bool fold;   // chunks of at most kFoldDepth, for a float result
-};
+// Longest chunk of K of a float result: the tensor core's additions truncate.
 constexpr int kFoldDepth = 2048;
-StreamParts row_stream_parts(const RowStream& p, int sms);   // with part == nullptr
-int row_stream(const RowStream& p, const StreamParts& parts, const LoraDevice& d,
-               cudaStream_t stream);
 
-// X (M x K) times W (K x N) in 8-bit integers, rows on the 16-byte grid.
-struct I8Stream {
-  const int8_t *X, *W;
+// op(X) (M x K, stored K x M where trans_x) times op(W) (K x `cols`; N x K) in halves, or
+// X W in 8-bit integers; rows on the 16-byte grid.
+struct NarrowStream {
+  const void *X, *W;
   long long ldx, ldw;
-  int M, N, K;
+  int K;
+  bool trans_x, trans_w, i8;
 };
-StreamParts i8_stream_parts(const I8Stream& p, int sms);
-int i8_stream(const I8Stream& p, const StreamParts& parts, const LoraDevice& d, bool early,
-              cudaStream_t stream);
+// Its partial sums; fold: of a float result.
+StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, int sms);
+int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const StreamParts& parts,
+                   const LoraDevice& d, bool early, cudaStream_t stream);
 
 // What becomes of the sums S (gate 0: N columns; else 2 N, G and U):
 //   gate 0   C := alpha S + beta C (half, or float when f32); with scales S
@@ -59,6 +52,11 @@ struct StreamSum {
   bool f32, scaled;
   GateArgs g;
 };
+// The whole product in one launch, finished as `s` says (its parts unused), where one
+// wave of clusters covers it.  N: output columns.
+bool narrow_cluster_suits(bool i8, int M, int N, int K, int gate, bool f32, int sms);
+int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,
+                   cudaStream_t stream);
 int stream_sum(const StreamSum& s, const LoraDevice& d, cudaStream_t stream);
 
 }  // namespace gb300
