@@ -22,7 +22,7 @@ SOURCES = ["api.cu", "gemm_f16_tc.cu", "gemm_f16_pair_narrow.cu", "gemm_f16_f32o
            "gemm_f16_skinny.cu", "sgemm_ffma.cu", "sgemm_split.cu", "aux_kernels.cu",
            "splitk_static.cu", "lora.cu", "lora_stream.cu", "lora_rows.cu", "lora_shrink.cu", "lora_outer.cu", "gemm_f16_lora.cu", "moe.cu", "moe_stream.cu",
            "dense_block.cu", "stream_sum.cu", "gemm_f16_trans.cu", "gemm_f16_gate.cu", "i8.cu",
-           "narrow_stream.cu"]
+           "narrow_stream.cu", "i8_stream.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -37,9 +37,9 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   Aligned x(X, ldx, trans_x ? K : M, trans_x ? M : K, true);
   Aligned w(W, ldw, trans_w ? cols : K, trans_w ? K : cols, true);
   const size_t copies = x.bytes() + w.bytes();
-  const bool cluster = narrow_cluster_suits(false, M, s.N, K, s.gate, s.f32, d.sms);
-  NarrowStream p{X, W, ldx, ldw, K, trans_x, trans_w, false};
-  if (!cluster) s.parts = narrow_parts(p, M, cols, s.f32, d.sms);
+  const bool cluster = narrow_cluster_suits(s, K, d);
+  NarrowStream p{X, W, ldx, ldw, K, trans_x, trans_w};
+  if (!cluster) s.parts = narrow_parts(p, M, cols, s.f32, d);
   void* buf = nullptr;
   if (copies + s.parts.bytes)
     if (int rc = routed_scratch(stream, copies + s.parts.bytes, &buf)) return rc;
@@ -47,7 +47,7 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
                               stream))
     return rc;
   *copied = copies != 0;
-  p = NarrowStream{X, W, ldx, ldw, K, trans_x, trans_w, false};
+  p = NarrowStream{X, W, ldx, ldw, K, trans_x, trans_w};
   if (cluster) return narrow_cluster(p, s, d, *copied, stream);
   s.parts.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + copies);
   if (int rc = narrow_partial(p, M, cols, s.f32, s.parts, d, *copied, stream)) return rc;

@@ -5,7 +5,7 @@
 //   product    S = X W exactly as integers, C := sx[i] sw[n] S + beta C, or gated
 //   tokens     a = max_k |X[i,k]|, scale[i] = a / 127, Q[i,k] = round(127 X[i,k] / a)
 //
-// Few rows or few tiles: narrow_stream.cu (bytes to halves on their way to the tensor
+// Few rows or few tiles: i8_stream.cu (bytes to halves on their way to the tensor
 // cores).  Else both operands become halves in scratch, read back
 // from L2 by the pair kernel (gemm_f16_tc_kernel.cuh), whose epilogue scales.
 #include <cuda_fp16.h>
@@ -238,10 +238,19 @@ bool on_grid(const int8_t* p, int ld) {
 }
 
 int streamed(const I8Args& p, const GateArgs& g, const LoraDevice& d, cudaStream_t stream) {
-  NarrowStream r{p.X, p.W, p.ldx, p.ldw, p.K, false, false, true};
+  NarrowStream r{p.X, p.W, p.ldx, p.ldw, p.K, false, false};
   StreamSum s{};
-  const bool cluster = narrow_cluster_suits(true, p.M, p.N, p.K, p.gated(), false, d.sms);
-  if (!cluster) s.parts = narrow_parts(r, p.M, p.cols(), false, d.sms);
+  s.C = p.C;
+  s.ldc = p.ldc;
+  s.M = p.M;
+  s.N = p.N;
+  s.alpha = 1.0f;
+  s.beta = p.beta;
+  s.gate = p.gated();
+  s.scaled = true;
+  s.g = g;
+  const bool cluster = i8_cluster_suits(s, p.K, d);
+  if (!cluster) s.parts = i8_parts(r, p.M, p.cols(), d);
   const bool copy_x = !on_grid(p.X, p.ldx), copy_w = !on_grid(p.W, p.ldw);
   const int kx = (p.K + 15) / 16 * 16, kw = (p.cols() + 15) / 16 * 16;
   const size_t x_bytes = copy_x ? lora_round256(static_cast<size_t>(p.M) * kx) : 0;
@@ -265,20 +274,11 @@ int streamed(const I8Args& p, const GateArgs& g, const LoraDevice& d, cudaStream
   at += w_bytes;
   if (b.n)
     if (int rc = spread(b, false, d.sms, stream)) return rc;
-  s.C = p.C;
-  s.ldc = p.ldc;
-  s.M = p.M;
-  s.N = p.N;
-  s.alpha = 1.0f;
-  s.beta = p.beta;
-  s.gate = p.gated();
-  s.scaled = true;
-  s.g = g;
   if (cluster) {
-    if (int rc = narrow_cluster(r, s, d, b.n > 0, stream)) return rc;
+    if (int rc = i8_cluster(r, s, d, b.n > 0, stream)) return rc;
   } else {
     s.parts.part = reinterpret_cast<float*>(at);
-    if (int rc = narrow_partial(r, p.M, p.cols(), false, s.parts, d, b.n > 0, stream)) return rc;
+    if (int rc = i8_partial(r, p.M, p.cols(), s.parts, d, b.n > 0, stream)) return rc;
     if (int rc = stream_sum(s, d, stream)) return rc;
   }
   set_last_path(b.n ? "i8.stream.realigned" : "i8.stream");

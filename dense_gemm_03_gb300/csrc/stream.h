@@ -1,6 +1,6 @@
 // stream.h -- products with few rows or few tiles: as one kernel where a wave of
-// clusters covers them, else as fp32 partial sums by K chunks (narrow_stream.cu) and the
-// kernel that adds them up and finishes the result (stream_sum.cu).
+// clusters covers them, else as fp32 partial sums by K chunks (narrow_stream.cu for halves, i8_stream.cu
+// for 8-bit integers) and the kernel that adds them up and finishes the result (stream_sum.cu).
 #pragma once
 
 #include <cstddef>
@@ -25,17 +25,20 @@ int plan_chunks(int units, int blocks, int kb, int rows, int sms, int least = 1)
 constexpr int kFoldDepth = 2048;
 
 // op(X) (M x K, stored K x M where trans_x) times op(W) (K x `cols`; N x K) in halves, or
-// X W in 8-bit integers; rows on the 16-byte grid.
+// X W in 8-bit integers (i8_*); rows on the 16-byte grid.
 struct NarrowStream {
   const void *X, *W;
   long long ldx, ldw;
   int K;
-  bool trans_x, trans_w, i8;
+  bool trans_x, trans_w;
 };
 // Its partial sums; fold: of a float result.
-StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, int sms);
+StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, const LoraDevice& d);
 int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const StreamParts& parts,
                    const LoraDevice& d, bool early, cudaStream_t stream);
+StreamParts i8_parts(const NarrowStream& p, int M, int cols, const LoraDevice& d);
+int i8_partial(const NarrowStream& p, int M, int cols, const StreamParts& parts,
+               const LoraDevice& d, bool early, cudaStream_t stream);
 
 // What becomes of the sums S (gate 0: N columns; else 2 N, G and U):
 //   gate 0   C := alpha S + beta C (half, or float when f32); with scales S
@@ -53,10 +56,13 @@ struct StreamSum {
   GateArgs g;
 };
 // The whole product in one launch, finished as `s` says (its parts unused), where one
-// wave of clusters covers it.  N: output columns.
-bool narrow_cluster_suits(bool i8, int M, int N, int K, int gate, bool f32, int sms);
+// wave of clusters covers it.
+bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d);
 int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,
                    cudaStream_t stream);
+bool i8_cluster_suits(const StreamSum& s, int K, const LoraDevice& d);
+int i8_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,
+               cudaStream_t stream);
 int stream_sum(const StreamSum& s, const LoraDevice& d, cudaStream_t stream);
 
 }  // namespace gb300
