@@ -17,13 +17,13 @@
 // 1.1 us: the loads that were to run ahead did not.)
 //
 // Warps: 16 convert (quadrant q = warp % 4 has lanes, columns of W, 32 q .. + 31; warp / 4
-// the 32 k of the step), then write the sums; one issues the MMAs, one the loads.
+// the 32 k of the step), then write the sums; two issue the MMAs, one the loads.
 //
 // Shared memory: kBufs buffers of X as halves, two 64-deep halves [row][64 halves]
 // (K-major, 128-byte swizzle); then ring stages of raw steps, W as [128 k][128 bytes]
 // (of a gate, in the cluster form, two blocks [128 k][64 bytes]) and X as [row][128
-// bytes], swizzled over their rows.  Tensor memory: the sums, 128 columns, then kBufs
-// buffers of 64 columns of W.
+// bytes], swizzled over their rows.  Tensor memory: the issuers' sums, 128 columns each,
+// then kBufs buffers of 64 columns of W.
 #include "i8_convert.cuh"
 #include "narrow.cuh"
 
@@ -34,10 +34,11 @@ constexpr int kRawW = kStepK * 128;         // a step of 128 columns
 constexpr int kMaxStages = 8;
 constexpr int kBufs = 4;                    // of operands
 constexpr int kWarps = 16;                  // converting, then writing sums
-constexpr int kMmaWarp = kWarps, kLoadWarp = kWarps + 1;
-constexpr int kThreads = 32 * (kWarps + 2);
+constexpr int kIssuers = 2;
+constexpr int kMmaWarp = kWarps, kLoadWarp = kWarps + kIssuers;
+constexpr int kThreads = 32 * (kWarps + kIssuers + 1);
 constexpr int kBlockRows = 128;
-constexpr int kTmemW = 128;                 // first column of W's buffers
+constexpr int kTmemW = 128 * kIssuers;      // first column of W's buffers
 constexpr int kTmemCols = 512;
 
 struct Args : Tiles {
@@ -96,9 +97,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(op_empty(lane), 1u);
     }
     if (lane == 31) {
-      mbar_init(acc_full, 1u);
+      mbar_init(acc_full, kIssuers);
       mbar_init(acc_empty, kWarps);
-      mbar_init(done_bar, 1u);
+      mbar_init(done_bar, kIssuers);
     }
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -153,9 +154,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         settle_wait(raw_full(static_cast<int>(i % S)), (i / S) & 1u, st, 71);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp >= kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuers
+    // Issuer i takes the item's steps i, i + 2, ... into sums of its own: one thread took
+    // 0.43 us for a step's eight MMAs, their barriers and the loop, more than HBM for
+    // the step.
     if (lane == 0) {
+      const int me = warp - kMmaWarp;
       // A (W) K-major in tensor memory, B (X) K-major in shared memory
       const uint32_t idesc = make_idesc(0u, 128u, static_cast<uint32_t>(p.n_cols), 0u, 0u);
       // (descriptors are added up, and the next buffer's barrier is looked at before this
@@ -163,35 +168,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t stride = static_cast<uint32_t>(p.buf_bytes) >> 4;
       const uint64_t xd0 = smem_desc_sw128(base, 16u, 1024u);
       const uint32_t xq = static_cast<uint32_t>(p.n_cols) * 8u;   // 64 k on, in 16 bytes
-      int b = 0;
-      uint32_t phase = 0, local = 0, off = 0;
+      uint32_t step = 0, local = 0;   // of all items'
       bool ok = true, ready = false;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x, ++local) {
-        int left = p.end_step(it) - p.first_step(it);
+        const uint32_t end = step + static_cast<uint32_t>(p.end_step(it) - p.first_step(it));
         if (!wait_parity(acc_empty, (local & 1u) ^ 1u, limit, st, 72)) break;
         tc_fence_after();
-        for (uint32_t acc = 0; left > 0; --left) {
-          if (!ready && !wait_parity(op_full(b), phase, limit, st, 73)) {
+        ready = false;
+        for (uint32_t n = step + me, acc = 0; n < end; n += kIssuers) {
+          const uint32_t b = n % kBufs, next = n + kIssuers;
+          if (!ready && !wait_parity(op_full(b), (n / kBufs) & 1u, limit, st, 73)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t done = op_empty(b), wt = tmem + kTmemW + 64u * b;
-          const uint64_t xd = xd0 + off;
-          off += stride;
-          if (++b == kBufs) {
-            b = 0;
-            off = 0;
-            phase ^= 1u;
-          }
-          ready = mbar_try_wait(op_full(b), phase);
+          const uint32_t wt = tmem + kTmemW + 64u * b;
+          const uint64_t xd = xd0 + b * stride;
+          ready = next < end && mbar_try_wait(op_full(next % kBufs), (next / kBufs) & 1u);
 #pragma unroll
           for (uint32_t kk = 0; kk < 8; ++kk) {
-            mma_f16_ts(tmem, wt + 8u * kk, xd + ((kk >> 2) * xq + (kk & 3) * 2u), idesc, acc);
+            mma_f16_ts(tmem + 128u * me, wt + 8u * kk, xd + ((kk >> 2) * xq + (kk & 3) * 2u), idesc,
+                       acc);
             acc = 1u;
           }
-          mma_commit(done);
+          mma_commit(op_empty(b));
         }
+        step = end;
         if (!ok) break;
         mma_commit(acc_full);
       }
@@ -282,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       // to global memory or, the buffers being done with, to the start of shared memory
-      write_sums(tmem, quad, lane, part, kWarps / 4, min(p.rows, p.M - p.row0(it)),
+      write_sums(tmem, p.end_step(it) - p.first_step(it) > 1 ? 128u : 0u, quad, lane, part,
+                 kWarps / 4, min(p.rows, p.M - p.row0(it)),
                  kCluster ? reinterpret_cast<float*>(base_ptr)
                           : p.part + static_cast<long long>(it) * p.rows * 128);
       tc_fence_before();

@@ -49,8 +49,9 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 }
 
 // The accumulator, 32 columns of W (lanes of this warp's quadrant) by rows of X, to
-// out[row][128]; `part` of `parts` warps of the quadrant.
-__device__ __forceinline__ void write_sums(uint32_t tmem, int quad, int lane, int part, int parts,
+// out[row][128]; `part` of `parts` warps of the quadrant.  more != 0: the second half of
+// the sums lies that many columns on.
+__device__ __forceinline__ void write_sums(uint32_t tmem, uint32_t more, int quad, int lane, int part, int parts,
                                            int rows, float* out) {
   const uint32_t d0 = tmem + (static_cast<uint32_t>(32 * quad) << 16);
   out += 32 * quad + lane;
@@ -59,6 +60,17 @@ __device__ __forceinline__ void write_sums(uint32_t tmem, int quad, int lane, in
     tmem_ld_32x32b_x8(d0 + r0, g);
     tmem_ld_32x32b_x8(d0 + r0 + 8, h);
     tmem_wait_ld2(g, h);
+    if (more) {
+      uint32_t a[8], b[8];
+      tmem_ld_32x32b_x8(d0 + more + r0, a);
+      tmem_ld_32x32b_x8(d0 + more + r0 + 8, b);
+      tmem_wait_ld2(a, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = __float_as_uint(__uint_as_float(g[i]) + __uint_as_float(a[i]));
+        h[i] = __float_as_uint(__uint_as_float(h[i]) + __uint_as_float(b[i]));
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (r0 + i < rows) out[(r0 + i) * 128] = __uint_as_float(g[i]);

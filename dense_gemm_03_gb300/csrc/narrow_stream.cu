@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_parity(acc_full, local & 1u, limit, st, 77)) break;
       tc_fence_after();
       // to global memory or, the ring being done with, to the start of shared memory
-      write_sums(tmem, quad, lane, part, kEpi / 4, min(p.rows, p.M - p.row0(it)),
+      write_sums(tmem, 0u, quad, lane, part, kEpi / 4, min(p.rows, p.M - p.row0(it)),
                  kCluster ? reinterpret_cast<float*>(base_ptr)
                           : p.part + static_cast<long long>(it) * p.rows * 128);
       tc_fence_before();
