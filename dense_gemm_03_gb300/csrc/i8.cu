@@ -114,6 +114,51 @@ int spread(SpreadBatch& b, bool halves, int sms, cudaStream_t stream) {
 // = (2k + 1) a, has 127 among the factors of 2k + 1 or of A.  2k + 1 = 127 is x = a / 2,
 // whose product is 63.5 or a little more and rounds to 64, the even one; rows whose A is a
 // multiple of 127 divide instead (127 x is exact, and so is a tie's quotient).
+struct RowScale {
+  float a, inv;         // the maximum, 127 / a rounded up (0: the row's integers are zeros)
+  bool finite, divide;
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t bits) {   // of the maximum, as a half
+  RowScale s;
+  s.a = lora_h2f(static_cast<uint16_t>(bits));
+  s.finite = bits < 0x7C00u;
+  s.inv = bits != 0u && s.finite ? __fdiv_ru(127.0f, s.a) : 0.0f;
+  const uint32_t significand = (bits & 0x3FFu) | (bits >= 0x400u ? 0x400u : 0u);
+  s.divide = s.finite && bits != 0u && significand % 127u == 0u;
+  return s;
+}
+
+// The larger of each half's magnitude bits.
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint4 v) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  return __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
+}
+
+// Eight halves as integers, one to a byte.
+__device__ __forceinline__ uint2 round_row8(const RowScale& s, uint4 v) {
+  constexpr float kMagic = 12582912.0f;   // 1.5 2^23: the integer is in the low bits
+  if (!s.finite) v = make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 h = lora_h2f2(w[i]);
+    b[2 * i] = __float_as_uint(fmaf(h.x, s.inv, kMagic));
+    b[2 * i + 1] = __float_as_uint(fmaf(h.y, s.inv, kMagic));
+  }
+  if (s.divide)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 h = lora_h2f2(w[i]);
+      b[2 * i] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * h.x, s.a), kMagic));
+      b[2 * i + 1] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * h.y, s.a), kMagic));
+    }
+  return make_uint2(
+      __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+}
+
 template <int T, int V>
 __global__ void __launch_bounds__(T < 256 ? 256 : T)
     to_i8_kernel(const uint16_t* __restrict__ X, int8_t* __restrict__ Q, float* __restrict__ scales,
@@ -133,9 +178,9 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T)
       const uintptr_t a = reinterpret_cast<uintptr_t>(x + e0);
       const uint32_t m = static_cast<uint32_t>(a & 15u);
       const uint4* const blk = reinterpret_cast<const uint4*>(a - m);
-      const uint4 lo = __ldcs(blk);
+      const uint4 lo = __ldg(blk);
       if (m == 0) return lo;
-      const uint4 hi = __ldcs(blk + 1);   // (holds elements of the group)
+      const uint4 hi = __ldg(blk + 1);   // (holds elements of the group)
       const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       const uint32_t sh = (m & 3u) * 8u;
       uint32_t o[4] = {0u, 0u, 0u, 0u};
@@ -152,10 +197,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T)
     return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
   };
   uint32_t m2 = 0u;
-  auto look = [&](uint4 v) {
-    constexpr uint32_t kAbs = 0x7FFF7FFFu;
-    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
-  };
+  auto look = [&](uint4 v) { m2 = max_bits(m2, v); };
   uint4 kept[V > 0 ? V : 1];
   if constexpr (V > 0) {
 #pragma unroll
@@ -176,36 +218,18 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T)
     for (int i = 1; i < T / 32; ++i) bits = max(bits, top[i]);
   }
   if (!there) return;
-  const float a = lora_h2f(static_cast<uint16_t>(bits));
-  const bool finite = bits < 0x7C00u;
-  if (t == 0) scales[row] = __fdiv_rn(a, 127.0f);
-  const float inv = bits != 0u && finite ? __fdiv_ru(127.0f, a) : 0.0f;
-  const uint32_t significand = (bits & 0x3FFu) | (bits >= 0x400u ? 0x400u : 0u);
-  const bool divide = finite && bits != 0u && significand % 127u == 0u;
+  const RowScale scale = row_scale(bits);
+  if (t == 0) scales[row] = __fdiv_rn(scale.a, 127.0f);
   auto put = [&](int j, uint4 v) {
-    constexpr float kMagic = 12582912.0f;   // 1.5 2^23: the integer is in the low bits
-    if (!finite) v = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t b[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 h = lora_h2f2(w[i]);
-      b[2 * i] = __float_as_uint(fmaf(h.x, inv, kMagic));
-      b[2 * i + 1] = __float_as_uint(fmaf(h.y, inv, kMagic));
-      if (divide) {
-        b[2 * i] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * h.x, a), kMagic));
-        b[2 * i + 1] = __float_as_uint(__fadd_rn(__fdiv_rn(127.0f * h.y, a), kMagic));
-      }
-    }
+    const uint2 b = round_row8(scale, v);
     const int e0 = 8 * j - md;
     if (e0 >= 0 && e0 + 8 <= K) {
-      const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-      const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-      *reinterpret_cast<uint2*>(q + e0) = make_uint2(lo, hi);
+      *reinterpret_cast<uint2*>(q + e0) = b;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (e0 + i >= 0 && e0 + i < K) q[e0 + i] = static_cast<int8_t>(b[i] & 0xFFu);
+        if (e0 + i >= 0 && e0 + i < K)
+          q[e0 + i] = static_cast<int8_t>(((i < 4 ? b.x : b.y) >> (8 * (i & 3))) & 0xFFu);
     }
   };
   if constexpr (V > 0) {
@@ -215,6 +239,116 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T)
   } else {
     for (int j = t; j < groups; j += T) put(j, load(j));
   }
+}
+
+// The same for many rows on the 16-byte grid: persistent blocks, each with a ring of
+// rows in shared memory that bulk copies fill, so that loads are always in flight
+// (single rows a block: 45 us for 8192 x 8192; a copy of as many bytes takes 35).  T
+// threads a row, V pieces of 16 elements each; a group of T threads has every
+// (kRingThreads / T)-th stage to itself and refills it as soon as its threads hold the row.
+constexpr int kRingThreads = 512;
+constexpr int kRingBytes = 196608;
+constexpr int kRingStages = 48;
+
+template <int T, int V>
+__global__ void __launch_bounds__(kRingThreads, 1)
+    to_i8_ring_kernel(const uint16_t* __restrict__ X, int8_t* __restrict__ Q,
+                      float* __restrict__ scales, int M, int K, long long ldx, long long ldq,
+                      int stages, unsigned long long limit, DeviceStatus* st) {
+  constexpr int kGroups = kRingThreads / T;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) unsigned long long bars[kRingStages];
+  __shared__ uint32_t top[2][kRingThreads / 32];
+  const int group = static_cast<int>(threadIdx.x) / T, t = static_cast<int>(threadIdx.x) % T;
+  const int warp = static_cast<int>(threadIdx.x) / 32;
+  const uint32_t bytes = static_cast<uint32_t>(2 * K);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(smem_addr(&bars[s]), 1u);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+  // row number i of this block, in stage i % stages
+  auto row_of = [&](long long i) { return blockIdx.x + i * gridDim.x; };
+  auto fetch = [&](long long i, int s) {
+    const uint32_t bar = smem_addr(&bars[s]);
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_load(smem_addr(ring + static_cast<size_t>(s) * bytes), X + row_of(i) * ldx, bytes, bar);
+  };
+  if (t == 0)
+    for (int s = group; s < stages; s += kGroups)
+      if (row_of(s) < M) fetch(s, s);
+  bool ok = true;
+  int s = group, turn = 0;
+  uint32_t phase = 0;
+  for (long long i = group; ok && row_of(i) < M; i += kGroups, turn ^= 1) {
+    const long long row = row_of(i);
+    ok = wait_parity(smem_addr(&bars[s]), phase, limit, st, 80);
+    const uint4* const src = reinterpret_cast<const uint4*>(ring + static_cast<size_t>(s) * bytes);
+    uint4 v[V][2];
+    uint32_t m2 = 0u;
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int e = t + T * u;   // piece of 16
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[u][h] = 16 * e < K ? src[2 * e + h] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < V; ++u) m2 = max_bits(max_bits(m2, v[u][0]), v[u][1]);
+    constexpr uint32_t kGaveUp = 0xFFFFFFFFu;   // one thread's wait did: the whole group's
+    uint32_t bits = __reduce_max_sync(0xffffffffu, ok ? max(m2 & 0xFFFFu, m2 >> 16) : kGaveUp);
+    if constexpr (T > 32) {
+      if ((threadIdx.x & 31) == 0) top[turn][warp] = bits;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(T) : "memory");
+#pragma unroll
+      for (int w = 0; w < T / 32; ++w) bits = max(bits, top[turn][group * (T / 32) + w]);
+    }
+    ok = bits != kGaveUp;
+    if (!ok) break;
+    // every thread of the group holds its part of the row
+    if (t == 0 && row_of(i + stages) < M) fetch(i + stages, s);
+    const RowScale scale = row_scale(bits);
+    if (t == 0) scales[row] = __fdiv_rn(scale.a, 127.0f);
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const int e = t + T * u;
+      if (16 * e < K) {
+        const uint2 lo = round_row8(scale, v[u][0]), hi = round_row8(scale, v[u][1]);
+        __stcs(reinterpret_cast<uint4*>(Q + row * ldq) + e, make_uint4(lo.x, lo.y, hi.x, hi.y));
+      }
+    }
+    s += kGroups;
+    if (s >= stages) {
+      s -= stages;
+      phase ^= 1u;
+    }
+  }
+  // a wait that gave up leaves copies in flight
+  if (!ok && t == 0)
+    for (int r = group; r < stages; r += kGroups) {
+      settle_wait(smem_addr(&bars[r]), 0u, st, 81);
+      settle_wait(smem_addr(&bars[r]), 1u, st, 81);
+    }
+}
+
+template <int T, int V>
+int launch_ring(const uint16_t* X, int8_t* Q, float* scales, int M, int K, int ldx, int ldq,
+                const LoraDevice& d, cudaStream_t stream) {
+  constexpr int kGroups = kRingThreads / T;
+  static bool configured[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
+  if (dev < 64 && !configured[dev]) {
+    if (cudaFuncSetAttribute(to_i8_ring_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kRingBytes) != cudaSuccess)
+      return GEMM_ERR_CUDA;
+    configured[dev] = true;
+  }
+  const int stages = std::min(kRingStages, kRingBytes / (2 * K)) / kGroups * kGroups;
+  to_i8_ring_kernel<T, V><<<d.sms, kRingThreads, static_cast<size_t>(stages) * 2 * K, stream>>>(
+      X, Q, scales, M, K, ldx, ldq, stages, d.wait_limit_ns, d.status);
+  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 __global__ void __launch_bounds__(kThreads) zero_floats_kernel(float* p, int n) {
@@ -381,6 +515,18 @@ int gemm_f16_to_i8(const uint16_t* X, int8_t* Q, float* scales, int M, int K, in
     return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
   }
   set_last_path("to_i8");
+  // rings from 12 million elements on: 4096 x 4096 12.4 us (14.2 by single rows), 4096 x
+  // 2048 6.8 (7.3), but 2048 x 4096 7.1 (6.1) and 8192 x 1024 6.9 (6.3)
+  if (K % 16 == 0 && ldx % 8 == 0 && ldq % 16 == 0 && !misaligned({X, Q}, 16) && K <= 16384 &&
+      1ll * M * K >= 12ll << 20) {
+    set_last_path("to_i8.ring");
+    if (K <= 512) return launch_ring<32, 1>(X, Q, scales, M, K, ldx, ldq, d, stream);
+    if (K <= 1024) return launch_ring<32, 2>(X, Q, scales, M, K, ldx, ldq, d, stream);
+    if (K <= 2048) return launch_ring<32, 4>(X, Q, scales, M, K, ldx, ldq, d, stream);
+    if (K <= 4096) return launch_ring<128, 2>(X, Q, scales, M, K, ldx, ldq, d, stream);
+    if (K <= 8192) return launch_ring<128, 4>(X, Q, scales, M, K, ldx, ldq, d, stream);
+    return launch_ring<256, 4>(X, Q, scales, M, K, ldx, ldq, d, stream);
+  }
   // groups of a row: at most, when Q's rows leave its 8-byte grid
   const bool grid8 = (reinterpret_cast<uintptr_t>(Q) & 7u) == 0 && ldq % 8 == 0;
   const int groups = grid8 ? (K - 1) / 8 + 1 : K / 8 + 2;

@@ -335,7 +335,7 @@ Args plan_partial(const NarrowStream& p, int M, int cols, const LoraDevice& d) {
 StreamParts i8_parts(const NarrowStream& p, int M, int cols, const LoraDevice& d) {
   const Args a = plan_partial(p, M, cols, d);
   return StreamParts{nullptr, a.chunks, a.units, a.rows,
-                     4 * static_cast<size_t>(a.items) * a.rows * 128, kBlockRows};
+                     4 * static_cast<size_t>(a.items) * a.rows * 128, a.rows};
 }
 
 int i8_partial(const NarrowStream& p, int M, int cols, const StreamParts& parts,

@@ -85,7 +85,11 @@ template <int FIN>
 __device__ __forceinline__ void cluster_finish(const Tiles& p, const StreamSum& fin, uint32_t sums,
                                                int threads) {
   __syncwarp();
-  cluster_sync();   // every chunk's sums are there
+  // every chunk's sums are there
+  if (p.chunks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   constexpr int kGateOf = FIN == kGateGrad ? 2 : (paired<FIN>() ? 1 : 0);
   constexpr int kQuads = paired<FIN>() ? 16 : 32;   // quads of output columns in a unit
   const int it = blockIdx.x, rank = it % p.chunks, row0 = p.row0(it);
@@ -113,7 +117,8 @@ __device__ __forceinline__ void cluster_finish(const Tiles& p, const StreamSum& 
     stream_finish<kGateOf, FIN == kFloat, FIN == kScaled || FIN == kScaledGate, 4>(
         fin, row0 + r, c, n, p.vec && n == 4, s, u);
   }
-  cluster_sync();   // nobody leaves while its sums are being read
+  if (p.chunks > 1) cluster_sync();   // nobody leaves while its sums are being read
+  else __syncthreads();
 }
 
 // ------------------------------------------------------------------- plans
@@ -128,10 +133,16 @@ inline int cluster_chunks(long long tiles, int steps, int sms) {
   return best;
 }
 
+// Rows of a block: all blocks about as long, in 16s, at most `most`.
+inline int block_rows(int M, int most) {
+  const int blocks = (M + most - 1) / most;
+  return std::min(M, ((M + blocks - 1) / blocks + 15) / 16 * 16);
+}
+
 inline void common_tiles(Tiles& a, int M, int K, int rows, const LoraDevice& d) {
   a.M = M;
   a.K = K;
-  a.rows = std::min(M, rows);
+  a.rows = block_rows(M, rows);
   a.kb = (K + kStepK - 1) / kStepK;
   a.n_cols = (a.rows + 15) / 16 * 16;
   a.acc_cols = 32;
@@ -146,7 +157,7 @@ inline Tiles partial_tiles(int M, int cols, int K, int rows, int kb16, int least
                            const LoraDevice& d) {
   Tiles a{};
   common_tiles(a, M, K, rows, d);
-  const int blocks = (M + rows - 1) / rows;
+  const int blocks = (M + a.rows - 1) / a.rows;
   a.N = cols;
   a.units = (cols + 127) / 128;
   a.unit_cols = 128;
@@ -159,7 +170,7 @@ inline Tiles partial_tiles(int M, int cols, int K, int rows, int kb16, int least
 inline Tiles cluster_tiles(const StreamSum& s, int K, int rows, const LoraDevice& d) {
   Tiles a{};
   common_tiles(a, s.M, K, rows, d);
-  const int blocks = (s.M + rows - 1) / rows;
+  const int blocks = (s.M + a.rows - 1) / a.rows;
   a.N = s.gate ? 2 * s.N : s.N;
   a.unit_cols = s.gate ? 64 : 128;
   a.units = (s.N + a.unit_cols - 1) / a.unit_cols;

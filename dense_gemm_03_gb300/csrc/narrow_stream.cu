@@ -314,7 +314,7 @@ Args plan_partial(const NarrowStream& p, int M, int cols, bool fold, const LoraD
 StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, const LoraDevice& d) {
   const Args a = plan_partial(p, M, cols, fold, d);
   return StreamParts{nullptr, a.chunks, a.units, a.rows,
-                     4 * static_cast<size_t>(a.items) * a.rows * 128, kBlockRows};
+                     4 * static_cast<size_t>(a.items) * a.rows * 128, a.rows};
 }
 
 int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const StreamParts& parts,

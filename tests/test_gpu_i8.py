@@ -183,6 +183,35 @@ def test_to_i8_ties_and_every_half():
     assert bool((want.abs() == 127).any(1).all())
 
 
+@pytest.mark.parametrize("M,K,pad", [(25000, 512, 0), (26011, 496, 16), (13000, 1008, 0),
+                                     (7001, 1824, 0), (3200, 4096, 32), (1601, 8000, 0),
+                                     (803, 16384, 0), (1500, 16400, 0)])
+def test_to_i8_many_rows(M, K, pad):
+    """Rows by way of the ring (and, past its longest, not), with special rows among them.
+    rne(127 x / a) by 64-bit division, as in the test above."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    gen = t.Generator(device="cuda").manual_seed(K)
+    X = t.randn(M, K + pad, generator=gen, device="cuda").half()
+    X *= t.exp2(t.randint(-9, 9, (M, 1), generator=gen, device="cuda").float()).half()
+    X[7], X[11, 5], X[13, K - 1] = 0.0, float("inf"), float("nan")
+    X[17, :K] = 254.0
+    X[17, :100] = t.arange(100, device="cuda").half()      # ties: 127 x / 254 = x / 2
+    Q = t.full((M, K + pad), 9, dtype=t.int8, device="cuda")
+    scales = t.empty(M, device="cuda")
+    g.f16_to_i8(X, Q, scales, M=M, K=K, ldx=K + pad, ldq=K + pad)
+    sync(t)
+    assert g.last_path() == ("to_i8" if K > 16384 else "to_i8.ring")
+    x = X[:, :K].double()
+    a = x.abs().amax(1, keepdim=True)
+    want = t.round(127 * x / a)
+    want[[7, 11, 13]] = 0
+    assert t.equal(Q[:, :K].double(), want) and bool((Q[:, K:] == 9).all())
+    s = a[:, 0].float() / t.full_like(scales, 127.0)
+    fine = s.isfinite()
+    assert t.equal(scales[fine], s[fine]) and scales[11] == float("inf") and bool(scales[13].isnan())
+
+
 @pytest.mark.parametrize("K", [40, 3000, 50000])
 def test_to_i8_special_rows(K):
     """Zeros, infinities and NaNs, each in a row by itself."""
