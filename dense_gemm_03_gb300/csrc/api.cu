@@ -942,6 +942,7 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   };
+  a.set_divisors();
   // one CTA (pair) per worker; with stream-K over all tiles or the last waves
   // exactly sk_workers of them, with the stream-K tail every worker
   const long long nw = a.sk_tiles > 0 ? (a.sk_order ? workers : a.sk_workers)
@@ -1472,6 +1473,7 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   } else if (epi == kEpiF32Tma) {
     if (int rc = make_map_f32(&tmC, a.Cf, M, N, ldc, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
   }
+  a.set_divisors();
   const int grid = 2 * static_cast<int>(std::min<long long>(a.num_units, workers));
   snprintf(t_path_buf, sizeof(t_path_buf), "f16.tc.pair.%s%s%s%s%s%s%s%s",
            q.trans_a ? "ta." : "", q.trans_b ? "tb." : "", q.scaled ? "scaled." : "",

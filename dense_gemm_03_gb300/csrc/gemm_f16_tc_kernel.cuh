@@ -153,13 +153,13 @@ struct Unit {
 // share B panels in L2.
 __device__ __forceinline__ void tile_origin(const TcArgs& p, int tile, int bn, int bm_tile,
                                             int rank, Unit& x) {
-  const int group = p.group_m * p.tiles_n;
-  const int g = tile / group;
+  const int g = p.by_group.div(tile);
   const int first_m = g * p.group_m;
-  const int gm = min(p.tiles_m - first_m, p.group_m);
-  const int r = tile - g * group;
-  x.m0 = (first_m + r % gm) * bm_tile + rank * BM;
-  x.n0 = (r / gm) * bn;
+  const FastDiv& gm = p.tiles_m - first_m < p.group_m ? p.by_last : p.by_gm;
+  const int r = tile - g * static_cast<int>(p.by_group.d);
+  const int col = gm.div(r);
+  x.m0 = (first_m + r - col * static_cast<int>(gm.d)) * bm_tile + rank * BM;
+  x.n0 = col * bn;
 }
 
 // Work unit u -> output tile and K range.  Units [0, dp_tiles*splits) are
@@ -197,7 +197,7 @@ __device__ __forceinline__ Unit decode_unit(const TcArgs& p, int u, int bn, int 
     return x;
   }
   if (u < dp_units) {
-    tile = u / p.splits;
+    tile = p.splits == 1 ? u : u / p.splits;
     x.split = u - tile * p.splits;
     kpb = p.kb_per_split;
     x.tail = 0;
@@ -612,19 +612,18 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   auto stage_a = [&](int s) { return base + static_cast<uint32_t>(s * Cfg::kStageBytes); };
   auto stage_b = [&](int s) { return stage_a(s) + kAB; };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full_bar(s), LOAD == kLoadTma ? 1u : 128u);
-      mbar_init(empty_bar(s), 1u);
+  if (warp == 0) {   // a lane for each barrier (one thread took 0.3 us for all)
+    for (int i = lane; i < L::kNumBars; i += 32) {
+      uint32_t count = 1u;
+      if (i < S && LOAD != kLoadTma) count = 128u;                               // full
+      if (i == 2 * S + 2 || i == 2 * S + 3) count = (PAIR ? 2 : 1) * R::kEpiWarps;   // acc_empty
+      if (i == 2 * S + 5) count = R::kEpiWarps;                                  // tmem_free
+      mbar_init(bars + 8u * i, count);
     }
-    for (uint32_t b = 0; b < 2; ++b) {
-      mbar_init(accf_bar(b), 1u);
-      mbar_init(acce_bar(b), static_cast<uint32_t>((PAIR ? 2 : 1) * R::kEpiWarps));
-    }
-    mbar_init(done_bar, 1u);
-    mbar_init(tmem_free_bar, static_cast<uint32_t>(R::kEpiWarps));
-    for (int w = 0; w < 8; ++w)
-      for (int b = 0; b < L::kBufs; ++b) mbar_init(cfull_bar(w, b), 1u);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (LORA::kOn && threadIdx.x == 0) {
     if constexpr (LORA::kOn)
       for (int s = 0; s < S; ++s) {
         mbar_init(vfull_bar(s), 2u);
@@ -1783,7 +1782,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
     for (int b = 0; b < NB; ++b)
       if (kCs && c_pending[b] && lane == 0)
         drain_wait(cfull_bar(ew, b), (c_loads[b] - 1u) & 1u, st, 17);
-    if ((EPI == kEpiTma || kCs) && lane == 0) bulk_wait_group<0>();   // stores done reading smem
+    // the stores have read shared memory (their writes end before the kernel counts as ended)
+    if ((EPI == kEpiTma || kCs) && lane == 0) bulk_wait_group_read<0>();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(tmem_free_bar);

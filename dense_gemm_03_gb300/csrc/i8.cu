@@ -14,6 +14,7 @@
 #include "i8_convert.cuh"
 #include "lora.h"
 #include "operands.h"
+#include "ptx_i8.cuh"
 #include "stream.h"
 
 namespace gb300 {

@@ -26,6 +26,7 @@
 // then kBufs buffers of 64 columns of W.
 #include "i8_convert.cuh"
 #include "narrow.cuh"
+#include "ptx_i8.cuh"
 
 namespace gb300 {
 namespace {

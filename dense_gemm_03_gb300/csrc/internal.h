@@ -30,6 +30,21 @@ enum LoadMode : int { kLoadTma = 0, kLoadManual = 1 };
 // and TMA (CTA pairs, C 16-byte aligned, N % 4 == 0).
 enum EpiMode : int { kEpiTma = 0, kEpiManual = 1, kEpiPartial = 2, kEpiF32 = 3, kEpiF32Tma = 4 };
 
+// Division of numbers below 2^32 by a fixed one, as a multiplication.
+struct FastDiv {
+  unsigned long long m;   // 2^64 / d rounded up (0: d is 1)
+  unsigned int d;
+#ifdef __CUDACC__
+  __device__ int div(int n) const {
+    return m ? static_cast<int>(__umul64hi(m, static_cast<unsigned int>(n))) : n;
+  }
+#endif
+};
+inline FastDiv fast_div(long long d) {
+  return FastDiv{d > 1 ? ~0ull / static_cast<unsigned long long>(d) + 1 : 0,
+                 static_cast<unsigned int>(d)};
+}
+
 struct TcArgs {
   const uint16_t* A;
   const uint16_t* B;
@@ -43,6 +58,14 @@ struct TcArgs {
   int kb_per_split;   // K blocks per slice (every slice non-empty)
   int num_units;      // dp_tiles * splits + tail tiles * tail_splits
   int group_m;        // tile-order grouping along M (L2 reuse of B panels)
+  // by group_m * tiles_n, group_m, and the tile rows of the last group: a thread's
+  // divisions took 0.6 us before its first load (set_divisors)
+  FastDiv by_group, by_gm, by_last;
+  void set_divisors() {
+    by_group = fast_div(1ll * group_m * tiles_n);
+    by_gm = fast_div(group_m);
+    by_last = fast_div((tiles_m - 1) % group_m + 1);
+  }
   float* ws;          // split-K partials [splits][M][ws_ld]
   long long ws_ld;
   // Tail balancing (splits == 1 only): the first dp_tiles tiles (in visiting

@@ -123,6 +123,7 @@ extern "C" int gemm_f16_splitk_noalloc(const uint16_t* A, const uint16_t* B, uin
   a.tiles_n = (N + bn - 1) / bn;
   a.kb_total = (K + kBK - 1) / kBK;
   a.group_m = 8;
+  a.set_divisors();
   a.wait_limit_ns = wait_limit;
   a.status = status;
   const long long tiles = 1ll * a.tiles_m * a.tiles_n;
