@@ -1437,8 +1437,7 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   long long workers = std::min(tiles, slots);
   const char* cut = "";
   const long long rem = tiles % slots;
-  // (float results are folded by whole K)
-  const int first_kb = q.c_f32 ? 0 : tail_first_slice(tiles, slots, a.kb_total);
+  const int first_kb = tail_first_slice(tiles, slots, a.kb_total);
   if (first_kb > 0) {
     a.dp_tiles = static_cast<int>(tiles - rem);
     a.tail_splits = 2;

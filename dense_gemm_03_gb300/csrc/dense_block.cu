@@ -55,6 +55,17 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   return stream_sum(s, d, stream);
 }
 
+// Whether K chunks suit the product better than whole 256 x 256 tiles (`cols` columns of
+// W).  Measured, chunks against tiles: one block of rows wins as long as it is not full
+// (192 x 8192 x 2048 14.5 us, 16.4; 256 rows 16.5, 16.4); so do few tiles with a long
+// K (16 tiles: K = 1024 10.0, 10.5; K = 4096 15.0, 24.0; but 32 tiles, K = 512 10.5, 8.7 and K =
+// 1024 12.1, 11.1) and narrow results (2048 x 256 x 2048 10.8, 14.6).
+bool narrow_suits(int M, int cols, int K, int sms) {
+  const long long tiles = static_cast<long long>((M + 255) / 256) * ((cols + 255) / 256);
+  if (M <= 224) return true;
+  return 4 * tiles <= sms && (cols <= 128 || (8 * tiles <= sms && K >= 1024));
+}
+
 struct GluArgs {
   const uint16_t *X, *W;
   int M, N, K, ldx, ldw, act;
@@ -69,7 +80,7 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
   g.dC = dC;
   g.lddc = lddc;
   g.dU = gate == 2 ? C + p.N : nullptr;
-  if (lora_stream_suits(p.M, 2 * p.N, d.sms)) {
+  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) {
     StreamSum s{};
     s.C = C;
     s.ldc = ldc;
@@ -104,7 +115,7 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
 int transposed(const uint16_t* A, const uint16_t* B, void* C, bool f32, bool ta, bool tb, int M,
                int N, int K, int lda, int ldb, int ldc, float alpha, float beta, bool follows,
                const LoraDevice& d, cudaStream_t stream) {
-  if (lora_stream_suits(M, N, d.sms)) {
+  if (narrow_suits(M, N, K, d.sms)) {
     StreamSum s{};
     s.C = C;
     s.ldc = ldc;

@@ -496,7 +496,7 @@ constexpr int kFoldKb = 16;
 
 // Operands stored transposed (CTA pairs, TMA loads).  A stage's part of A is then
 // two blocks of 64 (k) rows x 64 halves, like B's.  FOLD: float results of long sums
-// (gradients over the tokens of a batch), units of whole K only.
+// (gradients over the tokens of a batch).
 template <bool TRANSA, bool TRANSB, bool FOLD>
 struct Transposed : NoLora {
   static constexpr bool kFold = FOLD;
@@ -1418,7 +1418,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
                              buf * Cfg::kAccStride + static_cast<uint32_t>(wcol0);
 
-      if (EPI != kEpiPartial && !LORA::kFold && t.tail && finish) {
+      if (EPI != kEpiPartial && t.tail && finish) {
         unsigned long long* cnt = p.tail_counters + tail_part * kTailCounters + h * 4 + q;
         // If every other slice of the tile has already published, this one
         // finishes the tile straight from TMEM and need not publish.
@@ -1437,7 +1437,19 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           // Publish this slice's partial sums, then count the slice in; the last
           // slice to arrive finishes the tile.
           float4* mine = tail_partials(p, tail_part, t.split, BN) + 32 * q + lane;
-          for (int k = 0; k < (kGate ? 2 : 1) * kSubs; ++k) {
+          if constexpr (LORA::kFold) {
+#pragma unroll
+            for (int k = 0; k < kSubs; ++k)
+              if (k < nsub && colw + kSubCols * k < p.N) {
+                const int cq0 = (wcol0 + kSubCols * k) / 4;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  __stcg(mine + (cq0 + i) * BM,
+                         make_float4(sum[kSubCols * k + 4 * i], sum[kSubCols * k + 4 * i + 1],
+                                     sum[kSubCols * k + 4 * i + 2], sum[kSubCols * k + 4 * i + 3]));
+              }
+          }
+          for (int k = 0; !LORA::kFold && k < (kGate ? 2 : 1) * kSubs; ++k) {
             // (a gate's chunks, then those it gates)
             const int kc = k < kSubs ? k : k - kSubs, col = kSubCols * kc;
             const int off = k < kSubs ? col : col + t.ncols;
@@ -1483,6 +1495,22 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         if (finish && lane == 0) *reinterpret_cast<volatile unsigned long long*>(cnt) = 0ull;
       }
 
+      if constexpr (LORA::kFold) {
+        // a tile in two slices: the other's sums (of two, in either order)
+        if (t.tail && finish) {
+          const float4* part = tail_partials(p, tail_part, 1 - t.split, BN) + 32 * q + lane +
+                               wcol0 / 4 * BM;
+#pragma unroll
+          for (int i = 0; i < kSubs * kSubCols / 4; ++i)
+            if (i / 8 < nsub && colw + kSubCols * (i / 8) < p.N) {
+              const float4 v = __ldcg(part + i * BM);
+              sum[4 * i] += v.x;
+              sum[4 * i + 1] += v.y;
+              sum[4 * i + 2] += v.z;
+              sum[4 * i + 3] += v.w;
+            }
+        }
+      }
       if (kCs && !finish) {   // unused C retired
         bool ok_c = true;
 #pragma unroll

@@ -372,6 +372,22 @@ bool on_grid(const int8_t* p, int ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 16 == 0;
 }
 
+// Whether to convert W on its way (streamed), once for each block of 128 rows, or once and
+// for all into scratch (tiled).  Estimates in us, from GB300: a 128-deep step of 128 rows
+// and columns takes 0.6 where one wave of CTAs holds all tiles, else 0.85 of an SM; the tiled
+// form makes, writes and reads back three bytes for each of W at 4.5 TB/s, then runs
+// waves of tiles at 0.3 a k-block.  Measured, streamed against tiled: 4096 x 2*8192 with 384
+// rows 75, 85, with 512 99, 85; 4096 x 4096 with 512 rows 27, 36, with 768 44, 39.
+bool stream_suits(const I8Args& p, int sms) {
+  if (p.M <= 128) return true;
+  const double steps = (p.K + 127) / 128;
+  const double units = 1.0 * ((p.M + 127) / 128) * ((p.cols() + 127) / 128);
+  const double stream = 7 + steps * (units <= sms ? 0.6 : 0.85 * units / sms);
+  const long long tiles = 1ll * ((p.M + 255) / 256) * ((p.cols() + 255) / 256);
+  const long long waves = (2 * tiles + sms - 1) / sms;
+  return stream < 0.85 * (17 + 3e-6 / 4.5 * p.K * p.cols() + 0.6 * waves * steps);
+}
+
 int streamed(const I8Args& p, const GateArgs& g, const LoraDevice& d, cudaStream_t stream) {
   NarrowStream r{p.X, p.W, p.ldx, p.ldw, p.K, false, false};
   StreamSum s{};
@@ -495,7 +511,7 @@ int gemm_i8(const int8_t* X, const int8_t* W, uint16_t* C, const float* sx, cons
   g.up = N;
   g.sx = sx;
   g.sw = sw;
-  return lora_stream_suits(M, p.cols(), d.sms) ? streamed(p, g, d, stream) : tiled(p, g, d, stream);
+  return stream_suits(p, d.sms) ? streamed(p, g, d, stream) : tiled(p, g, d, stream);
 }
 
 int gemm_f16_to_i8(const uint16_t* X, int8_t* Q, float* scales, int M, int K, int ldx, int ldq,
