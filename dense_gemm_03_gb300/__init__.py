@@ -376,6 +376,31 @@ def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True,
     _check(rc, "gemm_f16_moe")
 
 
+def _matrix(x, rows, cols, ld, dtype, name):
+    """Address and leading dimension of a rows x cols matrix of `dtype` in device memory:
+    a tensor whose rows are dense (their distance is the leading dimension unless one is
+    given), or an address, taken at its word."""
+    try:                                          # the usual tensor, in little time
+        if _dtype_names[x.dtype] == dtype and x.is_cuda and x.is_contiguous() \
+                and x.numel() >= rows * cols and ld is None:
+            return x.data_ptr(), cols
+    except (AttributeError, KeyError):
+        pass
+    if x is None or isinstance(x, int):
+        return x, cols if ld is None else ld
+    if _dtype_name(x) != dtype:
+        raise TypeError("%s is %s, not %s" % (name, _dtype_name(x), dtype))
+    if not getattr(x, "is_cuda", False):
+        raise ValueError("%s is not in device memory" % name)
+    if ld is None:
+        if x.dim() != 2 or x.shape[0] < rows or x.shape[1] < cols:
+            raise ValueError("%s is %s, not %d x %d" % (name, tuple(x.shape), rows, cols))
+        if rows * cols and (x.stride(1) != 1 and cols > 1 or x.stride(0) < cols and rows > 1):
+            raise ValueError("the rows of %s are not dense (a transposed view?)" % name)
+        ld = max(cols, x.stride(0)) if rows > 1 else cols
+    return x.data_ptr(), ld
+
+
 def _act(act):
     if isinstance(act, str):
         try:
@@ -385,7 +410,7 @@ def _act(act):
     return act
 
 
-def _trans(name, A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc, stream):
+def _trans(name, ctype, A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc, stream):
     whole = K is None
     if M is None or K is None:
         m, k = A.shape
@@ -398,10 +423,11 @@ def _trans(name, A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc,
             k, N = N, k
         if k != K and whole:
             _differ("K of B and A", k, K)
-    rc = getattr(_lib or lib(), name)(
-        bool(trans_a), bool(trans_b), _addr(A), _addr(B), _addr(C), M, N, K,
-        (M if trans_a else K) if lda is None else lda, (K if trans_b else N) if ldb is None else ldb,
-        N if ldc is None else ldc, alpha, beta, _stream(stream))
+    a, lda = _matrix(A, K if trans_a else M, M if trans_a else K, lda, "float16", "A")
+    b, ldb = _matrix(B, N if trans_b else K, K if trans_b else N, ldb, "float16", "B")
+    c, ldc = _matrix(C, M, N, ldc, ctype, "C")
+    rc = getattr(_lib or lib(), name)(bool(trans_a), bool(trans_b), a, b, c, M, N, K, lda, ldb, ldc,
+                                      alpha, beta, _stream(stream))
     if rc:
         _check(rc, name)
 
@@ -410,14 +436,15 @@ def gemm_f16_trans(A, B, C, trans_a=False, trans_b=False, alpha=1.0, beta=0.0, M
                    K=None, lda=None, ldb=None, ldc=None, stream=None):
     """C := alpha*op(A)*op(B) + beta*C on device fp16 operands: A is (M, K), or
     (K, M) with trans_a; B (K, N), or (N, K) with trans_b."""
-    _trans("gemm_f16_trans", A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc, stream)
+    _trans("gemm_f16_trans", "float16", A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb,
+           ldc, stream)
 
 
 def gemm_f16_trans_f32out(A, B, C, trans_a=False, trans_b=False, alpha=1.0, beta=0.0, M=None,
                           N=None, K=None, lda=None, ldb=None, ldc=None, stream=None):
     """As gemm_f16_trans with an fp32 C."""
-    _trans("gemm_f16_trans_f32out", A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda, ldb, ldc,
-           stream)
+    _trans("gemm_f16_trans_f32out", "float32", A, B, C, trans_a, trans_b, alpha, beta, M, N, K, lda,
+           ldb, ldc, stream)
 
 
 def _glu_dims(X, W, M, N, K):
@@ -440,9 +467,11 @@ def gemm_f16_glu(X, W, C, act="silu", M=None, N=None, K=None, ldx=None, ldw=None
     """C := f(X*Wg) .* (X*Wu) on device fp16 operands; W is (K, 2N), N gate
     columns, then N up columns.  act: "silu", "gelu", "gelu_tanh" or "relu"."""
     M, N, K = _glu_dims(X, W, M, N, K)
-    rc = (_lib or lib()).gemm_f16_glu(_addr(X), _addr(W), _addr(C), M, N, K, _act(act),
-                                      K if ldx is None else ldx, 2 * N if ldw is None else ldw,
-                                      N if ldc is None else ldc, _stream(stream))
+    act = _act(act)
+    x, ldx = _matrix(X, M, K, ldx, "float16", "X")
+    w, ldw = _matrix(W, K, 2 * N, ldw, "float16", "W")
+    c, ldc = _matrix(C, M, N, ldc, "float16", "C")
+    rc = (_lib or lib()).gemm_f16_glu(x, w, c, M, N, K, act, ldx, ldw, ldc, _stream(stream))
     if rc:
         _check(rc, "gemm_f16_glu")
 
@@ -454,27 +483,32 @@ def gemm_f16_glu_grad(dC, X, W, dGU, dX=None, dW=None, act="silu", beta=0.0, M=N
     the product; dX (M, K) and dW (K, 2N), which is added onto beta times its old
     value.  All fp16; dX and dW may be None."""
     M, N, K = _glu_dims(X, W, M, N, K)
-    rc = (_lib or lib()).gemm_f16_glu_grad(
-        _addr(dC), _addr(X), _addr(W), _addr(dGU), _addr(dX), _addr(dW), M, N, K, _act(act),
-        N if lddc is None else lddc, K if ldx is None else ldx, 2 * N if ldw is None else ldw,
-        2 * N if lddgu is None else lddgu, K if lddx is None else lddx,
-        2 * N if lddw is None else lddw, beta, _stream(stream))
+    act = _act(act)
+    dc, lddc = _matrix(dC, M, N, lddc, "float16", "dC")
+    x, ldx = _matrix(X, M, K, ldx, "float16", "X")
+    w, ldw = _matrix(W, K, 2 * N, ldw, "float16", "W")
+    gu, lddgu = _matrix(dGU, M, 2 * N, lddgu, "float16", "dGU")
+    dx, lddx = _matrix(dX, M, K, lddx, "float16", "dX")
+    dw, lddw = _matrix(dW, K, 2 * N, lddw, "float16", "dW")
+    rc = (_lib or lib()).gemm_f16_glu_grad(dc, x, w, gu, dx, dw, M, N, K, act, lddc, ldx, ldw,
+                                           lddgu, lddx, lddw, beta, _stream(stream))
     if rc:
         _check(rc, "gemm_f16_glu_grad")
 
 
-def _int8(x, name):
-    """The address of a matrix of 8-bit integers."""
-    try:
-        if _dtype_names[x.dtype] == "int8":
+def _scales(x, n, name):
+    """The address of n floats in device memory."""
+    try:                                          # the usual tensor, in little time
+        if _dtype_names[x.dtype] == "float32" and x.is_cuda and x.is_contiguous() \
+                and x.numel() >= n:
             return x.data_ptr()
     except (AttributeError, KeyError):
         pass
     if x is None or isinstance(x, int):
         return x
-    if _dtype_name(x) != "int8":
-        raise TypeError("%s is %s, not int8" % (name, _dtype_name(x)))
-    return _addr(x)
+    if not getattr(x, "is_cuda", False) and _dtype_name(x) == "float32":
+        raise ValueError("%s is not in device memory" % name)
+    return _typed(x, "float32", n, name)
 
 
 def gemm_i8(X, W, C, sx=None, sw=None, act=None, beta=0.0, M=None, N=None, K=None, ldx=None,
@@ -495,11 +529,12 @@ def gemm_i8(X, W, C, sx=None, sw=None, act=None, beta=0.0, M=None, N=None, K=Non
                 raise ValueError("W has %d columns: a gate and an up column for each output" % N)
             N //= 2
     cols = N if act is None else 2 * N
-    rc = (_lib or lib()).gemm_i8(
-        _int8(X, "X"), _int8(W, "W"), _addr(C), _typed(sx, "float32", M, "sx"),
-        _typed(sw, "float32", cols, "sw"), M, N, K, -1 if act is None else _act(act),
-        K if ldx is None else ldx, cols if ldw is None else ldw, N if ldc is None else ldc, beta,
-        _stream(stream))
+    act = -1 if act is None else _act(act)
+    x, ldx = _matrix(X, M, K, ldx, "int8", "X")
+    w, ldw = _matrix(W, K, cols, ldw, "int8", "W")
+    c, ldc = _matrix(C, M, N, ldc, "float16", "C")
+    rc = (_lib or lib()).gemm_i8(x, w, c, _scales(sx, M, "sx"), _scales(sw, cols, "sw"), M, N, K,
+                                 act, ldx, ldw, ldc, beta, _stream(stream))
     if rc:
         _check(rc, "gemm_i8")
 
@@ -509,8 +544,9 @@ def f16_to_i8(X, Q, scales, M=None, K=None, ldx=None, ldq=None, stream=None):
     if M is None or K is None:
         m, k = X.shape
         M, K = m if M is None else M, k if K is None else K
-    rc = (_lib or lib()).gemm_f16_to_i8(_addr(X), _int8(Q, "Q"), _typed(scales, "float32", M, "scales"),
-                                        M, K, K if ldx is None else ldx, K if ldq is None else ldq,
+    x, ldx = _matrix(X, M, K, ldx, "float16", "X")
+    q, ldq = _matrix(Q, M, K, ldq, "int8", "Q")
+    rc = (_lib or lib()).gemm_f16_to_i8(x, q, _scales(scales, M, "scales"), M, K, ldx, ldq,
                                         _stream(stream))
     if rc:
         _check(rc, "gemm_f16_to_i8")

@@ -155,6 +155,7 @@ int trans_entry(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, 
                 cudaStream_t stream) {
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
   if ((trans_a != 0 && trans_a != 1) || (trans_b != 0 && trans_b != 1)) return GEMM_ERR_ARG;
+  if (std::max({M, N, K}) > kMaxDim) return GEMM_ERR_ARG;
   if (!trans_a && !trans_b)
     return f32 ? gemm_f16_f32out(A, B, static_cast<float*>(C), M, N, K, lda, ldb, ldc, alpha, beta,
                                  stream)
@@ -205,7 +206,7 @@ int gemm_f16_trans_f32out(int trans_a, int trans_b, const uint16_t* A, const uin
 int gemm_f16_glu(const uint16_t* X, const uint16_t* W, uint16_t* C, int M, int N, int K, int act,
                  int ldx, int ldw, int ldc, cudaStream_t stream) {
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
-  if (!known_act(act) || N > GEMM_GLU_MAX_N) return GEMM_ERR_ARG;
+  if (!known_act(act) || N > GEMM_GLU_MAX_N || std::max(M, K) > kMaxDim) return GEMM_ERR_ARG;
   if (M == 0 || N == 0) {
     set_last_path("noop");
     return GEMM_OK;
@@ -228,7 +229,7 @@ int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, 
                       uint16_t* dX, uint16_t* dW, int M, int N, int K, int act, int lddc, int ldx,
                       int ldw, int lddgu, int lddx, int lddw, float beta, cudaStream_t stream) {
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
-  if (!known_act(act) || N > GEMM_GLU_MAX_N) return GEMM_ERR_ARG;
+  if (!known_act(act) || N > GEMM_GLU_MAX_N || std::max(M, K) > kMaxDim) return GEMM_ERR_ARG;
   const bool want_gu = M > 0 && N > 0;   // dGU has elements, and every product some
   const bool want_dx = dX && M > 0 && K > 0, want_dw = dW && N > 0 && K > 0;
   if (!want_gu && !want_dx && !want_dw) {

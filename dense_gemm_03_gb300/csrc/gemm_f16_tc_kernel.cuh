@@ -488,11 +488,11 @@ struct NoLora {
   static constexpr int kWarps = 0;
 };
 
-// With kFold the accumulator holds kFoldKb k-blocks at most; the epilogue warps add
+// With kFold the accumulator holds fold_kb k-blocks at most; the epilogue warps add
 // these parts up in registers, rounding to nearest.  The tensor core's own additions
 // truncate: over 8192 products the sums drift by 9e-6 of their norm, folded every
-// 1024 by 1e-6.
-constexpr int kFoldKb = 16;
+// 1024 by 1.3e-6, every 512 by 0.7e-6.  fold_kb is 16 from K = 4096 on, where sums rounded to
+// nearest one by one are off by as much, else 8 (4096 x 4096 over 8192: 195 us and 206).
 
 // Operands stored transposed (CTA pairs, TMA loads).  A stage's part of A is then
 // two blocks of 64 (k) rows x 64 halves, like B's.  FOLD: float results of long sums
@@ -500,6 +500,7 @@ constexpr int kFoldKb = 16;
 template <bool TRANSA, bool TRANSB, bool FOLD>
 struct Transposed : NoLora {
   static constexpr bool kFold = FOLD;
+  int fold_kb = 16;
   static constexpr bool kTransA = TRANSA;
   static constexpr bool kTransB = TRANSB;
 };
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         int first_kb = t.kb0;   // of the accumulator in hand
         for (int kb = t.kb0; kb < t.kb1; kb += KPB) {
           if constexpr (LORA::kFold) {
-            if (kb - first_kb == kFoldKb) {   // this part is the epilogue's now
+            if (kb - first_kb == x.fold_kb) {   // this part is the epilogue's now
               mma_commit_pair_multicast(accf_bar(buf), 3);
               ++local;
               buf = local & 1u;
@@ -1381,7 +1382,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
 #pragma unroll
         for (int i = 0; i < kSubs * kSubCols; ++i) sum[i] = 0.0f;
         bool ok = true;
-        for (int kb = t.kb0; kb < t.kb1; kb += kFoldKb) {
+        for (int kb = t.kb0; kb < t.kb1; kb += x.fold_kb) {
           const uint32_t b = local & 1u;
           ok = wait_parity(accf_bar(b), (local >> 1) & 1u, limit, st, 5);
           if (!ok) break;

@@ -11,13 +11,15 @@ cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CU
                    const TcArgs& args, int grid, cudaStream_t s) {
   using T = Transposed<TA, TB, false>;
   using F = Transposed<TA, TB, true>;
+  F fold;
+  fold.fold_kb = args.kb_total >= 64 ? 16 : 8;
   switch (epi) {
     case kEpiTma:
       return launch_one<256, kLoadTma, kEpiTma, true, 128, 128, 1, T>(a, b, c, args, grid, s);
     case kEpiF32Tma:
-      return launch_one<256, kLoadTma, kEpiF32Tma, true, 128, 128, 1, F>(a, b, c, args, grid, s);
+      return launch_one<256, kLoadTma, kEpiF32Tma, true, 128, 128, 1, F>(a, b, c, args, grid, s, fold);
     case kEpiF32:
-      return launch_one<256, kLoadTma, kEpiF32, true, 128, 128, 1, F>(a, b, c, args, grid, s);
+      return launch_one<256, kLoadTma, kEpiF32, true, 128, 128, 1, F>(a, b, c, args, grid, s, fold);
     default:
       return cudaErrorInvalidValue;
   }

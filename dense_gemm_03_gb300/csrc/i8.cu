@@ -487,7 +487,8 @@ int gemm_i8(const int8_t* X, const int8_t* W, uint16_t* C, const float* sx, cons
             int N, int K, int act, int ldx, int ldw, int ldc, float beta, cudaStream_t stream) {
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_DIM;
   const bool gated = act != GEMM_ACT_NONE;
-  if (act < GEMM_ACT_NONE || act > GEMM_ACT_RELU || (gated && (beta != 0.0f || N > GEMM_GLU_MAX_N)))
+  if (act < GEMM_ACT_NONE || act > GEMM_ACT_RELU ||
+      (gated && (beta != 0.0f || N > GEMM_GLU_MAX_N)) || std::max({M, N, K}) > kMaxDim)
     return GEMM_ERR_ARG;
   if (M == 0 || N == 0) {
     set_last_path("noop");
@@ -517,6 +518,7 @@ int gemm_i8(const int8_t* X, const int8_t* W, uint16_t* C, const float* sx, cons
 int gemm_f16_to_i8(const uint16_t* X, int8_t* Q, float* scales, int M, int K, int ldx, int ldq,
                    cudaStream_t stream) {
   if (M < 0 || K < 0) return GEMM_ERR_DIM;
+  if (std::max(M, K) > kMaxDim) return GEMM_ERR_ARG;
   if (M == 0) {
     set_last_path("noop");
     return GEMM_OK;

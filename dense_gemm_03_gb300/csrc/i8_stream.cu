@@ -348,7 +348,7 @@ int i8_partial(const NarrowStream& p, int M, int cols, const StreamParts& parts,
 
 bool i8_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
   // U's columns start on the 16-byte grid
-  return (!s.gate || s.N % 16 == 0) && cluster_tiles(s, K, kBlockRows, d).chunks > 0;
+  return (!s.gate || s.N % 16 == 0) && cluster_pays(cluster_tiles(s, K, kBlockRows, d), d.sms);
 }
 
 int i8_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,

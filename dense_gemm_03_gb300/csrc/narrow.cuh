@@ -133,6 +133,17 @@ inline int cluster_chunks(long long tiles, int steps, int sms) {
   return best;
 }
 
+// Whether the cluster form is expected to be faster than partial sums over all SMs: these
+// share the steps out evenly but take 3.3 us more (a second kernel, sums through L2).  A
+// step takes about 0.3 us and 0.003 for each row of the block.  (8 tiles of 256 x 128 over
+// 64 steps, 64 CTAs: cluster 13.9 us, partial 12.2.)
+inline bool cluster_pays(const Tiles& a, int sms) {
+  if (a.chunks == 0) return false;
+  const double longest = (a.kb + a.chunks - 1) / a.chunks;
+  const double even = 1.0 * a.items / a.chunks * a.kb / sms;
+  return (longest - even) * (0.3 + 0.003 * a.n_cols) < 3.3;
+}
+
 // Rows of a block: all blocks about as long, in 16s, at most `most`.
 inline int block_rows(int M, int most) {
   const int blocks = (M + most - 1) / most;
@@ -186,7 +197,11 @@ inline Tiles cluster_tiles(const StreamSum& s, int K, int rows, const LoraDevice
   return a;
 }
 
-// A launch of `grid` CTAs, in clusters of `chunks` (0: none).
+// A launch of `grid` CTAs, in clusters of `chunks` (0: none).  CTAs of a cluster wait for one
+// another, and for tensor memory that a CTA beside them on the SM may hold: two clusters
+// with a CTA each on the same two SMs could wait for ever.  So they take all of an SM's
+// shared memory, and no other CTA that uses tensor memory (which all use shared memory)
+// is there beside them.
 template <class K, class... A>
 int launch_narrow(K kernel, int threads, size_t smem, int grid, int chunks, bool early,
                   bool* configured, cudaStream_t stream, const A&... args) {
@@ -215,7 +230,7 @@ int launch_narrow(K kernel, int threads, size_t smem, int grid, int chunks, bool
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = chunks > 1 ? kSmemMax : smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = n;

@@ -301,10 +301,17 @@ int make_maps(Args& a, const NarrowStream& p, bool paired, int up, CUtensorMap* 
                  : encode_map_3d(tmX, 2, p.X, {K, a.M, 0}, {p.ldx, 0}, {64, a.n_cols, 0});
 }
 
+// The longest of `chunks` chunks of K.
+int longest_chunk(int K, int chunks) {
+  const int steps = (K + kStepK - 1) / kStepK;
+  return std::min(K, (steps + chunks - 1) / chunks * kStepK);
+}
+
 Args plan_partial(const NarrowStream& p, int M, int cols, bool fold, const LoraDevice& d) {
   Args a{};
-  static_cast<Tiles&>(a) = partial_tiles(M, cols, p.K, kBlockRows, (p.K + 63) / 64,
-                                         fold ? (p.K + kFoldDepth - 1) / kFoldDepth : 1, d);
+  int least = 1;
+  while (fold && longest_chunk(p.K, least) > kFoldDepth) ++least;
+  static_cast<Tiles&>(a) = partial_tiles(M, cols, p.K, kBlockRows, (p.K + 63) / 64, least, d);
   lay_out(a, p, kMaxStages, false);
   return a;
 }
@@ -328,8 +335,8 @@ int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const Stre
 
 bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
   if (s.gate && s.N % 8 != 0) return false;   // U's columns start on TMA's 16-byte grid
-  const int chunks = cluster_tiles(s, K, kBlockRows, d).chunks;
-  return chunks > 0 && (!s.f32 || (K + chunks - 1) / chunks + kStepK <= kFoldDepth);
+  const Tiles a = cluster_tiles(s, K, kBlockRows, d);
+  return cluster_pays(a, d.sms) && (!s.f32 || longest_chunk(K, a.chunks) <= kFoldDepth);
 }
 
 int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,

@@ -9,6 +9,9 @@
 
 namespace gb300 {
 
+// Largest size of the calls below: sizes are rounded up to tiles in 32 bits.
+constexpr int kMaxDim = 0x7fffffff - 1023;
+
 inline bool misaligned(std::initializer_list<const void*> ptrs, size_t elem) {
   uintptr_t bits = 0;
   for (const void* p : ptrs) bits |= reinterpret_cast<uintptr_t>(p);

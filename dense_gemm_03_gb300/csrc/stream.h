@@ -21,8 +21,9 @@ struct StreamParts {
 // Chunks per unit (of `kb` steps of 16 KB of W each): see lora_stream.cu.
 int plan_chunks(int units, int blocks, int kb, int rows, int sms, int least = 1);
 
-// Longest chunk of K of a float result: the tensor core's additions truncate.
-constexpr int kFoldDepth = 2048;
+// Longest chunk of K of a float result: the tensor core's additions truncate (over 512
+// products by 0.7e-6 of the sums' norm).
+constexpr int kFoldDepth = 512;
 
 // op(X) (M x K, stored K x M where trans_x) times op(W) (K x `cols`; N x K) in halves, or
 // X W in 8-bit integers (i8_*); rows on the 16-byte grid.

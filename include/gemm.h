@@ -232,14 +232,15 @@ int gemm_f16_moe(const uint16_t* X, const uint16_t* Wr, const uint16_t* W1, cons
  * Dense block: the gated projections of a model's feed-forward block, their
  * gradients, products with transposed operands, and products in 8-bit integers.
  * Same types, layouts, streams, graphs, scratch and errors as above; results overlap
- * no operand.
+ * no operand; a size past 2^31 - 1024 is GEMM_ERR_ARG.
  *
  * C := alpha * op(A) * op(B) + beta * C with op(A) = A, or A^T where trans_a is 1;
  * likewise B (another value: GEMM_ERR_ARG).  M, N, K are those of op(A) (M x K) and
  * op(B) (K x N): with trans_a A is stored K x M, lda >= M; with trans_b B is stored
  * N x K, ldb >= K.  The gradients of C = X * W are products of this kind: dX = dC * W^T
  * and dW = X^T * dC (in float, beta = 1 adds up micro-batches).  Otherwise as
- * gemm_f16_ld and gemm_f16_f32out, which do the work when neither is transposed.
+ * gemm_f16_ld and gemm_f16_f32out, which do the work when neither is transposed; with a
+ * transposed operand a float C's sums are rounded to nearest at least every 1024 products.
  */
 int gemm_f16_trans(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, uint16_t* C,
                    int M, int N, int K, int lda, int ldb, int ldc, float alpha, float beta,

@@ -114,23 +114,73 @@ def test_to_i8_refusals(L):
     assert call(0, 8, X=None, Q=None, scales=None) == 0
 
 
+def test_matrix_of_the_binding():
+    """Addresses and leading dimensions of what the calls are given.  (A tensor that says
+    it is in device memory; nothing is launched.)"""
+    torch = pytest.importorskip("torch")
+
+    class OnDevice:
+        is_cuda = True
+
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    t = torch.zeros(8, 12, dtype=torch.float16)
+    m = lambda x, rows, cols, ld=None: g._matrix(OnDevice(x), rows, cols, ld, "float16", "X")
+    assert m(t, 8, 12) == (t.data_ptr(), 12)
+    assert m(t[2:6, 4:], 4, 8) == (t[2:, 4:].data_ptr(), 12)      # rows of a larger matrix
+    assert m(t[:, :5], 3, 5, 24) == (t.data_ptr(), 24)            # a given one counts
+    assert m(t[3:4, :7], 1, 7) == (t[3:].data_ptr(), 7)
+    assert g._matrix(4096, 8, 12, None, "float16", "X") == (4096, 12)
+    assert g._matrix(None, 8, 12, None, "float16", "X") == (None, 12)
+    for bad in (t.t(), t[:, ::2], t[::2].t()):
+        with pytest.raises(ValueError, match="not dense"):
+            m(bad, *bad.shape)
+    with pytest.raises(ValueError, match="not 9 x 12"):
+        m(t, 9, 12)
+    with pytest.raises(ValueError, match="not 8 x 13"):
+        m(t, 8, 13)
+    with pytest.raises(TypeError, match="X is bfloat16"):
+        m(t.bfloat16(), 8, 12)
+    with pytest.raises(ValueError, match="device memory"):
+        g._matrix(t, 8, 12, None, "float16", "X")
+    with pytest.raises(ValueError, match="device memory"):
+        g._matrix(t.numpy(), 8, 12, None, "float16", "X")
+
+
 def test_i8_binding(L):
     torch = pytest.importorskip("torch")
     q = lambda *s: torch.zeros(*s, dtype=torch.int8)
     c = torch.zeros(2, 4, dtype=torch.float16)
     with pytest.raises(TypeError, match="X is float16"):
         g.gemm_i8(c, q(4, 4), c)
+    with pytest.raises(ValueError, match="X is not in device memory"):
+        g.gemm_i8(q(2, 4), q(4, 4), c)
     with pytest.raises(TypeError, match="W is uint8"):
-        g.gemm_i8(q(2, 4), torch.zeros(4, 4, dtype=torch.uint8), c)
+        g.gemm_i8(16, torch.zeros(4, 4, dtype=torch.uint8), 16, M=2, K=4)
     with pytest.raises(TypeError, match="sx is float16"):
-        g.gemm_i8(q(2, 4), q(4, 4), c, torch.zeros(2, dtype=torch.float16))
-    with pytest.raises(ValueError, match="sw is not 8 dense"):
-        g.gemm_i8(q(2, 4), q(4, 8), c, None, torch.zeros(4), "silu")
+        g.gemm_i8(16, 16, 16, torch.zeros(2, dtype=torch.float16), M=2, N=4, K=4)
+    with pytest.raises(ValueError, match="sw is not in device memory"):
+        g.gemm_i8(16, 16, 16, None, torch.zeros(8), "silu", M=2, N=4, K=4)
     with pytest.raises(ValueError, match="K of W and X"):
         g.gemm_i8(q(2, 4), q(5, 4), c)
     with pytest.raises(ValueError, match="columns"):
         g.gemm_i8(q(2, 4), q(4, 7), c, act="relu")
     with pytest.raises(TypeError, match="Q is float16"):
-        g.f16_to_i8(c, c, torch.zeros(2))
-    with pytest.raises(ValueError, match="scales is not 2 dense"):
-        g.f16_to_i8(c, q(2, 4), torch.zeros(1))
+        g.f16_to_i8(16, c, 16, M=2, K=4)
+    with pytest.raises(ValueError, match="scales is not in device memory"):
+        g.f16_to_i8(16, 16, torch.zeros(1), M=2, K=4)
+
+
+def test_sizes_near_the_largest_int(L):
+    for M, N, K in ((BIG, 8, 8), (8, BIG, 8), (8, 8, BIG)):
+        assert L.gemm_f16_trans(1, 0, 16, 16, 16, M, N, K, BIG, BIG, BIG, 1.0, 0.0, None) == -7
+        assert L.gemm_f16_glu(16, 16, 16, M, N, K, 0, BIG, BIG, BIG, None) == -7
+        assert L.gemm_f16_glu_grad(16, 16, 16, 16, 16, 16, M, N, K, 0, BIG, BIG, BIG, BIG, BIG, BIG,
+                                   0.0, None) == -7
+        assert L.gemm_i8(16, 16, 16, None, None, M, N, K, -1, BIG, BIG, BIG, 0.0, None) == -7
+    assert L.gemm_f16_to_i8(16, 16, 16, BIG, 8, BIG, BIG, None) == -7
+    assert L.gemm_f16_to_i8(16, 16, 16, 8, BIG, BIG, BIG, None) == -7
