@@ -16,9 +16,8 @@ cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CU
   x.a = gate;
   if (epi == kEpiTma)
     return launch_one<256, kLoadTma, kEpiTma, true, 128, 128, 1, G>(a, b, c, args, grid, s, x);
-  // (a half C off the 16-byte grid is written by way of an aligned copy; a gate's
-  // gradient has two results and goes there directly)
-  if constexpr (GATE == 2)
+  // (a plain product's C off the 16-byte grid is written by way of an aligned copy)
+  if constexpr (GATE != 0)
     if (epi == kEpiManual)
       return launch_one<256, kLoadTma, kEpiManual, true, 128, 128, 1, G>(a, b, c, args, grid, s, x);
   return cudaErrorInvalidValue;

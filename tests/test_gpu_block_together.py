@@ -296,3 +296,38 @@ def test_past_32_bit_offsets(op):
         i = rows(M) if op == "i8" else t.arange(M)
         cols = t.tensor([0, 77, N // 2, N - 1])
         ref.check(C[i][:, cols].cpu(), *ref.i8(X[i].cpu(), W[:, cols].cpu(), sx[i].cpu(), None), op)
+
+
+def test_example():
+    """It runs, and its gradients are the definition's: those of the mean squared
+    distance, by 64-bit autograd on the same rows."""
+    import importlib.util
+    import os
+    t = torch()
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "dense_block.py")
+    spec = importlib.util.spec_from_file_location("dense_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    out = ex.main(H=64, I=96, T=40, steps=2)
+    assert len(out["losses"]) == 2 and all(np.isfinite(out["losses"]))
+    # 8 bits: two roundings to 1/254 of a row's or channel's largest entry on each side
+    assert 0 < out["off"] < 0.1
+    gen = t.Generator(device="cuda").manual_seed(8)
+    x, dy = (t.randn(s, generator=gen, device="cuda").half() for s in ((40, 64), (40, 64)))
+    w1, w2 = out["weights"]
+    dw1, dw2 = (t.full(w.shape, float("nan"), device="cuda") for w in (w1, w2))
+    h, _ = ex.forward(x, w1, w2)
+    ex.backward(x, w1, w2, h, dy, dw1, dw2, True)
+    a, b = (w.double().requires_grad_(True) for w in (w1, w2))
+    s = x.double() @ a
+    y = (t.nn.functional.silu(s[:, :96]) * s[:, 96:]) @ b
+    y.backward(dy.double())
+    # h, dh and dgu are halves: each rounding is at most 2^-11 of every term
+    terms = lambda p, q: p.double().abs().t() @ q.double().abs()
+    assert bool(((dw2.double() - b.grad).abs() <= 1.01 * ref.HALF * terms(h, dy) + 1e-6).all())
+    dh_terms = dy.double().abs() @ w2.double().abs().t()
+    g_, u_ = s[:, :96].detach(), s[:, 96:].detach()
+    f, df = ref.act_both("silu", g_)
+    each = t.cat([dh_terms * u_.abs() * df.abs(), dh_terms * f.abs()], 1)
+    assert bool(((dw1.double() - a.grad).abs() <= 2.02 * ref.HALF * (x.double().abs().t() @ each) + 1e-6).all())
