@@ -376,6 +376,18 @@ def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True,
     _check(rc, "gemm_f16_moe")
 
 
+_devices = 0      # counted at the first call; with one, tensors are where they must be
+
+
+def _elsewhere(x, name):
+    """Refuses a tensor on another device than the current one, which calls run on."""
+    global _devices
+    import torch
+    _devices = _devices or torch.cuda.device_count()
+    if _devices > 1 and x.get_device() != torch.cuda.current_device():
+        raise ValueError("%s is on device %d, not the current one" % (name, x.get_device()))
+
+
 def _matrix(x, rows, cols, ld, dtype, name):
     """Address and leading dimension of a rows x cols matrix of `dtype` in device memory:
     a tensor whose rows are dense (their distance is the leading dimension unless one is
@@ -383,6 +395,8 @@ def _matrix(x, rows, cols, ld, dtype, name):
     try:                                          # the usual tensor, in little time
         if _dtype_names[x.dtype] == dtype and x.is_cuda and x.is_contiguous() \
                 and x.numel() >= rows * cols and ld is None:
+            if _devices != 1:
+                _elsewhere(x, name)
             return x.data_ptr(), cols
     except (AttributeError, KeyError):
         pass
@@ -392,6 +406,7 @@ def _matrix(x, rows, cols, ld, dtype, name):
         raise TypeError("%s is %s, not %s" % (name, _dtype_name(x), dtype))
     if not getattr(x, "is_cuda", False):
         raise ValueError("%s is not in device memory" % name)
+    _elsewhere(x, name)
     if ld is None:
         if x.dim() != 2 or x.shape[0] < rows or x.shape[1] < cols:
             raise ValueError("%s is %s, not %d x %d" % (name, tuple(x.shape), rows, cols))
@@ -517,6 +532,8 @@ def gemm_i8(X, W, C, sx=None, sw=None, act=None, beta=0.0, M=None, N=None, K=Non
     None for ones, C fp16.  With an activation W is (K, 2N), sw has 2N scales and
     C := f(G) .* U of the scaled gate and up products."""
     whole = K is None
+    if act == -1:
+        act = None
     if M is None or K is None:
         m, k = X.shape
         M, K = m if M is None else M, k if K is None else K

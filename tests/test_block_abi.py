@@ -139,6 +139,16 @@ def test_matrix_of_the_binding():
     for bad in (t.t(), t[:, ::2], t[::2].t()):
         with pytest.raises(ValueError, match="not dense"):
             m(bad, *bad.shape)
+    seen = g._devices
+    try:
+        g._devices = 2          # as if there were another: get_device() of a CPU tensor is -1
+        with pytest.MonkeyPatch.context() as patch:
+            patch.setattr(torch.cuda, "current_device", lambda: 0)
+            for x in (t, t[:, :5]):
+                with pytest.raises(ValueError, match="on device -1"):
+                    m(x, 2, 5)
+    finally:
+        g._devices = seen
     with pytest.raises(ValueError, match="not 9 x 12"):
         m(t, 9, 12)
     with pytest.raises(ValueError, match="not 8 x 13"):
