@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();   // copies onto the 16-byte grid, if any
     // the first item's first steps: their stages are empty
     if (lane == 0) {
-      const int it = blockIdx.x, n = min(S, p.end_step(it) - p.first_step(it));
+      const int it = blockIdx.x, n = min(S, p.steps(it));
       for (int s = 0; s < n; ++s) load_step(s, p.n0(it), p.row0(it), p.first_step(it) + s);
     }
     __syncwarp();
@@ -128,11 +128,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       // (the first item's first steps are on their way)
-      int skip = min(S, p.end_step(blockIdx.x) - p.first_step(blockIdx.x)), s = 0;
+      int skip = min(S, p.steps(blockIdx.x)), s = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        const int n0 = p.n0(it), row0 = p.row0(it), end = p.end_step(it);
+        const int n0 = p.n0(it), row0 = p.row0(it), end = p.first_step(it) + p.steps(it);
         for (int step = p.first_step(it); step < end; ++step) {
           if (skip > 0) {
             --skip;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t step = 0, local = 0;   // of all items'
       bool ok = true, ready = false;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x, ++local) {
-        const uint32_t end = step + static_cast<uint32_t>(p.end_step(it) - p.first_step(it));
+        const uint32_t end = step + static_cast<uint32_t>(p.steps(it));
         if (!wait_parity(acc_empty, (local & 1u) ^ 1u, limit, st, 72)) break;
         tc_fence_after();
         ready = false;
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t wt = tmem + kTmemW + 64u * b;
           const uint64_t xd = xd0 + b * stride;
-          ready = next < end && mbar_try_wait(op_full(next % kBufs), (next / kBufs) & 1u);
+          ready = next < end && mbar_test_wait(op_full(next % kBufs), (next / kBufs) & 1u);
 #pragma unroll
           for (uint32_t kk = 0; kk < 8; ++kk) {
             mma_f16_ts(tmem + 128u * me, wt + 8u * kk, xd + ((kk >> 2) * xq + (kk & 3) * 2u), idesc,
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, op_phase = 0, local = 0;
     bool ok = true;
     for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x, ++local) {
-      for (int left = p.end_step(it) - p.first_step(it); left > 0; --left) {
+      for (int left = p.steps(it); left > 0; --left) {
         if (!wait_parity(raw_full(s), phase, limit, st, 75) ||
             !wait_parity(op_empty(b), op_phase ^ 1u, limit, st, 76)) {
           ok = false;
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after();
       // to global memory or, the buffers being done with, to the start of shared memory
-      write_sums(tmem, p.end_step(it) - p.first_step(it) > 1 ? 128u : 0u, quad, lane, part,
+      write_sums(tmem, p.steps(it) > 1 ? 128u : 0u, quad, lane, part,
                  kWarps / 4, min(p.rows, p.M - p.row0(it)),
                  kCluster ? reinterpret_cast<float*>(base_ptr)
                           : p.part + static_cast<long long>(it) * p.rows * 128);

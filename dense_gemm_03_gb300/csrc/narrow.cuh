@@ -25,6 +25,7 @@ constexpr bool paired() {
 struct Tiles {
   int M, N, K;                  // rows; columns of W that exist
   int kb, chunks, units, items; // steps, chunks, units, blocks x units x chunks
+  int each, more;               // kb / chunks, kb % chunks
   int unit_cols;                // first columns of units apart
   int rows;                     // rows of a block (at most)
   int n_cols, acc_cols;         // columns of the accumulator
@@ -34,11 +35,28 @@ struct Tiles {
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
 
-  __device__ int first_step(int it) const { return it % chunks * kb / chunks; }
-  __device__ int end_step(int it) const { return (it % chunks + 1) * kb / chunks; }
+  // the first kb % chunks chunks of an output are a step longer than the rest
+  __device__ int first_step(int it) const {
+    const int c = it % chunks;
+    return c * each + min(c, more);
+  }
+  __device__ int steps(int it) const { return each + (it % chunks < more ? 1 : 0); }
   __device__ int n0(int it) const { return it / chunks % units * unit_cols; }
   __device__ int row0(int it) const { return it / chunks / units * rows; }
 };
+
+// Whether the phase is complete, without a pause (try_wait may suspend the thread).
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
@@ -163,6 +181,13 @@ inline void common_tiles(Tiles& a, int M, int K, int rows, const LoraDevice& d) 
   a.status = d.status;
 }
 
+inline void cut(Tiles& a, long long tiles, int chunks) {
+  a.chunks = chunks;
+  a.each = chunks ? a.kb / chunks : 0;
+  a.more = a.kb - a.each * chunks;
+  a.items = static_cast<int>(tiles * chunks);
+}
+
 // Partial sums over persistent CTAs.
 inline Tiles partial_tiles(int M, int cols, int K, int rows, int kb16, int least,
                            const LoraDevice& d) {
@@ -172,8 +197,8 @@ inline Tiles partial_tiles(int M, int cols, int K, int rows, int kb16, int least
   a.N = cols;
   a.units = (cols + 127) / 128;
   a.unit_cols = 128;
-  a.chunks = std::min(a.kb, plan_chunks(a.units, blocks, kb16, a.rows, d.sms, least));
-  a.items = blocks * a.units * a.chunks;
+  cut(a, 1ll * blocks * a.units,
+      std::min(a.kb, plan_chunks(a.units, blocks, kb16, a.rows, d.sms, least)));
   return a;
 }
 
@@ -185,8 +210,8 @@ inline Tiles cluster_tiles(const StreamSum& s, int K, int rows, const LoraDevice
   a.N = s.gate ? 2 * s.N : s.N;
   a.unit_cols = s.gate ? 64 : 128;
   a.units = (s.N + a.unit_cols - 1) / a.unit_cols;
-  a.chunks = cluster_chunks(1ll * blocks * a.units, a.kb, d.sms);
-  a.items = blocks * a.units * a.chunks;
+  const long long tiles = 1ll * blocks * a.units;
+  cut(a, tiles, cluster_chunks(tiles, a.kb, d.sms));
   uintptr_t bits = reinterpret_cast<uintptr_t>(s.C);
   a.vec = s.ldc % 4 == 0;
   if (s.gate == 2) {

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_wait();   // copies onto the 16-byte grid, if any
     // the first item's first steps: their stages are empty
     if (lane == 0) {
-      const int it = blockIdx.x, n = min(S, p.end_step(it) - p.first_step(it));
+      const int it = blockIdx.x, n = min(S, p.steps(it));
       for (int s = 0; s < n; ++s) load_step(s, p.n0(it), p.row0(it), p.first_step(it) + s);
     }
     __syncwarp();
@@ -148,11 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       // (the first item's first steps are on their way)
-      int skip = min(S, p.end_step(blockIdx.x) - p.first_step(blockIdx.x)), s = 0;
+      int skip = min(S, p.steps(blockIdx.x)), s = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x) {
-        const int n0 = p.n0(it), row0 = p.row0(it), end = p.end_step(it);
+        const int n0 = p.n0(it), row0 = p.row0(it), end = p.first_step(it) + p.steps(it);
         for (int step = p.first_step(it); step < end; ++step) {
           if (skip > 0) {
             --skip;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, local = 0, off = 0;
       bool ok = true, ready = false;
       for (int it = blockIdx.x; it < p.items && ok; it += gridDim.x, ++local) {
-        int left = p.end_step(it) - p.first_step(it);
+        int left = p.steps(it);
         if (!wait_parity(acc_empty, (local & 1u) ^ 1u, limit, st, 72)) break;
         tc_fence_after();
         for (uint32_t acc = 0; left > 0; --left) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             off = 0;
             phase ^= 1u;
           }
-          ready = mbar_try_wait(full_bar(s), phase);
+          ready = left > 1 && mbar_test_wait(full_bar(s), phase);
 #pragma unroll
           for (uint32_t kk = 0; kk < 8; ++kk) {
             mma_f16_ss(tmem, wd + ((kk >> 2) * wq + (kk & 3) * wk), xd + ((kk >> 2) * xq + (kk & 3) * xk),
@@ -309,8 +309,8 @@ int longest_chunk(int K, int chunks) {
 
 Args plan_partial(const NarrowStream& p, int M, int cols, bool fold, const LoraDevice& d) {
   Args a{};
-  int least = 1;
-  while (fold && longest_chunk(p.K, least) > kFoldDepth) ++least;
+  // chunks of kFoldDepth at most
+  const int least = fold ? ((p.K + kStepK - 1) / kStepK - 1) / (kFoldDepth / kStepK) + 1 : 1;
   static_cast<Tiles&>(a) = partial_tiles(M, cols, p.K, kBlockRows, (p.K + 63) / 64, least, d);
   lay_out(a, p, kMaxStages, false);
   return a;

@@ -340,3 +340,23 @@ def test_long_k_tail(M, N, K):
     assert float((gu.double().abs() @ W.double().abs().t()).max()) < 2 ** 24
     assert t.equal(dX, (gu.double() @ W.double().t()).half())
     assert t.equal(dW, (X.double().t() @ gu.double()).half())
+
+
+@pytest.mark.parametrize("f32", [True, False])
+def test_sums_over_millions_of_tokens(f32):
+    """So many short chunks of K that their count times K's steps passes 32 bits.  Of -1, 0
+    and 1 every partial sum is an integer below 2^24: a float result is exact."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    K, M, N = 13_000_007, 64, 56
+    gen = t.Generator(device="cuda").manual_seed(7)
+    A = t.randint(-1, 2, (K, M), generator=gen, device="cuda", dtype=t.int8).half()
+    B = t.randint(-1, 2, (K, N), generator=gen, device="cuda", dtype=t.int8).half()
+    want = t.zeros(M, N, dtype=t.float64, device="cuda")
+    for k in range(0, K, 1 << 20):
+        want += (A[k:k + (1 << 20)].double().t() @ B[k:k + (1 << 20)].double())
+    C = t.full((M, N), float("nan"), dtype=t.float32 if f32 else t.float16, device="cuda")
+    (g.gemm_f16_trans_f32out if f32 else g.gemm_f16_trans)(A, B, C, True, False)
+    sync(t)
+    # half results: |sums| stay below 2^24, exact in fp32 too, and are rounded once
+    assert t.equal(C, want.to(C.dtype))
