@@ -1348,7 +1348,7 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   const size_t c_bytes = copy_c ? round256(static_cast<size_t>(M) * n8 * 2) : 0;
   uint16_t* c_user = nullptr;
   long long ldc_user = 0;
-  bool prepass = false;
+  bool copied = false;
   if (a_bytes + b_bytes + c_bytes) {
     uint8_t* buf = nullptr;
     {
@@ -1395,8 +1395,9 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
       ldc = n8;
     }
     if (batch.n > 0) {
+      batch.early = true;
       if (launch_realign_f16(batch, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-      prepass = true;
+      copied = true;
     }
   }
   const bool vec_c = q.c_f32 && aligned16(q.C) && ldc % 4 == 0;
@@ -1406,7 +1407,7 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
 
   TcArgs a{};
   a.wait_operands = 1;
-  a.pdl = prepass || q.follows;
+  a.pdl = true;
   a.A = A;
   a.B = B;
   a.C = C;
@@ -1480,7 +1481,7 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
            q.gate == 2 ? "gate_grad." : (q.gate ? "gate." : ""),
            epi == kEpiF32Tma ? "epi_f32_tma"
                              : (epi == kEpiF32 ? "epi_f32" : (epi == kEpiTma ? "epi_tma" : "epi_manual")),
-           cut, prepass ? ".realigned" : "", c_user ? ".c" : "");
+           cut, copied ? ".realigned" : "", c_user ? ".c" : "");
   t_last_path = t_path_buf;
   const cudaError_t e =
       q.gate || q.scaled

@@ -139,6 +139,7 @@ __device__ __forceinline__ void realign_rows(const uint16_t* __restrict__ src, l
 
 // Up to three copies in one launch: blocks [end[i-1], end[i]) copy job i.
 __global__ void realign_f16_kernel(const RealignBatch b) {
+  griddep_wait();
   int i = 0;
   while (i + 1 < b.n && static_cast<int>(blockIdx.x) >= b.end[i]) ++i;
   const int first = i ? b.end[i - 1] : 0;
@@ -556,7 +557,9 @@ cudaError_t launch_f16x3_split(const float* A, long long lda, const float* B, lo
 
 cudaError_t launch_realign_f16(const RealignBatch& batch, cudaStream_t stream) {
   if (batch.n < 1 || batch.n > 3) return cudaErrorInvalidValue;
-  realign_f16_kernel<<<batch.end[batch.n - 1], 256, 0, stream>>>(batch);
+  const unsigned grid = static_cast<unsigned>(batch.end[batch.n - 1]);
+  if (batch.early) return counted_launch(launch_early(realign_f16_kernel, grid, 256, 0, stream, batch));
+  realign_f16_kernel<<<grid, 256, 0, stream>>>(batch);
   return counted_launch(cudaGetLastError());
 }
 

@@ -30,9 +30,9 @@ int blank(uint16_t* C, long long ldc, int M, int N, float beta, const LoraDevice
 }
 
 // The streamed form: op(X) op(W) with `cols` columns, then the sum `s` (its parts are
-// filled in here).  `follows`: a kernel of the same call was launched just before.
+// filled in here).
 int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ldw, bool trans_w,
-             int M, int cols, int K, StreamSum s, bool follows, const LoraDevice& d,
+             int M, int cols, int K, StreamSum s, const LoraDevice& d,
              cudaStream_t stream, bool* copied) {
   Aligned x(X, ldx, trans_x ? K : M, trans_x ? M : K, true);
   Aligned w(W, ldw, trans_w ? cols : K, trans_w ? K : cols, true);
@@ -44,14 +44,13 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   if (copies + s.parts.bytes)
     if (int rc = routed_scratch(stream, copies + s.parts.bytes, &buf)) return rc;
   if (int rc = align_operands({{x, &X, &ldx}, {w, &W, &ldw}}, static_cast<uint8_t*>(buf), d.sms,
-                              stream))
+                              stream, true))
     return rc;
   *copied = copies != 0;
   p = NarrowStream{X, W, ldx, ldw, K, trans_x, trans_w};
-  const bool early = *copied || follows;
-  if (cluster) return narrow_cluster(p, s, d, early, stream);
+  if (cluster) return narrow_cluster(p, s, d, stream);
   s.parts.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + copies);
-  if (int rc = narrow_partial(p, M, cols, s.f32, s.parts, d, early, stream)) return rc;
+  if (int rc = narrow_partial(p, M, cols, s.f32, s.parts, d, stream)) return rc;
   return stream_sum(s, d, stream);
 }
 
@@ -89,8 +88,8 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
     s.gate = gate;
     s.g = g;
     bool copied = false;
-    if (int rc = streamed(p.X, p.ldx, false, p.W, p.ldw, false, p.M, 2 * p.N, p.K, s, false, d,
-                          stream, &copied))
+    if (int rc = streamed(p.X, p.ldx, false, p.W, p.ldw, false, p.M, 2 * p.N, p.K, s, d, stream,
+                          &copied))
       return rc;
     set_last_path(copied ? "glu.stream.realigned" : "glu.stream");
     return GEMM_OK;
@@ -113,7 +112,7 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
 
 // C := alpha op(A) op(B) + beta C, checked, with M, N, K > 0 and alpha != 0.
 int transposed(const uint16_t* A, const uint16_t* B, void* C, bool f32, bool ta, bool tb, int M,
-               int N, int K, int lda, int ldb, int ldc, float alpha, float beta, bool follows,
+               int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
                const LoraDevice& d, cudaStream_t stream) {
   if (narrow_suits(M, N, K, d.sms)) {
     StreamSum s{};
@@ -125,7 +124,7 @@ int transposed(const uint16_t* A, const uint16_t* B, void* C, bool f32, bool ta,
     s.beta = beta;
     s.f32 = f32;
     bool copied = false;
-    if (int rc = streamed(A, lda, ta, B, ldb, tb, M, N, K, s, follows, d, stream, &copied)) return rc;
+    if (int rc = streamed(A, lda, ta, B, ldb, tb, M, N, K, s, d, stream, &copied)) return rc;
     set_last_path(copied ? "trans.stream.realigned" : "trans.stream");
     return GEMM_OK;
   }
@@ -144,7 +143,6 @@ int transposed(const uint16_t* A, const uint16_t* B, void* C, bool f32, bool ta,
   q.beta = beta;
   q.trans_a = ta;
   q.trans_b = tb;
-  q.follows = follows;
   return gemm_f16_pair(q, stream);
 }
 
@@ -180,8 +178,8 @@ int trans_entry(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, 
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   }
-  return transposed(A, B, C, f32, trans_a != 0, trans_b != 0, M, N, K, lda, ldb, ldc, alpha, beta, false,
-                    d, stream);
+  return transposed(A, B, C, f32, trans_a != 0, trans_b != 0, M, N, K, lda, ldb, ldc, alpha, beta, d,
+                    stream);
 }
 
 }  // namespace
@@ -258,11 +256,11 @@ int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, 
     return rc;
   if (want_dx)
     if (int rc = transposed(dGU, W, dX, false, false, true, M, K, 2 * N, lddgu, ldw, lddx, 1.0f,
-                            0.0f, true, d, stream))
+                            0.0f, d, stream))
       return rc;
   if (want_dw)
     if (int rc = transposed(X, dGU, dW, false, true, false, K, 2 * N, M, ldx, lddgu, lddw, 1.0f,
-                            beta, true, d, stream))
+                            beta, d, stream))
       return rc;
   return GEMM_OK;
 }

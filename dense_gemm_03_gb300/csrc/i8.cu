@@ -68,6 +68,7 @@ __device__ __forceinline__ uint4 load16(const int8_t* p, int n) {
 template <bool HALVES>
 __global__ void __launch_bounds__(kThreads) spread_i8_kernel(const SpreadBatch b) {
   griddep_launch_dependents();
+  griddep_wait();
   int i = 0;
   while (i + 1 < b.n && static_cast<int>(blockIdx.x) >= b.end[i]) ++i;
   const int first = i ? b.end[i - 1] : 0;
@@ -95,11 +96,8 @@ int spread(SpreadBatch& b, bool halves, int sms, cudaStream_t stream) {
     blocks += static_cast<int>(std::max(1ll, std::min<long long>(want, 16ll * sms)));
     b.end[i] = blocks;
   }
-  if (halves)
-    spread_i8_kernel<true><<<blocks, kThreads, 0, stream>>>(b);
-  else
-    spread_i8_kernel<false><<<blocks, kThreads, 0, stream>>>(b);
-  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  return counted_launch(launch_early(halves ? spread_i8_kernel<true> : spread_i8_kernel<false>,
+                                     blocks, kThreads, 0, stream, b)) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 // ------------------------------------------------------------ tokens to bytes
@@ -166,6 +164,8 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T)
                  int M, int K, long long ldx, long long ldq) {
   constexpr int kRowsPerBlock = T < 256 ? 256 / T : 1;
   __shared__ uint32_t top[32];
+  griddep_launch_dependents();
+  griddep_wait();
   const int t = static_cast<int>(threadIdx.x) % T;
   const int row = blockIdx.x * kRowsPerBlock + static_cast<int>(threadIdx.x) / T;
   const bool there = row < M;   // (uniform over a warp)
@@ -269,6 +269,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     fence_proxy_async_smem();
   }
   __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
   // row number i of this block, in stage i % stages
   auto row_of = [&](long long i) { return blockIdx.x + i * gridDim.x; };
   auto fetch = [&](long long i, int s) {
@@ -347,9 +349,12 @@ int launch_ring(const uint16_t* X, int8_t* Q, float* scales, int M, int K, int l
     configured[dev] = true;
   }
   const int stages = std::min(kRingStages, kRingBytes / (2 * K)) / kGroups * kGroups;
-  to_i8_ring_kernel<T, V><<<d.sms, kRingThreads, static_cast<size_t>(stages) * 2 * K, stream>>>(
-      X, Q, scales, M, K, ldx, ldq, stages, d.wait_limit_ns, d.status);
-  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  return counted_launch(launch_early(to_i8_ring_kernel<T, V>, d.sms, kRingThreads,
+                                     static_cast<size_t>(stages) * 2 * K, stream, X, Q, scales, M, K,
+                                     static_cast<long long>(ldx), static_cast<long long>(ldq), stages,
+                                     d.wait_limit_ns, d.status)) == cudaSuccess
+             ? GEMM_OK
+             : GEMM_ERR_CUDA;
 }
 
 __global__ void __launch_bounds__(kThreads) zero_floats_kernel(float* p, int n) {
@@ -426,10 +431,10 @@ int streamed(const I8Args& p, const GateArgs& g, const LoraDevice& d, cudaStream
   if (b.n)
     if (int rc = spread(b, false, d.sms, stream)) return rc;
   if (cluster) {
-    if (int rc = i8_cluster(r, s, d, b.n > 0, stream)) return rc;
+    if (int rc = i8_cluster(r, s, d, stream)) return rc;
   } else {
     s.parts.part = reinterpret_cast<float*>(at);
-    if (int rc = i8_partial(r, p.M, p.cols(), s.parts, d, b.n > 0, stream)) return rc;
+    if (int rc = i8_partial(r, p.M, p.cols(), s.parts, d, stream)) return rc;
     if (int rc = stream_sum(s, d, stream)) return rc;
   }
   set_last_path(b.n ? "i8.stream.realigned" : "i8.stream");
@@ -472,7 +477,6 @@ int tiled(const I8Args& p, GateArgs g, const LoraDevice& d, cudaStream_t stream)
   q.scaled = true;
   q.g = g;
   q.g.up = apart ? n16 : p.N;
-  q.follows = true;
   return gemm_f16_pair(q, stream);
 }
 
@@ -549,8 +553,10 @@ int gemm_f16_to_i8(const uint16_t* X, int8_t* Q, float* scales, int M, int K, in
   // groups of a row: at most, when Q's rows leave its 8-byte grid
   const bool grid8 = (reinterpret_cast<uintptr_t>(Q) & 7u) == 0 && ldq % 8 == 0;
   const int groups = grid8 ? (K - 1) / 8 + 1 : K / 8 + 2;
+  cudaError_t e = cudaSuccess;
   auto launch = [&](auto kernel, int threads, int rows) {
-    kernel<<<(M - 1) / rows + 1, threads, 0, stream>>>(X, Q, scales, M, K, ldx, ldq);
+    e = launch_early(kernel, (M - 1) / rows + 1, threads, 0, stream, X, Q, scales, M, K,
+                     static_cast<long long>(ldx), static_cast<long long>(ldq));
   };
   if (groups <= 32)
     launch(to_i8_kernel<32, 1>, 256, 8);
@@ -568,7 +574,7 @@ int gemm_f16_to_i8(const uint16_t* X, int8_t* Q, float* scales, int M, int K, in
     launch(to_i8_kernel<1024, 4>, 1024, 1);
   else
     launch(to_i8_kernel<1024, 0>, 1024, 1);
-  return counted_launch(cudaGetLastError()) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+  return counted_launch(e) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -310,7 +310,7 @@ void lay_out(Args& a, int steps, bool cluster) {
 }
 
 template <int FIN>
-int launch(const Args& a, const NarrowStream& p, const StreamSum& fin, int grid, bool early,
+int launch(const Args& a, const NarrowStream& p, const StreamSum& fin, int grid,
            cudaStream_t stream) {
   CUtensorMap tmW{}, tmX{};
   if (int rc = paired<FIN>()
@@ -321,7 +321,7 @@ int launch(const Args& a, const NarrowStream& p, const StreamSum& fin, int grid,
     return rc;
   static bool configured[64] = {};
   return launch_narrow(i8_stream_kernel<FIN>, kThreads, static_cast<size_t>(a.bar_off) + 2048, grid,
-                       FIN == kPartial ? 0 : a.chunks, early, configured, stream, tmW, tmX, a, fin);
+                       FIN == kPartial ? 0 : a.chunks, configured, stream, tmW, tmX, a, fin);
 }
 
 Args plan_partial(const NarrowStream& p, int M, int cols, const LoraDevice& d) {
@@ -340,10 +340,10 @@ StreamParts i8_parts(const NarrowStream& p, int M, int cols, const LoraDevice& d
 }
 
 int i8_partial(const NarrowStream& p, int M, int cols, const StreamParts& parts,
-               const LoraDevice& d, bool early, cudaStream_t stream) {
+               const LoraDevice& d, cudaStream_t stream) {
   Args a = plan_partial(p, M, cols, d);
   a.part = parts.part;
-  return launch<kPartial>(a, p, StreamSum{}, std::min(a.items, d.sms), early, stream);
+  return launch<kPartial>(a, p, StreamSum{}, std::min(a.items, d.sms), stream);
 }
 
 bool i8_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
@@ -351,14 +351,14 @@ bool i8_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
   return (!s.gate || s.N % 16 == 0) && cluster_pays(cluster_tiles(s, K, kBlockRows, d), d.sms);
 }
 
-int i8_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,
+int i8_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,
                cudaStream_t stream) {
   Args a{};
   static_cast<Tiles&>(a) = cluster_tiles(s, p.K, kBlockRows, d);
   if (a.chunks == 0) return GEMM_ERR_ARG;
   lay_out(a, (a.kb + a.chunks - 1) / a.chunks, true);
-  return s.gate ? launch<kScaledGate>(a, p, s, a.items, early, stream)
-                : launch<kScaled>(a, p, s, a.items, early, stream);
+  return s.gate ? launch<kScaledGate>(a, p, s, a.items, stream)
+                : launch<kScaled>(a, p, s, a.items, stream);
 }
 
 }  // namespace gb300

@@ -228,8 +228,8 @@ inline Tiles cluster_tiles(const StreamSum& s, int K, int rows, const LoraDevice
 // shared memory, and no other CTA that uses tensor memory (which all use shared memory)
 // is there beside them.
 template <class K, class... A>
-int launch_narrow(K kernel, int threads, size_t smem, int grid, int chunks, bool early,
-                  bool* configured, cudaStream_t stream, const A&... args) {
+int launch_narrow(K kernel, int threads, size_t smem, int grid, int chunks, bool* configured,
+                  cudaStream_t stream, const A&... args) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return GEMM_ERR_CUDA;
   if (dev < 64 && !configured[dev]) {
@@ -247,11 +247,9 @@ int launch_narrow(K kernel, int threads, size_t smem, int grid, int chunks, bool
     attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (early) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // see launch_early
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);

@@ -262,10 +262,10 @@ void lay_out(Args& a, const NarrowStream& p, int steps, bool cluster) {
 
 template <int FIN>
 int launch(const Args& a, const StreamSum& fin, const CUtensorMap& tmW, const CUtensorMap& tmX,
-           int grid, bool early, cudaStream_t stream) {
+           int grid, cudaStream_t stream) {
   static bool configured[64] = {};
   return launch_narrow(narrow_stream_kernel<FIN>, kThreads, static_cast<size_t>(a.bar_off) + 2048,
-                       grid, FIN == kPartial ? 0 : a.chunks, early, configured, stream, tmW, tmX, a,
+                       grid, FIN == kPartial ? 0 : a.chunks, configured, stream, tmW, tmX, a,
                        fin);
 }
 
@@ -325,12 +325,12 @@ StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, cons
 }
 
 int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const StreamParts& parts,
-                   const LoraDevice& d, bool early, cudaStream_t stream) {
+                   const LoraDevice& d, cudaStream_t stream) {
   Args a = plan_partial(p, M, cols, fold, d);
   a.part = parts.part;
   CUtensorMap tmW{}, tmX{};
   if (int rc = make_maps(a, p, false, 0, &tmW, &tmX)) return rc;
-  return launch<kPartial>(a, StreamSum{}, tmW, tmX, std::min(a.items, d.sms), early, stream);
+  return launch<kPartial>(a, StreamSum{}, tmW, tmX, std::min(a.items, d.sms), stream);
 }
 
 bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
@@ -339,7 +339,7 @@ bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
   return cluster_pays(a, d.sms) && (!s.f32 || longest_chunk(K, a.chunks) <= kFoldDepth);
 }
 
-int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,
+int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,
                    cudaStream_t stream) {
   Args a{};
   static_cast<Tiles&>(a) = cluster_tiles(s, p.K, kBlockRows, d);
@@ -347,10 +347,10 @@ int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& 
   lay_out(a, p, (a.kb + a.chunks - 1) / a.chunks, true);
   CUtensorMap tmW{}, tmX{};
   if (int rc = make_maps(a, p, s.gate != 0, s.N, &tmW, &tmX)) return rc;
-  return s.gate == 2 ? launch<kGateGrad>(a, s, tmW, tmX, a.items, early, stream)
-         : s.gate    ? launch<kGate>(a, s, tmW, tmX, a.items, early, stream)
-         : s.f32     ? launch<kFloat>(a, s, tmW, tmX, a.items, early, stream)
-                     : launch<kHalf>(a, s, tmW, tmX, a.items, early, stream);
+  return s.gate == 2 ? launch<kGateGrad>(a, s, tmW, tmX, a.items, stream)
+         : s.gate    ? launch<kGate>(a, s, tmW, tmX, a.items, stream)
+         : s.f32     ? launch<kFloat>(a, s, tmW, tmX, a.items, stream)
+                     : launch<kHalf>(a, s, tmW, tmX, a.items, stream);
 }
 
 }  // namespace gb300

@@ -45,10 +45,12 @@ struct Operand {
   int* ld;
 };
 
-inline int align_operands(std::initializer_list<Operand> ops, uint8_t* buf, int sms, cudaStream_t stream) {
+inline int align_operands(std::initializer_list<Operand> ops, uint8_t* buf, int sms, cudaStream_t stream,
+                          bool early = false) {
   RealignBatch batch{};
   auto flush = [&]() {
     if (batch.n == 0) return GEMM_OK;
+    batch.early = early;
     const cudaError_t e = launch_realign_f16(batch, stream);
     batch = RealignBatch{};
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;

@@ -36,10 +36,10 @@ struct NarrowStream {
 // Its partial sums; fold: of a float result.
 StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, const LoraDevice& d);
 int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const StreamParts& parts,
-                   const LoraDevice& d, bool early, cudaStream_t stream);
+                   const LoraDevice& d, cudaStream_t stream);
 StreamParts i8_parts(const NarrowStream& p, int M, int cols, const LoraDevice& d);
 int i8_partial(const NarrowStream& p, int M, int cols, const StreamParts& parts,
-               const LoraDevice& d, bool early, cudaStream_t stream);
+               const LoraDevice& d, cudaStream_t stream);
 
 // What becomes of the sums S (gate 0: N columns; else 2 N, G and U):
 //   gate 0   C := alpha S + beta C (half, or float when f32); with scales S
@@ -59,10 +59,10 @@ struct StreamSum {
 // The whole product in one launch, finished as `s` says (its parts unused), where one
 // wave of clusters covers it.
 bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d);
-int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,
+int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,
                    cudaStream_t stream);
 bool i8_cluster_suits(const StreamSum& s, int K, const LoraDevice& d);
-int i8_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d, bool early,
+int i8_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,
                cudaStream_t stream);
 int stream_sum(const StreamSum& s, const LoraDevice& d, cudaStream_t stream);
 

@@ -89,17 +89,9 @@ cudaError_t launch(const StreamSum& s, const LoraDevice& d, cudaStream_t stream)
     vec = vec && s.g.lddc % 4 == 0;
   }
   vec = vec && bits % elem == 0;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, stream_sum_kernel<GATE, F32, SCALED, 4>, s, vec)
-              : cudaLaunchKernelEx(&cfg, stream_sum_kernel<GATE, F32, SCALED, 1>, s, vec);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  return wide ? launch_early(stream_sum_kernel<GATE, F32, SCALED, 4>, grid, kThreads, 0, stream, s, vec)
+              : launch_early(stream_sum_kernel<GATE, F32, SCALED, 1>, grid, kThreads, 0, stream, s, vec);
 }
 
 }  // namespace

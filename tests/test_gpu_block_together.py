@@ -331,3 +331,111 @@ def test_example():
     f, df = ref.act_both("silu", g_)
     each = t.cat([dh_terms * u_.abs() * df.abs(), dh_terms * f.abs()], 1)
     assert bool(((dw1.double() - a.grad).abs() <= 2.02 * ref.HALF * (x.double().abs().t() @ each) + 1e-6).all())
+
+
+# ------------------------------------------- calls that start as others end
+def chain(t, seed, T, H, I):
+    """Calls that each read what the one before wrote, or write what it reads, between a
+    framework's own kernels, copies and fills."""
+    import dense_gemm_03_gb300 as g
+    rng = np.random.default_rng(seed)
+    x, dy = (normal(t, rng, (T, H), 1.0).cuda() for _ in "xd")
+    w = normal(t, rng, (H, 2 * I), H ** -0.5).cuda()
+    wd = normal(t, rng, (I, H), I ** -0.5).cuda()
+    q = t.zeros((T, H), dtype=t.int8, device="cuda")
+    wq = t.randint(-127, 128, (H, H), dtype=t.int8, device="cuda",
+                   generator=t.Generator(device="cuda").manual_seed(seed))
+    sq, sw = t.zeros(T, device="cuda"), t.full((H,), 1.0 / 73 / H ** 0.5, device="cuda")
+    new = lambda *s, dtype=t.float16: t.zeros(s, dtype=dtype, device="cuda")
+    h, y, z, dgu, dx = new(T, I), new(T, H), new(T, H), new(T, 2 * I), new(T, H)
+    dw, dh = new(H, 2 * I), new(T, I)
+    dwd = new(I, H, dtype=t.float32)
+    first = x.clone()
+    def steps():
+        yield lambda: x.copy_(first)
+        for turn in range(3):
+            yield lambda: g.gemm_f16_glu(x, w, h, "silu")
+            yield lambda: g.gemm_f16(h, wd, y)
+            yield lambda: g.f16_to_i8(y, q, sq)
+            yield lambda: g.gemm_i8(q, wq, z, sq, sw)
+            yield lambda: y.zero_()
+            yield lambda: g.gemm_f16_trans(z, wd, dh, False, True)
+            yield lambda: g.gemm_f16_trans_f32out(h, z, dwd, True, False, beta=0.5 if turn else 0.0)
+            yield lambda: h.mul_(0.5)
+            yield lambda: g.gemm_f16_glu_grad(dh, x, w, dgu, dx, dw, "gelu", beta=0.5 if turn else 0.0)
+            yield lambda: x.copy_(dx)
+            yield lambda: x.add_(first)
+            yield lambda: g.f16_to_i8(x, q, sq)
+            yield lambda: g.gemm_i8(q, wq, z, sq, sw)
+            yield lambda: x.add_(z)
+    return steps, [x, y, z, h, q, sq, dgu, dx, dw, dh, dwd]
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 256, 512), (24, 515, 1001), (300, 512, 1024), (700, 777, 1201)])
+def test_calls_in_a_row_wait_for_the_ones_before(T, H, I):
+    t = torch()
+    steps, outs = chain(t, 5, T, H, I)
+    for step in steps():     # one at a time
+        step()
+        t.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    # (values grow from turn to turn: entries of the last dW pass the half range)
+    assert not any(bool(t.isnan(o.float()).any()) for o in outs)
+    for stream in (t.cuda.current_stream(), t.cuda.Stream()):
+        with t.cuda.stream(stream):
+            for _ in range(20):
+                for step in steps():
+                    step()
+        sync(t)
+        assert all(t.equal(a, b) for a, b in zip(want, outs))
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph, stream=stream):
+        for step in steps():
+            step()
+    for _ in range(3):
+        graph.replay()
+    sync(t)
+    assert all(t.equal(a, b) for a, b in zip(want, outs))
+
+
+@pytest.mark.parametrize("big", [False, True])
+def test_a_captured_call_after_a_join(big):
+    """Calls captured first on a forked stream, and behind two streams at once."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    T, H, I = (600, 512, 1024) if big else (24, 512, 1024)
+    rng = np.random.default_rng(3)
+    x, w = normal(t, rng, (T, H), 1.0).cuda(), normal(t, rng, (H, 2 * I), H ** -0.5).cuda()
+    h, v = (t.zeros((T, I), dtype=t.float16, device="cuda") for _ in "hv")
+    dw = t.zeros((I, I), dtype=t.float32, device="cuda")
+    q, sq = t.zeros((T, I), dtype=t.int8, device="cuda"), t.zeros(T, device="cuda")
+    a, b = t.cuda.Stream(), t.cuda.Stream()
+
+    def run():
+        x2 = x * 0.5
+        b.wait_stream(a)
+        g.gemm_f16_glu(x, w, h, "silu", stream=a)
+        with t.cuda.stream(b):
+            g.gemm_f16_glu(x2, w, v, "gelu", stream=b)
+        a.wait_stream(b)
+        g.gemm_f16_trans_f32out(h, v, dw, True, False, stream=a)   # behind both
+        b.wait_stream(a)
+        with t.cuda.stream(b):
+            g.f16_to_i8(h, q, sq, stream=b)
+            g.f16_to_i8(v, q, sq, stream=b)
+        a.wait_stream(b)
+    with t.cuda.stream(a):
+        run()
+    sync(t)
+    want = [o.clone() for o in (h, v, dw, q, sq)]
+    ref.check(dw.cpu(), *ref.product(h.cpu().t(), v.cpu(), f32=True), "dW")
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph, stream=a):
+        run()
+    for _ in range(3):
+        for o in (h, v, dw, q, sq):
+            o.zero_()
+        t.cuda.synchronize()
+        graph.replay()
+        sync(t)
+        assert all(t.equal(p, r) for p, r in zip((h, v, dw, q, sq), want))
