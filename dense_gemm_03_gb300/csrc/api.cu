@@ -1431,8 +1431,9 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   a.status = d->status;
   const long long tiles = 1ll * a.tiles_m * a.tiles_n;
   if (tiles * 4 > 0x7fffffffll) return GEMM_ERR_ARG;
-  const long long slots = tc_pair_max_clusters(epi);
+  long long slots = tc_pair_max_clusters(epi);
   if (slots <= 0) return GEMM_ERR_CUDA;
+  if (q.pairs > 0) slots = std::min<long long>(slots, q.pairs);
   a.dp_tiles = static_cast<int>(tiles);
   a.tail_splits = 1;
   a.tail_kb_per_split = a.kb_total;
@@ -1440,7 +1441,9 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   const char* cut = "";
   const long long rem = tiles % slots;
   const int first_kb = tail_first_slice(tiles, slots, a.kb_total);
+  bool parts = false;
   if (first_kb > 0) {
+    parts = true;
     a.dp_tiles = static_cast<int>(tiles - rem);
     a.tail_splits = 2;
     a.tail_kb_per_split = first_kb;
@@ -1455,7 +1458,7 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
     a.epoch = ++w->epoch;
     if (a.epoch == 0) a.epoch = ++w->epoch;   // 0 marks never-used counters
     cut = ".ktail";
-  } else if (rem > 0 && 2 * rem <= slots) {
+  } else if (!q.whole && rem > 0 && 2 * rem <= slots) {
     a.dp_tiles = static_cast<int>(tiles - rem);
     a.tail_splits = 2;
     a.tail_halves = 1;
@@ -1474,6 +1477,9 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   } else if (epi == kEpiF32Tma) {
     if (int rc = make_map_f32(&tmC, a.Cf, M, N, ldc, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
   }
+  a.beside = q.before && q.before->pair && a_bytes + b_bytes + c_bytes == 0 &&
+             !(parts && q.before->parts);
+  if (q.done) *q.done = PairDone{!c_user, parts};
   a.set_divisors();
   const int grid = 2 * static_cast<int>(std::min<long long>(a.num_units, workers));
   snprintf(t_path_buf, sizeof(t_path_buf), "f16.tc.pair.%s%s%s%s%s%s%s%s",

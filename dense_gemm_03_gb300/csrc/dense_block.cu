@@ -32,7 +32,7 @@ int blank(uint16_t* C, long long ldc, int M, int N, float beta, const LoraDevice
 // The streamed form: op(X) op(W) with `cols` columns, then the sum `s` (its parts are
 // filled in here).
 int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ldw, bool trans_w,
-             int M, int cols, int K, StreamSum s, const LoraDevice& d,
+             int M, int cols, int K, StreamSum s, const PairDone* before, const LoraDevice& d,
              cudaStream_t stream, bool* copied) {
   Aligned x(X, ldx, trans_x ? K : M, trans_x ? M : K, true);
   Aligned w(W, ldw, trans_w ? cols : K, trans_w ? K : cols, true);
@@ -47,7 +47,7 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
                               stream, true))
     return rc;
   *copied = copies != 0;
-  p = NarrowStream{X, W, ldx, ldw, K, trans_x, trans_w};
+  p = NarrowStream{X, W, ldx, ldw, K, trans_x, trans_w, before && before->pair && !*copied};
   if (cluster) return narrow_cluster(p, s, d, stream);
   s.parts.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + copies);
   if (int rc = narrow_partial(p, M, cols, s.f32, s.parts, d, stream)) return rc;
@@ -88,8 +88,8 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
     s.gate = gate;
     s.g = g;
     bool copied = false;
-    if (int rc = streamed(p.X, p.ldx, false, p.W, p.ldw, false, p.M, 2 * p.N, p.K, s, d, stream,
-                          &copied))
+    if (int rc = streamed(p.X, p.ldx, false, p.W, p.ldw, false, p.M, 2 * p.N, p.K, s, nullptr, d,
+                          stream, &copied))
       return rc;
     set_last_path(copied ? "glu.stream.realigned" : "glu.stream");
     return GEMM_OK;
@@ -111,39 +111,89 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
 }
 
 // C := alpha op(A) op(B) + beta C, checked, with M, N, K > 0 and alpha != 0.
-int transposed(const uint16_t* A, const uint16_t* B, void* C, bool f32, bool ta, bool tb, int M,
-               int N, int K, int lda, int ldb, int ldc, float alpha, float beta,
+struct Trans {
+  const uint16_t *A, *B;
+  void* C;
+  bool f32, ta, tb;
+  int M, N, K, lda, ldb, ldc;
+  float alpha, beta;
+  bool tiled(int sms) const { return !narrow_suits(M, N, K, sms); }
+  bool on_grid() const {   // no copies of the operands
+    return !misaligned({A, B}, 16) && lda % 8 == 0 && ldb % 8 == 0;
+  }
+  bool c_on_grid() const { return f32 || (!misaligned({C}, 16) && ldc % 8 == 0 && N % 8 == 0); }
+  long long tiles() const { return 1ll * ((M + 255) / 256) * ((N + 255) / 256); }
+};
+
+// whole, most_pairs, before, done: see PairCall.
+int transposed(const Trans& p, bool whole, int most_pairs, const PairDone* before, PairDone* done,
                const LoraDevice& d, cudaStream_t stream) {
-  if (narrow_suits(M, N, K, d.sms)) {
+  if (!p.tiled(d.sms)) {
     StreamSum s{};
-    s.C = C;
-    s.ldc = ldc;
-    s.M = M;
-    s.N = N;
-    s.alpha = alpha;
-    s.beta = beta;
-    s.f32 = f32;
+    s.C = p.C;
+    s.ldc = p.ldc;
+    s.M = p.M;
+    s.N = p.N;
+    s.alpha = p.alpha;
+    s.beta = p.beta;
+    s.f32 = p.f32;
     bool copied = false;
-    if (int rc = streamed(A, lda, ta, B, ldb, tb, M, N, K, s, d, stream, &copied)) return rc;
+    if (int rc = streamed(p.A, p.lda, p.ta, p.B, p.ldb, p.tb, p.M, p.N, p.K, s, before, d, stream,
+                          &copied))
+      return rc;
     set_last_path(copied ? "trans.stream.realigned" : "trans.stream");
     return GEMM_OK;
   }
   PairCall q{};
-  q.A = A;
-  q.B = B;
-  q.C = C;
-  q.c_f32 = f32;
-  q.M = M;
-  q.N = N;
-  q.K = K;
-  q.lda = lda;
-  q.ldb = ldb;
-  q.ldc = ldc;
-  q.alpha = alpha;
-  q.beta = beta;
-  q.trans_a = ta;
-  q.trans_b = tb;
+  q.A = p.A;
+  q.B = p.B;
+  q.C = p.C;
+  q.c_f32 = p.f32;
+  q.M = p.M;
+  q.N = p.N;
+  q.K = p.K;
+  q.lda = p.lda;
+  q.ldb = p.ldb;
+  q.ldc = p.ldc;
+  q.alpha = p.alpha;
+  q.beta = p.beta;
+  q.trans_a = p.ta;
+  q.trans_b = p.tb;
+  q.whole = whole;
+  q.pairs = most_pairs;
+  q.before = before;
+  q.done = done;
   return gemm_f16_pair(q, stream);
+}
+
+// Two products of one call's operands.  Side by side (see PairDone) where one leaves
+// enough SMs idle: whole tiles of that, the other on the SMs left, in as many rounds as it
+// takes; k-blocks of the longer way are weighed against one after the other over all SMs, a
+// kernel's start and end counting as 12.  Gradients of 1500 x 1000 x 2*1368, 24 tiles of 43
+// k-blocks and 44 of 24: 61.5 us one after the other, 47 side by side; 4096 x 1024 x 2*1024, 32
+// of 64 and 64 of 32: 80 and 61; 300 x 1000 x 2*1368, 44 of 5 and a streamed product: 37.5
+// and 33.7.  Else the second starts as the first's last blocks end.
+int both(const Trans& a, const Trans& b, const LoraDevice& d, cudaStream_t stream) {
+  const bool ta = a.tiled(d.sms), tb = b.tiled(d.sms);
+  // tiles before a streamed product, longer tiles before shorter ones
+  const bool swap = ta != tb ? tb : b.K > a.K;
+  const Trans &x = swap ? b : a, &y = swap ? a : b;
+  const long long pairs = d.sms / 2, left = pairs - x.tiles();
+  bool beside = (ta || tb) && left > 0 && x.c_on_grid() && y.on_grid() && y.c_on_grid();
+  if (beside && ta && tb) {
+    auto way = [](const Trans& t, long long on) {
+      return static_cast<double>((t.tiles() + on - 1) / on) * ((t.K + 63) / 64);
+    };
+    auto alone = [&](const Trans& t) { return way(t, pairs) * (2 * t.tiles() <= pairs ? 0.75 : 1.0); };
+    beside = std::max(way(x, pairs), way(y, left)) < alone(x) + alone(y) + 12;
+  }
+  PairDone done{};
+  if (!beside) {
+    if (int rc = transposed(a, false, 0, nullptr, &done, d, stream)) return rc;
+    return transposed(b, false, 0, &done, nullptr, d, stream);
+  }
+  if (int rc = transposed(x, true, 0, nullptr, &done, d, stream)) return rc;
+  return transposed(y, false, static_cast<int>(left), &done, nullptr, d, stream);
 }
 
 int device(LoraDevice* d) { return query_device(&d->sms, &d->status, &d->wait_limit_ns); }
@@ -178,8 +228,8 @@ int trans_entry(int trans_a, int trans_b, const uint16_t* A, const uint16_t* B, 
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   }
-  return transposed(A, B, C, f32, trans_a != 0, trans_b != 0, M, N, K, lda, ldb, ldc, alpha, beta, d,
-                    stream);
+  return transposed(Trans{A, B, C, f32, trans_a != 0, trans_b != 0, M, N, K, lda, ldb, ldc, alpha, beta},
+                    false, 0, nullptr, nullptr, d, stream);
 }
 
 }  // namespace
@@ -254,15 +304,11 @@ int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, 
   }
   if (int rc = gated(GluArgs{X, W, M, N, K, ldx, ldw, act}, 2, dGU, lddgu, dC, lddc, d, stream))
     return rc;
-  if (want_dx)
-    if (int rc = transposed(dGU, W, dX, false, false, true, M, K, 2 * N, lddgu, ldw, lddx, 1.0f,
-                            0.0f, d, stream))
-      return rc;
-  if (want_dw)
-    if (int rc = transposed(X, dGU, dW, false, true, false, K, 2 * N, M, ldx, lddgu, lddw, 1.0f,
-                            beta, d, stream))
-      return rc;
-  return GEMM_OK;
+  const Trans dx{dGU, W, dX, false, false, true, M, K, 2 * N, lddgu, ldw, lddx, 1.0f, 0.0f};
+  const Trans dw{X, dGU, dW, false, true, false, K, 2 * N, M, ldx, lddgu, lddw, 1.0f, beta};
+  if (!want_dx && !want_dw) return GEMM_OK;
+  if (!want_dx || !want_dw) return transposed(want_dx ? dx : dw, false, 0, nullptr, nullptr, d, stream);
+  return both(dx, dw, d, stream);
 }
 
 }  // extern "C"

@@ -9,9 +9,10 @@
 //   gelu_tanh  f = g s,             s = 1 / (1 + e^-2z) = (1 + tanh z) / 2,
 //              z = sqrt(2/pi) (g + 0.044715 g^3);           f' = s + 2 g z' s (1 - s)
 //   relu       f = max(g, 0);                                f' = 1 for g > 0, else 0
-// All forms are exact in the tails (no difference of near-equal numbers): a
-// large negative g makes e^-g infinite and s zero.  1 - s is taken as e^-g s, which
-// keeps its bits where s is near 1.  A NaN stays a NaN.
+// f is exact in the tails (no difference of near-equal numbers): a large negative g
+// makes e^-g infinite and s zero.  In f' 1 - s is off by 2^-25 where s is near 1, times |g| < 17 (it
+// is zero past that) beside an f' of about 1.  A NaN stays a NaN.  Results below 2^-126 may be
+// zero on the way: s, e^-x and 1 / x are one instruction each then.
 #pragma once
 #include <type_traits>
 
@@ -19,12 +20,21 @@
 
 namespace gb300 {
 
-// s = 1 / (1 + e^-x) and 1 - s.  e^-x past the largest float: s = 0 and 1 - s = 1.
-__device__ __forceinline__ float gate_logistic(float x, float& rest) {
-  const float e = __expf(-x);
-  const float s = __fdividef(1.0f, 1.0f + e);   // 0 past 2^126
-  rest = e < 0x1p60f ? e * s : 1.0f;
-  return s;
+// e^-x = 2^(-x / ln 2) and 1 / x, with relative errors of about 2^-22 (1 + |x| / 4) and 2^-23.
+__device__ __forceinline__ float gate_exp_neg(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  return e;
+}
+__device__ __forceinline__ float gate_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// s = 1 / (1 + e^-x); 0 where e^-x passes 2^126.
+__device__ __forceinline__ float gate_logistic(float x) {
+  return gate_inverse(1.0f + gate_exp_neg(x));
 }
 
 constexpr float kGeluC = 0.7978845608028654f;    // sqrt(2 / pi)
@@ -34,14 +44,13 @@ constexpr float kGeluA = 0.044715f;
 template <int ACT>
 __device__ __forceinline__ float gate_both(float g, float& d) {
   if (ACT == GEMM_ACT_SILU) {
-    float rest;
-    const float s = gate_logistic(g, rest);
-    d = s * fmaf(g, rest, 1.0f);
+    const float s = gate_logistic(g);
+    d = s * fmaf(g, 1.0f - s, 1.0f);
     return g * s;
   }
   if (ACT == GEMM_ACT_GELU) {
     const float x = 0.7071067811865476f * fabsf(g);
-    const float e = __expf(-x * x), t = __fdividef(1.0f, fmaf(0.44f, x, 1.0f));
+    const float e = gate_exp_neg(x * x), t = gate_inverse(fmaf(0.44f, x, 1.0f));
     float q = 0.07122123653597495f;
     q = fmaf(q, t, -0.2779385877587885f);
     q = fmaf(q, t, 0.2966708364139223f);
@@ -57,11 +66,10 @@ __device__ __forceinline__ float gate_both(float g, float& d) {
   }
   if (ACT == GEMM_ACT_GELU_TANH) {
     const float g2 = g * g;
-    float rest;
-    const float s = gate_logistic(2.0f * kGeluC * g * fmaf(kGeluA, g2, 1.0f), rest);
+    const float s = gate_logistic(2.0f * kGeluC * g * fmaf(kGeluA, g2, 1.0f));
     const float dz = 2.0f * kGeluC * fmaf(3.0f * kGeluA, g2, 1.0f);
     // past any use of the product dz could overflow: s or 1 - s is zero there
-    d = fabsf(g) > 16.0f ? s : fmaf(g * dz, s * rest, s);
+    d = fabsf(g) > 16.0f ? s : fmaf(g * dz, s * (1.0f - s), s);
     return g * s;
   }
   d = g > 0.0f || g != g ? 1.0f : 0.0f;

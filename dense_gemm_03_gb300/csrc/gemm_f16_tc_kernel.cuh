@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   // before this kernel has completed
   // (with adapters only their own warps and the epilogue read or overwrite what
   // the kernels before this one touch, unless the operands are copies)
-  if (!LORA::kOn || p.wait_operands || warp >= R::kEpiWarp0) griddep_wait();
+  if (LORA::kOn ? p.wait_operands || warp >= R::kEpiWarp0 : !p.beside) griddep_wait();
   // a copy-back kernel launched after this one may be scheduled now (it waits
   // for this kernel's completion before reading anything this kernel writes)
   griddep_launch_dependents();
@@ -999,6 +999,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
     else
       tmem_dealloc(tmem_base, Cfg::kTmemCols);
+    // (the last block does, so that the grid ends no sooner)
+    if (!LORA::kOn && p.beside && blockIdx.x + 1 == gridDim.x) griddep_wait();
   } else if (LORA::kOn && warp >= R::kWarps) {
     // ------------------------------------------------------------ adapters' V tiles
     // The first of these warps hands the usable entries of each tile's list, and
@@ -1374,7 +1376,11 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       if constexpr (LORA::kScaled)
         sx_row = x.a.sx && finish && row < p.M ? __ldg(x.a.sx + row) : 1.0f;
       if constexpr (kGate == 2) {
-        if (EPI == kEpiTma && finish) load_dc(row, colw, dc_next);
+        if (EPI == kEpiTma && finish) {
+          load_dc(row, colw, dc_next);
+          if (nsub > 1 && row < p.M && colw + kSubCols < p.N)
+            prefetch_l2(x.a.dC + static_cast<long long>(row) * x.a.lddc + colw + kSubCols);
+        }
       }
       // kFold: this row's sums, every part of the accumulator added as it comes
       [[maybe_unused]] float sum[LORA::kFold ? kSubs * kSubCols : 1];

@@ -118,6 +118,8 @@ struct TcArgs {
   int stream_a, stream_b;
   // adapters: A, B or C was copied by the kernel launched just before
   int wait_operands;
+  // started beside the kernel before it, on operands that one waited for: waits at its end
+  int beside;
   unsigned long long wait_limit_ns;
   DeviceStatus* status;
   // host only: may start early (programmatic dependent launch: the kernel waits for
@@ -186,6 +188,17 @@ cudaError_t launch_gemm_f16_tc_gate(int gate, bool scaled, int epi_mode, const C
 // `gate` B is K x (up + N) and C the gated result (gate 1), or dG with dU beside it
 // (gate 2).  C is float when c_f32.  Rows of A and B, and of a half C, that are off
 // the 16-byte grid are copied.  Returns a GEMM_* code.
+//
+// Two products of one call whose operands the kernel before both wrote can run side
+// by side: the second names what the first left behind (`before`).  A pair kernel lets the kernel
+// after it start only when it has itself waited for the one before, so what it reads is
+// there for the second too, which waits for the first only as it ends (the order on the
+// stream then holds for all that follows).  The second must not need a copy of an operand,
+// which another kernel would make, nor scratch that the first uses.
+struct PairDone {
+  bool pair;       // the last kernel is a pair kernel
+  bool parts;      // that keeps partial sums in scratch
+};
 struct PairCall {
   const uint16_t *A, *B;
   void* C;
@@ -197,6 +210,10 @@ struct PairCall {
   int gate;
   bool scaled;
   GateArgs g;
+  bool whole;              // no half-width tiles: they would take SMs of a product beside
+  int pairs;               // of SMs at most (0: all)
+  const PairDone* before;  // see above; or NULL
+  PairDone* done;          // or NULL
 };
 int gemm_f16_pair(const PairCall& call, cudaStream_t stream);
 

@@ -30,6 +30,7 @@ struct Tiles {
   int rows;                     // rows of a block (at most)
   int n_cols, acc_cols;         // columns of the accumulator
   bool reread;                  // several blocks of rows read W
+  bool beside;                  // waits for the kernel before it at the end
   bool vec;                     // results' rows (and dC's) on the grid of four elements
   float* part;
   unsigned long long wait_limit_ns;

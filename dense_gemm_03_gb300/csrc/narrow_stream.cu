@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     fence_proxy_async_smem();
     __syncwarp();
-    griddep_wait();   // copies onto the 16-byte grid, if any
+    if (!p.beside) griddep_wait();   // copies onto the 16-byte grid, if any
     // the first item's first steps: their stages are empty
     if (lane == 0) {
       const int it = blockIdx.x, n = min(S, p.steps(it));
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp > 0) griddep_wait();   // (what the results are joined with)
+  if (warp > 0 && !p.beside) griddep_wait();   // (what the results are joined with)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_ptr);
 
   if (warp == 0) {
@@ -248,11 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, p.acc_cols);
+  if (p.beside && blockIdx.x + 1 == gridDim.x) griddep_wait();   // the grid ends no sooner
 }
 
 // Stages and the place of the barriers, for `steps` steps a CTA at most.
 void lay_out(Args& a, const NarrowStream& p, int steps, bool cluster) {
   a.trans_w = p.trans_w;
+  a.beside = p.beside;
   a.trans_x = p.trans_x;
   a.x_bytes = a.trans_x ? (a.n_cols + 63) / 64 * 16384 : a.n_cols * 256;
   a.stage_bytes = kWBytes + a.x_bytes;

@@ -32,6 +32,7 @@ struct NarrowStream {
   long long ldx, ldw;
   int K;
   bool trans_x, trans_w;
+  bool beside = false;   // see PairDone (internal.h)
 };
 // Its partial sums; fold: of a float result.
 StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, const LoraDevice& d);

@@ -371,7 +371,8 @@ def chain(t, seed, T, H, I):
     return steps, [x, y, z, h, q, sq, dgu, dx, dw, dh, dwd]
 
 
-@pytest.mark.parametrize("T,H,I", [(1, 256, 512), (24, 515, 1001), (300, 512, 1024), (700, 777, 1201)])
+@pytest.mark.parametrize("T,H,I", [(1, 256, 512), (24, 515, 1001), (300, 512, 1024), (700, 777, 1201),
+                                   (2048, 768, 1024)])
 def test_calls_in_a_row_wait_for_the_ones_before(T, H, I):
     t = torch()
     steps, outs = chain(t, 5, T, H, I)
