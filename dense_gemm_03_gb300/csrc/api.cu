@@ -937,8 +937,11 @@ int gemm_f16_impl(const uint16_t* A, const uint16_t* B, void* C, bool c_f32, int
   // which goes back to the caller's C last
   auto copy_back = [&]() -> int {
     if (!c_user) return GEMM_OK;
-    const RealignJob j{a.C, ldc, c_user, ldc_user, M, N};
-    return launch_unalign_f16(j, scale_grid(*d, 1ll * M * (N / 8 + 2)), stream) == cudaSuccess
+    RealignBatch j{};
+    j.job[0] = RealignJob{a.C, ldc, c_user, ldc_user, M, N};
+    j.end[0] = scale_grid(*d, 1ll * M * (N / 8 + 2));
+    j.n = 1;
+    return launch_unalign_f16(j, stream) == cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_CUDA;
   };
@@ -1337,7 +1340,8 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   // predicated stores (777 x 1000 x 2*1501 20.6 -> 18.6 us, 4096 x 2048 x 2*4095 106 -> 98)
   const bool a_ok = aligned16(A) && lda % 8 == 0;
   const bool b_ok = aligned16(B) && ldb % 8 == 0 && (!q.gate || g.up % 8 == 0);
-  const bool c_ok = q.c_f32 || (aligned16(C) && ldc % 8 == 0 && N % 8 == 0);
+  // (a TMA store writes whole pieces of eight halves, past column N too)
+  const bool c_ok = q.c_f32 || (aligned16(C) && ldc % 8 == 0 && (N % 8 == 0 || q.c_padded));
   const bool dc_ok = q.gate != 2 || (aligned16(g.dC) && g.lddc % 8 == 0 && aligned16(g.dU));
   const bool copy_c = !c_ok && q.gate == 0;
   const long long lda2 = (a_cols + 7) / 8 * 8, n8 = (N + 7) / 8 * 8;
@@ -1495,8 +1499,11 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
           : launch_gemm_f16_tc_trans(q.trans_a, q.trans_b, epi, tmA, tmB, tmC, a, grid, stream);
   if (e != cudaSuccess) return GEMM_ERR_CUDA;
   if (!c_user) return GEMM_OK;
-  const RealignJob j{C, ldc, c_user, ldc_user, M, N};
-  return launch_unalign_f16(j, scale_grid(*d, 1ll * M * (N / 8 + 2)), stream) == cudaSuccess
+  RealignBatch j{};
+  j.job[0] = RealignJob{C, ldc, c_user, ldc_user, M, N};
+  j.end[0] = scale_grid(*d, 1ll * M * (N / 8 + 2));
+  j.n = 1;
+  return launch_unalign_f16(j, stream) == cudaSuccess
              ? GEMM_OK
              : GEMM_ERR_CUDA;
 }
@@ -1505,6 +1512,16 @@ int lock_stream(cudaStream_t stream, std::unique_lock<std::recursive_mutex>* cal
   DevState* d = nullptr;
   if (int rc = device_state(&d, nullptr)) return rc;
   *call = stream_call(d, stream);
+  return GEMM_OK;
+}
+
+int realigned_scratch(cudaStream_t stream, size_t bytes, void** out) {
+  DevState* d = nullptr;
+  if (int rc = device_state(&d, nullptr)) return rc;
+  std::lock_guard<std::mutex> lk(g_mu);
+  StreamWs& w = d->ws[stream_key(stream)];
+  if (int rc = ensure_buffer(d, &w.realigned, bytes, stream)) return rc;
+  *out = w.realigned.ptr;
   return GEMM_OK;
 }
 

@@ -137,7 +137,7 @@ __device__ __forceinline__ void realign_rows(const uint16_t* __restrict__ src, l
   }
 }
 
-// Up to three copies in one launch: blocks [end[i-1], end[i]) copy job i.
+// Several copies in one launch: blocks [end[i-1], end[i]) copy job i.
 __global__ void realign_f16_kernel(const RealignBatch b) {
   griddep_wait();
   int i = 0;
@@ -159,13 +159,12 @@ __global__ void realign_f16_kernel(const RealignBatch b) {
 // row that hold them, which lie within the row's lds, and shifted into
 // place), the pieces at the two ends of the row element by element (nothing
 // outside the row's columns is written).
-__global__ void unalign_f16_kernel(const uint16_t* __restrict__ src, long long lds,
-                                   uint16_t* __restrict__ dst, long long ldd, int rows, int cols) {
-  griddep_wait();   // the kernel that writes src may still be running
+__device__ __forceinline__ void unalign_rows(const uint16_t* __restrict__ src, long long lds,
+                                             uint16_t* __restrict__ dst, long long ldd, int rows,
+                                             int cols, long long block, long long nblocks) {
   const long long pieces = cols / 8 + 2;   // enough for any alignment of a row
   const long long total = static_cast<long long>(rows) * pieces;
-  for (long long g = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; g < total;
-       g += static_cast<long long>(gridDim.x) * blockDim.x) {
+  for (long long g = block * blockDim.x + threadIdx.x; g < total; g += nblocks * blockDim.x) {
     const int r = static_cast<int>(g / pieces);
     const int j = static_cast<int>(g % pieces);
     uint16_t* const d = dst + static_cast<long long>(r) * ldd;
@@ -186,6 +185,15 @@ __global__ void unalign_f16_kernel(const uint16_t* __restrict__ src, long long l
       }
     }
   }
+}
+
+__global__ void unalign_f16_kernel(const RealignBatch b) {
+  griddep_wait();   // the kernel that writes the sources may still be running
+  int i = 0;
+  while (i + 1 < b.n && static_cast<int>(blockIdx.x) >= b.end[i]) ++i;
+  const int first = i ? b.end[i - 1] : 0;
+  const RealignJob& j = b.job[i];
+  unalign_rows(j.src, j.lds, j.dst, j.ldd, j.rows, j.cols, blockIdx.x - first, b.end[i] - first);
 }
 
 // tf32 value nearest to x (ties away from zero), as fp32 bits with the low 13
@@ -556,27 +564,17 @@ cudaError_t launch_f16x3_split(const float* A, long long lda, const float* B, lo
 }
 
 cudaError_t launch_realign_f16(const RealignBatch& batch, cudaStream_t stream) {
-  if (batch.n < 1 || batch.n > 3) return cudaErrorInvalidValue;
+  if (batch.n < 1 || batch.n > kRealignJobs) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(batch.end[batch.n - 1]);
   if (batch.early) return counted_launch(launch_early(realign_f16_kernel, grid, 256, 0, stream, batch));
   realign_f16_kernel<<<grid, 256, 0, stream>>>(batch);
   return counted_launch(cudaGetLastError());
 }
 
-cudaError_t launch_unalign_f16(const RealignJob& job, int grid, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, unalign_f16_kernel, static_cast<const uint16_t*>(job.src),
-                                           job.lds, job.dst, job.ldd, job.rows, job.cols);
-  if (e != cudaSuccess) return e;
-  return counted_launch(cudaGetLastError());
+cudaError_t launch_unalign_f16(const RealignBatch& batch, cudaStream_t stream) {
+  if (batch.n < 1 || batch.n > kRealignJobs) return cudaErrorInvalidValue;
+  return counted_launch(launch_early(unalign_f16_kernel, static_cast<unsigned>(batch.end[batch.n - 1]),
+                                     256, 0, stream, batch));
 }
 
 cudaError_t launch_splitk_reduce_f16(const float* ws, long long ws_ld, int splits, uint16_t* C,

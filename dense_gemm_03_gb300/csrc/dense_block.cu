@@ -68,6 +68,7 @@ bool narrow_suits(int M, int cols, int K, int sms) {
 struct GluArgs {
   const uint16_t *X, *W;
   int M, N, K, ldx, ldw, act;
+  int up;   // U's columns come so many after G's, in W and in dGU (tiles: N or more)
 };
 
 // gate 1: C := f(G) .* U; gate 2: C = dGU.
@@ -75,10 +76,10 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
           const LoraDevice& d, cudaStream_t stream) {
   GateArgs g{};
   g.act = p.act;
-  g.up = p.N;
+  g.up = p.up;
   g.dC = dC;
   g.lddc = lddc;
-  g.dU = gate == 2 ? C + p.N : nullptr;
+  g.dU = gate == 2 ? C + p.up : nullptr;
   if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) {
     StreamSum s{};
     s.C = C;
@@ -117,11 +118,14 @@ struct Trans {
   bool f32, ta, tb;
   int M, N, K, lda, ldb, ldc;
   float alpha, beta;
+  bool c_padded = false;   // see PairCall
   bool tiled(int sms) const { return !narrow_suits(M, N, K, sms); }
   bool on_grid() const {   // no copies of the operands
     return !misaligned({A, B}, 16) && lda % 8 == 0 && ldb % 8 == 0;
   }
-  bool c_on_grid() const { return f32 || (!misaligned({C}, 16) && ldc % 8 == 0 && N % 8 == 0); }
+  bool c_on_grid() const {
+    return f32 || (!misaligned({C}, 16) && ldc % 8 == 0 && (N % 8 == 0 || c_padded));
+  }
   long long tiles() const { return 1ll * ((M + 255) / 256) * ((N + 255) / 256); }
 };
 
@@ -159,6 +163,7 @@ int transposed(const Trans& p, bool whole, int most_pairs, const PairDone* befor
   q.beta = p.beta;
   q.trans_a = p.ta;
   q.trans_b = p.tb;
+  q.c_padded = p.c_padded;
   q.whole = whole;
   q.pairs = most_pairs;
   q.before = before;
@@ -194,6 +199,134 @@ int both(const Trans& a, const Trans& b, const LoraDevice& d, cudaStream_t strea
   }
   if (int rc = transposed(x, true, 0, nullptr, &done, d, stream)) return rc;
   return transposed(y, false, static_cast<int>(left), &done, nullptr, d, stream);
+}
+
+struct GradArgs {
+  const uint16_t *dC, *X, *W;
+  uint16_t *dGU, *dX, *dW;   // dX, dW: NULL when not wanted
+  int M, N, K, act, lddc, ldx, ldw, lddgu, lddx, lddw;
+  int up;                    // as in GluArgs; dX and dW are products with all 2 up columns
+  float beta;
+  bool dx_padded = false;    // columns of dX up to a multiple of eight may be written
+};
+
+int grad_products(const GradArgs& p, const LoraDevice& d, cudaStream_t stream) {
+  if (int rc = gated(GluArgs{p.X, p.W, p.M, p.N, p.K, p.ldx, p.ldw, p.act, p.up}, 2, p.dGU, p.lddgu,
+                     p.dC, p.lddc, d, stream))
+    return rc;
+  const int cols = 2 * p.up;
+  const Trans dx{p.dGU, p.W, p.dX, false, false, true, p.M, p.K, cols, p.lddgu, p.ldw, p.lddx, 1.0f, 0.0f,
+                 p.dx_padded};
+  const Trans dw{p.X, p.dGU, p.dW, false, true, false, p.K, cols, p.M, p.ldx, p.lddgu, p.lddw, 1.0f, p.beta};
+  if (p.dX && p.dW) return both(dx, dw, d, stream);
+  if (!p.dX && !p.dW) return GEMM_OK;
+  return transposed(p.dX ? dx : dw, false, 0, nullptr, nullptr, d, stream);
+}
+
+// Matrices that are copied onto the 16-byte grid, and results copied back, in one
+// launch each.
+struct Copies {
+  RealignBatch in{}, out{};
+  uint8_t* at;
+  int sms;
+  static int pad(int cols) { return (cols + 7) / 8 * 8; }
+  static size_t bytes(int rows, int ld) { return lora_round256(2 * static_cast<size_t>(rows) * ld); }
+  uint16_t* take(int rows, int ld) {
+    uint16_t* const p = reinterpret_cast<uint16_t*>(at);
+    at += bytes(rows, ld);
+    return p;
+  }
+  void add(RealignBatch& b, const uint16_t* src, int lds, uint16_t* dst, int ldd, int rows, int cols,
+           int width) {
+    const long long blocks = (1ll * rows * (width / 8) + 255) / 256;
+    b.job[b.n] = RealignJob{src, lds, dst, ldd, rows, cols, width};
+    b.end[b.n] = (b.n ? b.end[b.n - 1] : 0) + static_cast<int>(std::max(1ll, std::min(blocks, 8ll * sms)));
+    ++b.n;
+  }
+  // rows x cols; or two such halves, `up` columns apart in the copy
+  void fetch(const uint16_t* src, int lds, uint16_t* dst, int ldd, int rows, int cols, int up = 0) {
+    add(in, src, lds, dst, ldd, rows, cols, pad(cols));
+    if (up) add(in, src + cols, lds, dst + up, ldd, rows, cols, pad(cols));
+  }
+  void put(const uint16_t* src, int lds, uint16_t* dst, int ldd, int rows, int cols, int up = 0) {
+    add(out, src, lds, dst, ldd, rows, cols, pad(cols) + 16);
+    if (up) add(out, src + up, lds, dst + cols, ldd, rows, cols, pad(cols) + 16);
+  }
+};
+
+// The gradients.  Where whole tiles compute the gate's, matrices off the grid are
+// copied here, once for all three products; G's and U's columns then lie a multiple of eight
+// apart, with zeros between them in W and dGU, which add nothing to dX.  2000 x 1501 x 2*1111: 73 us
+// (copied for each product by itself 110; 1504 x 2*1112, no copies, 53).
+int grad(GradArgs p, const LoraDevice& d, cudaStream_t stream) {
+  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) return grad_products(p, d, stream);
+  auto off = [](const void* m, int ld) { return misaligned({m}, 16) || ld % 8 != 0; };
+  const int n8 = Copies::pad(p.N), k8 = Copies::pad(p.K);
+  const bool apart = p.N % 8 != 0;
+  const bool x = off(p.X, p.ldx), w = apart || off(p.W, p.ldw), c = off(p.dC, p.lddc);
+  const bool gu = apart || off(p.dGU, p.lddgu);
+  const bool dx = p.dX && (p.K % 8 != 0 || off(p.dX, p.lddx)), dw = p.dW && (apart || off(p.dW, p.lddw));
+  if (!(x || w || c || gu || dx || dw)) return grad_products(p, d, stream);
+  const size_t bytes = (x ? Copies::bytes(p.M, k8) : 0) + (w ? Copies::bytes(p.K, 2 * n8) : 0) +
+                       (c ? Copies::bytes(p.M, n8) : 0) + (gu ? Copies::bytes(p.M, 2 * n8) : 0) +
+                       (dx ? Copies::bytes(p.M, k8) : 0) + (dw ? Copies::bytes(p.K, 2 * n8) : 0);
+  void* buf = nullptr;
+  if (int rc = realigned_scratch(stream, bytes, &buf)) return rc;
+  Copies s;
+  s.at = static_cast<uint8_t*>(buf);
+  s.sms = d.sms;
+  const int half = apart ? p.N : 2 * p.N, up = apart ? n8 : 0;   // as copied
+  if (x) {
+    uint16_t* const m = s.take(p.M, k8);
+    s.fetch(p.X, p.ldx, m, k8, p.M, p.K);
+    p.X = m;
+    p.ldx = k8;
+  }
+  if (w) {
+    uint16_t* const m = s.take(p.K, 2 * n8);
+    s.fetch(p.W, p.ldw, m, 2 * n8, p.K, half, up);
+    p.W = m;
+    p.ldw = 2 * n8;
+  }
+  if (c) {
+    uint16_t* const m = s.take(p.M, n8);
+    s.fetch(p.dC, p.lddc, m, n8, p.M, p.N);
+    p.dC = m;
+    p.lddc = n8;
+  }
+  if (gu) {
+    uint16_t* const m = s.take(p.M, 2 * n8);
+    if (apart) {   // zeros where no gradient is written
+      s.add(s.in, m, 2 * n8, m + n8 - 8, 2 * n8, p.M, 0, 8);
+      s.add(s.in, m, 2 * n8, m + 2 * n8 - 8, 2 * n8, p.M, 0, 8);
+    }
+    s.put(m, 2 * n8, p.dGU, p.lddgu, p.M, half, up);
+    p.dGU = m;
+    p.lddgu = 2 * n8;
+  }
+  if (dx) {
+    uint16_t* const m = s.take(p.M, k8);
+    s.put(m, k8, p.dX, p.lddx, p.M, p.K);
+    p.dX = m;
+    p.lddx = k8;
+    p.dx_padded = true;
+  }
+  if (dw) {
+    uint16_t* const m = s.take(p.K, 2 * n8);
+    if (p.beta != 0.0f) s.fetch(p.dW, p.lddw, m, 2 * n8, p.K, half, up);
+    s.put(m, 2 * n8, p.dW, p.lddw, p.K, half, up);
+    p.dW = m;
+    p.lddw = 2 * n8;
+  }
+  if (apart) p.up = n8;
+  if (s.in.n) {
+    s.in.early = true;
+    if (launch_realign_f16(s.in, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+  }
+  if (int rc = grad_products(p, d, stream)) return rc;
+  set_last_path("glu_grad.copied");
+  if (!s.out.n) return GEMM_OK;
+  return launch_unalign_f16(s.out, stream) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
 int device(LoraDevice* d) { return query_device(&d->sms, &d->status, &d->wait_limit_ns); }
@@ -270,7 +403,7 @@ int gemm_f16_glu(const uint16_t* X, const uint16_t* W, uint16_t* C, int M, int N
     set_last_path("glu.blank");
     return blank(C, ldc, M, N, 0.0f, d, stream);
   }
-  return gated(GluArgs{X, W, M, N, K, ldx, ldw, act}, 1, C, ldc, nullptr, 0, d, stream);
+  return gated(GluArgs{X, W, M, N, K, ldx, ldw, act, N}, 1, C, ldc, nullptr, 0, d, stream);
 }
 
 int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, uint16_t* dGU,
@@ -302,13 +435,9 @@ int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, 
       if (int rc = blank(dX, lddx, M, K, 0.0f, d, stream)) return rc;
     return want_dw ? blank(dW, lddw, K, 2 * N, beta, d, stream) : GEMM_OK;
   }
-  if (int rc = gated(GluArgs{X, W, M, N, K, ldx, ldw, act}, 2, dGU, lddgu, dC, lddc, d, stream))
-    return rc;
-  const Trans dx{dGU, W, dX, false, false, true, M, K, 2 * N, lddgu, ldw, lddx, 1.0f, 0.0f};
-  const Trans dw{X, dGU, dW, false, true, false, K, 2 * N, M, ldx, lddgu, lddw, 1.0f, beta};
-  if (!want_dx && !want_dw) return GEMM_OK;
-  if (!want_dx || !want_dw) return transposed(want_dx ? dx : dw, false, 0, nullptr, nullptr, d, stream);
-  return both(dx, dw, d, stream);
+  return grad(GradArgs{dC, X, W, dGU, want_dx ? dX : nullptr, want_dw ? dW : nullptr, M, N, K, act,
+                       lddc, ldx, ldw, lddgu, lddx, lddw, N, beta},
+              d, stream);
 }
 
 }  // extern "C"

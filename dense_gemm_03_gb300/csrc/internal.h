@@ -210,6 +210,7 @@ struct PairCall {
   int gate;
   bool scaled;
   GateArgs g;
+  bool c_padded;           // C's columns up to a multiple of eight may be written
   bool whole;              // no half-width tiles: they would take SMs of a product beside
   int pairs;               // of SMs at most (0: all)
   const PairDone* before;  // see above; or NULL
@@ -309,20 +310,21 @@ struct RealignJob {
   int rows, cols;
   long long width = 0;   // 0: ldd
 };
-// One launch for up to three copies: blocks [end[i-1], end[i]) copy jobs[i].
+// One launch for several copies: blocks [end[i-1], end[i]) copy jobs[i].
+constexpr int kRealignJobs = 8;
 struct RealignBatch {
-  RealignJob job[3];
-  int end[3];
+  RealignJob job[kRealignJobs];
+  int end[kRealignJobs];
   int n;
   bool early = false;   // see launch_early
 };
 cudaError_t launch_realign_f16(const RealignBatch& batch, cudaStream_t stream);
 
-// The copy back: dst (rows x cols, any 2-byte alignment and leading dimension
+// The copies back: dst (rows x cols, any 2-byte alignment and leading dimension
 // ldd) := src (16-byte-aligned rows, lds >= cols rounded up to 8).  Launched
 // after the kernel that writes src, which it may overlap (programmatic
 // dependent launch; it waits for that kernel's completion before reading).
-cudaError_t launch_unalign_f16(const RealignJob& job, int grid, cudaStream_t stream);
+cudaError_t launch_unalign_f16(const RealignBatch& batch, cudaStream_t stream);
 
 // Both splits of a 3xTF32 product in one launch: A (M x K) into Ab, As and
 // B^T (B is K x N) into Bb, Bs, all with leading dimension ld2 (>= K, % 4 == 0);
@@ -443,6 +445,8 @@ int lock_stream(cudaStream_t stream, std::unique_lock<std::recursive_mutex>* cal
 // gemm_release().  Returns a GEMM_* code.
 // `zeroed`: a separate region of at least that many bytes that starts at zero
 // when it is first handed out and then keeps what kernels leave in it.
+// The buffer of the copies that gemm_f16_pair makes (it makes none of operands on the grid).
+int realigned_scratch(cudaStream_t stream, size_t bytes, void** out);
 int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed = 0,
                    void** zeroed_out = nullptr);
 // Tensor map of a stack of `depth` fp16 matrices (rows x cols, leading

@@ -360,3 +360,43 @@ def test_sums_over_millions_of_tokens(f32):
     sync(t)
     # half results: |sums| stay below 2^24, exact in fp32 too, and are rounded once
     assert t.equal(C, want.to(C.dtype))
+
+
+@pytest.mark.parametrize("off", ["none", "x", "w", "dc", "gu", "dx", "dw", "all"])
+@pytest.mark.parametrize("M,N,K", [(300, 1504, 264), (700, 1111, 331)])
+def test_glu_grad_with_single_matrices_off_the_grid(M, N, K, off):
+    """Every matrix by itself at an odd address and pitch, the others on the 16-byte grid
+    (odd widths in rows padded to it); a row with an infinity leaves the others alone."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    X, W, dC = operands(t, M, N, K)
+    bad = M - 3
+    X[bad, 5] = float("inf")
+    good = [i for i in range(M) if i != bad]
+    nan = lambda *s: t.full(s, float("nan"), dtype=t.float16)
+    W0 = normal(t, np.random.default_rng(3), (K, 2 * N))
+
+    def put(name, v):
+        if off in (name, "all"):
+            return Padded(t, v, 1 + v.shape[1] % 2 * 2, 3)      # odd pitches, odd address
+        return Padded(t, v, -v.shape[1] % 8, 0)
+    x, w, dc = put("x", X), put("w", W), put("dc", dC)
+    gu, dx, dw = put("gu", nan(M, 2 * N)), put("dx", nan(M, K)), put("dw", W0)
+    for rows, beta in ((good, 0.0), (None, 0.5)):
+        if rows is None:                 # dW of finite rows, added onto what is there
+            X[bad, 5] = 1.0
+            x.view.copy_(X.cuda())
+            rows = range(M)
+            dw.view.copy_(W0.cuda())
+        g.gemm_f16_glu_grad(dc.ptr, x.ptr, w.ptr, gu.ptr, dx.ptr, dw.ptr, "silu", beta, M=M, N=N, K=K,
+                            lddc=dc.ld, ldx=x.ld, ldw=w.ld, lddgu=gu.ld, lddx=dx.ld, lddw=dw.ld)
+        sync(t)
+        rows = list(rows)
+        held = gu.view.cpu()
+        ref.check(held[rows], *ref.glu_grad(dC[rows], X[rows], W, "silu"), "dGU")
+        ref.check(dx.view.cpu()[rows], *ref.product(held[rows], W.t()), "dX")
+        if len(rows) == M:
+            ref.check(dw.view.cpu(), *ref.product(X.t(), held, 1.0, beta, W0), "dW")
+        else:
+            assert not bool(held[bad].isfinite().all()) and not bool(dx.view[bad].isfinite().any())
+        assert all(m.untouched(t) for m in (gu, dx, dw))
