@@ -20,7 +20,7 @@
 // W in 0.31 us, whatever the bytes.  The first loads are issued before tensor memory is
 // allocated and the CTA's threads have met.
 //
-// What bounds: one token of 2048 x 2*4096, 34 MB of W, takes 8.6 us: 4.6 us at the HBM rate
+// What bounds: one token of 2048 x 2*4096, 34 MB of W, takes 8.4 us: 4.6 us at the HBM rate
 // and the chain of a launch, the first load's latency and two cluster barriers.
 //
 // Shared memory: ring stages of W, two 64-column blocks [128 k][64 halves]
