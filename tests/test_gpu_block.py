@@ -400,3 +400,34 @@ def test_glu_grad_with_single_matrices_off_the_grid(M, N, K, off):
         else:
             assert not bool(held[bad].isfinite().all()) and not bool(dx.view[bad].isfinite().any())
         assert all(m.untouched(t) for m in (gu, dx, dw))
+
+
+@pytest.mark.parametrize("M,N", [(8192, 1056), (6000, 1312), (16384, 296)])
+@pytest.mark.parametrize("K", [24, 72])
+def test_short_sums_and_a_narrow_last_tile(M, N, K):
+    """Tiles that follow one another at once, the last of a row of tiles only 32 or 40
+    columns wide: what a tile leaves on its way out is not overwritten by the next.
+    Small integers, exact throughout."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    gen = t.Generator(device="cuda").manual_seed(9)
+    draw = lambda *s: t.randint(-2, 3, s, generator=gen, device="cuda").half()
+    A, B, B2, dC = draw(M, K), draw(K, N), draw(K, 2 * N), draw(M, N)
+    AT, C, H = A.t().contiguous(), *(t.empty(M, N, dtype=t.float16, device="cuda") for _ in "ch")
+    F, gu = t.empty(M, N, device="cuda"), t.empty(M, 2 * N, dtype=t.float16, device="cuda")
+    P, S = A.float() @ B.float(), A.float() @ B2.float()
+    G, U = S[:, :N], S[:, N:]
+    for _ in range(5):
+        for o in (C, H, F, gu):
+            o.fill_(float("nan"))
+        g.gemm_f16(A, B, C)
+        assert t.equal(C.float(), P)
+        C.fill_(float("nan"))
+        g.gemm_f16_trans(AT, B, C, True, False)
+        g.gemm_f16_trans_f32out(AT, B, F, True, False)
+        g.gemm_f16_glu(A, B2, H, "relu")
+        g.gemm_f16_glu_grad(dC, A, B2, gu, act="relu")
+        sync(t)
+        assert t.equal(C.float(), P) and t.equal(F, P)
+        assert t.equal(H, (G.clamp(min=0) * U).half())
+        assert t.equal(gu, t.cat([dC.float() * U * (G > 0), dC.float() * G.clamp(min=0)], 1).half())
