@@ -1396,6 +1396,55 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         }
       }
     };
+    // Whole tiles whose results replace C: a short loop, whose instructions stay
+    // near the SM's schedulers.  (Unrolled, the general code below waits for them for most of
+    // its time: 4096 x 8192 halves over 64, an epilogue for each k-block, 30.6 us, here 22.2;
+    // 4096 x 4096 floats over 64 transposed 25.8 and 17.4.)
+    constexpr bool kBrief = kGate == 0 && kCs && !LORA::kOn && !LORA::kScaled;
+    [[maybe_unused]] auto brief_epilogue = [&](uint32_t tbase, int nsub, int colw, int row0) {
+      if constexpr (kBrief) {
+#pragma unroll 1
+        for (int j = 0; j < nsub * kTpc && colw + kTc * j < p.N; ++j) {
+          const uint32_t b = static_cast<uint32_t>(j) & 1u;
+          uint8_t* const sptr = sptr0 + b * kEpiBufBytes;
+          uint32_t acc[kTc];
+          if constexpr (EPI == kEpiTma) {
+            tmem_ld_32x32b_x32(tbase + kTc * j, acc);
+          } else {
+            uint32_t v[8], w[8];
+            tmem_ld_32x32b_x8(tbase + kTc * j, v);
+            tmem_ld_32x32b_x8(tbase + kTc * j + 8, w);
+            tmem_wait_ld2(v, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[i] = v[i];
+              acc[8 + i] = w[i];
+            }
+          }
+          if (lane == 0) staged_stores_read(j == 0);
+          __syncwarp();
+          const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+          if constexpr (EPI == kEpiTma) {
+            tmem_wait_regs(acc);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<uint4*>(sptr + sw64_chunk(lane, g)) =
+                  epilogue8(acc + 8 * g, none, false, p.alpha, 0.0f);
+          } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<uint4*>(sptr + sw64_chunk(lane, g)) =
+                  epilogue4f(acc + 4 * g, none, false, p.alpha, 0.0f);
+          }
+          fence_proxy_async_smem();   // generic writes -> TMA store reads
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmC, sbuf0 + b * kEpiBufBytes, colw + kTc * j, row0);
+            bulk_commit_group();
+          }
+        }
+      }
+    };
     UnitCursor cur = first_unit(p, worker);
     Unit t, tn;
     bool have = next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, t);
@@ -1467,9 +1516,24 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             prefetch_l2(x.a.dC + static_cast<long long>(row) * x.a.lddc + colw + kSubCols);
         }
       }
+      // (a folded sum in one part needs no folding)
+      bool brief = kBrief && !has_c && !t.tail;
+      if constexpr (LORA::kFold) brief = brief && t.kb1 - t.kb0 <= x.fold_kb;
       // kFold: this row's sums, every part of the accumulator added as it comes
       [[maybe_unused]] float sum[LORA::kFold ? kSubs * kSubCols : 1];
-      if constexpr (LORA::kFold) {
+      if (LORA::kFold && brief) {
+        const uint32_t b = local & 1u;
+        if (!wait_parity(accf_bar(b), (local >> 1) & 1u, limit, st, 5)) break;
+        tc_fence_after();
+        if (finish)
+          brief_epilogue(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + b * Cfg::kAccStride +
+                             static_cast<uint32_t>(wcol0),
+                         nsub, colw, row0);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_acc_empty(map_to_cta(acce_bar(b), 0));
+        ++local;
+      } else if constexpr (LORA::kFold) {
 #pragma unroll
         for (int i = 0; i < kSubs * kSubCols; ++i) sum[i] = 0.0f;
         bool ok = true;
@@ -1614,36 +1678,8 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         if (finish && kGate == 2)
           gate_grad_epilogue(t, tail_part, tbase, wcol0, nsub, colw, row0, row);
       }
-      // Whole tiles of half results that replace C: a short loop, whose instructions
-      // stay near the SM's schedulers.  (Unrolled, the general code below waits for them for
-      // most of its time: 4096 x 8192 over 64, an epilogue for each k-block, 30.6 us, here
-      // 22.2.)
-      constexpr bool kBrief = kGate == 0 && kCs && EPI == kEpiTma && !LORA::kOn && !LORA::kFold &&
-                              !LORA::kScaled;
-      const bool brief = kBrief && !has_c && !t.tail;
-      if constexpr (kBrief) {
-        if (brief && finish) {
-#pragma unroll 1
-          for (int k = 0; k < nsub && colw + kSubCols * k < p.N; ++k) {
-            const uint32_t b = static_cast<uint32_t>(k) & 1u;
-            uint8_t* const sptr = sptr0 + b * kEpiBufBytes;
-            uint32_t acc[32];
-            tmem_ld_32x32b_x32(tbase + kSubCols * k, acc);
-            if (lane == 0) staged_stores_read(k == 0);
-            __syncwarp();
-            tmem_wait_regs(acc);
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              *reinterpret_cast<uint4*>(sptr + sw64_chunk(lane, g)) =
-                  epilogue8(acc + 8 * g, make_uint4(0u, 0u, 0u, 0u), false, p.alpha, 0.0f);
-            fence_proxy_async_smem();   // generic writes -> TMA store reads
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(&tmC, sbuf0 + b * kEpiBufBytes, colw + kSubCols * k, row0);
-              bulk_commit_group();
-            }
-          }
-        }
+      if constexpr (kBrief && !LORA::kFold) {
+        if (brief && finish) brief_epilogue(tbase, nsub, colw, row0);
       }
       if (kGate == 0 && finish && !brief) {
         uint32_t acc_a[32], acc_b[32];
