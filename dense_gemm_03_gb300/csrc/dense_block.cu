@@ -55,14 +55,17 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
 }
 
 // Whether K chunks suit the product better than whole 256 x 256 tiles (`cols` columns of
-// W).  Measured, chunks against tiles: one block of rows wins as long as it is not full
-// (192 x 8192 x 2048 14.5 us, 16.4; 256 rows 16.5, 16.4); so do few tiles with a long
-// K (16 tiles: K = 1024 10.0, 10.5; K = 4096 15.0, 24.0; but 32 tiles, K = 512 10.5, 8.7 and K =
-// 1024 12.1, 11.1) and narrow results (2048 x 256 x 2048 10.8, 14.6).
+// W).  Measured, chunks against tiles: a block of up to 128 rows wins or draws (128 x 8192
+// x 2048 11.1 us, 14.4; 128 x 4096 x 512 6.2, 6.2), up to 192 with a sum long enough (160 x 4096 x
+// 768 7.0, 7.3, but 192 x 4096 x 512 7.2, 6.2; 192 x 8192 x 2048 14.2, 14.5, but 224 rows 15.4,
+// 14.6); so do few tiles with a long K (512 x 512 x 1536 9.5, 10.5; 331 x 2048 x 4096 11.7, 21.9; but
+// 1024^3 9.3, 8.4, and 32 tiles, 1024 x 2048 x 2048, 14.4, 13.8) and narrow results (6000 x 128 x
+// 1536 10.3, 11.0, 9000 x 64 x 1024 8.6, 8.8, but 2048 x 128 x 512 8.0, 6.1).
 bool narrow_suits(int M, int cols, int K, int sms) {
+  if (M <= 128) return true;
+  if (M <= 192) return K >= 768;
   const long long tiles = static_cast<long long>((M + 255) / 256) * ((cols + 255) / 256);
-  if (M <= 224) return true;
-  return 4 * tiles <= sms && (cols <= 128 || (8 * tiles <= sms && K >= 1024));
+  return cols <= 128 ? 4 * tiles <= sms && K >= 1024 : 8 * tiles <= sms && K >= 1536;
 }
 
 struct GluArgs {
