@@ -178,9 +178,9 @@ int transposed(const Trans& p, bool whole, int most_pairs, const PairDone* befor
 // enough SMs idle: whole tiles of that, the other on the SMs left, in as many rounds as it
 // takes; k-blocks of the longer way are weighed against one after the other over all SMs, a
 // kernel's start and end counting as 12.  Gradients of 1500 x 1000 x 2*1368, 24 tiles of 43
-// k-blocks and 44 of 24: 61.5 us one after the other, 47 side by side; 4096 x 1024 x 2*1024, 32
-// of 64 and 64 of 32: 80 and 61; 300 x 1000 x 2*1368, 44 of 5 and a streamed product: 37.5
-// and 33.7.  Else the second starts as the first's last blocks end.
+// k-blocks and 44 of 24: 48.2 us one after the other, 40.8 side by side; 4096 x 1024 x 2*1024, 32
+// of 64 and 64 of 32: 66.3 and 52.6; 300 x 1000 x 2*1368, 44 of 5 and a streamed product: 32.2
+// and 28.3.  Else the second starts as the first's last blocks end.
 int both(const Trans& a, const Trans& b, const LoraDevice& d, cudaStream_t stream) {
   const bool ta = a.tiled(d.sms), tb = b.tiled(d.sms);
   // tiles before a streamed product, longer tiles before shorter ones
@@ -259,8 +259,8 @@ struct Copies {
 
 // The gradients.  Where whole tiles compute the gate's, matrices off the grid are
 // copied here, once for all three products; G's and U's columns then lie a multiple of eight
-// apart, with zeros between them in W and dGU, which add nothing to dX.  2000 x 1501 x 2*1111: 73 us
-// (copied for each product by itself 110; 1504 x 2*1112, no copies, 53).
+// apart, with zeros between them in W and dGU, which add nothing to dX.  2000 x 1501 x 2*1111: 71 us
+// (1504 x 2*1112, no copies: 51; copied for each product by itself 37 more than here).
 int grad(GradArgs p, const LoraDevice& d, cudaStream_t stream) {
   if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) return grad_products(p, d, stream);
   auto off = [](const void* m, int ld) { return misaligned({m}, 16) || ld % 8 != 0; };
