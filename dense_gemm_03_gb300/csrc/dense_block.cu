@@ -39,7 +39,7 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   const size_t copies = x.bytes() + w.bytes();
   const bool cluster = narrow_cluster_suits(s, K, d);
   NarrowStream p{X, W, ldx, ldw, K, trans_x, trans_w};
-  if (!cluster) s.parts = narrow_parts(p, M, cols, s.f32, d);
+  if (!cluster) s.parts = narrow_parts(p, M, cols, s.f32 || s.fold, d);
   void* buf = nullptr;
   if (copies + s.parts.bytes)
     if (int rc = routed_scratch(stream, copies + s.parts.bytes, &buf)) return rc;
@@ -50,7 +50,7 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   p = NarrowStream{X, W, ldx, ldw, K, trans_x, trans_w, before && before->pair && !*copied};
   if (cluster) return narrow_cluster(p, s, d, stream);
   s.parts.part = reinterpret_cast<float*>(static_cast<uint8_t*>(buf) + copies);
-  if (int rc = narrow_partial(p, M, cols, s.f32, s.parts, d, stream)) return rc;
+  if (int rc = narrow_partial(p, M, cols, s.f32 || s.fold, s.parts, d, stream)) return rc;
   return stream_sum(s, d, stream);
 }
 
@@ -68,6 +68,15 @@ bool narrow_suits(int M, int cols, int K, int sms) {
   return cols <= 128 ? 4 * tiles <= sms && K >= 1024 : 8 * tiles <= sms && K >= 1536;
 }
 
+// relu's derivative jumps at 0, where a sum's error turns dC U into nothing or back.
+// The tensor core's additions truncate, and long sums of G drift further than sums
+// rounded to nearest; so a relu's gradient over more than 1024 products takes chunks of
+// kFoldDepth, added up in fp32, as long as their partial sums stay within 4 GB.
+bool folds(int gate, int act, int M, int N, int K) {
+  return gate == 2 && act == GEMM_ACT_RELU && K > 1024 &&
+         8.0 * M * N * ((K + kFoldDepth - 1) / kFoldDepth) <= 4e9;
+}
+
 struct GluArgs {
   const uint16_t *X, *W;
   int M, N, K, ldx, ldw, act;
@@ -83,8 +92,10 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
   g.dC = dC;
   g.lddc = lddc;
   g.dU = gate == 2 ? C + p.up : nullptr;
-  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) {
+  const bool fold = folds(gate, p.act, p.M, p.N, p.K);
+  if (fold || narrow_suits(p.M, 2 * p.N, p.K, d.sms)) {
     StreamSum s{};
+    s.fold = fold;
     s.C = C;
     s.ldc = ldc;
     s.M = p.M;
@@ -262,7 +273,8 @@ struct Copies {
 // apart, with zeros between them in W and dGU, which add nothing to dX.  2000 x 1501 x 2*1111: 71 us
 // (1504 x 2*1112, no copies: 51; copied for each product by itself 37 more than here).
 int grad(GradArgs p, const LoraDevice& d, cudaStream_t stream) {
-  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) return grad_products(p, d, stream);
+  if (folds(2, p.act, p.M, p.N, p.K) || narrow_suits(p.M, 2 * p.N, p.K, d.sms))
+    return grad_products(p, d, stream);
   auto off = [](const void* m, int ld) { return misaligned({m}, 16) || ld % 8 != 0; };
   const int n8 = Copies::pad(p.N), k8 = Copies::pad(p.K);
   const bool apart = p.N % 8 != 0;

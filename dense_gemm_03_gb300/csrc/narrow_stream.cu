@@ -338,7 +338,7 @@ int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const Stre
 bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
   if (s.gate && s.N % 8 != 0) return false;   // U's columns start on TMA's 16-byte grid
   const Tiles a = cluster_tiles(s, K, kBlockRows, d);
-  return cluster_pays(a, d.sms) && (!s.f32 || longest_chunk(K, a.chunks) <= kFoldDepth);
+  return cluster_pays(a, d.sms) && (!(s.f32 || s.fold) || longest_chunk(K, a.chunks) <= kFoldDepth);
 }
 
 int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,

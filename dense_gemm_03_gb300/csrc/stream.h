@@ -55,6 +55,7 @@ struct StreamSum {
   float alpha, beta;
   int gate;
   bool f32, scaled;
+  bool fold;   // chunks of kFoldDepth at most, as a float result's
   GateArgs g;
 };
 // The whole product in one launch, finished as `s` says (its parts unused), where one

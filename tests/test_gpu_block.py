@@ -431,3 +431,21 @@ def test_short_sums_and_a_narrow_last_tile(M, N, K):
         assert t.equal(C.float(), P) and t.equal(F, P)
         assert t.equal(H, (G.clamp(min=0) * U).half())
         assert t.equal(gu, t.cat([dC.float() * U * (G > 0), dC.float() * G.clamp(min=0)], 1).half())
+
+
+@pytest.mark.parametrize("M,N,K", [(700, 1368, 4096), (300, 1111, 2049), (64, 1000, 3000)])
+def test_relu_gradient_of_long_sums(M, N, K):
+    """relu's derivative jumps where G is 0: sums of G as near as sums in fp32 get.  Rounded
+    to nearest in runs of 512, G's error is below 2e-6 of its size here (one in 2^24 for
+    each of the runs' additions, and the truncation within them), so at most 2 sqrt(2/pi) 2e-6
+    of the entries (a normal density about 0) can be on the wrong side: 4 in a million,
+    and as many again for the unlucky."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    X, W, dC = operands(t, M, N, K)
+    gu = t.empty(M, 2 * N, dtype=t.float16, device="cuda")
+    g.gemm_f16_glu_grad(dC.cuda(), X.cuda(), W.cuda(), gu, act="relu")
+    sync(t)
+    want, tol = ref.glu_grad(dC, X, W, "relu")
+    off = ((gu.cpu().double() - want).abs() > tol + 1e-5).double().mean()
+    assert float(off) <= 8e-6 + 2.0 / (M * N)
