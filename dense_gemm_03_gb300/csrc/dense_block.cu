@@ -37,8 +37,8 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   Aligned x(X, ldx, trans_x ? K : M, trans_x ? M : K, true);
   Aligned w(W, ldw, trans_w ? cols : K, trans_w ? K : cols, true);
   const size_t copies = x.bytes() + w.bytes();
-  const bool cluster = narrow_cluster_suits(s, K, d);
   NarrowStream p{X, W, ldx, ldw, K, trans_x, trans_w};
+  const bool cluster = narrow_cluster_suits(p, s, d);
   if (!cluster) s.parts = narrow_parts(p, M, cols, s.f32 || s.fold, d);
   void* buf = nullptr;
   if (copies + s.parts.bytes)

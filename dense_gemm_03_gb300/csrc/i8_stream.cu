@@ -326,7 +326,7 @@ int launch(const Args& a, const NarrowStream& p, const StreamSum& fin, int grid,
 
 Args plan_partial(const NarrowStream& p, int M, int cols, const LoraDevice& d) {
   Args a{};
-  static_cast<Tiles&>(a) = partial_tiles(M, cols, p.K, kBlockRows, (p.K + 127) / 128, 1, d);
+  static_cast<Tiles&>(a) = partial_tiles(M, cols, p.K, kBlockRows, false, (p.K + 127) / 128, 1, d);
   lay_out(a, kMaxStages, false);
   return a;
 }
@@ -348,13 +348,13 @@ int i8_partial(const NarrowStream& p, int M, int cols, const StreamParts& parts,
 
 bool i8_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
   // U's columns start on the 16-byte grid
-  return (!s.gate || s.N % 16 == 0) && cluster_pays(cluster_tiles(s, K, kBlockRows, d), d.sms);
+  return (!s.gate || s.N % 16 == 0) && cluster_pays(cluster_tiles(s, K, kBlockRows, false, d), d.sms);
 }
 
 int i8_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,
                cudaStream_t stream) {
   Args a{};
-  static_cast<Tiles&>(a) = cluster_tiles(s, p.K, kBlockRows, d);
+  static_cast<Tiles&>(a) = cluster_tiles(s, p.K, kBlockRows, false, d);
   if (a.chunks == 0) return GEMM_ERR_ARG;
   lay_out(a, (a.kb + a.chunks - 1) / a.chunks, true);
   return s.gate ? launch<kScaledGate>(a, p, s, a.items, stream)

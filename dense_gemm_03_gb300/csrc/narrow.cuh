@@ -163,16 +163,10 @@ inline bool cluster_pays(const Tiles& a, int sms) {
   return (longest - even) * (0.3 + 0.003 * a.n_cols) < 3.3;
 }
 
-// Rows of a block: all blocks about as long, in 16s, at most `most`.
-inline int block_rows(int M, int most) {
-  const int blocks = (M + most - 1) / most;
-  return std::min(M, ((M + blocks - 1) / blocks + 15) / 16 * 16);
-}
-
-inline void common_tiles(Tiles& a, int M, int K, int rows, const LoraDevice& d) {
+inline void common_tiles(Tiles& a, int M, int K, int rows, bool trans_x, const LoraDevice& d) {
   a.M = M;
   a.K = K;
-  a.rows = block_rows(M, rows);
+  a.rows = block_rows(M, rows, trans_x);
   a.kb = (K + kStepK - 1) / kStepK;
   a.n_cols = (a.rows + 15) / 16 * 16;
   a.acc_cols = 32;
@@ -190,10 +184,10 @@ inline void cut(Tiles& a, long long tiles, int chunks) {
 }
 
 // Partial sums over persistent CTAs.
-inline Tiles partial_tiles(int M, int cols, int K, int rows, int kb16, int least,
+inline Tiles partial_tiles(int M, int cols, int K, int rows, bool trans_x, int kb16, int least,
                            const LoraDevice& d) {
   Tiles a{};
-  common_tiles(a, M, K, rows, d);
+  common_tiles(a, M, K, rows, trans_x, d);
   const int blocks = (M + a.rows - 1) / a.rows;
   a.N = cols;
   a.units = (cols + 127) / 128;
@@ -204,9 +198,9 @@ inline Tiles partial_tiles(int M, int cols, int K, int rows, int kb16, int least
 }
 
 // The cluster form; chunks == 0: it does not suit.
-inline Tiles cluster_tiles(const StreamSum& s, int K, int rows, const LoraDevice& d) {
+inline Tiles cluster_tiles(const StreamSum& s, int K, int rows, bool trans_x, const LoraDevice& d) {
   Tiles a{};
-  common_tiles(a, s.M, K, rows, d);
+  common_tiles(a, s.M, K, rows, trans_x, d);
   const int blocks = (s.M + a.rows - 1) / a.rows;
   a.N = s.gate ? 2 * s.N : s.N;
   a.unit_cols = s.gate ? 64 : 128;

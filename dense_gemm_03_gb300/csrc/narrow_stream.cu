@@ -293,7 +293,7 @@ int make_maps(Args& a, const NarrowStream& p, bool paired, int up, CUtensorMap* 
   }
   if (rc) return rc;
   if (a.trans_x) {
-    a.one_x = a.M % 64 == 0;
+    a.one_x = block_of_64s(a.M, a.rows);   // (its coordinate counts 64-row blocks)
     return a.one_x ? encode_map_3d(tmX, 2, p.X, {64, K, a.M / 64}, {p.ldx, 64},
                                    {64, kStepK, (a.n_cols + 63) / 64})
                    : encode_map_3d(tmX, 2, p.X, {a.M, K, 0}, {p.ldx, 0}, {64, kStepK, 0});
@@ -313,7 +313,7 @@ Args plan_partial(const NarrowStream& p, int M, int cols, bool fold, const LoraD
   Args a{};
   // chunks of kFoldDepth at most
   const int least = fold ? ((p.K + kStepK - 1) / kStepK - 1) / (kFoldDepth / kStepK) + 1 : 1;
-  static_cast<Tiles&>(a) = partial_tiles(M, cols, p.K, kBlockRows, (p.K + 63) / 64, least, d);
+  static_cast<Tiles&>(a) = partial_tiles(M, cols, p.K, kBlockRows, p.trans_x, (p.K + 63) / 64, least, d);
   lay_out(a, p, kMaxStages, false);
   return a;
 }
@@ -335,16 +335,16 @@ int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const Stre
   return launch<kPartial>(a, StreamSum{}, tmW, tmX, std::min(a.items, d.sms), stream);
 }
 
-bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d) {
+bool narrow_cluster_suits(const NarrowStream& p, const StreamSum& s, const LoraDevice& d) {
   if (s.gate && s.N % 8 != 0) return false;   // U's columns start on TMA's 16-byte grid
-  const Tiles a = cluster_tiles(s, K, kBlockRows, d);
-  return cluster_pays(a, d.sms) && (!(s.f32 || s.fold) || longest_chunk(K, a.chunks) <= kFoldDepth);
+  const Tiles a = cluster_tiles(s, p.K, kBlockRows, p.trans_x, d);
+  return cluster_pays(a, d.sms) && (!(s.f32 || s.fold) || longest_chunk(p.K, a.chunks) <= kFoldDepth);
 }
 
 int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,
                    cudaStream_t stream) {
   Args a{};
-  static_cast<Tiles&>(a) = cluster_tiles(s, p.K, kBlockRows, d);
+  static_cast<Tiles&>(a) = cluster_tiles(s, p.K, kBlockRows, p.trans_x, d);
   if (a.chunks == 0) return GEMM_ERR_ARG;
   lay_out(a, p, (a.kb + a.chunks - 1) / a.chunks, true);
   CUtensorMap tmW{}, tmX{};

@@ -8,13 +8,14 @@
 
 #include "internal.h"
 #include "lora.h"
+#include "row_blocks.h"
 
 namespace gb300 {
 
 // Partial sums: [block of `block` rows][128-column unit][chunk][row of the block][128].
 struct StreamParts {
   float* part;
-  int chunks, units, block_rows;   // block_rows = min(M, block)
+  int chunks, units, block_rows;   // block_rows = block: see row_blocks.h
   size_t bytes;
   int block;
 };
@@ -60,7 +61,7 @@ struct StreamSum {
 };
 // The whole product in one launch, finished as `s` says (its parts unused), where one
 // wave of clusters covers it.
-bool narrow_cluster_suits(const StreamSum& s, int K, const LoraDevice& d);
+bool narrow_cluster_suits(const NarrowStream& p, const StreamSum& s, const LoraDevice& d);
 int narrow_cluster(const NarrowStream& p, const StreamSum& s, const LoraDevice& d,
                    cudaStream_t stream);
 bool i8_cluster_suits(const StreamSum& s, int K, const LoraDevice& d);
