@@ -390,11 +390,13 @@ def _elsewhere(x, name):
 
 def _matrix(x, rows, cols, ld, dtype, name):
     """Address and leading dimension of a rows x cols matrix of `dtype` in device memory:
-    a tensor whose rows are dense (their distance is the leading dimension unless one is
-    given), or an address, taken at its word."""
+    a tensor of two dimensions, as large or larger, whose rows are dense (their distance is
+    the leading dimension unless one is given); a contiguous one of another number of
+    dimensions, whose last has `cols` elements (a batch's tokens) or which has no other (a flat
+    buffer); or an address, taken at its word."""
     try:                                          # the usual tensor, in little time
-        if _dtype_names[x.dtype] == dtype and x.is_cuda and x.is_contiguous() \
-                and x.numel() >= rows * cols and ld is None:
+        if x.shape == (rows, cols) and ld is None and _dtype_names[x.dtype] == dtype and x.is_cuda \
+                and x.is_contiguous():
             if _devices != 1:
                 _elsewhere(x, name)
             return x.data_ptr(), cols
@@ -408,6 +410,9 @@ def _matrix(x, rows, cols, ld, dtype, name):
         raise ValueError("%s is not in device memory" % name)
     _elsewhere(x, name)
     if ld is None:
+        if x.dim() != 2 and x.is_contiguous() and x.numel() >= rows * cols \
+                and (x.dim() == 1 or x.dim() and x.shape[-1] == cols):
+            return x.data_ptr(), cols
         if x.dim() != 2 or x.shape[0] < rows or x.shape[1] < cols:
             raise ValueError("%s is %s, not %d x %d" % (name, tuple(x.shape), rows, cols))
         if rows * cols and (x.stride(1) != 1 and cols > 1 or x.stride(0) < cols and rows > 1):
