@@ -521,6 +521,8 @@ def _scales(x, n, name):
     try:                                          # the usual tensor, in little time
         if _dtype_names[x.dtype] == "float32" and x.is_cuda and x.is_contiguous() \
                 and x.numel() >= n:
+            if _devices != 1:
+                _elsewhere(x, name)
             return x.data_ptr()
     except (AttributeError, KeyError):
         pass
@@ -528,7 +530,9 @@ def _scales(x, n, name):
         return x
     if not getattr(x, "is_cuda", False) and _dtype_name(x) == "float32":
         raise ValueError("%s is not in device memory" % name)
-    return _typed(x, "float32", n, name)
+    at = _typed(x, "float32", n, name)
+    _elsewhere(x, name)
+    return at
 
 
 def gemm_i8(X, W, C, sx=None, sw=None, act=None, beta=0.0, M=None, N=None, K=None, ldx=None,

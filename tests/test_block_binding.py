@@ -86,3 +86,15 @@ def test_results_with_padding_or_transposed(monkeypatch):
         g.gemm_f16_glu_grad(h(4, 6), h(4, 8), h(8, 12), h(4, 12), None, h(12, 8), stream=0)
     with pytest.raises(ValueError, match="C is"):
         g.gemm_f16_trans(h(8, 4), h(8, 6), h(6, 4), True, stream=0)
+
+
+def test_scales_of_another_device(monkeypatch):
+    """Scales are read on the current device, as the matrices are."""
+    monkeypatch.setattr(g, "_devices", 2)       # (get_device() of a CPU tensor is -1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x = OnDevice(torch.zeros(8))
+    for _ in range(2):
+        with pytest.raises(ValueError, match="sx is on device -1"):
+            g._scales(x, 8, "sx")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    assert g._scales(x, 8, "sx") == x.data_ptr()
