@@ -376,6 +376,7 @@ def gemm_f16_moe(X, Wr, W1, W2, Y, topk, ids=None, probs=None, renormalize=True,
     _check(rc, "gemm_f16_moe")
 
 
+_INT = 2 ** 31 - 1      # largest size and leading dimension of a call
 _devices = 0      # counted at the first call; with one, tensors are where they must be
 
 
@@ -396,12 +397,15 @@ def _matrix(x, rows, cols, ld, dtype, name):
     buffer); or an address, taken at its word."""
     try:                                          # the usual tensor, in little time
         if x.shape == (rows, cols) and ld is None and _dtype_names[x.dtype] == dtype and x.is_cuda \
-                and x.is_contiguous():
+                and x.is_contiguous() and rows <= _INT and cols <= _INT:
             if _devices != 1:
                 _elsewhere(x, name)
             return x.data_ptr(), cols
     except (AttributeError, KeyError):
         pass
+    for size in (rows, cols, 0 if ld is None else ld):
+        if not -_INT <= size <= _INT:             # (ctypes would keep 32 bits of it)
+            raise GemmError(-7, "%s, %d x %d" % (name, rows, cols))
     if x is None or isinstance(x, int):
         return x, cols if ld is None else ld
     if _dtype_name(x) != dtype:
@@ -418,6 +422,8 @@ def _matrix(x, rows, cols, ld, dtype, name):
         if rows * cols and (x.stride(1) != 1 and cols > 1 or x.stride(0) < cols and rows > 1):
             raise ValueError("the rows of %s are not dense (a transposed view?)" % name)
         ld = max(cols, x.stride(0)) if rows > 1 else cols
+        if ld > _INT:
+            raise GemmError(-7, "%s, rows %d apart" % (name, ld))
     return x.data_ptr(), ld
 
 

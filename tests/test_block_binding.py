@@ -98,3 +98,45 @@ def test_scales_of_another_device(monkeypatch):
             g._scales(x, 8, "sx")
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     assert g._scales(x, 8, "sx") == x.data_ptr()
+
+
+@pytest.mark.parametrize("size", [2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5])
+def test_sizes_past_32_bits(monkeypatch, size):
+    """They are refused, not cut to their low 32 bits."""
+    class Lib:                              # (none of the calls)
+        def gemm_strerror(self, code):
+            return b""
+
+    monkeypatch.setattr(g, "_lib", Lib())
+    for sizes in (dict(M=size, N=8, K=8), dict(M=8, N=size, K=8), dict(M=8, N=8, K=size),
+                  dict(M=8, N=8, K=8, ldc=size)):
+        for call in (g.gemm_f16_trans, g.gemm_f16_trans_f32out, g.gemm_f16_glu, g.gemm_i8):
+            with pytest.raises(g.GemmError) as e:
+                call(16, 16, 16, **sizes)
+            assert e.value.code == -7
+        sizes["lddx"] = sizes.pop("ldc", None)
+        with pytest.raises(g.GemmError):
+            g.gemm_f16_glu_grad(16, 16, 16, 16, 16, 16, **sizes)
+    for sizes in (dict(M=size, K=8), dict(M=8, K=size), dict(M=8, K=8, ldq=size)):
+        with pytest.raises(g.GemmError):
+            g.f16_to_i8(16, 16, 16, **sizes)
+
+
+def test_tensors_past_32_bits():
+    """(Expanded, so that they take no memory.)"""
+    long = torch.zeros(1, 8, dtype=torch.float16).expand(2 ** 32 + 5, 8)
+    long.is_contiguous = lambda: True
+    with pytest.raises(g.GemmError):
+        matrix(long, *long.shape)
+    far = torch.zeros(1, dtype=torch.float16).as_strided((1, 8), (2 ** 31, 0))
+    assert matrix(far, 1, 1) == (far.data_ptr(), 1)
+    far = far.expand(1, 8)
+
+    class Rows(OnDevice):
+        shape = (2, 8)
+
+        def stride(self, i):
+            return (2 ** 31, 1)[i]
+
+    with pytest.raises(g.GemmError, match="apart"):
+        g._matrix(Rows(far), 2, 8, None, "float16", "X")
