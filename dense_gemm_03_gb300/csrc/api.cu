@@ -1488,14 +1488,14 @@ int gemm_f16_pair(const PairCall& q, cudaStream_t stream) {
   const int grid = 2 * static_cast<int>(std::min<long long>(a.num_units, workers));
   snprintf(t_path_buf, sizeof(t_path_buf), "f16.tc.pair.%s%s%s%s%s%s%s%s",
            q.trans_a ? "ta." : "", q.trans_b ? "tb." : "", q.scaled ? "scaled." : "",
-           q.gate == 2 ? "gate_grad." : (q.gate ? "gate." : ""),
+           q.gate == 2 ? (q.fold ? "gate_grad.fold." : "gate_grad.") : (q.gate ? "gate." : ""),
            epi == kEpiF32Tma ? "epi_f32_tma"
                              : (epi == kEpiF32 ? "epi_f32" : (epi == kEpiTma ? "epi_tma" : "epi_manual")),
            cut, copied ? ".realigned" : "", c_user ? ".c" : "");
   t_last_path = t_path_buf;
   const cudaError_t e =
       q.gate || q.scaled
-          ? launch_gemm_f16_tc_gate(q.gate, q.scaled, epi, tmA, tmB, tmC, tmU, g, a, grid, stream)
+          ? launch_gemm_f16_tc_gate(q.gate, q.scaled, q.fold, epi, tmA, tmB, tmC, tmU, g, a, grid, stream)
           : launch_gemm_f16_tc_trans(q.trans_a, q.trans_b, epi, tmA, tmB, tmC, a, grid, stream);
   if (e != cudaSuccess) return GEMM_ERR_CUDA;
   if (!c_user) return GEMM_OK;

@@ -70,12 +70,9 @@ bool narrow_suits(int M, int cols, int K, int sms) {
 
 // relu's derivative jumps at 0, where a sum's error turns dC U into nothing or back.
 // The tensor core's additions truncate, and long sums of G drift further than sums
-// rounded to nearest; so a relu's gradient over more than 1024 products takes chunks of
-// kFoldDepth, added up in fp32, as long as their partial sums stay within 4 GB.
-bool folds(int gate, int act, int M, int N, int K) {
-  return gate == 2 && act == GEMM_ACT_RELU && K > 1024 &&
-         8.0 * M * N * ((K + kFoldDepth - 1) / kFoldDepth) <= 4e9;
-}
+// rounded to nearest; so a relu's gradient over more than 1024 products adds up runs of
+// kFoldDepth in fp32, in the tiles' registers or as the stream's chunks.
+bool folds(int gate, int act, int K) { return gate == 2 && act == GEMM_ACT_RELU && K > 1024; }
 
 struct GluArgs {
   const uint16_t *X, *W;
@@ -92,8 +89,8 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
   g.dC = dC;
   g.lddc = lddc;
   g.dU = gate == 2 ? C + p.up : nullptr;
-  const bool fold = folds(gate, p.act, p.M, p.N, p.K);
-  if (fold || narrow_suits(p.M, 2 * p.N, p.K, d.sms)) {
+  const bool fold = folds(gate, p.act, p.K);
+  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) {
     StreamSum s{};
     s.fold = fold;
     s.C = C;
@@ -121,6 +118,7 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
   q.ldc = ldc;
   q.alpha = 1.0f;
   q.gate = gate;
+  q.fold = fold;
   q.g = g;
   return gemm_f16_pair(q, stream);
 }
@@ -273,8 +271,7 @@ struct Copies {
 // apart, with zeros between them in W and dGU, which add nothing to dX.  2000 x 1501 x 2*1111: 71 us
 // (1504 x 2*1112, no copies: 51; copied for each product by itself 37 more than here).
 int grad(GradArgs p, const LoraDevice& d, cudaStream_t stream) {
-  if (folds(2, p.act, p.M, p.N, p.K) || narrow_suits(p.M, 2 * p.N, p.K, d.sms))
-    return grad_products(p, d, stream);
+  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) return grad_products(p, d, stream);
   auto off = [](const void* m, int ld) { return misaligned({m}, 16) || ld % 8 != 0; };
   const int n8 = Copies::pad(p.N), k8 = Copies::pad(p.K);
   const bool apart = p.N % 8 != 0;

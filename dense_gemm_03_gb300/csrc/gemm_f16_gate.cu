@@ -6,11 +6,11 @@
 namespace gb300 {
 namespace {
 
-template <int GATE, bool SCALED>
+template <int GATE, bool SCALED, bool FOLD = false>
 cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
                    const CUtensorMap& u, const GateArgs& gate, const TcArgs& args, int grid,
                    cudaStream_t s) {
-  using G = Gated<GATE, SCALED>;
+  using G = Gated<GATE, SCALED, FOLD>;
   G x{};
   x.tmU = u;
   x.a = gate;
@@ -25,7 +25,7 @@ cudaError_t launch(int epi, const CUtensorMap& a, const CUtensorMap& b, const CU
 
 }  // namespace
 
-cudaError_t launch_gemm_f16_tc_gate(int gate, bool scaled, int epi_mode, const CUtensorMap& tmA,
+cudaError_t launch_gemm_f16_tc_gate(int gate, bool scaled, bool fold, int epi_mode, const CUtensorMap& tmA,
                                     const CUtensorMap& tmB, const CUtensorMap& tmC,
                                     const CUtensorMap& tmU, const GateArgs& gate_args,
                                     const TcArgs& args, int grid, cudaStream_t stream) {
@@ -38,6 +38,7 @@ cudaError_t launch_gemm_f16_tc_gate(int gate, bool scaled, int epi_mode, const C
                     : launch<1, false>(epi_mode, tmA, tmB, tmC, tmU, gate_args, args, grid, stream);
     default:
       return scaled ? cudaErrorInvalidValue
+             : fold ? launch<2, false, true>(epi_mode, tmA, tmB, tmC, tmU, gate_args, args, grid, stream)
                     : launch<2, false>(epi_mode, tmA, tmB, tmC, tmU, gate_args, args, grid, stream);
   }
 }

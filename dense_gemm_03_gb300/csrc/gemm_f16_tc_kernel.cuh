@@ -48,7 +48,7 @@
 #pragma once
 #include "gate.cuh"
 #include "internal.h"
-#include "ptx.cuh"
+#include "ptx_tmem_st.cuh"
 
 namespace gb300 {
 namespace {
@@ -502,6 +502,9 @@ struct NoLora {
 // truncate: over 8192 products the sums drift by 9e-6 of their norm, folded every
 // 1024 by 1.3e-6, every 512 by 0.7e-6.  fold_kb is 16 from K = 4096 on, where sums rounded to
 // nearest one by one are off by as much, else 8 (4096 x 4096 over 8192: 195 us and 206).
+// A gate's gradient (relu's, whose derivative jumps where G is 0) folds every 512: the sum of
+// the parts before the last is then added onto the last in tensor memory, where the epilogue
+// finds G and U as it would unfolded.
 
 // Operands stored transposed (CTA pairs, TMA loads).  A stage's part of A is then
 // two blocks of 64 (k) rows x 64 halves, like B's.  FOLD: float results of long sums
@@ -523,10 +526,12 @@ struct Transposed : NoLora {
 // f'(G) to C and dU = dC .* f(G) to dU.  p.N counts output columns.
 // SCALED: results (G and U, or the plain product's) are multiplied by sx[row] and
 // sw[column of B].
-template <int GATE, bool SCALED>
+template <int GATE, bool SCALED, bool FOLD = false>
 struct Gated : NoLora {
   static constexpr int kGate = GATE;
   static constexpr bool kScaled = SCALED;
+  static constexpr bool kFold = FOLD;
+  int fold_kb = 8;
   CUtensorMap tmU;        // GATE == 2: dU, as tmC is dG
   GateArgs a;
 };
@@ -579,8 +584,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
   static_assert(!(LORA::kTransA || LORA::kTransB || kGate || LORA::kScaled) ||
                     (PAIR && BN == 256 && KPB == 1),
                 "transposed operands and gates run on 256-wide pairs");
-  static_assert(!LORA::kFold || (PAIR && KPB == 1 && (EPI == kEpiF32 || EPI == kEpiF32Tma)),
-                "long sums of float results");
+  static_assert(!LORA::kFold || (PAIR && KPB == 1 && (EPI == kEpiF32 || EPI == kEpiF32Tma || kGate == 2)),
+                "long sums of float results and of a gate's gradient");
+  constexpr bool kFoldSums = LORA::kFold && kGate == 0;    // sums end in registers
+  constexpr bool kFoldTmem = LORA::kFold && kGate != 0;    // ... in tensor memory
   static_assert(!kGate || EPI == kEpiTma || EPI == kEpiManual, "gated results are halves");
   constexpr int kBn = kGate ? BN / 2 : BN;   // output columns of a tile
   // MM = 64: 64-row tiles (tcgen05.mma with M = 64), whole-K units only, TMA
@@ -1445,6 +1452,61 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         }
       }
     };
+    // kFoldTmem: waits for a unit's parts of G and U and leaves their sum in the last one's
+    // accumulator (buffer local & 1, still this warp's); false: a wait gave up.
+    [[maybe_unused]] auto fold_parts = [&](const Unit& u, bool outputs, int wcol0, int nsub, int colw) {
+      if constexpr (kFoldTmem) {
+        float sum[2 * kSubs * kSubCols];   // G's, then U's
+#pragma unroll
+        for (int i = 0; i < 2 * kSubs * kSubCols; ++i) sum[i] = 0.0f;
+        for (int kb = u.kb0;; kb += x.fold_kb) {
+          const uint32_t b = local & 1u;
+          if (!wait_parity(accf_bar(b), (local >> 1) & 1u, limit, st, 5)) return false;
+          tc_fence_after();
+          const bool last = kb + x.fold_kb >= u.kb1;
+          if (last && kb == u.kb0) return true;   // nothing to add
+          const uint32_t part = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
+                                b * Cfg::kAccStride + static_cast<uint32_t>(wcol0);
+          if (outputs) {
+#pragma unroll
+            for (int k = 0; k < 2 * kSubs; ++k) {
+              const int kc = k % kSubs;
+              if (kc < nsub && colw + kSubCols * kc < p.N) {
+                const uint32_t at = part + kSubCols * kc + (k < kSubs ? 0 : u.ncols);
+#pragma unroll
+                for (int c = 0; c < kSubCols; c += 16) {
+                  uint32_t v[8], w[8];
+                  tmem_ld_32x32b_x8(at + c, v);
+                  tmem_ld_32x32b_x8(at + c + 8, w);
+                  tmem_wait_ld2(v, w);
+                  float* const s = sum + kSubCols * k + c;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    s[i] += __uint_as_float(v[i]);
+                    s[8 + i] += __uint_as_float(w[i]);
+                    v[i] = __float_as_uint(s[i]);
+                    w[i] = __float_as_uint(s[8 + i]);
+                  }
+                  if (last) {
+                    tmem_st_32x32b_x8(at + c, v);
+                    tmem_st_32x32b_x8(at + c + 8, w);
+                  }
+                }
+              }
+            }
+          }
+          if (last) {
+            tmem_wait_st();
+            return true;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_acc_empty(map_to_cta(acce_bar(b), 0));
+          ++local;
+        }
+      }
+      return true;
+    };
     UnitCursor cur = first_unit(p, worker);
     Unit t, tn;
     bool have = next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, t);
@@ -1452,7 +1514,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
     while (have) {
       // kCs looks one unit ahead (its C tile is loaded during the next main loop)
       const bool have_next = kCs && next_unit(p, cur, worker, nworkers, kBn, bm_tile, rank, tn);
-      const uint32_t buf = local & 1u, use = local >> 1;
+      uint32_t buf = local & 1u;
       const int row0 = t.m0 + kQRows * q;
       // tail bookkeeping is per CTA: the rows of one CTA of a pair form their own part
       const int tail_part = PAIR ? 2 * t.tail_idx + static_cast<int>(rank) : t.tail_idx;
@@ -1518,10 +1580,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
       }
       // (a folded sum in one part needs no folding)
       bool brief = kBrief && !has_c && !t.tail;
-      if constexpr (LORA::kFold) brief = brief && t.kb1 - t.kb0 <= x.fold_kb;
-      // kFold: this row's sums, every part of the accumulator added as it comes
-      [[maybe_unused]] float sum[LORA::kFold ? kSubs * kSubCols : 1];
-      if (LORA::kFold && brief) {
+      if constexpr (kFoldSums) brief = brief && t.kb1 - t.kb0 <= x.fold_kb;
+      // kFoldSums: this row's sums, every part of the accumulator added as it comes
+      [[maybe_unused]] float sum[kFoldSums ? kSubs * kSubCols : 1];
+      if (kFoldSums && brief) {
         const uint32_t b = local & 1u;
         if (!wait_parity(accf_bar(b), (local >> 1) & 1u, limit, st, 5)) break;
         tc_fence_after();
@@ -1533,7 +1595,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         __syncwarp();
         if (lane == 0) arrive_acc_empty(map_to_cta(acce_bar(b), 0));
         ++local;
-      } else if constexpr (LORA::kFold) {
+      } else if constexpr (kFoldSums) {
 #pragma unroll
         for (int i = 0; i < kSubs * kSubCols; ++i) sum[i] = 0.0f;
         bool ok = true;
@@ -1567,8 +1629,11 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           ++local;
         }
         if (!ok) break;
+      } else if constexpr (kFoldTmem) {
+        if (!fold_parts(t, finish, wcol0, nsub, colw)) break;
+        buf = local & 1u;   // of the last part
       } else {
-        if (!wait_parity(accf_bar(buf), use & 1u, limit, st, 5)) break;
+        if (!wait_parity(accf_bar(buf), (local >> 1) & 1u, limit, st, 5)) break;
         tc_fence_after();
       }
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) +
@@ -1593,7 +1658,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           // Publish this slice's partial sums, then count the slice in; the last
           // slice to arrive finishes the tile.
           float4* mine = tail_partials(p, tail_part, t.split, BN) + 32 * q + lane;
-          if constexpr (LORA::kFold) {
+          if constexpr (kFoldSums) {
 #pragma unroll
             for (int k = 0; k < kSubs; ++k)
               if (k < nsub && colw + kSubCols * k < p.N) {
@@ -1605,7 +1670,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
                                      sum[kSubCols * k + 4 * i + 2], sum[kSubCols * k + 4 * i + 3]));
               }
           }
-          for (int k = 0; !LORA::kFold && k < (kGate ? 2 : 1) * kSubs; ++k) {
+          for (int k = 0; !kFoldSums && k < (kGate ? 2 : 1) * kSubs; ++k) {
             // (a gate's chunks, then those it gates)
             const int kc = k < kSubs ? k : k - kSubs, col = kSubCols * kc;
             const int off = k < kSubs ? col : col + t.ncols;
@@ -1651,7 +1716,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         if (finish && lane == 0) *reinterpret_cast<volatile unsigned long long*>(cnt) = 0ull;
       }
 
-      if constexpr (LORA::kFold) {
+      if constexpr (kFoldSums) {
         // a tile in two slices: the other's sums (of two, in either order)
         if (t.tail && finish) {
           const float4* part = tail_partials(p, tail_part, 1 - t.split, BN) + 32 * q + lane +
@@ -1678,12 +1743,12 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
         if (finish && kGate == 2)
           gate_grad_epilogue(t, tail_part, tbase, wcol0, nsub, colw, row0, row);
       }
-      if constexpr (kBrief && !LORA::kFold) {
+      if constexpr (kBrief && !kFoldSums) {
         if (brief && finish) brief_epilogue(tbase, nsub, colw, row0);
       }
       if (kGate == 0 && finish && !brief) {
         uint32_t acc_a[32], acc_b[32];
-        if (!LORA::kFold && !t.tail) {
+        if (!kFoldSums && !t.tail) {
           tmem_ld_32x32b_x32(tbase, acc_a);
           tmem_wait_regs(acc_a);
         }
@@ -1694,7 +1759,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
           const int col0 = colw + kSubCols * k;
           if (k >= nsub || col0 >= p.N) break;
           const bool more = k + 1 < nsub && col0 + kSubCols < p.N;
-          if constexpr (LORA::kFold) {
+          if constexpr (kFoldSums) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) cur[i] = __float_as_uint(sum[kSubCols * k + i]);
           } else {
@@ -1706,7 +1771,7 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
             for (int g = 0; g < 4; ++g) c_cur[g] = c_next[g];
             if (has_c && more) load_c_sub(p, row, col0 + kSubCols, c_next);
           }
-          if (EPI != kEpiPartial && !LORA::kFold && t.tail) {
+          if (EPI != kEpiPartial && !kFoldSums && t.tail) {
             // cur := sum of every slice's partial sums in slice order; this
             // slice's own term is still in TMEM (bit-identical to what it
             // published), so only the other slices are read back.
@@ -1943,10 +2008,10 @@ __global__ void __launch_bounds__(Roles<LOAD>::kThreads + 32 * LORA::kWarps, 1)
               if (row0 + r < p.M && col_ok) cout[static_cast<long long>(r) * p.ldc] = o[r];
             __syncwarp();
           }
-          if (!LORA::kFold && more && !t.tail) tmem_wait_regs(nxt);
+          if (!kFoldSums && more && !t.tail) tmem_wait_regs(nxt);
         }
       }
-      if constexpr (!LORA::kFold) {
+      if constexpr (!kFoldSums) {
         tc_fence_before();
         __syncwarp();
         // the accumulator may be overwritten (with pairs: counted on the leader)

@@ -179,8 +179,8 @@ cudaError_t launch_gemm_f16_tc_trans(bool trans_a, bool trans_b, int epi_mode,
                                      const CUtensorMap& tmC, const TcArgs& args, int grid,
                                      cudaStream_t stream);
 // ... gated products (gate 1), their gradient (gate 2), and products scaled by row and
-// column (gate 0 or 1); tmU: dU's map (gate 2).
-cudaError_t launch_gemm_f16_tc_gate(int gate, bool scaled, int epi_mode, const CUtensorMap& tmA,
+// column (gate 0 or 1); tmU: dU's map (gate 2); fold: G and U folded (gate 2, see the kernel).
+cudaError_t launch_gemm_f16_tc_gate(int gate, bool scaled, bool fold, int epi_mode, const CUtensorMap& tmA,
                                     const CUtensorMap& tmB, const CUtensorMap& tmC,
                                     const CUtensorMap& tmU, const GateArgs& gate_args,
                                     const TcArgs& args, int grid, cudaStream_t stream);
@@ -209,6 +209,7 @@ struct PairCall {
   bool trans_a, trans_b;
   int gate;
   bool scaled;
+  bool fold;               // gate 2: long sums folded into registers
   GateArgs g;
   bool c_padded;           // C's columns up to a multiple of eight may be written
   bool whole;              // no half-width tiles: they would take SMs of a product beside

@@ -1,6 +1,6 @@
 // ptx_i8.cuh -- inline PTX of the kernels of 8-bit integers, beside ptx.cuh.
 #pragma once
-#include "ptx.cuh"
+#include "ptx_tmem_st.cuh"
 
 namespace gb300 {
 
@@ -22,19 +22,6 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// 16 lanes x 16 columns of tensor memory from the registers of a warp: thread 4 g + t
-// holds, for each group of four columns, those of lanes g and g + 8 in column t of it.
-__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 // Two 16 x 16 matrices of bytes, transposed: lanes 0-15 (16-31) give the addresses of the

@@ -281,7 +281,8 @@ int gemm_f16_glu(const uint16_t* X, const uint16_t* W, uint16_t* C, int M, int N
  * then holds (entries past the half range are infinite, small ones rounded to the
  * half's 2^-24 grid: scale the loss, as in any training in half), summed in fp32 and
  * rounded once.  dX and dW may each be NULL (not wanted); dGU may not.  For a dW in
- * float call gemm_f16_trans_f32out on X and dGU.  f'(0) is 0 for GEMM_ACT_RELU.
+ * float call gemm_f16_trans_f32out on X and dGU.  f'(0) is 0 for GEMM_ACT_RELU, whose
+ * sums G and U are rounded to nearest at least every 1024 products (f' jumps where G is 0).
  * K == 0: dGU := 0.
  */
 int gemm_f16_glu_grad(const uint16_t* dC, const uint16_t* X, const uint16_t* W, uint16_t* dGU,
