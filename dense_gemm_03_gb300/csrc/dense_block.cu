@@ -54,6 +54,19 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
   return stream_sum(s, d, stream);
 }
 
+// Folded sums (`fold`) come as a chunk for each kFoldDepth of K: once these pass the L2, as many bytes again twice
+// over HBM, and scratch.  Tiles that fold in registers take about 0.35 us a k-block and wave, chunks 5.9 TB/s:
+// float results of 192 x 16384 over 16384, 403 MB of partial sums, 225 us, tiles 100; relu's gradient of 128 x 8192 x
+// 2*8192, 134 MB, 90, 61; draws at 134 MB of 128 x 16384 x 2*4096 and 537 of 128 x 8192 over 65536; but 67 MB of
+// 128 x 8192 over 8192 40, 49, and 34 of 128 x 1024 over 32768 28, 166.
+bool folds_in_tiles(int M, int cols, int K, int sms) {
+  const double part = 4.0 * M * cols * ((K + kFoldDepth - 1) / kFoldDepth);
+  if (K <= kFoldDepth || part <= 96e6) return false;
+  const long long tiles = ((M + 255ll) / 256) * ((cols + 255ll) / 256), pairs = sms / 2;
+  return 0.35 * ((tiles + pairs - 1) / pairs) * ((K + 63) / 64) <
+         (2.0 * K * (1.0 * M + cols) + 2 * part) / 5.9e6;
+}
+
 // Whether K chunks suit the product better than whole 256 x 256 tiles (`cols` columns of
 // W).  Measured, chunks against tiles: a block of up to 128 rows wins or draws (128 x 8192
 // x 2048 11.1 us, 14.4; 128 x 4096 x 512 6.2, 6.2), up to 192 with a sum long enough (160 x 4096 x
@@ -61,7 +74,8 @@ int streamed(const uint16_t* X, int ldx, bool trans_x, const uint16_t* W, int ld
 // 14.6); so do few tiles with a long K (512 x 512 x 1536 9.5, 10.5; 331 x 2048 x 4096 11.7, 21.9; but
 // 1024^3 9.3, 8.4, and 32 tiles, 1024 x 2048 x 2048, 14.4, 13.8) and narrow results (6000 x 128 x
 // 1536 10.3, 11.0, 9000 x 64 x 1024 8.6, 8.8, but 2048 x 128 x 512 8.0, 6.1).
-bool narrow_suits(int M, int cols, int K, int sms) {
+bool narrow_suits(int M, int cols, int K, bool fold, int sms) {
+  if (fold && folds_in_tiles(M, cols, K, sms)) return false;
   if (M <= 128) return true;
   if (M <= 192) return K >= 768;
   const long long tiles = static_cast<long long>((M + 255) / 256) * ((cols + 255) / 256);
@@ -90,7 +104,7 @@ int gated(const GluArgs& p, int gate, uint16_t* C, int ldc, const uint16_t* dC, 
   g.lddc = lddc;
   g.dU = gate == 2 ? C + p.up : nullptr;
   const bool fold = folds(gate, p.act, p.K);
-  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) {
+  if (narrow_suits(p.M, 2 * p.N, p.K, fold, d.sms)) {
     StreamSum s{};
     s.fold = fold;
     s.C = C;
@@ -131,7 +145,7 @@ struct Trans {
   int M, N, K, lda, ldb, ldc;
   float alpha, beta;
   bool c_padded = false;   // see PairCall
-  bool tiled(int sms) const { return !narrow_suits(M, N, K, sms); }
+  bool tiled(int sms) const { return !narrow_suits(M, N, K, f32, sms); }
   bool on_grid() const {   // no copies of the operands
     return !misaligned({A, B}, 16) && lda % 8 == 0 && ldb % 8 == 0;
   }
@@ -271,7 +285,7 @@ struct Copies {
 // apart, with zeros between them in W and dGU, which add nothing to dX.  2000 x 1501 x 2*1111: 71 us
 // (1504 x 2*1112, no copies: 51; copied for each product by itself 37 more than here).
 int grad(GradArgs p, const LoraDevice& d, cudaStream_t stream) {
-  if (narrow_suits(p.M, 2 * p.N, p.K, d.sms)) return grad_products(p, d, stream);
+  if (narrow_suits(p.M, 2 * p.N, p.K, folds(2, p.act, p.K), d.sms)) return grad_products(p, d, stream);
   auto off = [](const void* m, int ld) { return misaligned({m}, 16) || ld % 8 != 0; };
   const int n8 = Copies::pad(p.N), k8 = Copies::pad(p.K);
   const bool apart = p.N % 8 != 0;

@@ -103,3 +103,23 @@ def test_float_results(M, N, K, path, ta, tb):
     sync(t)
     want = (A.t() if ta else A).double() @ (B.t() if tb else B).double()
     assert rms(t, C - want) <= 2.5e-6 * rms(t, want)
+
+
+@pytest.mark.parametrize("M,N,K", [(192, 16384, 16384), (128, 16384, 16384)])
+def test_long_float_sums_over_few_rows(M, N, K):
+    """Their parts are added up on the chip too: as exact, and with the scratch of a last wave."""
+    import dense_gemm_03_gb300 as g
+    t = torch()
+    gen = t.Generator(device="cuda").manual_seed(M)
+    A, B = (t.randn(K, n, generator=gen, device="cuda").half() for n in (M, N))
+    C = t.empty(M, N, device="cuda")
+    g.gemm_f16_trans_f32out(A, B, C, True)            # (its code is loaded)
+    sync(t)
+    stream = t.cuda.Stream()
+    before = t.cuda.mem_get_info()[0]
+    g.gemm_f16_trans_f32out(A, B, C, True, stream=stream)
+    sync(t)
+    assert before - t.cuda.mem_get_info()[0] <= 76 * 2 * 256 * 256 * 4 + (8 << 20)
+    rows = [0, M // 2, M - 1]
+    want = A[:, rows].double().t() @ B.double()
+    assert rms(t, C[rows] - want) <= 2.5e-6 * rms(t, want)
