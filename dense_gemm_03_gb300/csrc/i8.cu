@@ -2,7 +2,9 @@
 // rounding of tokens to 8 bits: argument checks, path choice and the kernels that
 // turn rows of halves into rows of integers and back.
 //
-//   product    S = X W exactly as integers, C := sx[i] sw[n] S + beta C, or gated
+//   product    S = X W, C := sx[i] sw[n] S + beta C, or gated.  Products are exact in fp32, and S is
+//              while its partial sums stay below 2^24 (whatever the values up to K = 1024);
+//              past that it is rounded, the tensor core truncating, as a product of halves is
 //   tokens     a = max_k |X[i,k]|, scale[i] = a / 127, Q[i,k] = round(127 X[i,k] / a)
 //
 // Few rows or few tiles: i8_stream.cu (bytes to halves on their way to the tensor
