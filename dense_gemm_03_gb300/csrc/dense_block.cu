@@ -10,6 +10,10 @@
 // Two ways for each product: whole 256 x 256 tiles on CTA pairs
 // (gemm_f16_tc_kernel.cuh), or, where a few rows or few tiles would leave SMs idle,
 // K cut into chunks (narrow_stream.cu).  Sums are fp32; every result is rounded once.
+// dX and dW are products of dGU as it was rounded, where a chain that kept dGU in 32 bits would
+// be 1.4 times nearer to 64 bits (errors of 2.9e-4 and 2.1e-4 of their norm): dGU in half is an
+// output that the backward chain reads anyway, and the tensor cores take no wider operands at this
+// rate (two halves each would double both products).
 #include "gemm.h"
 #include "lora.h"
 #include "operands.h"

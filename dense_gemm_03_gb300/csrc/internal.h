@@ -278,9 +278,6 @@ cudaError_t launch_splitk_reduce_f16(const float* ws, long long ws_ld, int split
                                      long long ldc, int M, int N, float alpha, float beta,
                                      int grid, cudaStream_t stream);
 
-// Copies a rows x cols half matrix with any leading dimension and alignment
-// into a 16-byte-aligned one with ldd = cols rounded up to 8 (zero padding), or
-// into `width` columns (a multiple of 8, at least cols) of one with a larger ldd.
 // A launch that may begin while the kernel before it on the stream, whoever
 // launched that, is in its last blocks, so that its own set-up is not waited for.  The kernel
 // waits (griddep_wait) for all of that one before it touches global memory, and so for
@@ -303,6 +300,9 @@ cudaError_t launch_early(K kernel, unsigned grid, unsigned threads, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Copies a rows x cols half matrix with any leading dimension and alignment
+// into a 16-byte-aligned one with ldd = cols rounded up to 8 (zero padding), or
+// into `width` columns (a multiple of 8, at least cols) of one with a larger ldd.
 struct RealignJob {
   const uint16_t* src;
   long long lds;
@@ -446,10 +446,10 @@ int lock_stream(cudaStream_t stream, std::unique_lock<std::recursive_mutex>* cal
 // gemm_release().  Returns a GEMM_* code.
 // `zeroed`: a separate region of at least that many bytes that starts at zero
 // when it is first handed out and then keeps what kernels leave in it.
-// The buffer of the copies that gemm_f16_pair makes (it makes none of operands on the grid).
-int realigned_scratch(cudaStream_t stream, size_t bytes, void** out);
 int routed_scratch(cudaStream_t stream, size_t bytes, void** out, size_t zeroed = 0,
                    void** zeroed_out = nullptr);
+// The buffer of the copies that gemm_f16_pair makes (it makes none of operands on the grid).
+int realigned_scratch(cudaStream_t stream, size_t bytes, void** out);
 // Tensor map of a stack of `depth` fp16 matrices (rows x cols, leading
 // dimension ld, `stride` elements apart), 128-, 64- or 32-byte swizzle, boxes of
 // box_cols x box_rows of one matrix; what lies outside a matrix reads as zero.

@@ -531,13 +531,13 @@ __global__ void __launch_bounds__(kCombThreads) lora_combine_kernel(const Combin
   }
 }
 
-// Chunks per unit: the count whose rounds of chunks over the SMs, in k-block
-// times of an SM, and whose partial sums take least.  A k-block takes 0.36 us
+}  // namespace
+
+// Chunks per unit, `least` or more: the count whose rounds of chunks over the SMs, in
+// k-block times of an SM, and whose partial sums take least.  A k-block takes 0.36 us
 // (its 16 KB of W at an SM's share of HBM) or, for a full block of rows, as long
 // as its 48 KB from L2; the partial sums are 1 KB per row written and read,
 // through L2 at about twice HBM's rate.
-}  // namespace
-
 int plan_chunks(int units, int blocks, int kb, int rows, int sms, int least) {
   int best = least;
   double best_t = 1e30;

@@ -15,15 +15,15 @@ namespace gb300 {
 // Partial sums: [block of `block` rows][128-column unit][chunk][row of the block][128].
 struct StreamParts {
   float* part;
-  int chunks, units, block_rows;   // block_rows = block: see row_blocks.h
+  int chunks, units, block_rows;
   size_t bytes;
-  int block;
+  int block;                       // (block_rows: see row_blocks.h)
 };
 // Chunks per unit (of `kb` steps of 16 KB of W each): see lora_stream.cu.
 int plan_chunks(int units, int blocks, int kb, int rows, int sms, int least = 1);
 
-// Longest chunk of K of a float result: the tensor core's additions truncate (over 512
-// products by 0.7e-6 of the sums' norm).
+// Longest chunk of K of a folded sum (float results, relu's gradient): the tensor core's
+// additions truncate (over 512 products by 0.7e-6 of the sums' norm).
 constexpr int kFoldDepth = 512;
 
 // op(X) (M x K, stored K x M where trans_x) times op(W) (K x `cols`; N x K) in halves, or
@@ -35,7 +35,7 @@ struct NarrowStream {
   bool trans_x, trans_w;
   bool beside = false;   // see PairDone (internal.h)
 };
-// Its partial sums; fold: of a float result.
+// Its partial sums; fold: in chunks of kFoldDepth at most.
 StreamParts narrow_parts(const NarrowStream& p, int M, int cols, bool fold, const LoraDevice& d);
 int narrow_partial(const NarrowStream& p, int M, int cols, bool fold, const StreamParts& parts,
                    const LoraDevice& d, cudaStream_t stream);

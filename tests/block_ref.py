@@ -6,9 +6,10 @@ Bounds.  u = 2^-24.  A sum of n products in fp32, in any order and with truncati
 additions, is off by at most n * 2u * sum |terms| (sum_tol); a result's rounding to half
 adds 2^-11 |result| and, below the normal range, 2^-25, to float 2^-24 |result|.
 
-f is evaluated with CUDA's __expf (2 + 1.16 |x| units of 2^-23), a division (2), for gelu a
-polynomial fitted to 1.8e-7 (1.5 units, and as much again for its roundings), and an
-argument that is itself rounded: a relative error of f of at most act_rel(g), in
+f is evaluated with ex2.approx (2 units of 2^-23) of a product that is rounded (half a unit of
+|x| and as much for its constant), rcp.approx (1), for gelu a
+polynomial fitted to 1.8e-7 (1.5 units, and as much again for its roundings), an addition and two
+products (half a unit each), and an argument that is itself rounded, by up to three units: a relative error of f of at most act_rel(g), in
 which the argument's rounding counts by the derivative of the exponent (|g| for silu, g^2
 for gelu, about 1.6 |g| + 0.08 |g|^3 for gelu_tanh).  f' is a sum of two such terms, of
 magnitudes at most 1 and |g f''|-like 0.6: off by at most 2 act_rel(g).  f is
